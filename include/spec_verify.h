@@ -302,6 +302,166 @@ spec_status_t spec_tree_draft(const void *draft_logits, spec_dtype_t draft_dtype
                               int N, int V, int max_children, float temperature, int32_t *node_tokens,
                               float *node_logq, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Serving steps around verification: a paged cache held in 4 bits, the
+ * attention that scores a chain or a tree over it, and what changes the logits
+ * before they are verified.  One speculative step of a decode loop calls
+ *   spec_page_map -> spec_attend_q4 (in every layer) -> spec_adjust_logits ->
+ *   spec_verify_* -> spec_kv_commit_q4 (in every layer).
+ *
+ * The cache: [num_pages, Hkv, page_tokens / 32, spec_q4_block_bytes(D)] bytes,
+ * 16-byte aligned, page_tokens a multiple of 32, D 64 or 128.  A block holds 32
+ * tokens of one kv head:
+ *   [32 x D/2 key codes | 32 x D/2 value codes |
+ *    32 x D/16 key scales | 32 x D/16 value scales]
+ * Element d of a token is e2m1(code) * e4m3(scale[d / 16]) * 2^shift; codes are
+ * packed two to a byte, the even element in the low half.  The shift (k_shift
+ * for keys, v_shift for values, -32..32) is not stored: a cache is written and
+ * read with the same one.  Quantising a group of 16: s = e4m3(max|x| 2^-shift /
+ * 6) to nearest even, at most 448; code = e2m1(x 2^-shift / s) to nearest even,
+ * at most 6 in size; s = 0 gives codes 0; a group with a NaN or an infinity is
+ * stored with the scale NaN and codes 0.
+ * A slot is page * page_tokens + token in page.
+ * ------------------------------------------------------------------------- */
+
+/* Bytes of one block (36 * D); 0 for a D other than 64 or 128. */
+size_t spec_q4_block_bytes(int D);
+
+/* Block tables and slot maps of a paged cache from the requests' lengths.
+ *
+ *   lengths [B] int32 (device): tokens that sequence b has in the cache.
+ *   count [B] int32 (device): tokens that it wants places for now (a prompt's
+ *       length; K + 1 for a speculative step); negative: the sequence has ended
+ *       and gives its pages back.
+ *   held [B] int32 (device): pages it holds, entries 0..held-1 of its table row.
+ *   ring [ring_size] int32 (device, in/out): the pool's free page ids, a
+ *       circular list; the pool's pages are 0..ring_size-1.
+ *   ring_state [2] int32 (device): position of the first free id, number of
+ *       free ids.
+ *   block_table [B, max_pages] int32 (device, in/out).
+ *   max_tokens: places in slots and positions.
+ *   offsets [B + 1] int32 (device, written): sequence b's places are
+ *       offsets[b] .. offsets[b + 1] - 1 (max(count, 0) of them, whether its
+ *       request is granted or not; never past max_tokens).
+ *   slots, positions [max_tokens] int32 (device, written): the slot and the
+ *       position in its sequence of each place; -1 where there is none.
+ *   new_held [B], new_ring_state [2] int32 (device, written; not the inputs'
+ *       buffers: a call with the same inputs gives the same results).
+ *   status [B] int32 (device, written): 0; -1 for a request that breaks a rule
+ *       (a negative length or held, held > max_pages, lengths + count >
+ *       max_pages * page_tokens, places past max_tokens, a ring_state outside
+ *       the ring); -3 when the pool has too few free pages.  A refused sequence
+ *       keeps its pages, takes none, and its places have slot -1.
+ *
+ * Sequences are served in order: a request is granted iff the pages that the
+ * sequences up to and including it need together are free before the call
+ * (pages given back in a call are free for the next one).  A page id outside
+ * the pool gives slot -1.  Limits: ring_size * page_tokens and max_pages *
+ * page_tokens below 2^31. */
+spec_status_t spec_page_map(const int32_t *lengths, const int32_t *count, const int32_t *held, int32_t *ring,
+                            const int32_t *ring_state, int32_t *block_table, int B, int ring_size, int page_tokens,
+                            int max_pages, int max_tokens, int32_t *offsets, int32_t *slots, int32_t *positions,
+                            int32_t *new_held, int32_t *new_ring_state, int32_t *status, void *stream);
+
+/* Keys and values into the cache, by slot (prompts, packed or padded).
+ *
+ *   k, v [T, Hkv, D] bf16 (device, 16-byte aligned); slots [T] int32 (device),
+ *       e.g. spec_page_map's: entry t goes to slots[t], a slot outside the cache
+ *       (negative: none) is skipped.  Two entries with one slot leave one of the
+ *       two, groups of both may mix.
+ * Nothing else in the cache is written.  Limit: num_pages * page_tokens below
+ * 2^31. */
+spec_status_t spec_kv_store_q4(const void *k, const void *v, const int32_t *slots, int T, int Hkv, int D,
+                               int page_tokens, int num_pages, int k_shift, int v_shift, void *cache, void *stream);
+
+/* spec_kv_commit for the paged 4-bit cache: the accepted drafts' bf16 entries
+ * are quantised and appended behind lengths[b].
+ *
+ *   block_table [B, max_pages], lengths, count [B], path [B, W] or NULL: as in
+ *       spec_kv_commit and spec_page_map; the pages of the appended positions
+ *       must be in the table (spec_page_map for K + 1 tokens before the step).
+ *   k, v [B, N, Hkv, D] bf16 (device, 16-byte aligned).
+ *   new_lengths [B] int32 (device, written): lengths + count; lengths when
+ *       count < 0; -1, with nothing appended, when lengths is negative, the
+ *       positions pass the table, a page id is outside the cache, a path entry
+ *       is outside [0, N), or count > W (count > N without a path).
+ * new_lengths must not alias lengths. */
+spec_status_t spec_kv_commit_q4(void *cache, const int32_t *block_table, const int32_t *lengths, const void *k,
+                                const void *v, const int32_t *path, const int32_t *count, int B, int N, int W, int Hkv,
+                                int D, int page_tokens, int num_pages, int max_pages, int k_shift, int v_shift,
+                                int32_t *new_lengths, void *stream);
+
+/* Scratch bytes needed by spec_attend_q4.  Pure host function; 0 for invalid
+ * sizes. */
+size_t spec_attend_workspace_bytes(int B, int N, int Hq, int Hkv, int D);
+
+/* Verification attention over the paged 4-bit cache ("Speculative decoding and
+ * EAGLE", section "Tree attention verification": the target scores the whole
+ * tree in one pass, each node attending to the context, its ancestors and
+ * itself).
+ *
+ *   q [B, N, Hq, D] bf16: the queries of N nodes per sequence; query head i
+ *       reads kv head i / (Hq / Hkv).
+ *   k_new, v_new [B, N, Hkv, D] bf16, or both NULL: the nodes' own entries, not
+ *       yet in the cache.
+ *   masks [B, N, ceil(N/32)] uint32 (spec_tree_mask's) or NULL: bit j of row i
+ *       lets node i attend to node j; NULL is a chain, node i attends to nodes
+ *       0..i.  Every node attends to all cached tokens.
+ *   block_table [B, max_pages], lengths [B] int32: the cached tokens.
+ *   scale: factor of the scores, finite (usually 1 / sqrt(D)).
+ *   out [B, N, Hq, D] bf16 (written): softmax(scale * q.k) v.
+ *   lse [B, N, Hq] float32 (written) or NULL: the natural logarithm of the sum
+ *       of exp(scale * q.k) over what the row attends to.
+ *
+ * N = 1 without k_new is the plain decoding step over a cache that already
+ * holds the token.  A row that attends to nothing (no cached token, an empty
+ * mask row), or whose scores are all -inf, gives 0 and lse = -inf.  Keys and
+ * values that a row's mask rules out do not reach it, whatever they hold.  A
+ * sequence whose length is negative or passes its table, or a needed page id
+ * outside the cache, gives NaN in all its rows that need it, as does an
+ * internal wait that hit its time limit.  q, k_new, v_new, out, cache and the
+ * workspace must be 16-byte aligned.
+ * Limits: 1 <= N <= 1024, B <= 4096, Hq a multiple of Hkv, Hq / Hkv <= 64,
+ * num_pages * page_tokens and max_pages * page_tokens below 2^31. */
+spec_status_t spec_attend_q4(const void *q, const void *k_new, const void *v_new, const uint32_t *masks,
+                             const void *cache, const int32_t *block_table, const int32_t *lengths, int B, int N,
+                             int Hq, int Hkv, int D, int page_tokens, int num_pages, int max_pages, int k_shift,
+                             int v_shift, float scale, void *out, float *lse, void *workspace,
+                             size_t workspace_bytes, void *stream);
+
+/* Penalties, biases and grammar masks on the logits of a verification (the
+ * target's rows) or of a drafting step.
+ *
+ *   logits, out [B, R, V] (dtype): out may be logits (in place) or must not
+ *       overlap it.
+ *   history [B, H] int32 or NULL: tokens so far; the first prompt_lengths[b]
+ *       are the prompt (NULL: none), up to history_lengths[b] (clipped to
+ *       0..H) count.
+ *   repetition, frequency, presence [B] float32, each or NULL (1, 0, 0).
+ *   node_tokens [B, Nt] int32 or NULL: proposed tokens that rows see beside the
+ *       history.  Without masks row r sees node_tokens[b, 0..r-1] (a chain's
+ *       row r follows r drafts; Nt >= R - 1); with masks [B, R, ceil(R/32)]
+ *       uint32 (spec_tree_mask's, Nt = R) row r sees the nodes whose bits are
+ *       set, node 0 excepted (the root is the history's last token).
+ *   bias_tokens [B, M] int32, bias_values [B, M] float32, or both NULL: a
+ *       token's biases are added in the list's order.
+ *   allowed [B, R, ceil(V/32)] uint32 or NULL: bit v % 32 of word v / 32 lets
+ *       row r take token v.
+ *
+ * With n = the times v was generated (history behind the prompt) or is seen as
+ * a proposed token, in fp32 and rounded to the dtype once:
+ *   l = logit; if v is in the prompt or n > 0: l = l > 0 ? l / repetition
+ *   : l * repetition; if n > 0: l -= frequency * n + presence; l += biases;
+ *   l = -inf where v is not allowed.
+ * Tokens outside [0, V) are ignored, wherever they stand.  Limits: R <= 1024,
+ * Nt <= 1024, V <= 2^30. */
+spec_status_t spec_adjust_logits(const void *logits, spec_dtype_t dtype, const int32_t *history,
+                                 const int32_t *prompt_lengths, const int32_t *history_lengths,
+                                 const float *repetition, const float *frequency, const float *presence,
+                                 const int32_t *node_tokens, const uint32_t *masks, const int32_t *bias_tokens,
+                                 const float *bias_values, const uint32_t *allowed, int B, int R, int V, int H, int Nt,
+                                 int M, void *out, void *stream);
+
 /* Timing hooks for benchmarks: while enabled, each verify call records CUDA
  * events on the call's stream around its kernels (at most max_calls calls are
  * recorded).  spec_profile_end synchronises on the recorded events and returns

@@ -10,6 +10,7 @@ is missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 import threading
@@ -71,6 +72,20 @@ def lib() -> ctypes.CDLL:
             L.spec_row_stats.restype = I
             L.spec_tree_draft.argtypes = [P, I, P, I, I, I, I, F, P, P, P]
             L.spec_tree_draft.restype = I
+            L.spec_q4_block_bytes.argtypes = [I]
+            L.spec_q4_block_bytes.restype = Z
+            L.spec_page_map.argtypes = [P] * 6 + [I] * 5 + [P] * 7
+            L.spec_page_map.restype = I
+            L.spec_kv_store_q4.argtypes = [P] * 3 + [I] * 7 + [P] * 2
+            L.spec_kv_store_q4.restype = I
+            L.spec_kv_commit_q4.argtypes = [P] * 7 + [I] * 10 + [P] * 2
+            L.spec_kv_commit_q4.restype = I
+            L.spec_attend_workspace_bytes.argtypes = [I] * 5
+            L.spec_attend_workspace_bytes.restype = Z
+            L.spec_attend_q4.argtypes = [P] * 7 + [I] * 10 + [F, P, P, P, Z, P]
+            L.spec_attend_q4.restype = I
+            L.spec_adjust_logits.argtypes = [P, I] + [P] * 11 + [I] * 6 + [P] * 2
+            L.spec_adjust_logits.restype = I
             L.spec_profile_begin.argtypes = [I]
             L.spec_profile_begin.restype = I
             L.spec_profile_end.argtypes = [P, P, P]
@@ -87,7 +102,7 @@ def declared_functions() -> list[str]:
     """Names of the functions include/spec_verify.h declares."""
     with open(HEADER) as f:
         text = re.sub(r"/\*.*?\*/", "", f.read(), flags=re.S)
-    return sorted(set(re.findall(r"\b(spec_[a-z_]+)\s*\(", text)))
+    return sorted(set(re.findall(r"\b(spec_[a-z0-9_]+)\s*\(", text)))
 
 
 def status_string(status: int) -> str:
@@ -356,6 +371,194 @@ def spec_tree_draft(draft_logits, parents, temperature, max_children: int, *, no
                                _stream(stream))
     _check("spec_tree_draft", st)
     return node_tokens, node_logq
+
+
+# ---------------------------------------------------------------------------
+# serving steps around verification
+#
+# These check every tensor's type and shape (the C side gets bare pointers), run
+# with the tensors' device current, and allocate outputs that are not supplied on
+# the stream that the call uses.
+# ---------------------------------------------------------------------------
+def _take(t, name: str, dtype, shape, dev):
+    """A tensor argument: type, shape (None: any size there), device, layout.
+    Its address; None for an argument that is None."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    s = t.shape
+    if len(s) != len(shape) or any(w is not None and w != h for w, h in zip(shape, s)):
+        raise ValueError(f"{name} must have shape {tuple('any' if w is None else w for w in shape)}, got {tuple(s)}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _serve(fn):
+    """Runs a serving call on its tensors' device and the given stream."""
+    @functools.wraps(fn)
+    def call(first, *args, stream=None, **kw):
+        if not isinstance(first, torch.Tensor) or not first.is_cuda:
+            raise ValueError(f"{fn.__name__}: tensors must be CUDA tensors")
+        dev = first.device
+        if stream is None and dev.index == torch.cuda.current_device():
+            return fn(first, *args, stream=torch._C._cuda_getCurrentRawStream(dev.index), **kw)
+        if stream is not None and stream.device != dev:
+            raise ValueError(f"{fn.__name__}: the stream is on {stream.device}, the tensors on {dev}")
+        with torch.cuda.device(dev), torch.cuda.stream(stream):
+            return fn(first, *args, stream=torch.cuda.current_stream(dev).cuda_stream, **kw)
+    return call
+
+
+def _out(t, name: str, dtype, shape, dev):
+    """An output: the one supplied, or a new one."""
+    return t if t is not None else torch.empty(shape, dtype=dtype, device=dev)
+
+
+def spec_q4_block_bytes(D: int) -> int:
+    """Bytes of a block of 32 tokens of one kv head (36 * D); 0 if D is not 64 or 128."""
+    return int(lib().spec_q4_block_bytes(D))
+
+
+def spec_attend_workspace_bytes(B: int, N: int, Hq: int, Hkv: int, D: int) -> int:
+    return int(lib().spec_attend_workspace_bytes(B, N, Hq, Hkv, D))
+
+
+def q4_cache(num_pages: int, Hkv: int, page_tokens: int, D: int, device) -> torch.Tensor:
+    """An empty 4-bit cache [num_pages, Hkv, page_tokens / 32, 36 * D] (bytes)."""
+    if page_tokens % 32 or D not in (64, 128):
+        raise ValueError("page_tokens must be a multiple of 32 and D 64 or 128")
+    return torch.zeros((num_pages, Hkv, page_tokens // 32, 36 * D), dtype=torch.uint8, device=device)
+
+
+def _q4_shape(cache, name="cache"):
+    """(pages, Hkv, page_tokens, D) of a cache tensor."""
+    if cache.dim() != 4 or cache.shape[3] % 36:
+        raise ValueError(f"{name} must be [pages, Hkv, page_tokens / 32, 36 * D], got {tuple(cache.shape)}")
+    return cache.shape[0], cache.shape[1], 32 * cache.shape[2], cache.shape[3] // 36
+
+
+@_serve
+def spec_page_map(lengths, count, held, ring, ring_state, block_table, page_tokens: int, max_tokens: int, *,
+                  offsets=None, slots=None, positions=None, new_held=None, new_ring_state=None, status=None,
+                  stream=None):
+    """Block tables and slot maps from the requests' lengths.  lengths, count, held
+    [B] int32; ring [F], ring_state [2], block_table [B, W] int32 (ring and table
+    updated in place).  Returns (offsets [B+1], slots [max_tokens], positions
+    [max_tokens], new_held [B], new_ring_state [2], status [B]), all int32."""
+    dev, i32 = lengths.device, torch.int32
+    B = lengths.numel()
+    offsets = _out(offsets, "offsets", i32, (B + 1,), dev)
+    slots = _out(slots, "slots", i32, (max_tokens,), dev)
+    positions = _out(positions, "positions", i32, (max_tokens,), dev)
+    new_held = _out(new_held, "new_held", i32, (B,), dev)
+    new_ring_state = _out(new_ring_state, "new_ring_state", i32, (2,), dev)
+    status = _out(status, "status", i32, (B,), dev)
+    st = lib().spec_page_map(
+        _take(lengths, "lengths", i32, (B,), dev), _take(count, "count", i32, (B,), dev), _take(held, "held", i32, (B,), dev),
+        _take(ring, "ring", i32, (None,), dev), _take(ring_state, "ring_state", i32, (2,), dev),
+        _take(block_table, "block_table", i32, (B, None), dev), B, ring.shape[0], page_tokens, block_table.shape[1], max_tokens,
+        _take(offsets, "offsets", i32, (B + 1,), dev), _take(slots, "slots", i32, (max_tokens,), dev),
+        _take(positions, "positions", i32, (max_tokens,), dev), _take(new_held, "new_held", i32, (B,), dev),
+        _take(new_ring_state, "new_ring_state", i32, (2,), dev), _take(status, "status", i32, (B,), dev), stream)
+    _check("spec_page_map", st)
+    return offsets, slots, positions, new_held, new_ring_state, status
+
+
+@_serve
+def spec_kv_store_q4(k, v, slots, cache, *, k_shift: int = 0, v_shift: int = 0, stream=None):
+    """Entries t of k and v [T, Hkv, D] bf16 into the 4-bit cache at slots[t]
+    ([T] int32; a slot outside the cache is skipped).  Returns the cache."""
+    pages, Hkv, P, D = _q4_shape(cache)
+    dev, T = k.device, k.shape[0]
+    st = lib().spec_kv_store_q4(
+        _take(k, "k", torch.bfloat16, (T, Hkv, D), dev), _take(v, "v", torch.bfloat16, (T, Hkv, D), dev),
+        _take(slots, "slots", torch.int32, (T,), dev), T, Hkv, D, P, pages, k_shift, v_shift,
+        _take(cache, "cache", torch.uint8, (None,) * 4, dev), stream)
+    _check("spec_kv_store_q4", st)
+    return cache
+
+
+@_serve
+def spec_kv_commit_q4(cache, block_table, lengths, k, v, count, *, path=None, new_lengths=None, k_shift: int = 0,
+                      v_shift: int = 0, stream=None):
+    """Appends accepted entries of k and v [B, N, Hkv, D] bf16 to the paged 4-bit
+    cache behind lengths [B]: entries path[b, :count[b]] ([B, W] int32), or the
+    first count[b] without a path.  block_table [B, pages].  Returns new_lengths."""
+    pages, Hkv, P, D = _q4_shape(cache)
+    dev, i32 = cache.device, torch.int32
+    B, N = k.shape[:2]
+    new_lengths = _out(new_lengths, "new_lengths", i32, (B,), dev)
+    st = lib().spec_kv_commit_q4(
+        _take(cache, "cache", torch.uint8, (None,) * 4, dev), _take(block_table, "block_table", i32, (B, None), dev),
+        _take(lengths, "lengths", i32, (B,), dev), _take(k, "k", torch.bfloat16, (B, N, Hkv, D), dev),
+        _take(v, "v", torch.bfloat16, (B, N, Hkv, D), dev), _take(path, "path", i32, (B, None), dev),
+        _take(count, "count", i32, (B,), dev), B, N, 0 if path is None else path.shape[1], Hkv, D, P, pages,
+        block_table.shape[1], k_shift, v_shift, _take(new_lengths, "new_lengths", i32, (B,), dev), stream)
+    _check("spec_kv_commit_q4", st)
+    return new_lengths
+
+
+@_serve
+def spec_attend_q4(q, cache, block_table, lengths, *, k_new=None, v_new=None, masks=None, scale=None, k_shift: int = 0,
+                   v_shift: int = 0, out=None, lse=None, workspace_buf=None, stream=None):
+    """Attention of N nodes per sequence over the paged 4-bit cache and the nodes'
+    own entries.  q [B, N, Hq, D], k_new / v_new [B, N, Hkv, D] bf16 (or neither),
+    masks [B, N, ceil(N/32)] int32 (spec_tree_mask's; None: a chain), block_table
+    [B, pages], lengths [B] int32; scale defaults to 1 / sqrt(D).  Returns (out
+    [B, N, Hq, D] bf16, lse [B, N, Hq] f32)."""
+    pages, Hkv, P, D = _q4_shape(cache)
+    dev, i32, bf = q.device, torch.int32, torch.bfloat16
+    if q.dim() != 4:
+        raise ValueError(f"q must be [B, N, Hq, D], got {tuple(q.shape)}")
+    B, N, Hq = q.shape[:3]
+    out = _out(out, "out", bf, (B, N, Hq, D), dev)
+    lse = _out(lse, "lse", torch.float32, (B, N, Hq), dev)
+    if workspace_buf is None:
+        workspace_buf = workspace(spec_attend_workspace_bytes(B, N, Hq, Hkv, D), dev)
+    st = lib().spec_attend_q4(
+        _take(q, "q", bf, (B, N, Hq, D), dev), _take(k_new, "k_new", bf, (B, N, Hkv, D), dev),
+        _take(v_new, "v_new", bf, (B, N, Hkv, D), dev), _take(masks, "masks", i32, (B, N, (N + 31) // 32), dev),
+        _take(cache, "cache", torch.uint8, (None,) * 4, dev), _take(block_table, "block_table", i32, (B, None), dev),
+        _take(lengths, "lengths", i32, (B,), dev), B, N, Hq, Hkv, D, P, pages, block_table.shape[1], k_shift, v_shift,
+        D ** -0.5 if scale is None else scale, _take(out, "out", bf, (B, N, Hq, D), dev),
+        _take(lse, "lse", torch.float32, (B, N, Hq), dev), _take(workspace_buf, "workspace_buf", torch.uint8, (None,), dev),
+        workspace_buf.numel(), stream)
+    _check("spec_attend_q4", st)
+    return out, lse
+
+
+@_serve
+def spec_adjust_logits(logits, *, out=None, history=None, prompt_lengths=None, history_lengths=None, repetition=None,
+                       frequency=None, presence=None, node_tokens=None, masks=None, bias_tokens=None,
+                       bias_values=None, allowed=None, stream=None):
+    """Penalties, biases and grammar masks on logits [B, R, V] (bf16/f32).  history
+    [B, H] int32 with prompt_lengths and history_lengths [B]; repetition,
+    frequency, presence [B] f32; node_tokens [B, Nt] int32 (row r sees the first r
+    of them, or with masks [B, R, ceil(R/32)] int32 the row's ancestors);
+    bias_tokens / bias_values [B, M]; allowed [B, R, ceil(V/32)] int32 bit words.
+    out may be logits.  Returns out."""
+    if logits.dim() != 3:
+        raise ValueError(f"logits must be [B, R, V], got {tuple(logits.shape)}")
+    B, R, V = logits.shape
+    dev, i32, f32 = logits.device, torch.int32, torch.float32
+    code = _dtype_code(logits)
+    out = _out(out, "out", logits.dtype, (B, R, V), dev)
+    st = lib().spec_adjust_logits(
+        _take(logits, "logits", logits.dtype, (B, R, V), dev), code, _take(history, "history", i32, (B, None), dev),
+        _take(prompt_lengths, "prompt_lengths", i32, (B,), dev), _take(history_lengths, "history_lengths", i32, (B,), dev),
+        _take(repetition, "repetition", f32, (B,), dev), _take(frequency, "frequency", f32, (B,), dev),
+        _take(presence, "presence", f32, (B,), dev), _take(node_tokens, "node_tokens", i32, (B, None), dev),
+        _take(masks, "masks", i32, (B, R, (R + 31) // 32), dev), _take(bias_tokens, "bias_tokens", i32, (B, None), dev),
+        _take(bias_values, "bias_values", f32, (B, None if bias_tokens is None else bias_tokens.shape[1]), dev),
+        _take(allowed, "allowed", i32, (B, R, (V + 31) // 32), dev), B, R, V, 0 if history is None else history.shape[1],
+        0 if node_tokens is None else node_tokens.shape[1], 0 if bias_tokens is None else bias_tokens.shape[1],
+        _take(out, "out", logits.dtype, (B, R, V), dev), stream)
+    _check("spec_adjust_logits", st)
+    return out
 
 
 def spec_profile_begin(max_calls: int):

@@ -1,7 +1,9 @@
 """Build the CUDA library (libspecverify.so) in-tree with nvcc for sm_103a.
 
-One translation unit; host code is plain C++17, device code targets
-``compute_103a`` / ``sm_103a`` only.  The result sits next to this file and is
+Two translation units (verification and its neighbours in spec_verify.cu, the
+paged 4-bit cache and the logit adjustments in serving.cu), compiled in
+parallel; host code is plain C++17, device code targets ``compute_103a`` /
+``sm_103a`` only.  The result sits next to this file and is
 what the Python binding loads.
 """
 from __future__ import annotations
@@ -38,8 +40,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-shared",
-           "-I", INCLUDE, "-o", tmp, os.path.join(CSRC, "spec_verify.cu")]
+    units = [os.path.join(CSRC, f) for f in ("spec_verify.cu", "serving.cu")]
+    cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "--threads", "0", "-Xcompiler", "-fPIC", "-shared",
+           "-I", INCLUDE, "-o", tmp, *units]
     if verbose:
         cmd.insert(1, "-Xptxas=-v")
     subprocess.run(cmd, check=True)

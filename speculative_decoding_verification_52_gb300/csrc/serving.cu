@@ -1,0 +1,397 @@
+// serving.cu -- host side of the serving steps around verification declared in
+// include/spec_verify.h: the paged 4-bit cache (page map, store, commit,
+// attention) and the logit adjustments.  Argument checks, launch shapes,
+// dispatch; one or two launches a call on the caller's stream, no sync.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "adjust.cuh"
+#include "attend_q4.cuh"
+#include "common.cuh"
+#include "host.cuh"
+#include "kv_q4.cuh"
+#include "page_map.cuh"
+#include "spec_verify.h"
+
+namespace {
+
+using namespace sv;
+using namespace svh;
+
+constexpr int kMaxShift = 32;
+constexpr int kSmemPerSm = 227 * 1024;   // shared memory that the CTAs of an SM can use together
+
+bool q4_dim(int D) { return D == 64 || D == 128; }
+bool below_2g(long long a, long long b) { return a * b < (1LL << 31); }
+
+spec_status_t check_q4(int Hkv, int D, int P, int pages, int k_shift, int v_shift) {
+  if (!q4_dim(D)) return fail(SPEC_ERR_UNSUPPORTED, "D=%d: the 4-bit cache takes 64 or 128", D);
+  if (Hkv < 1 || P < 1 || pages < 1) return fail(SPEC_ERR_INVALID_ARG, "bad sizes Hkv=%d page_tokens=%d num_pages=%d", Hkv, P, pages);
+  if (P % Q4_BLOCK != 0) return fail(SPEC_ERR_INVALID_ARG, "page_tokens=%d is not a multiple of %d", P, Q4_BLOCK);
+  if (!below_2g(P, pages)) return fail(SPEC_ERR_UNSUPPORTED, "num_pages * page_tokens must stay below 2^31");
+  if (std::abs(k_shift) > kMaxShift || std::abs(v_shift) > kMaxShift)
+    return fail(SPEC_ERR_INVALID_ARG, "shifts (%d, %d) outside [-%d, %d]", k_shift, v_shift, kMaxShift, kMaxShift);
+  return SPEC_OK;
+}
+
+// ---------------------------------------------------------------------------
+// attention
+// ---------------------------------------------------------------------------
+// rows of a warp's tile, in units of 16: two where there are more rows than one
+// tile holds, so that a block is fetched and unpacked once for 32 of them
+int attend_tiles(int rows) { return rows <= 16 ? 1 : 2; }
+constexpr int kMaxSms = 160;   // bound of the workspace size; the grid never exceeds it
+constexpr int attend_ctas(int RT) { return RT == 1 ? 3 : 2; }   // CTAs an SM (register use)
+
+template <int D, int RT>
+spec_status_t launch_attend(const DevInfo& di, int dev, AttendArgs a, cudaStream_t st) {
+  auto kern = attend_q4_kernel<D, RT>;
+  constexpr int ctas = attend_ctas(RT);
+  const size_t fixed = static_cast<size_t>(AT_WARPS) * at_q_bytes(D, RT) + 8 * (static_cast<size_t>(a.B) + 1);
+  const size_t stage = static_cast<size_t>(AT_WARPS) * (at_stage_bytes(D) + 8);
+  // as many stages (at most 6) as leave room for all CTAs; 1 KB a CTA is the system's
+  const size_t room = kSmemPerSm / ctas - 1024;
+  const int stages = static_cast<int>(std::min<size_t>(6, std::max<size_t>(2, room > fixed ? (room - fixed) / stage : 0)));
+  const size_t smem = fixed + stages * stage;
+  if (!once_per_device(dev, [&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerSm - 1024) == cudaSuccess;
+      }))
+    return fail(SPEC_ERR_CUDA, "attention kernel setup failed: %s", cudaGetErrorString(cudaGetLastError()));
+  const int grid = std::min(di.sms, kMaxSms) * ctas;
+  kern<<<grid, AT_THREADS, smem, st>>>(a, stages);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "attention launch");
+  const long long triples = static_cast<long long>(a.B) * a.Hkv * a.row_tiles;
+  const int jgrid = static_cast<int>(std::min<long long>(triples, static_cast<long long>(di.sms) * 8));
+  attend_q4_join_kernel<D, RT><<<jgrid, AJN_THREADS, 8 * (static_cast<size_t>(a.B) + 1), st>>>(a, grid * AT_WARPS);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "attention join launch");
+  return SPEC_OK;
+}
+
+// ---------------------------------------------------------------------------
+// logit adjustments
+// ---------------------------------------------------------------------------
+template <class T, bool VEC>
+spec_status_t launch_adjust(int dev, unsigned grid, const AdjustArgs& a, cudaStream_t st) {
+  auto kern = adjust_logits_kernel<T, VEC>;
+  if (!once_per_device(dev, [&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 6 * AJ_MAX_CHUNK) == cudaSuccess;
+      }))
+    return fail(SPEC_ERR_CUDA, "logit adjustment setup failed: %s", cudaGetErrorString(cudaGetLastError()));
+  const long long marks = (a.nodes ? a.Nt : 0) + static_cast<long long>(a.bias_tokens ? a.M : 0);
+  const size_t smem = 4 * static_cast<size_t>(a.chunk) + 2 * static_cast<size_t>(std::min<long long>(a.chunk, marks));
+  kern<<<grid, AJ_THREADS, smem, st>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "logit adjustment launch");
+  return SPEC_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t spec_q4_block_bytes(int D) { return q4_dim(D) ? static_cast<size_t>(q4_block_bytes(D)) : 0; }
+
+spec_status_t spec_page_map(const int32_t* lengths, const int32_t* count, const int32_t* held, int32_t* ring,
+                            const int32_t* ring_state, int32_t* block_table, int B, int ring_size, int page_tokens,
+                            int max_pages, int max_tokens, int32_t* offsets, int32_t* slots, int32_t* positions,
+                            int32_t* new_held, int32_t* new_ring_state, int32_t* status, void* stream) {
+  try {
+    if (B < 0 || ring_size < 1 || page_tokens < 1 || max_pages < 1 || max_tokens < 0)
+      return fail(SPEC_ERR_INVALID_ARG, "bad sizes B=%d ring_size=%d page_tokens=%d max_pages=%d max_tokens=%d", B,
+                  ring_size, page_tokens, max_pages, max_tokens);
+    if (!below_2g(ring_size, page_tokens) || !below_2g(max_pages, page_tokens))
+      return fail(SPEC_ERR_UNSUPPORTED, "ring_size and max_pages times page_tokens must stay below 2^31");
+    if (B == 0) return SPEC_OK;
+    if (!lengths || !count || !held || !ring || !ring_state || !block_table || !offsets || !new_held ||
+        !new_ring_state || !status || (max_tokens > 0 && (!slots || !positions)))
+      return fail(SPEC_ERR_INVALID_ARG, "NULL pointer argument");
+    if (new_held == held || new_ring_state == ring_state)
+      return fail(SPEC_ERR_INVALID_ARG, "new_held / new_ring_state must not be held / ring_state");
+    int dev;
+    DevInfo di;
+    spec_status_t s = device_info(di, dev);
+    if (s != SPEC_OK) return s;
+    PageMapArgs a{};
+    a.lengths = lengths;
+    a.count = count;
+    a.held = held;
+    a.ring = ring;
+    a.ring_state = ring_state;
+    a.table = block_table;
+    a.B = B;
+    a.F = ring_size;
+    a.P = page_tokens;
+    a.W = max_pages;
+    a.T = max_tokens;
+    a.offsets = offsets;
+    a.slots = slots;
+    a.positions = positions;
+    a.new_held = new_held;
+    a.new_ring_state = new_ring_state;
+    a.status = status;
+    a.vec = aligned16(slots) && aligned16(positions);
+    const int grid = std::max(1, ceil_div(max_tokens, PM_TILE));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    prof_mark(0, st);
+    page_map_kernel<<<grid, PM_THREADS, 0, st>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "page map launch");
+    prof_mark(1, st);
+    prof_mark(2, st);
+    return SPEC_OK;
+  } catch (...) {
+    return fail(SPEC_ERR_CUDA, "unexpected host exception");
+  }
+}
+
+spec_status_t spec_kv_store_q4(const void* k, const void* v, const int32_t* slots, int T, int Hkv, int D,
+                               int page_tokens, int num_pages, int k_shift, int v_shift, void* cache, void* stream) {
+  try {
+    spec_status_t s = check_q4(Hkv, D, page_tokens, num_pages, k_shift, v_shift);
+    if (s != SPEC_OK) return s;
+    if (T < 0) return fail(SPEC_ERR_INVALID_ARG, "T=%d must be >= 0", T);
+    if (Hkv > 65535) return fail(SPEC_ERR_UNSUPPORTED, "Hkv=%d beyond 65535", Hkv);
+    if (T == 0) return SPEC_OK;
+    if (!k || !v || !slots || !cache) return fail(SPEC_ERR_INVALID_ARG, "NULL k/v/slots/cache");
+    if (!aligned16(k) || !aligned16(v) || !aligned16(cache))
+      return fail(SPEC_ERR_INVALID_ARG, "k, v and cache must be 16-byte aligned");
+    int dev;
+    DevInfo di;
+    s = device_info(di, dev);
+    if (s != SPEC_OK) return s;
+    KvQ4Args a{};
+    a.k = static_cast<const uint16_t*>(k);
+    a.v = static_cast<const uint16_t*>(v);
+    a.cache = static_cast<unsigned char*>(cache);
+    a.slots = slots;
+    a.T = T;
+    a.Hkv = Hkv;
+    a.P = page_tokens;
+    a.pages = num_pages;
+    a.k_mul = std::ldexp(1.f, -k_shift);
+    a.v_mul = std::ldexp(1.f, -v_shift);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const dim3 grid(static_cast<unsigned>(ceil_div(T, Q4_THREADS / (D / 16))), static_cast<unsigned>(Hkv));
+    prof_mark(0, st);
+    if (D == 128) kv_store_q4_kernel<128><<<grid, Q4_THREADS, 0, st>>>(a);
+    else kv_store_q4_kernel<64><<<grid, Q4_THREADS, 0, st>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "kv store launch");
+    prof_mark(1, st);
+    prof_mark(2, st);
+    return SPEC_OK;
+  } catch (...) {
+    return fail(SPEC_ERR_CUDA, "unexpected host exception");
+  }
+}
+
+spec_status_t spec_kv_commit_q4(void* cache, const int32_t* block_table, const int32_t* lengths, const void* k,
+                                const void* v, const int32_t* path, const int32_t* count, int B, int N, int W, int Hkv,
+                                int D, int page_tokens, int num_pages, int max_pages, int k_shift, int v_shift,
+                                int32_t* new_lengths, void* stream) {
+  try {
+    spec_status_t s = check_q4(Hkv, D, page_tokens, num_pages, k_shift, v_shift);
+    if (s != SPEC_OK) return s;
+    if (B < 0 || N < 1 || max_pages < 1 || (path && W < 1))
+      return fail(SPEC_ERR_INVALID_ARG, "bad sizes B=%d N=%d W=%d max_pages=%d", B, N, W, max_pages);
+    if (!below_2g(max_pages, page_tokens)) return fail(SPEC_ERR_UNSUPPORTED, "max_pages * page_tokens must stay below 2^31");
+    if (B == 0) return SPEC_OK;
+    if (!cache || !block_table || !lengths || !k || !v || !count || !new_lengths)
+      return fail(SPEC_ERR_INVALID_ARG, "NULL cache/block_table/lengths/k/v/count/new_lengths");
+    if (new_lengths == lengths) return fail(SPEC_ERR_INVALID_ARG, "new_lengths must not be lengths");
+    if (!aligned16(k) || !aligned16(v) || !aligned16(cache))
+      return fail(SPEC_ERR_INVALID_ARG, "k, v and cache must be 16-byte aligned");
+    int dev;
+    DevInfo di;
+    s = device_info(di, dev);
+    if (s != SPEC_OK) return s;
+    KvQ4Args a{};
+    a.k = static_cast<const uint16_t*>(k);
+    a.v = static_cast<const uint16_t*>(v);
+    a.cache = static_cast<unsigned char*>(cache);
+    a.table = block_table;
+    a.lengths = lengths;
+    a.path = path;
+    a.count = count;
+    a.new_lengths = new_lengths;
+    a.B = B;
+    a.N = N;
+    a.W = max_pages;
+    a.PW = path ? W : 0;
+    a.Hkv = Hkv;
+    a.P = page_tokens;
+    a.pages = num_pages;
+    a.k_mul = std::ldexp(1.f, -k_shift);
+    a.v_mul = std::ldexp(1.f, -v_shift);
+    // enough CTAs a sequence for its largest request, no more than fill the device
+    const long long items = static_cast<long long>(path ? W : N) * Hkv * (D / 16);
+    const long long want = (items + Q4_THREADS - 1) / Q4_THREADS;
+    const long long cap = std::max(1, di.sms * 16 / B);
+    const dim3 grid(static_cast<unsigned>(B), static_cast<unsigned>(std::min(std::min(want, cap), 65535LL)));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    prof_mark(0, st);
+    if (D == 128) kv_commit_q4_kernel<128><<<grid, Q4_THREADS, 0, st>>>(a);
+    else kv_commit_q4_kernel<64><<<grid, Q4_THREADS, 0, st>>>(a);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "kv commit launch");
+    prof_mark(1, st);
+    prof_mark(2, st);
+    return SPEC_OK;
+  } catch (...) {
+    return fail(SPEC_ERR_CUDA, "unexpected host exception");
+  }
+}
+
+size_t spec_attend_workspace_bytes(int B, int N, int Hq, int Hkv, int D) {
+  if (B < 0 || B > AT_MAX_B || N < 1 || N > SPEC_MAX_TREE_NODES || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 ||
+      Hq / Hkv > 64 || !q4_dim(D))
+    return 0;
+  const int RT = attend_tiles(N * (Hq / Hkv));
+  const size_t shares = static_cast<size_t>(kMaxSms) * attend_ctas(RT) * AT_WARPS;
+  return align_up(shares * 2 * at_partial_floats(D, RT) * sizeof(float), 256);
+}
+
+spec_status_t spec_attend_q4(const void* q, const void* k_new, const void* v_new, const uint32_t* masks,
+                             const void* cache, const int32_t* block_table, const int32_t* lengths, int B, int N,
+                             int Hq, int Hkv, int D, int page_tokens, int num_pages, int max_pages, int k_shift,
+                             int v_shift, float scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                             void* stream) {
+  try {
+    spec_status_t s = check_q4(Hkv, D, page_tokens, num_pages, k_shift, v_shift);
+    if (s != SPEC_OK) return s;
+    if (B < 0 || N < 1 || N > SPEC_MAX_TREE_NODES || max_pages < 1)
+      return fail(SPEC_ERR_INVALID_ARG, "bad sizes B=%d N=%d max_pages=%d (N in [1, %d])", B, N, max_pages, SPEC_MAX_TREE_NODES);
+    if (Hq < 1 || Hq % Hkv != 0) return fail(SPEC_ERR_INVALID_ARG, "Hq=%d is not a multiple of Hkv=%d", Hq, Hkv);
+    if (Hq / Hkv > 64) return fail(SPEC_ERR_UNSUPPORTED, "%d query heads to a kv head: at most 64", Hq / Hkv);
+    if (B > AT_MAX_B) return fail(SPEC_ERR_UNSUPPORTED, "B=%d beyond %d", B, AT_MAX_B);
+    if (!below_2g(max_pages, page_tokens)) return fail(SPEC_ERR_UNSUPPORTED, "max_pages * page_tokens must stay below 2^31");
+    if (!std::isfinite(scale)) return fail(SPEC_ERR_INVALID_ARG, "scale must be finite");
+    if ((k_new == nullptr) != (v_new == nullptr)) return fail(SPEC_ERR_INVALID_ARG, "k_new and v_new come together");
+    if (masks && !k_new) return fail(SPEC_ERR_INVALID_ARG, "masks without k_new and v_new");
+    if (B == 0) return SPEC_OK;
+    if (!q || !cache || !block_table || !lengths || !out) return fail(SPEC_ERR_INVALID_ARG, "NULL q/cache/block_table/lengths/out");
+    if (!aligned16(q) || !aligned16(cache) || !aligned16(out) || !aligned16(k_new) || !aligned16(v_new))
+      return fail(SPEC_ERR_INVALID_ARG, "q, k_new, v_new, cache and out must be 16-byte aligned");
+    s = check_ws(workspace, workspace_bytes, spec_attend_workspace_bytes(B, N, Hq, Hkv, D));
+    if (s != SPEC_OK) return s;
+    int dev;
+    DevInfo di;
+    s = device_info(di, dev);
+    if (s != SPEC_OK) return s;
+    AttendArgs a{};
+    a.q = static_cast<const uint16_t*>(q);
+    a.k_new = static_cast<const uint16_t*>(k_new);
+    a.v_new = static_cast<const uint16_t*>(v_new);
+    a.masks = masks;
+    a.cache = static_cast<const unsigned char*>(cache);
+    a.table = block_table;
+    a.lengths = lengths;
+    a.B = B;
+    a.N = N;
+    a.G = Hq / Hkv;
+    a.Hkv = Hkv;
+    a.P = page_tokens;
+    a.pages = num_pages;
+    a.W = max_pages;
+    a.NW = (N + 31) / 32;
+    const int rows = N * a.G, RT = attend_tiles(rows);
+    a.row_tiles = ceil_div(rows, 16 * RT);
+    a.scale_log2 = static_cast<float>(1.4426950408889634 * static_cast<double>(scale));
+    a.k_mul = std::ldexp(1.f, k_shift);
+    a.v_mul = std::ldexp(1.f, v_shift);
+    a.out = static_cast<uint16_t*>(out);
+    a.lse = lse;
+    a.ws = static_cast<float*>(workspace);
+    a.timeout_ns = kWaitNs;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    prof_mark(0, st);
+    if (D == 128) s = RT == 1 ? launch_attend<128, 1>(di, dev, a, st) : launch_attend<128, 2>(di, dev, a, st);
+    else s = RT == 1 ? launch_attend<64, 1>(di, dev, a, st) : launch_attend<64, 2>(di, dev, a, st);
+    if (s != SPEC_OK) return s;
+    prof_mark(1, st);
+    prof_mark(2, st);
+    return SPEC_OK;
+  } catch (...) {
+    return fail(SPEC_ERR_CUDA, "unexpected host exception");
+  }
+}
+
+spec_status_t spec_adjust_logits(const void* logits, spec_dtype_t dtype, const int32_t* history,
+                                 const int32_t* prompt_lengths, const int32_t* history_lengths,
+                                 const float* repetition, const float* frequency, const float* presence,
+                                 const int32_t* node_tokens, const uint32_t* masks, const int32_t* bias_tokens,
+                                 const float* bias_values, const uint32_t* allowed, int B, int R, int V, int H, int Nt,
+                                 int M, void* out, void* stream) {
+  try {
+    if (B < 0 || R < 1 || R > SPEC_MAX_TREE_NODES || V < 1 || H < 0 || Nt < 0 || Nt > SPEC_MAX_TREE_NODES || M < 0)
+      return fail(SPEC_ERR_INVALID_ARG, "bad sizes B=%d R=%d V=%d H=%d Nt=%d M=%d (R, Nt at most %d)", B, R, V, H, Nt, M,
+                  SPEC_MAX_TREE_NODES);
+    if (V > (1 << 30)) return fail(SPEC_ERR_UNSUPPORTED, "V=%d beyond 2^30", V);
+    if (!dtype_ok(dtype)) return fail(SPEC_ERR_INVALID_ARG, "bad dtype");
+    if (history && H > 0 && !history_lengths) return fail(SPEC_ERR_INVALID_ARG, "history without history_lengths");
+    if (masks && (!node_tokens || Nt != R)) return fail(SPEC_ERR_INVALID_ARG, "masks need node_tokens of R columns (Nt=%d, R=%d)", Nt, R);
+    if (node_tokens && !masks && Nt < R - 1) return fail(SPEC_ERR_INVALID_ARG, "node_tokens has %d columns for %d rows", Nt, R);
+    if ((bias_tokens == nullptr) != (bias_values == nullptr)) return fail(SPEC_ERR_INVALID_ARG, "bias_tokens and bias_values come together");
+    if (B == 0) return SPEC_OK;
+    if (!logits || !out) return fail(SPEC_ERR_INVALID_ARG, "NULL logits/out");
+    const int esz = esz_of(dtype);
+    if (reinterpret_cast<uintptr_t>(logits) % esz || reinterpret_cast<uintptr_t>(out) % esz)
+      return fail(SPEC_ERR_INVALID_ARG, "logits and out must be aligned to their elements");
+    int dev;
+    DevInfo di;
+    spec_status_t s = device_info(di, dev);
+    if (s != SPEC_OK) return s;
+    AdjustArgs a{};
+    a.logits = static_cast<const unsigned char*>(logits);
+    a.out = static_cast<unsigned char*>(out);
+    a.history = H > 0 ? history : nullptr;
+    a.prompt_len = prompt_lengths;
+    a.hist_len = history_lengths;
+    a.repetition = repetition;
+    a.frequency = frequency;
+    a.presence = presence;
+    a.nodes = Nt > 0 ? node_tokens : nullptr;
+    a.masks = masks;
+    a.bias_tokens = M > 0 ? bias_tokens : nullptr;
+    a.bias_values = bias_values;
+    a.allowed = allowed;
+    a.B = B;
+    a.R = R;
+    a.V = V;
+    a.H = H;
+    a.Nt = Nt;
+    a.NW = (R + 31) / 32;
+    a.M = M;
+    a.VW = (V + 31) / 32;
+    const bool vec = aligned16(logits) && aligned16(out) && (static_cast<long long>(V) * esz) % 16 == 0;
+    // Chunks as large as shared memory likes (a chunk counts the whole history),
+    // smaller ones where the batch alone does not give every SM two CTAs; then
+    // the rows are shared out.
+    const long long want = 2LL * di.sms;
+    a.chunk = AJ_MAX_CHUNK;
+    while (a.chunk > 2048 && static_cast<long long>(B) * ceil_div(V, a.chunk) < want) a.chunk /= 2;
+    while (a.chunk > 32 && a.chunk / 2 >= V) a.chunk /= 2;
+    a.chunks = ceil_div(V, a.chunk);
+    const long long ctas = static_cast<long long>(B) * a.chunks;
+    a.row_splits = static_cast<int>(std::max<long long>(1, std::min<long long>(R, want / std::max<long long>(1, ctas))));
+    if (ctas * a.row_splits > 0x7fffffffLL) return fail(SPEC_ERR_UNSUPPORTED, "grid too large");
+    const unsigned grid = static_cast<unsigned>(ctas * a.row_splits);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    prof_mark(0, st);
+    if (dtype == SPEC_BF16) s = vec ? launch_adjust<BF16T, true>(dev, grid, a, st) : launch_adjust<BF16T, false>(dev, grid, a, st);
+    else s = vec ? launch_adjust<F32T, true>(dev, grid, a, st) : launch_adjust<F32T, false>(dev, grid, a, st);
+    if (s != SPEC_OK) return s;
+    prof_mark(1, st);
+    prof_mark(2, st);
+    return SPEC_OK;
+  } catch (...) {
+    return fail(SPEC_ERR_CUDA, "unexpected host exception");
+  }
+}
+
+}  // extern "C"
