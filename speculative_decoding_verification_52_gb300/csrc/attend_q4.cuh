@@ -22,13 +22,20 @@
 //   that its largest element lies in [128, 256): what f16 then cannot hold is
 //   below 2^-32 of that element.
 // * No unpacked element crosses shared memory.  The products are
-//   mma.m16n8k16 with the rows as M; for q.k a thread's share of the B operand
-//   is D / 4 consecutive elements of one token (the contraction index is
-//   permuted alike in q), for p.v it is D / 8 consecutive elements of four
-//   tokens (the output columns are permuted), with the nibbles of two tokens
-//   interleaved before they are widened.  The tokens of a group of 8 are taken
-//   in the order 0 1 3 2 4 5 7 6, which spreads both kinds of reads over the
-//   banks as well as 64-byte rows allow.
+//   mma.m16n8k16 with the rows as N, eight at a time: k q^T (tokens as M), then
+//   v^T p^T (columns as M).  A thread's part of a key operand is D / 4
+//   consecutive elements of one token (the contraction index is permuted alike
+//   in q), of a value operand D / 8 consecutive elements of four tokens (the
+//   output columns are permuted), with the nibbles of two tokens interleaved
+//   before they are widened.  The weights pass from the first product's result
+//   to the second's operand by an 8 x 8 transpose across the warp.  The tokens
+//   of a group of 8 are taken in the order 0 1 3 2 4 5 7 6, which spreads both
+//   kinds of reads over the banks as well as 64-byte rows allow.
+// * Measured rates of an SM: mma.m16n8k16 1 per 2 clocks, packed f16
+//   multiplications and conversions from e2m1 2 warps a clock each.  A block
+//   (D = 128) crosses the bus in about 196 clocks; it takes 128 conversions, 128
+//   multiplications (64 clocks each) and 32 products per eight rows (64 clocks).
+//   With the rows as M, 16 at a time, eight rows cost 128 clocks of products.
 // * The weights of v are 2^(z - max + 15) in f16: the largest is 2^15, so a
 //   weight has 11 significant bits down to 2^-29 of it.  Sums are fp32.
 // * The fresh entries are bf16 with bf16's range, so their blocks use bf16
@@ -194,135 +201,145 @@ __device__ __forceinline__ float at_corr(float d) { return fmaxf(ex2_approx(d), 
 // token of a group of 8 that column j of a product stands for
 __device__ __forceinline__ int at_token(int j) { return j ^ ((j >> 1) & 1); }
 
+// 8 x 8 matrix of 16-bit elements, transposed across the warp's fragments
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
 __host__ __device__ constexpr int at_stage_bytes(int D) { return q4_block_bytes(D); }
-__host__ __device__ constexpr int at_q_bytes(int D, int RT) { return RT * (D / 16) * 512; }
-// partial: [16 RT rows x D] sums of v, then m[16 RT], l[16 RT]
-__host__ __device__ constexpr size_t at_partial_floats(int D, int RT) { return static_cast<size_t>(16 * RT) * (D + 2); }
+__host__ __device__ constexpr int at_q_bytes(int D, int NR) { return NR * (D / 32) * 512; }
+// partial: [8 NR rows x D] sums of v, then m[8 NR], l[8 NR]
+__host__ __device__ constexpr size_t at_partial_floats(int D, int NR) { return static_cast<size_t>(8 * NR) * (D + 2); }
 
 // ---------------------------------------------------------------------------
-// the state of one (sequence, head, row tile) in a warp's registers
+// the state of one (sequence, head, row tile) in a warp's registers: lane
+// (g, t) holds rows 8 j + 2 t + e and the D / 8 columns from g * D / 8
 // ---------------------------------------------------------------------------
-template <int D, int RT>
+template <int D, int NR>
 struct AtState {
-  static constexpr int CH = D / 4;    // elements of a row that a thread loads and writes
-  static constexpr int NT = D / 8;    // column groups of the output
-  float o[RT][NT][4];
-  float m[RT][2], l[RT][2];           // running maximum (log2 domain) and this lane's part of the sum
-  float c[RT][2];                     // factor from a row's f16 products to the log2 domain
+  static constexpr int MT = D / 16;   // products that cover the output's columns
+  float o[NR][MT][4];                 // [.][i][e + 2 f]: column g * D / 8 + 2 i + f of row e
+  float m[NR][2], l[NR][2];           // running maximum (log2 domain) and this lane's part of the sum
+  float c[NR][2];                     // factor from a row's f16 products to the log2 domain
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
+    for (int j = 0; j < NR; ++j) {
 #pragma unroll
-      for (int i = 0; i < NT; ++i)
+      for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) o[rt][i][k] = 0.f;
-      m[rt][0] = m[rt][1] = kNegInf;
-      l[rt][0] = l[rt][1] = 0.f;
+        for (int k = 0; k < 4; ++k) o[j][i][k] = 0.f;
+      m[j][0] = m[j][1] = kNegInf;
+      l[j][0] = l[j][1] = 0.f;
     }
   }
 
-  // z (log2 domain, -inf where masked) becomes the weights 2^(z - max + 15)
-  __device__ __forceinline__ void weigh(float (&z)[RT][4][4]) {
+  // z (log2 domain, -inf where masked; [.][.][e + 2 f]: token g + 8 f of row e)
+  // becomes the weights 2^(z - max + 15)
+  __device__ __forceinline__ void weigh(float (&z)[2][NR][4]) {
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
+    for (int j = 0; j < NR; ++j) {
+      float mn[2];
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        float mx = kNegInf;
-#pragma unroll
-        for (int nt = 0; nt < 4; ++nt) mx = fmaxf(mx, fmaxf(z[rt][nt][2 * hf], z[rt][nt][2 * hf + 1]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float mn = fmaxf(m[rt][hf], mx);
-        if (__any_sync(0xffffffffu, mn > m[rt][hf])) {
-          const float corr = mn == kNegInf ? 1.f : at_corr(m[rt][hf] - mn);
-          l[rt][hf] *= corr;
-#pragma unroll
-          for (int i = 0; i < NT; ++i) {
-            o[rt][i][2 * hf] *= corr;
-            o[rt][i][2 * hf + 1] *= corr;
-          }
-          m[rt][hf] = mn;
-        }
-        const float ref = (mn == kNegInf ? 0.f : mn) - AT_PSHIFT;
-        float sum = 0.f;
-#pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-          for (int k = 2 * hf; k < 2 * hf + 2; ++k) {
-            z[rt][nt][k] = ex2_approx(z[rt][nt][k] - ref);
-            sum += z[rt][nt][k];
-          }
-        l[rt][hf] += sum;
+      for (int e = 0; e < 2; ++e) {
+        float mx = fmaxf(fmaxf(z[0][j][e], z[0][j][e + 2]), fmaxf(z[1][j][e], z[1][j][e + 2]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+        mn[e] = fmaxf(m[j][e], mx);
       }
+      if (__any_sync(0xffffffffu, mn[0] > m[j][0] || mn[1] > m[j][1])) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float corr = mn[e] == kNegInf ? 1.f : at_corr(m[j][e] - mn[e]);
+          l[j][e] *= corr;
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            o[j][i][e] *= corr;
+            o[j][i][e + 2] *= corr;
+          }
+          m[j][e] = mn[e];
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float ref = (mn[e] == kNegInf ? 0.f : mn[e]) - AT_PSHIFT;
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int f = 0; f < 2; ++f) z[mt][j][e + 2 * f] = ex2_approx(z[mt][j][e + 2 * f] - ref);
+        l[j][e] += (z[0][j][e] + z[0][j][e + 2]) + (z[1][j][e] + z[1][j][e + 2]);
+      }
+    }
   }
 };
 
+__device__ __forceinline__ long long at_row(const AttendArgs& a, int b, int h, int r) {
+  const int n = r / a.G;
+  return ((static_cast<long long>(b) * a.N + n) * a.Hkv + h) * a.G + (r - n * a.G);
+}
+
 // Queries of a row tile: the f16 operand into the lane's own part of `qf`
 // (nothing is shared between lanes), the rows' factors into st.c.
-template <int D, int RT>
-__device__ __forceinline__ void at_load_q(const AttendArgs& a, int b, int h, int row0, int rows, uint4* qf, AtState<D, RT>& st) {
-  constexpr int CH = D / 4, KS = D / 16;
+template <int D, int NR>
+__device__ __forceinline__ void at_load_q(const AttendArgs& a, int b, int h, int row0, int rows, uint4* qf, AtState<D, NR>& st) {
+  constexpr int CH = D / 4, WK = D / 32;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt) {
-    uint32_t f[2][CH / 2];
+  for (int j = 0; j < NR; ++j) {
+    const int r = row0 + 8 * j + g;
+    uint4 w[CH / 8];
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      const int r = row0 + 16 * rt + 8 * hf + g;
-      uint4 w[CH / 8];
+    for (int i = 0; i < CH / 8; ++i) w[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (r < rows) {
+      const uint4* p = reinterpret_cast<const uint4*>(a.q + at_row(a, b, h, r) * D + t * CH);
 #pragma unroll
-      for (int i = 0; i < CH / 8; ++i) w[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (r < rows) {
-        const int n = r / a.G;
-        const long long at = ((static_cast<long long>(b) * a.N + n) * a.Hkv + h) * a.G + (r - n * a.G);
-        const uint4* p = reinterpret_cast<const uint4*>(a.q + at * D + t * CH);
-#pragma unroll
-        for (int i = 0; i < CH / 8; ++i) w[i] = __ldg(p + i);
-      }
-      uint32_t mx = 0u;
-#pragma unroll
-      for (int i = 0; i < CH / 8; ++i) {
-        mx = bf16x2_max_nan(mx, bf16x2_max_nan(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu));
-        mx = bf16x2_max_nan(mx, bf16x2_max_nan(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
-      }
-      float top = fmax_nan(__uint_as_float(mx << 16), __uint_as_float(mx & 0xffff0000u));
-      top = fmax_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmax_nan(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-      const int sh = top > 0.f ? min(7 - e, 100) : 0;
-      const float mul = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
-      // a row with a NaN or an infinity has no finite scores: the factor says so
-      st.c[rt][hf] = top < __builtin_huge_valf()
-                         ? a.scale_log2 * a.k_mul * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23)
-                         : __int_as_float(0x7fc00000);
-#pragma unroll
-      for (int i = 0; i < CH / 8; ++i) {
-        const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          f[hf][4 * i + j] = f16x2_pack(__uint_as_float(x[j] << 16) * mul, __uint_as_float(x[j] & 0xffff0000u) * mul);
-      }
+      for (int i = 0; i < CH / 8; ++i) w[i] = __ldg(p + i);
     }
+    uint32_t mx = 0u;
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks)
-      qf[(rt * KS + ks) * 32 + lane] = make_uint4(f[0][2 * ks], f[1][2 * ks], f[0][2 * ks + 1], f[1][2 * ks + 1]);
+    for (int i = 0; i < CH / 8; ++i) {
+      mx = bf16x2_max_nan(mx, bf16x2_max_nan(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu));
+      mx = bf16x2_max_nan(mx, bf16x2_max_nan(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
+    }
+    float top = fmax_nan(__uint_as_float(mx << 16), __uint_as_float(mx & 0xffff0000u));
+    top = fmax_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmax_nan(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+    const int sh = top > 0.f ? min(7 - ex, 100) : 0;
+    const float mul = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
+    // a row with a NaN or an infinity has no finite scores: the factor says so
+    const float c = top < __builtin_huge_valf()
+                        ? a.scale_log2 * a.k_mul * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23)
+                        : __int_as_float(0x7fc00000);
+    st.c[j][0] = __shfl_sync(0xffffffffu, c, 8 * t);
+    st.c[j][1] = __shfl_sync(0xffffffffu, c, 8 * t + 4);
+#pragma unroll
+    for (int i = 0; i < CH / 8; ++i) {
+      const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+      uint32_t f[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) f[k] = f16x2_pack(__uint_as_float(x[k] << 16) * mul, __uint_as_float(x[k] & 0xffff0000u) * mul);
+      qf[(j * WK + i) * 32 + lane] = make_uint4(f[0], f[1], f[2], f[3]);
+    }
   }
 }
 
 // A cached block: `left` tokens of it (1..32) belong to the sequence.
-template <int D, int RT>
-__device__ __forceinline__ void at_cached_block(const unsigned char* sb, int left, const uint4* qf, AtState<D, RT>& st) {
-  constexpr int KS = D / 16, WK = D / 32;   // words of a key chunk
+template <int D, int NR>
+__device__ __forceinline__ void at_cached_block(const unsigned char* sb, int left, const uint4* qf, AtState<D, NR>& st) {
+  constexpr int WK = D / 32;   // words of a key chunk
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int tr = at_token(g);
-  float z[RT][4][4];
+  float z[2][NR][4];
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt)
+  for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-    for (int nt = 0; nt < 4; ++nt)
+    for (int j = 0; j < NR; ++j)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) z[rt][nt][k] = 0.f;
+      for (int k = 0; k < 4; ++k) z[mt][j][k] = 0.f;
 
   uint32_t kw[4][WK];
   uint32_t ks2[4][D / 64];   // the chunk's scales, each twice
@@ -344,52 +361,53 @@ __device__ __forceinline__ void at_cached_block(const unsigned char* sb, int lef
   }
 #pragma unroll
   for (int w = 0; w < WK; ++w) {
-    uint4 qa[RT][2];
+    uint4 qb[NR];
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      qa[rt][0] = qf[(rt * KS + 2 * w) * 32 + lane];
-      qa[rt][1] = qf[(rt * KS + 2 * w + 1) * 32 + lane];
-    }
+    for (int j = 0; j < NR; ++j) qb[j] = qf[(j * WK + w) * 32 + lane];
 #pragma unroll
-    for (int nt = 0; nt < 4; ++nt) {
-      uint32_t r[4];
-      e2m1x8_to_f16(kw[nt][w], r);
+    for (int mt = 0; mt < 2; ++mt) {
+      uint32_t r0[4], r1[4];   // tokens g and g + 8
+      e2m1x8_to_f16(kw[2 * mt][w], r0);
+      e2m1x8_to_f16(kw[2 * mt + 1][w], r1);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) r[i] = f16x2_mul(r[i], ks2[nt][w / 2]);
+      for (int i = 0; i < 4; ++i) {
+        r0[i] = f16x2_mul(r0[i], ks2[2 * mt][w / 2]);
+        r1[i] = f16x2_mul(r1[i], ks2[2 * mt + 1][w / 2]);
+      }
+      const uint4 k0 = make_uint4(r0[0], r1[0], r0[1], r1[1]), k1 = make_uint4(r0[2], r1[2], r0[3], r1[3]);
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        mma_f16(z[rt][nt], qa[rt][0], r[0], r[1]);
-        mma_f16(z[rt][nt], qa[rt][1], r[2], r[3]);
+      for (int j = 0; j < NR; ++j) {
+        mma_f16(z[mt][j], k0, qb[j].x, qb[j].y);
+        mma_f16(z[mt][j], k1, qb[j].z, qb[j].w);
       }
     }
   }
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt)
+  for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-    for (int nt = 0; nt < 4; ++nt)
+    for (int j = 0; j < NR; ++j)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) z[rt][nt][k] *= st.c[rt][k >> 1];
+      for (int k = 0; k < 4; ++k) z[mt][j][k] *= st.c[j][k & 1];
   if (left < Q4_BLOCK) {
 #pragma unroll
-    for (int nt = 0; nt < 4; ++nt)
+    for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        if (8 * nt + at_token(2 * t + k) >= left) {
+      for (int f = 0; f < 2; ++f)
+        if (16 * mt + 8 * f + tr >= left) {
 #pragma unroll
-          for (int rt = 0; rt < RT; ++rt) z[rt][nt][k] = z[rt][nt][k + 2] = kNegInf;
+          for (int j = 0; j < NR; ++j) z[mt][j][2 * f] = z[mt][j][2 * f + 1] = kNegInf;
         }
   }
   st.weigh(z);
 
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
-    uint4 p[RT];
+    uint32_t p[NR][2];
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt)
-      p[rt] = make_uint4(f16x2_pack(z[rt][2 * s][0], z[rt][2 * s][1]), f16x2_pack(z[rt][2 * s][2], z[rt][2 * s][3]),
-                         f16x2_pack(z[rt][2 * s + 1][0], z[rt][2 * s + 1][1]),
-                         f16x2_pack(z[rt][2 * s + 1][2], z[rt][2 * s + 1][3]));
-    uint32_t vw[4][D / 64];   // tokens of columns 2t, 2t+1 of the two groups
+    for (int j = 0; j < NR; ++j)
+#pragma unroll
+      for (int f = 0; f < 2; ++f) p[j][f] = transpose8(f16x2_pack(z[s][j][2 * f], z[s][j][2 * f + 1]));
+    uint32_t vw[4][D / 64];   // tokens 2t, 2t+1 of the two groups of 8
     uint32_t sc[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -413,14 +431,10 @@ __device__ __forceinline__ void at_cached_block(const unsigned char* sb, int lef
       e2m1x8_to_f16((vw[2][w] & 0x0f0f0f0fu) | ((vw[3][w] << 4) & 0xf0f0f0f0u), e23);
       e2m1x8_to_f16(((vw[2][w] >> 4) & 0x0f0f0f0fu) | (vw[3][w] & 0xf0f0f0f0u), o23);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t b0 = f16x2_mul(e01[j], s01), b1 = f16x2_mul(e23[j], s23);
-        const uint32_t d0 = f16x2_mul(o01[j], s01), d1 = f16x2_mul(o23[j], s23);
+      for (int i = 0; i < 4; ++i) {
+        const uint4 v = make_uint4(f16x2_mul(e01[i], s01), f16x2_mul(o01[i], s01), f16x2_mul(e23[i], s23), f16x2_mul(o23[i], s23));
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          mma_f16(st.o[rt][8 * w + 2 * j], p[rt], b0, b1);
-          mma_f16(st.o[rt][8 * w + 2 * j + 1], p[rt], d0, d1);
-        }
+        for (int j = 0; j < NR; ++j) mma_f16(st.o[j][4 * w + i], v, p[j][0], p[j][1]);
       }
     }
   }
@@ -431,66 +445,61 @@ __device__ __forceinline__ bool bf16x2_unbounded(uint32_t w) {
 }
 
 // A block of fresh entries: nodes j0 .. j0 + 31.
-template <int D, int RT>
-__device__ __forceinline__ void at_fresh_block(const AttendArgs& a, int b, int h, int row0, int rows, int j0, AtState<D, RT>& st) {
+template <int D, int NR>
+__device__ __forceinline__ void at_fresh_block(const AttendArgs& a, int b, int h, int row0, int rows, int j0, AtState<D, NR>& st) {
   constexpr int CH = D / 4, KS = D / 16, CV = D / 8;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int tr = at_token(g);
   const long long rstride = static_cast<long long>(a.Hkv) * D;
   const long long base = (static_cast<long long>(b) * a.N * a.Hkv + h) * D;   // node 0's entry
-  float z[RT][4][4];
+  float z[2][NR][4];
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt)
+  for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-    for (int nt = 0; nt < 4; ++nt)
+    for (int j = 0; j < NR; ++j)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) z[rt][nt][k] = 0.f;
-  const uint16_t* qrow[RT][2];
+      for (int k = 0; k < 4; ++k) z[mt][j][k] = 0.f;
+  long long qat[NR];
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      const int r = row0 + 16 * rt + 8 * hf + g;
-      const int n = r / a.G;
-      qrow[rt][hf] = r < rows ? a.q + (((static_cast<long long>(b) * a.N + n) * a.Hkv + h) * a.G + (r - n * a.G)) * D + t * CH : nullptr;
-    }
-#pragma unroll 1
+  for (int j = 0; j < NR; ++j) qat[j] = row0 + 8 * j + g < rows ? at_row(a, b, h, row0 + 8 * j + g) * D + t * CH : -1;
+#pragma unroll 2
   for (int ks = 0; ks < KS; ++ks) {
-    uint4 qa[RT];
+    uint2 qb[NR];
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      uint2 x[2];
+    for (int j = 0; j < NR; ++j)
+      qb[j] = qat[j] >= 0 ? __ldg(reinterpret_cast<const uint2*>(a.q + qat[j] + 4 * ks)) : make_uint2(0u, 0u);
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf)
-        x[hf] = qrow[rt][hf] ? __ldg(reinterpret_cast<const uint2*>(qrow[rt][hf] + 4 * ks)) : make_uint2(0u, 0u);
-      qa[rt] = make_uint4(x[0].x, x[1].x, x[0].y, x[1].y);
-    }
+    for (int mt = 0; mt < 2; ++mt) {
+      uint2 kx[2];
 #pragma unroll
-    for (int nt = 0; nt < 4; ++nt) {
-      const int j = j0 + 8 * nt + at_token(g);
-      const uint2 kx = j < a.N ? __ldg(reinterpret_cast<const uint2*>(a.k_new + base + j * rstride + t * CH + 4 * ks)) : make_uint2(0u, 0u);
+      for (int f = 0; f < 2; ++f) {
+        const int n = j0 + 16 * mt + 8 * f + tr;
+        kx[f] = n < a.N ? __ldg(reinterpret_cast<const uint2*>(a.k_new + base + n * rstride + t * CH + 4 * ks)) : make_uint2(0u, 0u);
+      }
+      const uint4 k = make_uint4(kx[0].x, kx[1].x, kx[0].y, kx[1].y);
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) mma_bf16(z[rt][nt], qa[rt], kx.x, kx.y);
+      for (int j = 0; j < NR; ++j) mma_bf16(z[mt][j], k, qb[j].x, qb[j].y);
     }
   }
-  uint32_t sees[RT][2];   // nodes of the block that the lane's rows attend to
+  uint32_t sees[NR][2];   // nodes of the block that the lane's rows attend to
 #pragma unroll
-  for (int rt = 0; rt < RT; ++rt)
+  for (int j = 0; j < NR; ++j)
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      const int n = (row0 + 16 * rt + 8 * hf + g) / a.G;
+    for (int e = 0; e < 2; ++e) {
+      const int n = (row0 + 8 * j + 2 * t + e) / a.G;
       uint32_t see = 0u;
       if (n < a.N) {
         if (a.masks) see = __ldg(a.masks + (static_cast<long long>(b) * a.N + n) * a.NW + j0 / 32);
         else see = n - j0 >= 31 ? ~0u : n < j0 ? 0u : (2u << (n - j0)) - 1u;
         if (a.N - j0 < 32) see &= (1u << (a.N - j0)) - 1u;
       }
-      sees[rt][hf] = see;
+      sees[j][e] = see;
 #pragma unroll
-      for (int nt = 0; nt < 4; ++nt)
+      for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          float& x = z[rt][nt][2 * hf + k];
-          x = (see >> (8 * nt + at_token(2 * t + k))) & 1u ? x * a.scale_log2 : kNegInf;
+        for (int f = 0; f < 2; ++f) {
+          float& x = z[mt][j][e + 2 * f];
+          x = (see >> (16 * mt + 8 * f + tr)) & 1u ? x * a.scale_log2 : kNegInf;
         }
     }
   st.weigh(z);
@@ -500,27 +509,24 @@ __device__ __forceinline__ void at_fresh_block(const AttendArgs& a, int b, int h
   bool odd = false;   // this lane saw a NaN or an infinity
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
-    uint4 hi[RT], lo[RT];
+    uint32_t hi[NR][2], lo[NR][2];
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      uint32_t ph[4], pl[4];
+    for (int j = 0; j < NR; ++j)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float x = z[rt][2 * s + (k >> 1)][2 * (k & 1)] * unit, y = z[rt][2 * s + (k >> 1)][2 * (k & 1) + 1] * unit;
-        ph[k] = bf16x2_pack(x, y);
-        pl[k] = bf16x2_pack(x - __uint_as_float(ph[k] << 16), y - __uint_as_float(ph[k] & 0xffff0000u));
+      for (int f = 0; f < 2; ++f) {
+        const float x = z[s][j][2 * f] * unit, y = z[s][j][2 * f + 1] * unit;
+        const uint32_t ph = bf16x2_pack(x, y);
+        lo[j][f] = transpose8(bf16x2_pack(x - __uint_as_float(ph << 16), y - __uint_as_float(ph & 0xffff0000u)));
+        hi[j][f] = transpose8(ph);
       }
-      hi[rt] = make_uint4(ph[0], ph[1], ph[2], ph[3]);
-      lo[rt] = make_uint4(pl[0], pl[1], pl[2], pl[3]);
-    }
 #pragma unroll
     for (int w = 0; w < CV / 8; ++w) {   // eight columns of the chunk at a time
       uint32_t vw[4][4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int j = j0 + 16 * s + 8 * (k >> 1) + at_token(2 * t + (k & 1));
+        const int n = j0 + 16 * s + 8 * (k >> 1) + at_token(2 * t + (k & 1));
         uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (j < a.N) x = __ldg(reinterpret_cast<const uint4*>(a.v_new + base + j * rstride + g * CV) + w);
+        if (n < a.N) x = __ldg(reinterpret_cast<const uint4*>(a.v_new + base + n * rstride + g * CV) + w);
         const uint32_t y[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -534,14 +540,12 @@ __device__ __forceinline__ void at_fresh_block(const AttendArgs& a, int b, int h
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t b0 = __byte_perm(vw[0][i], vw[1][i], 0x5410), b1 = __byte_perm(vw[2][i], vw[3][i], 0x5410);
-        const uint32_t d0 = __byte_perm(vw[0][i], vw[1][i], 0x7632), d1 = __byte_perm(vw[2][i], vw[3][i], 0x7632);
+        const uint4 v = make_uint4(__byte_perm(vw[0][i], vw[1][i], 0x5410), __byte_perm(vw[0][i], vw[1][i], 0x7632),
+                                   __byte_perm(vw[2][i], vw[3][i], 0x5410), __byte_perm(vw[2][i], vw[3][i], 0x7632));
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          mma_bf16(st.o[rt][8 * w + 2 * i], hi[rt], b0, b1);
-          mma_bf16(st.o[rt][8 * w + 2 * i], lo[rt], b0, b1);
-          mma_bf16(st.o[rt][8 * w + 2 * i + 1], hi[rt], d0, d1);
-          mma_bf16(st.o[rt][8 * w + 2 * i + 1], lo[rt], d0, d1);
+        for (int j = 0; j < NR; ++j) {
+          mma_bf16(st.o[j][4 * w + i], v, hi[j][0], hi[j][1]);
+          mma_bf16(st.o[j][4 * w + i], v, lo[j][0], lo[j][1]);
         }
       }
     }
@@ -551,52 +555,44 @@ __device__ __forceinline__ void at_fresh_block(const AttendArgs& a, int b, int h
   // small: a weight that underflowed counts as the smallest one).
   if (__any_sync(0xffffffffu, odd)) {
 #pragma unroll 1
-    for (int col = 0; col < 8; ++col) {
-      const int src = (lane & ~3) | (col >> 1);
+    for (int x = 0; x < 8; ++x) {
 #pragma unroll
-      for (int nt = 0; nt < 4; ++nt) {
-        const int j = j0 + 8 * nt + at_token(col);
+      for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
+        for (int f = 0; f < 2; ++f) {
+          const int n = 16 * mt + 8 * f + at_token(x);
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            const float p = __shfl_sync(0xffffffffu, col & 1 ? z[rt][nt][2 * hf + 1] : z[rt][nt][2 * hf], src);
-            if (!((sees[rt][hf] >> (j - j0)) & 1u)) continue;
+          for (int j = 0; j < NR; ++j)
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i)
+            for (int e = 0; e < 2; ++e) {
+              const float p = __shfl_sync(0xffffffffu, z[mt][j][e + 2 * f], 4 * x + t);
+              if (!((sees[j][e] >> n) & 1u)) continue;
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const uint32_t v = a.v_new[base + j * rstride + t * CH + e * (D / 8) + i];
-                if ((v & 0x7f80u) == 0x7f80u) st.o[rt][i][2 * hf + e] += (p == 0.f ? 1.17549435e-38f : p) * __uint_as_float(v << 16);
-              }
-          }
-      }
+              for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const uint32_t v = a.v_new[base + (j0 + n) * rstride + g * CV + 2 * i + k];
+                  if ((v & 0x7f80u) == 0x7f80u) st.o[j][i][e + 2 * k] += (p == 0.f ? 1.17549435e-38f : p) * __uint_as_float(v << 16);
+                }
+            }
+        }
     }
   }
 }
 
-// out row of this lane's chunk from a sum, 1 / l and the row's place
-template <int D>
-__device__ __forceinline__ void at_write_row(const AttendArgs& a, int b, int h, int r, const float* x, float inv, int t) {
-  constexpr int CH = D / 4;
-  const int n = r / a.G;
-  const long long at = ((static_cast<long long>(b) * a.N + n) * a.Hkv + h) * a.G + (r - n * a.G);
-  uint4* p = reinterpret_cast<uint4*>(a.out + at * D + t * CH);
-#pragma unroll
-  for (int i = 0; i < CH / 8; ++i)
-    p[i] = make_uint4(bf16x2_pack(x[8 * i] * inv, x[8 * i + 1] * inv), bf16x2_pack(x[8 * i + 2] * inv, x[8 * i + 3] * inv),
-                      bf16x2_pack(x[8 * i + 4] * inv, x[8 * i + 5] * inv), bf16x2_pack(x[8 * i + 6] * inv, x[8 * i + 7] * inv));
-}
 __device__ __forceinline__ float at_lse(float m, float l) {
   // m in the log2 domain, l relative to 2^(m - 15)
   return l == 0.f ? kNegInf : (m - AT_PSHIFT + log2f(l)) * 0.69314718055994530942f;
 }
 
-template <int D, int RT>
-__global__ void __launch_bounds__(AT_THREADS, RT == 1 ? 3 : 2) attend_q4_kernel(const AttendArgs a, int stages) {
+// CTAs an SM: what the registers of a row tile leave room for
+__host__ __device__ constexpr int at_ctas(int NR) { return NR == 1 ? 4 : NR == 4 ? 2 : 3; }
+
+template <int D, int NR>
+__global__ void __launch_bounds__(AT_THREADS, at_ctas(NR)) attend_q4_kernel(const AttendArgs a, int stages) {
   extern __shared__ __align__(128) unsigned char at_smem[];
   __shared__ long long scratch[AT_WARPS];
-  constexpr int SB = at_stage_bytes(D), QB = at_q_bytes(D, RT);
+  constexpr int SB = at_stage_bytes(D), QB = at_q_bytes(D, NR);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   unsigned char* ring = at_smem + static_cast<size_t>(warp) * stages * SB;
   uint4* qf = reinterpret_cast<uint4*>(at_smem + static_cast<size_t>(AT_WARPS) * stages * SB + warp * QB);
@@ -617,27 +613,35 @@ __global__ void __launch_bounds__(AT_THREADS, RT == 1 ? 3 : 2) attend_q4_kernel(
   const long long u0 = at_start(units, shares, share), u1 = at_start(units, shares, share + 1);
 
   const int rows = a.N * a.G, bpp = a.P / Q4_BLOCK;
-  AtState<D, RT> st;
-  AtCursor cur, pre;   // the block at hand; the next one to fetch
-  at_seek(a, prefix, HR, u0, cur);
-  pre = cur;
-  long long pu = u0;
-  uint32_t phase = 0u;      // a bit per stage
-  bool failed = false;
+  AtState<D, NR> st;
 
-  // Fetches the next block of the share into stage s (if it is a cached one
-  // with a page in range); bit s of `have` says so.
-  uint32_t have = 0u, bad = 0u;
+  // The cursor of what is fetched runs ahead of what is worked on.  The page id
+  // of a fetch was loaded one fetch earlier, so that nothing waits for it.
+  AtCursor pre;
+  at_seek(a, prefix, HR, u0, pre);
+  AtCursor cur = pre;
+  int left = static_cast<int>(u1 - u0);            // fetches to come
+  int pcached = 0, pblk = 0, phead = 0, page = -1;
+  const int32_t* prow = nullptr;
+  auto triple = [&] {                              // the cursor entered a triple (at block pre.i)
+    pcached = at_len_ok(a, pre.len) ? (pre.len + Q4_BLOCK - 1) / Q4_BLOCK : 0;
+    prow = a.table + static_cast<long long>(pre.b) * a.W + pre.i / bpp;
+    pblk = pre.i % bpp;
+    phead = pre.pair / a.row_tiles;
+    if (pre.i < pcached) page = __ldg(prow);
+  };
+  triple();
+  uint32_t phase = 0u, have = 0u, bad = 0u;        // a bit per stage
   auto fetch = [&](int s) {
     have &= ~(1u << s);
     bad &= ~(1u << s);
-    if (pu >= u1) return;
-    if (at_len_ok(a, pre.len) && pre.i * Q4_BLOCK < pre.len) {
-      const int page = __ldg(a.table + static_cast<long long>(pre.b) * a.W + pre.i / bpp);
+    if (left <= 0) return;
+    --left;
+    if (pre.i < pcached) {
       if (page >= 0 && page < a.pages) {
         have |= 1u << s;
         if (lane == 0) {
-          const unsigned long long blk = (static_cast<unsigned long long>(page) * a.Hkv + pre.pair / a.row_tiles) * bpp + pre.i % bpp;
+          const unsigned long long blk = (static_cast<unsigned long long>(page) * a.Hkv + phead) * bpp + pblk;
           mbar_arrive_expect_tx(&bars[s], SB);
           bulk_g2s(ring + s * SB, a.cache + blk * SB, SB, &bars[s]);
         }
@@ -645,100 +649,111 @@ __global__ void __launch_bounds__(AT_THREADS, RT == 1 ? 3 : 2) attend_q4_kernel(
         bad |= 1u << s;
       }
     }
-    at_next(a, prefix, HR, pre);
-    ++pu;
+    if (pre.i + 1 < pre.units) {
+      ++pre.i;
+      if (++pblk == bpp) {
+        pblk = 0;
+        ++prow;
+        if (pre.i < pcached) page = __ldg(prow);
+      }
+    } else if (left > 0) {
+      at_next(a, prefix, HR, pre);
+      triple();
+    }
   };
   for (int s = 0; s < stages; ++s) fetch(s);
 
-  bool start = true, poison = false;   // a new triple begins; its result is void
-  int first_i = 0, stage = 0;
-  for (long long u = u0; u < u1; ++u) {
-    const int h = cur.pair / a.row_tiles, row0 = (cur.pair - h * a.row_tiles) * 16 * RT;
-    if (start) {
-      st.clear();
-      at_load_q<D, RT>(a, cur.b, h, row0, rows, qf, st);
-      first_i = cur.i;
-      start = poison = false;
-    }
-    if (!at_len_ok(a, cur.len)) {
-      poison = true;
-    } else if (cur.i * Q4_BLOCK < cur.len) {
-      if (have & (1u << stage)) {
-        if (!mbar_wait(&bars[stage], (phase >> stage) & 1u, a.timeout_ns)) failed = true;
-        phase ^= 1u << stage;
-        if (failed) poison = true;
-        else at_cached_block<D, RT>(ring + stage * SB, min(cur.len - cur.i * Q4_BLOCK, Q4_BLOCK), qf, st);
-      }
-      if (bad & (1u << stage)) poison = true;
-    } else if (a.k_new) {
-      const int cached = (cur.len + Q4_BLOCK - 1) / Q4_BLOCK;
-      at_fresh_block<D, RT>(a, cur.b, h, row0, rows, (cur.i - cached) * Q4_BLOCK, st);
-    }
-    __syncwarp();
-    if (failed) break;   // no copy is started after one that did not arrive
-    fetch(stage);
-    stage = stage + 1 == stages ? 0 : stage + 1;
-
-    if (cur.i + 1 == cur.units || u + 1 == u1) {
-      const bool whole = first_i == 0 && cur.i + 1 == cur.units;
-      float* part = a.ws + (static_cast<size_t>(share) * 2 + (first_i == 0 ? 1 : 0)) * at_partial_floats(D, RT);
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          float l = st.l[rt][hf];
-          l += __shfl_xor_sync(0xffffffffu, l, 1);
-          l += __shfl_xor_sync(0xffffffffu, l, 2);
-          if (poison) l = __int_as_float(0x7fc00000);
-          float x[D / 4];
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            x[i] = st.o[rt][i][2 * hf];
-            x[D / 8 + i] = st.o[rt][i][2 * hf + 1];
+  bool failed = false;
+  int stage = 0;
+  for (long long u = u0; u < u1 && !failed;) {
+    // one triple, or the part of it that lies in the share
+    const int h = cur.pair / a.row_tiles, row0 = (cur.pair - h * a.row_tiles) * 8 * NR;
+    const int first = cur.i, last = static_cast<int>(min(static_cast<long long>(cur.units), first + (u1 - u)));
+    const bool len_ok = at_len_ok(a, cur.len);
+    const int cached = len_ok ? (cur.len + Q4_BLOCK - 1) / Q4_BLOCK : 0;
+    bool poison = !len_ok;
+    st.clear();
+    at_load_q<D, NR>(a, cur.b, h, row0, rows, qf, st);
+    for (int i = first; i < last; ++i) {
+      if (i < cached) {
+        if (have & (1u << stage)) {
+          if (!mbar_wait(&bars[stage], (phase >> stage) & 1u, a.timeout_ns)) {
+            failed = true;
+            break;   // no copy is started after one that did not arrive
           }
-          const int lr = 16 * rt + 8 * hf + g, r = row0 + lr;
-          if (whole) {
-            if (r < rows) {
-              at_write_row<D>(a, cur.b, h, r, x, l == 0.f ? 0.f : a.v_mul / l, t);
-              if (a.lse && t == 0) {
-                const int n = r / a.G;
-                a.lse[((static_cast<long long>(cur.b) * a.N + n) * a.Hkv + h) * a.G + (r - n * a.G)] = at_lse(st.m[rt][hf], l);
-              }
-            }
-          } else {
-            float4* p = reinterpret_cast<float4*>(part + static_cast<size_t>(lr) * D + t * (D / 4));
+          phase ^= 1u << stage;
+          at_cached_block<D, NR>(ring + stage * SB, min(cur.len - i * Q4_BLOCK, Q4_BLOCK), qf, st);
+        } else {
+          poison = true;
+        }
+      } else if (a.k_new && len_ok) {
+        at_fresh_block<D, NR>(a, cur.b, h, row0, rows, (i - cached) * Q4_BLOCK, st);
+      }
+      __syncwarp();
+      fetch(stage);
+      stage = stage + 1 == stages ? 0 : stage + 1;
+    }
+    if (failed) break;
+    u += last - first;
+
+    const bool whole = first == 0 && last == cur.units;
+    float* part = a.ws + (static_cast<size_t>(share) * 2 + (first == 0 ? 1 : 0)) * at_partial_floats(D, NR);
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) p[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-            if (t == 0) {
-              part[16 * RT * D + lr] = st.m[rt][hf];
-              part[16 * RT * D + 16 * RT + lr] = l;
-            }
+    for (int j = 0; j < NR; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float l = st.l[j][e];
+        l += __shfl_xor_sync(0xffffffffu, l, 4);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        if (poison) l = __int_as_float(0x7fc00000);
+        const int lr = 8 * j + 2 * t + e, r = row0 + lr;
+        if (whole) {
+          if (r >= rows) continue;
+          const long long at = at_row(a, cur.b, h, r);
+          const float inv = l == 0.f ? 0.f : a.v_mul / l;
+          uint4* p = reinterpret_cast<uint4*>(a.out + at * D + g * (D / 8));
+#pragma unroll
+          for (int i = 0; i < D / 16; i += 4)
+            p[i / 4] = make_uint4(bf16x2_pack(st.o[j][i][e] * inv, st.o[j][i][e + 2] * inv),
+                                  bf16x2_pack(st.o[j][i + 1][e] * inv, st.o[j][i + 1][e + 2] * inv),
+                                  bf16x2_pack(st.o[j][i + 2][e] * inv, st.o[j][i + 2][e + 2] * inv),
+                                  bf16x2_pack(st.o[j][i + 3][e] * inv, st.o[j][i + 3][e + 2] * inv));
+          if (a.lse && g == 0) a.lse[at] = at_lse(st.m[j][e], l);
+        } else {
+          float4* p = reinterpret_cast<float4*>(part + static_cast<size_t>(lr) * D + g * (D / 8));
+#pragma unroll
+          for (int i = 0; i < D / 16; i += 2)
+            p[i / 2] = make_float4(st.o[j][i][e], st.o[j][i][e + 2], st.o[j][i + 1][e], st.o[j][i + 1][e + 2]);
+          if (g == 0) {
+            part[8 * NR * D + lr] = st.m[j][e];
+            part[8 * NR * D + 8 * NR + lr] = l;
           }
         }
-      start = true;
-    }
-    at_next(a, prefix, HR, cur);
+      }
+    cur.i = last - 1;
+    if (u < u1) at_next(a, prefix, HR, cur);
   }
   if (failed) {
     // copies still on their way land before the warp leaves (or the wait gives up)
     for (int s = 0; s < stages; ++s)
       if (s != stage && (have & (1u << s))) mbar_wait(&bars[s], (phase >> s) & 1u, a.timeout_ns);
-    // what this share did not finish is void: every triple of it
+    // every triple of the share is void
     AtCursor c;
     at_seek(a, prefix, HR, u0, c);
     for (long long u = u0; u < u1;) {
       const long long end = min(u1, u + c.units - c.i);
       const bool whole = c.i == 0 && end - u == c.units;
-      const int h = c.pair / a.row_tiles, row0 = (c.pair - h * a.row_tiles) * 16 * RT;
-      float* part = a.ws + (static_cast<size_t>(share) * 2 + (c.i == 0 ? 1 : 0)) * at_partial_floats(D, RT);
-      for (int lr = lane; lr < 16 * RT; lr += 32) {
-        const int r = row0 + lr, n = r / a.G;
+      const int h = c.pair / a.row_tiles, row0 = (c.pair - h * a.row_tiles) * 8 * NR;
+      float* part = a.ws + (static_cast<size_t>(share) * 2 + (c.i == 0 ? 1 : 0)) * at_partial_floats(D, NR);
+      for (int lr = lane; lr < 8 * NR; lr += 32) {
+        const int r = row0 + lr;
         if (!whole) {
           for (int d = 0; d < D; ++d) part[lr * D + d] = 0.f;
-          part[16 * RT * D + lr] = 0.f;
-          part[16 * RT * D + 16 * RT + lr] = __int_as_float(0x7fc00000);
+          part[8 * NR * D + lr] = 0.f;
+          part[8 * NR * D + 8 * NR + lr] = __int_as_float(0x7fc00000);
         } else if (r < rows) {
-          const long long at = ((static_cast<long long>(c.b) * a.N + n) * a.Hkv + h) * a.G + (r - n * a.G);
+          const long long at = at_row(a, c.b, h, r);
           for (int d = 0; d < D; ++d) a.out[at * D + d] = 0x7fc0u;
           if (a.lse) a.lse[at] = __int_as_float(0x7fc00000);
         }
@@ -748,48 +763,72 @@ __global__ void __launch_bounds__(AT_THREADS, RT == 1 ? 3 : 2) attend_q4_kernel(
   }
 }
 
-// Joins the partials of triples that several shares worked on: a CTA a triple,
-// a thread four columns of a row, the shares in their order.
-constexpr int AJN_THREADS = 128;
-template <int D, int RT>
-__global__ void __launch_bounds__(AJN_THREADS) attend_q4_join_kernel(const AttendArgs a, int warps) {
+// Joins the partials of triples that several shares worked on: a CTA a row of a
+// triple; its warps take the shares in turn (a lane D / 32 columns), then their
+// results are joined in order.
+constexpr int ATJ_WARPS = 4, ATJ_THREADS = 32 * ATJ_WARPS;
+template <int D, int NR>
+__global__ void __launch_bounds__(ATJ_THREADS) attend_q4_join_kernel(const AttendArgs a, int warps) {
   extern __shared__ __align__(128) unsigned char at_smem[];
-  __shared__ long long scratch[AJN_THREADS / 32];
+  __shared__ long long scratch[ATJ_WARPS];
+  __shared__ float sm[ATJ_WARPS], sl[ATJ_WARPS], so[ATJ_WARPS][D];
   long long* prefix = reinterpret_cast<long long*>(at_smem);
-  at_prefix<AJN_THREADS>(a, prefix, scratch);
+  at_prefix<ATJ_THREADS>(a, prefix, scratch);
+  constexpr int C = D / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int HR = a.Hkv * a.row_tiles, rows = a.N * a.G;
   const long long units = prefix[a.B] * HR;
   const int shares = at_shares(units, warps);
-  for (long long x = blockIdx.x; x < static_cast<long long>(a.B) * HR; x += gridDim.x) {
-    const int b = static_cast<int>(x / HR), pair = static_cast<int>(x % HR);
+  const int per = min(rows, 8 * NR);   // rows of a tile that can be real
+  for (long long x = blockIdx.x; x < static_cast<long long>(a.B) * HR * per; x += gridDim.x) {
+    const long long y = x / per;
+    const int lr = static_cast<int>(x - y * per), b = static_cast<int>(y / HR), pair = static_cast<int>(y % HR);
     const long long n = prefix[b + 1] - prefix[b], u = prefix[b] * HR + pair * n;
     const int wa = at_owner(units, shares, u), wb = at_owner(units, shares, u + n - 1);
     if (wa == wb) continue;
-    const int h = pair / a.row_tiles, row0 = (pair - h * a.row_tiles) * 16 * RT;
-    for (int e = threadIdx.x; e < 16 * RT * (D / 4); e += AJN_THREADS) {
-      const int lr = e / (D / 4), d4 = e % (D / 4), r = row0 + lr;
-      if (r >= rows) continue;
-      float m = kNegInf, l = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (int w = wa; w <= wb; ++w) {
-        const float* part = a.ws + (static_cast<size_t>(w) * 2 + (w == wa ? 1 : 0)) * at_partial_floats(D, RT);
-        const float pm = part[16 * RT * D + lr], pl = part[16 * RT * D + 16 * RT + lr];
-        const float4 po = *reinterpret_cast<const float4*>(part + static_cast<size_t>(lr) * D + d4 * 4);
-        const float mn = fmaxf(m, pm), ref = mn == kNegInf ? 0.f : mn;
-        const float c0 = at_corr(m - ref), c1 = at_corr(pm - ref);
-        l = l * c0 + pl * c1;
-        o.x = o.x * c0 + po.x * c1;
-        o.y = o.y * c0 + po.y * c1;
-        o.z = o.z * c0 + po.z * c1;
-        o.w = o.w * c0 + po.w * c1;
-        m = mn;
-      }
-      const float inv = l == 0.f ? 0.f : a.v_mul / l;
-      const int node = r / a.G;
-      const long long at = ((static_cast<long long>(b) * a.N + node) * a.Hkv + h) * a.G + (r - node * a.G);
-      *reinterpret_cast<uint2*>(a.out + at * D + d4 * 4) = make_uint2(bf16x2_pack(o.x * inv, o.y * inv), bf16x2_pack(o.z * inv, o.w * inv));
-      if (a.lse && d4 == 0) a.lse[at] = at_lse(m, l);
+    const int h = pair / a.row_tiles, r = (pair - h * a.row_tiles) * 8 * NR + lr;
+    if (r >= rows) continue;
+    float m = kNegInf, l = 0.f, o[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) o[i] = 0.f;
+#pragma unroll 4
+    for (int w = wa + warp; w <= wb; w += ATJ_WARPS) {
+      const float* part = a.ws + (static_cast<size_t>(w) * 2 + (w == wa ? 1 : 0)) * at_partial_floats(D, NR);
+      const float pm = part[8 * NR * D + lr], pl = part[8 * NR * D + 8 * NR + lr];
+      float po[C];
+#pragma unroll
+      for (int i = 0; i < C; ++i) po[i] = part[lr * D + i * 32 + lane];
+      const float mn = fmaxf(m, pm), ref = mn == kNegInf ? 0.f : mn;
+      const float c0 = at_corr(m - ref), c1 = at_corr(pm - ref);
+      l = l * c0 + pl * c1;
+#pragma unroll
+      for (int i = 0; i < C; ++i) o[i] = o[i] * c0 + po[i] * c1;
+      m = mn;
     }
+    if (lane == 0) {
+      sm[warp] = m;
+      sl[warp] = l;
+    }
+#pragma unroll
+    for (int i = 0; i < C; ++i) so[warp][i * 32 + lane] = o[i];
+    __syncthreads();
+    if (threadIdx.x < D) {
+      m = kNegInf;
+      for (int w = 0; w < ATJ_WARPS; ++w) m = fmaxf(m, sm[w]);
+      const float ref = m == kNegInf ? 0.f : m;
+      float sum = 0.f;
+      l = 0.f;
+      for (int w = 0; w < ATJ_WARPS; ++w) {
+        const float c = at_corr(sm[w] - ref);
+        l += sl[w] * c;
+        sum += so[w][threadIdx.x] * c;
+      }
+      const long long at = at_row(a, b, h, r);
+      const uint32_t two = bf16x2_pack(sum * (l == 0.f ? 0.f : a.v_mul / l), 0.f);
+      a.out[at * D + threadIdx.x] = static_cast<uint16_t>(two);
+      if (a.lse && threadIdx.x == 0) a.lse[at] = at_lse(m, l);
+    }
+    __syncthreads();
   }
 }
 

@@ -40,17 +40,20 @@ spec_status_t check_q4(int Hkv, int D, int P, int pages, int k_shift, int v_shif
 // ---------------------------------------------------------------------------
 // attention
 // ---------------------------------------------------------------------------
-// rows of a warp's tile, in units of 16: two where there are more rows than one
-// tile holds, so that a block is fetched and unpacked once for 32 of them
-int attend_tiles(int rows) { return rows <= 16 ? 1 : 2; }
+// Rows of a warp's tile, in units of 8: as few tiles of at most 32 rows as hold
+// them all, since a block is fetched and unpacked once for each tile, and no
+// wider than that needs.
+void attend_tiles(int rows, int& tiles, int& NR) {
+  tiles = ceil_div(rows, 32);
+  NR = ceil_div(ceil_div(rows, 8), tiles);
+}
 constexpr int kMaxSms = 160;   // bound of the workspace size; the grid never exceeds it
-constexpr int attend_ctas(int RT) { return RT == 1 ? 3 : 2; }   // CTAs an SM (register use)
 
-template <int D, int RT>
-spec_status_t launch_attend(const DevInfo& di, int dev, AttendArgs a, cudaStream_t st) {
-  auto kern = attend_q4_kernel<D, RT>;
-  constexpr int ctas = attend_ctas(RT);
-  const size_t fixed = static_cast<size_t>(AT_WARPS) * at_q_bytes(D, RT) + 8 * (static_cast<size_t>(a.B) + 1);
+template <int D, int NR>
+spec_status_t launch_attend(const DevInfo& di, int dev, const AttendArgs& a, cudaStream_t st) {
+  auto kern = attend_q4_kernel<D, NR>;
+  constexpr int ctas = at_ctas(NR);
+  const size_t fixed = static_cast<size_t>(AT_WARPS) * at_q_bytes(D, NR) + 8 * (static_cast<size_t>(a.B) + 1);
   const size_t stage = static_cast<size_t>(AT_WARPS) * (at_stage_bytes(D) + 8);
   // as many stages (at most 6) as leave room for all CTAs; 1 KB a CTA is the system's
   const size_t room = kSmemPerSm / ctas - 1024;
@@ -64,12 +67,22 @@ spec_status_t launch_attend(const DevInfo& di, int dev, AttendArgs a, cudaStream
   kern<<<grid, AT_THREADS, smem, st>>>(a, stages);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "attention launch");
-  const long long triples = static_cast<long long>(a.B) * a.Hkv * a.row_tiles;
-  const int jgrid = static_cast<int>(std::min<long long>(triples, static_cast<long long>(di.sms) * 8));
-  attend_q4_join_kernel<D, RT><<<jgrid, AJN_THREADS, 8 * (static_cast<size_t>(a.B) + 1), st>>>(a, grid * AT_WARPS);
+  const long long rows = static_cast<long long>(a.B) * a.Hkv * a.row_tiles * std::min(a.N * a.G, 8 * NR);
+  const int jgrid = static_cast<int>(std::min<long long>(rows, static_cast<long long>(di.sms) * 16));
+  attend_q4_join_kernel<D, NR><<<jgrid, ATJ_THREADS, 8 * (static_cast<size_t>(a.B) + 1), st>>>(a, grid * AT_WARPS);
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "attention join launch");
   return SPEC_OK;
+}
+
+template <int D>
+spec_status_t launch_attend(int NR, const DevInfo& di, int dev, const AttendArgs& a, cudaStream_t st) {
+  switch (NR) {
+    case 1: return launch_attend<D, 1>(di, dev, a, st);
+    case 2: return launch_attend<D, 2>(di, dev, a, st);
+    case 3: return launch_attend<D, 3>(di, dev, a, st);
+    default: return launch_attend<D, 4>(di, dev, a, st);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -251,9 +264,10 @@ size_t spec_attend_workspace_bytes(int B, int N, int Hq, int Hkv, int D) {
   if (B < 0 || B > AT_MAX_B || N < 1 || N > SPEC_MAX_TREE_NODES || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 ||
       Hq / Hkv > 64 || !q4_dim(D))
     return 0;
-  const int RT = attend_tiles(N * (Hq / Hkv));
-  const size_t shares = static_cast<size_t>(kMaxSms) * attend_ctas(RT) * AT_WARPS;
-  return align_up(shares * 2 * at_partial_floats(D, RT) * sizeof(float), 256);
+  int tiles, NR;
+  attend_tiles(N * (Hq / Hkv), tiles, NR);
+  const size_t shares = static_cast<size_t>(kMaxSms) * at_ctas(NR) * AT_WARPS;
+  return align_up(shares * 2 * at_partial_floats(D, NR) * sizeof(float), 256);
 }
 
 spec_status_t spec_attend_q4(const void* q, const void* k_new, const void* v_new, const uint32_t* masks,
@@ -299,8 +313,8 @@ spec_status_t spec_attend_q4(const void* q, const void* k_new, const void* v_new
     a.pages = num_pages;
     a.W = max_pages;
     a.NW = (N + 31) / 32;
-    const int rows = N * a.G, RT = attend_tiles(rows);
-    a.row_tiles = ceil_div(rows, 16 * RT);
+    int NR;
+    attend_tiles(N * a.G, a.row_tiles, NR);
     a.scale_log2 = static_cast<float>(1.4426950408889634 * static_cast<double>(scale));
     a.k_mul = std::ldexp(1.f, k_shift);
     a.v_mul = std::ldexp(1.f, v_shift);
@@ -310,8 +324,7 @@ spec_status_t spec_attend_q4(const void* q, const void* k_new, const void* v_new
     a.timeout_ns = kWaitNs;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     prof_mark(0, st);
-    if (D == 128) s = RT == 1 ? launch_attend<128, 1>(di, dev, a, st) : launch_attend<128, 2>(di, dev, a, st);
-    else s = RT == 1 ? launch_attend<64, 1>(di, dev, a, st) : launch_attend<64, 2>(di, dev, a, st);
+    s = D == 128 ? launch_attend<128>(NR, di, dev, a, st) : launch_attend<64>(NR, di, dev, a, st);
     if (s != SPEC_OK) return s;
     prof_mark(1, st);
     prof_mark(2, st);
