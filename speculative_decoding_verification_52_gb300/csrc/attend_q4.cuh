@@ -13,10 +13,12 @@
 //
 // * The unit of work is a block of 32 tokens (one contiguous run of 36 * D
 //   bytes, one bulk copy).  All blocks of all (sequence, head, row tile) triples
-//   form one list; every warp takes an equal, contiguous share of it, whatever
-//   the lengths, and fetches it through a ring of its own.  A triple that lies in
-//   one warp's share is finished there; the others leave partial (max, sum, sum
-//   of v) in the workspace and a second kernel joins them in a fixed order.
+//   form one list, a triple's fresh blocks before its cached ones; every warp
+//   takes an equal, contiguous share of it, whatever the lengths, and fetches it
+//   through a ring of its own.  A triple that lies in one warp's share is
+//   finished there.  The warps of a CTA have neighbouring shares and join what
+//   they share at the end; what CTAs share goes through the workspace (maximum,
+//   sum, sum of v) and a second kernel.  All joins are in the list's order.
 // * Everything is unpacked in f16, exactly: a code times its scale has 6
 //   significant bits.  q enters as f16 too, scaled by a power of two per row so
 //   that its largest element lies in [128, 256): what f16 then cannot hold is
@@ -142,9 +144,9 @@ __device__ __forceinline__ void at_next(const AttendArgs& a, const long long* pr
   c.units = static_cast<int>(prefix[c.b + 1] - prefix[c.b]);
 }
 
-// as many shares as there are warps, none of them empty
-__device__ __forceinline__ int at_shares(long long units, int warps) {
-  return static_cast<int>(min(units, static_cast<long long>(warps)));
+// CTAs that get work: the list is cut in AT_WARPS shares a CTA, none of the CTAs empty
+__device__ __forceinline__ int at_active(long long units, int ctas) {
+  return static_cast<int>(min((units + AT_WARPS - 1) / AT_WARPS, static_cast<long long>(ctas)));
 }
 // share w of n of a list of `units`: [at_start(w), at_start(w + 1)), and the share that unit u falls in
 __device__ __forceinline__ long long at_start(long long units, int n, long long w) { return units * w / n; }
@@ -210,8 +212,16 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 
 __host__ __device__ constexpr int at_stage_bytes(int D) { return q4_block_bytes(D); }
 __host__ __device__ constexpr int at_q_bytes(int D, int NR) { return NR * (D / 32) * 512; }
-// partial: [8 NR rows x D] sums of v, then m[8 NR], l[8 NR]
+// The workspace.  A CTA has two partials, of the triple that it shares with the
+// CTAs before it and of the one that it shares with those behind:
+//   [8 NR rows x D] sums of v, then m[8 NR], l[8 NR];
+// a warp has two copies of a state in its lanes' order: what its CTA's other
+// warps join, and the result of a triple's fresh blocks.
 __host__ __device__ constexpr size_t at_partial_floats(int D, int NR) { return static_cast<size_t>(8 * NR) * (D + 2); }
+__host__ __device__ constexpr size_t at_state_floats(int D, int NR) { return static_cast<size_t>(32 * NR) * (D / 4 + 4); }
+__host__ __device__ constexpr size_t at_cta_floats(int D, int NR) {
+  return 2 * at_partial_floats(D, NR) + 2 * AT_WARPS * at_state_floats(D, NR);
+}
 
 // ---------------------------------------------------------------------------
 // the state of one (sequence, head, row tile) in a warp's registers: lane
@@ -233,6 +243,56 @@ struct AtState {
         for (int k = 0; k < 4; ++k) o[j][i][k] = 0.f;
       m[j][0] = m[j][1] = kNegInf;
       l[j][0] = l[j][1] = 0.f;
+    }
+  }
+
+  // the state in the order of its lanes: only the lane that wrote a value reads it
+  __device__ __forceinline__ void save(float* p) const {
+    float4* q = reinterpret_cast<float4*>(p) + (threadIdx.x & 31);
+#pragma unroll
+    for (int j = 0; j < NR; ++j) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i) q[32 * (j * (MT + 1) + i)] = make_float4(o[j][i][0], o[j][i][1], o[j][i][2], o[j][i][3]);
+      q[32 * (j * (MT + 1) + MT)] = make_float4(m[j][0], m[j][1], l[j][0], l[j][1]);
+    }
+  }
+  __device__ __forceinline__ void load(const float* p) {
+    const float4* q = reinterpret_cast<const float4*>(p) + (threadIdx.x & 31);
+#pragma unroll
+    for (int j = 0; j < NR; ++j) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const float4 x = q[32 * (j * (MT + 1) + i)];
+        o[j][i][0] = x.x; o[j][i][1] = x.y; o[j][i][2] = x.z; o[j][i][3] = x.w;
+      }
+      const float4 x = q[32 * (j * (MT + 1) + MT)];
+      m[j][0] = x.x; m[j][1] = x.y; l[j][0] = x.z; l[j][1] = x.w;
+    }
+  }
+  // joins a saved state of the same rows
+  __device__ __forceinline__ void join(const float* p) {
+    const float4* q = reinterpret_cast<const float4*>(p) + (threadIdx.x & 31);
+#pragma unroll
+    for (int j = 0; j < NR; ++j) {
+      const float4 x = q[32 * (j * (MT + 1) + MT)];
+      const float pm[2] = {x.x, x.y}, pl[2] = {x.z, x.w};
+      float c0[2], c1[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float mn = fmaxf(m[j][e], pm[e]), ref = mn == kNegInf ? 0.f : mn;
+        c0[e] = at_corr(m[j][e] - ref);
+        c1[e] = at_corr(pm[e] - ref);
+        l[j][e] = l[j][e] * c0[e] + pl[e] * c1[e];
+        m[j][e] = mn;
+      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const float4 y = q[32 * (j * (MT + 1) + i)];
+        o[j][i][0] = o[j][i][0] * c0[0] + y.x * c1[0];
+        o[j][i][1] = o[j][i][1] * c0[1] + y.y * c1[1];
+        o[j][i][2] = o[j][i][2] * c0[0] + y.z * c1[0];
+        o[j][i][3] = o[j][i][3] * c0[1] + y.w * c1[1];
+      }
     }
   }
 
@@ -580,6 +640,17 @@ __device__ __forceinline__ void at_fresh_block(const AttendArgs& a, int b, int h
   }
 }
 
+// The state after fresh blocks first .. last - 1 of a triple, saved at `p`.  A
+// function of its own: these blocks are few, and their registers would push the
+// cached blocks' loop into local memory.
+template <int D, int NR>
+__device__ __noinline__ void at_fresh(const AttendArgs& a, int b, int h, int row0, int rows, int first, int last, float* p) {
+  AtState<D, NR> st;
+  st.clear();
+  for (int i = first; i < last; ++i) at_fresh_block<D, NR>(a, b, h, row0, rows, i * Q4_BLOCK, st);
+  st.save(p);
+}
+
 __device__ __forceinline__ float at_lse(float m, float l) {
   // m in the log2 domain, l relative to 2^(m - 15)
   return l == 0.f ? kNegInf : (m - AT_PSHIFT + log2f(l)) * 0.69314718055994530942f;
@@ -588,12 +659,62 @@ __device__ __forceinline__ float at_lse(float m, float l) {
 // CTAs an SM: what the registers of a row tile leave room for
 __host__ __device__ constexpr int at_ctas(int NR) { return NR == 1 ? 4 : NR == 4 ? 2 : 3; }
 
+// this lane's rows of a finished state
 template <int D, int NR>
-__global__ void __launch_bounds__(AT_THREADS, at_ctas(NR)) attend_q4_kernel(const AttendArgs a, int stages) {
+__device__ __forceinline__ void at_write(const AttendArgs& a, int b, int h, int row0, int rows, const AtState<D, NR>& st) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int j = 0; j < NR; ++j)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float l = st.l[j][e];
+      l += __shfl_xor_sync(0xffffffffu, l, 4);
+      l += __shfl_xor_sync(0xffffffffu, l, 8);
+      l += __shfl_xor_sync(0xffffffffu, l, 16);
+      const int r = row0 + 8 * j + 2 * t + e;
+      if (r >= rows) continue;
+      const long long at = at_row(a, b, h, r);
+      const float inv = l == 0.f ? 0.f : a.v_mul / l;
+      uint4* p = reinterpret_cast<uint4*>(a.out + at * D + g * (D / 8));
+#pragma unroll
+      for (int i = 0; i < D / 16; i += 4)
+        p[i / 4] = make_uint4(bf16x2_pack(st.o[j][i][e] * inv, st.o[j][i][e + 2] * inv),
+                              bf16x2_pack(st.o[j][i + 1][e] * inv, st.o[j][i + 1][e + 2] * inv),
+                              bf16x2_pack(st.o[j][i + 2][e] * inv, st.o[j][i + 2][e + 2] * inv),
+                              bf16x2_pack(st.o[j][i + 3][e] * inv, st.o[j][i + 3][e + 2] * inv));
+      if (a.lse && g == 0) a.lse[at] = at_lse(st.m[j][e], l);
+    }
+}
+// the same as a partial
+template <int D, int NR>
+__device__ __forceinline__ void at_write_partial(float* part, const AtState<D, NR>& st) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int j = 0; j < NR; ++j)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float l = st.l[j][e];
+      l += __shfl_xor_sync(0xffffffffu, l, 4);
+      l += __shfl_xor_sync(0xffffffffu, l, 8);
+      l += __shfl_xor_sync(0xffffffffu, l, 16);
+      const int lr = 8 * j + 2 * t + e;
+      float4* p = reinterpret_cast<float4*>(part + static_cast<size_t>(lr) * D + g * (D / 8));
+#pragma unroll
+      for (int i = 0; i < D / 16; i += 2)
+        p[i / 2] = make_float4(st.o[j][i][e], st.o[j][i][e + 2], st.o[j][i + 1][e], st.o[j][i + 1][e + 2]);
+      if (g == 0) {
+        part[8 * NR * D + lr] = st.m[j][e];
+        part[8 * NR * D + 8 * NR + lr] = l;
+      }
+    }
+}
+
+template <int D, int NR>
+__global__ void __launch_bounds__(AT_THREADS, at_ctas(NR)) attend_q4_kernel(const __grid_constant__ AttendArgs a, int stages) {
   extern __shared__ __align__(128) unsigned char at_smem[];
   __shared__ long long scratch[AT_WARPS];
   constexpr int SB = at_stage_bytes(D), QB = at_q_bytes(D, NR);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   unsigned char* ring = at_smem + static_cast<size_t>(warp) * stages * SB;
   uint4* qf = reinterpret_cast<uint4*>(at_smem + static_cast<size_t>(AT_WARPS) * stages * SB + warp * QB);
   uint64_t* bars = reinterpret_cast<uint64_t*>(at_smem + static_cast<size_t>(AT_WARPS) * (stages * SB + QB)) + warp * stages;
@@ -607,37 +728,64 @@ __global__ void __launch_bounds__(AT_THREADS, at_ctas(NR)) attend_q4_kernel(cons
 
   const int HR = a.Hkv * a.row_tiles;
   const long long units = prefix[a.B] * HR;
-  const int shares = at_shares(units, gridDim.x * AT_WARPS);
-  const int share = warp * gridDim.x + blockIdx.x;   // few shares: one an SM
-  if (share >= shares) return;
+  const int ctas = at_active(units, gridDim.x);
+  if (blockIdx.x >= ctas) return;
+  const int shares = ctas * AT_WARPS, share = blockIdx.x * AT_WARPS + warp;
   const long long u0 = at_start(units, shares, share), u1 = at_start(units, shares, share + 1);
+  float* cta_ws = a.ws + static_cast<size_t>(blockIdx.x) * at_cta_floats(D, NR);
+  float* states = cta_ws + 2 * at_partial_floats(D, NR);
+  float* mine = states + warp * at_state_floats(D, NR);
+  float* fresh_at = states + (AT_WARPS + warp) * at_state_floats(D, NR);
 
   const int rows = a.N * a.G, bpp = a.P / Q4_BLOCK;
+  const int nfresh = a.k_new ? (a.N + Q4_BLOCK - 1) / Q4_BLOCK : 0;
   AtState<D, NR> st;
+  AtCursor pre, cur;
+  uint32_t phase = 0u, have = 0u;        // a bit per stage
+  int stage = 0;
+  bool failed = false;
+  // the piece in registers at the end
+  int first = 0, last = 0, h = 0, row0 = 0;
+  long long upiece = u0;
 
-  // The cursor of what is fetched runs ahead of what is worked on.  The page id
-  // of a fetch was loaded one fetch earlier, so that nothing waits for it.
-  AtCursor pre;
-  at_seek(a, prefix, HR, u0, pre);
-  AtCursor cur = pre;
-  int left = static_cast<int>(u1 - u0);            // fetches to come
-  int pcached = 0, pblk = 0, phead = 0, page = -1;
-  const int32_t* prow = nullptr;
-  auto triple = [&] {                              // the cursor entered a triple (at block pre.i)
-    pcached = at_len_ok(a, pre.len) ? (pre.len + Q4_BLOCK - 1) / Q4_BLOCK : 0;
-    prow = a.table + static_cast<long long>(pre.b) * a.W + pre.i / bpp;
-    pblk = pre.i % bpp;
-    phead = pre.pair / a.row_tiles;
-    if (pre.i < pcached) page = __ldg(prow);
-  };
-  triple();
-  uint32_t phase = 0u, have = 0u, bad = 0u;        // a bit per stage
-  auto fetch = [&](int s) {
-    have &= ~(1u << s);
-    bad &= ~(1u << s);
-    if (left <= 0) return;
-    --left;
-    if (pre.i < pcached) {
+  if (u0 < u1) {
+    // The cursor of what is fetched runs ahead of what is worked on.  The page
+    // id of a fetch was loaded one fetch earlier, so that nothing waits for it.
+    at_seek(a, prefix, HR, u0, pre);
+    cur = pre;
+    int left = static_cast<int>(u1 - u0);            // blocks that the cursor has still to pass
+    int pblk = 0, phead = 0, page = -1;
+    const int32_t* prow = nullptr;
+    auto enter = [&] {                               // the cursor moved into a triple: past its fresh blocks
+      if (!at_len_ok(a, pre.len)) return;
+      if (pre.i < nfresh) {
+        const int skip = min(nfresh - pre.i, left);
+        pre.i += skip;
+        left -= skip;
+      }
+      if (left <= 0 || pre.i >= pre.units) return;
+      const int c = pre.i - nfresh;
+      prow = a.table + static_cast<long long>(pre.b) * a.W + c / bpp;
+      pblk = c % bpp;
+      phead = pre.pair / a.row_tiles;
+      if (c * Q4_BLOCK < pre.len) page = __ldg(prow);
+    };
+    enter();
+    auto fetch = [&](int s) {                        // the next cached block of the share into stage s
+      have &= ~(1u << s);
+      // triples without a block to fetch are passed over
+      while (left > 0 && (pre.i >= pre.units || !at_len_ok(a, pre.len) || (pre.i - nfresh) * Q4_BLOCK >= pre.len)) {
+        if (pre.i < pre.units) {                     // its one empty block
+          pre.i = pre.units;
+          --left;
+          continue;
+        }
+        pre.i = pre.units - 1;
+        at_next(a, prefix, HR, pre);
+        enter();
+      }
+      if (left <= 0) return;
+      --left;
       if (page >= 0 && page < a.pages) {
         have |= 1u << s;
         if (lane == 0) {
@@ -645,190 +793,215 @@ __global__ void __launch_bounds__(AT_THREADS, at_ctas(NR)) attend_q4_kernel(cons
           mbar_arrive_expect_tx(&bars[s], SB);
           bulk_g2s(ring + s * SB, a.cache + blk * SB, SB, &bars[s]);
         }
-      } else {
-        bad |= 1u << s;
       }
-    }
-    if (pre.i + 1 < pre.units) {
       ++pre.i;
       if (++pblk == bpp) {
         pblk = 0;
         ++prow;
-        if (pre.i < pcached) page = __ldg(prow);
+        if (pre.i < pre.units) page = __ldg(prow);
       }
-    } else if (left > 0) {
-      at_next(a, prefix, HR, pre);
-      triple();
-    }
-  };
-  for (int s = 0; s < stages; ++s) fetch(s);
+    };
+    for (int s = 0; s < stages; ++s) fetch(s);
 
-  bool failed = false;
-  int stage = 0;
-  for (long long u = u0; u < u1 && !failed;) {
-    // one triple, or the part of it that lies in the share
-    const int h = cur.pair / a.row_tiles, row0 = (cur.pair - h * a.row_tiles) * 8 * NR;
-    const int first = cur.i, last = static_cast<int>(min(static_cast<long long>(cur.units), first + (u1 - u)));
-    const bool len_ok = at_len_ok(a, cur.len);
-    const int cached = len_ok ? (cur.len + Q4_BLOCK - 1) / Q4_BLOCK : 0;
-    bool poison = !len_ok;
-    st.clear();
-    at_load_q<D, NR>(a, cur.b, h, row0, rows, qf, st);
-    for (int i = first; i < last; ++i) {
-      if (i < cached) {
+    for (long long u = u0;;) {
+      // one triple, or the part of it that lies in the share
+      h = cur.pair / a.row_tiles;
+      row0 = (cur.pair - h * a.row_tiles) * 8 * NR;
+      first = cur.i;
+      last = static_cast<int>(min(static_cast<long long>(cur.units), first + (u1 - u)));
+      upiece = u;
+      bool poison = !at_len_ok(a, cur.len);
+      const int nf = poison ? 0 : nfresh, ncached = poison ? 0 : (cur.len + Q4_BLOCK - 1) / Q4_BLOCK;
+      if (first < nf) {
+        at_fresh<D, NR>(a, cur.b, h, row0, rows, first, min(last, nf), fresh_at);
+        st.load(fresh_at);
+      } else {
+        st.clear();
+      }
+      const int c1 = min(last - nf, ncached);
+      int c = max(first - nf, 0);
+      if (c < c1) at_load_q<D, NR>(a, cur.b, h, row0, rows, qf, st);
+      for (; c < c1; ++c) {
         if (have & (1u << stage)) {
           if (!mbar_wait(&bars[stage], (phase >> stage) & 1u, a.timeout_ns)) {
             failed = true;
             break;   // no copy is started after one that did not arrive
           }
           phase ^= 1u << stage;
-          at_cached_block<D, NR>(ring + stage * SB, min(cur.len - i * Q4_BLOCK, Q4_BLOCK), qf, st);
+          at_cached_block<D, NR>(ring + stage * SB, min(cur.len - c * Q4_BLOCK, Q4_BLOCK), qf, st);
         } else {
           poison = true;
         }
-      } else if (a.k_new && len_ok) {
-        at_fresh_block<D, NR>(a, cur.b, h, row0, rows, (i - cached) * Q4_BLOCK, st);
+        __syncwarp();
+        fetch(stage);
+        stage = stage + 1 == stages ? 0 : stage + 1;
       }
-      __syncwarp();
-      fetch(stage);
-      stage = stage + 1 == stages ? 0 : stage + 1;
+      if (failed) break;
+      if (poison) {
+#pragma unroll
+        for (int j = 0; j < NR; ++j) st.l[j][0] = st.l[j][1] = __int_as_float(0x7fc00000);
+      }
+      u += last - first;
+      if (first == 0 && last == cur.units) at_write<D, NR>(a, cur.b, h, row0, rows, st);
+      else if (first != 0) st.save(mine);
+      if (u >= u1) break;
+      cur.i = last - 1;
+      at_next(a, prefix, HR, cur);
     }
-    if (failed) break;
-    u += last - first;
-
-    const bool whole = first == 0 && last == cur.units;
-    float* part = a.ws + (static_cast<size_t>(share) * 2 + (first == 0 ? 1 : 0)) * at_partial_floats(D, NR);
+    if (failed) {
+      // copies still on their way land before the warp goes on (or the wait gives up)
+      for (int s = 0; s < stages; ++s)
+        if (s != stage && (have & (1u << s))) mbar_wait(&bars[s], (phase >> s) & 1u, a.timeout_ns);
+      // every triple of the share from here on is void
+      bool again = true;
+      for (long long u = upiece; again;) {
+        st.clear();
 #pragma unroll
-    for (int j = 0; j < NR; ++j)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float l = st.l[j][e];
-        l += __shfl_xor_sync(0xffffffffu, l, 4);
-        l += __shfl_xor_sync(0xffffffffu, l, 8);
-        l += __shfl_xor_sync(0xffffffffu, l, 16);
-        if (poison) l = __int_as_float(0x7fc00000);
-        const int lr = 8 * j + 2 * t + e, r = row0 + lr;
-        if (whole) {
-          if (r >= rows) continue;
-          const long long at = at_row(a, cur.b, h, r);
-          const float inv = l == 0.f ? 0.f : a.v_mul / l;
-          uint4* p = reinterpret_cast<uint4*>(a.out + at * D + g * (D / 8));
-#pragma unroll
-          for (int i = 0; i < D / 16; i += 4)
-            p[i / 4] = make_uint4(bf16x2_pack(st.o[j][i][e] * inv, st.o[j][i][e + 2] * inv),
-                                  bf16x2_pack(st.o[j][i + 1][e] * inv, st.o[j][i + 1][e + 2] * inv),
-                                  bf16x2_pack(st.o[j][i + 2][e] * inv, st.o[j][i + 2][e + 2] * inv),
-                                  bf16x2_pack(st.o[j][i + 3][e] * inv, st.o[j][i + 3][e + 2] * inv));
-          if (a.lse && g == 0) a.lse[at] = at_lse(st.m[j][e], l);
-        } else {
-          float4* p = reinterpret_cast<float4*>(part + static_cast<size_t>(lr) * D + g * (D / 8));
-#pragma unroll
-          for (int i = 0; i < D / 16; i += 2)
-            p[i / 2] = make_float4(st.o[j][i][e], st.o[j][i][e + 2], st.o[j][i + 1][e], st.o[j][i + 1][e + 2]);
-          if (g == 0) {
-            part[8 * NR * D + lr] = st.m[j][e];
-            part[8 * NR * D + 8 * NR + lr] = l;
-          }
+        for (int j = 0; j < NR; ++j) st.l[j][0] = st.l[j][1] = __int_as_float(0x7fc00000);
+        h = cur.pair / a.row_tiles;
+        row0 = (cur.pair - h * a.row_tiles) * 8 * NR;
+        first = cur.i;
+        last = static_cast<int>(min(static_cast<long long>(cur.units), first + (u1 - u)));
+        upiece = u;
+        u += last - first;
+        if (first == 0 && last == cur.units) at_write<D, NR>(a, cur.b, h, row0, rows, st);
+        else if (first != 0) st.save(mine);
+        again = u < u1;
+        if (again) {
+          cur.i = last - 1;
+          at_next(a, prefix, HR, cur);
         }
       }
-    cur.i = last - 1;
-    if (u < u1) at_next(a, prefix, HR, cur);
+    }
   }
-  if (failed) {
-    // copies still on their way land before the warp leaves (or the wait gives up)
-    for (int s = 0; s < stages; ++s)
-      if (s != stage && (have & (1u << s))) mbar_wait(&bars[s], (phase >> s) & 1u, a.timeout_ns);
-    // every triple of the share is void
+  __syncthreads();
+
+  // Joins within the CTA.  A triple that begins in a warp's share and goes on is
+  // joined by that warp, whose registers hold its first part; the other parts
+  // were saved.
+  if (u0 < u1 && first == 0 && last != cur.units) {
+    const long long tri_end = upiece + cur.units;
+    for (int w = warp + 1; w < AT_WARPS; ++w) {
+      const long long s0 = at_start(units, shares, share + w - warp), s1 = at_start(units, shares, share + w - warp + 1);
+      if (s0 >= tri_end) break;
+      if (s0 < s1) st.join(states + w * at_state_floats(D, NR));
+    }
+    if (tri_end <= at_start(units, shares, (blockIdx.x + 1) * AT_WARPS)) at_write<D, NR>(a, cur.b, h, row0, rows, st);
+    else at_write_partial<D, NR>(cta_ws + at_partial_floats(D, NR), st);
+  }
+  // A triple that came from the CTA before is joined by warp 0.
+  if (warp == 0) {
     AtCursor c;
     at_seek(a, prefix, HR, u0, c);
-    for (long long u = u0; u < u1;) {
-      const long long end = min(u1, u + c.units - c.i);
-      const bool whole = c.i == 0 && end - u == c.units;
-      const int h = c.pair / a.row_tiles, row0 = (c.pair - h * a.row_tiles) * 8 * NR;
-      float* part = a.ws + (static_cast<size_t>(share) * 2 + (c.i == 0 ? 1 : 0)) * at_partial_floats(D, NR);
-      for (int lr = lane; lr < 8 * NR; lr += 32) {
-        const int r = row0 + lr;
-        if (!whole) {
-          for (int d = 0; d < D; ++d) part[lr * D + d] = 0.f;
-          part[8 * NR * D + lr] = 0.f;
-          part[8 * NR * D + 8 * NR + lr] = __int_as_float(0x7fc00000);
-        } else if (r < rows) {
-          const long long at = at_row(a, c.b, h, r);
-          for (int d = 0; d < D; ++d) a.out[at * D + d] = 0x7fc0u;
-          if (a.lse) a.lse[at] = __int_as_float(0x7fc00000);
-        }
+    if (c.i != 0) {
+      const long long tri_end = u0 + (c.units - c.i);
+      st.clear();
+      for (int w = 0; w < AT_WARPS; ++w) {
+        const long long s0 = at_start(units, shares, share + w), s1 = at_start(units, shares, share + w + 1);
+        if (s0 >= tri_end) break;
+        if (s0 < s1) st.join(states + w * at_state_floats(D, NR));
       }
-      for (; u < end; ++u) at_next(a, prefix, HR, c);
+      at_write_partial<D, NR>(cta_ws, st);
     }
   }
 }
 
-// Joins the partials of triples that several shares worked on: a CTA a row of a
-// triple; its warps take the shares in turn (a lane D / 32 columns), then their
-// results are joined in order.
-constexpr int ATJ_WARPS = 4, ATJ_THREADS = 32 * ATJ_WARPS;
-template <int D, int NR>
-__global__ void __launch_bounds__(ATJ_THREADS) attend_q4_join_kernel(const AttendArgs a, int warps) {
+// Joins the partials of triples that several CTAs worked on: a warp takes eight
+// rows of a triple (a lane D / 32 columns).  Where a triple is spread over many
+// CTAs, a CTA's warps take its partials in turn and their results are joined.
+constexpr int ATJ_WARPS = 8, ATJ_THREADS = 32 * ATJ_WARPS;
+template <int D, int NR, bool SPREAD>
+__global__ void __launch_bounds__(ATJ_THREADS) attend_q4_join_kernel(const __grid_constant__ AttendArgs a, int grid) {
   extern __shared__ __align__(128) unsigned char at_smem[];
   __shared__ long long scratch[ATJ_WARPS];
-  __shared__ float sm[ATJ_WARPS], sl[ATJ_WARPS], so[ATJ_WARPS][D];
+  constexpr int C = D / 32, PL = SPREAD ? ATJ_WARPS : 1;
+  __shared__ float sml[PL][2][8], so[PL][8][SPREAD ? D : 1];
   long long* prefix = reinterpret_cast<long long*>(at_smem);
   at_prefix<ATJ_THREADS>(a, prefix, scratch);
-  constexpr int C = D / 32;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int HR = a.Hkv * a.row_tiles, rows = a.N * a.G;
   const long long units = prefix[a.B] * HR;
-  const int shares = at_shares(units, warps);
-  const int per = min(rows, 8 * NR);   // rows of a tile that can be real
-  for (long long x = blockIdx.x; x < static_cast<long long>(a.B) * HR * per; x += gridDim.x) {
-    const long long y = x / per;
-    const int lr = static_cast<int>(x - y * per), b = static_cast<int>(y / HR), pair = static_cast<int>(y % HR);
+  const int ctas = at_active(units, grid);
+  const int items = a.B * HR * NR;
+  const int step = gridDim.x * (SPREAD ? 1 : ATJ_WARPS);
+  for (int x = SPREAD ? blockIdx.x : blockIdx.x * ATJ_WARPS + warp; x < items; x += step) {
+    const int y = x / NR, j = x - y * NR, b = y / HR, pair = y - b * HR;
     const long long n = prefix[b + 1] - prefix[b], u = prefix[b] * HR + pair * n;
-    const int wa = at_owner(units, shares, u), wb = at_owner(units, shares, u + n - 1);
+    const int wa = at_owner(units, ctas, u), wb = at_owner(units, ctas, u + n - 1);
     if (wa == wb) continue;
-    const int h = pair / a.row_tiles, r = (pair - h * a.row_tiles) * 8 * NR + lr;
-    if (r >= rows) continue;
-    float m = kNegInf, l = 0.f, o[C];
+    const int h = pair / a.row_tiles, r0 = ((pair - h * a.row_tiles) * NR + j) * 8;
+    if (r0 >= rows) continue;
+    float m[8], l[8], o[8][C];
 #pragma unroll
-    for (int i = 0; i < C; ++i) o[i] = 0.f;
-#pragma unroll 4
-    for (int w = wa + warp; w <= wb; w += ATJ_WARPS) {
-      const float* part = a.ws + (static_cast<size_t>(w) * 2 + (w == wa ? 1 : 0)) * at_partial_floats(D, NR);
-      const float pm = part[8 * NR * D + lr], pl = part[8 * NR * D + 8 * NR + lr];
-      float po[C];
+    for (int r = 0; r < 8; ++r) {
+      m[r] = kNegInf;
+      l[r] = 0.f;
 #pragma unroll
-      for (int i = 0; i < C; ++i) po[i] = part[lr * D + i * 32 + lane];
-      const float mn = fmaxf(m, pm), ref = mn == kNegInf ? 0.f : mn;
-      const float c0 = at_corr(m - ref), c1 = at_corr(pm - ref);
-      l = l * c0 + pl * c1;
-#pragma unroll
-      for (int i = 0; i < C; ++i) o[i] = o[i] * c0 + po[i] * c1;
-      m = mn;
+      for (int i = 0; i < C; ++i) o[r][i] = 0.f;
     }
-    if (lane == 0) {
-      sm[warp] = m;
-      sl[warp] = l;
-    }
+    for (int w = wa + (SPREAD ? warp : 0); w <= wb; w += PL) {
+      const float* part = a.ws + static_cast<size_t>(w) * at_cta_floats(D, NR) + (w == wa ? at_partial_floats(D, NR) : 0);
+      float pm[8], pl[8], po[8][C];
 #pragma unroll
-    for (int i = 0; i < C; ++i) so[warp][i * 32 + lane] = o[i];
-    __syncthreads();
-    if (threadIdx.x < D) {
-      m = kNegInf;
-      for (int w = 0; w < ATJ_WARPS; ++w) m = fmaxf(m, sm[w]);
-      const float ref = m == kNegInf ? 0.f : m;
-      float sum = 0.f;
-      l = 0.f;
-      for (int w = 0; w < ATJ_WARPS; ++w) {
-        const float c = at_corr(sm[w] - ref);
-        l += sl[w] * c;
-        sum += so[w][threadIdx.x] * c;
+      for (int r = 0; r < 8; ++r) {
+        pm[r] = part[8 * NR * D + 8 * j + r];
+        pl[r] = part[8 * NR * D + 8 * NR + 8 * j + r];
+#pragma unroll
+        for (int i = 0; i < C; ++i) po[r][i] = part[(8 * j + r) * D + i * 32 + lane];
       }
-      const long long at = at_row(a, b, h, r);
-      const uint32_t two = bf16x2_pack(sum * (l == 0.f ? 0.f : a.v_mul / l), 0.f);
-      a.out[at * D + threadIdx.x] = static_cast<uint16_t>(two);
-      if (a.lse && threadIdx.x == 0) a.lse[at] = at_lse(m, l);
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        const float mn = fmaxf(m[r], pm[r]), ref = mn == kNegInf ? 0.f : mn;
+        const float c0 = at_corr(m[r] - ref), c1 = at_corr(pm[r] - ref);
+        l[r] = l[r] * c0 + pl[r] * c1;
+#pragma unroll
+        for (int i = 0; i < C; ++i) o[r][i] = o[r][i] * c0 + po[r][i] * c1;
+        m[r] = mn;
+      }
     }
-    __syncthreads();
+    if constexpr (SPREAD) {
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        if (lane == 0) {
+          sml[warp][0][r] = m[r];
+          sml[warp][1][r] = l[r];
+        }
+#pragma unroll
+        for (int i = 0; i < C; ++i) so[warp][r][i * 32 + lane] = o[r][i];
+      }
+      __syncthreads();
+      // warp r joins row r
+      const int r = r0 + warp;
+      if (r < rows) {
+        float mx = kNegInf, sum = 0.f, acc[C];
+        for (int w = 0; w < PL; ++w) mx = fmaxf(mx, sml[w][0][warp]);
+        const float ref = mx == kNegInf ? 0.f : mx;
+#pragma unroll
+        for (int i = 0; i < C; ++i) acc[i] = 0.f;
+        for (int w = 0; w < PL; ++w) {
+          const float c = at_corr(sml[w][0][warp] - ref);
+          sum += sml[w][1][warp] * c;
+#pragma unroll
+          for (int i = 0; i < C; ++i) acc[i] += so[w][warp][i * 32 + lane] * c;
+        }
+        const long long at = at_row(a, b, h, r);
+        const float inv = sum == 0.f ? 0.f : a.v_mul / sum;
+#pragma unroll
+        for (int i = 0; i < C; ++i) a.out[at * D + i * 32 + lane] = static_cast<uint16_t>(bf16x2_pack(acc[i] * inv, 0.f));
+        if (a.lse && lane == 0) a.lse[at] = at_lse(mx, sum);
+      }
+      __syncthreads();
+    } else {
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        if (r0 + r >= rows) continue;
+        const long long at = at_row(a, b, h, r0 + r);
+        const float inv = l[r] == 0.f ? 0.f : a.v_mul / l[r];
+#pragma unroll
+        for (int i = 0; i < C; ++i) a.out[at * D + i * 32 + lane] = static_cast<uint16_t>(bf16x2_pack(o[r][i] * inv, 0.f));
+        if (a.lse && lane == 0) a.lse[at] = at_lse(m[r], l[r]);
+      }
+    }
   }
 }
 

@@ -67,9 +67,17 @@ spec_status_t launch_attend(const DevInfo& di, int dev, const AttendArgs& a, cud
   kern<<<grid, AT_THREADS, smem, st>>>(a, stages);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "attention launch");
-  const long long rows = static_cast<long long>(a.B) * a.Hkv * a.row_tiles * std::min(a.N * a.G, 8 * NR);
-  const int jgrid = static_cast<int>(std::min<long long>(rows, static_cast<long long>(di.sms) * 16));
-  attend_q4_join_kernel<D, NR><<<jgrid, ATJ_THREADS, 8 * (static_cast<size_t>(a.B) + 1), st>>>(a, grid * AT_WARPS);
+  // Few triples: each is spread over many CTAs, and a CTA joins eight rows of
+  // one; else a warp does.
+  const long long items = static_cast<long long>(a.B) * a.Hkv * a.row_tiles * NR;
+  const size_t jsmem = 8 * (static_cast<size_t>(a.B) + 1);
+  if (items > 0x7fffffffLL) return fail(SPEC_ERR_UNSUPPORTED, "batch too large for one call");
+  if (static_cast<long long>(a.B) * a.Hkv * a.row_tiles * 4 <= grid) {
+    attend_q4_join_kernel<D, NR, true><<<static_cast<unsigned>(items), ATJ_THREADS, jsmem, st>>>(a, grid);
+  } else {
+    const int jgrid = static_cast<int>(std::min<long long>((items + ATJ_WARPS - 1) / ATJ_WARPS, static_cast<long long>(di.sms) * 4));
+    attend_q4_join_kernel<D, NR, false><<<jgrid, ATJ_THREADS, jsmem, st>>>(a, grid);
+  }
   e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "attention join launch");
   return SPEC_OK;
@@ -266,8 +274,7 @@ size_t spec_attend_workspace_bytes(int B, int N, int Hq, int Hkv, int D) {
     return 0;
   int tiles, NR;
   attend_tiles(N * (Hq / Hkv), tiles, NR);
-  const size_t shares = static_cast<size_t>(kMaxSms) * at_ctas(NR) * AT_WARPS;
-  return align_up(shares * 2 * at_partial_floats(D, NR) * sizeof(float), 256);
+  return align_up(static_cast<size_t>(kMaxSms) * at_ctas(NR) * at_cta_floats(D, NR) * sizeof(float), 256);
 }
 
 spec_status_t spec_attend_q4(const void* q, const void* k_new, const void* v_new, const uint32_t* masks,
