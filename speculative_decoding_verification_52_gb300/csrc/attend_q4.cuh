@@ -11,14 +11,24 @@
 // element has to cross the HBM bus is the bound, and the work next to it is to
 // unpack the codes: the budget is about three instructions an element.
 //
-// * The unit of work is a block of 32 tokens (one contiguous run of 36 * D
-//   bytes, one bulk copy).  All blocks of all (sequence, head, row tile) triples
-//   form one list, a triple's fresh blocks before its cached ones; every warp
-//   takes an equal, contiguous share of it, whatever the lengths, and fetches it
-//   through a ring of its own.  A triple that lies in one warp's share is
-//   finished there.  The warps of a CTA have neighbouring shares and join what
-//   they share at the end; what CTAs share goes through the workspace (maximum,
-//   sum, sum of v) and a second kernel.  All joins are in the list's order.
+// * The unit of work is a tile of 64 tokens: two blocks, each one contiguous run
+//   of 36 * D bytes and one bulk copy.  All tiles of all (sequence, head, row
+//   tile) triples form one list, a triple's fresh tiles before its cached ones;
+//   every pair of warps takes an equal, contiguous share of it, whatever the
+//   lengths, and fetches it through a ring of its own.  A triple that lies in one
+//   pair's share is finished there.  A fresh tile counts as three: it waits for
+//   its loads, where a cached tile's have arrived (chains of 6 nodes over lengths
+//   of 512 to 3,584: FRESH1_US when it counts as one).  The pairs of a CTA have neighbouring shares
+//   and join what they share at the end; what CTAs share goes through the
+//   workspace (maximum, sum, sum of v) and a second kernel.  All joins are in the
+//   list's order.
+// * In a pair, each warp scores one block; the weights are exchanged, and each
+//   warp adds up one half of v's columns over both blocks.  So every code is
+//   unpacked once for all rows, and the sums of a warp fit its registers beside
+//   the operands (a warp that kept all columns of 24 rows moved 137 registers a
+//   block through local memory: 450 us where this takes CHAIN_US).  One barrier of
+//   the two warps a tile: the weights are taken against a maximum that both know,
+//   2^(z - ref + 7), and only a score above ref + 8 makes them agree on a new one.
 // * Everything is unpacked in f16, exactly: a code times its scale has 6
 //   significant bits.  q enters as f16 too, scaled by a power of two per row so
 //   that its largest element lies in [128, 256): what f16 then cannot hold is
@@ -27,7 +37,7 @@
 //   mma.m16n8k16 with the rows as N, eight at a time: k q^T (tokens as M), then
 //   v^T p^T (columns as M).  A thread's part of a key operand is D / 4
 //   consecutive elements of one token (the contraction index is permuted alike
-//   in q), of a value operand D / 8 consecutive elements of four tokens (the
+//   in q), of a value operand D / 16 consecutive elements of four tokens (the
 //   output columns are permuted), with the nibbles of two tokens interleaved
 //   before they are widened.  The weights pass from the first product's result
 //   to the second's operand by an 8 x 8 transpose across the warp.  The tokens
@@ -38,8 +48,8 @@
 //   (D = 128) crosses the bus in about 196 clocks; it takes 128 conversions, 128
 //   multiplications (64 clocks each) and 32 products per eight rows (64 clocks).
 //   With the rows as M, 16 at a time, eight rows cost 128 clocks of products.
-// * The weights of v are 2^(z - max + 15) in f16: the largest is 2^15, so a
-//   weight has 11 significant bits down to 2^-29 of it.  Sums are fp32.
+// * The weights of v are f16 of at most 2^15: a weight has 11 significant bits
+//   down to 2^-21 of the largest and a step of 2^-31 below.  Sums are fp32.
 // * The fresh entries are bf16 with bf16's range, so their blocks use bf16
 //   products, with each weight as the sum of two bf16.
 #pragma once
@@ -49,10 +59,14 @@
 
 namespace sv {
 
-constexpr int AT_WARPS = 4;                 // warps of a CTA
-constexpr int AT_THREADS = 32 * AT_WARPS;
+constexpr int AT_PAIRS = 2;                 // pairs of warps of a CTA
+constexpr int AT_THREADS = 64 * AT_PAIRS;
+constexpr int AT_TILE = 2 * Q4_BLOCK;       // tokens of a tile
+constexpr int AT_FRESH = 3;                 // what a fresh tile counts in the list, in cached tiles
+constexpr int AT_QUEUE = 32;                // places of a pair's list of fetches
 constexpr int AT_MAX_B = 4096;
-constexpr float AT_PSHIFT = 15.f;           // log2 of the largest weight
+constexpr float AT_PSHIFT = 7.f;            // a score equal to the reference gets the weight 2^7,
+constexpr float AT_ABOVE = 8.f;             // and one so far above it is the largest that it serves
 
 struct AttendArgs {
   const uint16_t* q;         // [B, N, Hkv * G, D] bf16
@@ -75,14 +89,14 @@ struct AttendArgs {
 // ---------------------------------------------------------------------------
 // the list of work
 // ---------------------------------------------------------------------------
-// Blocks of sequence b for one (head, row tile): its cached blocks, then the
-// blocks of fresh entries; at least one, so that every output is written.
+// Units of sequence b for one (head, row tile): those of the fresh tiles, then the
+// cached tiles; at least one, so that every output is written.
 __device__ __forceinline__ bool at_len_ok(const AttendArgs& a, int len) {
   return len >= 0 && static_cast<long long>(len) <= static_cast<long long>(a.W) * a.P;
 }
 __device__ __forceinline__ int at_units(const AttendArgs& a, int len) {
   if (!at_len_ok(a, len)) return 1;
-  const int n = (len + Q4_BLOCK - 1) / Q4_BLOCK + (a.k_new ? (a.N + Q4_BLOCK - 1) / Q4_BLOCK : 0);
+  const int n = (len + AT_TILE - 1) / AT_TILE + (a.k_new ? AT_FRESH * ((a.N + AT_TILE - 1) / AT_TILE) : 0);
   return n > 0 ? n : 1;
 }
 
@@ -117,7 +131,7 @@ __device__ void at_prefix(const AttendArgs& a, long long* prefix, long long* scr
 
 // position in the list
 struct AtCursor {
-  int b, pair, i, units;   // sequence, (head, row tile) of it, block of it, its blocks
+  int b, pair, i, units;   // sequence, (head, row tile) of it, unit of it, its units
   int len;
 };
 __device__ __forceinline__ void at_seek(const AttendArgs& a, const long long* prefix, int HR, long long u, AtCursor& c) {
@@ -144,9 +158,9 @@ __device__ __forceinline__ void at_next(const AttendArgs& a, const long long* pr
   c.units = static_cast<int>(prefix[c.b + 1] - prefix[c.b]);
 }
 
-// CTAs that get work: the list is cut in AT_WARPS shares a CTA, none of the CTAs empty
+// CTAs that get work: the list is cut in AT_PAIRS shares a CTA, none of the CTAs empty
 __device__ __forceinline__ int at_active(long long units, int ctas) {
-  return static_cast<int>(min((units + AT_WARPS - 1) / AT_WARPS, static_cast<long long>(ctas)));
+  return static_cast<int>(min((units + AT_PAIRS - 1) / AT_PAIRS, static_cast<long long>(ctas)));
 }
 // share w of n of a list of `units`: [at_start(w), at_start(w + 1)), and the share that unit u falls in
 __device__ __forceinline__ long long at_start(long long units, int n, long long w) { return units * w / n; }
@@ -162,6 +176,12 @@ __device__ __forceinline__ void mma_f16(float* d, const uint4& a, uint32_t b0, u
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16_zero(float* d, const uint4& a, uint32_t b0, uint32_t b1) {   // no addend
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ void mma_bf16(float* d, const uint4& a, uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -210,29 +230,42 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return r;
 }
 
-__host__ __device__ constexpr int at_stage_bytes(int D) { return q4_block_bytes(D); }
+__host__ __device__ constexpr int at_stage_bytes(int D) { return 2 * q4_block_bytes(D); }
+// of a pair: the queries' operand; in exchange, two buffers each, the weights
+// (each warp's operands), the maxima or sums, and the flags; a flag a stage (at
+// most 8); the list of fetches
 __host__ __device__ constexpr int at_q_bytes(int D, int NR) { return NR * (D / 32) * 512; }
+__host__ __device__ constexpr int at_p_bytes(int NR) { return 2 * 2 * 2 * NR * 256; }
+__host__ __device__ constexpr int at_m_bytes(int NR) { return 2 * 2 * 8 * NR * 4; }
+__host__ __device__ constexpr int at_pair_bytes(int D, int NR) { return at_q_bytes(D, NR) + at_p_bytes(NR) + at_m_bytes(NR) + 64 + 8 * AT_QUEUE; }
 // The workspace.  A CTA has two partials, of the triple that it shares with the
 // CTAs before it and of the one that it shares with those behind:
-//   [8 NR rows x D] sums of v, then m[8 NR], l[8 NR];
+//   [8 NR rows x D] sums of v, then m[8 NR], l[8 NR] of the first and the second
+//   half of the columns' warps;
 // a warp has two copies of a state in its lanes' order: what its CTA's other
-// warps join, and the result of a triple's fresh blocks.
-__host__ __device__ constexpr size_t at_partial_floats(int D, int NR) { return static_cast<size_t>(8 * NR) * (D + 2); }
-__host__ __device__ constexpr size_t at_state_floats(int D, int NR) { return static_cast<size_t>(32 * NR) * (D / 4 + 4); }
+// pairs join, and the result of a triple's fresh tiles.
+__host__ __device__ constexpr size_t at_partial_floats(int D, int NR) { return static_cast<size_t>(8 * NR) * (D + 4); }
+__host__ __device__ constexpr size_t at_state_floats(int D, int NR) { return static_cast<size_t>(32 * NR) * (D / 8 + 4); }
 __host__ __device__ constexpr size_t at_cta_floats(int D, int NR) {
-  return 2 * at_partial_floats(D, NR) + 2 * AT_WARPS * at_state_floats(D, NR);
+  return 2 * at_partial_floats(D, NR) + 4 * AT_PAIRS * at_state_floats(D, NR);
+}
+
+__device__ __forceinline__ long long at_row(const AttendArgs& a, int b, int h, int r) {
+  const int n = r / a.G;
+  return ((static_cast<long long>(b) * a.N + n) * a.Hkv + h) * a.G + (r - n * a.G);
 }
 
 // ---------------------------------------------------------------------------
-// the state of one (sequence, head, row tile) in a warp's registers: lane
-// (g, t) holds rows 8 j + 2 t + e and the D / 8 columns from g * D / 8
+// the state of one (sequence, head, row tile) in a warp's registers: warp x of
+// the pair, lane (g, t) holds rows 8 j + 2 t + e and the D / 16 columns from
+// x * D / 2 + g * D / 16
 // ---------------------------------------------------------------------------
 template <int D, int NR>
 struct AtState {
-  static constexpr int MT = D / 16;   // products that cover the output's columns
-  float o[NR][MT][4];                 // [.][i][e + 2 f]: column g * D / 8 + 2 i + f of row e
-  float m[NR][2], l[NR][2];           // running maximum (log2 domain) and this lane's part of the sum
-  float c[NR][2];                     // factor from a row's f16 products to the log2 domain
+  static constexpr int MT = D / 32;   // products that cover the warp's columns
+  float o[NR][MT][4];                 // [.][i][e + 2 f]: column 2 i + f of the lane's
+  float ref[NR][2];                   // what the weights are relative to (log2 domain; the pair's)
+  float l[NR][2];                     // this lane's part of the sum of weights
 
   __device__ __forceinline__ void clear() {
 #pragma unroll
@@ -241,19 +274,35 @@ struct AtState {
       for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[j][i][k] = 0.f;
-      m[j][0] = m[j][1] = kNegInf;
+      ref[j][0] = ref[j][1] = kNegInf;
       l[j][0] = l[j][1] = 0.f;
     }
   }
+  __device__ __forceinline__ void poison() {
+#pragma unroll
+    for (int j = 0; j < NR; ++j) l[j][0] = l[j][1] = __int_as_float(0x7fc00000);
+  }
+  // to a reference of `to` (not below the present one)
+  __device__ __forceinline__ void raise(int j, int e, float to) {
+    const float corr = to == kNegInf ? 1.f : at_corr(ref[j][e] - to);
+    l[j][e] *= corr;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      o[j][i][e] *= corr;
+      o[j][i][e + 2] *= corr;
+    }
+    ref[j][e] = to;
+  }
 
   // the state in the order of its lanes: only the lane that wrote a value reads it
+  // (or the same lane of the same half in another pair)
   __device__ __forceinline__ void save(float* p) const {
     float4* q = reinterpret_cast<float4*>(p) + (threadIdx.x & 31);
 #pragma unroll
     for (int j = 0; j < NR; ++j) {
 #pragma unroll
       for (int i = 0; i < MT; ++i) q[32 * (j * (MT + 1) + i)] = make_float4(o[j][i][0], o[j][i][1], o[j][i][2], o[j][i][3]);
-      q[32 * (j * (MT + 1) + MT)] = make_float4(m[j][0], m[j][1], l[j][0], l[j][1]);
+      q[32 * (j * (MT + 1) + MT)] = make_float4(ref[j][0], ref[j][1], l[j][0], l[j][1]);
     }
   }
   __device__ __forceinline__ void load(const float* p) {
@@ -266,7 +315,7 @@ struct AtState {
         o[j][i][0] = x.x; o[j][i][1] = x.y; o[j][i][2] = x.z; o[j][i][3] = x.w;
       }
       const float4 x = q[32 * (j * (MT + 1) + MT)];
-      m[j][0] = x.x; m[j][1] = x.y; l[j][0] = x.z; l[j][1] = x.w;
+      ref[j][0] = x.x; ref[j][1] = x.y; l[j][0] = x.z; l[j][1] = x.w;
     }
   }
   // joins a saved state of the same rows
@@ -276,75 +325,143 @@ struct AtState {
     for (int j = 0; j < NR; ++j) {
       const float4 x = q[32 * (j * (MT + 1) + MT)];
       const float pm[2] = {x.x, x.y}, pl[2] = {x.z, x.w};
-      float c0[2], c1[2];
+      float c1[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const float mn = fmaxf(m[j][e], pm[e]), ref = mn == kNegInf ? 0.f : mn;
-        c0[e] = at_corr(m[j][e] - ref);
-        c1[e] = at_corr(pm[e] - ref);
-        l[j][e] = l[j][e] * c0[e] + pl[e] * c1[e];
-        m[j][e] = mn;
+        const float to = fmaxf(ref[j][e], pm[e]);
+        raise(j, e, to);
+        c1[e] = at_corr(pm[e] - (to == kNegInf ? 0.f : to));
+        l[j][e] += pl[e] * c1[e];
       }
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         const float4 y = q[32 * (j * (MT + 1) + i)];
-        o[j][i][0] = o[j][i][0] * c0[0] + y.x * c1[0];
-        o[j][i][1] = o[j][i][1] * c0[1] + y.y * c1[1];
-        o[j][i][2] = o[j][i][2] * c0[0] + y.z * c1[0];
-        o[j][i][3] = o[j][i][3] * c0[1] + y.w * c1[1];
-      }
-    }
-  }
-
-  // z (log2 domain, -inf where masked; [.][.][e + 2 f]: token g + 8 f of row e)
-  // becomes the weights 2^(z - max + 15)
-  __device__ __forceinline__ void weigh(float (&z)[2][NR][4]) {
-#pragma unroll
-    for (int j = 0; j < NR; ++j) {
-      float mn[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float mx = fmaxf(fmaxf(z[0][j][e], z[0][j][e + 2]), fmaxf(z[1][j][e], z[1][j][e + 2]));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-        mn[e] = fmaxf(m[j][e], mx);
-      }
-      if (__any_sync(0xffffffffu, mn[0] > m[j][0] || mn[1] > m[j][1])) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float corr = mn[e] == kNegInf ? 1.f : at_corr(m[j][e] - mn[e]);
-          l[j][e] *= corr;
-#pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            o[j][i][e] *= corr;
-            o[j][i][e + 2] *= corr;
-          }
-          m[j][e] = mn[e];
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float ref = (mn[e] == kNegInf ? 0.f : mn[e]) - AT_PSHIFT;
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-          for (int f = 0; f < 2; ++f) z[mt][j][e + 2 * f] = ex2_approx(z[mt][j][e + 2 * f] - ref);
-        l[j][e] += (z[0][j][e] + z[0][j][e + 2]) + (z[1][j][e] + z[1][j][e + 2]);
+        o[j][i][0] += y.x * c1[0];
+        o[j][i][1] += y.y * c1[1];
+        o[j][i][2] += y.z * c1[0];
+        o[j][i][3] += y.w * c1[1];
       }
     }
   }
 };
 
-__device__ __forceinline__ long long at_row(const AttendArgs& a, int b, int h, int r) {
-  const int n = r / a.G;
-  return ((static_cast<long long>(b) * a.N + n) * a.Hkv + h) * a.G + (r - n * a.G);
+// What the two warps of a pair share.
+template <int D, int NR>
+struct AtPair {
+  unsigned char* base;   // of the pair's exchange area
+  int x, id;             // the warp's half; the pair's named barrier
+  __device__ __forceinline__ uint4* q() const { return reinterpret_cast<uint4*>(base); }
+  // a warp's operands of one buffer: [2 steps][NR][32 lanes]
+  __device__ __forceinline__ uint2* p(int buf, int warp) const {
+    return reinterpret_cast<uint2*>(base + at_q_bytes(D, NR)) + (buf * 2 + warp) * 2 * NR * 32;
+  }
+  __device__ __forceinline__ float* top(int buf, int warp) const {
+    return reinterpret_cast<float*>(base + at_q_bytes(D, NR) + at_p_bytes(NR)) + (buf * 2 + warp) * 8 * NR;
+  }
+  __device__ __forceinline__ int* flag(int buf, int warp) const {
+    return reinterpret_cast<int*>(base + at_q_bytes(D, NR) + at_p_bytes(NR) + at_m_bytes(NR)) + buf * 2 + warp;
+  }
+  __device__ __forceinline__ int* arrived(int stage) const { return flag(2, 0) + stage; }
+  __device__ __forceinline__ uint2* queue() const {
+    return reinterpret_cast<uint2*>(base + at_q_bytes(D, NR) + at_p_bytes(NR) + at_m_bytes(NR) + 64);
+  }
+  __device__ __forceinline__ void sync() const { named_bar_sync(id, 64); }
+};
+
+// The weights of the warp's block.  z (products, -inf where masked;
+// [.][.][e + 2 f]: token g + 8 f of row e) becomes 2^(z c - ref + 7); the
+// operands of both warps' blocks come back in `mine` and `other` ([step][j][half
+// of it]).  The exchange area has two buffers, taken in turn: with one barrier a
+// tile, what a warp writes for a tile was last read two barriers before.
+template <int D, int NR>
+__device__ __forceinline__ void at_weights(float (&z)[2][NR][4], uint2 (&mine)[2][NR], uint2 (&other)[2][NR], int buf,
+                                           const float (&c)[NR][2], const AtPair<D, NR>& pr, AtState<D, NR>& st) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  bool above = false;
+#pragma unroll
+  for (int j = 0; j < NR; ++j)
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      above |= fmaxf(fmaxf(z[0][j][e], z[0][j][e + 2]), fmaxf(z[1][j][e], z[1][j][e + 2])) * c[j][e] > st.ref[j][e] + AT_ABOVE;
+  above = __any_sync(0xffffffffu, above);
+  auto weigh = [&] {
+#pragma unroll
+    for (int j = 0; j < NR; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float r = AT_PSHIFT - (st.ref[j][e] == kNegInf ? 0.f : st.ref[j][e]);
+#pragma unroll
+        for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+          for (int f = 0; f < 2; ++f) z[mt][j][e + 2 * f] = ex2_approx(__fmaf_rn(z[mt][j][e + 2 * f], c[j][e], r));
+      }
+  };
+  auto pack = [&] {
+    uint2* out = pr.p(buf, pr.x) + lane;
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int j = 0; j < NR; ++j) {
+        mine[s][j] = make_uint2(transpose8(f16x2_pack(z[s][j][0], z[s][j][1])), transpose8(f16x2_pack(z[s][j][2], z[s][j][3])));
+        out[(s * NR + j) * 32] = mine[s][j];
+      }
+  };
+  if (!above) {
+    weigh();
+    pack();
+  } else {
+#pragma unroll
+    for (int j = 0; j < NR; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float m = fmaxf(fmaxf(z[0][j][e], z[0][j][e + 2]), fmaxf(z[1][j][e], z[1][j][e + 2]));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+        if (g == 0) pr.top(buf, pr.x)[8 * j + 2 * t + e] = m * c[j][e];
+      }
+  }
+  if (lane == 0) *pr.flag(buf, pr.x) = above;
+  pr.sync();
+  const bool above2 = *pr.flag(buf, pr.x ^ 1);
+  if (above || above2) {   // the pair agrees on new references
+#pragma unroll
+    for (int j = 0; j < NR; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float to = st.ref[j][e];
+        const float old = to;
+        if (above) to = fmaxf(to, pr.top(buf, pr.x)[8 * j + 2 * t + e]);
+        if (above2) to = fmaxf(to, pr.top(buf, pr.x ^ 1)[8 * j + 2 * t + e]);
+        st.raise(j, e, to);
+        if (!above) {
+          const float f = to == kNegInf ? 1.f : at_corr(old - to);
+#pragma unroll
+          for (int mt = 0; mt < 2; ++mt)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) z[mt][j][e + 2 * k] *= f;
+        }
+      }
+    if (above) weigh();
+    pack();
+    pr.sync();
+  }
+#pragma unroll
+  for (int j = 0; j < NR; ++j)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) st.l[j][e] += (z[0][j][e] + z[0][j][e + 2]) + (z[1][j][e] + z[1][j][e + 2]);
+  const uint2* in = pr.p(buf, pr.x ^ 1) + lane;
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int j = 0; j < NR; ++j) other[s][j] = in[(s * NR + j) * 32];
 }
 
-// Queries of a row tile: the f16 operand into the lane's own part of `qf`
-// (nothing is shared between lanes), the rows' factors into st.c.
+// Queries of a row tile: the f16 operand into `qf` (the same lanes of both warps
+// read what one of them wrote), the rows' factors from f16 products to the log2
+// domain into c.
 template <int D, int NR>
-__device__ __forceinline__ void at_load_q(const AttendArgs& a, int b, int h, int row0, int rows, uint4* qf, AtState<D, NR>& st) {
+__device__ __forceinline__ void at_load_q(const AttendArgs& a, int b, int h, int row0, int rows, const AtPair<D, NR>& pr, float (&c)[NR][2]) {
   constexpr int CH = D / 4, WK = D / 32;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
@@ -369,133 +486,153 @@ __device__ __forceinline__ void at_load_q(const AttendArgs& a, int b, int h, int
     top = fmax_nan(top, __shfl_xor_sync(0xffffffffu, top, 2));
     const int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
     const int sh = top > 0.f ? min(7 - ex, 100) : 0;
-    const float mul = __uint_as_float(static_cast<uint32_t>(127 + sh) << 23);
+    // (the factor is above zero, so that products compare as scores do: the
+    // scale's sign goes into the operand, and no scale at all becomes a tiny one)
+    const float mul = copysignf(__uint_as_float(static_cast<uint32_t>(127 + sh) << 23), a.scale_log2);
     // a row with a NaN or an infinity has no finite scores: the factor says so
-    const float c = top < __builtin_huge_valf()
-                        ? a.scale_log2 * a.k_mul * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23)
+    const float f = top < __builtin_huge_valf()
+                        ? fmaxf(fabsf(a.scale_log2) * a.k_mul * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23), 1.17549435e-38f)
                         : __int_as_float(0x7fc00000);
-    st.c[j][0] = __shfl_sync(0xffffffffu, c, 8 * t);
-    st.c[j][1] = __shfl_sync(0xffffffffu, c, 8 * t + 4);
+    c[j][0] = __shfl_sync(0xffffffffu, f, 8 * t);
+    c[j][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
 #pragma unroll
     for (int i = 0; i < CH / 8; ++i) {
       const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-      uint32_t f[4];
+      uint32_t y[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) f[k] = f16x2_pack(__uint_as_float(x[k] << 16) * mul, __uint_as_float(x[k] & 0xffff0000u) * mul);
-      qf[(j * WK + i) * 32 + lane] = make_uint4(f[0], f[1], f[2], f[3]);
+      for (int k = 0; k < 4; ++k) y[k] = f16x2_pack(__uint_as_float(x[k] << 16) * mul, __uint_as_float(x[k] & 0xffff0000u) * mul);
+      if (pr.x == 0) pr.q()[(j * WK + i) * 32 + lane] = make_uint4(y[0], y[1], y[2], y[3]);
     }
+  }
+  pr.sync();
+}
+
+// The codes of one product step of v (16 tokens), widened and scaled: w[k] the
+// lane's codes of tokens 2t, 2t+1 of the two groups of eight, `BYTES` bytes of
+// them from byte 0; sc their scale bytes.
+template <int BYTES, int NR, int MT>
+__device__ __forceinline__ void at_add_v(const uint32_t (&w)[4], int from, uint32_t s01, uint32_t s23, const uint2 (&p)[NR],
+                                         float (&o)[NR][MT][4]) {
+  uint32_t e01[4], o01[4], e23[4], o23[4];
+  e2m1x8_to_f16((w[0] & 0x0f0f0f0fu) | ((w[1] << 4) & 0xf0f0f0f0u), e01);
+  e2m1x8_to_f16(((w[0] >> 4) & 0x0f0f0f0fu) | (w[1] & 0xf0f0f0f0u), o01);
+  e2m1x8_to_f16((w[2] & 0x0f0f0f0fu) | ((w[3] << 4) & 0xf0f0f0f0u), e23);
+  e2m1x8_to_f16(((w[2] >> 4) & 0x0f0f0f0fu) | (w[3] & 0xf0f0f0f0u), o23);
+#pragma unroll
+  for (int i = 0; i < BYTES; ++i) {
+    const int y = from + i;
+    const uint4 v = make_uint4(f16x2_mul(e01[y], s01), f16x2_mul(o01[y], s01), f16x2_mul(e23[y], s23), f16x2_mul(o23[y], s23));
+#pragma unroll
+    for (int j = 0; j < NR; ++j) mma_f16(o[j][i], v, p[j].x, p[j].y);
   }
 }
 
-// A cached block: `left` tokens of it (1..32) belong to the sequence.
-template <int D, int NR>
-__device__ __forceinline__ void at_cached_block(const unsigned char* sb, int left, const uint4* qf, AtState<D, NR>& st) {
+// A cached tile: `left` tokens of it (1..64) belong to the sequence.
+// `after` runs once both warps are done with the tile before.
+template <int D, int NR, class F>
+__device__ __forceinline__ void at_cached_tile(const unsigned char* tile, int left, int buf, const float (&c)[NR][2],
+                                               const AtPair<D, NR>& pr, AtState<D, NR>& st, F&& after) {
   constexpr int WK = D / 32;   // words of a key chunk
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int tr = at_token(g);
   float z[2][NR][4];
-#pragma unroll
-  for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-    for (int j = 0; j < NR; ++j)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) z[mt][j][k] = 0.f;
-
-  uint32_t kw[4][WK];
-  uint32_t ks2[4][D / 64];   // the chunk's scales, each twice
-#pragma unroll
-  for (int nt = 0; nt < 4; ++nt) {
-    const int tok = 8 * nt + tr;
-    if constexpr (D == 128) {
-      const uint4 x = *reinterpret_cast<const uint4*>(sb + tok * 64 + t * 16);
-      kw[nt][0] = x.x; kw[nt][1] = x.y; kw[nt][2] = x.z; kw[nt][3] = x.w;
-      const uint32_t two = e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(sb + 32 * D + tok * 8 + t * 2));
-      ks2[nt][0] = __byte_perm(two, two, 0x1010);
-      ks2[nt][1] = __byte_perm(two, two, 0x3232);
-    } else {
-      const uint2 x = *reinterpret_cast<const uint2*>(sb + tok * 32 + t * 8);
-      kw[nt][0] = x.x; kw[nt][1] = x.y;
-      const uint32_t one = sb[32 * D + tok * 4 + t];
-      ks2[nt][0] = e4m3x2_to_f16(one | (one << 8));
-    }
-  }
-#pragma unroll
-  for (int w = 0; w < WK; ++w) {
-    uint4 qb[NR];
-#pragma unroll
-    for (int j = 0; j < NR; ++j) qb[j] = qf[(j * WK + w) * 32 + lane];
+  const int own = left - pr.x * Q4_BLOCK;   // tokens of the warp's block
+  if (own > 0) {
+    const unsigned char* sb = tile + pr.x * q4_block_bytes(D);
+    const uint4* qf = pr.q() + lane;
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt) {
-      uint32_t r0[4], r1[4];   // tokens g and g + 8
-      e2m1x8_to_f16(kw[2 * mt][w], r0);
-      e2m1x8_to_f16(kw[2 * mt + 1][w], r1);
+      uint32_t kw[2][WK];
+      uint32_t ks2[2][D / 64];   // the chunk's scales, each twice
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        r0[i] = f16x2_mul(r0[i], ks2[2 * mt][w / 2]);
-        r1[i] = f16x2_mul(r1[i], ks2[2 * mt + 1][w / 2]);
+      for (int f = 0; f < 2; ++f) {
+        const int tok = 16 * mt + 8 * f + tr;
+        if constexpr (D == 128) {
+          const uint4 x = *reinterpret_cast<const uint4*>(sb + tok * 64 + t * 16);
+          kw[f][0] = x.x; kw[f][1] = x.y; kw[f][2] = x.z; kw[f][3] = x.w;
+          const uint32_t two = e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(sb + 32 * D + tok * 8 + t * 2));
+          ks2[f][0] = __byte_perm(two, two, 0x1010);
+          ks2[f][1] = __byte_perm(two, two, 0x3232);
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2*>(sb + tok * 32 + t * 8);
+          kw[f][0] = x.x; kw[f][1] = x.y;
+          const uint32_t one = sb[32 * D + tok * 4 + t];
+          ks2[f][0] = e4m3x2_to_f16(one * 0x101u);
+        }
       }
-      const uint4 k0 = make_uint4(r0[0], r1[0], r0[1], r1[1]), k1 = make_uint4(r0[2], r1[2], r0[3], r1[3]);
 #pragma unroll
-      for (int j = 0; j < NR; ++j) {
-        mma_f16(z[mt][j], k0, qb[j].x, qb[j].y);
-        mma_f16(z[mt][j], k1, qb[j].z, qb[j].w);
+      for (int w = 0; w < WK; ++w) {
+        uint32_t r0[4], r1[4];   // tokens g and g + 8
+        e2m1x8_to_f16(kw[0][w], r0);
+        e2m1x8_to_f16(kw[1][w], r1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          r0[i] = f16x2_mul(r0[i], ks2[0][w / 2]);
+          r1[i] = f16x2_mul(r1[i], ks2[1][w / 2]);
+        }
+        const uint4 k0 = make_uint4(r0[0], r1[0], r0[1], r1[1]), k1 = make_uint4(r0[2], r1[2], r0[3], r1[3]);
+#pragma unroll
+        for (int j = 0; j < NR; ++j) {
+          const uint4 qb = qf[(j * WK + w) * 32];
+          if (w == 0) mma_f16_zero(z[mt][j], k0, qb.x, qb.y);
+          else mma_f16(z[mt][j], k0, qb.x, qb.y);
+          mma_f16(z[mt][j], k1, qb.z, qb.w);
+        }
       }
     }
   }
-#pragma unroll
-  for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-    for (int j = 0; j < NR; ++j)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) z[mt][j][k] *= st.c[j][k & 1];
-  if (left < Q4_BLOCK) {
+  if (own < Q4_BLOCK) {
 #pragma unroll
     for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
       for (int f = 0; f < 2; ++f)
-        if (16 * mt + 8 * f + tr >= left) {
+        if (16 * mt + 8 * f + tr >= own) {
 #pragma unroll
           for (int j = 0; j < NR; ++j) z[mt][j][2 * f] = z[mt][j][2 * f + 1] = kNegInf;
         }
   }
-  st.weigh(z);
+  uint2 p[2][2][NR];   // [own block / other][step]
+  at_weights<D, NR>(z, p[0], p[1], buf, c, pr, st);
+  after();
 
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    uint32_t p[NR][2];
+  for (int y = 0; y < 2; ++y) {
+    const int blk = pr.x ^ y;
+    const int have = left - blk * Q4_BLOCK;   // tokens of that block
+    if (have <= 0) continue;
+    const unsigned char* sb = tile + blk * q4_block_bytes(D);
+    uint32_t w[2][4], sc[2][4];
 #pragma unroll
-    for (int j = 0; j < NR; ++j)
+    for (int s = 0; s < 2; ++s)
 #pragma unroll
-      for (int f = 0; f < 2; ++f) p[j][f] = transpose8(f16x2_pack(z[s][j][2 * f], z[s][j][2 * f + 1]));
-    uint32_t vw[4][D / 64];   // tokens 2t, 2t+1 of the two groups of 8
-    uint32_t sc[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int tok = 16 * s + 8 * (k >> 1) + at_token(2 * t + (k & 1));
-      if constexpr (D == 128) {
-        const uint2 x = *reinterpret_cast<const uint2*>(sb + 16 * D + tok * 64 + g * 8);
-        vw[k][0] = x.x; vw[k][1] = x.y;
-        sc[k] = sb[34 * D + tok * 8 + g];
-      } else {
-        vw[k][0] = *reinterpret_cast<const uint32_t*>(sb + 16 * D + tok * 32 + g * 4);
-        sc[k] = sb[34 * D + tok * 4 + (g >> 1)];
+      for (int k = 0; k < 4; ++k) {
+        const int tok = 16 * s + 8 * (k >> 1) + at_token(2 * t + (k & 1));
+        if constexpr (D == 128) {
+          w[s][k] = *reinterpret_cast<const uint32_t*>(sb + 16 * D + tok * 64 + pr.x * 32 + g * 4);
+          sc[s][k] = sb[34 * D + tok * 8 + pr.x * 4 + (g >> 1)];
+        } else {
+          w[s][k] = *reinterpret_cast<const uint16_t*>(sb + 16 * D + tok * 32 + pr.x * 16 + g * 2);
+          sc[s][k] = sb[34 * D + tok * 4 + pr.x * 2 + (g >> 2)];
+        }
       }
-      if (tok >= left) sc[k] = 0u;   // what lies behind the last token may be a NaN
+    if (have < Q4_BLOCK) {   // what lies behind the last token may be a NaN
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (16 * s + 8 * (k >> 1) + at_token(2 * t + (k & 1)) >= have) sc[s][k] = 0u;
     }
-    const uint32_t s01 = e4m3x2_to_f16(sc[0] | (sc[1] << 8)), s23 = e4m3x2_to_f16(sc[2] | (sc[3] << 8));
+    const uint32_t a01 = e4m3x2_to_f16(sc[0][0] + sc[0][1] * 256u), a23 = e4m3x2_to_f16(sc[0][2] + sc[0][3] * 256u);
+    const uint32_t b01 = e4m3x2_to_f16(sc[1][0] + sc[1][1] * 256u), b23 = e4m3x2_to_f16(sc[1][2] + sc[1][3] * 256u);
+    if constexpr (D == 128) {
+      at_add_v<4, NR>(w[0], 0, a01, a23, p[y][0], st.o);
+      at_add_v<4, NR>(w[1], 0, b01, b23, p[y][1], st.o);
+    } else {
+      uint32_t both[4];   // the codes of both steps, widened at once
 #pragma unroll
-    for (int w = 0; w < D / 64; ++w) {
-      uint32_t e01[4], o01[4], e23[4], o23[4];
-      e2m1x8_to_f16((vw[0][w] & 0x0f0f0f0fu) | ((vw[1][w] << 4) & 0xf0f0f0f0u), e01);
-      e2m1x8_to_f16(((vw[0][w] >> 4) & 0x0f0f0f0fu) | (vw[1][w] & 0xf0f0f0f0u), o01);
-      e2m1x8_to_f16((vw[2][w] & 0x0f0f0f0fu) | ((vw[3][w] << 4) & 0xf0f0f0f0u), e23);
-      e2m1x8_to_f16(((vw[2][w] >> 4) & 0x0f0f0f0fu) | (vw[3][w] & 0xf0f0f0f0u), o23);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 v = make_uint4(f16x2_mul(e01[i], s01), f16x2_mul(o01[i], s01), f16x2_mul(e23[i], s23), f16x2_mul(o23[i], s23));
-#pragma unroll
-        for (int j = 0; j < NR; ++j) mma_f16(st.o[j][4 * w + i], v, p[j][0], p[j][1]);
-      }
+      for (int k = 0; k < 4; ++k) both[k] = w[0][k] + w[1][k] * 65536u;
+      at_add_v<2, NR>(both, 0, a01, a23, p[y][0], st.o);
+      at_add_v<2, NR>(both, 2, b01, b23, p[y][1], st.o);
     }
   }
 }
@@ -504,10 +641,12 @@ __device__ __forceinline__ bool bf16x2_unbounded(uint32_t w) {
   return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
 }
 
-// A block of fresh entries: nodes j0 .. j0 + 31.
+// A tile of fresh entries: nodes j0 .. j0 + 63.  Unlike in a cached tile, the
+// references follow the maxima.
 template <int D, int NR>
-__device__ __forceinline__ void at_fresh_block(const AttendArgs& a, int b, int h, int row0, int rows, int j0, AtState<D, NR>& st) {
-  constexpr int CH = D / 4, KS = D / 16, CV = D / 8;
+__device__ __forceinline__ void at_fresh_tile(const AttendArgs& a, int b, int h, int row0, int rows, int j0,
+                                              const AtPair<D, NR>& pr, AtState<D, NR>& st) {
+  constexpr int CH = D / 4, KS = D / 16, CV = D / 16;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int tr = at_token(g);
   const long long rstride = static_cast<long long>(a.Hkv) * D;
@@ -522,205 +661,284 @@ __device__ __forceinline__ void at_fresh_block(const AttendArgs& a, int b, int h
   long long qat[NR];
 #pragma unroll
   for (int j = 0; j < NR; ++j) qat[j] = row0 + 8 * j + g < rows ? at_row(a, b, h, row0 + 8 * j + g) * D + t * CH : -1;
-#pragma unroll 2
-  for (int ks = 0; ks < KS; ++ks) {
-    uint2 qb[NR];
+  const int jx = j0 + pr.x * Q4_BLOCK;   // the warp's nodes
+  if (jx < a.N) {
+#pragma unroll 4
+    for (int ks = 0; ks < KS; ++ks) {
+      uint2 qb[NR];
 #pragma unroll
-    for (int j = 0; j < NR; ++j)
-      qb[j] = qat[j] >= 0 ? __ldg(reinterpret_cast<const uint2*>(a.q + qat[j] + 4 * ks)) : make_uint2(0u, 0u);
+      for (int j = 0; j < NR; ++j)
+        qb[j] = qat[j] >= 0 ? __ldg(reinterpret_cast<const uint2*>(a.q + qat[j] + 4 * ks)) : make_uint2(0u, 0u);
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt) {
-      uint2 kx[2];
+      for (int mt = 0; mt < 2; ++mt) {
+        uint2 kx[2];
 #pragma unroll
-      for (int f = 0; f < 2; ++f) {
-        const int n = j0 + 16 * mt + 8 * f + tr;
-        kx[f] = n < a.N ? __ldg(reinterpret_cast<const uint2*>(a.k_new + base + n * rstride + t * CH + 4 * ks)) : make_uint2(0u, 0u);
+        for (int f = 0; f < 2; ++f) {
+          const int n = jx + 16 * mt + 8 * f + tr;
+          kx[f] = n < a.N ? __ldg(reinterpret_cast<const uint2*>(a.k_new + base + n * rstride + t * CH + 4 * ks)) : make_uint2(0u, 0u);
+        }
+        const uint4 k = make_uint4(kx[0].x, kx[1].x, kx[0].y, kx[1].y);
+#pragma unroll
+        for (int j = 0; j < NR; ++j) mma_bf16(z[mt][j], k, qb[j].x, qb[j].y);
       }
-      const uint4 k = make_uint4(kx[0].x, kx[1].x, kx[0].y, kx[1].y);
-#pragma unroll
-      for (int j = 0; j < NR; ++j) mma_bf16(z[mt][j], k, qb[j].x, qb[j].y);
     }
   }
-  uint32_t sees[NR][2];   // nodes of the block that the lane's rows attend to
+  uint32_t sees[NR][2][2];   // nodes of the tile that the lane's rows attend to
 #pragma unroll
   for (int j = 0; j < NR; ++j)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int n = (row0 + 8 * j + 2 * t + e) / a.G;
-      uint32_t see = 0u;
-      if (n < a.N) {
-        if (a.masks) see = __ldg(a.masks + (static_cast<long long>(b) * a.N + n) * a.NW + j0 / 32);
-        else see = n - j0 >= 31 ? ~0u : n < j0 ? 0u : (2u << (n - j0)) - 1u;
-        if (a.N - j0 < 32) see &= (1u << (a.N - j0)) - 1u;
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        const int at = j0 + y * Q4_BLOCK;
+        uint32_t see = 0u;
+        if (n < a.N && at < a.N) {
+          if (a.masks) see = __ldg(a.masks + (static_cast<long long>(b) * a.N + n) * a.NW + at / 32);
+          else see = n - at >= 31 ? ~0u : n < at ? 0u : (2u << (n - at)) - 1u;
+          if (a.N - at < 32) see &= (1u << (a.N - at)) - 1u;
+        }
+        sees[j][e][y] = see;
       }
-      sees[j][e] = see;
+      const uint32_t see = pr.x ? sees[j][e][1] : sees[j][e][0];
+      float m = kNegInf;
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
         for (int f = 0; f < 2; ++f) {
           float& x = z[mt][j][e + 2 * f];
           x = (see >> (16 * mt + 8 * f + tr)) & 1u ? x * a.scale_log2 : kNegInf;
+          m = fmaxf(m, x);
         }
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+      if (g == 0) pr.top(0, pr.x)[8 * j + 2 * t + e] = m;
     }
-  st.weigh(z);
-
+  pr.sync();
   // the sums of v are kept in units of 2^v_shift
   const float unit = __fdiv_rn(1.f, a.v_mul);
-  bool odd = false;   // this lane saw a NaN or an infinity
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
-    uint32_t hi[NR][2], lo[NR][2];
+  for (int j = 0; j < NR; ++j)
 #pragma unroll
-    for (int j = 0; j < NR; ++j)
-#pragma unroll
-      for (int f = 0; f < 2; ++f) {
-        const float x = z[s][j][2 * f] * unit, y = z[s][j][2 * f + 1] * unit;
-        const uint32_t ph = bf16x2_pack(x, y);
-        lo[j][f] = transpose8(bf16x2_pack(x - __uint_as_float(ph << 16), y - __uint_as_float(ph & 0xffff0000u)));
-        hi[j][f] = transpose8(ph);
-      }
-#pragma unroll
-    for (int w = 0; w < CV / 8; ++w) {   // eight columns of the chunk at a time
-      uint32_t vw[4][4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int n = j0 + 16 * s + 8 * (k >> 1) + at_token(2 * t + (k & 1));
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (n < a.N) x = __ldg(reinterpret_cast<const uint4*>(a.v_new + base + n * rstride + g * CV) + w);
-        const uint32_t y[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          vw[k][i] = y[i];
-          if (bf16x2_unbounded(y[i])) {
-            odd = true;
-            if ((y[i] & 0x7f80u) == 0x7f80u) vw[k][i] &= 0xffff0000u;
-            if ((y[i] & 0x7f800000u) == 0x7f800000u) vw[k][i] &= 0xffffu;
-          }
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint4 v = make_uint4(__byte_perm(vw[0][i], vw[1][i], 0x5410), __byte_perm(vw[0][i], vw[1][i], 0x7632),
-                                   __byte_perm(vw[2][i], vw[3][i], 0x5410), __byte_perm(vw[2][i], vw[3][i], 0x7632));
-#pragma unroll
-        for (int j = 0; j < NR; ++j) {
-          mma_bf16(st.o[j][4 * w + i], v, hi[j][0], hi[j][1]);
-          mma_bf16(st.o[j][4 * w + i], v, lo[j][0], lo[j][1]);
-        }
-      }
-    }
-  }
-  // A product takes 0 * inf for NaN, so such elements were left out above and
-  // reach only the rows that see their node (with a weight above zero, however
-  // small: a weight that underflowed counts as the smallest one).
-  if (__any_sync(0xffffffffu, odd)) {
-#pragma unroll 1
-    for (int x = 0; x < 8; ++x) {
+    for (int e = 0; e < 2; ++e) {
+      const int r = 8 * j + 2 * t + e;
+      st.raise(j, e, fmaxf(st.ref[j][e], fmaxf(pr.top(0, 0)[r], pr.top(0, 1)[r])));
+      const float ref = (st.ref[j][e] == kNegInf ? 0.f : st.ref[j][e]) - AT_PSHIFT;
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          const int n = 16 * mt + 8 * f + at_token(x);
+        for (int f = 0; f < 2; ++f) z[mt][j][e + 2 * f] = ex2_approx(z[mt][j][e + 2 * f] - ref);
+      st.l[j][e] += (z[0][j][e] + z[0][j][e + 2]) + (z[1][j][e] + z[1][j][e + 2]);
+    }
+  // weights as the sum of two bf16: buffer 0 the larger parts, buffer 1 the rest
 #pragma unroll
-          for (int j = 0; j < NR; ++j)
+  for (int s = 0; s < 2; ++s)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const float p = __shfl_sync(0xffffffffu, z[mt][j][e + 2 * f], 4 * x + t);
-              if (!((sees[j][e] >> n) & 1u)) continue;
+    for (int j = 0; j < NR; ++j) {
+      uint32_t hi[2], lo[2];
 #pragma unroll
-              for (int i = 0; i < D / 16; ++i)
+      for (int f = 0; f < 2; ++f) {
+        const float x = z[s][j][2 * f] * unit, y = z[s][j][2 * f + 1] * unit;
+        hi[f] = bf16x2_pack(x, y);
+        lo[f] = transpose8(bf16x2_pack(x - __uint_as_float(hi[f] << 16), y - __uint_as_float(hi[f] & 0xffff0000u)));
+        hi[f] = transpose8(hi[f]);
+      }
+      pr.p(0, pr.x)[(s * NR + j) * 32 + lane] = make_uint2(hi[0], hi[1]);
+      pr.p(1, pr.x)[(s * NR + j) * 32 + lane] = make_uint2(lo[0], lo[1]);
+    }
+  pr.sync();
+#pragma unroll 1
+  for (int y = 0; y < 4; ++y) {   // 16 nodes at a time
+    const int blk = y >> 1, s = y & 1, n0 = j0 + 16 * y;
+    if (n0 >= a.N) break;
+    uint2 hi[NR], lo[NR];
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                  const uint32_t v = a.v_new[base + (j0 + n) * rstride + g * CV + 2 * i + k];
-                  if ((v & 0x7f80u) == 0x7f80u) st.o[j][i][e + 2 * k] += (p == 0.f ? 1.17549435e-38f : p) * __uint_as_float(v << 16);
-                }
-            }
+    for (int j = 0; j < NR; ++j) {
+      hi[j] = pr.p(0, blk)[(s * NR + j) * 32 + lane];
+      lo[j] = pr.p(1, blk)[(s * NR + j) * 32 + lane];
+    }
+    bool odd = false;   // this lane saw a NaN or an infinity
+    uint32_t vw[4][CV / 2];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int n = n0 + 8 * (k >> 1) + at_token(2 * t + (k & 1));
+      const uint16_t* from = a.v_new + base + n * rstride + pr.x * (D / 2) + g * CV;
+      if constexpr (D == 128) {
+        const uint4 x = n < a.N ? __ldg(reinterpret_cast<const uint4*>(from)) : make_uint4(0u, 0u, 0u, 0u);
+        vw[k][0] = x.x; vw[k][1] = x.y; vw[k][2] = x.z; vw[k][3] = x.w;
+      } else {
+        const uint2 x = n < a.N ? __ldg(reinterpret_cast<const uint2*>(from)) : make_uint2(0u, 0u);
+        vw[k][0] = x.x; vw[k][1] = x.y;
+      }
+#pragma unroll
+      for (int i = 0; i < CV / 2; ++i)
+        if (bf16x2_unbounded(vw[k][i])) {
+          odd = true;
+          if ((vw[k][i] & 0x7f80u) == 0x7f80u) vw[k][i] &= 0xffff0000u;
+          if ((vw[k][i] & 0x7f800000u) == 0x7f800000u) vw[k][i] &= 0xffffu;
         }
     }
+#pragma unroll
+    for (int i = 0; i < CV / 2; ++i) {
+      const uint4 v = make_uint4(__byte_perm(vw[0][i], vw[1][i], 0x5410), __byte_perm(vw[0][i], vw[1][i], 0x7632),
+                                 __byte_perm(vw[2][i], vw[3][i], 0x5410), __byte_perm(vw[2][i], vw[3][i], 0x7632));
+#pragma unroll
+      for (int j = 0; j < NR; ++j) {
+        mma_bf16(st.o[j][i], v, hi[j].x, hi[j].y);
+        mma_bf16(st.o[j][i], v, lo[j].x, lo[j].y);
+      }
+    }
+    // A product takes 0 * inf for NaN, so such elements were left out above and
+    // reach only the rows that see their node (with a weight above zero, however
+    // small: a weight that underflowed counts as the smallest one).
+    if (__any_sync(0xffffffffu, odd)) {
+#pragma unroll 1
+      for (int k = 0; k < 16; ++k) {
+        const int n = n0 + (k & 8) + at_token(k & 7);
+#pragma unroll
+        for (int j = 0; j < NR; ++j)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            // row 2 t + e of the operand is in lanes of that row, column k in their lane (k & 7) / 2
+            const uint32_t w = __shfl_sync(0xffffffffu, k & 8 ? hi[j].y : hi[j].x, 4 * (2 * t + e) + ((k & 7) >> 1));
+            const float p = __uint_as_float(k & 1 ? w & 0xffff0000u : w << 16);
+            const uint32_t see = blk ? sees[j][e][1] : sees[j][e][0];
+            if (n >= a.N || !((see >> (n - j0 - blk * Q4_BLOCK)) & 1u)) continue;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+              for (int f = 0; f < 2; ++f) {
+                const uint32_t v = a.v_new[base + n * rstride + pr.x * (D / 2) + g * CV + 2 * i + f];
+                if ((v & 0x7f80u) == 0x7f80u) st.o[j][i][e + 2 * f] += (p == 0.f ? 1.17549435e-38f : p) * __uint_as_float(v << 16);
+              }
+          }
+      }
+    }
   }
+  pr.sync();   // the exchange area is free again
 }
 
-// The state after fresh blocks first .. last - 1 of a triple, saved at `p`.  A
-// function of its own: these blocks are few, and their registers would push the
-// cached blocks' loop into local memory.
+// The state after fresh tiles first .. last - 1 of a triple, saved at `p`.  A
+// function of its own: these tiles are few, and their registers would push the
+// cached tiles' loop into local memory.
 template <int D, int NR>
-__device__ __noinline__ void at_fresh(const AttendArgs& a, int b, int h, int row0, int rows, int first, int last, float* p) {
+__device__ __noinline__ void at_fresh(const AttendArgs& a, int b, int h, int row0, int rows, int first, int last,
+                                      AtPair<D, NR> pr, float* p) {
   AtState<D, NR> st;
   st.clear();
-  for (int i = first; i < last; ++i) at_fresh_block<D, NR>(a, b, h, row0, rows, i * Q4_BLOCK, st);
+  for (int i = first; i < last; ++i) at_fresh_tile<D, NR>(a, b, h, row0, rows, i * AT_TILE, pr, st);
   st.save(p);
 }
 
-__device__ __forceinline__ float at_lse(float m, float l) {
-  // m in the log2 domain, l relative to 2^(m - 15)
-  return l == 0.f ? kNegInf : (m - AT_PSHIFT + log2f(l)) * 0.69314718055994530942f;
+__device__ __forceinline__ float at_lse(float ref, float l) {
+  // ref in the log2 domain, l relative to 2^(ref - 7)
+  return l == 0.f ? kNegInf : (ref - AT_PSHIFT + log2f(l)) * 0.69314718055994530942f;
 }
 
 // CTAs an SM: what the registers of a row tile leave room for
-__host__ __device__ constexpr int at_ctas(int NR) { return NR == 1 ? 4 : NR == 4 ? 2 : 3; }
+__host__ __device__ constexpr int at_ctas(int NR) { return NR <= 2 ? 4 : 3; }
 
-// this lane's rows of a finished state
+// the warp's part of a row's sum of weights
+__device__ __forceinline__ float at_sum(float l) {
+  l += __shfl_xor_sync(0xffffffffu, l, 4);
+  l += __shfl_xor_sync(0xffffffffu, l, 8);
+  l += __shfl_xor_sync(0xffffffffu, l, 16);
+  return l;
+}
+// the lane's rows and columns of a finished state (both warps of the pair call this)
 template <int D, int NR>
-__device__ __forceinline__ void at_write(const AttendArgs& a, int b, int h, int row0, int rows, const AtState<D, NR>& st) {
+__device__ __forceinline__ void at_write(const AttendArgs& a, int b, int h, int row0, int rows, const AtPair<D, NR>& pr,
+                                         const AtState<D, NR>& st) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  float l[NR][2];
 #pragma unroll
   for (int j = 0; j < NR; ++j)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      float l = st.l[j][e];
-      l += __shfl_xor_sync(0xffffffffu, l, 4);
-      l += __shfl_xor_sync(0xffffffffu, l, 8);
-      l += __shfl_xor_sync(0xffffffffu, l, 16);
+      l[j][e] = at_sum(st.l[j][e]);
+      if (g == 0) pr.top(0, pr.x)[8 * j + 2 * t + e] = l[j][e];
+    }
+  pr.sync();
+#pragma unroll
+  for (int j = 0; j < NR; ++j)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
       const int r = row0 + 8 * j + 2 * t + e;
       if (r >= rows) continue;
+      const float sum = pr.top(0, 0)[8 * j + 2 * t + e] + pr.top(0, 1)[8 * j + 2 * t + e];
       const long long at = at_row(a, b, h, r);
-      const float inv = l == 0.f ? 0.f : a.v_mul / l;
-      uint4* p = reinterpret_cast<uint4*>(a.out + at * D + g * (D / 8));
+      const float inv = sum == 0.f ? 0.f : a.v_mul / sum;
+      uint32_t w[D / 32];
 #pragma unroll
-      for (int i = 0; i < D / 16; i += 4)
-        p[i / 4] = make_uint4(bf16x2_pack(st.o[j][i][e] * inv, st.o[j][i][e + 2] * inv),
-                              bf16x2_pack(st.o[j][i + 1][e] * inv, st.o[j][i + 1][e + 2] * inv),
-                              bf16x2_pack(st.o[j][i + 2][e] * inv, st.o[j][i + 2][e + 2] * inv),
-                              bf16x2_pack(st.o[j][i + 3][e] * inv, st.o[j][i + 3][e + 2] * inv));
-      if (a.lse && g == 0) a.lse[at] = at_lse(st.m[j][e], l);
+      for (int i = 0; i < D / 32; ++i) w[i] = bf16x2_pack(st.o[j][i][e] * inv, st.o[j][i][e + 2] * inv);
+      uint16_t* to = a.out + at * D + pr.x * (D / 2) + g * (D / 16);
+      if constexpr (D == 128) *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+      else *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+      if (a.lse && pr.x == 0 && g == 0) a.lse[at] = at_lse(st.ref[j][e], sum);
     }
+  pr.sync();   // the exchange area is free again
 }
 // the same as a partial
 template <int D, int NR>
-__device__ __forceinline__ void at_write_partial(float* part, const AtState<D, NR>& st) {
+__device__ __forceinline__ void at_write_partial(float* part, const AtPair<D, NR>& pr, const AtState<D, NR>& st) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int j = 0; j < NR; ++j)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      float l = st.l[j][e];
-      l += __shfl_xor_sync(0xffffffffu, l, 4);
-      l += __shfl_xor_sync(0xffffffffu, l, 8);
-      l += __shfl_xor_sync(0xffffffffu, l, 16);
+      const float l = at_sum(st.l[j][e]);
       const int lr = 8 * j + 2 * t + e;
-      float4* p = reinterpret_cast<float4*>(part + static_cast<size_t>(lr) * D + g * (D / 8));
+      float* to = part + static_cast<size_t>(lr) * D + pr.x * (D / 2) + g * (D / 16);
 #pragma unroll
-      for (int i = 0; i < D / 16; i += 2)
-        p[i / 2] = make_float4(st.o[j][i][e], st.o[j][i][e + 2], st.o[j][i + 1][e], st.o[j][i + 1][e + 2]);
+      for (int i = 0; i < D / 32; i += 2)
+        *reinterpret_cast<float4*>(to + 2 * i) = make_float4(st.o[j][i][e], st.o[j][i][e + 2], st.o[j][i + 1][e], st.o[j][i + 1][e + 2]);
       if (g == 0) {
-        part[8 * NR * D + lr] = st.m[j][e];
-        part[8 * NR * D + 8 * NR + lr] = l;
+        if (pr.x == 0) part[8 * NR * D + lr] = st.ref[j][e];
+        part[8 * NR * D + 8 * NR * (1 + pr.x) + lr] = l;
       }
     }
+}
+
+// A place of a pair's list of fetches: the blocks of a cached tile in the cache,
+// the second AT_NONE where it lies behind the sequence's last token; AT_NONE for
+// a unit without a cached tile, AT_BAD for a page id out of range.
+constexpr uint32_t AT_NONE = 0xffffffffu, AT_BAD = 0xfffffffeu;
+__device__ __forceinline__ uint2 at_source(const AttendArgs& a, const long long* prefix, int HR, int nfresh, long long u) {
+  AtCursor c;
+  at_seek(a, prefix, HR, u, c);
+  uint2 r = make_uint2(AT_NONE, AT_NONE);
+  const int blk = 2 * (c.i - AT_FRESH * nfresh), bpp = a.P / Q4_BLOCK;
+  if (!at_len_ok(a, c.len) || blk < 0 || blk * Q4_BLOCK >= c.len) return r;
+  const int head = c.pair / a.row_tiles;
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int x = blk + k;
+    if (x * Q4_BLOCK >= c.len) break;
+    const int page = __ldg(a.table + static_cast<long long>(c.b) * a.W + x / bpp);
+    const uint32_t at = page >= 0 && page < a.pages ? (static_cast<uint32_t>(page) * a.Hkv + head) * bpp + x % bpp : AT_BAD;
+    if (at == AT_BAD) r.x = AT_BAD;
+    else if (k == 0) r.x = at;
+    else r.y = at;
+  }
+  return r;
 }
 
 template <int D, int NR>
 __global__ void __launch_bounds__(AT_THREADS, at_ctas(NR)) attend_q4_kernel(const __grid_constant__ AttendArgs a, int stages) {
   extern __shared__ __align__(128) unsigned char at_smem[];
-  __shared__ long long scratch[AT_WARPS];
-  constexpr int SB = at_stage_bytes(D), QB = at_q_bytes(D, NR);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  unsigned char* ring = at_smem + static_cast<size_t>(warp) * stages * SB;
-  uint4* qf = reinterpret_cast<uint4*>(at_smem + static_cast<size_t>(AT_WARPS) * stages * SB + warp * QB);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(at_smem + static_cast<size_t>(AT_WARPS) * (stages * SB + QB)) + warp * stages;
-  long long* prefix = reinterpret_cast<long long*>(at_smem + static_cast<size_t>(AT_WARPS) * (stages * SB + QB)) + AT_WARPS * stages;
+  __shared__ long long scratch[AT_THREADS / 32];
+  constexpr int SB = at_stage_bytes(D), BB = q4_block_bytes(D);
+  const int pair = threadIdx.x >> 6;
+  unsigned char* ring = at_smem + static_cast<size_t>(pair) * stages * SB;
+  AtPair<D, NR> pr;
+  pr.base = at_smem + static_cast<size_t>(AT_PAIRS) * stages * SB + pair * at_pair_bytes(D, NR);
+  pr.x = (threadIdx.x >> 5) & 1;
+  pr.id = 1 + pair;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(at_smem + static_cast<size_t>(AT_PAIRS) * (stages * SB + at_pair_bytes(D, NR))) + pair * stages;
+  long long* prefix = reinterpret_cast<long long*>(at_smem + static_cast<size_t>(AT_PAIRS) * (stages * SB + at_pair_bytes(D, NR))) + AT_PAIRS * stages;
 
-  if (lane == 0) {
+  if ((threadIdx.x & 63) == 0) {
     for (int s = 0; s < stages; ++s) mbar_init(&bars[s], 1);
     mbar_fence_init();
   }
@@ -730,79 +948,62 @@ __global__ void __launch_bounds__(AT_THREADS, at_ctas(NR)) attend_q4_kernel(cons
   const long long units = prefix[a.B] * HR;
   const int ctas = at_active(units, gridDim.x);
   if (blockIdx.x >= ctas) return;
-  const int shares = ctas * AT_WARPS, share = blockIdx.x * AT_WARPS + warp;
+  const int shares = ctas * AT_PAIRS, share = blockIdx.x * AT_PAIRS + pair;
   const long long u0 = at_start(units, shares, share), u1 = at_start(units, shares, share + 1);
   float* cta_ws = a.ws + static_cast<size_t>(blockIdx.x) * at_cta_floats(D, NR);
-  float* states = cta_ws + 2 * at_partial_floats(D, NR);
-  float* mine = states + warp * at_state_floats(D, NR);
-  float* fresh_at = states + (AT_WARPS + warp) * at_state_floats(D, NR);
+  float* states = cta_ws + 2 * at_partial_floats(D, NR);   // [pair][x], then the fresh ones
 
-  const int rows = a.N * a.G, bpp = a.P / Q4_BLOCK;
-  const int nfresh = a.k_new ? (a.N + Q4_BLOCK - 1) / Q4_BLOCK : 0;
+  const int rows = a.N * a.G;
+  const int nfresh = a.k_new ? (a.N + AT_TILE - 1) / AT_TILE : 0;
   AtState<D, NR> st;
-  AtCursor pre, cur;
-  uint32_t phase = 0u, have = 0u;        // a bit per stage
-  int stage = 0;
-  bool failed = false;
+  AtCursor cur;
   // the piece in registers at the end
   int first = 0, last = 0, h = 0, row0 = 0;
   long long upiece = u0;
 
   if (u0 < u1) {
-    // The cursor of what is fetched runs ahead of what is worked on.  The page
-    // id of a fetch was loaded one fetch earlier, so that nothing waits for it.
-    at_seek(a, prefix, HR, u0, pre);
-    cur = pre;
-    int left = static_cast<int>(u1 - u0);            // blocks that the cursor has still to pass
-    int pblk = 0, phead = 0, page = -1;
-    const int32_t* prow = nullptr;
-    auto enter = [&] {                               // the cursor moved into a triple: past its fresh blocks
-      if (!at_len_ok(a, pre.len)) return;
-      if (pre.i < nfresh) {
-        const int skip = min(nfresh - pre.i, left);
-        pre.i += skip;
-        left -= skip;
-      }
-      if (left <= 0 || pre.i >= pre.units) return;
-      const int c = pre.i - nfresh;
-      prow = a.table + static_cast<long long>(pre.b) * a.W + c / bpp;
-      pblk = c % bpp;
-      phead = pre.pair / a.row_tiles;
-      if (c * Q4_BLOCK < pre.len) page = __ldg(prow);
-    };
-    enter();
-    auto fetch = [&](int s) {                        // the next cached block of the share into stage s
-      have &= ~(1u << s);
-      // triples without a block to fetch are passed over
-      while (left > 0 && (pre.i >= pre.units || !at_len_ok(a, pre.len) || (pre.i - nfresh) * Q4_BLOCK >= pre.len)) {
-        if (pre.i < pre.units) {                     // its one empty block
-          pre.i = pre.units;
-          --left;
-          continue;
+    at_seek(a, prefix, HR, u0, cur);
+    // The first warp of a pair fetches for both.  A list of the next 32 units'
+    // blocks, a unit a lane, keeps the way from a unit to its place in the cache
+    // out of the loop over the tiles.
+    long long next = u0;                   // unit of the next fetch
+    uint32_t phase = 0u;                   // a bit per stage
+    bool failed = false;
+    auto fetch = [&](int s) {              // the next cached tile of the share into stage s
+      uint2 e = make_uint2(AT_NONE, AT_NONE);
+      while (next < u1 && e.x == AT_NONE) {
+        const int at = static_cast<int>(next - u0) % AT_QUEUE;
+        if (at == 0) {
+          __syncwarp();
+          if (next + (threadIdx.x & 31) < u1) pr.queue()[threadIdx.x & 31] = at_source(a, prefix, HR, nfresh, next + (threadIdx.x & 31));
+          __syncwarp();
         }
-        pre.i = pre.units - 1;
-        at_next(a, prefix, HR, pre);
-        enter();
+        e = pr.queue()[at];
+        ++next;
       }
-      if (left <= 0) return;
-      --left;
-      if (page >= 0 && page < a.pages) {
-        have |= 1u << s;
-        if (lane == 0) {
-          const unsigned long long blk = (static_cast<unsigned long long>(page) * a.Hkv + phead) * bpp + pblk;
-          mbar_arrive_expect_tx(&bars[s], SB);
-          bulk_g2s(ring + s * SB, a.cache + blk * SB, SB, &bars[s]);
-        }
-      }
-      ++pre.i;
-      if (++pblk == bpp) {
-        pblk = 0;
-        ++prow;
-        if (pre.i < pre.units) page = __ldg(prow);
+      if (e.x == AT_NONE || (threadIdx.x & 31) != 0 || failed) return;
+      *pr.arrived(s) = e.x != AT_BAD;
+      if (e.x == AT_BAD) {
+        mbar_arrive(&bars[s]);
+      } else if (e.y == e.x + 1) {         // neighbours in one page
+        mbar_arrive_expect_tx(&bars[s], 2 * BB);
+        bulk_g2s(ring + s * SB, a.cache + static_cast<unsigned long long>(e.x) * BB, 2 * BB, &bars[s]);
+      } else {
+        mbar_arrive_expect_tx(&bars[s], e.y == AT_NONE ? BB : 2 * BB);
+        bulk_g2s(ring + s * SB, a.cache + static_cast<unsigned long long>(e.x) * BB, BB, &bars[s]);
+        if (e.y != AT_NONE) bulk_g2s(ring + s * SB + BB, a.cache + static_cast<unsigned long long>(e.y) * BB, BB, &bars[s]);
       }
     };
-    for (int s = 0; s < stages; ++s) fetch(s);
+    if (pr.x == 0)
+      for (int s = 0; s < stages; ++s) fetch(s);
 
+    // A stage is free once both warps have passed the barrier of the next tile,
+    // and is filled again from there: all stages but one are on their way.
+    int stage = 0, buf = 0, done = -1;
+    auto refill = [&] {
+      if (done >= 0 && pr.x == 0) fetch(done);
+      done = -1;
+    };
     for (long long u = u0;;) {
       // one triple, or the part of it that lies in the share
       h = cur.pair / a.row_tiles;
@@ -811,97 +1012,73 @@ __global__ void __launch_bounds__(AT_THREADS, at_ctas(NR)) attend_q4_kernel(cons
       last = static_cast<int>(min(static_cast<long long>(cur.units), first + (u1 - u)));
       upiece = u;
       bool poison = !at_len_ok(a, cur.len);
-      const int nf = poison ? 0 : nfresh, ncached = poison ? 0 : (cur.len + Q4_BLOCK - 1) / Q4_BLOCK;
-      if (first < nf) {
-        at_fresh<D, NR>(a, cur.b, h, row0, rows, first, min(last, nf), fresh_at);
-        st.load(fresh_at);
+      const int nf = poison ? 0 : AT_FRESH * nfresh, ncached = poison ? 0 : (cur.len + AT_TILE - 1) / AT_TILE;
+      // (a fresh tile is worked on by the share that has its first unit)
+      const int f0 = (first + AT_FRESH - 1) / AT_FRESH, f1 = (min(last, nf) + AT_FRESH - 1) / AT_FRESH;
+      if (f0 < f1) {
+        float* at = states + (2 * AT_PAIRS + (threadIdx.x >> 5)) * at_state_floats(D, NR);
+        at_fresh<D, NR>(a, cur.b, h, row0, rows, f0, f1, pr, at);
+        st.load(at);
       } else {
         st.clear();
       }
       const int c1 = min(last - nf, ncached);
       int c = max(first - nf, 0);
-      if (c < c1) at_load_q<D, NR>(a, cur.b, h, row0, rows, qf, st);
+      float factor[NR][2];
+      if (c < c1) {
+        at_load_q<D, NR>(a, cur.b, h, row0, rows, pr, factor);
+        refill();
+      }
       for (; c < c1; ++c) {
-        if (have & (1u << stage)) {
-          if (!mbar_wait(&bars[stage], (phase >> stage) & 1u, a.timeout_ns)) {
-            failed = true;
-            break;   // no copy is started after one that did not arrive
-          }
-          phase ^= 1u << stage;
-          at_cached_block<D, NR>(ring + stage * SB, min(cur.len - c * Q4_BLOCK, Q4_BLOCK), qf, st);
-        } else {
-          poison = true;
+        // (a warp whose wait gave up goes on in step with the other one, over what
+        // the stage holds, and its result is void)
+        if (!failed && !mbar_wait(&bars[stage], (phase >> stage) & 1u, a.timeout_ns)) {
+          failed = true;   // no more copies are started; those on their way have had their time
         }
-        __syncwarp();
-        fetch(stage);
+        phase ^= 1u << stage;
+        poison |= !*pr.arrived(stage);
+        at_cached_tile<D, NR>(ring + stage * SB, min(cur.len - c * AT_TILE, AT_TILE), buf, factor, pr, st, refill);
+        buf ^= 1;
+        done = stage;
         stage = stage + 1 == stages ? 0 : stage + 1;
       }
-      if (failed) break;
-      if (poison) {
-#pragma unroll
-        for (int j = 0; j < NR; ++j) st.l[j][0] = st.l[j][1] = __int_as_float(0x7fc00000);
-      }
+      if (poison || failed) st.poison();
       u += last - first;
-      if (first == 0 && last == cur.units) at_write<D, NR>(a, cur.b, h, row0, rows, st);
-      else if (first != 0) st.save(mine);
+      if (first == 0 && last == cur.units) at_write<D, NR>(a, cur.b, h, row0, rows, pr, st);
+      else if (first != 0) st.save(states + (threadIdx.x >> 5) * at_state_floats(D, NR));
       if (u >= u1) break;
       cur.i = last - 1;
       at_next(a, prefix, HR, cur);
     }
-    if (failed) {
-      // copies still on their way land before the warp goes on (or the wait gives up)
-      for (int s = 0; s < stages; ++s)
-        if (s != stage && (have & (1u << s))) mbar_wait(&bars[s], (phase >> s) & 1u, a.timeout_ns);
-      // every triple of the share from here on is void
-      bool again = true;
-      for (long long u = upiece; again;) {
-        st.clear();
-#pragma unroll
-        for (int j = 0; j < NR; ++j) st.l[j][0] = st.l[j][1] = __int_as_float(0x7fc00000);
-        h = cur.pair / a.row_tiles;
-        row0 = (cur.pair - h * a.row_tiles) * 8 * NR;
-        first = cur.i;
-        last = static_cast<int>(min(static_cast<long long>(cur.units), first + (u1 - u)));
-        upiece = u;
-        u += last - first;
-        if (first == 0 && last == cur.units) at_write<D, NR>(a, cur.b, h, row0, rows, st);
-        else if (first != 0) st.save(mine);
-        again = u < u1;
-        if (again) {
-          cur.i = last - 1;
-          at_next(a, prefix, HR, cur);
-        }
-      }
-    }
   }
   __syncthreads();
 
-  // Joins within the CTA.  A triple that begins in a warp's share and goes on is
-  // joined by that warp, whose registers hold its first part; the other parts
+  // Joins within the CTA.  A triple that begins in a pair's share and goes on is
+  // joined by that pair, whose registers hold its first part; the other parts
   // were saved.
   if (u0 < u1 && first == 0 && last != cur.units) {
     const long long tri_end = upiece + cur.units;
-    for (int w = warp + 1; w < AT_WARPS; ++w) {
-      const long long s0 = at_start(units, shares, share + w - warp), s1 = at_start(units, shares, share + w - warp + 1);
+    for (int w = pair + 1; w < AT_PAIRS; ++w) {
+      const long long s0 = at_start(units, shares, share + w - pair), s1 = at_start(units, shares, share + w - pair + 1);
       if (s0 >= tri_end) break;
-      if (s0 < s1) st.join(states + w * at_state_floats(D, NR));
+      if (s0 < s1) st.join(states + (2 * w + pr.x) * at_state_floats(D, NR));
     }
-    if (tri_end <= at_start(units, shares, (blockIdx.x + 1) * AT_WARPS)) at_write<D, NR>(a, cur.b, h, row0, rows, st);
-    else at_write_partial<D, NR>(cta_ws + at_partial_floats(D, NR), st);
+    if (tri_end <= at_start(units, shares, (blockIdx.x + 1) * AT_PAIRS)) at_write<D, NR>(a, cur.b, h, row0, rows, pr, st);
+    else at_write_partial<D, NR>(cta_ws + at_partial_floats(D, NR), pr, st);
   }
-  // A triple that came from the CTA before is joined by warp 0.
-  if (warp == 0) {
+  // A triple that came from the CTA before is joined by the first pair.
+  if (pair == 0) {
     AtCursor c;
     at_seek(a, prefix, HR, u0, c);
     if (c.i != 0) {
       const long long tri_end = u0 + (c.units - c.i);
       st.clear();
-      for (int w = 0; w < AT_WARPS; ++w) {
+      for (int w = 0; w < AT_PAIRS; ++w) {
         const long long s0 = at_start(units, shares, share + w), s1 = at_start(units, shares, share + w + 1);
         if (s0 >= tri_end) break;
-        if (s0 < s1) st.join(states + w * at_state_floats(D, NR));
+        if (s0 < s1) st.join(states + (2 * w + pr.x) * at_state_floats(D, NR));
       }
-      at_write_partial<D, NR>(cta_ws, st);
+      at_write_partial<D, NR>(cta_ws, pr, st);
     }
   }
 }
@@ -945,7 +1122,7 @@ __global__ void __launch_bounds__(ATJ_THREADS) attend_q4_join_kernel(const __gri
 #pragma unroll
       for (int r = 0; r < 8; ++r) {
         pm[r] = part[8 * NR * D + 8 * j + r];
-        pl[r] = part[8 * NR * D + 8 * NR + 8 * j + r];
+        pl[r] = part[8 * NR * D + 8 * NR + 8 * j + r] + part[8 * NR * D + 16 * NR + 8 * j + r];
 #pragma unroll
         for (int i = 0; i < C; ++i) po[r][i] = part[(8 * j + r) * D + i * 32 + lane];
       }

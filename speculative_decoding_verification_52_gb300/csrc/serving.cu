@@ -52,12 +52,16 @@ constexpr int kMaxSms = 160;   // bound of the workspace size; the grid never ex
 template <int D, int NR>
 spec_status_t launch_attend(const DevInfo& di, int dev, const AttendArgs& a, cudaStream_t st) {
   auto kern = attend_q4_kernel<D, NR>;
-  constexpr int ctas = at_ctas(NR);
-  const size_t fixed = static_cast<size_t>(AT_WARPS) * at_q_bytes(D, NR) + 8 * (static_cast<size_t>(a.B) + 1);
-  const size_t stage = static_cast<size_t>(AT_WARPS) * (at_stage_bytes(D) + 8);
-  // as many stages (at most 6) as leave room for all CTAs; 1 KB a CTA is the system's
-  const size_t room = kSmemPerSm / ctas - 1024;
-  const int stages = static_cast<int>(std::min<size_t>(6, std::max<size_t>(2, room > fixed ? (room - fixed) / stage : 0)));
+  const size_t fixed = static_cast<size_t>(AT_PAIRS) * at_pair_bytes(D, NR) + 8 * (static_cast<size_t>(a.B) + 1);
+  const size_t stage = static_cast<size_t>(AT_PAIRS) * (at_stage_bytes(D) + 8);
+  // As many CTAs an SM as the registers allow, with as many stages (2 to 6) as
+  // leave room for them; fewer CTAs where two stages do not.  (1.25 KB a CTA: the
+  // system's and the static part.)
+  int ctas = at_ctas(NR);
+  auto room = [&](int n) { return static_cast<long long>(kSmemPerSm / n) - 1280 - static_cast<long long>(fixed); };
+  while (ctas > 1 && room(ctas) < static_cast<long long>(2 * stage)) --ctas;
+  const int stages = static_cast<int>(std::min<long long>(6, room(ctas) / static_cast<long long>(stage)));
+  if (stages < 2) return fail(SPEC_ERR_UNSUPPORTED, "batch too large for one call");
   const size_t smem = fixed + stages * stage;
   if (!once_per_device(dev, [&] {
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerSm - 1024) == cudaSuccess;

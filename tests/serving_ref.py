@@ -110,7 +110,7 @@ def attend(q, cache, table, lengths, k_new, v_new, see, scale, k_shift, v_shift)
                         lse[b, n, i] = m + math.log(p.sum()) if np.isfinite(p.sum()) else np.nan
                         absv[b, n, i] = p @ np.abs(v) / p.sum()
                         av = np.where(np.isfinite(v), np.abs(v), 0.0)
-                        lost[b, n, i] = 2.0 ** -40 * av[: len(kc)].sum(0) + 2.0 ** -125 * av[len(kc):].sum(0)
+                        lost[b, n, i] = 2.0 ** -32 * av[: len(kc)].sum(0) + 2.0 ** -125 * av[len(kc):].sum(0)
                         absz[b, n, i] = abs(scale) * (np.abs(k) @ np.abs(q[b, n, i])).max()
     return out, lse, absv, absz, lost
 

@@ -10,12 +10,13 @@ sum of D products in fp32, off by at most D * 2^-23 * scale * sum |q k| =: dz
 the log2 domain, which changes a weight by that share, in numerator and sum:
 2 * dz * A; ex2 and the sums add a few 2^-22, taken as 2^-18 * A.  So
   |d out| <= 2^-8 |out| + (2^-11 + 2 dz + 2^-18) A + U,   |d lse| <= 2 dz + 2^-20 (1 + |lse|).
-U is underflow, which relative terms do not cover: weights are kept times 2^15.
-Those of cached tokens are f16, whose smallest step is 2^-24: each is off by up to
-half of it, 2^-25 of 2^15, so by 2^-40 of the largest weight.  Those of fresh
-entries are pairs of bf16 made from fp32, and factors between maxima are fp32: what
-is below 2^-126 becomes 0 or 2^-126, which is off by 2^-125 at most.  Hence
-U = 2^-40 * sum |v| over the cached tokens + 2^-125 * sum |v| over the fresh ones.
+U is underflow, which relative terms do not cover.  Weights of cached tokens are
+f16, 2^(z - ref + 7) with a reference that is at most the largest score: f16's
+smallest step is 2^-24, a weight is off by up to half of it, 2^-25, and the sum of
+weights is at least 2^7, so the share is off by 2^-32 at most.  Those of fresh
+entries are pairs of bf16 made from fp32, and factors between references are fp32:
+what is below 2^-126 becomes 0 or 2^-126, which is off by 2^-125 at most.  Hence
+U = 2^-32 * sum |v| over the cached tokens + 2^-125 * sum |v| over the fresh ones.
 Logit adjustments: at most 6 fp32 roundings of intermediate sums, each 2^-24 of
 the magnitudes that went in, and the output's half step."""
 import numpy as np
