@@ -78,6 +78,7 @@ struct AttendArgs {
   const int32_t* lengths;    // [B]
   int B, N, G, Hkv, P, pages, W, NW;
   int row_tiles;             // row tiles of a (sequence, head)
+  int tile, fresh;           // tokens of a tile; what a tile of fresh entries counts in the list
   float scale_log2;          // scale * log2(e)
   float k_mul, v_mul;        // 2^shift
   uint16_t* out;             // [B, N, Hkv * G, D] bf16
@@ -96,7 +97,7 @@ __device__ __forceinline__ bool at_len_ok(const AttendArgs& a, int len) {
 }
 __device__ __forceinline__ int at_units(const AttendArgs& a, int len) {
   if (!at_len_ok(a, len)) return 1;
-  const int n = (len + AT_TILE - 1) / AT_TILE + (a.k_new ? AT_FRESH * ((a.N + AT_TILE - 1) / AT_TILE) : 0);
+  const int n = (len + a.tile - 1) / a.tile + (a.k_new ? a.fresh * ((a.N + a.tile - 1) / a.tile) : 0);
   return n > 0 ? n : 1;
 }
 
@@ -158,9 +159,9 @@ __device__ __forceinline__ void at_next(const AttendArgs& a, const long long* pr
   c.units = static_cast<int>(prefix[c.b + 1] - prefix[c.b]);
 }
 
-// CTAs that get work: the list is cut in AT_PAIRS shares a CTA, none of the CTAs empty
-__device__ __forceinline__ int at_active(long long units, int ctas) {
-  return static_cast<int>(min((units + AT_PAIRS - 1) / AT_PAIRS, static_cast<long long>(ctas)));
+// CTAs that get work: the list is cut in `shares` parts a CTA, none of the CTAs empty
+__device__ __forceinline__ int at_active(long long units, int ctas, int shares) {
+  return static_cast<int>(min((units + shares - 1) / shares, static_cast<long long>(ctas)));
 }
 // share w of n of a list of `units`: [at_start(w), at_start(w + 1)), and the share that unit u falls in
 __device__ __forceinline__ long long at_start(long long units, int n, long long w) { return units * w / n; }
@@ -946,7 +947,7 @@ __global__ void __launch_bounds__(AT_THREADS, at_ctas(NR)) attend_q4_kernel(cons
 
   const int HR = a.Hkv * a.row_tiles;
   const long long units = prefix[a.B] * HR;
-  const int ctas = at_active(units, gridDim.x);
+  const int ctas = at_active(units, gridDim.x, AT_PAIRS);
   if (blockIdx.x >= ctas) return;
   const int shares = ctas * AT_PAIRS, share = blockIdx.x * AT_PAIRS + pair;
   const long long u0 = at_start(units, shares, share), u1 = at_start(units, shares, share + 1);
@@ -1086,9 +1087,12 @@ __global__ void __launch_bounds__(AT_THREADS, at_ctas(NR)) attend_q4_kernel(cons
 // Joins the partials of triples that several CTAs worked on: a warp takes eight
 // rows of a triple (a lane D / 32 columns).  Where a triple is spread over many
 // CTAs, a CTA's warps take its partials in turn and their results are joined.
+// R8: rows of a tile, in units of 8; a CTA's two partials are at the start of its
+// part of the workspace, `stride` floats apart from the next CTA's.
 constexpr int ATJ_WARPS = 8, ATJ_THREADS = 32 * ATJ_WARPS;
-template <int D, int NR, bool SPREAD>
-__global__ void __launch_bounds__(ATJ_THREADS) attend_q4_join_kernel(const __grid_constant__ AttendArgs a, int grid) {
+template <int D, bool SPREAD>
+__global__ void __launch_bounds__(ATJ_THREADS) attend_q4_join_kernel(const __grid_constant__ AttendArgs a, int grid, int shares,
+                                                                     int R8, size_t stride) {
   extern __shared__ __align__(128) unsigned char at_smem[];
   __shared__ long long scratch[ATJ_WARPS];
   constexpr int C = D / 32, PL = SPREAD ? ATJ_WARPS : 1;
@@ -1098,15 +1102,16 @@ __global__ void __launch_bounds__(ATJ_THREADS) attend_q4_join_kernel(const __gri
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int HR = a.Hkv * a.row_tiles, rows = a.N * a.G;
   const long long units = prefix[a.B] * HR;
-  const int ctas = at_active(units, grid);
-  const int items = a.B * HR * NR;
+  const int ctas = at_active(units, grid, shares);
+  const size_t partial = static_cast<size_t>(8 * R8) * (D + 4);
+  const int items = a.B * HR * R8;
   const int step = gridDim.x * (SPREAD ? 1 : ATJ_WARPS);
   for (int x = SPREAD ? blockIdx.x : blockIdx.x * ATJ_WARPS + warp; x < items; x += step) {
-    const int y = x / NR, j = x - y * NR, b = y / HR, pair = y - b * HR;
+    const int y = x / R8, j = x - y * R8, b = y / HR, pair = y - b * HR;
     const long long n = prefix[b + 1] - prefix[b], u = prefix[b] * HR + pair * n;
     const int wa = at_owner(units, ctas, u), wb = at_owner(units, ctas, u + n - 1);
     if (wa == wb) continue;
-    const int h = pair / a.row_tiles, r0 = ((pair - h * a.row_tiles) * NR + j) * 8;
+    const int h = pair / a.row_tiles, r0 = ((pair - h * a.row_tiles) * R8 + j) * 8;
     if (r0 >= rows) continue;
     float m[8], l[8], o[8][C];
 #pragma unroll
@@ -1117,12 +1122,13 @@ __global__ void __launch_bounds__(ATJ_THREADS) attend_q4_join_kernel(const __gri
       for (int i = 0; i < C; ++i) o[r][i] = 0.f;
     }
     for (int w = wa + (SPREAD ? warp : 0); w <= wb; w += PL) {
-      const float* part = a.ws + static_cast<size_t>(w) * at_cta_floats(D, NR) + (w == wa ? at_partial_floats(D, NR) : 0);
+      const float* part = a.ws + static_cast<size_t>(w) * stride + (w == wa ? partial : 0);
+      const float* ml = part + static_cast<size_t>(8 * R8) * D + 8 * j;
       float pm[8], pl[8], po[8][C];
 #pragma unroll
       for (int r = 0; r < 8; ++r) {
-        pm[r] = part[8 * NR * D + 8 * j + r];
-        pl[r] = part[8 * NR * D + 8 * NR + 8 * j + r] + part[8 * NR * D + 16 * NR + 8 * j + r];
+        pm[r] = ml[r];
+        pl[r] = ml[8 * R8 + r] + ml[16 * R8 + r];
 #pragma unroll
         for (int i = 0; i < C; ++i) po[r][i] = part[(8 * j + r) * D + i * 32 + lane];
       }

@@ -1,0 +1,1062 @@
+// attend_q4_tc.cuh -- verification attention over the 4-bit cache for more rows
+// than the bus alone bounds (chains of grouped heads, trees, chunks of prompts),
+// on the tcgen05 tensor cores.
+//
+// The products keep the tokens, not the rows, as M, so that any number of rows
+// fits without padding M:
+//   S^T[128 tokens x NC rows] = K[128 x D] Q^T      (A = K in tensor memory, B = Q)
+//   O^T[128 >= D x NC rows] += V^T[D x 128] P^T     (A = V, B = P in shared memory)
+// NC, the rows of a tile, is 16, 32, 64 or 128.  What this buys beside that:
+// * a thread of the unpacking warps has one token: it reads the token's codes,
+//   widens them (exactly, in f16, as attend_q4.cuh does) and stores its row of K
+//   straight into its lane of tensor memory; V goes to shared memory in the plain
+//   core-matrix order (8 x 16 bytes), which a warp of tokens writes without
+//   conflicts.  The codes come by tensor-map copies whose 64- or 32-byte swizzle
+//   spreads a warp's reads, one row a lane, over the banks.
+// * a thread of the softmax warps has one token and half of the tile's rows;
+//   the weights go to shared memory the way V does.
+// A row's maximum over the tokens would be a reduction across threads in every
+// tile.  Instead the weights are 2^(z - ref + 7) against a reference per row that
+// all threads know; only when some score exceeds its row's reference by 8 (always
+// in a triple's first tile, rarely later) the four warps that have the row agree on
+// new references and rescale their rows of O^T and of the sums.
+//
+// Roles of a CTA (one an SM): four softmax warps for each half of the rows, which
+// also write the results; four or eight warps for the queries and the unpacking; one
+// that issues the products, and one for the copies.  K, S^T, V and P have two buffers each, queries
+// and O^T two where tensor and shared memory hold them (NC <= 64).  Each CTA has
+// one contiguous share of the list of tiles (attend_q4.cuh), with at most two
+// triples cut off at its ends, whose parts the join kernel puts together.
+//
+// Bounds, per tile of 128 tokens and D = 128: 784 clocks of the bus; products
+// 1,024 clocks at NC = 128; unpacking 256 conversions, 256 multiplications and 16
+// stores of 16 bytes a thread.
+//
+// Fresh entries are converted to f16 in units of the cache's shifts (exact from
+// 2^-14 to 65504 of them, an absolute 2^-25 below, where the cache itself resolves
+// 2^-10).  A tile with an entry beyond that range, or with a NaN or an infinity, is
+// rare: its scores are computed on the CUDA cores, and its entries out of range
+// are added to O^T one by one, for the rows that see them.
+#pragma once
+
+#include <cuda.h>
+
+#include "attend_q4.cuh"
+
+namespace sv {
+
+constexpr int TC_TILE = 128;                 // tokens of a tile
+constexpr uint32_t TC_VBUF = 128 * 128 * 2;  // bytes of a V buffer (16 groups of 8 columns, also for D = 64)
+
+template <int D, int NC>
+struct TcLayout {
+  static constexpr int HC = NC / 2;                            // rows of a softmax thread
+  static constexpr int CH = HC < 32 ? HC : 32;                 // of them at a time
+  static constexpr int SOFT = 8;                               // softmax warps: four for each half of the rows
+  // Unpacking: four warps for keys and four for values; at NC = 128, where the
+  // softmax is what takes longest and needs the registers, four for both.
+  static constexpr int UNPACK = NC == 128 ? 4 : 8;
+  static constexpr int WARPS = SOFT + UNPACK + 2, THREADS = 32 * WARPS;
+  static constexpr int QB = NC <= 64 ? 2 : 1;                  // buffers of queries and of O^T
+  static constexpr int STAGES = NC == 128 ? 2 : 4;
+  static constexpr uint32_t stage_bytes = 4 * q4_block_bytes(D);
+  static constexpr uint32_t q_bytes = NC * D * 2, p_bytes = 128 * NC * 2;
+  // offsets (each a multiple of 1024 where a swizzled copy lands, of 128 elsewhere)
+  static constexpr uint32_t ring = 0;
+  static constexpr uint32_t v = ring + ((STAGES * stage_bytes + 1023) / 1024) * 1024;
+  static constexpr uint32_t p = v + 2 * TC_VBUF;
+  static constexpr uint32_t q = p + 2 * p_bytes;
+  static constexpr uint32_t factor = q + QB * q_bytes;         // [2][NC]: from products to the log2 domain
+  static constexpr uint32_t shift = factor + 2 * NC * 4;      // [NC]: 7 - reference (inf: none yet)
+  static constexpr uint32_t corr = shift + NC * 4;             // [NC]
+  static constexpr uint32_t top = corr + NC * 4;               // [4][NC]: maxima or sums of the four warps
+  static constexpr uint32_t seen = top + 4 * NC * 4;           // [4][NC]: mask words
+  static constexpr uint32_t rows = seen + 4 * NC * 4;          // [NC] 8 bytes: the rows' places in the output
+  static constexpr uint32_t bars = rows + NC * 8;
+  static constexpr uint32_t bytes = bars + 384;
+  // tensor memory columns
+  static constexpr uint32_t t_s = 0, t_o = 2 * NC, t_k = t_o + QB * NC;
+  static constexpr uint32_t t_need = t_k + 2 * (D / 2);
+  static constexpr uint32_t t_cols = t_need <= 256 ? 256 : 512;
+};
+// A CTA's part of the workspace: two partials as in attend_q4.cuh, then the
+// weights of one tile (for fresh entries out of range)
+__host__ __device__ constexpr size_t tc_cta_floats(int D, int NC) {
+  return 2 * static_cast<size_t>(NC) * (D + 4) + static_cast<size_t>(128) * NC;
+}
+
+struct TcBars {
+  uint64_t full[4], empty[4], kready[2], vready[2], qready[2], qfree[2], sready[2], sfree[2], pready[2],
+      pvdone[2], ofree[2], drain;
+  uint32_t tmem;
+  int dead;       // a wait ran out of time
+  float common[2]; // the factor of all rows of a triple, 0: they differ
+  float qmax[4], qmin[4];
+  int wide[2];    // 1 + the last tile of the buffer that has fresh entries out of range
+  int arrived[4]; // the stage's tile came (its page ids are in range)
+};
+static_assert(sizeof(TcBars) <= 384, "barriers");
+
+// ---------------------------------------------------------------------------
+// tcgen05
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+// shared-memory operand without swizzle: start, strides of the two directions
+__device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | (static_cast<uint64_t>(lbo >> 4) << 16) |
+         (static_cast<uint64_t>(sbo >> 4) << 32) | (1ull << 46);
+}
+// f16 operands, fp32 result, M = 128; A and B with their M or N direction contiguous where asked
+__host__ __device__ constexpr uint32_t tc_idesc(int n, bool a_mn, bool b_mn) {
+  return (1u << 4) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
+}
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+      : "memory");
+}
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+      : "memory");
+}
+template <int N>
+__device__ __forceinline__ void tc_ld(uint32_t addr, float (&x)[N]) {
+  static_assert(N == 8 || N == 16 || N == 32, "columns of a load");
+  uint32_t r[N];
+  if constexpr (N == 8) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(addr));
+  } else if constexpr (N == 16) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+  } else {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr));
+  }
+  tc_wait_ld();
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tc_st8(uint32_t addr, const float* x) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0,%1,%2,%3,%4,%5,%6,%7};" ::"f"(x[0]), "f"(x[1]), "f"(x[2]),
+               "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]), "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void tc_st1(uint32_t addr, float x) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%1], {%0};" ::"f"(x), "r"(addr) : "memory");
+}
+__device__ __forceinline__ float tc_ld1(uint32_t addr) {
+  uint32_t r;
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(addr));
+  tc_wait_ld();
+  return __uint_as_float(r);
+}
+// whether any of the N threads at a named barrier says so
+template <int N>
+__device__ __forceinline__ bool tc_any(int id, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(x)), "r"(id), "n"(N)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ void tc_proxy_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// What a role seldom does is kept out of the way of its loop: every jump over such
+// code costs a warp that is alone on its scheduler a fetch of instructions.
+#define TC_RARE(x) (__builtin_expect(!!(x), 0))
+
+// Bounded wait.  False when time is up here or was up elsewhere in the CTA.  The
+// roles hand over to each other several times a tile, so a wait polls without a
+// hint how long it may sleep (with one of a millisecond, a hand-over took about 500
+// clocks), and looks at the time once in 64 polls.
+__device__ __forceinline__ bool tc_poll(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __noinline__ bool tc_wait_long(uint64_t* bar, uint32_t parity, TcBars* b, unsigned long long limit) {
+  const uint64_t t0 = global_ns();
+  for (uint32_t i = 1; i < (1u << 28); ++i) {
+    if (tc_poll(bar, parity)) return true;
+    if ((i & 63u) == 0u) {
+      if (*reinterpret_cast<volatile int*>(&b->dead)) return false;
+      if (global_ns() - t0 > limit) break;
+    }
+  }
+  *reinterpret_cast<volatile int*>(&b->dead) = 1;
+  return false;
+}
+__device__ __forceinline__ bool tc_wait_one(uint64_t* bar, uint32_t parity, TcBars* b, unsigned long long limit) {
+  if (__builtin_expect(tc_poll(bar, parity), 1)) return true;
+  return tc_wait_long(bar, parity, b, limit);
+}
+
+// the same for a whole warp, whose lanes go on alike
+__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, TcBars* b, unsigned long long limit) {
+  return __all_sync(0xffffffffu, tc_wait_one(bar, parity, b, limit));
+}
+
+// byte `o` of a block of rows of 64 (D = 128) or 32 bytes, as the swizzled copy leaves it
+template <int D>
+__device__ __forceinline__ uint32_t tc_swz(uint32_t o) {
+  return D == 128 ? o ^ (((o >> 7) & 3u) << 4) : o ^ (((o >> 7) & 1u) << 4);
+}
+
+// ---------------------------------------------------------------------------
+// the list of tiles of a CTA, walked alike by all roles
+// ---------------------------------------------------------------------------
+struct TcTile {
+  AtCursor c;
+  int h, row0;           // kv head, first row
+  int kind, at, left;    // what the tile is; its first token or node; tokens of it (0..128)
+  bool first, last;      // of the triple's part in the share
+};
+enum { TC_CACHED = 0, TC_FRESH = 1, TC_VOID = 2 };   // void: a length out of range (left = 1), or nothing at all (left = 0)
+
+template <int NC>
+__device__ __noinline__ void tc_open_slow(const AttendArgs& a, int nfresh, TcTile& t) {
+  t.h = t.c.pair / a.row_tiles;
+  t.row0 = (t.c.pair - t.h * a.row_tiles) * NC;
+  t.at = 0;
+  if (!at_len_ok(a, t.c.len)) {
+    t.kind = TC_VOID;
+    t.left = 1;
+  } else if (t.c.i < nfresh) {
+    t.kind = TC_FRESH;
+    t.at = t.c.i * TC_TILE;
+    t.left = min(a.N - t.at, TC_TILE);
+  } else {
+    t.at = (t.c.i - nfresh) * TC_TILE;
+    t.left = min(t.c.len - t.at, TC_TILE);
+    t.kind = t.left > 0 ? TC_CACHED : TC_VOID;
+    if (t.left < 0) t.left = 0;
+  }
+}
+template <int NC>
+__device__ __forceinline__ void tc_open(const AttendArgs& a, int nfresh, TcTile& t) {
+  TcTile x = t;   // (by a copy: the tile itself stays in registers)
+  tc_open_slow<NC>(a, nfresh, x);
+  t = x;
+}
+template <int NC>
+__device__ __forceinline__ void tc_begin(const AttendArgs& a, const long long* prefix, int HR, int nfresh, long long u, int n, TcTile& t) {
+  at_seek(a, prefix, HR, u, t.c);
+  tc_open<NC>(a, nfresh, t);
+  t.first = true;
+  t.last = t.c.i + 1 == t.c.units || n == 1;
+}
+// to the next tile; `left`: tiles of the share from there on
+template <int NC>
+__device__ __forceinline__ void tc_step(const AttendArgs& a, const long long* prefix, int HR, int nfresh, int left, TcTile& t) {
+  if (TC_RARE(t.c.i + 1 == t.c.units || t.c.i + 1 == nfresh)) {   // another triple, or its first cached tile
+    t.first = t.c.i + 1 == t.c.units;
+    at_next(a, prefix, HR, t.c);
+    tc_open<NC>(a, nfresh, t);
+  } else {
+    ++t.c.i;
+    t.first = false;
+    t.at += TC_TILE;
+    t.left = min((t.kind == TC_FRESH ? a.N : t.c.len) - t.at, TC_TILE);
+  }
+  t.last = t.c.i + 1 == t.c.units || left == 1;
+}
+
+// ---------------------------------------------------------------------------
+// unpacking
+// ---------------------------------------------------------------------------
+// sixteen codes (two words) under one scale (twice in s2) to eight f16 pairs
+__device__ __forceinline__ void tc_widen(uint32_t w0, uint32_t w1, uint32_t s2, uint32_t* r) {
+  e2m1x8_to_f16(w0, r);
+  e2m1x8_to_f16(w1, r + 4);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = f16x2_mul(r[i], s2);
+}
+// scale byte g of a word as an f16 pair of equals
+__device__ __forceinline__ uint32_t tc_scale(uint32_t sc, int g) { return e4m3x2_to_f16(__byte_perm(sc, 0u, g * 0x11)); }
+// eight f16 pairs of a fresh entry's 16 elements, in units of 1 / mul; `odd` when one does not fit
+__device__ __forceinline__ void tc_narrow(const uint4& x, const uint4& y, float mul, uint32_t* r, bool& odd) {
+  const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    float lo = __uint_as_float(w[i] << 16) * mul, hi = __uint_as_float(w[i] & 0xffff0000u) * mul;
+    if (!(fabsf(lo) <= 65504.f)) { odd = true; lo = 0.f; }
+    if (!(fabsf(hi) <= 65504.f)) { odd = true; hi = 0.f; }
+    r[i] = f16x2_pack(lo, hi);
+  }
+}
+
+// A fresh node's key into its lane of tensor memory.  True when an element of the
+// key or of the value does not fit.
+template <int D>
+__device__ __noinline__ bool tc_fresh_key(const AttendArgs& a, int b, int h, int node, bool mine, uint32_t k_at) {
+  const long long at = ((static_cast<long long>(b) * a.N + (mine ? node : 0)) * a.Hkv + h) * D;
+  const uint4 *k = reinterpret_cast<const uint4*>(a.k_new + at), *v = reinterpret_cast<const uint4*>(a.v_new + at);
+  const float kmul = __fdiv_rn(1.f, a.k_mul), vmul = __fdiv_rn(1.f, a.v_mul);
+  bool odd = false;
+#pragma unroll 1
+  for (int c = 0; c < D / 32; ++c) {
+    uint4 x[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = mine ? __ldg(k + 4 * c + i) : make_uint4(0u, 0u, 0u, 0u);
+      x[4 + i] = mine ? __ldg(v + 4 * c + i) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    uint32_t r[16];
+    tc_narrow(x[4], x[5], vmul, r, odd);
+    tc_narrow(x[6], x[7], vmul, r + 8, odd);
+    tc_narrow(x[0], x[1], kmul, r, odd);
+    tc_narrow(x[2], x[3], kmul, r + 8, odd);
+    __syncwarp();
+    tc_st16(k_at + c * 16, r);
+  }
+  return odd;
+}
+// its value into shared memory (0 for what does not fit)
+template <int D>
+__device__ __noinline__ void tc_fresh_value(const AttendArgs& a, int b, int h, int node, bool mine, unsigned char* vb) {
+  const long long at = ((static_cast<long long>(b) * a.N + (mine ? node : 0)) * a.Hkv + h) * D;
+  const uint4* v = reinterpret_cast<const uint4*>(a.v_new + at);
+  const float vmul = __fdiv_rn(1.f, a.v_mul);
+  bool odd = false;
+#pragma unroll 1
+  for (int c = 0; c < D / 32; ++c) {
+    uint4 x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = mine ? __ldg(v + 4 * c + i) : make_uint4(0u, 0u, 0u, 0u);
+    uint32_t r[16];
+    tc_narrow(x[0], x[1], vmul, r, odd);
+    tc_narrow(x[2], x[3], vmul, r + 8, odd);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      *reinterpret_cast<uint4*>(vb + (4 * c + i) * 2048) = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+  }
+}
+
+// Queries of a row tile (128 threads).  Usually one power of two scales all rows,
+// so that the largest element lies in [128, 256); where the rows' largest elements
+// lie more than 2^8 apart, each row gets its own (an element is off by 2^-25 at
+// most: 2^-24 of its row's largest with one power of two, 2^-32 with its own).
+template <int D, int NC>
+__device__ __noinline__ void tc_load_q(const AttendArgs& a, int b, int h, int row0, int rows, int qb, int fb, unsigned char* smem, TcBars* bar) {
+  using L = TcLayout<D, NC>;
+  constexpr int PER = D / 16;            // threads of a row, 16 elements each
+  constexpr int STEP = 128 / PER, U = NC / STEP < 4 ? (NC / STEP < 1 ? 1 : NC / STEP) : 4;
+  const int tid = threadIdx.x - 32 * L::SOFT, part = tid % PER, quad = tid >> 5;
+  float hi = 0.f, lo = __builtin_huge_valf();
+  bool odd = false;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    float common = 0.f;
+    if (pass == 1) {
+      // over the four warps
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+      }
+      odd = __any_sync(0xffffffffu, odd);
+      if ((tid & 31) == 0) {
+        bar->qmax[quad] = odd ? __builtin_huge_valf() : hi;
+        bar->qmin[quad] = lo;
+      }
+      named_bar_sync(6, 128);
+      hi = fmaxf(fmaxf(bar->qmax[0], bar->qmax[1]), fmaxf(bar->qmax[2], bar->qmax[3]));
+      lo = fminf(fminf(bar->qmin[0], bar->qmin[1]), fminf(bar->qmin[2], bar->qmin[3]));
+      common = hi < __builtin_huge_valf() && hi > 0.f && hi <= lo * 256.f ? hi : 0.f;
+      if (tid == 0) {
+        const int sh = min(7 - (static_cast<int>(__float_as_uint(common) >> 23) - 127), 100);
+        bar->common[fb] = common == 0.f ? 0.f
+                                        : fmaxf(fabsf(a.scale_log2) * a.k_mul * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23), 1.17549435e-38f);
+      }
+    }
+#pragma unroll 1
+    for (int r0 = tid / PER; r0 < NC; r0 += STEP * U) {
+      uint4 x[U], y[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int r = r0 + k * STEP;
+        x[k] = y[k] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < NC && row0 + r < rows) {
+          const uint4* p = reinterpret_cast<const uint4*>(a.q + at_row(a, b, h, row0 + r) * D + part * 16);
+          x[k] = __ldg(p);
+          y[k] = __ldg(p + 1);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int r = r0 + k * STEP;
+        const uint32_t w[8] = {x[k].x, x[k].y, x[k].z, x[k].w, y[k].x, y[k].y, y[k].z, y[k].w};
+        uint32_t m = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = bf16x2_max_nan(m, w[i] & 0x7fff7fffu);
+        float top = fmax_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+#pragma unroll
+        for (int o = 1; o < PER; o <<= 1) top = fmax_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (pass == 0) {
+          odd |= !(top < __builtin_huge_valf());
+          hi = fmaxf(hi, top);
+          if (top > 0.f) lo = fminf(lo, top);
+          continue;
+        }
+        const float by = common > 0.f ? common : top;
+        const int sh = by > 0.f ? min(7 - (static_cast<int>(__float_as_uint(by) >> 23) - 127), 100) : 0;
+        const float mul = copysignf(__uint_as_float(static_cast<uint32_t>(127 + sh) << 23), a.scale_log2);
+        uint32_t f[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = f16x2_pack(__uint_as_float(w[i] << 16) * mul, __uint_as_float(w[i] & 0xffff0000u) * mul);
+        if (r >= NC) continue;
+        unsigned char* to = smem + L::q + qb * L::q_bytes + r * 16;
+        *reinterpret_cast<uint4*>(to + (2 * part) * (NC * 16)) = make_uint4(f[0], f[1], f[2], f[3]);
+        *reinterpret_cast<uint4*>(to + (2 * part + 1) * (NC * 16)) = make_uint4(f[4], f[5], f[6], f[7]);
+        if (part == 0)
+          reinterpret_cast<float*>(smem + L::factor)[fb * NC + r] =
+              top < __builtin_huge_valf()
+                  ? fmaxf(fabsf(a.scale_log2) * a.k_mul * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23), 1.17549435e-38f)
+                  : __int_as_float(0x7fc00000);
+      }
+    }
+  }
+  named_bar_sync(6, 128);   // qmax and qmin are free again
+}
+
+// Scores of a tile with fresh entries out of range, on the CUDA cores, into the
+// products' place in tensor memory: this thread's node, the rows from col0.
+template <int D, int NC>
+__device__ __noinline__ void tc_wide_scores(const AttendArgs& a, int b, int h, int row0, int rows, int node, int col0, int cols,
+                                            const float* factor, uint32_t addr) {
+  for (int c = 0; c < cols; ++c) {
+    float s = 0.f;
+    const int r = row0 + col0 + c;
+    if (r < rows && node < a.N) {
+      const uint16_t* q = a.q + at_row(a, b, h, r) * D;
+      const uint16_t* k = a.k_new + ((static_cast<long long>(b) * a.N + node) * a.Hkv + h) * D;
+      for (int d = 0; d < D; ++d)
+        s += __uint_as_float(static_cast<uint32_t>(q[d]) << 16) * __uint_as_float(static_cast<uint32_t>(k[d]) << 16);
+      s = s * a.scale_log2 / factor[col0 + c];
+    }
+    __syncwarp();
+    tc_st1(addr + c, s);
+  }
+  tc_wait_st();
+}
+// Adds the fresh values out of range to O^T: this thread's column d, the rows from
+// col0; weights (negative: the row does not see the node) at w[node][NC].
+template <int D, int NC>
+__device__ __noinline__ void tc_wide_values(const AttendArgs& a, int b, int h, int node0, int left, int d, int col0, int cols,
+                                            const float* w, uint32_t addr) {
+  for (int j = 0; j < left; ++j) {
+    float v = 0.f;
+    if (d < D)
+      v = __uint_as_float(static_cast<uint32_t>(a.v_new[((static_cast<long long>(b) * a.N + node0 + j) * a.Hkv + h) * D + d]) << 16) / a.v_mul;
+    const bool odd = !(fabsf(v) <= 65504.f);
+    if (!__any_sync(0xffffffffu, odd)) continue;
+    for (int c = 0; c < cols; ++c) {
+      const float p = __ldcg(w + j * NC + col0 + c);
+      float o = tc_ld1(addr + c);
+      __syncwarp();
+      if (odd && !(p < 0.f)) o += (p == 0.f ? 1.17549435e-38f : p) * v;
+      __syncwarp();
+      tc_st1(addr + c, o);
+      tc_wait_st();
+    }
+  }
+}
+
+// column i of 32 (or fewer) over the lanes of a warp: lane i gets the maximum or the sum
+template <int N, bool SUM>
+__device__ __forceinline__ float tc_reduce(float (&x)[N]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    if (o >= N) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float y = __shfl_xor_sync(0xffffffffu, x[i], o);
+        x[i] = SUM ? x[i] + y : fmaxf(x[i], y);
+      }
+    } else {
+      // lanes with bit o keep the upper half of what is left
+#pragma unroll
+      for (int i = 0; i < o; ++i) {
+        const bool up = lane & o;
+        const float keep = up ? x[i + o] : x[i], give = up ? x[i] : x[i + o];
+        const float y = __shfl_xor_sync(0xffffffffu, give, o);
+        x[i] = SUM ? keep + y : fmaxf(keep, y);
+      }
+    }
+  }
+  return x[0];   // of column lane % N
+}
+
+// bits of the rows of a chunk that do not see this thread's node: those without its
+// bit in the warp's words (a tree), or those before row `open` (a chain)
+template <int CH>
+__device__ __noinline__ uint32_t tc_hidden(bool tree, const uint32_t* seen, int open) {
+  if (!tree) return open <= 0 ? 0u : open >= 32 ? ~0u : (1u << open) - 1u;
+  uint32_t hide = 0u;
+#pragma unroll 1
+  for (int i = 0; i < CH; ++i) hide |= (~(seen[i] >> (threadIdx.x & 31)) & 1u) << i;
+  return hide;
+}
+
+// New references for CH rows: the 128 threads of a half call this together.
+// s_at: the tile's products (hide: bits of rows that do not see this thread's
+// token), o_at: the rows' sums of v so far, if there are any.
+template <int CH, int NC>
+__device__ __noinline__ void tc_raise(uint32_t s_at, uint32_t o_at, const float* factor, float* shift, float* corr, float* top,
+                                      uint32_t hide, bool sums, int quad, int id) {
+  const int lane = threadIdx.x & 31;
+  float z[CH];
+  tc_ld<CH>(s_at, z);
+#pragma unroll
+  for (int i = 0; i < CH; ++i) z[i] = (hide >> i) & 1u ? kNegInf : fmaxf(z[i] * factor[i], kNegInf);   // (no NaN)
+  const float mx = tc_reduce<CH, false>(z);
+  if (lane < CH) top[quad * NC + lane] = mx;
+  named_bar_sync(id, 128);
+  if (quad == 0 && lane < CH) {
+    const float m = fmaxf(fmaxf(top[lane], top[NC + lane]), fmaxf(top[2 * NC + lane], top[3 * NC + lane]));
+    const float old = shift[lane];                                // 7 - ref, inf: none
+    const float now = m == kNegInf ? old : fminf(old, AT_PSHIFT - m);
+    shift[lane] = now;
+    corr[lane] = old == __builtin_huge_valf() ? 1.f : at_corr(now - old);
+  }
+  named_bar_sync(id, 128);
+  if (sums) {
+    tc_fence_after();
+#pragma unroll 1
+    for (int i = 0; i < CH; i += 8) {
+      float o[8];
+      tc_ld<8>(o_at + i, o);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o[k] *= corr[i + k];
+      tc_st8(o_at + i, o);
+    }
+    tc_wait_st();
+  }
+}
+
+// The end of a triple, or of its part in the share: the sums of weights over the
+// four warps of a part of the rows, then O^T row by row, as the result or (not
+// whole) as a partial.
+template <int D, int NC>
+__device__ __noinline__ void tc_finish(const AttendArgs& a, int b, int h, int row0, int rows, bool whole, float* partial, const float* l,
+                                       const float* shift, float* corr, float* top, long long* place, uint32_t o_at, int part) {
+  constexpr int HC = TcLayout<D, NC>::HC, CH = TcLayout<D, NC>::CH;
+  const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, col0 = part * HC, id = 1 + part, d = 32 * quad + lane;
+  tc_fence_after();
+#pragma unroll 1
+  for (int c0 = 0; c0 < HC; c0 += CH) {
+    float z[CH];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) z[i] = l[c0 + i];
+    const float sum = tc_reduce<CH, true>(z);
+    if (lane < CH) top[quad * NC + c0 + lane] = sum;
+  }
+  named_bar_sync(id, 128);
+  for (int i = threadIdx.x & 127; i < HC; i += 128) {
+    place[i] = at_row(a, b, h, min(row0 + col0 + i, rows - 1)) * D;
+    const float sum = (top[i] + top[NC + i]) + (top[2 * NC + i] + top[3 * NC + i]);
+    const int r = row0 + col0 + i;
+    const float ref = AT_PSHIFT - shift[i];
+    corr[i] = sum == 0.f ? 0.f : a.v_mul / sum;
+    if (whole) {
+      if (r < rows && a.lse) a.lse[place[i] / D] = at_lse(ref, sum);
+    } else {
+      float* ml = partial + static_cast<size_t>(NC) * D + col0 + i;
+      ml[0] = ref;
+      ml[NC] = sum;
+      ml[2 * NC] = 0.f;
+    }
+  }
+  named_bar_sync(id, 128);
+  const int real = rows - row0 - col0;   // rows of the half that there are
+#pragma unroll 1
+  for (int c0 = 0; c0 < HC; c0 += 8) {
+    float o[8];
+    __syncwarp();
+    tc_ld<8>(o_at + c0, o);
+    if (d >= D) continue;
+    if (whole) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (c0 + i < real) a.out[place[c0 + i] + d] = static_cast<uint16_t>(bf16x2_pack(o[i] * corr[c0 + i], 0.f));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) partial[static_cast<size_t>(col0 + c0 + i) * D + d] = o[i];
+    }
+  }
+}
+
+template <int D, int NC>
+__global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kernel(const __grid_constant__ AttendArgs a,
+                                                                     const __grid_constant__ CUtensorMap map) {
+  using L = TcLayout<D, NC>;
+  extern __shared__ unsigned char tc_raw[];
+  __shared__ long long scratch[L::WARPS];
+  unsigned char* tc_smem = tc_raw + ((1024u - (smem_addr(tc_raw) & 1023u)) & 1023u);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  TcBars* bar = reinterpret_cast<TcBars*>(tc_smem + L::bars);
+  long long* prefix = reinterpret_cast<long long*>(tc_smem + L::bytes);
+  const uint32_t sbase = smem_addr(tc_smem);
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&bar->full[i], 1);
+      mbar_init(&bar->empty[i], L::UNPACK);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar->kready[i], 4);
+      mbar_init(&bar->vready[i], 4);
+      mbar_init(&bar->qready[i], 4);
+      mbar_init(&bar->qfree[i], 1);
+      mbar_init(&bar->sready[i], 1);
+      mbar_init(&bar->sfree[i], L::SOFT);
+      mbar_init(&bar->pready[i], L::SOFT);
+      mbar_init(&bar->pvdone[i], 1);
+      mbar_init(&bar->ofree[i], L::SOFT);
+      bar->wide[i] = 0;
+    }
+    mbar_init(&bar->drain, 1);
+    bar->dead = 0;
+    mbar_fence_init();
+  }
+  at_prefix<L::THREADS>(a, prefix, scratch);   // (synchronises the CTA)
+  const int HR = a.Hkv * a.row_tiles;
+  const long long units = prefix[a.B] * HR;
+  const int ctas = at_active(units, gridDim.x, 1);
+  if (blockIdx.x >= ctas) return;
+  const long long u0 = at_start(units, ctas, blockIdx.x);
+  const int ntiles = static_cast<int>(at_start(units, ctas, blockIdx.x + 1) - u0);
+  const int rows = a.N * a.G, nfresh = a.k_new ? (a.N + TC_TILE - 1) / TC_TILE : 0;
+  if (warp == L::SOFT + L::UNPACK) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&bar->tmem)), "r"(L::t_cols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bar->tmem;
+  const unsigned long long limit = a.timeout_ns;
+  float* cta_ws = a.ws + static_cast<size_t>(blockIdx.x) * tc_cta_floats(D, NC);
+
+  if (warp == L::SOFT + L::UNPACK + 1) {
+    // ---- copies: up to four blocks a tile, a lane each --------------------------------
+    TcTile t;
+    tc_begin<NC>(a, prefix, HR, nfresh, u0, ntiles, t);
+    int n = 0;                        // cached tiles so far
+    int page = -1, page_at = -1;      // a lane's entry of the 32 blocks from page_at on (of this triple)
+    const int bpp = a.P / Q4_BLOCK;
+    for (int u = 0;;) {
+      if (t.kind == TC_CACHED) {
+        const int blk = t.at / Q4_BLOCK, nblk = (t.left + Q4_BLOCK - 1) / Q4_BLOCK;
+        if (t.first || page_at < 0 || blk >= page_at + 32) {
+          page_at = blk;
+          const int x = blk + lane;
+          page = x * Q4_BLOCK < t.c.len ? __ldg(a.table + static_cast<long long>(t.c.b) * a.W + x / bpp) : -1;
+        }
+        const int mine = __shfl_sync(0xffffffffu, page, blk - page_at + (lane & 3));
+        const bool ok = lane >= nblk || (mine >= 0 && mine < a.pages);
+        const int s = n % L::STAGES;
+        bool go = true;
+        if (n >= L::STAGES) go = tc_wait(&bar->empty[s], ((n / L::STAGES) & 1) ^ 1, bar, limit);
+        if (!go) break;
+        const bool all = __all_sync(0xffffffffu, ok);
+        if (lane == 0) bar->arrived[s] = all;
+        if (all) {
+          if (lane == 0) mbar_arrive_expect_tx(&bar->full[s], nblk * q4_block_bytes(D));
+          __syncwarp();
+          if (lane < nblk) {
+            const int x = blk + lane;
+            const int z = static_cast<int>((static_cast<long long>(mine) * a.Hkv + t.h) * bpp + x % bpp);
+            asm volatile(
+                "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+                    sbase + L::ring + s * L::stage_bytes + lane * q4_block_bytes(D)),
+                "l"(&map), "r"(0), "r"(0), "r"(z), "r"(smem_addr(&bar->full[s]))
+                : "memory");
+          }
+        } else if (lane == 0) {
+          mbar_arrive(&bar->full[s]);
+        }
+        ++n;
+      } else {
+        page_at = -1;
+      }
+      if (++u >= ntiles) break;
+      tc_step<NC>(a, prefix, HR, nfresh, ntiles - u, t);
+    }
+    // copies still on their way land before the CTA ends (or the wait gives up)
+    if (*reinterpret_cast<volatile int*>(&bar->dead))
+      for (int i = max(0, n - L::STAGES); i < n; ++i) mbar_wait(&bar->full[i % L::STAGES], (i / L::STAGES) & 1, limit);
+  } else if (warp == L::SOFT + L::UNPACK) {
+    // ---- products: one thread ------------------------------------------------------------
+    if (lane == 0) {
+      constexpr uint32_t id_s = tc_idesc(NC, false, false), id_o = tc_idesc(NC, true, true);
+      TcTile t;
+      tc_begin<NC>(a, prefix, HR, nfresh, u0, ntiles, t);
+      bool pfirst = false;              // the tile before: was it a triple's first
+      int n = 0, tri = 0, ptri = 0;     // tiles, triples so far; the tile before's triple
+      auto add_v = [&](int m, bool first, int tr) {   // O^T += V^T P^T of tile m
+        const int x = m & 1;
+        if (!tc_wait_one(&bar->pready[x], (m >> 1) & 1, bar, limit) || !tc_wait_one(&bar->vready[x], (m >> 1) & 1, bar, limit)) return false;
+        const int ob = tr % L::QB;
+        if (first && tr >= L::QB && !tc_wait_one(&bar->ofree[(tr - L::QB) & 1], ((tr - L::QB) >> 1) & 1, bar, limit)) return false;
+        tc_fence_after();
+        const uint64_t vd = tc_desc(sbase + L::v + x * TC_VBUF, 128, 2048), pd = tc_desc(sbase + L::p + x * L::p_bytes, 128, 2048);
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)   // (16 tokens: 256 bytes on)
+          tc_mma_ss(tmem + L::t_o + ob * NC, vd + ks * 16, pd + ks * 16, id_o, !(first && ks == 0));
+        tc_commit(&bar->pvdone[x]);
+        return true;
+      };
+      bool ok = true;
+      for (int u = 0;;) {
+        const int x = n & 1, qb = tri % L::QB;
+        if (t.first) ok = tc_wait_one(&bar->qready[qb], (tri / L::QB) & 1, bar, limit);
+        ok = ok && tc_wait_one(&bar->kready[x], (n >> 1) & 1, bar, limit);
+        if (ok && n >= 2) ok = tc_wait_one(&bar->sfree[x], ((n >> 1) & 1) ^ 1, bar, limit);
+        if (!ok) break;
+        tc_fence_after();
+        const uint64_t qd = tc_desc(sbase + L::q + qb * L::q_bytes, NC * 16, 128);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks)   // (16 elements: two core-matrix columns on)
+          tc_mma_ts(tmem + L::t_s + x * NC, tmem + L::t_k + x * (D / 2) + ks * 8, qd + ks * (2 * NC), id_s, ks > 0);
+        tc_commit(&bar->sready[x]);   // (and K's buffer is free)
+        if (t.last) tc_commit(&bar->qfree[qb]);
+        if (n > 0) ok = add_v(n - 1, pfirst, ptri);
+        if (!ok) break;
+        pfirst = t.first;
+        ptri = tri;
+        if (t.last) ++tri;
+        ++n;
+        if (++u >= ntiles) {
+          add_v(n - 1, pfirst, ptri);
+          break;
+        }
+        tc_step<NC>(a, prefix, HR, nfresh, ntiles - u, t);
+      }
+      tc_commit(&bar->drain);
+      mbar_wait(&bar->drain, 0, limit);   // nothing is in flight when tensor memory is given back
+    }
+    __syncwarp();
+  } else if (warp >= L::SOFT) {
+    // ---- queries and unpacking: a thread a token ----------------------------------------------
+    const int quad = warp & 3, tok = 32 * quad + lane;
+    const uint32_t lane_at = static_cast<uint32_t>(32 * quad) << 16;
+    const bool keys = warp < L::SOFT + 4, values = L::UNPACK == 4 || !keys;
+    TcTile t;
+    tc_begin<NC>(a, prefix, HR, nfresh, u0, ntiles, t);
+    int n = 0, tri = 0, copies = 0;
+    for (int u = 0;;) {
+      const int x = n & 1;
+      if (TC_RARE(t.first)) {
+        if (keys) {
+          const int qb = tri % L::QB;
+          // (the factors have two buffers, which the softmax warps read to the triple's end)
+          if (tri >= L::QB && !tc_wait(&bar->qfree[qb], ((tri / L::QB) & 1) ^ 1, bar, limit)) break;
+          if (tri >= 2 && !tc_wait(&bar->ofree[tri & 1], ((tri >> 1) & 1) ^ 1, bar, limit)) break;
+          tc_load_q<D, NC>(a, t.c.b, t.h, t.row0, rows, qb, tri & 1, tc_smem, bar);
+          tc_proxy_fence();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar->qready[qb]);
+        }
+        ++tri;
+      }
+      const int stage = copies % L::STAGES;
+      if (t.kind == TC_CACHED && !tc_wait(&bar->full[stage], (copies / L::STAGES) & 1, bar, limit)) break;
+      const unsigned char* blk = tc_smem + L::ring + stage * L::stage_bytes + quad * q4_block_bytes(D);
+      // A token that counts has its scales; others get 0, and one of a tile that did
+      // not come, or of a length out of range, NaN for its key.
+      const bool mine = tok < t.left;
+      const bool good = t.kind == TC_CACHED && *reinterpret_cast<volatile int*>(&bar->arrived[stage]);
+      auto scales = [&](int from) -> uint64_t {
+        if constexpr (D == 128) return *reinterpret_cast<const uint64_t*>(blk + tc_swz<D>(from + lane * 8));
+        else return *reinterpret_cast<const uint32_t*>(blk + tc_swz<D>(from + lane * 4));
+      };
+      // Where the same warps do both, the key goes first: its buffer is free long
+      // before the value's, and the scores of this tile can then be taken beside the
+      // weights of the last one.  (Rolled loops: a warp that is alone on its
+      // scheduler waits for its instructions otherwise.)
+      if (keys) {
+        if (n >= 2 && !tc_wait(&bar->sready[x], ((n >> 1) & 1) ^ 1, bar, limit)) break;
+        tc_fence_after();
+        const uint32_t k_at = tmem + lane_at + L::t_k + x * (D / 2);
+        if (TC_RARE(t.kind == TC_FRESH)) {
+          if (tc_fresh_key<D>(a, t.c.b, t.h, t.at + tok, mine, k_at)) *reinterpret_cast<volatile int*>(&bar->wide[x]) = n + 1;
+        } else {
+          uint64_t sc = !mine ? 0ull : good ? scales(32 * D) : 0x7f7f7f7f7f7f7f7full;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            const uint4 w = *reinterpret_cast<const uint4*>(blk + tc_swz<D>(lane * (D / 2) + c * 16));
+            uint32_t r[16];
+            tc_widen(w.x, w.y, tc_scale(static_cast<uint32_t>(sc), 0), r);
+            tc_widen(w.z, w.w, tc_scale(static_cast<uint32_t>(sc), 1), r + 8);
+            tc_st16(k_at + c * 16, r);
+            sc >>= 16;
+          }
+        }
+        tc_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar->kready[x]);
+      }
+      if (values) {
+        if (n >= 2 && !tc_wait(&bar->pvdone[x], ((n >> 1) & 1) ^ 1, bar, limit)) break;
+        unsigned char* vb = tc_smem + L::v + x * TC_VBUF + tok * 16;
+        if (TC_RARE(t.kind == TC_FRESH)) {
+          tc_fresh_value<D>(a, t.c.b, t.h, t.at + tok, mine, vb);
+        } else {
+          uint64_t sc = mine && good ? scales(34 * D) : 0ull;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            const uint4 w = *reinterpret_cast<const uint4*>(blk + tc_swz<D>(16 * D + lane * (D / 2) + c * 16));
+            uint32_t r[16];
+            tc_widen(w.x, w.y, tc_scale(static_cast<uint32_t>(sc), 0), r);
+            tc_widen(w.z, w.w, tc_scale(static_cast<uint32_t>(sc), 1), r + 8);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint4*>(vb + (4 * c + i) * 2048) = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+            sc >>= 16;
+          }
+        }
+        tc_proxy_fence();
+      }
+      __syncwarp();
+      if (lane == 0) {
+        if (values) mbar_arrive(&bar->vready[x]);
+        if (t.kind == TC_CACHED) mbar_arrive(&bar->empty[stage]);
+      }
+      if (t.kind == TC_CACHED) ++copies;
+      ++n;
+      if (++u >= ntiles) break;
+      tc_step<NC>(a, prefix, HR, nfresh, ntiles - u, t);
+    }
+  } else {
+    // ---- softmax: a thread a token and a part of the rows ---------------------------------------
+    constexpr int HC = L::HC, CH = L::CH;
+    const int part = warp >> 2, quad = warp & 3, tok = 32 * quad + lane, id = 1 + part, col0 = part * HC;
+    const uint32_t lane_at = static_cast<uint32_t>(32 * quad) << 16;
+    float* shift = reinterpret_cast<float*>(tc_smem + L::shift) + col0;
+    float* corr = reinterpret_cast<float*>(tc_smem + L::corr) + col0;
+    float* top = reinterpret_cast<float*>(tc_smem + L::top) + col0;            // [4][NC], the part's columns
+    uint32_t* seen = reinterpret_cast<uint32_t*>(tc_smem + L::seen) + quad * NC + col0;
+    unsigned long long l[HC / 2];                                              // sums of weights, two rows each
+    TcTile t;
+    tc_begin<NC>(a, prefix, HR, nfresh, u0, ntiles, t);
+    int n = 0, tri = 0;
+    int itri = t.c.i;
+    float common = 0.f;                     // the rows' factor, 0: each its own
+    unsigned long long common2 = 0ull;      // what the packed product takes
+    bool alive = true;
+    for (int u = 0;;) {
+      const int x = n & 1, qb = tri % L::QB;
+      const float* factor = reinterpret_cast<const float*>(tc_smem + L::factor) + (tri & 1) * NC + col0;
+      if (TC_RARE(t.first)) {
+        itri = t.c.i;
+#pragma unroll
+        for (int i = 0; i < HC / 2; ++i) l[i] = 0ull;
+        for (int i = threadIdx.x & 127; i < HC; i += 128) shift[i] = __builtin_huge_valf();
+        named_bar_sync(id, 128);
+      }
+      // (A warp whose wait fails goes on in step with the others, which it meets at
+      // barriers; every wait then returns at once.)
+      alive = tc_wait(&bar->sready[x], (n >> 1) & 1, bar, limit) && alive;
+      tc_fence_after();
+      const uint32_t s_at = tmem + lane_at + L::t_s + x * NC + col0;
+      const uint32_t o_at = tmem + lane_at + L::t_o + qb * NC + col0;
+      if (TC_RARE(t.first)) {
+        common = bar->common[tri & 1];
+        common2 = common == 0.f ? f2_pack(1.f, 1.f) : f2_pack(common, common);
+      }
+      bool wide = false, some = false;
+      int open = 0;   // in a fresh tile of a chain, the node's first row in the half
+      if (TC_RARE(t.kind != TC_CACHED || t.left < TC_TILE)) {
+        some = true;
+        if (t.kind == TC_FRESH) {
+          // (one answer for the half, whatever the flag does once a wait has failed)
+          wide = tc_any<128>(id, *reinterpret_cast<volatile int*>(&bar->wide[x]) == n + 1);
+          if (a.masks) {   // the warp's 32 nodes are one word of each row's mask
+            for (int i = lane; i < HC; i += 32) {
+              const int r = t.row0 + col0 + i;
+              uint32_t w = 0u;
+              if (r < rows && t.at + 32 * quad < a.N)
+                w = __ldg(a.masks + (static_cast<long long>(t.c.b) * a.N + r / a.G) * a.NW + t.at / 32 + quad);
+              seen[i] = w;
+            }
+            __syncwarp();
+          } else {
+            open = (t.at + tok) * a.G - t.row0 - col0;
+          }
+          if (wide) {
+            tc_wide_scores<D, NC>(a, t.c.b, t.h, t.row0, rows, t.at + tok, col0, HC, factor - col0, s_at);
+            tc_fence_before();
+          }
+        }
+      }
+#pragma unroll
+      for (int c0 = 0; c0 < HC; c0 += CH) {
+        // which of the rows do not see this thread's token
+        uint32_t hide = 0u;
+        if (TC_RARE(some)) {
+          hide = tc_hidden<CH>(t.kind == TC_FRESH && a.masks, seen + c0, open - c0);
+          if (tok >= t.left) hide = ~0u;
+        }
+        const bool hides = some && __any_sync(0xffffffffu, hide != 0u);
+        float y[CH];
+        for (bool again = false;; again = true) {
+          tc_ld<CH>(s_at + c0, y);
+          float m = 0.f;
+          if (TC_RARE(common == 0.f)) {
+#pragma unroll
+            for (int i = 0; i < CH; ++i) y[i] *= factor[c0 + i];
+          }
+          // (one factor for all rows: a value for each row and tile less to read, where
+          // the bandwidth of shared memory is what bounds a tile of many rows)
+#pragma unroll
+          for (int i = 0; i < CH; i += 4) {
+            const float4 s = *reinterpret_cast<const float4*>(shift + c0 + i);
+            f2_unpack(f2_fma(f2_pack(y[i], y[i + 1]), common2, f2_pack(s.x, s.y)), y[i], y[i + 1]);
+            f2_unpack(f2_fma(f2_pack(y[i + 2], y[i + 3]), common2, f2_pack(s.z, s.w)), y[i + 2], y[i + 3]);
+          }
+          if (TC_RARE(hides)) {
+#pragma unroll
+            for (int i = 0; i < CH; ++i)
+              if ((hide >> i) & 1u) y[i] = kNegInf;
+          }
+#pragma unroll
+          for (int i = 0; i < CH; i += 2) m = fmax3_nan(m, y[i], y[i + 1]);
+          // (a row without a reference: a score that counts is infinite there)
+          if (__builtin_expect(again || !tc_any<128>(id, !(m <= AT_PSHIFT + AT_ABOVE)), 1)) break;
+          if (!t.first) alive = tc_wait(&bar->pvdone[(n - 1) & 1], ((n - 1) >> 1) & 1, bar, limit) && alive;
+          tc_raise<CH, NC>(s_at + c0, o_at + c0, factor + c0, shift + c0, corr + c0, top + c0, hide, !t.first, quad, id);
+#pragma unroll
+          for (int i = 0; i < CH; i += 2) {
+            float l0, l1;
+            f2_unpack(l[(c0 + i) / 2], l0, l1);
+            l[(c0 + i) / 2] = f2_pack(l0 * corr[c0 + i], l1 * corr[c0 + i + 1]);
+          }
+        }
+        if (c0 + CH == HC) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar->sfree[x]);   // the scores have been read
+        }
+#pragma unroll
+        for (int i = 0; i < CH; i += 2) {
+          y[i] = ex2_approx(y[i]);
+          y[i + 1] = ex2_approx(y[i + 1]);
+          l[(c0 + i) / 2] = f2_add(l[(c0 + i) / 2], f2_pack(y[i], y[i + 1]));
+        }
+        if (TC_RARE(wide)) {   // weights for the values out of range, -1 where the row does not see the node
+          float* w = cta_ws + 2 * static_cast<size_t>(NC) * (D + 4) + static_cast<size_t>(tok) * NC + col0 + c0;
+#pragma unroll
+          for (int i = 0; i < CH; ++i) __stcg(w + i, (hide >> i) & 1u ? -1.f : y[i]);
+        }
+        if (c0 == 0 && n >= 2) alive = tc_wait(&bar->pvdone[x], ((n >> 1) & 1) ^ 1, bar, limit) && alive;
+        unsigned char* pb = tc_smem + L::p + x * L::p_bytes + tok * 16 + (col0 + c0) / 8 * 2048;
+#pragma unroll
+        for (int i = 0; i < CH; i += 8)
+          *reinterpret_cast<uint4*>(pb + i / 8 * 2048) = make_uint4(f16x2_pack(y[i], y[i + 1]), f16x2_pack(y[i + 2], y[i + 3]),
+                                                                    f16x2_pack(y[i + 4], y[i + 5]), f16x2_pack(y[i + 6], y[i + 7]));
+      }
+      tc_fence_before();
+      tc_proxy_fence();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar->pready[x]);
+      if (TC_RARE(wide)) {
+        named_bar_sync(id, 128);   // the weights are written
+        alive = tc_wait(&bar->pvdone[x], (n >> 1) & 1, bar, limit) && alive;
+        tc_fence_after();
+        tc_wide_values<D, NC>(a, t.c.b, t.h, t.at, t.left, tok, col0, HC, cta_ws + 2 * static_cast<size_t>(NC) * (D + 4), o_at);
+        tc_fence_before();
+      }
+      if (TC_RARE(t.last)) {
+        alive = tc_wait(&bar->pvdone[x], (n >> 1) & 1, bar, limit) && alive;
+        float z[HC];
+#pragma unroll
+        for (int i = 0; i < HC / 2; ++i) f2_unpack(l[i], z[2 * i], z[2 * i + 1]);
+        tc_finish<D, NC>(a, t.c.b, t.h, t.row0, rows, itri == 0 && t.c.i + 1 == t.c.units,
+                         cta_ws + (itri == 0 ? static_cast<size_t>(NC) * (D + 4) : 0), z, shift, corr, top,
+                         reinterpret_cast<long long*>(tc_smem + L::rows) + col0, o_at, part);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bar->ofree[tri & 1]);
+        ++tri;
+        named_bar_sync(id, 128);   // top, corr and shift are free again
+      }
+      ++n;
+      if (++u >= ntiles) break;
+      tc_step<NC>(a, prefix, HR, nfresh, ntiles - u, t);
+    }
+  }
+  __syncthreads();
+  if (*reinterpret_cast<volatile int*>(&bar->dead)) {
+    // a wait ran out of time: every triple of the share is void
+    TcTile t;
+    tc_begin<NC>(a, prefix, HR, nfresh, u0, ntiles, t);
+    int i0 = t.c.i;
+    for (int u = 0;;) {
+      if (t.first) i0 = t.c.i;
+      if (t.last) {
+        const bool whole = i0 == 0 && t.c.i + 1 == t.c.units;
+        float* part = cta_ws + (i0 == 0 ? static_cast<size_t>(NC) * (D + 4) : 0);
+        for (int e = threadIdx.x; e < NC * D; e += L::THREADS) {
+          const int r = e / D, d = e - r * D;
+          if (!whole) {
+            part[e] = 0.f;
+            if (d < 3) part[static_cast<size_t>(NC) * D + d * NC + r] = d == 0 ? 0.f : __int_as_float(0x7fc00000);
+          } else if (t.row0 + r < rows) {
+            const long long at = at_row(a, t.c.b, t.h, t.row0 + r);
+            a.out[at * D + d] = 0x7fc0u;
+            if (a.lse && d == 0) a.lse[at] = __int_as_float(0x7fc00000);
+          }
+        }
+      }
+      if (++u >= ntiles) break;
+      tc_step<NC>(a, prefix, HR, nfresh, ntiles - u, t);
+    }
+  }
+  if (warp == L::SOFT + L::UNPACK)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(L::t_cols) : "memory");
+}
+
+}  // namespace sv

@@ -10,6 +10,7 @@
 
 #include "adjust.cuh"
 #include "attend_q4.cuh"
+#include "attend_q4_tc.cuh"
 #include "common.cuh"
 #include "host.cuh"
 #include "kv_q4.cuh"
@@ -49,6 +50,23 @@ void attend_tiles(int rows, int& tiles, int& NR) {
 }
 constexpr int kMaxSms = 160;   // bound of the workspace size; the grid never exceeds it
 
+// Joins what the CTAs' shares cut.  Few triples: each is spread over many CTAs,
+// and a CTA joins eight rows of one; else a warp does.
+template <int D>
+spec_status_t launch_join(const DevInfo& di, const AttendArgs& a, int grid, int shares, int R8, size_t stride, cudaStream_t st) {
+  const long long triples = static_cast<long long>(a.B) * a.Hkv * a.row_tiles, items = triples * R8;
+  const size_t smem = 8 * (static_cast<size_t>(a.B) + 1);
+  if (items > 0x7fffffffLL) return fail(SPEC_ERR_UNSUPPORTED, "batch too large for one call");
+  if (triples * 4 <= grid) {
+    attend_q4_join_kernel<D, true><<<static_cast<unsigned>(items), ATJ_THREADS, smem, st>>>(a, grid, shares, R8, stride);
+  } else {
+    const int jgrid = static_cast<int>(std::min<long long>((items + ATJ_WARPS - 1) / ATJ_WARPS, static_cast<long long>(di.sms) * 4));
+    attend_q4_join_kernel<D, false><<<jgrid, ATJ_THREADS, smem, st>>>(a, grid, shares, R8, stride);
+  }
+  cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? SPEC_OK : cuda_fail(e, "attention join launch");
+}
+
 template <int D, int NR>
 spec_status_t launch_attend(const DevInfo& di, int dev, const AttendArgs& a, cudaStream_t st) {
   auto kern = attend_q4_kernel<D, NR>;
@@ -71,20 +89,7 @@ spec_status_t launch_attend(const DevInfo& di, int dev, const AttendArgs& a, cud
   kern<<<grid, AT_THREADS, smem, st>>>(a, stages);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "attention launch");
-  // Few triples: each is spread over many CTAs, and a CTA joins eight rows of
-  // one; else a warp does.
-  const long long items = static_cast<long long>(a.B) * a.Hkv * a.row_tiles * NR;
-  const size_t jsmem = 8 * (static_cast<size_t>(a.B) + 1);
-  if (items > 0x7fffffffLL) return fail(SPEC_ERR_UNSUPPORTED, "batch too large for one call");
-  if (static_cast<long long>(a.B) * a.Hkv * a.row_tiles * 4 <= grid) {
-    attend_q4_join_kernel<D, NR, true><<<static_cast<unsigned>(items), ATJ_THREADS, jsmem, st>>>(a, grid);
-  } else {
-    const int jgrid = static_cast<int>(std::min<long long>((items + ATJ_WARPS - 1) / ATJ_WARPS, static_cast<long long>(di.sms) * 4));
-    attend_q4_join_kernel<D, NR, false><<<jgrid, ATJ_THREADS, jsmem, st>>>(a, grid);
-  }
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return cuda_fail(e, "attention join launch");
-  return SPEC_OK;
+  return launch_join<D>(di, a, grid, AT_PAIRS, NR, at_cta_floats(D, NR), st);
 }
 
 template <int D>
@@ -95,6 +100,89 @@ spec_status_t launch_attend(int NR, const DevInfo& di, int dev, const AttendArgs
     case 3: return launch_attend<D, 3>(di, dev, a, st);
     default: return launch_attend<D, 4>(di, dev, a, st);
   }
+}
+
+// ---------------------------------------------------------------------------
+// attention on the tcgen05 tensor cores
+// ---------------------------------------------------------------------------
+using TensorMapEncode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                     const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                     CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+TensorMapEncode tensor_map_encode() {
+  static TensorMapEncode fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    cudaGetLastError();
+    return reinterpret_cast<TensorMapEncode>(p);
+  }();
+  return fn;
+}
+
+template <int D, int NC>
+spec_status_t launch_attend_tc(const DevInfo& di, int dev, const AttendArgs& a, cudaStream_t st) {
+  auto kern = attend_q4_tc_kernel<D, NC>;
+  TensorMapEncode encode = tensor_map_encode();
+  if (!encode) return fail(SPEC_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  // the cache as blocks of 72 rows of D / 2 bytes (32 of keys, 32 of values, 8 of scales)
+  CUtensorMap map;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D / 2), 72,
+                              static_cast<cuuint64_t>(a.pages) * a.Hkv * (a.P / Q4_BLOCK)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D / 2), static_cast<cuuint64_t>(q4_block_bytes(D))};
+  const cuuint32_t box[3] = {D / 2, 72, 1}, step[3] = {1, 1, 1};
+  const CUresult r = encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<unsigned char*>(a.cache), dims, strides, box, step,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(SPEC_ERR_CUDA, "cuTensorMapEncodeTiled: %d", static_cast<int>(r));
+  if (!once_per_device(dev, [&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerSm - 1024) == cudaSuccess;
+      }))
+    return fail(SPEC_ERR_CUDA, "attention kernel setup failed: %s", cudaGetErrorString(cudaGetLastError()));
+  const int grid = std::min(di.sms, kMaxSms);
+  kern<<<grid, TcLayout<D, NC>::THREADS, TcLayout<D, NC>::bytes + 1024 + 8 * (static_cast<size_t>(a.B) + 1), st>>>(a, map);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return cuda_fail(e, "attention launch");
+  return launch_join<D>(di, a, grid, 1, NC / 8, tc_cta_floats(D, NC), st);
+}
+
+template <int D>
+spec_status_t launch_attend_tc(int NC, const DevInfo& di, int dev, const AttendArgs& a, cudaStream_t st) {
+  switch (NC) {
+    case 16: return launch_attend_tc<D, 16>(di, dev, a, st);
+    case 32: return launch_attend_tc<D, 32>(di, dev, a, st);
+    case 64: return launch_attend_tc<D, 64>(di, dev, a, st);
+    default: return launch_attend_tc<D, 128>(di, dev, a, st);
+  }
+}
+template <int D>
+size_t tc_smem_bytes(int NC) {
+  return NC == 16 ? TcLayout<D, 16>::bytes : NC == 32 ? TcLayout<D, 32>::bytes : NC == 64 ? TcLayout<D, 64>::bytes : TcLayout<D, 128>::bytes;
+}
+
+// Which kernel, and its row tile.
+struct AttendPlan {
+  bool tc;
+  int tiles;      // row tiles of a (sequence, head)
+  int size;       // NR of attend_q4_kernel (rows / 8 of a tile), NC of attend_q4_tc_kernel
+  size_t floats;  // of the workspace
+};
+constexpr int kTcRows = 33;   // rows from which the tensor cores' kernel is taken: 32 rows 645 us against 700, 128 rows see the header
+AttendPlan attend_plan(int B, int rows, int D) {
+  AttendPlan p{};
+  const int NC = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+  const size_t smem = (D == 128 ? tc_smem_bytes<128>(NC) : tc_smem_bytes<64>(NC)) + 1024 + 8 * (static_cast<size_t>(B) + 1);
+  p.tc = rows >= kTcRows && smem + 256 <= static_cast<size_t>(kSmemPerSm);
+  if (p.tc) {
+    p.size = NC;
+    p.tiles = ceil_div(rows, NC);
+    p.floats = static_cast<size_t>(kMaxSms) * tc_cta_floats(D, NC);
+  } else {
+    attend_tiles(rows, p.tiles, p.size);
+    p.floats = static_cast<size_t>(kMaxSms) * at_ctas(p.size) * at_cta_floats(D, p.size);
+  }
+  return p;
 }
 
 // ---------------------------------------------------------------------------
@@ -276,9 +364,7 @@ size_t spec_attend_workspace_bytes(int B, int N, int Hq, int Hkv, int D) {
   if (B < 0 || B > AT_MAX_B || N < 1 || N > SPEC_MAX_TREE_NODES || Hkv < 1 || Hq < 1 || Hq % Hkv != 0 ||
       Hq / Hkv > 64 || !q4_dim(D))
     return 0;
-  int tiles, NR;
-  attend_tiles(N * (Hq / Hkv), tiles, NR);
-  return align_up(static_cast<size_t>(kMaxSms) * at_ctas(NR) * at_cta_floats(D, NR) * sizeof(float), 256);
+  return align_up(attend_plan(B, N * (Hq / Hkv), D).floats * sizeof(float), 256);
 }
 
 spec_status_t spec_attend_q4(const void* q, const void* k_new, const void* v_new, const uint32_t* masks,
@@ -324,8 +410,10 @@ spec_status_t spec_attend_q4(const void* q, const void* k_new, const void* v_new
     a.pages = num_pages;
     a.W = max_pages;
     a.NW = (N + 31) / 32;
-    int NR;
-    attend_tiles(N * a.G, a.row_tiles, NR);
+    const AttendPlan plan = attend_plan(B, N * a.G, D);
+    a.row_tiles = plan.tiles;
+    a.tile = plan.tc ? TC_TILE : AT_TILE;
+    a.fresh = plan.tc ? 1 : AT_FRESH;
     a.scale_log2 = static_cast<float>(1.4426950408889634 * static_cast<double>(scale));
     a.k_mul = std::ldexp(1.f, k_shift);
     a.v_mul = std::ldexp(1.f, v_shift);
@@ -335,7 +423,8 @@ spec_status_t spec_attend_q4(const void* q, const void* k_new, const void* v_new
     a.timeout_ns = kWaitNs;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     prof_mark(0, st);
-    s = D == 128 ? launch_attend<128>(NR, di, dev, a, st) : launch_attend<64>(NR, di, dev, a, st);
+    if (plan.tc) s = D == 128 ? launch_attend_tc<128>(plan.size, di, dev, a, st) : launch_attend_tc<64>(plan.size, di, dev, a, st);
+    else s = D == 128 ? launch_attend<128>(plan.size, di, dev, a, st) : launch_attend<64>(plan.size, di, dev, a, st);
     if (s != SPEC_OK) return s;
     prof_mark(1, st);
     prof_mark(2, st);
