@@ -369,95 +369,6 @@ struct AtPair {
   __device__ __forceinline__ void sync() const { named_bar_sync(id, 64); }
 };
 
-// The weights of the warp's block.  z (products, -inf where masked;
-// [.][.][e + 2 f]: token g + 8 f of row e) becomes 2^(z c - ref + 7); the
-// operands of both warps' blocks come back in `mine` and `other` ([step][j][half
-// of it]).  The exchange area has two buffers, taken in turn: with one barrier a
-// tile, what a warp writes for a tile was last read two barriers before.
-template <int D, int NR>
-__device__ __forceinline__ void at_weights(float (&z)[2][NR][4], uint2 (&mine)[2][NR], uint2 (&other)[2][NR], int buf,
-                                           const float (&c)[NR][2], const AtPair<D, NR>& pr, AtState<D, NR>& st) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  bool above = false;
-#pragma unroll
-  for (int j = 0; j < NR; ++j)
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-      above |= fmaxf(fmaxf(z[0][j][e], z[0][j][e + 2]), fmaxf(z[1][j][e], z[1][j][e + 2])) * c[j][e] > st.ref[j][e] + AT_ABOVE;
-  above = __any_sync(0xffffffffu, above);
-  auto weigh = [&] {
-#pragma unroll
-    for (int j = 0; j < NR; ++j)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float r = AT_PSHIFT - (st.ref[j][e] == kNegInf ? 0.f : st.ref[j][e]);
-#pragma unroll
-        for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-          for (int f = 0; f < 2; ++f) z[mt][j][e + 2 * f] = ex2_approx(__fmaf_rn(z[mt][j][e + 2 * f], c[j][e], r));
-      }
-  };
-  auto pack = [&] {
-    uint2* out = pr.p(buf, pr.x) + lane;
-#pragma unroll
-    for (int s = 0; s < 2; ++s)
-#pragma unroll
-      for (int j = 0; j < NR; ++j) {
-        mine[s][j] = make_uint2(transpose8(f16x2_pack(z[s][j][0], z[s][j][1])), transpose8(f16x2_pack(z[s][j][2], z[s][j][3])));
-        out[(s * NR + j) * 32] = mine[s][j];
-      }
-  };
-  if (!above) {
-    weigh();
-    pack();
-  } else {
-#pragma unroll
-    for (int j = 0; j < NR; ++j)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float m = fmaxf(fmaxf(z[0][j][e], z[0][j][e + 2]), fmaxf(z[1][j][e], z[1][j][e + 2]));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
-        if (g == 0) pr.top(buf, pr.x)[8 * j + 2 * t + e] = m * c[j][e];
-      }
-  }
-  if (lane == 0) *pr.flag(buf, pr.x) = above;
-  pr.sync();
-  const bool above2 = *pr.flag(buf, pr.x ^ 1);
-  if (above || above2) {   // the pair agrees on new references
-#pragma unroll
-    for (int j = 0; j < NR; ++j)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float to = st.ref[j][e];
-        const float old = to;
-        if (above) to = fmaxf(to, pr.top(buf, pr.x)[8 * j + 2 * t + e]);
-        if (above2) to = fmaxf(to, pr.top(buf, pr.x ^ 1)[8 * j + 2 * t + e]);
-        st.raise(j, e, to);
-        if (!above) {
-          const float f = to == kNegInf ? 1.f : at_corr(old - to);
-#pragma unroll
-          for (int mt = 0; mt < 2; ++mt)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) z[mt][j][e + 2 * k] *= f;
-        }
-      }
-    if (above) weigh();
-    pack();
-    pr.sync();
-  }
-#pragma unroll
-  for (int j = 0; j < NR; ++j)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) st.l[j][e] += (z[0][j][e] + z[0][j][e + 2]) + (z[1][j][e] + z[1][j][e + 2]);
-  const uint2* in = pr.p(buf, pr.x ^ 1) + lane;
-#pragma unroll
-  for (int s = 0; s < 2; ++s)
-#pragma unroll
-    for (int j = 0; j < NR; ++j) other[s][j] = in[(s * NR + j) * 32];
-}
-
 // Queries of a row tile: the f16 operand into `qf` (the same lanes of both warps
 // read what one of them wrote), the rows' factors from f16 products to the log2
 // domain into c.
@@ -509,8 +420,8 @@ __device__ __forceinline__ void at_load_q(const AttendArgs& a, int b, int h, int
 }
 
 // The codes of one product step of v (16 tokens), widened and scaled: w[k] the
-// lane's codes of tokens 2t, 2t+1 of the two groups of eight, `BYTES` bytes of
-// them from byte 0; sc their scale bytes.
+// lane's codes of tokens 2t, 2t+1 of the two groups of eight, BYTES bytes of them
+// from byte `from`; s01, s23 their scales.
 template <int BYTES, int NR, int MT>
 __device__ __forceinline__ void at_add_v(const uint32_t (&w)[4], int from, uint32_t s01, uint32_t s23, const uint2 (&p)[NR],
                                          float (&o)[NR][MT][4]) {
@@ -528,21 +439,65 @@ __device__ __forceinline__ void at_add_v(const uint32_t (&w)[4], int from, uint3
   }
 }
 
-// A cached tile: `left` tokens of it (1..64) belong to the sequence.
-// `after` runs once both warps are done with the tile before.
+// New references for the pair, where a score of the tile lies too far above one.
+// mx: the lane's largest products of the warp's block.
+template <int D, int NR>
+__device__ __noinline__ void at_agree(const AtPair<D, NR>& pr, int buf, const float* mx, const float* c, const float* ref, float* to) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+  for (int i = 0; i < 2 * NR; ++i) {
+    float m = mx[i];
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+    if (g == 0) pr.top(buf, pr.x)[8 * (i >> 1) + 2 * t + (i & 1)] = m * c[i];
+  }
+  pr.sync();
+#pragma unroll
+  for (int i = 0; i < 2 * NR; ++i) {
+    const int r = 8 * (i >> 1) + 2 * t + (i & 1);
+    to[i] = fmaxf(ref[i], fmaxf(pr.top(buf, 0)[r], pr.top(buf, 1)[r]));
+  }
+  pr.sync();   // the maxima have been read, and what follows is written anew
+}
+
+// A cached tile: `left` tokens of it (1..64) belong to the sequence.  `after` runs
+// once both warps are done with the tile before.
+//
+// Both halves of the work are loops over 16 tokens that are not unrolled: the code
+// of a tile then is about 5 KB, which a warp gets through at about the rate of its
+// scheduler.  (Unrolled it was 15 KB, and a warp of the three or four on a scheduler
+// took 2.7 to 3.3 clocks an instruction to fetch: BEFORE_US where this takes
+// AFTER_US.)  So the weights are taken at once against the references as they are,
+// and only then the warps look whether a score was too far above one; if so, they
+// agree on new references and score the tile again.
+//
+// (The exchange area has two buffers, taken in turn: with one barrier a tile, what a
+// warp writes for a tile was last read two barriers before.)
 template <int D, int NR, class F>
 __device__ __forceinline__ void at_cached_tile(const unsigned char* tile, int left, int buf, const float (&c)[NR][2],
                                                const AtPair<D, NR>& pr, AtState<D, NR>& st, F&& after) {
   constexpr int WK = D / 32;   // words of a key chunk
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int tr = at_token(g);
-  float z[2][NR][4];
   const int own = left - pr.x * Q4_BLOCK;   // tokens of the warp's block
-  if (own > 0) {
-    const unsigned char* sb = tile + pr.x * q4_block_bytes(D);
-    const uint4* qf = pr.q() + lane;
+  const unsigned char* sb = tile + pr.x * q4_block_bytes(D);
+  const uint4* qf = pr.q() + lane;
+  uint2* out = pr.p(buf, pr.x) + lane;
+  float lt[NR][2];
+  for (;;) {
+    float mx[NR][2], r[NR][2];
 #pragma unroll
+    for (int j = 0; j < NR; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        lt[j][e] = 0.f;
+        mx[j][e] = kNegInf;
+        r[j][e] = AT_PSHIFT - (st.ref[j][e] == kNegInf ? 0.f : st.ref[j][e]);
+      }
+#pragma unroll 1
     for (int mt = 0; mt < 2; ++mt) {
+      float z[NR][4];
       uint32_t kw[2][WK];
       uint32_t ks2[2][D / 64];   // the chunk's scales, each twice
 #pragma unroll
@@ -575,65 +530,98 @@ __device__ __forceinline__ void at_cached_tile(const unsigned char* tile, int le
 #pragma unroll
         for (int j = 0; j < NR; ++j) {
           const uint4 qb = qf[(j * WK + w) * 32];
-          if (w == 0) mma_f16_zero(z[mt][j], k0, qb.x, qb.y);
-          else mma_f16(z[mt][j], k0, qb.x, qb.y);
-          mma_f16(z[mt][j], k1, qb.z, qb.w);
+          if (w == 0) mma_f16_zero(z[j], k0, qb.x, qb.y);
+          else mma_f16(z[j], k0, qb.x, qb.y);
+          mma_f16(z[j], k1, qb.z, qb.w);
         }
       }
-    }
-  }
-  if (own < Q4_BLOCK) {
+      if (own < 16 * mt + 16) {   // the sequence ends here (what the stage holds behind it may be anything)
 #pragma unroll
-    for (int mt = 0; mt < 2; ++mt)
+        for (int f = 0; f < 2; ++f)
+          if (16 * mt + 8 * f + tr >= own) {
 #pragma unroll
-      for (int f = 0; f < 2; ++f)
-        if (16 * mt + 8 * f + tr >= own) {
+            for (int j = 0; j < NR; ++j) z[j][2 * f] = z[j][2 * f + 1] = kNegInf;
+          }
+      }
 #pragma unroll
-          for (int j = 0; j < NR; ++j) z[mt][j][2 * f] = z[mt][j][2 * f + 1] = kNegInf;
+      for (int j = 0; j < NR; ++j) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          mx[j][e] = fmaxf(mx[j][e], fmaxf(z[j][e], z[j][e + 2]));
+          z[j][e] = ex2_approx(__fmaf_rn(z[j][e], c[j][e], r[j][e]));
+          z[j][e + 2] = ex2_approx(__fmaf_rn(z[j][e + 2], c[j][e], r[j][e]));
+          lt[j][e] += z[j][e] + z[j][e + 2];
         }
+        out[(mt * NR + j) * 32] = make_uint2(transpose8(f16x2_pack(z[j][0], z[j][1])), transpose8(f16x2_pack(z[j][2], z[j][3])));
+      }
+    }
+    bool above = false;
+#pragma unroll
+    for (int j = 0; j < NR; ++j)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) above |= mx[j][e] * c[j][e] > st.ref[j][e] + AT_ABOVE;
+    above = __any_sync(0xffffffffu, above);
+    if (lane == 0) *pr.flag(buf, pr.x) = above;
+    pr.sync();
+    if (__builtin_expect(!above && !*pr.flag(buf, pr.x ^ 1), 1)) break;
+    float m2[2 * NR], c2[2 * NR], ref[2 * NR], to[2 * NR];   // (copies: the state stays in registers)
+#pragma unroll
+    for (int i = 0; i < 2 * NR; ++i) {
+      m2[i] = mx[i >> 1][i & 1];
+      c2[i] = c[i >> 1][i & 1];
+      ref[i] = st.ref[i >> 1][i & 1];
+    }
+    at_agree<D, NR>(pr, buf, m2, c2, ref, to);
+#pragma unroll
+    for (int i = 0; i < 2 * NR; ++i) st.raise(i >> 1, i & 1, to[i]);
   }
-  uint2 p[2][2][NR];   // [own block / other][step]
-  at_weights<D, NR>(z, p[0], p[1], buf, c, pr, st);
+#pragma unroll
+  for (int j = 0; j < NR; ++j)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) st.l[j][e] += lt[j][e];
   after();
 
-#pragma unroll
-  for (int y = 0; y < 2; ++y) {
-    const int blk = pr.x ^ y;
+  // v: steps of 16 tokens (D = 128), or of 32 (D = 64, whose codes of two steps make a word)
+  constexpr int STEPS = D == 128 ? 4 : 2, S = 4 / STEPS;
+#pragma unroll 1
+  for (int y = 0; y < STEPS; ++y) {
+    const int blk = y / (STEPS / 2), s0 = D == 128 ? y & 1 : 0;
     const int have = left - blk * Q4_BLOCK;   // tokens of that block
-    if (have <= 0) continue;
-    const unsigned char* sb = tile + blk * q4_block_bytes(D);
-    uint32_t w[2][4], sc[2][4];
+    if (have <= 16 * s0) break;
+    const unsigned char* vb = tile + blk * q4_block_bytes(D);
+    const uint2* in = pr.p(buf, blk) + lane;
+    uint2 p[S][NR];
+    uint32_t w[S][4], sc[S][4];
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
+    for (int s = 0; s < S; ++s) {
+#pragma unroll
+      for (int j = 0; j < NR; ++j) p[s][j] = in[((s0 + s) * NR + j) * 32];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int tok = 16 * s + 8 * (k >> 1) + at_token(2 * t + (k & 1));
+        const int tok = 16 * (s0 + s) + 8 * (k >> 1) + at_token(2 * t + (k & 1));
         if constexpr (D == 128) {
-          w[s][k] = *reinterpret_cast<const uint32_t*>(sb + 16 * D + tok * 64 + pr.x * 32 + g * 4);
-          sc[s][k] = sb[34 * D + tok * 8 + pr.x * 4 + (g >> 1)];
+          w[s][k] = *reinterpret_cast<const uint32_t*>(vb + 16 * D + tok * 64 + pr.x * 32 + g * 4);
+          sc[s][k] = vb[34 * D + tok * 8 + pr.x * 4 + (g >> 1)];
         } else {
-          w[s][k] = *reinterpret_cast<const uint16_t*>(sb + 16 * D + tok * 32 + pr.x * 16 + g * 2);
-          sc[s][k] = sb[34 * D + tok * 4 + pr.x * 2 + (g >> 2)];
+          w[s][k] = *reinterpret_cast<const uint16_t*>(vb + 16 * D + tok * 32 + pr.x * 16 + g * 2);
+          sc[s][k] = vb[34 * D + tok * 4 + pr.x * 2 + (g >> 2)];
         }
       }
-    if (have < Q4_BLOCK) {   // what lies behind the last token may be a NaN
-#pragma unroll
-      for (int s = 0; s < 2; ++s)
+      if (have < 16 * (s0 + s) + 16) {   // what lies behind the last token may be a NaN
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          if (16 * s + 8 * (k >> 1) + at_token(2 * t + (k & 1)) >= have) sc[s][k] = 0u;
+          if (16 * (s0 + s) + 8 * (k >> 1) + at_token(2 * t + (k & 1)) >= have) sc[s][k] = 0u;
+      }
     }
-    const uint32_t a01 = e4m3x2_to_f16(sc[0][0] + sc[0][1] * 256u), a23 = e4m3x2_to_f16(sc[0][2] + sc[0][3] * 256u);
-    const uint32_t b01 = e4m3x2_to_f16(sc[1][0] + sc[1][1] * 256u), b23 = e4m3x2_to_f16(sc[1][2] + sc[1][3] * 256u);
     if constexpr (D == 128) {
-      at_add_v<4, NR>(w[0], 0, a01, a23, p[y][0], st.o);
-      at_add_v<4, NR>(w[1], 0, b01, b23, p[y][1], st.o);
+      at_add_v<4, NR>(w[0], 0, e4m3x2_to_f16(sc[0][0] + sc[0][1] * 256u), e4m3x2_to_f16(sc[0][2] + sc[0][3] * 256u), p[0], st.o);
     } else {
       uint32_t both[4];   // the codes of both steps, widened at once
 #pragma unroll
-      for (int k = 0; k < 4; ++k) both[k] = w[0][k] + w[1][k] * 65536u;
-      at_add_v<2, NR>(both, 0, a01, a23, p[y][0], st.o);
-      at_add_v<2, NR>(both, 2, b01, b23, p[y][1], st.o);
+      for (int k = 0; k < 4; ++k) both[k] = w[0][k] + w[S - 1][k] * 65536u;
+#pragma unroll
+      for (int s = 0; s < S; ++s)
+        at_add_v<2, NR>(both, 2 * s, e4m3x2_to_f16(sc[s][0] + sc[s][1] * 256u), e4m3x2_to_f16(sc[s][2] + sc[s][3] * 256u), p[s], st.o);
     }
   }
 }

@@ -476,22 +476,23 @@ spec_status_t spec_adjust_logits(const void* logits, spec_dtype_t dtype, const i
     a.B = B;
     a.R = R;
     a.V = V;
-    a.H = H;
+    a.H = a.history ? H : 0;
     a.Nt = Nt;
     a.NW = (R + 31) / 32;
     a.M = M;
     a.VW = (V + 31) / 32;
-    const bool vec = aligned16(logits) && aligned16(out) && (static_cast<long long>(V) * esz) % 16 == 0;
-    // Chunks as large as shared memory likes (a chunk counts the whole history),
-    // smaller ones where the batch alone does not give every SM two CTAs; then
-    // the rows are shared out.
+    const bool vec = ((reinterpret_cast<uintptr_t>(logits) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
+    // Chunks as large as shared memory likes (a CTA counts the whole history),
+    // smaller ones where the batch alone does not give every SM two CTAs; and the
+    // rows shared out, four a CTA at least, to eight CTAs an SM.
     const long long want = 2LL * di.sms;
     a.chunk = AJ_MAX_CHUNK;
-    while (a.chunk > 2048 && static_cast<long long>(B) * ceil_div(V, a.chunk) < want) a.chunk /= 2;
+    while (a.chunk > 1024 && static_cast<long long>(B) * ceil_div(V, a.chunk) < want) a.chunk /= 2;
     while (a.chunk > 32 && a.chunk / 2 >= V) a.chunk /= 2;
     a.chunks = ceil_div(V, a.chunk);
     const long long ctas = static_cast<long long>(B) * a.chunks;
-    a.row_splits = static_cast<int>(std::max<long long>(1, std::min<long long>(R, want / std::max<long long>(1, ctas))));
+    a.row_splits = static_cast<int>(std::max<long long>(
+        1, std::min<long long>(ceil_div(R, 4), (4 * want + ctas - 1) / std::max<long long>(1, ctas))));
     if (ctas * a.row_splits > 0x7fffffffLL) return fail(SPEC_ERR_UNSUPPORTED, "grid too large");
     const unsigned grid = static_cast<unsigned>(ctas * a.row_splits);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
