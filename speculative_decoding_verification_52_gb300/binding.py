@@ -380,42 +380,46 @@ def spec_tree_draft(draft_logits, parents, temperature, max_children: int, *, no
 # with the tensors' device current, and allocate outputs that are not supplied on
 # the stream that the call uses.
 # ---------------------------------------------------------------------------
-def _take(t, name: str, dtype, shape, dev):
-    """A tensor argument: type, shape (None: any size there), device, layout.
-    Its address; None for an argument that is None."""
+def _take(t, name: str, dtype, shape, dev: int):
+    """A tensor argument's address, after a look at its type, shape, device and
+    layout; None for an argument that is None."""
     if t is None:
         return None
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    s = t.shape
-    if len(s) != len(shape) or any(w is not None and w != h for w, h in zip(shape, s)):
-        raise ValueError(f"{name} must have shape {tuple('any' if w is None else w for w in shape)}, got {tuple(s)}")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}, got {t.device}")
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _serve(fn):
-    """Runs a serving call on its tensors' device and the given stream."""
+    """Runs a serving call on its tensors' device and the given stream: fn gets the
+    device's index and the stream's handle."""
     @functools.wraps(fn)
     def call(first, *args, stream=None, **kw):
         if not isinstance(first, torch.Tensor) or not first.is_cuda:
             raise ValueError(f"{fn.__name__}: tensors must be CUDA tensors")
-        dev = first.device
-        if stream is None and dev.index == torch.cuda.current_device():
-            return fn(first, *args, stream=torch._C._cuda_getCurrentRawStream(dev.index), **kw)
-        if stream is not None and stream.device != dev:
-            raise ValueError(f"{fn.__name__}: the stream is on {stream.device}, the tensors on {dev}")
+        dev = first.get_device()
+        if stream is None and dev == torch._C._cuda_getDevice():
+            return fn(first, *args, dev=dev, stream=torch._C._cuda_getCurrentRawStream(dev), **kw)
+        if stream is not None and stream.device.index != dev:
+            raise ValueError(f"{fn.__name__}: the stream is on {stream.device}, the tensors on cuda:{dev}")
         with torch.cuda.device(dev), torch.cuda.stream(stream):
-            return fn(first, *args, stream=torch.cuda.current_stream(dev).cuda_stream, **kw)
+            return fn(first, *args, dev=dev, stream=torch._C._cuda_getCurrentRawStream(dev), **kw)
     return call
 
 
-def _out(t, name: str, dtype, shape, dev):
-    """An output: the one supplied, or a new one."""
-    return t if t is not None else torch.empty(shape, dtype=dtype, device=dev)
+def _cols(t, rows, name):
+    """Shape [rows, any] of a two-dimensional argument."""
+    if t is None:
+        return None
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got {tuple(t.shape)}")
+    return (rows, t.shape[1])
 
 
 def spec_q4_block_bytes(D: int) -> int:
@@ -444,97 +448,112 @@ def _q4_shape(cache, name="cache"):
 @_serve
 def spec_page_map(lengths, count, held, ring, ring_state, block_table, page_tokens: int, max_tokens: int, *,
                   offsets=None, slots=None, positions=None, new_held=None, new_ring_state=None, status=None,
-                  stream=None):
+                  dev=None, stream=None):
     """Block tables and slot maps from the requests' lengths.  lengths, count, held
     [B] int32; ring [F], ring_state [2], block_table [B, W] int32 (ring and table
     updated in place).  Returns (offsets [B+1], slots [max_tokens], positions
-    [max_tokens], new_held [B], new_ring_state [2], status [B]), all int32."""
-    dev, i32 = lengths.device, torch.int32
-    B = lengths.numel()
-    offsets = _out(offsets, "offsets", i32, (B + 1,), dev)
-    slots = _out(slots, "slots", i32, (max_tokens,), dev)
-    positions = _out(positions, "positions", i32, (max_tokens,), dev)
-    new_held = _out(new_held, "new_held", i32, (B,), dev)
-    new_ring_state = _out(new_ring_state, "new_ring_state", i32, (2,), dev)
-    status = _out(status, "status", i32, (B,), dev)
-    st = lib().spec_page_map(
-        _take(lengths, "lengths", i32, (B,), dev), _take(count, "count", i32, (B,), dev), _take(held, "held", i32, (B,), dev),
-        _take(ring, "ring", i32, (None,), dev), _take(ring_state, "ring_state", i32, (2,), dev),
-        _take(block_table, "block_table", i32, (B, None), dev), B, ring.shape[0], page_tokens, block_table.shape[1], max_tokens,
-        _take(offsets, "offsets", i32, (B + 1,), dev), _take(slots, "slots", i32, (max_tokens,), dev),
-        _take(positions, "positions", i32, (max_tokens,), dev), _take(new_held, "new_held", i32, (B,), dev),
-        _take(new_ring_state, "new_ring_state", i32, (2,), dev), _take(status, "status", i32, (B,), dev), stream)
-    _check("spec_page_map", st)
+    [max_tokens], new_held [B], new_ring_state [2], status [B]), all int32; those
+    not supplied are parts of one allocation."""
+    i32, B = torch.int32, lengths.numel()
+    one, T = (B,), (max_tokens,)
+    if offsets is None or slots is None or positions is None or new_held is None or new_ring_state is None or status is None:
+        pad = -max_tokens % 4   # slots and positions start at 16-byte borders
+        new = torch.empty(2 * (max_tokens + pad) + 3 * B + 3, dtype=i32, device=lengths.device).split_with_sizes(
+            (max_tokens, pad, max_tokens, pad, B + 1, B, B, 2))
+        slots = new[0] if slots is None else slots
+        positions = new[2] if positions is None else positions
+        offsets = new[4] if offsets is None else offsets
+        new_held = new[5] if new_held is None else new_held
+        status = new[6] if status is None else status
+        new_ring_state = new[7] if new_ring_state is None else new_ring_state
+    table = _cols(block_table, B, "block_table")
+    st = (_lib or lib()).spec_page_map(
+        _take(lengths, "lengths", i32, one, dev), _take(count, "count", i32, one, dev), _take(held, "held", i32, one, dev),
+        _take(ring, "ring", i32, (ring.numel(),), dev), _take(ring_state, "ring_state", i32, (2,), dev),
+        _take(block_table, "block_table", i32, table, dev), B, ring.numel(), page_tokens, table[1], max_tokens,
+        _take(offsets, "offsets", i32, (B + 1,), dev), _take(slots, "slots", i32, T, dev),
+        _take(positions, "positions", i32, T, dev), _take(new_held, "new_held", i32, one, dev),
+        _take(new_ring_state, "new_ring_state", i32, (2,), dev), _take(status, "status", i32, one, dev), stream)
+    if st:
+        _check("spec_page_map", st)
     return offsets, slots, positions, new_held, new_ring_state, status
 
 
 @_serve
-def spec_kv_store_q4(k, v, slots, cache, *, k_shift: int = 0, v_shift: int = 0, stream=None):
+def spec_kv_store_q4(k, v, slots, cache, *, k_shift: int = 0, v_shift: int = 0, dev=None, stream=None):
     """Entries t of k and v [T, Hkv, D] bf16 into the 4-bit cache at slots[t]
     ([T] int32; a slot outside the cache is skipped).  Returns the cache."""
     pages, Hkv, P, D = _q4_shape(cache)
-    dev, T = k.device, k.shape[0]
-    st = lib().spec_kv_store_q4(
+    T = k.shape[0]
+    st = (_lib or lib()).spec_kv_store_q4(
         _take(k, "k", torch.bfloat16, (T, Hkv, D), dev), _take(v, "v", torch.bfloat16, (T, Hkv, D), dev),
         _take(slots, "slots", torch.int32, (T,), dev), T, Hkv, D, P, pages, k_shift, v_shift,
-        _take(cache, "cache", torch.uint8, (None,) * 4, dev), stream)
-    _check("spec_kv_store_q4", st)
+        _take(cache, "cache", torch.uint8, cache.shape, dev), stream)
+    if st:
+        _check("spec_kv_store_q4", st)
     return cache
 
 
 @_serve
 def spec_kv_commit_q4(cache, block_table, lengths, k, v, count, *, path=None, new_lengths=None, k_shift: int = 0,
-                      v_shift: int = 0, stream=None):
+                      v_shift: int = 0, dev=None, stream=None):
     """Appends accepted entries of k and v [B, N, Hkv, D] bf16 to the paged 4-bit
     cache behind lengths [B]: entries path[b, :count[b]] ([B, W] int32), or the
     first count[b] without a path.  block_table [B, pages].  Returns new_lengths."""
     pages, Hkv, P, D = _q4_shape(cache)
-    dev, i32 = cache.device, torch.int32
-    B, N = k.shape[:2]
-    new_lengths = _out(new_lengths, "new_lengths", i32, (B,), dev)
-    st = lib().spec_kv_commit_q4(
-        _take(cache, "cache", torch.uint8, (None,) * 4, dev), _take(block_table, "block_table", i32, (B, None), dev),
-        _take(lengths, "lengths", i32, (B,), dev), _take(k, "k", torch.bfloat16, (B, N, Hkv, D), dev),
-        _take(v, "v", torch.bfloat16, (B, N, Hkv, D), dev), _take(path, "path", i32, (B, None), dev),
-        _take(count, "count", i32, (B,), dev), B, N, 0 if path is None else path.shape[1], Hkv, D, P, pages,
-        block_table.shape[1], k_shift, v_shift, _take(new_lengths, "new_lengths", i32, (B,), dev), stream)
-    _check("spec_kv_commit_q4", st)
+    i32, bf = torch.int32, torch.bfloat16
+    if k.dim() != 4:
+        raise ValueError(f"k must be [B, N, Hkv, D], got {tuple(k.shape)}")
+    B, N = k.shape[0], k.shape[1]
+    if new_lengths is None:
+        new_lengths = torch.empty((B,), dtype=i32, device=cache.device)
+    table, way = _cols(block_table, B, "block_table"), _cols(path, B, "path")
+    st = (_lib or lib()).spec_kv_commit_q4(
+        _take(cache, "cache", torch.uint8, cache.shape, dev), _take(block_table, "block_table", i32, table, dev),
+        _take(lengths, "lengths", i32, (B,), dev), _take(k, "k", bf, (B, N, Hkv, D), dev), _take(v, "v", bf, (B, N, Hkv, D), dev),
+        _take(path, "path", i32, way, dev), _take(count, "count", i32, (B,), dev), B, N, 0 if path is None else way[1], Hkv, D,
+        P, pages, table[1], k_shift, v_shift, _take(new_lengths, "new_lengths", i32, (B,), dev), stream)
+    if st:
+        _check("spec_kv_commit_q4", st)
     return new_lengths
 
 
 @_serve
 def spec_attend_q4(q, cache, block_table, lengths, *, k_new=None, v_new=None, masks=None, scale=None, k_shift: int = 0,
-                   v_shift: int = 0, out=None, lse=None, workspace_buf=None, stream=None):
+                   v_shift: int = 0, out=None, lse=None, workspace_buf=None, dev=None, stream=None):
     """Attention of N nodes per sequence over the paged 4-bit cache and the nodes'
     own entries.  q [B, N, Hq, D], k_new / v_new [B, N, Hkv, D] bf16 (or neither),
     masks [B, N, ceil(N/32)] int32 (spec_tree_mask's; None: a chain), block_table
     [B, pages], lengths [B] int32; scale defaults to 1 / sqrt(D).  Returns (out
     [B, N, Hq, D] bf16, lse [B, N, Hq] f32)."""
     pages, Hkv, P, D = _q4_shape(cache)
-    dev, i32, bf = q.device, torch.int32, torch.bfloat16
+    i32, bf, f32 = torch.int32, torch.bfloat16, torch.float32
     if q.dim() != 4:
         raise ValueError(f"q must be [B, N, Hq, D], got {tuple(q.shape)}")
-    B, N, Hq = q.shape[:3]
-    out = _out(out, "out", bf, (B, N, Hq, D), dev)
-    lse = _out(lse, "lse", torch.float32, (B, N, Hq), dev)
+    B, N, Hq = q.shape[0], q.shape[1], q.shape[2]
+    if out is None:
+        out = torch.empty((B, N, Hq, D), dtype=bf, device=q.device)
+    if lse is None:
+        lse = torch.empty((B, N, Hq), dtype=f32, device=q.device)
     if workspace_buf is None:
-        workspace_buf = workspace(spec_attend_workspace_bytes(B, N, Hq, Hkv, D), dev)
-    st = lib().spec_attend_q4(
+        workspace_buf = workspace(spec_attend_workspace_bytes(B, N, Hq, Hkv, D), q.device)
+    table = _cols(block_table, B, "block_table")
+    st = (_lib or lib()).spec_attend_q4(
         _take(q, "q", bf, (B, N, Hq, D), dev), _take(k_new, "k_new", bf, (B, N, Hkv, D), dev),
         _take(v_new, "v_new", bf, (B, N, Hkv, D), dev), _take(masks, "masks", i32, (B, N, (N + 31) // 32), dev),
-        _take(cache, "cache", torch.uint8, (None,) * 4, dev), _take(block_table, "block_table", i32, (B, None), dev),
-        _take(lengths, "lengths", i32, (B,), dev), B, N, Hq, Hkv, D, P, pages, block_table.shape[1], k_shift, v_shift,
-        D ** -0.5 if scale is None else scale, _take(out, "out", bf, (B, N, Hq, D), dev),
-        _take(lse, "lse", torch.float32, (B, N, Hq), dev), _take(workspace_buf, "workspace_buf", torch.uint8, (None,), dev),
-        workspace_buf.numel(), stream)
-    _check("spec_attend_q4", st)
+        _take(cache, "cache", torch.uint8, cache.shape, dev), _take(block_table, "block_table", i32, table, dev),
+        _take(lengths, "lengths", i32, (B,), dev), B, N, Hq, Hkv, D, P, pages, table[1], k_shift, v_shift,
+        D ** -0.5 if scale is None else scale, _take(out, "out", bf, (B, N, Hq, D), dev), _take(lse, "lse", f32, (B, N, Hq), dev),
+        _take(workspace_buf, "workspace_buf", torch.uint8, (workspace_buf.numel(),), dev), workspace_buf.numel(), stream)
+    if st:
+        _check("spec_attend_q4", st)
     return out, lse
 
 
 @_serve
 def spec_adjust_logits(logits, *, out=None, history=None, prompt_lengths=None, history_lengths=None, repetition=None,
                        frequency=None, presence=None, node_tokens=None, masks=None, bias_tokens=None,
-                       bias_values=None, allowed=None, stream=None):
+                       bias_values=None, allowed=None, dev=None, stream=None):
     """Penalties, biases and grammar masks on logits [B, R, V] (bf16/f32).  history
     [B, H] int32 with prompt_lengths and history_lengths [B]; repetition,
     frequency, presence [B] f32; node_tokens [B, Nt] int32 (row r sees the first r
@@ -544,20 +563,22 @@ def spec_adjust_logits(logits, *, out=None, history=None, prompt_lengths=None, h
     if logits.dim() != 3:
         raise ValueError(f"logits must be [B, R, V], got {tuple(logits.shape)}")
     B, R, V = logits.shape
-    dev, i32, f32 = logits.device, torch.int32, torch.float32
+    i32, f32, one, shape, dt = torch.int32, torch.float32, (B,), (B, R, V), logits.dtype
     code = _dtype_code(logits)
-    out = _out(out, "out", logits.dtype, (B, R, V), dev)
-    st = lib().spec_adjust_logits(
-        _take(logits, "logits", logits.dtype, (B, R, V), dev), code, _take(history, "history", i32, (B, None), dev),
-        _take(prompt_lengths, "prompt_lengths", i32, (B,), dev), _take(history_lengths, "history_lengths", i32, (B,), dev),
-        _take(repetition, "repetition", f32, (B,), dev), _take(frequency, "frequency", f32, (B,), dev),
-        _take(presence, "presence", f32, (B,), dev), _take(node_tokens, "node_tokens", i32, (B, None), dev),
-        _take(masks, "masks", i32, (B, R, (R + 31) // 32), dev), _take(bias_tokens, "bias_tokens", i32, (B, None), dev),
-        _take(bias_values, "bias_values", f32, (B, None if bias_tokens is None else bias_tokens.shape[1]), dev),
-        _take(allowed, "allowed", i32, (B, R, (V + 31) // 32), dev), B, R, V, 0 if history is None else history.shape[1],
-        0 if node_tokens is None else node_tokens.shape[1], 0 if bias_tokens is None else bias_tokens.shape[1],
-        _take(out, "out", logits.dtype, (B, R, V), dev), stream)
-    _check("spec_adjust_logits", st)
+    if out is None:
+        out = torch.empty(shape, dtype=dt, device=logits.device)
+    past, nodes, biased = _cols(history, B, "history"), _cols(node_tokens, B, "node_tokens"), _cols(bias_tokens, B, "bias_tokens")
+    st = (_lib or lib()).spec_adjust_logits(
+        _take(logits, "logits", dt, shape, dev), code, _take(history, "history", i32, past, dev),
+        _take(prompt_lengths, "prompt_lengths", i32, one, dev), _take(history_lengths, "history_lengths", i32, one, dev),
+        _take(repetition, "repetition", f32, one, dev), _take(frequency, "frequency", f32, one, dev),
+        _take(presence, "presence", f32, one, dev), _take(node_tokens, "node_tokens", i32, nodes, dev),
+        _take(masks, "masks", i32, (B, R, (R + 31) // 32), dev), _take(bias_tokens, "bias_tokens", i32, biased, dev),
+        _take(bias_values, "bias_values", f32, biased or _cols(bias_values, B, "bias_values"), dev),
+        _take(allowed, "allowed", i32, (B, R, (V + 31) // 32), dev), B, R, V, past[1] if past else 0,
+        nodes[1] if nodes else 0, biased[1] if biased else 0, _take(out, "out", dt, shape, dev), stream)
+    if st:
+        _check("spec_adjust_logits", st)
     return out
 
 
