@@ -8,8 +8,9 @@
 //
 // Few rows (this kernel).  The cache is read once and each element takes part
 // in 2 * rows multiply-adds, so up to a few tens of rows the 9/16 byte an
-// element has to cross the HBM bus is the bound, and the work next to it is to
-// unpack the codes: the budget is about three instructions an element.
+// element has to cross the HBM bus is the bound; in that time a
+// scheduler issues about three instructions an element (one row of a warp's lanes),
+// and to unpack the codes takes one.
 //
 // * The unit of work is a tile of 64 tokens: two blocks, each one contiguous run
 //   of 36 * D bytes and one bulk copy.  All tiles of all (sequence, head, row
@@ -17,18 +18,18 @@
 //   every pair of warps takes an equal, contiguous share of it, whatever the
 //   lengths, and fetches it through a ring of its own.  A triple that lies in one
 //   pair's share is finished there.  A fresh tile counts as three: it waits for
-//   its loads, where a cached tile's have arrived (chains of 6 nodes over lengths
-//   of 512 to 3,584: FRESH1_US when it counts as one).  The pairs of a CTA have neighbouring shares
-//   and join what they share at the end; what CTAs share goes through the
-//   workspace (maximum, sum, sum of v) and a second kernel.  All joins are in the
-//   list's order.
+//   its loads, where a cached tile's have arrived (256 sequences of 4 nodes at
+//   2,048 tokens, 16 rows: 269 us when it counts as one, 252 as three).  The pairs
+//   of a CTA have neighbouring shares and join what they share at the end; what
+//   CTAs share goes through the workspace (reference, sum, sum of v) and a second
+//   kernel.  All joins are in the list's order.
 // * In a pair, each warp scores one block; the weights are exchanged, and each
 //   warp adds up one half of v's columns over both blocks.  So every code is
 //   unpacked once for all rows, and the sums of a warp fit its registers beside
 //   the operands (a warp that kept all columns of 24 rows moved 137 registers a
-//   block through local memory: 450 us where this takes CHAIN_US).  One barrier of
-//   the two warps a tile: the weights are taken against a maximum that both know,
-//   2^(z - ref + 7), and only a score above ref + 8 makes them agree on a new one.
+//   block through local memory: 450 us where this took 390).  One barrier of the
+//   two warps a tile: the weights are 2^(z - ref) for a reference that both know,
+//   and only a score above ref + 15 makes them agree on a new one.
 // * Everything is unpacked in f16, exactly: a code times its scale has 6
 //   significant bits.  q enters as f16 too, scaled by a power of two per row so
 //   that its largest element lies in [128, 256): what f16 then cannot hold is
@@ -65,8 +66,11 @@ constexpr int AT_TILE = 2 * Q4_BLOCK;       // tokens of a tile
 constexpr int AT_FRESH = 3;                 // what a fresh tile counts in the list, in cached tiles
 constexpr int AT_QUEUE = 32;                // places of a pair's list of fetches
 constexpr int AT_MAX_B = 4096;
-constexpr float AT_PSHIFT = 7.f;            // a score equal to the reference gets the weight 2^7,
-constexpr float AT_ABOVE = 8.f;             // and one so far above it is the largest that it serves
+// Weights are 2^(score - reference).  A reference is set so that the largest
+// score then known gets the weight 2^7, and serves up to 2^15.
+constexpr float AT_PSHIFT = 7.f;
+constexpr float AT_ABOVE = 8.f;
+constexpr float AT_UNSET = -3.402823466e+38f;   // a reference before any score
 
 struct AttendArgs {
   const uint16_t* q;         // [B, N, Hkv * G, D] bf16
@@ -243,12 +247,11 @@ __host__ __device__ constexpr int at_pair_bytes(int D, int NR) { return at_q_byt
 // CTAs before it and of the one that it shares with those behind:
 //   [8 NR rows x D] sums of v, then m[8 NR], l[8 NR] of the first and the second
 //   half of the columns' warps;
-// a warp has two copies of a state in its lanes' order: what its CTA's other
-// pairs join, and the result of a triple's fresh tiles.
+// a warp has a state in its lanes' order, which its CTA's other pairs join.
 __host__ __device__ constexpr size_t at_partial_floats(int D, int NR) { return static_cast<size_t>(8 * NR) * (D + 4); }
 __host__ __device__ constexpr size_t at_state_floats(int D, int NR) { return static_cast<size_t>(32 * NR) * (D / 8 + 4); }
 __host__ __device__ constexpr size_t at_cta_floats(int D, int NR) {
-  return 2 * at_partial_floats(D, NR) + 4 * AT_PAIRS * at_state_floats(D, NR);
+  return 2 * at_partial_floats(D, NR) + 2 * AT_PAIRS * at_state_floats(D, NR);
 }
 
 __device__ __forceinline__ long long at_row(const AttendArgs& a, int b, int h, int r) {
@@ -265,7 +268,7 @@ template <int D, int NR>
 struct AtState {
   static constexpr int MT = D / 32;   // products that cover the warp's columns
   float o[NR][MT][4];                 // [.][i][e + 2 f]: column 2 i + f of the lane's
-  float ref[NR][2];                   // what the weights are relative to (log2 domain; the pair's)
+  float ref[NR][2];                   // the references (log2 domain; the pair's)
   float l[NR][2];                     // this lane's part of the sum of weights
 
   __device__ __forceinline__ void clear() {
@@ -275,7 +278,7 @@ struct AtState {
       for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int k = 0; k < 4; ++k) o[j][i][k] = 0.f;
-      ref[j][0] = ref[j][1] = kNegInf;
+      ref[j][0] = ref[j][1] = AT_UNSET;
       l[j][0] = l[j][1] = 0.f;
     }
   }
@@ -285,7 +288,7 @@ struct AtState {
   }
   // to a reference of `to` (not below the present one)
   __device__ __forceinline__ void raise(int j, int e, float to) {
-    const float corr = to == kNegInf ? 1.f : at_corr(ref[j][e] - to);
+    const float corr = at_corr(ref[j][e] - to);
     l[j][e] *= corr;
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
@@ -306,19 +309,6 @@ struct AtState {
       q[32 * (j * (MT + 1) + MT)] = make_float4(ref[j][0], ref[j][1], l[j][0], l[j][1]);
     }
   }
-  __device__ __forceinline__ void load(const float* p) {
-    const float4* q = reinterpret_cast<const float4*>(p) + (threadIdx.x & 31);
-#pragma unroll
-    for (int j = 0; j < NR; ++j) {
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const float4 x = q[32 * (j * (MT + 1) + i)];
-        o[j][i][0] = x.x; o[j][i][1] = x.y; o[j][i][2] = x.z; o[j][i][3] = x.w;
-      }
-      const float4 x = q[32 * (j * (MT + 1) + MT)];
-      ref[j][0] = x.x; ref[j][1] = x.y; l[j][0] = x.z; l[j][1] = x.w;
-    }
-  }
   // joins a saved state of the same rows
   __device__ __forceinline__ void join(const float* p) {
     const float4* q = reinterpret_cast<const float4*>(p) + (threadIdx.x & 31);
@@ -331,7 +321,7 @@ struct AtState {
       for (int e = 0; e < 2; ++e) {
         const float to = fmaxf(ref[j][e], pm[e]);
         raise(j, e, to);
-        c1[e] = at_corr(pm[e] - (to == kNegInf ? 0.f : to));
+        c1[e] = at_corr(pm[e] - to);
         l[j][e] += pl[e] * c1[e];
       }
 #pragma unroll
@@ -439,8 +429,62 @@ __device__ __forceinline__ void at_add_v(const uint32_t (&w)[4], int from, uint3
   }
 }
 
-// New references for the pair, where a score of the tile lies too far above one.
-// mx: the lane's largest products of the warp's block.
+// The products of 16 tokens of a block (16 mt ...; own: the sequence's tokens of it)
+// with the rows: z[.][e + 2 f], row 2 t + e, token g of the f-th eight.
+template <int D, int NR>
+__device__ __forceinline__ void at_scores(const unsigned char* sb, const uint4* qf, int mt, int own, float (&z)[NR][4]) {
+  constexpr int WK = D / 32;   // words of a key chunk
+  const int lane = threadIdx.x & 31, t = lane & 3, tr = at_token(lane >> 2);
+  uint32_t kw[2][WK];
+  uint32_t ks2[2][D / 64];   // the chunk's scales, each twice
+#pragma unroll
+  for (int f = 0; f < 2; ++f) {
+    const int tok = 16 * mt + 8 * f + tr;
+    if constexpr (D == 128) {
+      const uint4 x = *reinterpret_cast<const uint4*>(sb + tok * 64 + t * 16);
+      kw[f][0] = x.x; kw[f][1] = x.y; kw[f][2] = x.z; kw[f][3] = x.w;
+      const uint32_t two = e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(sb + 32 * D + tok * 8 + t * 2));
+      ks2[f][0] = __byte_perm(two, two, 0x1010);
+      ks2[f][1] = __byte_perm(two, two, 0x3232);
+    } else {
+      const uint2 x = *reinterpret_cast<const uint2*>(sb + tok * 32 + t * 8);
+      kw[f][0] = x.x; kw[f][1] = x.y;
+      const uint32_t one = sb[32 * D + tok * 4 + t];
+      ks2[f][0] = e4m3x2_to_f16(one * 0x101u);
+    }
+  }
+#pragma unroll
+  for (int w = 0; w < WK; ++w) {
+    uint32_t r0[4], r1[4];   // tokens g and g + 8
+    e2m1x8_to_f16(kw[0][w], r0);
+    e2m1x8_to_f16(kw[1][w], r1);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r0[i] = f16x2_mul(r0[i], ks2[0][w / 2]);
+      r1[i] = f16x2_mul(r1[i], ks2[1][w / 2]);
+    }
+    const uint4 k0 = make_uint4(r0[0], r1[0], r0[1], r1[1]), k1 = make_uint4(r0[2], r1[2], r0[3], r1[3]);
+#pragma unroll
+    for (int j = 0; j < NR; ++j) {
+      const uint4 qb = qf[(j * WK + w) * 32];
+      if (w == 0) mma_f16_zero(z[j], k0, qb.x, qb.y);
+      else mma_f16(z[j], k0, qb.x, qb.y);
+      mma_f16(z[j], k1, qb.z, qb.w);
+    }
+  }
+  if (own < 16 * mt + 16) {   // the sequence ends here (what the stage holds behind it may be anything)
+#pragma unroll
+    for (int f = 0; f < 2; ++f)
+      if (16 * mt + 8 * f + tr >= own) {
+#pragma unroll
+        for (int j = 0; j < NR; ++j) z[j][2 * f] = z[j][2 * f + 1] = kNegInf;
+      }
+  }
+}
+
+// New references for the pair, of a tile with a score too far above an old one.
+// mx: the lane's largest products of the warp's block.  (Arrays are copies, so that
+// the state stays in registers.)
 template <int D, int NR>
 __device__ __noinline__ void at_agree(const AtPair<D, NR>& pr, int buf, const float* mx, const float* c, const float* ref, float* to) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -456,7 +500,7 @@ __device__ __noinline__ void at_agree(const AtPair<D, NR>& pr, int buf, const fl
 #pragma unroll
   for (int i = 0; i < 2 * NR; ++i) {
     const int r = 8 * (i >> 1) + 2 * t + (i & 1);
-    to[i] = fmaxf(ref[i], fmaxf(pr.top(buf, 0)[r], pr.top(buf, 1)[r]));
+    to[i] = fmaxf(ref[i], fmaxf(pr.top(buf, 0)[r], pr.top(buf, 1)[r]) - AT_PSHIFT);
   }
   pr.sync();   // the maxima have been read, and what follows is written anew
 }
@@ -464,92 +508,47 @@ __device__ __noinline__ void at_agree(const AtPair<D, NR>& pr, int buf, const fl
 // A cached tile: `left` tokens of it (1..64) belong to the sequence.  `after` runs
 // once both warps are done with the tile before.
 //
-// Both halves of the work are loops over 16 tokens that are not unrolled: the code
-// of a tile then is about 5 KB, which a warp gets through at about the rate of its
-// scheduler.  (Unrolled it was 15 KB, and a warp of the three or four on a scheduler
-// took 2.7 to 3.3 clocks an instruction to fetch: BEFORE_US where this takes
-// AFTER_US.)  So the weights are taken at once against the references as they are,
-// and only then the warps look whether a score was too far above one; if so, they
-// agree on new references and score the tile again.
+// Both halves of the work are loops over 16 tokens, unrolled only as far as the
+// code of a tile stays near 8 KB, up to which a warp gets through it at about the
+// rate of its scheduler; at 16 KB it takes 2.7 clocks an instruction to fetch.  32
+// rows fully unrolled took 645 us, two steps at a time 548, rolled 507; 24 rows 383,
+// 343 and 350; 16 rows two at a time 252, rolled 270; 8 rows unrolled 170, rolled
+// 187 (256 sequences at 2,048 tokens).  So that they can be loops, the weights are
+// taken at once against the references as they are, and only then the warps look
+// whether a score was too far above one; if so, they agree on new references and
+// score the tile again.
 //
 // (The exchange area has two buffers, taken in turn: with one barrier a tile, what a
 // warp writes for a tile was last read two barriers before.)
+__host__ __device__ constexpr int at_unroll(int NR) { return NR == 1 ? 4 : NR < 4 ? 2 : 1; }
 template <int D, int NR, class F>
 __device__ __forceinline__ void at_cached_tile(const unsigned char* tile, int left, int buf, const float (&c)[NR][2],
                                                const AtPair<D, NR>& pr, AtState<D, NR>& st, F&& after) {
-  constexpr int WK = D / 32;   // words of a key chunk
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int tr = at_token(g);
   const int own = left - pr.x * Q4_BLOCK;   // tokens of the warp's block
   const unsigned char* sb = tile + pr.x * q4_block_bytes(D);
-  const uint4* qf = pr.q() + lane;
   uint2* out = pr.p(buf, pr.x) + lane;
   float lt[NR][2];
   for (;;) {
-    float mx[NR][2], r[NR][2];
+    float mx[NR][2];
 #pragma unroll
     for (int j = 0; j < NR; ++j)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         lt[j][e] = 0.f;
         mx[j][e] = kNegInf;
-        r[j][e] = AT_PSHIFT - (st.ref[j][e] == kNegInf ? 0.f : st.ref[j][e]);
       }
-#pragma unroll 1
+#pragma unroll at_unroll(NR)
     for (int mt = 0; mt < 2; ++mt) {
       float z[NR][4];
-      uint32_t kw[2][WK];
-      uint32_t ks2[2][D / 64];   // the chunk's scales, each twice
-#pragma unroll
-      for (int f = 0; f < 2; ++f) {
-        const int tok = 16 * mt + 8 * f + tr;
-        if constexpr (D == 128) {
-          const uint4 x = *reinterpret_cast<const uint4*>(sb + tok * 64 + t * 16);
-          kw[f][0] = x.x; kw[f][1] = x.y; kw[f][2] = x.z; kw[f][3] = x.w;
-          const uint32_t two = e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(sb + 32 * D + tok * 8 + t * 2));
-          ks2[f][0] = __byte_perm(two, two, 0x1010);
-          ks2[f][1] = __byte_perm(two, two, 0x3232);
-        } else {
-          const uint2 x = *reinterpret_cast<const uint2*>(sb + tok * 32 + t * 8);
-          kw[f][0] = x.x; kw[f][1] = x.y;
-          const uint32_t one = sb[32 * D + tok * 4 + t];
-          ks2[f][0] = e4m3x2_to_f16(one * 0x101u);
-        }
-      }
-#pragma unroll
-      for (int w = 0; w < WK; ++w) {
-        uint32_t r0[4], r1[4];   // tokens g and g + 8
-        e2m1x8_to_f16(kw[0][w], r0);
-        e2m1x8_to_f16(kw[1][w], r1);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          r0[i] = f16x2_mul(r0[i], ks2[0][w / 2]);
-          r1[i] = f16x2_mul(r1[i], ks2[1][w / 2]);
-        }
-        const uint4 k0 = make_uint4(r0[0], r1[0], r0[1], r1[1]), k1 = make_uint4(r0[2], r1[2], r0[3], r1[3]);
-#pragma unroll
-        for (int j = 0; j < NR; ++j) {
-          const uint4 qb = qf[(j * WK + w) * 32];
-          if (w == 0) mma_f16_zero(z[j], k0, qb.x, qb.y);
-          else mma_f16(z[j], k0, qb.x, qb.y);
-          mma_f16(z[j], k1, qb.z, qb.w);
-        }
-      }
-      if (own < 16 * mt + 16) {   // the sequence ends here (what the stage holds behind it may be anything)
-#pragma unroll
-        for (int f = 0; f < 2; ++f)
-          if (16 * mt + 8 * f + tr >= own) {
-#pragma unroll
-            for (int j = 0; j < NR; ++j) z[j][2 * f] = z[j][2 * f + 1] = kNegInf;
-          }
-      }
+      at_scores<D, NR>(sb, pr.q() + lane, mt, own, z);
 #pragma unroll
       for (int j = 0; j < NR; ++j) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           mx[j][e] = fmaxf(mx[j][e], fmaxf(z[j][e], z[j][e + 2]));
-          z[j][e] = ex2_approx(__fmaf_rn(z[j][e], c[j][e], r[j][e]));
-          z[j][e + 2] = ex2_approx(__fmaf_rn(z[j][e + 2], c[j][e], r[j][e]));
+          z[j][e] = ex2_approx(__fmaf_rn(z[j][e], c[j][e], -st.ref[j][e]));
+          z[j][e + 2] = ex2_approx(__fmaf_rn(z[j][e + 2], c[j][e], -st.ref[j][e]));
           lt[j][e] += z[j][e] + z[j][e + 2];
         }
         out[(mt * NR + j) * 32] = make_uint2(transpose8(f16x2_pack(z[j][0], z[j][1])), transpose8(f16x2_pack(z[j][2], z[j][3])));
@@ -559,12 +558,12 @@ __device__ __forceinline__ void at_cached_tile(const unsigned char* tile, int le
 #pragma unroll
     for (int j = 0; j < NR; ++j)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) above |= mx[j][e] * c[j][e] > st.ref[j][e] + AT_ABOVE;
+      for (int e = 0; e < 2; ++e) above |= __fmul_rn(mx[j][e], c[j][e]) - AT_PSHIFT > st.ref[j][e] + AT_ABOVE;
     above = __any_sync(0xffffffffu, above);
     if (lane == 0) *pr.flag(buf, pr.x) = above;
     pr.sync();
     if (__builtin_expect(!above && !*pr.flag(buf, pr.x ^ 1), 1)) break;
-    float m2[2 * NR], c2[2 * NR], ref[2 * NR], to[2 * NR];   // (copies: the state stays in registers)
+    float m2[2 * NR], c2[2 * NR], ref[2 * NR], to[2 * NR];
 #pragma unroll
     for (int i = 0; i < 2 * NR; ++i) {
       m2[i] = mx[i >> 1][i & 1];
@@ -583,7 +582,7 @@ __device__ __forceinline__ void at_cached_tile(const unsigned char* tile, int le
 
   // v: steps of 16 tokens (D = 128), or of 32 (D = 64, whose codes of two steps make a word)
   constexpr int STEPS = D == 128 ? 4 : 2, S = 4 / STEPS;
-#pragma unroll 1
+#pragma unroll at_unroll(NR)
   for (int y = 0; y < STEPS; ++y) {
     const int blk = y / (STEPS / 2), s0 = D == 128 ? y & 1 : 0;
     const int have = left - blk * Q4_BLOCK;   // tokens of that block
@@ -651,27 +650,8 @@ __device__ __forceinline__ void at_fresh_tile(const AttendArgs& a, int b, int h,
 #pragma unroll
   for (int j = 0; j < NR; ++j) qat[j] = row0 + 8 * j + g < rows ? at_row(a, b, h, row0 + 8 * j + g) * D + t * CH : -1;
   const int jx = j0 + pr.x * Q4_BLOCK;   // the warp's nodes
-  if (jx < a.N) {
-#pragma unroll 4
-    for (int ks = 0; ks < KS; ++ks) {
-      uint2 qb[NR];
-#pragma unroll
-      for (int j = 0; j < NR; ++j)
-        qb[j] = qat[j] >= 0 ? __ldg(reinterpret_cast<const uint2*>(a.q + qat[j] + 4 * ks)) : make_uint2(0u, 0u);
-#pragma unroll
-      for (int mt = 0; mt < 2; ++mt) {
-        uint2 kx[2];
-#pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          const int n = jx + 16 * mt + 8 * f + tr;
-          kx[f] = n < a.N ? __ldg(reinterpret_cast<const uint2*>(a.k_new + base + n * rstride + t * CH + 4 * ks)) : make_uint2(0u, 0u);
-        }
-        const uint4 k = make_uint4(kx[0].x, kx[1].x, kx[0].y, kx[1].y);
-#pragma unroll
-        for (int j = 0; j < NR; ++j) mma_bf16(z[mt][j], k, qb[j].x, qb[j].y);
-      }
-    }
-  }
+  // (most tiles have few nodes and wait for their loads: what can be asked for
+  // early is)
   uint32_t sees[NR][2][2];   // nodes of the tile that the lane's rows attend to
 #pragma unroll
   for (int j = 0; j < NR; ++j)
@@ -685,9 +665,41 @@ __device__ __forceinline__ void at_fresh_tile(const AttendArgs& a, int b, int h,
         if (n < a.N && at < a.N) {
           if (a.masks) see = __ldg(a.masks + (static_cast<long long>(b) * a.N + n) * a.NW + at / 32);
           else see = n - at >= 31 ? ~0u : n < at ? 0u : (2u << (n - at)) - 1u;
-          if (a.N - at < 32) see &= (1u << (a.N - at)) - 1u;
         }
         sees[j][e][y] = see;
+      }
+    }
+  if (j0 + lane < a.N) asm volatile("prefetch.global.L1 [%0];" ::"l"(a.v_new + base + (j0 + lane) * rstride + pr.x * (D / 2)));
+  if (jx < a.N) {
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      uint2 qb[NR];
+#pragma unroll
+      for (int j = 0; j < NR; ++j)
+        qb[j] = qat[j] >= 0 ? __ldg(reinterpret_cast<const uint2*>(a.q + qat[j] + 4 * ks)) : make_uint2(0u, 0u);
+#pragma unroll
+      for (int mt = 0; mt < 2; ++mt) {
+        if (mt == 1 && jx + 16 >= a.N) break;
+        uint2 kx[2];
+#pragma unroll
+        for (int f = 0; f < 2; ++f) {
+          const int n = jx + 16 * mt + 8 * f + tr;
+          kx[f] = n < a.N ? __ldg(reinterpret_cast<const uint2*>(a.k_new + base + n * rstride + t * CH + 4 * ks)) : make_uint2(0u, 0u);
+        }
+        const uint4 k = make_uint4(kx[0].x, kx[1].x, kx[0].y, kx[1].y);
+#pragma unroll
+        for (int j = 0; j < NR; ++j) mma_bf16(z[mt][j], k, qb[j].x, qb[j].y);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NR; ++j)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {   // (no node behind the last)
+        const int behind = a.N - j0 - y * Q4_BLOCK;
+        if (behind < 32) sees[j][e][y] &= behind > 0 ? (1u << behind) - 1u : 0u;
       }
       const uint32_t see = pr.x ? sees[j][e][1] : sees[j][e][0];
       float m = kNegInf;
@@ -712,8 +724,8 @@ __device__ __forceinline__ void at_fresh_tile(const AttendArgs& a, int b, int h,
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       const int r = 8 * j + 2 * t + e;
-      st.raise(j, e, fmaxf(st.ref[j][e], fmaxf(pr.top(0, 0)[r], pr.top(0, 1)[r])));
-      const float ref = (st.ref[j][e] == kNegInf ? 0.f : st.ref[j][e]) - AT_PSHIFT;
+      st.raise(j, e, fmaxf(st.ref[j][e], fmaxf(pr.top(0, 0)[r], pr.top(0, 1)[r]) - AT_PSHIFT));
+      const float ref = st.ref[j][e];
 #pragma unroll
       for (int mt = 0; mt < 2; ++mt)
 #pragma unroll
@@ -808,21 +820,20 @@ __device__ __forceinline__ void at_fresh_tile(const AttendArgs& a, int b, int h,
   pr.sync();   // the exchange area is free again
 }
 
-// The state after fresh tiles first .. last - 1 of a triple, saved at `p`.  A
+// The state after fresh tiles first .. last - 1 of a triple.  A
 // function of its own: these tiles are few, and their registers would push the
 // cached tiles' loop into local memory.
 template <int D, int NR>
 __device__ __noinline__ void at_fresh(const AttendArgs& a, int b, int h, int row0, int rows, int first, int last,
-                                      AtPair<D, NR> pr, float* p) {
+                                      AtPair<D, NR> pr, AtState<D, NR>* to) {
   AtState<D, NR> st;
   st.clear();
   for (int i = first; i < last; ++i) at_fresh_tile<D, NR>(a, b, h, row0, rows, i * AT_TILE, pr, st);
-  st.save(p);
+  *to = st;
 }
 
 __device__ __forceinline__ float at_lse(float ref, float l) {
-  // ref in the log2 domain, l relative to 2^(ref - 7)
-  return l == 0.f ? kNegInf : (ref - AT_PSHIFT + log2f(l)) * 0.69314718055994530942f;
+  return l == 0.f ? kNegInf : (ref + log2f(l)) * 0.69314718055994530942f;   // l: the sum of weights, relative to 2^ref
 }
 
 // CTAs an SM: what the registers of a row tile leave room for
@@ -931,6 +942,7 @@ __global__ void __launch_bounds__(AT_THREADS, at_ctas(NR)) attend_q4_kernel(cons
     for (int s = 0; s < stages; ++s) mbar_init(&bars[s], 1);
     mbar_fence_init();
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (the join kernel may start; it waits for this grid's end)
   at_prefix<AT_THREADS>(a, prefix, scratch);   // (synchronises the CTA)
 
   const int HR = a.Hkv * a.row_tiles;
@@ -940,7 +952,7 @@ __global__ void __launch_bounds__(AT_THREADS, at_ctas(NR)) attend_q4_kernel(cons
   const int shares = ctas * AT_PAIRS, share = blockIdx.x * AT_PAIRS + pair;
   const long long u0 = at_start(units, shares, share), u1 = at_start(units, shares, share + 1);
   float* cta_ws = a.ws + static_cast<size_t>(blockIdx.x) * at_cta_floats(D, NR);
-  float* states = cta_ws + 2 * at_partial_floats(D, NR);   // [pair][x], then the fresh ones
+  float* states = cta_ws + 2 * at_partial_floats(D, NR);   // [pair][x]
 
   const int rows = a.N * a.G;
   const int nfresh = a.k_new ? (a.N + AT_TILE - 1) / AT_TILE : 0;
@@ -1005,9 +1017,9 @@ __global__ void __launch_bounds__(AT_THREADS, at_ctas(NR)) attend_q4_kernel(cons
       // (a fresh tile is worked on by the share that has its first unit)
       const int f0 = (first + AT_FRESH - 1) / AT_FRESH, f1 = (min(last, nf) + AT_FRESH - 1) / AT_FRESH;
       if (f0 < f1) {
-        float* at = states + (2 * AT_PAIRS + (threadIdx.x >> 5)) * at_state_floats(D, NR);
-        at_fresh<D, NR>(a, cur.b, h, row0, rows, f0, f1, pr, at);
-        st.load(at);
+        AtState<D, NR> fresh;   // (in local memory, so that `st` is not)
+        at_fresh<D, NR>(a, cur.b, h, row0, rows, f0, f1, pr, &fresh);
+        st = fresh;
       } else {
         st.clear();
       }
@@ -1087,6 +1099,7 @@ __global__ void __launch_bounds__(ATJ_THREADS) attend_q4_join_kernel(const __gri
   __shared__ float sml[PL][2][8], so[PL][8][SPREAD ? D : 1];
   long long* prefix = reinterpret_cast<long long*>(at_smem);
   at_prefix<ATJ_THREADS>(a, prefix, scratch);
+  asm volatile("griddepcontrol.wait;" ::: "memory");   // every CTA, before it reads a partial or ends
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int HR = a.Hkv * a.row_tiles, rows = a.N * a.G;
   const long long units = prefix[a.B] * HR;

@@ -596,7 +596,7 @@ __device__ __noinline__ void tc_finish(const AttendArgs& a, int b, int h, int ro
     place[i] = at_row(a, b, h, min(row0 + col0 + i, rows - 1)) * D;
     const float sum = (top[i] + top[NC + i]) + (top[2 * NC + i] + top[3 * NC + i]);
     const int r = row0 + col0 + i;
-    const float ref = AT_PSHIFT - shift[i];
+    const float ref = -shift[i];
     corr[i] = sum == 0.f ? 0.f : a.v_mul / sum;
     if (whole) {
       if (r < rows && a.lse) a.lse[place[i] / D] = at_lse(ref, sum);
@@ -1028,6 +1028,7 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
       tc_step<NC>(a, prefix, HR, nfresh, ntiles - u, t);
     }
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (the join kernel may start; it waits for this grid's end)
   __syncthreads();
   if (*reinterpret_cast<volatile int*>(&bar->dead)) {
     // a wait ran out of time: every triple of the share is void
