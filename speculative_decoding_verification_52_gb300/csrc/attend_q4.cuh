@@ -82,7 +82,9 @@ struct AttendArgs {
   const int32_t* lengths;    // [B]
   int B, N, G, Hkv, P, pages, W, NW;
   int row_tiles;             // row tiles of a (sequence, head)
-  int tile, fresh;           // tokens of a tile; what a tile of fresh entries counts in the list
+  uint32_t by_g;             // ceil(2^32 / G), 0 for G = 1: a row r < 65536 is of node r * by_g / 2^32
+  int tile;                  // tokens of a tile
+  int fresh, fresh_more;     // what a triple's first tile of fresh entries counts in the list, and another one
   float scale_log2;          // scale * log2(e)
   float k_mul, v_mul;        // 2^shift
   uint16_t* out;             // [B, N, Hkv * G, D] bf16
@@ -99,9 +101,12 @@ struct AttendArgs {
 __device__ __forceinline__ bool at_len_ok(const AttendArgs& a, int len) {
   return len >= 0 && static_cast<long long>(len) <= static_cast<long long>(a.W) * a.P;
 }
+__device__ __forceinline__ int at_fresh_units(const AttendArgs& a) {
+  return a.k_new ? a.fresh + a.fresh_more * ((a.N + a.tile - 1) / a.tile - 1) : 0;
+}
 __device__ __forceinline__ int at_units(const AttendArgs& a, int len) {
   if (!at_len_ok(a, len)) return 1;
-  const int n = (len + a.tile - 1) / a.tile + (a.k_new ? a.fresh * ((a.N + a.tile - 1) / a.tile) : 0);
+  const int n = (len + a.tile - 1) / a.tile + at_fresh_units(a);
   return n > 0 ? n : 1;
 }
 
@@ -254,9 +259,10 @@ __host__ __device__ constexpr size_t at_cta_floats(int D, int NR) {
   return 2 * at_partial_floats(D, NR) + 2 * AT_PAIRS * at_state_floats(D, NR);
 }
 
+__device__ __forceinline__ int at_node(const AttendArgs& a, int r) { return a.by_g ? static_cast<int>(__umulhi(static_cast<uint32_t>(r), a.by_g)) : r; }
 __device__ __forceinline__ long long at_row(const AttendArgs& a, int b, int h, int r) {
-  const int n = r / a.G;
-  return ((static_cast<long long>(b) * a.N + n) * a.Hkv + h) * a.G + (r - n * a.G);
+  const int n = at_node(a, r);
+  return (static_cast<long long>(b) * a.N + n) * (a.Hkv * a.G) + (h * a.G + r - n * a.G);
 }
 
 // ---------------------------------------------------------------------------
@@ -657,7 +663,7 @@ __device__ __forceinline__ void at_fresh_tile(const AttendArgs& a, int b, int h,
   for (int j = 0; j < NR; ++j)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int n = (row0 + 8 * j + 2 * t + e) / a.G;
+      const int n = at_node(a, row0 + 8 * j + 2 * t + e);
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
         const int at = j0 + y * Q4_BLOCK;
@@ -671,7 +677,7 @@ __device__ __forceinline__ void at_fresh_tile(const AttendArgs& a, int b, int h,
     }
   if (j0 + lane < a.N) asm volatile("prefetch.global.L1 [%0];" ::"l"(a.v_new + base + (j0 + lane) * rstride + pr.x * (D / 2)));
   if (jx < a.N) {
-#pragma unroll
+#pragma unroll 2
     for (int ks = 0; ks < KS; ++ks) {
       uint2 qb[NR];
 #pragma unroll
@@ -759,8 +765,7 @@ __device__ __forceinline__ void at_fresh_tile(const AttendArgs& a, int b, int h,
       hi[j] = pr.p(0, blk)[(s * NR + j) * 32 + lane];
       lo[j] = pr.p(1, blk)[(s * NR + j) * 32 + lane];
     }
-    bool odd = false;   // this lane saw a NaN or an infinity
-    uint32_t vw[4][CV / 2];
+    uint32_t most = 0u, vw[4][CV / 2];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int n = n0 + 8 * (k >> 1) + at_token(2 * t + (k & 1));
@@ -773,9 +778,14 @@ __device__ __forceinline__ void at_fresh_tile(const AttendArgs& a, int b, int h,
         vw[k][0] = x.x; vw[k][1] = x.y;
       }
 #pragma unroll
-      for (int i = 0; i < CV / 2; ++i)
-        if (bf16x2_unbounded(vw[k][i])) {
-          odd = true;
+      for (int i = 0; i < CV / 2; ++i) most = bf16x2_max_nan(most, vw[k][i] & 0x7fff7fffu);
+    }
+    const bool odd = bf16x2_unbounded(most);   // this lane saw a NaN or an infinity
+    if (__builtin_expect(odd, 0)) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int i = 0; i < CV / 2; ++i) {
           if ((vw[k][i] & 0x7f80u) == 0x7f80u) vw[k][i] &= 0xffff0000u;
           if ((vw[k][i] & 0x7f800000u) == 0x7f800000u) vw[k][i] &= 0xffffu;
         }
@@ -824,8 +834,9 @@ __device__ __forceinline__ void at_fresh_tile(const AttendArgs& a, int b, int h,
 // function of its own: these tiles are few, and their registers would push the
 // cached tiles' loop into local memory.
 template <int D, int NR>
-__device__ __noinline__ void at_fresh(const AttendArgs& a, int b, int h, int row0, int rows, int first, int last,
+__device__ __noinline__ void at_fresh(const AttendArgs& args, int b, int h, int row0, int rows, int first, int last,
                                       AtPair<D, NR> pr, AtState<D, NR>* to) {
+  const AttendArgs a = args;   // (in registers: through the reference each use would read it again after every store)
   AtState<D, NR> st;
   st.clear();
   for (int i = first; i < last; ++i) at_fresh_tile<D, NR>(a, b, h, row0, rows, i * AT_TILE, pr, st);

@@ -46,6 +46,7 @@
 namespace sv {
 
 constexpr int TC_TILE = 128;                 // tokens of a tile
+constexpr int TC_FRESH_UNITS = 9;            // what a triple's first fresh tile counts in the list, in cached tiles
 constexpr uint32_t TC_VBUF = 128 * 128 * 2;  // bytes of a V buffer (16 groups of 8 columns, also for D = 64)
 
 template <int D, int NC>
@@ -241,6 +242,9 @@ __device__ __forceinline__ uint32_t tc_swz(uint32_t o) {
   return D == 128 ? o ^ (((o >> 7) & 3u) << 4) : o ^ (((o >> 7) & 1u) << 4);
 }
 
+// (Functions that are not inlined take a copy of the arguments: through the
+// reference each use would read them again after every store.)
+
 // ---------------------------------------------------------------------------
 // the list of tiles of a CTA, walked alike by all roles
 // ---------------------------------------------------------------------------
@@ -248,21 +252,33 @@ struct TcTile {
   AtCursor c;
   int h, row0;           // kv head, first row
   int kind, at, left;    // what the tile is; its first token or node; tokens of it (0..128)
+  int step;              // units of the list that it stands for
   bool first, last;      // of the triple's part in the share
+  bool ends;             // the triple's end, in the share
 };
 enum { TC_CACHED = 0, TC_FRESH = 1, TC_VOID = 2 };   // void: a length out of range (left = 1), or nothing at all (left = 0)
 
+// A triple's first fresh tile stands for a.fresh units, every other tile for one
+// (nfresh: units of the fresh tiles).  A share that begins within those has a tile
+// of nothing first.
 template <int NC>
-__device__ __noinline__ void tc_open_slow(const AttendArgs& a, int nfresh, TcTile& t) {
+__device__ __noinline__ void tc_open_slow(const AttendArgs& args, int nfresh, TcTile& t) {
+  const AttendArgs a = args;
   t.h = t.c.pair / a.row_tiles;
   t.row0 = (t.c.pair - t.h * a.row_tiles) * NC;
   t.at = 0;
+  t.step = 1;
   if (!at_len_ok(a, t.c.len)) {
     t.kind = TC_VOID;
     t.left = 1;
+  } else if (t.c.i > 0 && t.c.i < nfresh && t.c.i < a.fresh) {
+    t.kind = TC_VOID;
+    t.left = 0;
+    t.step = a.fresh - t.c.i;
   } else if (t.c.i < nfresh) {
     t.kind = TC_FRESH;
-    t.at = t.c.i * TC_TILE;
+    if (t.c.i == 0) t.step = a.fresh;
+    else t.at = (t.c.i - a.fresh + 1) * TC_TILE;
     t.left = min(a.N - t.at, TC_TILE);
   } else {
     t.at = (t.c.i - nfresh) * TC_TILE;
@@ -282,22 +298,26 @@ __device__ __forceinline__ void tc_begin(const AttendArgs& a, const long long* p
   at_seek(a, prefix, HR, u, t.c);
   tc_open<NC>(a, nfresh, t);
   t.first = true;
-  t.last = t.c.i + 1 == t.c.units || n == 1;
+  t.ends = t.c.i + t.step == t.c.units && t.step <= n;
+  t.last = t.ends || t.step >= n;
 }
-// to the next tile; `left`: tiles of the share from there on
+// to the next tile; `left`: units of the share from there on
 template <int NC>
 __device__ __forceinline__ void tc_step(const AttendArgs& a, const long long* prefix, int HR, int nfresh, int left, TcTile& t) {
-  if (TC_RARE(t.c.i + 1 == t.c.units || t.c.i + 1 == nfresh)) {   // another triple, or its first cached tile
-    t.first = t.c.i + 1 == t.c.units;
+  t.c.i += t.step;
+  if (TC_RARE(t.c.i == t.c.units || t.c.i == nfresh || t.kind == TC_VOID)) {   // another triple, or its first cached tile
+    t.first = t.c.i == t.c.units;
+    --t.c.i;
     at_next(a, prefix, HR, t.c);
     tc_open<NC>(a, nfresh, t);
   } else {
-    ++t.c.i;
     t.first = false;
+    t.step = 1;
     t.at += TC_TILE;
     t.left = min((t.kind == TC_FRESH ? a.N : t.c.len) - t.at, TC_TILE);
   }
-  t.last = t.c.i + 1 == t.c.units || left == 1;
+  t.ends = t.c.i + t.step == t.c.units && t.step <= left;
+  t.last = t.ends || t.step >= left;
 }
 
 // ---------------------------------------------------------------------------
@@ -312,26 +332,43 @@ __device__ __forceinline__ void tc_widen(uint32_t w0, uint32_t w1, uint32_t s2, 
 }
 // scale byte g of a word as an f16 pair of equals
 __device__ __forceinline__ uint32_t tc_scale(uint32_t sc, int g) { return e4m3x2_to_f16(__byte_perm(sc, 0u, g * 0x11)); }
-// eight f16 pairs of a fresh entry's 16 elements, in units of 1 / mul; `odd` when one does not fit
-__device__ __forceinline__ void tc_narrow(const uint4& x, const uint4& y, float mul, uint32_t* r, bool& odd) {
+// eight f16 pairs of a fresh entry's 16 elements, in units of 1 / mul
+__device__ __forceinline__ void tc_narrow(const uint4& x, const uint4& y, float mul, uint32_t* r) {
   const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float lo = __uint_as_float(w[i] << 16) * mul, hi = __uint_as_float(w[i] & 0xffff0000u) * mul;
-    if (!(fabsf(lo) <= 65504.f)) { odd = true; lo = 0.f; }
-    if (!(fabsf(hi) <= 65504.f)) { odd = true; hi = 0.f; }
-    r[i] = f16x2_pack(lo, hi);
-  }
+  for (int i = 0; i < 8; ++i) r[i] = f16x2_pack(__uint_as_float(w[i] << 16) * mul, __uint_as_float(w[i] & 0xffff0000u) * mul);
+}
+// the largest of |m| and the elements (NaN if there is one)
+__device__ __forceinline__ uint32_t tc_most(uint32_t m, const uint4& x) {
+  return bf16x2_max_nan(m, bf16x2_max_nan(bf16x2_max_nan(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), bf16x2_max_nan(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+}
+__device__ __forceinline__ bool tc_fits(uint32_t most, float mul) {
+  return fmax_nan(__uint_as_float(most << 16), __uint_as_float(most & 0xffff0000u)) * mul <= 65504.f;
+}
+// 0 for the elements that do not fit
+__device__ __noinline__ void tc_drop(uint4* x, int n, float mul) {
+  uint16_t* e = reinterpret_cast<uint16_t*>(x);
+#pragma unroll 1
+  for (int i = 0; i < 8 * n; ++i)
+    if (!tc_fits(e[i] & 0x7fffu, mul)) e[i] = 0u;
+}
+
+// a row of D elements to the L2 cache
+template <int D>
+__device__ __forceinline__ void tc_prefetch(const uint16_t* p) {
+#pragma unroll
+  for (int i = 0; i < D; i += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i));
 }
 
 // A fresh node's key into its lane of tensor memory.  True when an element of the
-// key or of the value does not fit.
+// key or of the value does not fit (the tile's scores then are not taken from here).
 template <int D>
-__device__ __noinline__ bool tc_fresh_key(const AttendArgs& a, int b, int h, int node, bool mine, uint32_t k_at) {
+__device__ __noinline__ bool tc_fresh_key(const AttendArgs& args, int b, int h, int node, bool mine, uint32_t k_at) {
+  const AttendArgs a = args;
   const long long at = ((static_cast<long long>(b) * a.N + (mine ? node : 0)) * a.Hkv + h) * D;
   const uint4 *k = reinterpret_cast<const uint4*>(a.k_new + at), *v = reinterpret_cast<const uint4*>(a.v_new + at);
   const float kmul = __fdiv_rn(1.f, a.k_mul), vmul = __fdiv_rn(1.f, a.v_mul);
-  bool odd = false;
+  uint32_t kmost = 0u, vmost = 0u;
 #pragma unroll 1
   for (int c = 0; c < D / 32; ++c) {
     uint4 x[8];
@@ -340,31 +377,44 @@ __device__ __noinline__ bool tc_fresh_key(const AttendArgs& a, int b, int h, int
       x[i] = mine ? __ldg(k + 4 * c + i) : make_uint4(0u, 0u, 0u, 0u);
       x[4 + i] = mine ? __ldg(v + 4 * c + i) : make_uint4(0u, 0u, 0u, 0u);
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      kmost = tc_most(kmost, x[i]);
+      vmost = tc_most(vmost, x[4 + i]);
+    }
     uint32_t r[16];
-    tc_narrow(x[4], x[5], vmul, r, odd);
-    tc_narrow(x[6], x[7], vmul, r + 8, odd);
-    tc_narrow(x[0], x[1], kmul, r, odd);
-    tc_narrow(x[2], x[3], kmul, r + 8, odd);
+    tc_narrow(x[0], x[1], kmul, r);
+    tc_narrow(x[2], x[3], kmul, r + 8);
     __syncwarp();
     tc_st16(k_at + c * 16, r);
   }
-  return odd;
+  return !tc_fits(kmost, kmul) || !tc_fits(vmost, vmul);
 }
 // its value into shared memory (0 for what does not fit)
 template <int D>
-__device__ __noinline__ void tc_fresh_value(const AttendArgs& a, int b, int h, int node, bool mine, unsigned char* vb) {
+__device__ __noinline__ void tc_fresh_value(const AttendArgs& args, int b, int h, int node, bool mine, unsigned char* vb) {
+  const AttendArgs a = args;
   const long long at = ((static_cast<long long>(b) * a.N + (mine ? node : 0)) * a.Hkv + h) * D;
   const uint4* v = reinterpret_cast<const uint4*>(a.v_new + at);
   const float vmul = __fdiv_rn(1.f, a.v_mul);
-  bool odd = false;
 #pragma unroll 1
   for (int c = 0; c < D / 32; ++c) {
     uint4 x[4];
+    uint32_t most = 0u;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = mine ? __ldg(v + 4 * c + i) : make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < 4; ++i) {
+      x[i] = mine ? __ldg(v + 4 * c + i) : make_uint4(0u, 0u, 0u, 0u);
+      most = tc_most(most, x[i]);
+    }
+    if (TC_RARE(!tc_fits(most, vmul))) {
+      uint4 y[4] = {x[0], x[1], x[2], x[3]};
+      tc_drop(y, 4, vmul);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] = y[i];
+    }
     uint32_t r[16];
-    tc_narrow(x[0], x[1], vmul, r, odd);
-    tc_narrow(x[2], x[3], vmul, r + 8, odd);
+    tc_narrow(x[0], x[1], vmul, r);
+    tc_narrow(x[2], x[3], vmul, r + 8);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       *reinterpret_cast<uint4*>(vb + (4 * c + i) * 2048) = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
@@ -375,85 +425,89 @@ __device__ __noinline__ void tc_fresh_value(const AttendArgs& a, int b, int h, i
 // so that the largest element lies in [128, 256); where the rows' largest elements
 // lie more than 2^8 apart, each row gets its own (an element is off by 2^-25 at
 // most: 2^-24 of its row's largest with one power of two, 2^-32 with its own).
+// (What runs once a triple is short loops: its code has left the instruction
+// caches by then, and a line of it takes as long to fetch as ten hot instructions
+// an instruction.  Unrolled, this function took 15,000 clocks.)
 template <int D, int NC>
-__device__ __noinline__ void tc_load_q(const AttendArgs& a, int b, int h, int row0, int rows, int qb, int fb, unsigned char* smem, TcBars* bar) {
+__device__ __noinline__ void tc_load_q(const AttendArgs& args, int b, int h, int row0, int rows, int qb, int fb, unsigned char* smem, TcBars* bar) {
   using L = TcLayout<D, NC>;
-  constexpr int PER = D / 16;            // threads of a row, 16 elements each
-  constexpr int STEP = 128 / PER, U = NC / STEP < 4 ? (NC / STEP < 1 ? 1 : NC / STEP) : 4;
-  const int tid = threadIdx.x - 32 * L::SOFT, part = tid % PER, quad = tid >> 5;
+  const AttendArgs a = args;
+  // Four threads of a warp have a row, eight lanes eight rows (so that they access
+  // different banks); a thread has W columns of core matrices.
+  constexpr int W = D / 32;
+  const int tid = threadIdx.x - 32 * L::SOFT, part = (tid >> 3) & 3, quad = tid >> 5, r0 = 8 * quad + (tid & 7);
+  unsigned char* to = smem + L::q + qb * L::q_bytes + W * part * (NC * 16);
+  float* factor = reinterpret_cast<float*>(smem + L::factor) + fb * NC;
+  // as they are
+#pragma unroll 1
+  for (int r = r0; r < NC; r += 32) {
+    const bool there = row0 + r < rows;
+    const uint16_t* p = a.q + at_row(a, b, h, there ? row0 + r : row0) * D + part * (D / 4);
+    const uint32_t at = smem_addr(to + r * 16);
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at + i * (NC * 16)), "l"(p + 8 * i), "r"(there ? 16 : 0) : "memory");
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  // the rows' largest elements, in the factors' place
   float hi = 0.f, lo = __builtin_huge_valf();
   bool odd = false;
 #pragma unroll 1
-  for (int pass = 0; pass < 2; ++pass) {
-    float common = 0.f;
-    if (pass == 1) {
-      // over the four warps
+  for (int r = r0; r < NC; r += 32) {
+    uint32_t m = 0u;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-      }
-      odd = __any_sync(0xffffffffu, odd);
-      if ((tid & 31) == 0) {
-        bar->qmax[quad] = odd ? __builtin_huge_valf() : hi;
-        bar->qmin[quad] = lo;
-      }
-      named_bar_sync(6, 128);
-      hi = fmaxf(fmaxf(bar->qmax[0], bar->qmax[1]), fmaxf(bar->qmax[2], bar->qmax[3]));
-      lo = fminf(fminf(bar->qmin[0], bar->qmin[1]), fminf(bar->qmin[2], bar->qmin[3]));
-      common = hi < __builtin_huge_valf() && hi > 0.f && hi <= lo * 256.f ? hi : 0.f;
-      if (tid == 0) {
-        const int sh = min(7 - (static_cast<int>(__float_as_uint(common) >> 23) - 127), 100);
-        bar->common[fb] = common == 0.f ? 0.f
-                                        : fmaxf(fabsf(a.scale_log2) * a.k_mul * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23), 1.17549435e-38f);
-      }
+    for (int i = 0; i < W; ++i) {
+      const uint4 x = *reinterpret_cast<const uint4*>(to + r * 16 + i * (NC * 16));
+      m = bf16x2_max_nan(m, bf16x2_max_nan(bf16x2_max_nan(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), bf16x2_max_nan(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
     }
+#pragma unroll
+    for (int o = 8; o < 32; o <<= 1) m = bf16x2_max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float top = fmax_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+    odd |= !(top < __builtin_huge_valf());
+    hi = fmaxf(hi, top);
+    if (top > 0.f) lo = fminf(lo, top);
+    if (part == 0) factor[r] = top;
+  }
+  // over the four warps
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+  }
+  odd = __any_sync(0xffffffffu, odd);
+  if ((tid & 31) == 0) {
+    bar->qmax[quad] = odd ? __builtin_huge_valf() : hi;
+    bar->qmin[quad] = lo;
+  }
+  named_bar_sync(6, 128);
+  hi = fmaxf(fmaxf(bar->qmax[0], bar->qmax[1]), fmaxf(bar->qmax[2], bar->qmax[3]));
+  lo = fminf(fminf(bar->qmin[0], bar->qmin[1]), fminf(bar->qmin[2], bar->qmin[3]));
+  const float common = hi < __builtin_huge_valf() && hi > 0.f && hi <= lo * 256.f ? hi : 0.f;
+  // in place, times the power of two that takes the largest to [128, 256); the
+  // factor is what takes the products back, with the scale
+  auto power = [](float top) { return top > 0.f ? min(7 - (static_cast<int>(__float_as_uint(top) >> 23) - 127), 100) : 0; };
+  auto mult = [&](int e) { return copysignf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23), a.scale_log2); };
+  auto back = [&](int e) { return fmaxf(fabsf(a.scale_log2) * a.k_mul * __uint_as_float(static_cast<uint32_t>(127 - e) << 23), 1.17549435e-38f); };
+  float mul = mult(power(common)), f = back(power(common));
+  if (tid == 0) bar->common[fb] = common > 0.f ? f : 0.f;
 #pragma unroll 1
-    for (int r0 = tid / PER; r0 < NC; r0 += STEP * U) {
-      uint4 x[U], y[U];
-#pragma unroll
-      for (int k = 0; k < U; ++k) {
-        const int r = r0 + k * STEP;
-        x[k] = y[k] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < NC && row0 + r < rows) {
-          const uint4* p = reinterpret_cast<const uint4*>(a.q + at_row(a, b, h, row0 + r) * D + part * 16);
-          x[k] = __ldg(p);
-          y[k] = __ldg(p + 1);
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < U; ++k) {
-        const int r = r0 + k * STEP;
-        const uint32_t w[8] = {x[k].x, x[k].y, x[k].z, x[k].w, y[k].x, y[k].y, y[k].z, y[k].w};
-        uint32_t m = 0u;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) m = bf16x2_max_nan(m, w[i] & 0x7fff7fffu);
-        float top = fmax_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
-#pragma unroll
-        for (int o = 1; o < PER; o <<= 1) top = fmax_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if (pass == 0) {
-          odd |= !(top < __builtin_huge_valf());
-          hi = fmaxf(hi, top);
-          if (top > 0.f) lo = fminf(lo, top);
-          continue;
-        }
-        const float by = common > 0.f ? common : top;
-        const int sh = by > 0.f ? min(7 - (static_cast<int>(__float_as_uint(by) >> 23) - 127), 100) : 0;
-        const float mul = copysignf(__uint_as_float(static_cast<uint32_t>(127 + sh) << 23), a.scale_log2);
-        uint32_t f[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = f16x2_pack(__uint_as_float(w[i] << 16) * mul, __uint_as_float(w[i] & 0xffff0000u) * mul);
-        if (r >= NC) continue;
-        unsigned char* to = smem + L::q + qb * L::q_bytes + r * 16;
-        *reinterpret_cast<uint4*>(to + (2 * part) * (NC * 16)) = make_uint4(f[0], f[1], f[2], f[3]);
-        *reinterpret_cast<uint4*>(to + (2 * part + 1) * (NC * 16)) = make_uint4(f[4], f[5], f[6], f[7]);
-        if (part == 0)
-          reinterpret_cast<float*>(smem + L::factor)[fb * NC + r] =
-              top < __builtin_huge_valf()
-                  ? fmaxf(fabsf(a.scale_log2) * a.k_mul * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23), 1.17549435e-38f)
-                  : __int_as_float(0x7fc00000);
-      }
+  for (int r = r0; r < NC; r += 32) {
+    if (TC_RARE(common == 0.f)) {
+      const float top = factor[r];
+      __syncwarp();   // (the threads of a row are in one warp)
+      mul = mult(power(top));
+      f = top < __builtin_huge_valf() ? back(power(top)) : __int_as_float(0x7fc00000);
     }
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      uint4* at = reinterpret_cast<uint4*>(to + r * 16 + i * (NC * 16));
+      const uint4 w = *at;
+      *at = make_uint4(f16x2_pack(__uint_as_float(w.x << 16) * mul, __uint_as_float(w.x & 0xffff0000u) * mul),
+                       f16x2_pack(__uint_as_float(w.y << 16) * mul, __uint_as_float(w.y & 0xffff0000u) * mul),
+                       f16x2_pack(__uint_as_float(w.z << 16) * mul, __uint_as_float(w.z & 0xffff0000u) * mul),
+                       f16x2_pack(__uint_as_float(w.w << 16) * mul, __uint_as_float(w.w & 0xffff0000u) * mul));
+    }
+    if (part == 0) factor[r] = f;
   }
   named_bar_sync(6, 128);   // qmax and qmin are free again
 }
@@ -461,8 +515,9 @@ __device__ __noinline__ void tc_load_q(const AttendArgs& a, int b, int h, int ro
 // Scores of a tile with fresh entries out of range, on the CUDA cores, into the
 // products' place in tensor memory: this thread's node, the rows from col0.
 template <int D, int NC>
-__device__ __noinline__ void tc_wide_scores(const AttendArgs& a, int b, int h, int row0, int rows, int node, int col0, int cols,
+__device__ __noinline__ void tc_wide_scores(const AttendArgs& args, int b, int h, int row0, int rows, int node, int col0, int cols,
                                             const float* factor, uint32_t addr) {
+  const AttendArgs a = args;
   for (int c = 0; c < cols; ++c) {
     float s = 0.f;
     const int r = row0 + col0 + c;
@@ -481,8 +536,9 @@ __device__ __noinline__ void tc_wide_scores(const AttendArgs& a, int b, int h, i
 // Adds the fresh values out of range to O^T: this thread's column d, the rows from
 // col0; weights (negative: the row does not see the node) at w[node][NC].
 template <int D, int NC>
-__device__ __noinline__ void tc_wide_values(const AttendArgs& a, int b, int h, int node0, int left, int d, int col0, int cols,
+__device__ __noinline__ void tc_wide_values(const AttendArgs& args, int b, int h, int node0, int left, int d, int col0, int cols,
                                             const float* w, uint32_t addr) {
+  const AttendArgs a = args;
   for (int j = 0; j < left; ++j) {
     float v = 0.f;
     if (d < D)
@@ -548,7 +604,12 @@ __device__ __noinline__ void tc_raise(uint32_t s_at, uint32_t o_at, const float*
   float z[CH];
   tc_ld<CH>(s_at, z);
 #pragma unroll
-  for (int i = 0; i < CH; ++i) z[i] = (hide >> i) & 1u ? kNegInf : fmaxf(z[i] * factor[i], kNegInf);   // (no NaN)
+  for (int i = 0; i < CH; i += 4) {
+    const float4 x = *reinterpret_cast<const float4*>(factor + i);
+    const float f[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) z[i + k] = (hide >> (i + k)) & 1u ? kNegInf : fmaxf(z[i + k] * f[k], kNegInf);   // (no NaN)
+  }
   const float mx = tc_reduce<CH, false>(z);
   if (lane < CH) top[quad * NC + lane] = mx;
   named_bar_sync(id, 128);
@@ -574,27 +635,46 @@ __device__ __noinline__ void tc_raise(uint32_t s_at, uint32_t o_at, const float*
   }
 }
 
+// Where the 128 threads of a half of the rows leave their sums of weights of row c,
+// a token each: in the weights' buffers (p: the half's part of the first), which
+// nothing reads by then.
+template <int D, int NC>
+__device__ __forceinline__ float* tc_sums(const unsigned char* p, int c) {
+  using L = TcLayout<D, NC>;
+  return reinterpret_cast<float*>(const_cast<unsigned char*>(p) + c / (L::HC / 2) * L::p_bytes) + c % (L::HC / 2) * 128;
+}
+
 // The end of a triple, or of its part in the share: the sums of weights over the
-// four warps of a part of the rows, then O^T row by row, as the result or (not
+// tokens' threads, then O^T row by row, as the result or (not
 // whole) as a partial.
 template <int D, int NC>
-__device__ __noinline__ void tc_finish(const AttendArgs& a, int b, int h, int row0, int rows, bool whole, float* partial, const float* l,
+__device__ __noinline__ void tc_finish(const AttendArgs& args, int b, int h, int row0, int rows, bool whole, float* partial, const unsigned char* p,
                                        const float* shift, float* corr, float* top, long long* place, uint32_t o_at, int part) {
-  constexpr int HC = TcLayout<D, NC>::HC, CH = TcLayout<D, NC>::CH;
+  const AttendArgs a = args;
+  constexpr int HC = TcLayout<D, NC>::HC;
   const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, col0 = part * HC, id = 1 + part, d = 32 * quad + lane;
   tc_fence_after();
-#pragma unroll 1
-  for (int c0 = 0; c0 < HC; c0 += CH) {
-    float z[CH];
+  named_bar_sync(id, 128);
+  {
+    // 128 / HC threads add up a row, rotated so that the lanes read different banks
+    constexpr int TOK = HC, PER = TOK < 32 ? TOK : 32;   // tokens of a thread: 128 / (128 / HC)
+    const int tid = threadIdx.x & 127, c = tid % HC, t0 = tid / HC * TOK;
+    const float* from = tc_sums<D, NC>(p, c) + t0;
+    float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+    for (int t = 0; t < TOK; t += 4)
 #pragma unroll
-    for (int i = 0; i < CH; ++i) z[i] = l[c0 + i];
-    const float sum = tc_reduce<CH, true>(z);
-    if (lane < CH) top[quad * NC + c0 + lane] = sum;
+      for (int k = 0; k < 4; ++k) x[k] += from[((t + k) & ~(PER - 1)) + ((t + k + c) & (PER - 1))];
+    float sum = (x[0] + x[1]) + (x[2] + x[3]);
+#pragma unroll
+    for (int o = HC; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (HC >= 32 || lane < HC) top[(HC >= 32 ? tid / HC : quad) * NC + c] = sum;
   }
   named_bar_sync(id, 128);
+#pragma unroll 1
   for (int i = threadIdx.x & 127; i < HC; i += 128) {
     place[i] = at_row(a, b, h, min(row0 + col0 + i, rows - 1)) * D;
-    const float sum = (top[i] + top[NC + i]) + (top[2 * NC + i] + top[3 * NC + i]);
+    const float sum = HC == 64 ? top[i] + top[NC + i] : (top[i] + top[NC + i]) + (top[2 * NC + i] + top[3 * NC + i]);
     const int r = row0 + col0 + i;
     const float ref = -shift[i];
     corr[i] = sum == 0.f ? 0.f : a.v_mul / sum;
@@ -616,9 +696,15 @@ __device__ __noinline__ void tc_finish(const AttendArgs& a, int b, int h, int ro
     tc_ld<8>(o_at + c0, o);
     if (d >= D) continue;
     if (whole) {
+      const float4 f0 = *reinterpret_cast<const float4*>(corr + c0), f1 = *reinterpret_cast<const float4*>(corr + c0 + 4);
+      const float f[8] = {f0.x, f0.y, f0.z, f0.w, f1.x, f1.y, f1.z, f1.w};
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (c0 + i < real) a.out[place[c0 + i] + d] = static_cast<uint16_t>(bf16x2_pack(o[i] * corr[c0 + i], 0.f));
+      for (int i = 0; i < 8; i += 2) {
+        const longlong2 at = *reinterpret_cast<const longlong2*>(place + c0 + i);
+        const uint32_t two = bf16x2_pack(o[i] * f[i], o[i + 1] * f[i + 1]);
+        if (c0 + i < real) a.out[at.x + d] = static_cast<uint16_t>(two);
+        if (c0 + i + 1 < real) a.out[at.y + d] = static_cast<uint16_t>(two >> 16);
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) partial[static_cast<size_t>(col0 + c0 + i) * D + d] = o[i];
@@ -666,7 +752,7 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
   if (blockIdx.x >= ctas) return;
   const long long u0 = at_start(units, ctas, blockIdx.x);
   const int ntiles = static_cast<int>(at_start(units, ctas, blockIdx.x + 1) - u0);
-  const int rows = a.N * a.G, nfresh = a.k_new ? (a.N + TC_TILE - 1) / TC_TILE : 0;
+  const int rows = a.N * a.G, nfresh = at_fresh_units(a);
   if (warp == L::SOFT + L::UNPACK) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&bar->tmem)), "r"(L::t_cols)
                  : "memory");
@@ -721,7 +807,16 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
       } else {
         page_at = -1;
       }
-      if (++u >= ntiles) break;
+      // what the other warps load themselves is asked for as the copies come to it
+      if (t.first)
+        for (int r = lane; r < NC && t.row0 + r < rows; r += 32) tc_prefetch<D>(a.q + at_row(a, t.c.b, t.h, t.row0 + r) * D);
+      if (t.kind == TC_FRESH)
+        for (int j = lane; j < t.left; j += 32) {
+          const long long at = ((static_cast<long long>(t.c.b) * a.N + t.at + j) * a.Hkv + t.h) * D;
+          tc_prefetch<D>(a.k_new + at);
+          tc_prefetch<D>(a.v_new + at);
+        }
+      if ((u += t.step) >= ntiles) break;
       tc_step<NC>(a, prefix, HR, nfresh, ntiles - u, t);
     }
     // copies still on their way land before the CTA ends (or the wait gives up)
@@ -751,7 +846,10 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
       bool ok = true;
       for (int u = 0;;) {
         const int x = n & 1, qb = tri % L::QB;
-        if (t.first) ok = tc_wait_one(&bar->qready[qb], (tri / L::QB) & 1, bar, limit);
+        if (t.first) {   // (the triple before is finished beside the load of the queries)
+          if (n > 0) ok = add_v(n - 1, pfirst, ptri);
+          ok = ok && tc_wait_one(&bar->qready[qb], (tri / L::QB) & 1, bar, limit);
+        }
         ok = ok && tc_wait_one(&bar->kready[x], (n >> 1) & 1, bar, limit);
         if (ok && n >= 2) ok = tc_wait_one(&bar->sfree[x], ((n >> 1) & 1) ^ 1, bar, limit);
         if (!ok) break;
@@ -762,13 +860,13 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
           tc_mma_ts(tmem + L::t_s + x * NC, tmem + L::t_k + x * (D / 2) + ks * 8, qd + ks * (2 * NC), id_s, ks > 0);
         tc_commit(&bar->sready[x]);   // (and K's buffer is free)
         if (t.last) tc_commit(&bar->qfree[qb]);
-        if (n > 0) ok = add_v(n - 1, pfirst, ptri);
+        if (n > 0 && !t.first) ok = add_v(n - 1, pfirst, ptri);
         if (!ok) break;
         pfirst = t.first;
         ptri = tri;
         if (t.last) ++tri;
         ++n;
-        if (++u >= ntiles) {
+        if ((u += t.step) >= ntiles) {
           add_v(n - 1, pfirst, ptri);
           break;
         }
@@ -867,7 +965,7 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
       }
       if (t.kind == TC_CACHED) ++copies;
       ++n;
-      if (++u >= ntiles) break;
+      if ((u += t.step) >= ntiles) break;
       tc_step<NC>(a, prefix, HR, nfresh, ntiles - u, t);
     }
   } else {
@@ -1011,11 +1109,11 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
       }
       if (TC_RARE(t.last)) {
         alive = tc_wait(&bar->pvdone[x], (n >> 1) & 1, bar, limit) && alive;
-        float z[HC];
+        unsigned char* sums = tc_smem + L::p + col0 / 8 * 2048;
 #pragma unroll
-        for (int i = 0; i < HC / 2; ++i) f2_unpack(l[i], z[2 * i], z[2 * i + 1]);
-        tc_finish<D, NC>(a, t.c.b, t.h, t.row0, rows, itri == 0 && t.c.i + 1 == t.c.units,
-                         cta_ws + (itri == 0 ? static_cast<size_t>(NC) * (D + 4) : 0), z, shift, corr, top,
+        for (int i = 0; i < HC / 2; ++i) f2_unpack(l[i], tc_sums<D, NC>(sums, 2 * i)[tok], tc_sums<D, NC>(sums, 2 * i + 1)[tok]);
+        tc_finish<D, NC>(a, t.c.b, t.h, t.row0, rows, itri == 0 && t.ends,
+                         cta_ws + (itri == 0 ? static_cast<size_t>(NC) * (D + 4) : 0), sums, shift, corr, top,
                          reinterpret_cast<long long*>(tc_smem + L::rows) + col0, o_at, part);
         tc_fence_before();
         __syncwarp();
@@ -1024,7 +1122,7 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
         named_bar_sync(id, 128);   // top, corr and shift are free again
       }
       ++n;
-      if (++u >= ntiles) break;
+      if ((u += t.step) >= ntiles) break;
       tc_step<NC>(a, prefix, HR, nfresh, ntiles - u, t);
     }
   }
@@ -1038,7 +1136,7 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
     for (int u = 0;;) {
       if (t.first) i0 = t.c.i;
       if (t.last) {
-        const bool whole = i0 == 0 && t.c.i + 1 == t.c.units;
+        const bool whole = i0 == 0 && t.ends;
         float* part = cta_ws + (i0 == 0 ? static_cast<size_t>(NC) * (D + 4) : 0);
         for (int e = threadIdx.x; e < NC * D; e += L::THREADS) {
           const int r = e / D, d = e - r * D;
@@ -1052,7 +1150,7 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
           }
         }
       }
-      if (++u >= ntiles) break;
+      if ((u += t.step) >= ntiles) break;
       tc_step<NC>(a, prefix, HR, nfresh, ntiles - u, t);
     }
   }
