@@ -51,9 +51,9 @@ constexpr uint32_t TC_VBUF = 128 * 128 * 2;  // bytes of a V buffer (16 groups o
 
 template <int D, int NC>
 struct TcLayout {
-  static constexpr int HC = NC / 2;                            // rows of a softmax thread
+  static constexpr int SOFT = NC == 128 ? 16 : 8;               // softmax warps: four for each part of the rows
+  static constexpr int HC = 4 * NC / SOFT;                     // rows of a softmax thread
   static constexpr int CH = HC < 32 ? HC : 32;                 // of them at a time
-  static constexpr int SOFT = 8;                               // softmax warps: four for each half of the rows
   // Unpacking: four warps for keys and four for values; at NC = 128, where the
   // softmax is what takes longest and needs the registers, four for both.
   static constexpr int UNPACK = NC == 128 ? 4 : 8;
