@@ -52,8 +52,7 @@ constexpr uint32_t TC_VBUF = 128 * 128 * 2;  // bytes of a V buffer (16 groups o
 template <int D, int NC>
 struct TcLayout {
   static constexpr int SOFT = NC == 128 ? 16 : 8;               // softmax warps: four for each part of the rows
-  static constexpr int HC = 4 * NC / SOFT;                     // rows of a softmax thread
-  static constexpr int CH = HC < 32 ? HC : 32;                 // of them at a time
+  static constexpr int HC = 4 * NC / SOFT, CH = HC;            // rows of a softmax thread: 32
   // Unpacking: four warps for keys and four for values; at NC = 128, where the
   // softmax is what takes longest and needs the registers, four for both.
   static constexpr int UNPACK = NC == 128 ? 4 : 8;
@@ -259,8 +258,8 @@ struct TcTile {
 enum { TC_CACHED = 0, TC_FRESH = 1, TC_VOID = 2 };   // void: a length out of range (left = 1), or nothing at all (left = 0)
 
 // A triple's first fresh tile stands for a.fresh units, every other tile for one
-// (nfresh: units of the fresh tiles).  A share that begins within those has a tile
-// of nothing first.
+// (nfresh: units of the fresh tiles).  A share that begins within those units has a
+// tile of nothing first.
 template <int NC>
 __device__ __noinline__ void tc_open_slow(const AttendArgs& args, int nfresh, TcTile& t) {
   const AttendArgs a = args;
@@ -271,15 +270,16 @@ __device__ __noinline__ void tc_open_slow(const AttendArgs& args, int nfresh, Tc
   if (!at_len_ok(a, t.c.len)) {
     t.kind = TC_VOID;
     t.left = 1;
-  } else if (t.c.i > 0 && t.c.i < nfresh && t.c.i < a.fresh) {
-    t.kind = TC_VOID;
-    t.left = 0;
-    t.step = a.fresh - t.c.i;
   } else if (t.c.i < nfresh) {
-    t.kind = TC_FRESH;
-    if (t.c.i == 0) t.step = a.fresh;
-    else t.at = (t.c.i - a.fresh + 1) * TC_TILE;
+    const int j = t.c.i < a.fresh ? 0 : t.c.i - a.fresh + 1;
+    t.at = j * TC_TILE;
     t.left = min(a.N - t.at, TC_TILE);
+    t.kind = TC_FRESH;
+    t.step = t.c.i < a.fresh ? a.fresh - t.c.i : 1;
+    if (t.c.i > 0 && j == 0) {
+      t.kind = TC_VOID;
+      t.left = 0;
+    }
   } else {
     t.at = (t.c.i - nfresh) * TC_TILE;
     t.left = min(t.c.len - t.at, TC_TILE);
@@ -360,68 +360,80 @@ __device__ __forceinline__ void tc_prefetch(const uint16_t* p) {
   for (int i = 0; i < D; i += 64) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i));
 }
 
-// A fresh node's key into its lane of tensor memory.  True when an element of the
-// key or of the value does not fit (the tile's scores then are not taken from here).
+// Rows of fresh nodes (128 threads, `left` nodes of 128, zeros for the others; from:
+// the first one's, `stride` elements from node to node) by
+// asynchronous copies to where a value buffer has them, as they are: chunk j of 8
+// elements of node n at j * 2048 + n * 16.  Eight lanes take eight nodes, which lie
+// in different banks; a thread afterwards has a node's chunks to itself.
 template <int D>
-__device__ __noinline__ bool tc_fresh_key(const AttendArgs& args, int b, int h, int node, bool mine, uint32_t k_at) {
-  const AttendArgs a = args;
-  const long long at = ((static_cast<long long>(b) * a.N + (mine ? node : 0)) * a.Hkv + h) * D;
-  const uint4 *k = reinterpret_cast<const uint4*>(a.k_new + at), *v = reinterpret_cast<const uint4*>(a.v_new + at);
-  const float kmul = __fdiv_rn(1.f, a.k_mul), vmul = __fdiv_rn(1.f, a.v_mul);
-  uint32_t kmost = 0u, vmost = 0u;
+__device__ __forceinline__ void tc_fresh_copy(const uint16_t* from, int stride, int left, unsigned char* to, int id) {
+  const int tid = threadIdx.x & 127, n0 = 8 * (tid >> 5) + (tid & 7), part = (tid >> 3) & 3;
 #pragma unroll 1
-  for (int c = 0; c < D / 32; ++c) {
-    uint4 x[8];
+  for (int n = n0; n < TC_TILE; n += 32) {
+    const bool there = n < left;
+    const uint16_t* p = from + static_cast<long long>(there ? n : 0) * stride + part * (D / 4);
+    const uint32_t at = smem_addr(to + part * (D / 32) * 2048 + n * 16);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[i] = mine ? __ldg(k + 4 * c + i) : make_uint4(0u, 0u, 0u, 0u);
-      x[4 + i] = mine ? __ldg(v + 4 * c + i) : make_uint4(0u, 0u, 0u, 0u);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      kmost = tc_most(kmost, x[i]);
-      vmost = tc_most(vmost, x[4 + i]);
-    }
-    uint32_t r[16];
-    tc_narrow(x[0], x[1], kmul, r);
-    tc_narrow(x[2], x[3], kmul, r + 8);
-    __syncwarp();
-    tc_st16(k_at + c * 16, r);
+    for (int i = 0; i < D / 32; ++i)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at + i * 2048), "l"(p + 8 * i), "r"(there ? 16 : 0) : "memory");
   }
-  return !tc_fits(kmost, kmul) || !tc_fits(vmost, vmul);
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  named_bar_sync(id, 128);
 }
-// its value into shared memory (0 for what does not fit)
+
+// A fresh tile's keys into tensor memory, a thread a node, its lane; they pass
+// through the values' buffer.  True when an element does not fit (the tile's scores
+// then are not taken from here).
 template <int D>
-__device__ __noinline__ void tc_fresh_value(const AttendArgs& args, int b, int h, int node, bool mine, unsigned char* vb) {
-  const AttendArgs a = args;
-  const long long at = ((static_cast<long long>(b) * a.N + (mine ? node : 0)) * a.Hkv + h) * D;
-  const uint4* v = reinterpret_cast<const uint4*>(a.v_new + at);
-  const float vmul = __fdiv_rn(1.f, a.v_mul);
+__device__ __noinline__ bool tc_fresh_key(const uint16_t* from, int stride, int left, float k_mul, uint32_t k_at, unsigned char* vbuf) {
+  const float mul = __fdiv_rn(1.f, k_mul);
+  unsigned char* mine = vbuf + (threadIdx.x & 127) * 16;
+  tc_fresh_copy<D>(from, stride, left, vbuf, 6);
+  uint32_t most = 0u;
 #pragma unroll 1
   for (int c = 0; c < D / 32; ++c) {
     uint4 x[4];
-    uint32_t most = 0u;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      x[i] = mine ? __ldg(v + 4 * c + i) : make_uint4(0u, 0u, 0u, 0u);
+      x[i] = *reinterpret_cast<const uint4*>(mine + (4 * c + i) * 2048);
       most = tc_most(most, x[i]);
     }
-    if (TC_RARE(!tc_fits(most, vmul))) {
-      uint4 y[4] = {x[0], x[1], x[2], x[3]};
-      tc_drop(y, 4, vmul);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] = y[i];
-    }
     uint32_t r[16];
-    tc_narrow(x[0], x[1], vmul, r);
-    tc_narrow(x[2], x[3], vmul, r + 8);
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      *reinterpret_cast<uint4*>(vb + (4 * c + i) * 2048) = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+    tc_narrow(x[0], x[1], mul, r);
+    tc_narrow(x[2], x[3], mul, r + 8);
+    __syncwarp();
+    tc_st16(k_at + c * 16, r);
   }
+  return !tc_fits(most, mul);
+}
+// Its values, in place; 0 for what does not fit.  id: the threads' barrier.
+template <int D>
+__device__ __noinline__ bool tc_fresh_value(const uint16_t* from, int stride, int left, float v_mul, unsigned char* vbuf, int id) {
+  const float mul = __fdiv_rn(1.f, v_mul);
+  unsigned char* mine = vbuf + (threadIdx.x & 127) * 16;
+  tc_fresh_copy<D>(from, stride, left, vbuf, id);
+  uint32_t all = 0u;
+#pragma unroll 2
+  for (int j = 0; j < D / 8; j += 2) {
+    uint4* at[2] = {reinterpret_cast<uint4*>(mine + j * 2048), reinterpret_cast<uint4*>(mine + (j + 1) * 2048)};
+    uint4 x[2] = {*at[0], *at[1]};
+    const uint32_t most = tc_most(tc_most(0u, x[0]), x[1]);
+    all = bf16x2_max_nan(all, most);
+    if (TC_RARE(!tc_fits(most, mul))) {
+      uint4 y[2] = {x[0], x[1]};
+      tc_drop(y, 2, mul);
+      x[0] = y[0];
+      x[1] = y[1];
+    }
+    uint32_t r[8];
+    tc_narrow(x[0], x[1], mul, r);
+    *at[0] = make_uint4(r[0], r[1], r[2], r[3]);
+    *at[1] = make_uint4(r[4], r[5], r[6], r[7]);
+  }
+  return !tc_fits(all, mul);
 }
 
-// Queries of a row tile (128 threads).  Usually one power of two scales all rows,
+// Queries of a row tile (128 threads; from: the first row's of the kv head).  Usually one power of two scales all rows,
 // so that the largest element lies in [128, 256); where the rows' largest elements
 // lie more than 2^8 apart, each row gets its own (an element is off by 2^-25 at
 // most: 2^-24 of its row's largest with one power of two, 2^-32 with its own).
@@ -429,9 +441,9 @@ __device__ __noinline__ void tc_fresh_value(const AttendArgs& args, int b, int h
 // caches by then, and a line of it takes as long to fetch as ten hot instructions
 // an instruction.  Unrolled, this function took 15,000 clocks.)
 template <int D, int NC>
-__device__ __noinline__ void tc_load_q(const AttendArgs& args, int b, int h, int row0, int rows, int qb, int fb, unsigned char* smem, TcBars* bar) {
+__device__ __noinline__ void tc_load_q(const uint16_t* from, int G, uint32_t by_g, int Hq, float scale_log2, float k_mul, int row0, int rows, int qb,
+                                       int fb, unsigned char* smem, TcBars* bar) {
   using L = TcLayout<D, NC>;
-  const AttendArgs a = args;
   // Four threads of a warp have a row, eight lanes eight rows (so that they access
   // different banks); a thread has W columns of core matrices.
   constexpr int W = D / 32;
@@ -442,7 +454,8 @@ __device__ __noinline__ void tc_load_q(const AttendArgs& args, int b, int h, int
 #pragma unroll 1
   for (int r = r0; r < NC; r += 32) {
     const bool there = row0 + r < rows;
-    const uint16_t* p = a.q + at_row(a, b, h, there ? row0 + r : row0) * D + part * (D / 4);
+    const int x = there ? row0 + r : row0, node = by_g ? static_cast<int>(__umulhi(static_cast<uint32_t>(x), by_g)) : x;
+    const uint16_t* p = from + (static_cast<long long>(node) * Hq + (x - node * G)) * D + part * (D / 4);
     const uint32_t at = smem_addr(to + r * 16);
 #pragma unroll
     for (int i = 0; i < W; ++i)
@@ -486,8 +499,8 @@ __device__ __noinline__ void tc_load_q(const AttendArgs& args, int b, int h, int
   // in place, times the power of two that takes the largest to [128, 256); the
   // factor is what takes the products back, with the scale
   auto power = [](float top) { return top > 0.f ? min(7 - (static_cast<int>(__float_as_uint(top) >> 23) - 127), 100) : 0; };
-  auto mult = [&](int e) { return copysignf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23), a.scale_log2); };
-  auto back = [&](int e) { return fmaxf(fabsf(a.scale_log2) * a.k_mul * __uint_as_float(static_cast<uint32_t>(127 - e) << 23), 1.17549435e-38f); };
+  auto mult = [&](int e) { return copysignf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23), scale_log2); };
+  auto back = [&](int e) { return fmaxf(fabsf(scale_log2) * k_mul * __uint_as_float(static_cast<uint32_t>(127 - e) << 23), 1.17549435e-38f); };
   float mul = mult(power(common)), f = back(power(common));
   if (tid == 0) bar->common[fb] = common > 0.f ? f : 0.f;
 #pragma unroll 1
@@ -762,8 +775,7 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bar->tmem;
-  const unsigned long long limit = a.timeout_ns;
-  float* cta_ws = a.ws + static_cast<size_t>(blockIdx.x) * tc_cta_floats(D, NC);
+    float* cta_ws = a.ws + static_cast<size_t>(blockIdx.x) * tc_cta_floats(D, NC);
 
   if (warp == L::SOFT + L::UNPACK + 1) {
     // ---- copies: up to four blocks a tile, a lane each --------------------------------
@@ -784,7 +796,7 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
         const bool ok = lane >= nblk || (mine >= 0 && mine < a.pages);
         const int s = n % L::STAGES;
         bool go = true;
-        if (n >= L::STAGES) go = tc_wait(&bar->empty[s], ((n / L::STAGES) & 1) ^ 1, bar, limit);
+        if (n >= L::STAGES) go = tc_wait(&bar->empty[s], ((n / L::STAGES) & 1) ^ 1, bar, a.timeout_ns);
         if (!go) break;
         const bool all = __all_sync(0xffffffffu, ok);
         if (lane == 0) bar->arrived[s] = all;
@@ -821,7 +833,7 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
     }
     // copies still on their way land before the CTA ends (or the wait gives up)
     if (*reinterpret_cast<volatile int*>(&bar->dead))
-      for (int i = max(0, n - L::STAGES); i < n; ++i) mbar_wait(&bar->full[i % L::STAGES], (i / L::STAGES) & 1, limit);
+      for (int i = max(0, n - L::STAGES); i < n; ++i) mbar_wait(&bar->full[i % L::STAGES], (i / L::STAGES) & 1, a.timeout_ns);
   } else if (warp == L::SOFT + L::UNPACK) {
     // ---- products: one thread ------------------------------------------------------------
     if (lane == 0) {
@@ -832,9 +844,9 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
       int n = 0, tri = 0, ptri = 0;     // tiles, triples so far; the tile before's triple
       auto add_v = [&](int m, bool first, int tr) {   // O^T += V^T P^T of tile m
         const int x = m & 1;
-        if (!tc_wait_one(&bar->pready[x], (m >> 1) & 1, bar, limit) || !tc_wait_one(&bar->vready[x], (m >> 1) & 1, bar, limit)) return false;
+        if (!tc_wait_one(&bar->pready[x], (m >> 1) & 1, bar, a.timeout_ns) || !tc_wait_one(&bar->vready[x], (m >> 1) & 1, bar, a.timeout_ns)) return false;
         const int ob = tr % L::QB;
-        if (first && tr >= L::QB && !tc_wait_one(&bar->ofree[(tr - L::QB) & 1], ((tr - L::QB) >> 1) & 1, bar, limit)) return false;
+        if (first && tr >= L::QB && !tc_wait_one(&bar->ofree[(tr - L::QB) & 1], ((tr - L::QB) >> 1) & 1, bar, a.timeout_ns)) return false;
         tc_fence_after();
         const uint64_t vd = tc_desc(sbase + L::v + x * TC_VBUF, 128, 2048), pd = tc_desc(sbase + L::p + x * L::p_bytes, 128, 2048);
 #pragma unroll
@@ -848,10 +860,10 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
         const int x = n & 1, qb = tri % L::QB;
         if (t.first) {   // (the triple before is finished beside the load of the queries)
           if (n > 0) ok = add_v(n - 1, pfirst, ptri);
-          ok = ok && tc_wait_one(&bar->qready[qb], (tri / L::QB) & 1, bar, limit);
+          ok = ok && tc_wait_one(&bar->qready[qb], (tri / L::QB) & 1, bar, a.timeout_ns);
         }
-        ok = ok && tc_wait_one(&bar->kready[x], (n >> 1) & 1, bar, limit);
-        if (ok && n >= 2) ok = tc_wait_one(&bar->sfree[x], ((n >> 1) & 1) ^ 1, bar, limit);
+        ok = ok && tc_wait_one(&bar->kready[x], (n >> 1) & 1, bar, a.timeout_ns);
+        if (ok && n >= 2) ok = tc_wait_one(&bar->sfree[x], ((n >> 1) & 1) ^ 1, bar, a.timeout_ns);
         if (!ok) break;
         tc_fence_after();
         const uint64_t qd = tc_desc(sbase + L::q + qb * L::q_bytes, NC * 16, 128);
@@ -873,7 +885,7 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
         tc_step<NC>(a, prefix, HR, nfresh, ntiles - u, t);
       }
       tc_commit(&bar->drain);
-      mbar_wait(&bar->drain, 0, limit);   // nothing is in flight when tensor memory is given back
+      mbar_wait(&bar->drain, 0, a.timeout_ns);   // nothing is in flight when tensor memory is given back
     }
     __syncwarp();
   } else if (warp >= L::SOFT) {
@@ -884,15 +896,17 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
     TcTile t;
     tc_begin<NC>(a, prefix, HR, nfresh, u0, ntiles, t);
     int n = 0, tri = 0, copies = 0;
+    // (A warp whose wait fails goes on in step with the others, as the softmax warps
+    // do: over what the buffers hold, for results that are void.)
     for (int u = 0;;) {
       const int x = n & 1;
       if (TC_RARE(t.first)) {
         if (keys) {
           const int qb = tri % L::QB;
           // (the factors have two buffers, which the softmax warps read to the triple's end)
-          if (tri >= L::QB && !tc_wait(&bar->qfree[qb], ((tri / L::QB) & 1) ^ 1, bar, limit)) break;
-          if (tri >= 2 && !tc_wait(&bar->ofree[tri & 1], ((tri >> 1) & 1) ^ 1, bar, limit)) break;
-          tc_load_q<D, NC>(a, t.c.b, t.h, t.row0, rows, qb, tri & 1, tc_smem, bar);
+          if (tri >= L::QB) tc_wait(&bar->qfree[qb], ((tri / L::QB) & 1) ^ 1, bar, a.timeout_ns);
+          if (tri >= 2) tc_wait(&bar->ofree[tri & 1], ((tri >> 1) & 1) ^ 1, bar, a.timeout_ns);
+          tc_load_q<D, NC>(a.q + at_row(a, t.c.b, t.h, 0) * D, a.G, a.by_g, a.Hkv * a.G, a.scale_log2, a.k_mul, t.row0, rows, qb, tri & 1, tc_smem, bar);
           tc_proxy_fence();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar->qready[qb]);
@@ -900,12 +914,13 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
         ++tri;
       }
       const int stage = copies % L::STAGES;
-      if (t.kind == TC_CACHED && !tc_wait(&bar->full[stage], (copies / L::STAGES) & 1, bar, limit)) break;
+      if (t.kind == TC_CACHED) tc_wait(&bar->full[stage], (copies / L::STAGES) & 1, bar, a.timeout_ns);
       const unsigned char* blk = tc_smem + L::ring + stage * L::stage_bytes + quad * q4_block_bytes(D);
       // A token that counts has its scales; others get 0, and one of a tile that did
       // not come, or of a length out of range, NaN for its key.
       const bool mine = tok < t.left;
       const bool good = t.kind == TC_CACHED && *reinterpret_cast<volatile int*>(&bar->arrived[stage]);
+      auto fresh_at = [&] { return ((static_cast<long long>(t.c.b) * a.N + t.at) * a.Hkv + t.h) * D; };
       auto scales = [&](int from) -> uint64_t {
         if constexpr (D == 128) return *reinterpret_cast<const uint64_t*>(blk + tc_swz<D>(from + lane * 8));
         else return *reinterpret_cast<const uint32_t*>(blk + tc_swz<D>(from + lane * 4));
@@ -915,11 +930,12 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
       // weights of the last one.  (Rolled loops: a warp that is alone on its
       // scheduler waits for its instructions otherwise.)
       if (keys) {
-        if (n >= 2 && !tc_wait(&bar->sready[x], ((n >> 1) & 1) ^ 1, bar, limit)) break;
+        if (n >= 2) tc_wait(&bar->sready[x], ((n >> 1) & 1) ^ 1, bar, a.timeout_ns);
         tc_fence_after();
         const uint32_t k_at = tmem + lane_at + L::t_k + x * (D / 2);
         if (TC_RARE(t.kind == TC_FRESH)) {
-          if (tc_fresh_key<D>(a, t.c.b, t.h, t.at + tok, mine, k_at)) *reinterpret_cast<volatile int*>(&bar->wide[x]) = n + 1;
+          if (n >= 2) tc_wait(&bar->pvdone[x], ((n >> 1) & 1) ^ 1, bar, a.timeout_ns);
+          if (tc_fresh_key<D>(a.k_new + fresh_at(), a.Hkv * D, t.left, a.k_mul, k_at, tc_smem + L::v + x * TC_VBUF)) *reinterpret_cast<volatile int*>(&bar->wide[x]) = n + 1;
         } else {
           uint64_t sc = !mine ? 0ull : good ? scales(32 * D) : 0x7f7f7f7f7f7f7f7full;
 #pragma unroll 1
@@ -937,11 +953,15 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar->kready[x]);
       }
+      if (L::UNPACK == 8 && keys && TC_RARE(t.kind == TC_FRESH)) named_bar_arrive(8, 32 * L::UNPACK);   // the keys have left the values' buffer
       if (values) {
-        if (n >= 2 && !tc_wait(&bar->pvdone[x], ((n >> 1) & 1) ^ 1, bar, limit)) break;
+        if (n >= 2) tc_wait(&bar->pvdone[x], ((n >> 1) & 1) ^ 1, bar, a.timeout_ns);
         unsigned char* vb = tc_smem + L::v + x * TC_VBUF + tok * 16;
         if (TC_RARE(t.kind == TC_FRESH)) {
-          tc_fresh_value<D>(a, t.c.b, t.h, t.at + tok, mine, vb);
+          // (once the keys have left the buffer)
+          named_bar_sync(L::UNPACK == 4 ? 6 : 8, 32 * L::UNPACK);
+          if (tc_fresh_value<D>(a.v_new + fresh_at(), a.Hkv * D, t.left, a.v_mul, tc_smem + L::v + x * TC_VBUF, L::UNPACK == 4 ? 6 : 7))
+            *reinterpret_cast<volatile int*>(&bar->wide[x]) = n + 1;
         } else {
           uint64_t sc = mine && good ? scales(34 * D) : 0ull;
 #pragma unroll 1
@@ -977,27 +997,30 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
     float* corr = reinterpret_cast<float*>(tc_smem + L::corr) + col0;
     float* top = reinterpret_cast<float*>(tc_smem + L::top) + col0;            // [4][NC], the part's columns
     uint32_t* seen = reinterpret_cast<uint32_t*>(tc_smem + L::seen) + quad * NC + col0;
-    unsigned long long l[HC / 2];                                              // sums of weights, two rows each
+    // Sums of weights of two neighbouring tokens: an even lane has the first half of
+    // the rows, an odd one the second (a sum a row and thread beside the 32 scores
+    // would not fit the registers).
+    float l[CH / 2];
+    const bool odd = lane & 1;
     TcTile t;
     tc_begin<NC>(a, prefix, HR, nfresh, u0, ntiles, t);
     int n = 0, tri = 0;
     int itri = t.c.i;
     float common = 0.f;                     // the rows' factor, 0: each its own
     unsigned long long common2 = 0ull;      // what the packed product takes
-    bool alive = true;
     for (int u = 0;;) {
       const int x = n & 1, qb = tri % L::QB;
       const float* factor = reinterpret_cast<const float*>(tc_smem + L::factor) + (tri & 1) * NC + col0;
       if (TC_RARE(t.first)) {
         itri = t.c.i;
 #pragma unroll
-        for (int i = 0; i < HC / 2; ++i) l[i] = 0ull;
+        for (int i = 0; i < CH / 2; ++i) l[i] = 0.f;
         for (int i = threadIdx.x & 127; i < HC; i += 128) shift[i] = __builtin_huge_valf();
         named_bar_sync(id, 128);
       }
       // (A warp whose wait fails goes on in step with the others, which it meets at
       // barriers; every wait then returns at once.)
-      alive = tc_wait(&bar->sready[x], (n >> 1) & 1, bar, limit) && alive;
+      tc_wait(&bar->sready[x], (n >> 1) & 1, bar, a.timeout_ns);
       tc_fence_after();
       const uint32_t s_at = tmem + lane_at + L::t_s + x * NC + col0;
       const uint32_t o_at = tmem + lane_at + L::t_o + qb * NC + col0;
@@ -1010,7 +1033,9 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
       if (TC_RARE(t.kind != TC_CACHED || t.left < TC_TILE)) {
         some = true;
         if (t.kind == TC_FRESH) {
-          // (one answer for the half, whatever the flag does once a wait has failed)
+          // (one answer for the part, whatever the flag does once a wait has failed; the
+          // values have been looked at, too)
+          tc_wait(&bar->vready[x], (n >> 1) & 1, bar, a.timeout_ns);
           wide = tc_any<128>(id, *reinterpret_cast<volatile int*>(&bar->wide[x]) == n + 1);
           if (a.masks) {   // the warp's 32 nodes are one word of each row's mask
             for (int i = lane; i < HC; i += 32) {
@@ -1064,14 +1089,10 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
           for (int i = 0; i < CH; i += 2) m = fmax3_nan(m, y[i], y[i + 1]);
           // (a row without a reference: a score that counts is infinite there)
           if (__builtin_expect(again || !tc_any<128>(id, !(m <= AT_PSHIFT + AT_ABOVE)), 1)) break;
-          if (!t.first) alive = tc_wait(&bar->pvdone[(n - 1) & 1], ((n - 1) >> 1) & 1, bar, limit) && alive;
+          if (!t.first) tc_wait(&bar->pvdone[(n - 1) & 1], ((n - 1) >> 1) & 1, bar, a.timeout_ns);
           tc_raise<CH, NC>(s_at + c0, o_at + c0, factor + c0, shift + c0, corr + c0, top + c0, hide, !t.first, quad, id);
 #pragma unroll
-          for (int i = 0; i < CH; i += 2) {
-            float l0, l1;
-            f2_unpack(l[(c0 + i) / 2], l0, l1);
-            l[(c0 + i) / 2] = f2_pack(l0 * corr[c0 + i], l1 * corr[c0 + i + 1]);
-          }
+          for (int i = 0; i < CH / 2; ++i) l[i] *= corr[(odd ? CH / 2 : 0) + i];
         }
         if (c0 + CH == HC) {
           tc_fence_before();
@@ -1079,17 +1100,18 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
           if (lane == 0) mbar_arrive(&bar->sfree[x]);   // the scores have been read
         }
 #pragma unroll
-        for (int i = 0; i < CH; i += 2) {
-          y[i] = ex2_approx(y[i]);
-          y[i + 1] = ex2_approx(y[i + 1]);
-          l[(c0 + i) / 2] = f2_add(l[(c0 + i) / 2], f2_pack(y[i], y[i + 1]));
+        for (int i = 0; i < CH; ++i) y[i] = ex2_approx(y[i]);
+#pragma unroll
+        for (int i = 0; i < CH / 2; ++i) {
+          const float keep = odd ? y[i + CH / 2] : y[i], give = odd ? y[i] : y[i + CH / 2];
+          l[i] += keep + __shfl_xor_sync(0xffffffffu, give, 1);
         }
         if (TC_RARE(wide)) {   // weights for the values out of range, -1 where the row does not see the node
           float* w = cta_ws + 2 * static_cast<size_t>(NC) * (D + 4) + static_cast<size_t>(tok) * NC + col0 + c0;
 #pragma unroll
           for (int i = 0; i < CH; ++i) __stcg(w + i, (hide >> i) & 1u ? -1.f : y[i]);
         }
-        if (c0 == 0 && n >= 2) alive = tc_wait(&bar->pvdone[x], ((n >> 1) & 1) ^ 1, bar, limit) && alive;
+        if (c0 == 0 && n >= 2) tc_wait(&bar->pvdone[x], ((n >> 1) & 1) ^ 1, bar, a.timeout_ns);
         unsigned char* pb = tc_smem + L::p + x * L::p_bytes + tok * 16 + (col0 + c0) / 8 * 2048;
 #pragma unroll
         for (int i = 0; i < CH; i += 8)
@@ -1102,16 +1124,19 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
       if (lane == 0) mbar_arrive(&bar->pready[x]);
       if (TC_RARE(wide)) {
         named_bar_sync(id, 128);   // the weights are written
-        alive = tc_wait(&bar->pvdone[x], (n >> 1) & 1, bar, limit) && alive;
+        tc_wait(&bar->pvdone[x], (n >> 1) & 1, bar, a.timeout_ns);
         tc_fence_after();
         tc_wide_values<D, NC>(a, t.c.b, t.h, t.at, t.left, tok, col0, HC, cta_ws + 2 * static_cast<size_t>(NC) * (D + 4), o_at);
         tc_fence_before();
       }
       if (TC_RARE(t.last)) {
-        alive = tc_wait(&bar->pvdone[x], (n >> 1) & 1, bar, limit) && alive;
+        tc_wait(&bar->pvdone[x], (n >> 1) & 1, bar, a.timeout_ns);
         unsigned char* sums = tc_smem + L::p + col0 / 8 * 2048;
 #pragma unroll
-        for (int i = 0; i < HC / 2; ++i) f2_unpack(l[i], tc_sums<D, NC>(sums, 2 * i)[tok], tc_sums<D, NC>(sums, 2 * i + 1)[tok]);
+        for (int i = 0; i < CH / 2; ++i) {
+          tc_sums<D, NC>(sums, i)[tok] = odd ? 0.f : l[i];
+          tc_sums<D, NC>(sums, i + CH / 2)[tok] = odd ? l[i] : 0.f;
+        }
         tc_finish<D, NC>(a, t.c.b, t.h, t.row0, rows, itri == 0 && t.ends,
                          cta_ws + (itri == 0 ? static_cast<size_t>(NC) * (D + 4) : 0), sums, shift, corr, top,
                          reinterpret_cast<long long*>(tc_smem + L::rows) + col0, o_at, part);

@@ -155,15 +155,13 @@ spec_status_t launch_attend_tc(const DevInfo& di, int dev, const AttendArgs& a, 
 template <int D>
 spec_status_t launch_attend_tc(int NC, const DevInfo& di, int dev, const AttendArgs& a, cudaStream_t st) {
   switch (NC) {
-    case 16: return launch_attend_tc<D, 16>(di, dev, a, st);
-    case 32: return launch_attend_tc<D, 32>(di, dev, a, st);
     case 64: return launch_attend_tc<D, 64>(di, dev, a, st);
     default: return launch_attend_tc<D, 128>(di, dev, a, st);
   }
 }
 template <int D>
 size_t tc_smem_bytes(int NC) {
-  return NC == 16 ? TcLayout<D, 16>::bytes : NC == 32 ? TcLayout<D, 32>::bytes : NC == 64 ? TcLayout<D, 64>::bytes : TcLayout<D, 128>::bytes;
+  return NC == 64 ? TcLayout<D, 64>::bytes : TcLayout<D, 128>::bytes;
 }
 
 // Which kernel, and its row tile.
@@ -176,7 +174,7 @@ struct AttendPlan {
 constexpr int kTcRows = 33;   // rows from which the tensor cores' kernel is taken: 256 sequences at 2,048 tokens, 32 rows 507 us here against 700 there
 AttendPlan attend_plan(int B, int rows, int D) {
   AttendPlan p{};
-  const int NC = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+  const int NC = rows <= 64 ? 64 : 128;
   const size_t smem = (D == 128 ? tc_smem_bytes<128>(NC) : tc_smem_bytes<64>(NC)) + 1024 + 8 * (static_cast<size_t>(B) + 1);
   p.tc = rows >= kTcRows && smem + 256 <= static_cast<size_t>(kSmemPerSm);
   if (p.tc) {
