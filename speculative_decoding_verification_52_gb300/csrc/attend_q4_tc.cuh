@@ -241,8 +241,9 @@ __device__ __forceinline__ uint32_t tc_swz(uint32_t o) {
   return D == 128 ? o ^ (((o >> 7) & 3u) << 4) : o ^ (((o >> 7) & 1u) << 4);
 }
 
-// (Functions that are not inlined take a copy of the arguments: through the
-// reference each use would read them again after every store.)
+// (Functions that are not inlined and that run for every triple take values, not the
+// kernel's arguments by reference: those are read like global memory, at a few
+// hundred clocks a time.  Chunks of 1,024 tokens took 475 us with the reference.)
 
 // ---------------------------------------------------------------------------
 // the list of tiles of a CTA, walked alike by all roles
@@ -261,21 +262,20 @@ enum { TC_CACHED = 0, TC_FRESH = 1, TC_VOID = 2 };   // void: a length out of ra
 // (nfresh: units of the fresh tiles).  A share that begins within those units has a
 // tile of nothing first.
 template <int NC>
-__device__ __noinline__ void tc_open_slow(const AttendArgs& args, int nfresh, TcTile& t) {
-  const AttendArgs a = args;
-  t.h = t.c.pair / a.row_tiles;
-  t.row0 = (t.c.pair - t.h * a.row_tiles) * NC;
+__device__ __noinline__ void tc_open_slow(int row_tiles, int N, int fresh, bool len_ok, int nfresh, TcTile& t) {
+  t.h = t.c.pair / row_tiles;
+  t.row0 = (t.c.pair - t.h * row_tiles) * NC;
   t.at = 0;
   t.step = 1;
-  if (!at_len_ok(a, t.c.len)) {
+  if (!len_ok) {
     t.kind = TC_VOID;
     t.left = 1;
   } else if (t.c.i < nfresh) {
-    const int j = t.c.i < a.fresh ? 0 : t.c.i - a.fresh + 1;
+    const int j = t.c.i < fresh ? 0 : t.c.i - fresh + 1;
     t.at = j * TC_TILE;
-    t.left = min(a.N - t.at, TC_TILE);
+    t.left = min(N - t.at, TC_TILE);
     t.kind = TC_FRESH;
-    t.step = t.c.i < a.fresh ? a.fresh - t.c.i : 1;
+    t.step = t.c.i < fresh ? fresh - t.c.i : 1;
     if (t.c.i > 0 && j == 0) {
       t.kind = TC_VOID;
       t.left = 0;
@@ -290,7 +290,7 @@ __device__ __noinline__ void tc_open_slow(const AttendArgs& args, int nfresh, Tc
 template <int NC>
 __device__ __forceinline__ void tc_open(const AttendArgs& a, int nfresh, TcTile& t) {
   TcTile x = t;   // (by a copy: the tile itself stays in registers)
-  tc_open_slow<NC>(a, nfresh, x);
+  tc_open_slow<NC>(a.row_tiles, a.N, a.fresh, at_len_ok(a, t.c.len), nfresh, x);
   t = x;
 }
 template <int NC>
@@ -661,9 +661,8 @@ __device__ __forceinline__ float* tc_sums(const unsigned char* p, int c) {
 // tokens' threads, then O^T row by row, as the result or (not
 // whole) as a partial.
 template <int D, int NC>
-__device__ __noinline__ void tc_finish(const AttendArgs& args, int b, int h, int row0, int rows, bool whole, float* partial, const unsigned char* p,
-                                       const float* shift, float* corr, float* top, long long* place, uint32_t o_at, int part) {
-  const AttendArgs a = args;
+__device__ __noinline__ void tc_finish(uint16_t* out, float* lse, long long base, int G, uint32_t by_g, int Hq, float v_mul, int row0, int rows,
+                                       bool whole, float* partial, const unsigned char* p, const float* shift, float* corr, float* top, long long* place, uint32_t o_at, int part) {
   constexpr int HC = TcLayout<D, NC>::HC;
   const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, col0 = part * HC, id = 1 + part, d = 32 * quad + lane;
   tc_fence_after();
@@ -686,13 +685,14 @@ __device__ __noinline__ void tc_finish(const AttendArgs& args, int b, int h, int
   named_bar_sync(id, 128);
 #pragma unroll 1
   for (int i = threadIdx.x & 127; i < HC; i += 128) {
-    place[i] = at_row(a, b, h, min(row0 + col0 + i, rows - 1)) * D;
+    const int x = min(row0 + col0 + i, rows - 1), node = by_g ? static_cast<int>(__umulhi(static_cast<uint32_t>(x), by_g)) : x;
+    place[i] = (base + static_cast<long long>(node) * Hq + (x - node * G)) * D;
     const float sum = HC == 64 ? top[i] + top[NC + i] : (top[i] + top[NC + i]) + (top[2 * NC + i] + top[3 * NC + i]);
     const int r = row0 + col0 + i;
     const float ref = -shift[i];
-    corr[i] = sum == 0.f ? 0.f : a.v_mul / sum;
+    corr[i] = sum == 0.f ? 0.f : v_mul / sum;
     if (whole) {
-      if (r < rows && a.lse) a.lse[place[i] / D] = at_lse(ref, sum);
+      if (r < rows && lse) lse[place[i] / D] = at_lse(ref, sum);
     } else {
       float* ml = partial + static_cast<size_t>(NC) * D + col0 + i;
       ml[0] = ref;
@@ -715,8 +715,8 @@ __device__ __noinline__ void tc_finish(const AttendArgs& args, int b, int h, int
       for (int i = 0; i < 8; i += 2) {
         const longlong2 at = *reinterpret_cast<const longlong2*>(place + c0 + i);
         const uint32_t two = bf16x2_pack(o[i] * f[i], o[i + 1] * f[i + 1]);
-        if (c0 + i < real) a.out[at.x + d] = static_cast<uint16_t>(two);
-        if (c0 + i + 1 < real) a.out[at.y + d] = static_cast<uint16_t>(two >> 16);
+        if (c0 + i < real) out[at.x + d] = static_cast<uint16_t>(two);
+        if (c0 + i + 1 < real) out[at.y + d] = static_cast<uint16_t>(two >> 16);
       }
     } else {
 #pragma unroll
@@ -1137,7 +1137,7 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
           tc_sums<D, NC>(sums, i)[tok] = odd ? 0.f : l[i];
           tc_sums<D, NC>(sums, i + CH / 2)[tok] = odd ? l[i] : 0.f;
         }
-        tc_finish<D, NC>(a, t.c.b, t.h, t.row0, rows, itri == 0 && t.ends,
+        tc_finish<D, NC>(a.out, a.lse, at_row(a, t.c.b, t.h, 0), a.G, a.by_g, a.Hkv * a.G, a.v_mul, t.row0, rows, itri == 0 && t.ends,
                          cta_ws + (itri == 0 ? static_cast<size_t>(NC) * (D + 4) : 0), sums, shift, corr, top,
                          reinterpret_cast<long long*>(tc_smem + L::rows) + col0, o_at, part);
         tc_fence_before();
