@@ -6,31 +6,39 @@
 // fits without padding M:
 //   S^T[128 tokens x NC rows] = K[128 x D] Q^T      (A = K in tensor memory, B = Q)
 //   O^T[128 >= D x NC rows] += V^T[D x 128] P^T     (A = V, B = P in shared memory)
-// NC, the rows of a tile, is 16, 32, 64 or 128.  What this buys beside that:
+// NC, the rows of a tile, is 64 or 128.  What this buys beside that:
 // * a thread of the unpacking warps has one token: it reads the token's codes,
 //   widens them (exactly, in f16, as attend_q4.cuh does) and stores its row of K
 //   straight into its lane of tensor memory; V goes to shared memory in the plain
 //   core-matrix order (8 x 16 bytes), which a warp of tokens writes without
 //   conflicts.  The codes come by tensor-map copies whose 64- or 32-byte swizzle
 //   spreads a warp's reads, one row a lane, over the banks.
-// * a thread of the softmax warps has one token and half of the tile's rows;
-//   the weights go to shared memory the way V does.
+// * a thread of the softmax warps has one token and 32 of the tile's rows; the
+//   weights go to shared memory the way V does.
 // A row's maximum over the tokens would be a reduction across threads in every
 // tile.  Instead the weights are 2^(z - ref + 7) against a reference per row that
 // all threads know; only when some score exceeds its row's reference by 8 (always
 // in a triple's first tile, rarely later) the four warps that have the row agree on
 // new references and rescale their rows of O^T and of the sums.
 //
-// Roles of a CTA (one an SM): four softmax warps for each half of the rows, which
-// also write the results; four or eight warps for the queries and the unpacking; one
-// that issues the products, and one for the copies.  K, S^T, V and P have two buffers each, queries
-// and O^T two where tensor and shared memory hold them (NC <= 64).  Each CTA has
-// one contiguous share of the list of tiles (attend_q4.cuh), with at most two
-// triples cut off at its ends, whose parts the join kernel puts together.
+// Roles of a CTA (one an SM): four softmax warps for each 32 rows, which also write
+// the results; four or eight warps for the queries and the unpacking; one that issues
+// the products, and one for the copies.  K, S^T, V and P have two buffers each,
+// queries and O^T two where tensor and shared memory hold them (NC = 64).  Each CTA
+// has one contiguous share of the list of tiles (attend_q4.cuh), with at most two
+// triples cut off at its ends, whose parts the join kernel puts together.  A triple's
+// first fresh tile counts for nine in the list: with it come the queries, the first
+// references and the triple's end (32 trees of 64 nodes over lengths of 1,024 to
+// 7,168: 725 us when it counted as one, 523 as nine).
 //
 // Bounds, per tile of 128 tokens and D = 128: 784 clocks of the bus; products
 // 1,024 clocks at NC = 128; unpacking 256 conversions, 256 multiplications and 16
-// stores of 16 bytes a thread.
+// stores of 16 bytes a thread.  A tile takes about 3,400 clocks: the softmax of its
+// 16,384 scores, about 240 instructions a warp for 32 rows and 32 tokens, is what
+// takes them, by latency rather than by any unit's rate.  (With 64 rows a thread, in
+// eight warps, it was 4,300: half as many warps to wait with, and 13 KB of code.)
+// 64 sequences of 128 rows at 2,048 tokens take 248 us, where the products at the
+// rate of a large library product would take 37.
 //
 // Fresh entries are converted to f16 in units of the cache's shifts (exact from
 // 2^-14 to 65504 of them, an absolute 2^-25 below, where the cache itself resolves
@@ -47,14 +55,14 @@ namespace sv {
 
 constexpr int TC_TILE = 128;                 // tokens of a tile
 constexpr int TC_FRESH_UNITS = 9;            // what a triple's first fresh tile counts in the list, in cached tiles
+constexpr int TC_PART = 32;                  // rows of a softmax thread
 constexpr uint32_t TC_VBUF = 128 * 128 * 2;  // bytes of a V buffer (16 groups of 8 columns, also for D = 64)
 
 template <int D, int NC>
 struct TcLayout {
-  static constexpr int SOFT = NC == 128 ? 16 : 8;               // softmax warps: four for each part of the rows
-  static constexpr int HC = 4 * NC / SOFT, CH = HC;            // rows of a softmax thread: 32
+  static constexpr int SOFT = NC / 8;                          // softmax warps: four for each part of 32 rows
   // Unpacking: four warps for keys and four for values; at NC = 128, where the
-  // softmax is what takes longest and needs the registers, four for both.
+  // softmax needs the registers, four for both.
   static constexpr int UNPACK = NC == 128 ? 4 : 8;
   static constexpr int WARPS = SOFT + UNPACK + 2, THREADS = 32 * WARPS;
   static constexpr int QB = NC <= 64 ? 2 : 1;                  // buffers of queries and of O^T
@@ -607,7 +615,7 @@ __device__ __noinline__ uint32_t tc_hidden(bool tree, const uint32_t* seen, int 
   return hide;
 }
 
-// New references for CH rows: the 128 threads of a half call this together.
+// New references for CH rows: the 128 threads of a part call this together.
 // s_at: the tile's products (hide: bits of rows that do not see this thread's
 // token), o_at: the rows' sums of v so far, if there are any.
 template <int CH, int NC>
@@ -648,13 +656,13 @@ __device__ __noinline__ void tc_raise(uint32_t s_at, uint32_t o_at, const float*
   }
 }
 
-// Where the 128 threads of a half of the rows leave their sums of weights of row c,
-// a token each: in the weights' buffers (p: the half's part of the first), which
+// Where the 128 threads of a part of the rows leave their sums of weights of row c,
+// a token each: in the weights' buffers (p: the part's share of the first), which
 // nothing reads by then.
 template <int D, int NC>
 __device__ __forceinline__ float* tc_sums(const unsigned char* p, int c) {
   using L = TcLayout<D, NC>;
-  return reinterpret_cast<float*>(const_cast<unsigned char*>(p) + c / (L::HC / 2) * L::p_bytes) + c % (L::HC / 2) * 128;
+  return reinterpret_cast<float*>(const_cast<unsigned char*>(p) + c / (TC_PART / 2) * L::p_bytes) + c % (TC_PART / 2) * 128;
 }
 
 // The end of a triple, or of its part in the share: the sums of weights over the
@@ -662,32 +670,28 @@ __device__ __forceinline__ float* tc_sums(const unsigned char* p, int c) {
 // whole) as a partial.
 template <int D, int NC>
 __device__ __noinline__ void tc_finish(uint16_t* out, float* lse, long long base, int G, uint32_t by_g, int Hq, float v_mul, int row0, int rows,
-                                       bool whole, float* partial, const unsigned char* p, const float* shift, float* corr, float* top, long long* place, uint32_t o_at, int part) {
-  constexpr int HC = TcLayout<D, NC>::HC;
-  const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, col0 = part * HC, id = 1 + part, d = 32 * quad + lane;
+                                       bool whole, float* partial, const unsigned char* p, const float* shift, float* corr, float* top,
+                                       long long* place, uint32_t o_at, int part) {
+  const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, col0 = part * TC_PART, id = 1 + part, d = 32 * quad + lane;
   tc_fence_after();
   named_bar_sync(id, 128);
+  // a warp adds up its 32 tokens of the part's rows, a row a lane, rotated so that
+  // the lanes read different banks
   {
-    // 128 / HC threads add up a row, rotated so that the lanes read different banks
-    constexpr int TOK = HC, PER = TOK < 32 ? TOK : 32;   // tokens of a thread: 128 / (128 / HC)
-    const int tid = threadIdx.x & 127, c = tid % HC, t0 = tid / HC * TOK;
-    const float* from = tc_sums<D, NC>(p, c) + t0;
+    const float* from = tc_sums<D, NC>(p, lane) + 32 * quad;
     float x[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 2
-    for (int t = 0; t < TOK; t += 4)
+    for (int t = 0; t < 32; t += 4)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) x[k] += from[((t + k) & ~(PER - 1)) + ((t + k + c) & (PER - 1))];
-    float sum = (x[0] + x[1]) + (x[2] + x[3]);
-#pragma unroll
-    for (int o = HC; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (HC >= 32 || lane < HC) top[(HC >= 32 ? tid / HC : quad) * NC + c] = sum;
+      for (int k = 0; k < 4; ++k) x[k] += from[(t + k + lane) & 31];
+    top[quad * NC + lane] = (x[0] + x[1]) + (x[2] + x[3]);
   }
   named_bar_sync(id, 128);
-#pragma unroll 1
-  for (int i = threadIdx.x & 127; i < HC; i += 128) {
+  if (quad == 0) {
+    const int i = lane;
     const int x = min(row0 + col0 + i, rows - 1), node = by_g ? static_cast<int>(__umulhi(static_cast<uint32_t>(x), by_g)) : x;
     place[i] = (base + static_cast<long long>(node) * Hq + (x - node * G)) * D;
-    const float sum = HC == 64 ? top[i] + top[NC + i] : (top[i] + top[NC + i]) + (top[2 * NC + i] + top[3 * NC + i]);
+    const float sum = (top[i] + top[NC + i]) + (top[2 * NC + i] + top[3 * NC + i]);
     const int r = row0 + col0 + i;
     const float ref = -shift[i];
     corr[i] = sum == 0.f ? 0.f : v_mul / sum;
@@ -701,9 +705,9 @@ __device__ __noinline__ void tc_finish(uint16_t* out, float* lse, long long base
     }
   }
   named_bar_sync(id, 128);
-  const int real = rows - row0 - col0;   // rows of the half that there are
+  const int real = rows - row0 - col0;   // rows of the part that there are
 #pragma unroll 1
-  for (int c0 = 0; c0 < HC; c0 += 8) {
+  for (int c0 = 0; c0 < TC_PART; c0 += 8) {
     float o[8];
     __syncwarp();
     tc_ld<8>(o_at + c0, o);
@@ -990,7 +994,7 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
     }
   } else {
     // ---- softmax: a thread a token and a part of the rows ---------------------------------------
-    constexpr int HC = L::HC, CH = L::CH;
+    constexpr int HC = TC_PART;
     const int part = warp >> 2, quad = warp & 3, tok = 32 * quad + lane, id = 1 + part, col0 = part * HC;
     const uint32_t lane_at = static_cast<uint32_t>(32 * quad) << 16;
     float* shift = reinterpret_cast<float*>(tc_smem + L::shift) + col0;
@@ -1000,7 +1004,7 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
     // Sums of weights of two neighbouring tokens: an even lane has the first half of
     // the rows, an odd one the second (a sum a row and thread beside the 32 scores
     // would not fit the registers).
-    float l[CH / 2];
+    float l[HC / 2];
     const bool odd = lane & 1;
     TcTile t;
     tc_begin<NC>(a, prefix, HR, nfresh, u0, ntiles, t);
@@ -1014,7 +1018,7 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
       if (TC_RARE(t.first)) {
         itri = t.c.i;
 #pragma unroll
-        for (int i = 0; i < CH / 2; ++i) l[i] = 0.f;
+        for (int i = 0; i < HC / 2; ++i) l[i] = 0.f;
         for (int i = threadIdx.x & 127; i < HC; i += 128) shift[i] = __builtin_huge_valf();
         named_bar_sync(id, 128);
       }
@@ -1029,7 +1033,7 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
         common2 = common == 0.f ? f2_pack(1.f, 1.f) : f2_pack(common, common);
       }
       bool wide = false, some = false;
-      int open = 0;   // in a fresh tile of a chain, the node's first row in the half
+      int open = 0;   // in a fresh tile of a chain, the node's first row in the part
       if (TC_RARE(t.kind != TC_CACHED || t.left < TC_TILE)) {
         some = true;
         if (t.kind == TC_FRESH) {
@@ -1055,69 +1059,64 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
           }
         }
       }
-#pragma unroll
-      for (int c0 = 0; c0 < HC; c0 += CH) {
-        // which of the rows do not see this thread's token
-        uint32_t hide = 0u;
-        if (TC_RARE(some)) {
-          hide = tc_hidden<CH>(t.kind == TC_FRESH && a.masks, seen + c0, open - c0);
-          if (tok >= t.left) hide = ~0u;
-        }
-        const bool hides = some && __any_sync(0xffffffffu, hide != 0u);
-        float y[CH];
-        for (bool again = false;; again = true) {
-          tc_ld<CH>(s_at + c0, y);
-          float m = 0.f;
-          if (TC_RARE(common == 0.f)) {
-#pragma unroll
-            for (int i = 0; i < CH; ++i) y[i] *= factor[c0 + i];
-          }
-          // (one factor for all rows: a value for each row and tile less to read, where
-          // the bandwidth of shared memory is what bounds a tile of many rows)
-#pragma unroll
-          for (int i = 0; i < CH; i += 4) {
-            const float4 s = *reinterpret_cast<const float4*>(shift + c0 + i);
-            f2_unpack(f2_fma(f2_pack(y[i], y[i + 1]), common2, f2_pack(s.x, s.y)), y[i], y[i + 1]);
-            f2_unpack(f2_fma(f2_pack(y[i + 2], y[i + 3]), common2, f2_pack(s.z, s.w)), y[i + 2], y[i + 3]);
-          }
-          if (TC_RARE(hides)) {
-#pragma unroll
-            for (int i = 0; i < CH; ++i)
-              if ((hide >> i) & 1u) y[i] = kNegInf;
-          }
-#pragma unroll
-          for (int i = 0; i < CH; i += 2) m = fmax3_nan(m, y[i], y[i + 1]);
-          // (a row without a reference: a score that counts is infinite there)
-          if (__builtin_expect(again || !tc_any<128>(id, !(m <= AT_PSHIFT + AT_ABOVE)), 1)) break;
-          if (!t.first) tc_wait(&bar->pvdone[(n - 1) & 1], ((n - 1) >> 1) & 1, bar, a.timeout_ns);
-          tc_raise<CH, NC>(s_at + c0, o_at + c0, factor + c0, shift + c0, corr + c0, top + c0, hide, !t.first, quad, id);
-#pragma unroll
-          for (int i = 0; i < CH / 2; ++i) l[i] *= corr[(odd ? CH / 2 : 0) + i];
-        }
-        if (c0 + CH == HC) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&bar->sfree[x]);   // the scores have been read
-        }
-#pragma unroll
-        for (int i = 0; i < CH; ++i) y[i] = ex2_approx(y[i]);
-#pragma unroll
-        for (int i = 0; i < CH / 2; ++i) {
-          const float keep = odd ? y[i + CH / 2] : y[i], give = odd ? y[i] : y[i + CH / 2];
-          l[i] += keep + __shfl_xor_sync(0xffffffffu, give, 1);
-        }
-        if (TC_RARE(wide)) {   // weights for the values out of range, -1 where the row does not see the node
-          float* w = cta_ws + 2 * static_cast<size_t>(NC) * (D + 4) + static_cast<size_t>(tok) * NC + col0 + c0;
-#pragma unroll
-          for (int i = 0; i < CH; ++i) __stcg(w + i, (hide >> i) & 1u ? -1.f : y[i]);
-        }
-        if (c0 == 0 && n >= 2) tc_wait(&bar->pvdone[x], ((n >> 1) & 1) ^ 1, bar, a.timeout_ns);
-        unsigned char* pb = tc_smem + L::p + x * L::p_bytes + tok * 16 + (col0 + c0) / 8 * 2048;
-#pragma unroll
-        for (int i = 0; i < CH; i += 8)
-          *reinterpret_cast<uint4*>(pb + i / 8 * 2048) = make_uint4(f16x2_pack(y[i], y[i + 1]), f16x2_pack(y[i + 2], y[i + 3]),
-                                                                    f16x2_pack(y[i + 4], y[i + 5]), f16x2_pack(y[i + 6], y[i + 7]));
+      // which of the rows do not see this thread's token
+      uint32_t hide = 0u;
+      if (TC_RARE(some)) {
+        hide = tc_hidden<HC>(t.kind == TC_FRESH && a.masks, seen, open);
+        if (tok >= t.left) hide = ~0u;
       }
+      const bool hides = some && __any_sync(0xffffffffu, hide != 0u);
+      float y[HC];
+      for (bool again = false;; again = true) {
+        tc_ld<HC>(s_at, y);
+        float m = 0.f;
+        if (TC_RARE(common == 0.f)) {
+#pragma unroll
+          for (int i = 0; i < HC; ++i) y[i] *= factor[i];
+        }
+        // (one factor for all rows: a value for each row and tile less to read, where
+        // the bandwidth of shared memory is what bounds a tile of many rows)
+#pragma unroll
+        for (int i = 0; i < HC; i += 4) {
+          const float4 s = *reinterpret_cast<const float4*>(shift + i);
+          f2_unpack(f2_fma(f2_pack(y[i], y[i + 1]), common2, f2_pack(s.x, s.y)), y[i], y[i + 1]);
+          f2_unpack(f2_fma(f2_pack(y[i + 2], y[i + 3]), common2, f2_pack(s.z, s.w)), y[i + 2], y[i + 3]);
+        }
+        if (TC_RARE(hides)) {
+#pragma unroll
+          for (int i = 0; i < HC; ++i)
+            if ((hide >> i) & 1u) y[i] = kNegInf;
+        }
+#pragma unroll
+        for (int i = 0; i < HC; i += 2) m = fmax3_nan(m, y[i], y[i + 1]);
+        // (a row without a reference: a score that counts is infinite there)
+        if (__builtin_expect(again || !tc_any<128>(id, !(m <= AT_PSHIFT + AT_ABOVE)), 1)) break;
+        if (!t.first) tc_wait(&bar->pvdone[(n - 1) & 1], ((n - 1) >> 1) & 1, bar, a.timeout_ns);
+        tc_raise<HC, NC>(s_at, o_at, factor, shift, corr, top, hide, !t.first, quad, id);
+#pragma unroll
+        for (int i = 0; i < HC / 2; ++i) l[i] *= corr[(odd ? HC / 2 : 0) + i];
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar->sfree[x]);   // the scores have been read
+#pragma unroll
+      for (int i = 0; i < HC; ++i) y[i] = ex2_approx(y[i]);
+#pragma unroll
+      for (int i = 0; i < HC / 2; ++i) {
+        const float keep = odd ? y[i + HC / 2] : y[i], give = odd ? y[i] : y[i + HC / 2];
+        l[i] += keep + __shfl_xor_sync(0xffffffffu, give, 1);
+      }
+      if (TC_RARE(wide)) {   // weights for the values out of range, -1 where the row does not see the node
+        float* w = cta_ws + 2 * static_cast<size_t>(NC) * (D + 4) + static_cast<size_t>(tok) * NC + col0;
+#pragma unroll
+        for (int i = 0; i < HC; ++i) __stcg(w + i, (hide >> i) & 1u ? -1.f : y[i]);
+      }
+      if (n >= 2) tc_wait(&bar->pvdone[x], ((n >> 1) & 1) ^ 1, bar, a.timeout_ns);
+      unsigned char* pb = tc_smem + L::p + x * L::p_bytes + tok * 16 + col0 / 8 * 2048;
+#pragma unroll
+      for (int i = 0; i < HC; i += 8)
+        *reinterpret_cast<uint4*>(pb + i / 8 * 2048) = make_uint4(f16x2_pack(y[i], y[i + 1]), f16x2_pack(y[i + 2], y[i + 3]),
+                                                                  f16x2_pack(y[i + 4], y[i + 5]), f16x2_pack(y[i + 6], y[i + 7]));
       tc_fence_before();
       tc_proxy_fence();
       __syncwarp();
@@ -1133,9 +1132,9 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
         tc_wait(&bar->pvdone[x], (n >> 1) & 1, bar, a.timeout_ns);
         unsigned char* sums = tc_smem + L::p + col0 / 8 * 2048;
 #pragma unroll
-        for (int i = 0; i < CH / 2; ++i) {
+        for (int i = 0; i < HC / 2; ++i) {
           tc_sums<D, NC>(sums, i)[tok] = odd ? 0.f : l[i];
-          tc_sums<D, NC>(sums, i + CH / 2)[tok] = odd ? l[i] : 0.f;
+          tc_sums<D, NC>(sums, i + HC / 2)[tok] = odd ? l[i] : 0.f;
         }
         tc_finish<D, NC>(a.out, a.lse, at_row(a, t.c.b, t.h, 0), a.G, a.by_g, a.Hkv * a.G, a.v_mul, t.row0, rows, itri == 0 && t.ends,
                          cta_ws + (itri == 0 ? static_cast<size_t>(NC) * (D + 4) : 0), sums, shift, corr, top,

@@ -152,16 +152,12 @@ spec_status_t launch_attend_tc(const DevInfo& di, int dev, const AttendArgs& a, 
   return launch_join<D>(di, a, grid, 1, NC / 8, tc_cta_floats(D, NC), st);
 }
 
-template <int D>
-spec_status_t launch_attend_tc(int NC, const DevInfo& di, int dev, const AttendArgs& a, cudaStream_t st) {
-  switch (NC) {
-    case 64: return launch_attend_tc<D, 64>(di, dev, a, st);
-    default: return launch_attend_tc<D, 128>(di, dev, a, st);
-  }
+spec_status_t launch_attend_tc(int D, int NC, const DevInfo& di, int dev, const AttendArgs& a, cudaStream_t st) {
+  if (D == 64) return launch_attend_tc<64, 128>(di, dev, a, st);
+  return NC == 64 ? launch_attend_tc<128, 64>(di, dev, a, st) : launch_attend_tc<128, 128>(di, dev, a, st);
 }
-template <int D>
-size_t tc_smem_bytes(int NC) {
-  return NC == 64 ? TcLayout<D, 64>::bytes : TcLayout<D, 128>::bytes;
+size_t tc_smem_bytes(int D, int NC) {
+  return D == 64 ? TcLayout<64, 128>::bytes : NC == 64 ? TcLayout<128, 64>::bytes : TcLayout<128, 128>::bytes;
 }
 
 // Which kernel, and its row tile.
@@ -171,12 +167,16 @@ struct AttendPlan {
   int size;       // NR of attend_q4_kernel (rows / 8 of a tile), NC of attend_q4_tc_kernel
   size_t floats;  // of the workspace
 };
-constexpr int kTcRows = 33;   // rows from which the tensor cores' kernel is taken: 256 sequences at 2,048 tokens, 32 rows 507 us here against 700 there
+// Up to how many rows the bus' kernel is taken.  256 sequences at 2,048 tokens, against
+// the tensor cores': D = 128, 48 rows (two tiles of 24) 580 us against 771, 64 rows
+// (two of 32) 916 against 763; D = 64, 64 rows 576 against 734.  Longer sequences
+// favour the tensor cores more (32 at 8,192 tokens, D = 128, 64 rows 400 against 265).
+constexpr int kFewRows128 = 48, kFewRows64 = 64;
 AttendPlan attend_plan(int B, int rows, int D) {
   AttendPlan p{};
   const int NC = rows <= 64 ? 64 : 128;
-  const size_t smem = (D == 128 ? tc_smem_bytes<128>(NC) : tc_smem_bytes<64>(NC)) + 1024 + 8 * (static_cast<size_t>(B) + 1);
-  p.tc = rows >= kTcRows && smem + 256 <= static_cast<size_t>(kSmemPerSm);
+  const size_t smem = tc_smem_bytes(D, NC) + 1024 + 8 * (static_cast<size_t>(B) + 1);
+  p.tc = rows > (D == 128 ? kFewRows128 : kFewRows64) && smem + 256 <= static_cast<size_t>(kSmemPerSm);
   if (p.tc) {
     p.size = NC;
     p.tiles = ceil_div(rows, NC);
@@ -428,7 +428,7 @@ spec_status_t spec_attend_q4(const void* q, const void* k_new, const void* v_new
     a.timeout_ns = kWaitNs;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     prof_mark(0, st);
-    if (plan.tc) s = D == 128 ? launch_attend_tc<128>(plan.size, di, dev, a, st) : launch_attend_tc<64>(plan.size, di, dev, a, st);
+    if (plan.tc) s = launch_attend_tc(D, plan.size, di, dev, a, st);
     else s = D == 128 ? launch_attend<128>(plan.size, di, dev, a, st) : launch_attend<64>(plan.size, di, dev, a, st);
     if (s != SPEC_OK) return s;
     prof_mark(1, st);
