@@ -553,8 +553,10 @@ __device__ __forceinline__ void at_cached_tile(const unsigned char* tile, int le
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           mx[j][e] = fmaxf(mx[j][e], fmaxf(z[j][e], z[j][e + 2]));
-          z[j][e] = ex2_approx(__fmaf_rn(z[j][e], c[j][e], -st.ref[j][e]));
-          z[j][e + 2] = ex2_approx(__fmaf_rn(z[j][e + 2], c[j][e], -st.ref[j][e]));
+          // (the product is rounded as the reference was: a fused one would leave half a
+          // step of a score, which is beyond any weight for scores above 2^28)
+          z[j][e] = ex2_approx(__fsub_rn(__fmul_rn(z[j][e], c[j][e]), st.ref[j][e]));
+          z[j][e + 2] = ex2_approx(__fsub_rn(__fmul_rn(z[j][e + 2], c[j][e]), st.ref[j][e]));
           lt[j][e] += z[j][e] + z[j][e + 2];
         }
         out[(mt * NR + j) * 32] = make_uint2(transpose8(f16x2_pack(z[j][0], z[j][1])), transpose8(f16x2_pack(z[j][2], z[j][3])));

@@ -957,13 +957,14 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar->kready[x]);
       }
-      if (L::UNPACK == 8 && keys && TC_RARE(t.kind == TC_FRESH)) named_bar_arrive(8, 32 * L::UNPACK);   // the keys have left the values' buffer
+      // In a fresh tile the keys' and the values' warps meet once the keys have left
+      // the values' buffer.  (Both wait: an arrival for one tile would otherwise count
+      // for the tile before.)
+      if (TC_RARE(t.kind == TC_FRESH)) named_bar_sync(L::UNPACK == 4 ? 6 : 8, 32 * L::UNPACK);
       if (values) {
         if (n >= 2) tc_wait(&bar->pvdone[x], ((n >> 1) & 1) ^ 1, bar, a.timeout_ns);
         unsigned char* vb = tc_smem + L::v + x * TC_VBUF + tok * 16;
         if (TC_RARE(t.kind == TC_FRESH)) {
-          // (once the keys have left the buffer)
-          named_bar_sync(L::UNPACK == 4 ? 6 : 8, 32 * L::UNPACK);
           if (tc_fresh_value<D>(a.v_new + fresh_at(), a.Hkv * D, t.left, a.v_mul, tc_smem + L::v + x * TC_VBUF, L::UNPACK == 4 ? 6 : 7))
             *reinterpret_cast<volatile int*>(&bar->wide[x]) = n + 1;
         } else {
@@ -1070,7 +1071,10 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
       for (bool again = false;; again = true) {
         tc_ld<HC>(s_at, y);
         float m = 0.f;
-        if (TC_RARE(common == 0.f)) {
+        // (After new references the products are rounded as those were: of scores above
+        // 2^28 a fused product would leave half a step, which is beyond any weight.)
+        const unsigned long long by = again ? f2_pack(1.f, 1.f) : common2;
+        if (TC_RARE(again || common == 0.f)) {
 #pragma unroll
           for (int i = 0; i < HC; ++i) y[i] *= factor[i];
         }
@@ -1079,8 +1083,8 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
 #pragma unroll
         for (int i = 0; i < HC; i += 4) {
           const float4 s = *reinterpret_cast<const float4*>(shift + i);
-          f2_unpack(f2_fma(f2_pack(y[i], y[i + 1]), common2, f2_pack(s.x, s.y)), y[i], y[i + 1]);
-          f2_unpack(f2_fma(f2_pack(y[i + 2], y[i + 3]), common2, f2_pack(s.z, s.w)), y[i + 2], y[i + 3]);
+          f2_unpack(f2_fma(f2_pack(y[i], y[i + 1]), by, f2_pack(s.x, s.y)), y[i], y[i + 1]);
+          f2_unpack(f2_fma(f2_pack(y[i + 2], y[i + 3]), by, f2_pack(s.z, s.w)), y[i + 2], y[i + 3]);
         }
         if (TC_RARE(hides)) {
 #pragma unroll

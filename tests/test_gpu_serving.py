@@ -360,6 +360,57 @@ def test_attend_extreme_values():
     _close(_attend(c), _expect(c), 128)
 
 
+# rows of a kv head on both sides of each kernel's row tiles (32, 64 and 128 rows)
+TILES = [(16, 3, 1, 128), (13, 4, 1, 128), (16, 8, 2, 128), (65, 1, 1, 128), (64, 4, 2, 128), (129, 3, 3, 128), (16, 8, 2, 64), (65, 2, 2, 64), (43, 3, 1, 64)]
+
+
+@pytest.mark.parametrize("N,Hq,Hkv,D", TILES)
+@pytest.mark.parametrize("tree", [False, True])
+def test_attend_row_tiles(N, Hq, Hkv, D, tree):
+    c = _case(60 + N, 3, N, Hq, Hkv, D, 32, [300, 0, 129], tree=tree, shifts=(1, -1))
+    _close(_attend(c), _expect(c), D)
+
+
+@pytest.mark.parametrize("N,Hq,Hkv,D", TILES)
+def test_attend_fresh_entries_out_of_range_in_every_tile(N, Hq, Hkv, D):
+    """Infinities, NaN and elements beyond f16 in the fresh entries, and queries
+    whose rows need powers of two of their own."""
+    c = _case(61 + N, 2, N, Hq, Hkv, D, 32, [70, 0], tree=True)
+    c["v"][0, 3, 0, 5], c["v"][0, 4, Hkv - 1, D - 1], c["k"][1, 6, 0, 2] = float("inf"), float("nan"), float("nan")
+    c["v"][1, N - 1, Hkv - 1, 0], c["k"][1, 9, 0] = float("-inf"), -1e30
+    c["q"][0, 1, Hq - 1] *= 1e-30
+    c["q"][0, 2, 0] = 0
+    c["q"][1, 0, 0] *= 30
+    c["v"][1, 5, 0] *= 1e30
+    _close(_attend(c), _expect(c), D)
+
+
+@pytest.mark.parametrize("N,Hq,Hkv,D", [(1, 2, 1, 128), (6, 8, 2, 64)] + TILES[1::2])
+def test_attend_scores_beyond_the_weights_steps(N, Hq, Hkv, D):
+    """Scores so large that a rounding of one is worth more than any weight: every
+    result stays finite."""
+    c = _case(63 + N, 2, N, Hq, Hkv, D, 32, [500, 130], shifts=(32, 0))
+    c["q"] *= 3e4
+    exp = _expect(c)
+    assert np.isfinite(exp[0]).all() and np.abs(exp[1]).max() > 2.0 ** 40
+    _close(_attend(c), exp, D)
+
+
+@pytest.mark.parametrize("B,N,Hq,Hkv,D", [(350, 15, 8, 2, 128), (200, 60, 1, 1, 128), (60, 140, 4, 2, 64), (33, 300, 2, 1, 128), (9, 1024, 2, 2, 64)])
+@pytest.mark.parametrize("top", [1, 200])
+def test_attend_many_triples_with_little_behind_them(B, N, Hq, Hkv, D, top):
+    """A multiprocessor's share holds several (sequence, head, row tile) triples, many
+    of them with fresh entries alone, and begins anywhere within one."""
+    lengths = np.random.default_rng(B).integers(0, top, B)
+    c = _case(62, B, N, Hq, Hkv, D, 32, lengths)
+    if N > 500:   # (the reference of a few sequences is enough)
+        rows = [0, B // 2, B - 1]
+        part = dict(c, q=c["q"][rows], k=c["k"][rows], v=c["v"][rows], see=c["see"][rows], table=c["table"][rows], lengths=c["lengths"][rows])
+        _close([x[rows] for x in _attend(c)], _expect(part), D)
+    else:
+        _close(_attend(c), _expect(c), D)
+
+
 def test_attend_queries_that_are_not_finite():
     c = _case(8, 1, 3, 4, 2, 64, 32, [40])
     c["q"][0, 1, 1, 3], c["q"][0, 2, 2, 0] = float("nan"), float("inf")
