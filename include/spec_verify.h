@@ -352,6 +352,8 @@ size_t spec_q4_block_bytes(int D);
  *       max_pages * page_tokens, places past max_tokens, a ring_state outside
  *       the ring); -3 when the pool has too few free pages.  A refused sequence
  *       keeps its pages, takes none, and its places have slot -1.
+ *   B = 0 (the [B] buffers may be NULL) writes offsets, slots, positions and
+ *       new_ring_state as for any other batch.
  *
  * Sequences are served in order: a request is granted iff the pages that the
  * sequences up to and including it need together are free before the call

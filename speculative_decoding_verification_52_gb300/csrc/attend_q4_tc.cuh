@@ -222,6 +222,7 @@ __device__ __forceinline__ bool tc_poll(uint64_t* bar, uint32_t parity) {
   return ok != 0;
 }
 __device__ __noinline__ bool tc_wait_long(uint64_t* bar, uint32_t parity, TcBars* b, unsigned long long limit) {
+  if (*reinterpret_cast<volatile int*>(&b->dead)) return false;   // (at once: the others go on in step)
   const uint64_t t0 = global_ns();
   for (uint32_t i = 1; i < (1u << 28); ++i) {
     if (tc_poll(bar, parity)) return true;

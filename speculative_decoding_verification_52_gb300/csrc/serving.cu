@@ -222,11 +222,10 @@ spec_status_t spec_page_map(const int32_t* lengths, const int32_t* count, const 
                   ring_size, page_tokens, max_pages, max_tokens);
     if (!below_2g(ring_size, page_tokens) || !below_2g(max_pages, page_tokens))
       return fail(SPEC_ERR_UNSUPPORTED, "ring_size and max_pages times page_tokens must stay below 2^31");
-    if (B == 0) return SPEC_OK;
-    if (!lengths || !count || !held || !ring || !ring_state || !block_table || !offsets || !new_held ||
-        !new_ring_state || !status || (max_tokens > 0 && (!slots || !positions)))
+    if (!ring || !ring_state || !offsets || !new_ring_state || (max_tokens > 0 && (!slots || !positions)) ||
+        (B > 0 && (!lengths || !count || !held || !block_table || !new_held || !status)))
       return fail(SPEC_ERR_INVALID_ARG, "NULL pointer argument");
-    if (new_held == held || new_ring_state == ring_state)
+    if ((B > 0 && new_held == held) || new_ring_state == ring_state)
       return fail(SPEC_ERR_INVALID_ARG, "new_held / new_ring_state must not be held / ring_state");
     int dev;
     DevInfo di;

@@ -125,6 +125,16 @@ def _kv(rng, *shape):
     return bf(x)
 
 
+def test_page_map_of_an_empty_batch():
+    """Every place is empty, so that a store behind it touches nothing."""
+    e = torch.empty(0, dtype=torch.int32, device=DEV)
+    state = i32([3, 5])
+    slots = torch.full((9,), 7, dtype=torch.int32, device=DEV)
+    got = sv.spec_page_map(e, e, e, i32(range(8)), state, e.view(0, 4), 32, 9, slots=slots)
+    assert got[0].tolist() == [0] and got[1] is slots and slots.tolist() == [-1] * 9 and got[2].tolist() == [-1] * 9
+    assert got[3].numel() == 0 and got[4].tolist() == [3, 5] and got[5].numel() == 0
+
+
 @pytest.mark.parametrize("D,Hkv,P,T,shift", [(128, 2, 32, 1, 0), (128, 3, 64, 77, -2), (64, 1, 32, 40, 5), (64, 5, 128, 133, 0)])
 def test_store_matches_reference_bit_for_bit(D, Hkv, P, T, shift):
     rng = np.random.default_rng(T)

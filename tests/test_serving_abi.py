@@ -35,7 +35,7 @@ MAP = dict(p_lengths=16, p_count=32, p_held=48, p_ring=64, p_ring_state=80, p_ta
     (dict(p_lengths=0), BAD), (dict(p_count=0), BAD), (dict(p_held=0), BAD), (dict(p_ring=0), BAD), (dict(p_ring_state=0), BAD),
     (dict(p_table=0), BAD), (dict(p_offsets=0), BAD), (dict(p_slots=0), BAD), (dict(p_positions=0), BAD), (dict(p_status=0), BAD),
     (dict(p_new_held=48), BAD), (dict(p_new_state=80), BAD),
-    (dict(F=1 << 27, P=32), UNSUP), (dict(W=1 << 27, P=32), UNSUP),
+    (dict(F=1 << 27, P=32), UNSUP), (dict(W=1 << 27, P=32), UNSUP), (dict(B=0, p_offsets=0), BAD), (dict(B=0, p_slots=0), BAD),
 ])
 def test_page_map_refusals(L, kw, status):
     assert _call(L.spec_page_map, MAP, **kw) == status
