@@ -832,17 +832,30 @@ __device__ __forceinline__ void at_fresh_tile(const AttendArgs& a, int b, int h,
   pr.sync();   // the exchange area is free again
 }
 
-// The state after fresh tiles first .. last - 1 of a triple.  A
+// The state after fresh tiles first .. last - 1 of a triple.  From 16 rows on a
 // function of its own: these tiles are few, and their registers would push the
 // cached tiles' loop into local memory.
 template <int D, int NR>
-__device__ __noinline__ void at_fresh(const AttendArgs& args, int b, int h, int row0, int rows, int first, int last,
-                                      AtPair<D, NR> pr, AtState<D, NR>* to) {
+__device__ __noinline__ void at_fresh_apart(const AttendArgs& args, int b, int h, int row0, int rows, int first, int last,
+                                            AtPair<D, NR> pr, AtState<D, NR>* to) {
   const AttendArgs a = args;   // (in registers: through the reference each use would read it again after every store)
   AtState<D, NR> st;
   st.clear();
   for (int i = first; i < last; ++i) at_fresh_tile<D, NR>(a, b, h, row0, rows, i * AT_TILE, pr, st);
   *to = st;
+}
+template <int D, int NR>
+__device__ __forceinline__ void at_fresh(const AttendArgs& a, int b, int h, int row0, int rows, int first, int last, const AtPair<D, NR>& pr,
+                                         AtState<D, NR>& st) {
+  if constexpr (NR == 1) {
+    st.clear();
+#pragma unroll 1
+    for (int i = first; i < last; ++i) at_fresh_tile<D, NR>(a, b, h, row0, rows, i * AT_TILE, pr, st);
+  } else {
+    AtState<D, NR> fresh;   // (in local memory, so that `st` is not)
+    at_fresh_apart<D, NR>(a, b, h, row0, rows, first, last, pr, &fresh);
+    st = fresh;
+  }
 }
 
 __device__ __forceinline__ float at_lse(float ref, float l) {
@@ -1030,9 +1043,7 @@ __global__ void __launch_bounds__(AT_THREADS, at_ctas(NR)) attend_q4_kernel(cons
       // (a fresh tile is worked on by the share that has its first unit)
       const int f0 = (first + AT_FRESH - 1) / AT_FRESH, f1 = (min(last, nf) + AT_FRESH - 1) / AT_FRESH;
       if (f0 < f1) {
-        AtState<D, NR> fresh;   // (in local memory, so that `st` is not)
-        at_fresh<D, NR>(a, cur.b, h, row0, rows, f0, f1, pr, &fresh);
-        st = fresh;
+        at_fresh<D, NR>(a, cur.b, h, row0, rows, f0, f1, pr, st);
       } else {
         st.clear();
       }
