@@ -6,11 +6,10 @@
 //   z = scale * q.k,  out = softmax(z) v,  lse = log(sum exp z).
 // The rows of one kv head are its N * G (node, query head) pairs.
 //
-// Few rows (this kernel).  The cache is read once and each element takes part
-// in 2 * rows multiply-adds, so up to a few tens of rows the 9/16 byte an
-// element has to cross the HBM bus is the bound; in that time a
-// scheduler issues about three instructions an element (one row of a warp's lanes),
-// and to unpack the codes takes one.
+// Few rows (this kernel).  The cache is read once and each element takes part in
+// 2 * rows multiply-adds, so up to a few tens of rows the 9/16 byte an element has
+// to cross the HBM bus is the bound; next to it stands the work of unpacking the
+// codes, a conversion and a multiplication for two elements.
 //
 // * The unit of work is a tile of 64 tokens: two blocks, each one contiguous run
 //   of 36 * D bytes and one bulk copy.  All tiles of all (sequence, head, row
@@ -19,7 +18,7 @@
 //   lengths, and fetches it through a ring of its own.  A triple that lies in one
 //   pair's share is finished there.  A fresh tile counts as three: it waits for
 //   its loads, where a cached tile's have arrived (256 sequences of 4 nodes at
-//   2,048 tokens, 16 rows: 269 us when it counts as one, 252 as three).  The pairs
+//   2,048 tokens, 16 rows: 236 us when it counts as one, 226 as three).  The pairs
 //   of a CTA have neighbouring shares and join what they share at the end; what
 //   CTAs share goes through the workspace (reference, sum, sum of v) and a second
 //   kernel.  All joins are in the list's order.
@@ -516,17 +515,17 @@ __device__ __noinline__ void at_agree(const AtPair<D, NR>& pr, int buf, const fl
 //
 // Both halves of the work are loops over 16 tokens, unrolled only as far as the
 // code of a tile stays near 8 KB, up to which a warp gets through it at about the
-// rate of its scheduler; at 16 KB it takes 2.7 clocks an instruction to fetch.  32
-// rows fully unrolled took 645 us, two steps at a time 548, rolled 507; 24 rows 383,
-// 343 and 350; 16 rows two at a time 252, rolled 270; 8 rows unrolled 170, rolled
-// 187 (256 sequences at 2,048 tokens).  So that they can be loops, the weights are
+// rate of its scheduler; at 16 KB it takes 2.7 clocks an instruction to fetch.  256
+// sequences at 2,048 tokens: 32 rows two steps at a time 548 us, rolled 507; 24 rows
+// 304 and 295 (D = 64: 215 and 219); 16 rows two at a time 252, rolled 270; 8 rows
+// unrolled 170, rolled 187.  So that they can be loops, the weights are
 // taken at once against the references as they are, and only then the warps look
 // whether a score was too far above one; if so, they agree on new references and
 // score the tile again.
 //
 // (The exchange area has two buffers, taken in turn: with one barrier a tile, what a
 // warp writes for a tile was last read two barriers before.)
-__host__ __device__ constexpr int at_unroll(int NR) { return NR == 1 ? 4 : NR < 4 ? 2 : 1; }
+__host__ __device__ constexpr int at_unroll(int D, int NR) { return NR == 1 ? 4 : NR == 2 || (NR == 3 && D == 64) ? 2 : 1; }
 template <int D, int NR, class F>
 __device__ __forceinline__ void at_cached_tile(const unsigned char* tile, int left, int buf, const float (&c)[NR][2],
                                                const AtPair<D, NR>& pr, AtState<D, NR>& st, F&& after) {
@@ -544,7 +543,7 @@ __device__ __forceinline__ void at_cached_tile(const unsigned char* tile, int le
         lt[j][e] = 0.f;
         mx[j][e] = kNegInf;
       }
-#pragma unroll at_unroll(NR)
+#pragma unroll at_unroll(D, NR)
     for (int mt = 0; mt < 2; ++mt) {
       float z[NR][4];
       at_scores<D, NR>(sb, pr.q() + lane, mt, own, z);
@@ -590,7 +589,7 @@ __device__ __forceinline__ void at_cached_tile(const unsigned char* tile, int le
 
   // v: steps of 16 tokens (D = 128), or of 32 (D = 64, whose codes of two steps make a word)
   constexpr int STEPS = D == 128 ? 4 : 2, S = 4 / STEPS;
-#pragma unroll at_unroll(NR)
+#pragma unroll at_unroll(D, NR)
   for (int y = 0; y < STEPS; ++y) {
     const int blk = y / (STEPS / 2), s0 = D == 128 ? y & 1 : 0;
     const int have = left - blk * Q4_BLOCK;   // tokens of that block
@@ -832,32 +831,6 @@ __device__ __forceinline__ void at_fresh_tile(const AttendArgs& a, int b, int h,
   pr.sync();   // the exchange area is free again
 }
 
-// The state after fresh tiles first .. last - 1 of a triple.  From 16 rows on a
-// function of its own: these tiles are few, and their registers would push the
-// cached tiles' loop into local memory.
-template <int D, int NR>
-__device__ __noinline__ void at_fresh_apart(const AttendArgs& args, int b, int h, int row0, int rows, int first, int last,
-                                            AtPair<D, NR> pr, AtState<D, NR>* to) {
-  const AttendArgs a = args;   // (in registers: through the reference each use would read it again after every store)
-  AtState<D, NR> st;
-  st.clear();
-  for (int i = first; i < last; ++i) at_fresh_tile<D, NR>(a, b, h, row0, rows, i * AT_TILE, pr, st);
-  *to = st;
-}
-template <int D, int NR>
-__device__ __forceinline__ void at_fresh(const AttendArgs& a, int b, int h, int row0, int rows, int first, int last, const AtPair<D, NR>& pr,
-                                         AtState<D, NR>& st) {
-  if constexpr (NR == 1) {
-    st.clear();
-#pragma unroll 1
-    for (int i = first; i < last; ++i) at_fresh_tile<D, NR>(a, b, h, row0, rows, i * AT_TILE, pr, st);
-  } else {
-    AtState<D, NR> fresh;   // (in local memory, so that `st` is not)
-    at_fresh_apart<D, NR>(a, b, h, row0, rows, first, last, pr, &fresh);
-    st = fresh;
-  }
-}
-
 __device__ __forceinline__ float at_lse(float ref, float l) {
   return l == 0.f ? kNegInf : (ref + log2f(l)) * 0.69314718055994530942f;   // l: the sum of weights, relative to 2^ref
 }
@@ -1042,11 +1015,13 @@ __global__ void __launch_bounds__(AT_THREADS, at_ctas(NR)) attend_q4_kernel(cons
       const int nf = poison ? 0 : AT_FRESH * nfresh, ncached = poison ? 0 : (cur.len + AT_TILE - 1) / AT_TILE;
       // (a fresh tile is worked on by the share that has its first unit)
       const int f0 = (first + AT_FRESH - 1) / AT_FRESH, f1 = (min(last, nf) + AT_FRESH - 1) / AT_FRESH;
-      if (f0 < f1) {
-        at_fresh<D, NR>(a, cur.b, h, row0, rows, f0, f1, pr, st);
-      } else {
-        st.clear();
-      }
+      // (In line: in a function of their own these tiles leave the cached ones' loop
+      // more registers, but the state and the arguments then pass through memory: 24
+      // rows of 256 sequences at 2,048 tokens took 316 us where this takes 303, of 32
+      // at 16,384 239 us where this takes 246.)
+      st.clear();
+#pragma unroll 1
+      for (int i = f0; i < f1; ++i) at_fresh_tile<D, NR>(a, cur.b, h, row0, rows, i * AT_TILE, pr, st);
       const int c1 = min(last - nf, ncached);
       int c = max(first - nf, 0);
       float factor[NR][2];

@@ -167,11 +167,12 @@ struct AttendPlan {
   int size;       // NR of attend_q4_kernel (rows / 8 of a tile), NC of attend_q4_tc_kernel
   size_t floats;  // of the workspace
 };
-// Up to how many rows the bus' kernel is taken.  256 sequences at 2,048 tokens, against
-// the tensor cores': D = 128, 48 rows (two tiles of 24) 580 us against 771, 64 rows
-// (two of 32) 916 against 763; D = 64, 64 rows 576 against 734.  Longer sequences
-// favour the tensor cores more (32 at 8,192 tokens, D = 128, 64 rows 400 against 265).
-constexpr int kFewRows128 = 48, kFewRows64 = 64;
+// Up to how many rows attend_q4_kernel is taken, against the tensor cores' kernel.  256
+// sequences at 2,048 tokens (and 32 at 8,192): D = 128, 48 rows (two tiles of 24) 546 us
+// against 771, 64 rows (two of 32) 887 against 773 (392 against 269); D = 64, 72 rows
+// (three of 24) 566 against 783 (240 against 281), 96 rows (three of 32) 731 against 783
+// (304 against 287).
+constexpr int kFewRows128 = 48, kFewRows64 = 72;
 AttendPlan attend_plan(int B, int rows, int D) {
   AttendPlan p{};
   const int NC = rows <= 64 ? 64 : 128;
