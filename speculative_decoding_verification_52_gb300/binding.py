@@ -455,25 +455,27 @@ def spec_page_map(lengths, count, held, ring, ring_state, block_table, page_toke
     [max_tokens], new_held [B], new_ring_state [2], status [B]), all int32; those
     not supplied are parts of one allocation."""
     i32, B = torch.int32, lengths.numel()
-    one, T = (B,), (max_tokens,)
-    if offsets is None or slots is None or positions is None or new_held is None or new_ring_state is None or status is None:
+    one, given = (B,), (slots, positions, offsets, new_held, status, new_ring_state)
+    sizes = (max_tokens, max_tokens, B + 1, B, B, 2)
+    if all(t is None for t in given):
         pad = -max_tokens % 4   # slots and positions start at 16-byte borders
-        new = torch.empty(2 * (max_tokens + pad) + 3 * B + 3, dtype=i32, device=lengths.device).split_with_sizes(
+        new = torch.empty(2 * (max_tokens + pad) + 3 * B + 3, dtype=i32, device=lengths.device)
+        at = new.data_ptr()
+        slots, _, positions, _, offsets, new_held, status, new_ring_state = new.split_with_sizes(
             (max_tokens, pad, max_tokens, pad, B + 1, B, B, 2))
-        slots = new[0] if slots is None else slots
-        positions = new[2] if positions is None else positions
-        offsets = new[4] if offsets is None else offsets
-        new_held = new[5] if new_held is None else new_held
-        status = new[6] if status is None else status
-        new_ring_state = new[7] if new_ring_state is None else new_ring_state
+        rest = at + 8 * (max_tokens + pad)
+        to = (at, at + 4 * (max_tokens + pad), rest, rest + 4 * (B + 1), rest + 4 * (2 * B + 1), rest + 4 * (3 * B + 1))
+    else:
+        slots, positions, offsets, new_held, status, new_ring_state = out = tuple(
+            torch.empty(n, dtype=i32, device=lengths.device) if t is None else t for t, n in zip(given, sizes))
+        to = tuple(_take(t, name, i32, (n,), dev) for t, name, n in zip(
+            out, ("slots", "positions", "offsets", "new_held", "status", "new_ring_state"), sizes))
     table = _cols(block_table, B, "block_table")
     st = (_lib or lib()).spec_page_map(
         _take(lengths, "lengths", i32, one, dev), _take(count, "count", i32, one, dev), _take(held, "held", i32, one, dev),
         _take(ring, "ring", i32, (ring.numel(),), dev), _take(ring_state, "ring_state", i32, (2,), dev),
         _take(block_table, "block_table", i32, table, dev), B, ring.numel(), page_tokens, table[1], max_tokens,
-        _take(offsets, "offsets", i32, (B + 1,), dev), _take(slots, "slots", i32, T, dev),
-        _take(positions, "positions", i32, T, dev), _take(new_held, "new_held", i32, one, dev),
-        _take(new_ring_state, "new_ring_state", i32, (2,), dev), _take(status, "status", i32, one, dev), stream)
+        to[2], to[0], to[1], to[3], to[5], to[4], stream)
     if st:
         _check("spec_page_map", st)
     return offsets, slots, positions, new_held, new_ring_state, status
