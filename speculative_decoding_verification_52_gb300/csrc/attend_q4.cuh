@@ -513,19 +513,19 @@ __device__ __noinline__ void at_agree(const AtPair<D, NR>& pr, int buf, const fl
 // A cached tile: `left` tokens of it (1..64) belong to the sequence.  `after` runs
 // once both warps are done with the tile before.
 //
-// Both halves of the work are loops over 16 tokens, unrolled only as far as the
-// code of a tile stays near 8 KB, up to which a warp gets through it at about the
-// rate of its scheduler; at 16 KB it takes 2.7 clocks an instruction to fetch.  256
-// sequences at 2,048 tokens: 32 rows two steps at a time 548 us, rolled 507; 24 rows
-// 304 and 295 (D = 64: 215 and 219); 16 rows two at a time 252, rolled 270; 8 rows
-// unrolled 170, rolled 187.  So that they can be loops, the weights are
-// taken at once against the references as they are, and only then the warps look
-// whether a score was too far above one; if so, they agree on new references and
-// score the tile again.
+// Both halves of the work are loops over 16 tokens, unrolled where the registers hold
+// what that interleaves and the code of a tile stays small: up to 8 KB a warp gets
+// through it at about the rate of its scheduler, at 16 KB it takes 2.7 clocks an
+// instruction to fetch.  256 sequences at 2,048 tokens, D = 128: 32 rows unrolled 381
+// us, rolled 388; 24 rows two steps at a time 304, rolled 295 (D = 64: 215 and 219);
+// 16 rows unrolled 218, two steps 223; 8 rows unrolled 170, rolled 187.  So that they
+// can be loops, the weights are taken at once against the references as they are, and
+// only then the warps look whether a score was too far above one; if so, they agree on
+// new references and score the tile again.
 //
 // (The exchange area has two buffers, taken in turn: with one barrier a tile, what a
 // warp writes for a tile was last read two barriers before.)
-__host__ __device__ constexpr int at_unroll(int D, int NR) { return NR == 1 ? 4 : NR == 2 || (NR == 3 && D == 64) ? 2 : 1; }
+__host__ __device__ constexpr int at_unroll(int D, int NR) { return NR == 1 ? 4 : D == 64 ? (NR < 4 ? 2 : 1) : NR == 3 ? 1 : 4; }
 template <int D, int NR, class F>
 __device__ __forceinline__ void at_cached_tile(const unsigned char* tile, int left, int buf, const float (&c)[NR][2],
                                                const AtPair<D, NR>& pr, AtState<D, NR>& st, F&& after) {
@@ -835,8 +835,12 @@ __device__ __forceinline__ float at_lse(float ref, float l) {
   return l == 0.f ? kNegInf : (ref + log2f(l)) * 0.69314718055994530942f;   // l: the sum of weights, relative to 2^ref
 }
 
-// CTAs an SM: what the registers of a row tile leave room for
-__host__ __device__ constexpr int at_ctas(int NR) { return NR <= 2 ? 4 : 3; }
+// CTAs an SM, of four warps: what the registers of a row tile leave room for.  256
+// sequences at 2,048 tokens, D = 128: 32 rows 381 us with two, 485 with three (306
+// bytes of a thread in local memory); 24 rows 293 with three, 315 with two; 16 rows 218
+// with three, 226 with four.  D = 64, half the sums: 64 rows (two tiles of 32) 476 us
+// with three, 489 with two.
+__host__ __device__ constexpr int at_ctas(int D, int NR) { return NR == 1 ? 4 : D == 64 ? (NR == 2 ? 4 : 3) : NR < 4 ? 3 : 2; }
 
 // the warp's part of a row's sum of weights
 __device__ __forceinline__ float at_sum(float l) {
@@ -924,7 +928,7 @@ __device__ __forceinline__ uint2 at_source(const AttendArgs& a, const long long*
 }
 
 template <int D, int NR>
-__global__ void __launch_bounds__(AT_THREADS, at_ctas(NR)) attend_q4_kernel(const __grid_constant__ AttendArgs a, int stages) {
+__global__ void __launch_bounds__(AT_THREADS, at_ctas(D, NR)) attend_q4_kernel(const __grid_constant__ AttendArgs a, int stages) {
   extern __shared__ __align__(128) unsigned char at_smem[];
   __shared__ long long scratch[AT_THREADS / 32];
   constexpr int SB = at_stage_bytes(D), BB = q4_block_bytes(D);

@@ -80,7 +80,7 @@ spec_status_t launch_attend(const DevInfo& di, int dev, const AttendArgs& a, cud
   // As many CTAs an SM as the registers allow, with as many stages (2 to 6) as
   // leave room for them; fewer CTAs where two stages do not.  (1.25 KB a CTA: the
   // system's and the static part.)
-  int ctas = at_ctas(NR);
+  int ctas = at_ctas(D, NR);
   auto room = [&](int n) { return static_cast<long long>(kSmemPerSm / n) - 1280 - static_cast<long long>(fixed); };
   while (ctas > 1 && room(ctas) < static_cast<long long>(2 * stage)) --ctas;
   const int stages = static_cast<int>(std::min<long long>(6, room(ctas) / static_cast<long long>(stage)));
@@ -169,9 +169,9 @@ struct AttendPlan {
 };
 // Up to how many rows attend_q4_kernel is taken, against the tensor cores' kernel.  256
 // sequences at 2,048 tokens (and 32 at 8,192): D = 128, 48 rows (two tiles of 24) 546 us
-// against 771, 64 rows (two of 32) 887 against 773 (392 against 269); D = 64, 72 rows
-// (three of 24) 566 against 783 (240 against 281), 96 rows (three of 32) 731 against 783
-// (304 against 287).
+// against 771, 64 rows (two of 32) 689 against 773 (305 against 269); D = 64, 72 rows
+// (three of 24) 564 against 783 (240 against 281), 96 rows (three of 32) 724 against 783
+// (302 against 287).
 constexpr int kFewRows128 = 48, kFewRows64 = 72;
 AttendPlan attend_plan(int B, int rows, int D) {
   AttendPlan p{};
@@ -184,7 +184,7 @@ AttendPlan attend_plan(int B, int rows, int D) {
     p.floats = static_cast<size_t>(kMaxSms) * tc_cta_floats(D, NC);
   } else {
     attend_tiles(rows, p.tiles, p.size);
-    p.floats = static_cast<size_t>(kMaxSms) * at_ctas(p.size) * at_cta_floats(D, p.size);
+    p.floats = static_cast<size_t>(kMaxSms) * at_ctas(D, p.size) * at_cta_floats(D, p.size);
   }
   return p;
 }
