@@ -138,18 +138,12 @@ __device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, ui
 }
 template <int N>
 __device__ __forceinline__ void tc_ld(uint32_t addr, float (&x)[N]) {
-  static_assert(N == 8 || N == 16 || N == 32, "columns of a load");
+  static_assert(N == 8 || N == 32, "columns of a load");
   uint32_t r[N];
   if constexpr (N == 8) {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "r"(addr));
-  } else if constexpr (N == 16) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(addr));
   } else {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
@@ -579,63 +573,52 @@ __device__ __noinline__ void tc_wide_values(const AttendArgs& args, int b, int h
   }
 }
 
-// column i of 32 (or fewer) over the lanes of a warp: lane i gets the maximum or the sum
-template <int N, bool SUM>
-__device__ __forceinline__ float tc_reduce(float (&x)[N]) {
+// the largest of column i of 32 over the lanes of a warp, in lane i
+__device__ __forceinline__ float tc_top(float (&x)[32]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
-    if (o >= N) {
+    // lanes with bit o keep the upper half of what is left
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float y = __shfl_xor_sync(0xffffffffu, x[i], o);
-        x[i] = SUM ? x[i] + y : fmaxf(x[i], y);
-      }
-    } else {
-      // lanes with bit o keep the upper half of what is left
-#pragma unroll
-      for (int i = 0; i < o; ++i) {
-        const bool up = lane & o;
-        const float keep = up ? x[i + o] : x[i], give = up ? x[i] : x[i + o];
-        const float y = __shfl_xor_sync(0xffffffffu, give, o);
-        x[i] = SUM ? keep + y : fmaxf(keep, y);
-      }
+    for (int i = 0; i < o; ++i) {
+      const bool up = lane & o;
+      const float keep = up ? x[i + o] : x[i], give = up ? x[i] : x[i + o];
+      x[i] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, o));
     }
   }
-  return x[0];   // of column lane % N
+  return x[0];
 }
 
-// bits of the rows of a chunk that do not see this thread's node: those without its
+// bits of the rows of a part that do not see this thread's node: those without its
 // bit in the warp's words (a tree), or those before row `open` (a chain)
-template <int CH>
 __device__ __noinline__ uint32_t tc_hidden(bool tree, const uint32_t* seen, int open) {
   if (!tree) return open <= 0 ? 0u : open >= 32 ? ~0u : (1u << open) - 1u;
   uint32_t hide = 0u;
 #pragma unroll 1
-  for (int i = 0; i < CH; ++i) hide |= (~(seen[i] >> (threadIdx.x & 31)) & 1u) << i;
+  for (int i = 0; i < TC_PART; ++i) hide |= (~(seen[i] >> (threadIdx.x & 31)) & 1u) << i;
   return hide;
 }
 
-// New references for CH rows: the 128 threads of a part call this together.
+// New references for a part's rows: the 128 threads of a part call this together.
 // s_at: the tile's products (hide: bits of rows that do not see this thread's
 // token), o_at: the rows' sums of v so far, if there are any.
-template <int CH, int NC>
+template <int NC>
 __device__ __noinline__ void tc_raise(uint32_t s_at, uint32_t o_at, const float* factor, float* shift, float* corr, float* top,
                                       uint32_t hide, bool sums, int quad, int id) {
   const int lane = threadIdx.x & 31;
-  float z[CH];
-  tc_ld<CH>(s_at, z);
+  float z[TC_PART];
+  tc_ld<TC_PART>(s_at, z);
 #pragma unroll
-  for (int i = 0; i < CH; i += 4) {
+  for (int i = 0; i < TC_PART; i += 4) {
     const float4 x = *reinterpret_cast<const float4*>(factor + i);
     const float f[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) z[i + k] = (hide >> (i + k)) & 1u ? kNegInf : fmaxf(z[i + k] * f[k], kNegInf);   // (no NaN)
   }
-  const float mx = tc_reduce<CH, false>(z);
-  if (lane < CH) top[quad * NC + lane] = mx;
+  const float mx = tc_top(z);
+  top[quad * NC + lane] = mx;
   named_bar_sync(id, 128);
-  if (quad == 0 && lane < CH) {
+  if (quad == 0) {
     const float m = fmaxf(fmaxf(top[lane], top[NC + lane]), fmaxf(top[2 * NC + lane], top[3 * NC + lane]));
     const float old = shift[lane];                                // 7 - ref, inf: none
     const float now = m == kNegInf ? old : fminf(old, AT_PSHIFT - m);
@@ -646,7 +629,7 @@ __device__ __noinline__ void tc_raise(uint32_t s_at, uint32_t o_at, const float*
   if (sums) {
     tc_fence_after();
 #pragma unroll 1
-    for (int i = 0; i < CH; i += 8) {
+    for (int i = 0; i < TC_PART; i += 8) {
       float o[8];
       tc_ld<8>(o_at + i, o);
 #pragma unroll
@@ -1064,7 +1047,7 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
       // which of the rows do not see this thread's token
       uint32_t hide = 0u;
       if (TC_RARE(some)) {
-        hide = tc_hidden<HC>(t.kind == TC_FRESH && a.masks, seen, open);
+        hide = tc_hidden(t.kind == TC_FRESH && a.masks, seen, open);
         if (tok >= t.left) hide = ~0u;
       }
       const bool hides = some && __any_sync(0xffffffffu, hide != 0u);
@@ -1097,7 +1080,7 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
         // (a row without a reference: a score that counts is infinite there)
         if (__builtin_expect(again || !tc_any<128>(id, !(m <= AT_PSHIFT + AT_ABOVE)), 1)) break;
         if (!t.first) tc_wait(&bar->pvdone[(n - 1) & 1], ((n - 1) >> 1) & 1, bar, a.timeout_ns);
-        tc_raise<HC, NC>(s_at, o_at, factor, shift, corr, top, hide, !t.first, quad, id);
+        tc_raise<NC>(s_at, o_at, factor, shift, corr, top, hide, !t.first, quad, id);
 #pragma unroll
         for (int i = 0; i < HC / 2; ++i) l[i] *= corr[(odd ? HC / 2 : 0) + i];
       }
