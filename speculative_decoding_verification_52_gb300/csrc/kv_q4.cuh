@@ -70,14 +70,15 @@ __device__ __forceinline__ void q4_group(const uint4& lo, const uint4& hi, float
   uint32_t m = bf16x2_abs(w[0]);
 #pragma unroll
   for (int i = 1; i < 8; ++i) m = bf16x2_max_nan(m, bf16x2_abs(w[i]));
-  const float top = fmax_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u)) * mul;
+  const float top = fmax_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
   codes = make_uint2(0u, 0u);
   if (!(top < __builtin_huge_valf())) {
     scale = 0x7fu;
     return;
   }
+  // (a finite element times 2^-shift may pass fp32's range: the scale is 448 then)
   uint16_t e;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e) : "f"(0.f), "f"(q4_sixth(top)));
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(e) : "f"(0.f), "f"(q4_sixth(fminf(top * mul, 3.402823466e+38f))));
   scale = e & 0xffu;
   if (scale == 0u) return;
   uint32_t s2;

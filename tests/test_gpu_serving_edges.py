@@ -1,0 +1,42 @@
+"""Edges of the serving steps on the GPU: infinite scores, entries at the ends of
+their types' ranges, the largest batches, waits that run out.
+
+Tolerances are those of test_gpu_serving.py (derived there); where a score is an
+infinity, the expected values come from the same reference with that node left out,
+which is what a weight of zero means."""
+import numpy as np
+import pytest
+import torch
+
+import serving_ref as ref
+import speculative_decoding_verification_52_gb300 as sv
+import test_gpu_serving as base
+from test_gpu_serving import DEV, _attend, _case, _close, _expect, bf, f32, f64, i32
+
+pytestmark = pytest.mark.gpu
+# rows of a kv head below and above each kernel's row tiles
+ROWS = [(1, 2, 1, 128), (6, 8, 2, 64)] + base.TILES
+
+
+@pytest.mark.parametrize("shift", [-32, -9, 32])
+def test_store_of_the_largest_values(shift):
+    """Finite values whose quotient by 2^shift is beyond fp32: the scale is the largest
+    one, not a NaN."""
+    rng = np.random.default_rng(5)
+    T, D = 64, 64
+    k = bf(rng.standard_normal((T, 1, D)) * np.exp2(rng.integers(80, 127, (T, 1, 1))))
+    k[3, 0, 17] = float("inf")
+    k[5, 0, 40] = float("nan")
+    k[7, 0, :] = torch.finfo(torch.bfloat16).max
+    v = bf(rng.standard_normal((T, 1, D)) * np.exp2(rng.integers(-126, 127, (T, 1, D))))
+    assert torch.isfinite(v).all()
+    exp = np.zeros((2, 1, 1, 36 * D), np.uint8)
+    for t in range(T):
+        ref.q4_put(exp, t, 0, f64(k[t, 0]), f64(v[t, 0]), shift, shift)
+    c = sv.q4_cache(2, 1, 32, D, DEV)
+    sv.spec_kv_store_q4(k.to(DEV), v.to(DEV), i32(np.arange(T)), c, k_shift=shift, v_shift=shift)
+    np.testing.assert_array_equal(c.cpu().numpy(), exp)
+    c.zero_()
+    new = sv.spec_kv_commit_q4(c, i32([[0, 1]]), i32([0]), k.view(1, T, 1, D).to(DEV), v.view(1, T, 1, D).to(DEV), i32([T]), k_shift=shift, v_shift=shift)
+    assert new.tolist() == [T]
+    np.testing.assert_array_equal(c.cpu().numpy(), exp)
