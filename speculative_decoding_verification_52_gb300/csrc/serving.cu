@@ -24,6 +24,7 @@ using namespace svh;
 
 constexpr int kMaxShift = 32;
 constexpr int kSmemPerSm = 227 * 1024;   // shared memory that the CTAs of an SM can use together
+constexpr int kMaxDynSmem = kSmemPerSm - 1024;   // dynamic part of a CTA that is alone on an SM, beside its static part
 
 bool q4_dim(int D) { return D == 64 || D == 128; }
 bool below_2g(long long a, long long b) { return a * b < (1LL << 31); }
@@ -87,7 +88,7 @@ spec_status_t launch_attend(const DevInfo& di, int dev, const AttendArgs& a, cud
   if (stages < 2) return fail(SPEC_ERR_UNSUPPORTED, "batch too large for one call");
   const size_t smem = fixed + stages * stage;
   if (!once_per_device(dev, [&] {
-        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerSm - 1024) == cudaSuccess;
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynSmem) == cudaSuccess;
       }))
     return fail(SPEC_ERR_CUDA, "attention kernel setup failed: %s", cudaGetErrorString(cudaGetLastError()));
   const int grid = std::min(di.sms, kMaxSms) * ctas;
@@ -126,6 +127,12 @@ TensorMapEncode tensor_map_encode() {
   return fn;
 }
 
+// dynamic shared memory: the layout, its alignment, the batch's prefix sums
+size_t tc_smem_bytes(uint32_t layout, int B) { return layout + 1024 + 8 * (static_cast<size_t>(B) + 1); }
+size_t tc_smem_bytes(int D, int NC, int B) {
+  return tc_smem_bytes(D == 64 ? TcLayout<64, 128>::bytes : NC == 64 ? TcLayout<128, 64>::bytes : TcLayout<128, 128>::bytes, B);
+}
+
 template <int D, int NC>
 spec_status_t launch_attend_tc(const DevInfo& di, int dev, const AttendArgs& a, cudaStream_t st) {
   auto kern = attend_q4_tc_kernel<D, NC>;
@@ -142,11 +149,11 @@ spec_status_t launch_attend_tc(const DevInfo& di, int dev, const AttendArgs& a, 
                             CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(SPEC_ERR_CUDA, "cuTensorMapEncodeTiled: %d", static_cast<int>(r));
   if (!once_per_device(dev, [&] {
-        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerSm - 1024) == cudaSuccess;
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynSmem) == cudaSuccess;
       }))
     return fail(SPEC_ERR_CUDA, "attention kernel setup failed: %s", cudaGetErrorString(cudaGetLastError()));
   const int grid = std::min(di.sms, kMaxSms);
-  kern<<<grid, TcLayout<D, NC>::THREADS, TcLayout<D, NC>::bytes + 1024 + 8 * (static_cast<size_t>(a.B) + 1), st>>>(a, map);
+  kern<<<grid, TcLayout<D, NC>::THREADS, tc_smem_bytes(TcLayout<D, NC>::bytes, a.B), st>>>(a, map);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return cuda_fail(e, "attention launch");
   return launch_join<D>(di, a, grid, 1, NC / 8, tc_cta_floats(D, NC), st);
@@ -155,9 +162,6 @@ spec_status_t launch_attend_tc(const DevInfo& di, int dev, const AttendArgs& a, 
 spec_status_t launch_attend_tc(int D, int NC, const DevInfo& di, int dev, const AttendArgs& a, cudaStream_t st) {
   if (D == 64) return launch_attend_tc<64, 128>(di, dev, a, st);
   return NC == 64 ? launch_attend_tc<128, 64>(di, dev, a, st) : launch_attend_tc<128, 128>(di, dev, a, st);
-}
-size_t tc_smem_bytes(int D, int NC) {
-  return D == 64 ? TcLayout<64, 128>::bytes : NC == 64 ? TcLayout<128, 64>::bytes : TcLayout<128, 128>::bytes;
 }
 
 // Which kernel, and its row tile.
@@ -176,8 +180,8 @@ constexpr int kFewRows128 = 48, kFewRows64 = 72;
 AttendPlan attend_plan(int B, int rows, int D) {
   AttendPlan p{};
   const int NC = rows <= 64 ? 64 : 128;
-  const size_t smem = tc_smem_bytes(D, NC) + 1024 + 8 * (static_cast<size_t>(B) + 1);
-  p.tc = rows > (D == 128 ? kFewRows128 : kFewRows64) && smem + 256 <= static_cast<size_t>(kSmemPerSm);
+  // (the largest batches leave no room for the tensor cores' kernel)
+  p.tc = rows > (D == 128 ? kFewRows128 : kFewRows64) && tc_smem_bytes(D, NC, B) <= static_cast<size_t>(kMaxDynSmem);
   if (p.tc) {
     p.size = NC;
     p.tiles = ceil_div(rows, NC);

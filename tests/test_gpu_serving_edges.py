@@ -40,3 +40,23 @@ def test_store_of_the_largest_values(shift):
     new = sv.spec_kv_commit_q4(c, i32([[0, 1]]), i32([0]), k.view(1, T, 1, D).to(DEV), v.view(1, T, 1, D).to(DEV), i32([T]), k_shift=shift, v_shift=shift)
     assert new.tolist() == [T]
     np.testing.assert_array_equal(c.cpu().numpy(), exp)
+
+
+@pytest.mark.parametrize("N", [49, 65])
+def test_attend_batches_next_to_the_shared_memory_limit(N):
+    """The prefix sums of a batch lie in shared memory beside the buffers: every batch
+    up to the largest is taken."""
+    D, P = 128, 32
+    rng = np.random.default_rng(N)
+    for B in [*range(2560, 2920, 24), 2703, 2704, 2767, 2768, 2799, 2800, 2863, 2864, 4096]:
+        lengths = rng.integers(0, 4, B)
+        q = torch.randn(B, N, 1, D, device=DEV, dtype=torch.bfloat16)
+        k, v = (torch.randn(B, N, 1, D, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+        pages = base._cache(rng, 8, 1, P, D)
+        table = rng.integers(0, 8, (B, 1))
+        got = sv.spec_attend_q4(q, torch.from_numpy(pages).to(DEV), i32(table), i32(lengths), k_new=k, v_new=v)
+        rows = [0, B // 2, B - 1]
+        see = np.broadcast_to(np.tril(np.ones((N, N), bool)), (3, N, N))
+        exp = ref.attend(f64(q[rows]), pages, table[rows], lengths[rows], f64(k[rows]), f64(v[rows]), see, D ** -0.5, 0, 0)
+        _close([x[rows] for x in got], exp, D)
+        assert torch.isfinite(got[0]).all() and torch.isfinite(got[1]).all()
