@@ -56,6 +56,9 @@ namespace sv {
 constexpr int TC_TILE = 128;                 // tokens of a tile
 constexpr int TC_FRESH_UNITS = 9;            // what a triple's first fresh tile counts in the list, in cached tiles
 constexpr int TC_PART = 32;                  // rows of a softmax thread
+// 7 - reference before any score.  Finite, so that a score of -inf weighs nothing
+// against it; every other score is far above the reference and sets a new one.
+constexpr float TC_UNSET = -AT_UNSET;
 constexpr uint32_t TC_VBUF = 128 * 128 * 2;  // bytes of a V buffer (16 groups of 8 columns, also for D = 64)
 
 template <int D, int NC>
@@ -75,7 +78,7 @@ struct TcLayout {
   static constexpr uint32_t p = v + 2 * TC_VBUF;
   static constexpr uint32_t q = p + 2 * p_bytes;
   static constexpr uint32_t factor = q + QB * q_bytes;         // [2][NC]: from products to the log2 domain
-  static constexpr uint32_t shift = factor + 2 * NC * 4;      // [NC]: 7 - reference (inf: none yet)
+  static constexpr uint32_t shift = factor + 2 * NC * 4;      // [NC]: 7 - reference (TC_UNSET: none yet)
   static constexpr uint32_t corr = shift + NC * 4;             // [NC]
   static constexpr uint32_t top = corr + NC * 4;               // [4][NC]: maxima or sums of the four warps
   static constexpr uint32_t seen = top + 4 * NC * 4;           // [4][NC]: mask words
@@ -620,10 +623,10 @@ __device__ __noinline__ void tc_raise(uint32_t s_at, uint32_t o_at, const float*
   named_bar_sync(id, 128);
   if (quad == 0) {
     const float m = fmaxf(fmaxf(top[lane], top[NC + lane]), fmaxf(top[2 * NC + lane], top[3 * NC + lane]));
-    const float old = shift[lane];                                // 7 - ref, inf: none
+    const float old = shift[lane];                                // 7 - ref
     const float now = m == kNegInf ? old : fminf(old, AT_PSHIFT - m);
     shift[lane] = now;
-    corr[lane] = old == __builtin_huge_valf() ? 1.f : at_corr(now - old);
+    corr[lane] = at_corr(now - old);
   }
   named_bar_sync(id, 128);
   if (sums) {
@@ -1004,7 +1007,7 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
         itri = t.c.i;
 #pragma unroll
         for (int i = 0; i < HC / 2; ++i) l[i] = 0.f;
-        for (int i = threadIdx.x & 127; i < HC; i += 128) shift[i] = __builtin_huge_valf();
+        for (int i = threadIdx.x & 127; i < HC; i += 128) shift[i] = TC_UNSET;
         named_bar_sync(id, 128);
       }
       // (A warp whose wait fails goes on in step with the others, which it meets at
@@ -1077,7 +1080,7 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
         }
 #pragma unroll
         for (int i = 0; i < HC; i += 2) m = fmax3_nan(m, y[i], y[i + 1]);
-        // (a row without a reference: a score that counts is infinite there)
+        // (in a row without a reference every score but -inf is far above it)
         if (__builtin_expect(again || !tc_any<128>(id, !(m <= AT_PSHIFT + AT_ABOVE)), 1)) break;
         if (!t.first) tc_wait(&bar->pvdone[(n - 1) & 1], ((n - 1) >> 1) & 1, bar, a.timeout_ns);
         tc_raise<NC>(s_at, o_at, factor, shift, corr, top, hide, !t.first, quad, id);

@@ -60,3 +60,19 @@ def test_attend_batches_next_to_the_shared_memory_limit(N):
         exp = ref.attend(f64(q[rows]), pages, table[rows], lengths[rows], f64(k[rows]), f64(v[rows]), see, D ** -0.5, 0, 0)
         _close([x[rows] for x in got], exp, D)
         assert torch.isfinite(got[0]).all() and torch.isfinite(got[1]).all()
+
+
+@pytest.mark.parametrize("N,Hq,Hkv,D", ROWS)
+@pytest.mark.parametrize("every", [False, True])
+def test_attend_scores_of_minus_infinity(N, Hq, Hkv, D, every):
+    """A key with an infinity of the other sign than the queries' element gives every
+    row that sees it a score of -inf, which weighs nothing: the first node's (all that
+    row 0 sees of the fresh entries), or every node's."""
+    c = _case(70 + N, 3, N, Hq, Hkv, D, 32, [0, 300, 33], shifts=(1, -1))
+    c["q"][..., 5] = c["q"][..., 5].abs() + 0.5
+    see = c["see"].copy()
+    see[:, :, slice(None) if every else 0] = False
+    exp = _expect(dict(c, see=see))
+    c["k"][:, slice(None) if every else 0, :, 5] = float("-inf")
+    assert (exp[1][0, 0] == -np.inf).all() and np.isfinite(exp[1][1:]).all()
+    _close(_attend(c), exp, D)
