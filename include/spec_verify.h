@@ -431,6 +431,18 @@ spec_status_t spec_attend_q4(const void *q, const void *k_new, const void *v_new
                              int v_shift, float scale, void *out, float *lse, void *workspace,
                              size_t workspace_bytes, void *stream);
 
+/* Test hook for the attention's bounded waits: runs spec_attend_q4 with every
+ * device-side wait limited to timeout_us microseconds (100..1000000) while CTA
+ * stall_cta leaves out the first copy of its share of the cached tokens, so that
+ * the wait for it runs out.  What that CTA works on is NaN in out and lse, the
+ * rest is as without the hook, and the context and the workspace stay usable.
+ * SPEC_ERR_UNSUPPORTED for few rows a kv head. */
+spec_status_t spec_debug_attend_stall(const void *q, const void *k_new, const void *v_new, const uint32_t *masks,
+                                      const void *cache, const int32_t *block_table, const int32_t *lengths, int B,
+                                      int N, int Hq, int Hkv, int D, int page_tokens, int num_pages, int max_pages,
+                                      int k_shift, int v_shift, float scale, int stall_cta, unsigned timeout_us,
+                                      void *out, float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
 /* Penalties, biases and grammar masks on the logits of a verification (the
  * target's rows) or of a drafting step.
  *

@@ -13,5 +13,5 @@ from .binding import (  # noqa: F401
     spec_verify_sample_noalloc, spec_tree_mask, spec_kv_commit, spec_row_stats, spec_tree_draft,
     spec_verify_tree_greedy, spec_workspace_bytes, status_string, workspace,
     q4_cache, spec_adjust_logits, spec_attend_q4, spec_attend_workspace_bytes, spec_kv_commit_q4, spec_kv_store_q4,
-    spec_page_map, spec_q4_block_bytes,
+    spec_page_map, spec_q4_block_bytes, spec_debug_attend_stall,
 )

@@ -84,6 +84,8 @@ def lib() -> ctypes.CDLL:
             L.spec_attend_workspace_bytes.restype = Z
             L.spec_attend_q4.argtypes = [P] * 7 + [I] * 10 + [F, P, P, P, Z, P]
             L.spec_attend_q4.restype = I
+            L.spec_debug_attend_stall.argtypes = [P] * 7 + [I] * 10 + [F, I, ctypes.c_uint, P, P, P, Z, P]
+            L.spec_debug_attend_stall.restype = I
             L.spec_adjust_logits.argtypes = [P, I] + [P] * 11 + [I] * 6 + [P] * 2
             L.spec_adjust_logits.restype = I
             L.spec_profile_begin.argtypes = [I]
@@ -549,6 +551,28 @@ def spec_attend_q4(q, cache, block_table, lengths, *, k_new=None, v_new=None, ma
         _take(workspace_buf, "workspace_buf", torch.uint8, (workspace_buf.numel(),), dev), workspace_buf.numel(), stream)
     if st:
         _check("spec_attend_q4", st)
+    return out, lse
+
+
+@_serve
+def spec_debug_attend_stall(q, cache, block_table, lengths, stall_cta: int, timeout_us: int, *, k_new=None, v_new=None,
+                            dev=None, stream=None):
+    """Test hook: spec_attend_q4 with short wait limits while CTA stall_cta waits for a
+    copy that never comes.  Returns (out, lse); what that CTA works on is NaN."""
+    pages, Hkv, P, D = _q4_shape(cache)
+    B, N, Hq = q.shape[0], q.shape[1], q.shape[2]
+    i32, bf = torch.int32, torch.bfloat16
+    out = torch.empty_like(q)
+    lse = torch.empty((B, N, Hq), dtype=torch.float32, device=q.device)
+    ws = workspace(spec_attend_workspace_bytes(B, N, Hq, Hkv, D), q.device)
+    table = _cols(block_table, B, "block_table")
+    st = lib().spec_debug_attend_stall(
+        _take(q, "q", bf, (B, N, Hq, D), dev), _take(k_new, "k_new", bf, (B, N, Hkv, D), dev),
+        _take(v_new, "v_new", bf, (B, N, Hkv, D), dev), None, _take(cache, "cache", torch.uint8, cache.shape, dev),
+        _take(block_table, "block_table", i32, table, dev), _take(lengths, "lengths", i32, (B,), dev), B, N, Hq, Hkv, D, P,
+        pages, table[1], 0, 0, D ** -0.5, int(stall_cta), int(timeout_us), out.data_ptr(), lse.data_ptr(), ws.data_ptr(),
+        ws.numel(), stream)
+    _check("spec_debug_attend_stall", st)
     return out, lse
 
 

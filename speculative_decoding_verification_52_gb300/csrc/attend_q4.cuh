@@ -90,6 +90,7 @@ struct AttendArgs {
   float* lse;                // [B, N, Hkv * G] or null
   float* ws;
   unsigned long long timeout_ns;
+  int stall;                 // test hook: 1 + the CTA whose first copy is left out (0: none)
 };
 
 // ---------------------------------------------------------------------------

@@ -105,6 +105,7 @@ struct TcBars {
   float qmax[4], qmin[4];
   int wide[2];    // 1 + the last tile of the buffer that has fresh entries out of range
   int arrived[4]; // the stage's tile came (its page ids are in range)
+  int copied;     // tiles whose copies were started, once the copying warp has ended
 };
 static_assert(sizeof(TcBars) <= 384, "barriers");
 
@@ -746,7 +747,7 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
       bar->wide[i] = 0;
     }
     mbar_init(&bar->drain, 1);
-    bar->dead = 0;
+    bar->dead = bar->copied = 0;
     mbar_fence_init();
   }
   at_prefix<L::THREADS>(a, prefix, scratch);   // (synchronises the CTA)
@@ -786,12 +787,17 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
         const int mine = __shfl_sync(0xffffffffu, page, blk - page_at + (lane & 3));
         const bool ok = lane >= nblk || (mine >= 0 && mine < a.pages);
         const int s = n % L::STAGES;
+        // (Warps whose wait has failed go on in step and release stages whose copies may
+        // still be on their way; the flag was set before they did.)
         bool go = true;
-        if (n >= L::STAGES) go = tc_wait(&bar->empty[s], ((n / L::STAGES) & 1) ^ 1, bar, a.timeout_ns);
+        if (n >= L::STAGES)
+          go = tc_wait(&bar->empty[s], ((n / L::STAGES) & 1) ^ 1, bar, a.timeout_ns) && !__any_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&bar->dead));
         if (!go) break;
         const bool all = __all_sync(0xffffffffu, ok);
         if (lane == 0) bar->arrived[s] = all;
-        if (all) {
+        if (TC_RARE(n == 0 && a.stall == static_cast<int>(blockIdx.x) + 1)) {
+          // (test hook: this tile never comes)
+        } else if (all) {
           if (lane == 0) mbar_arrive_expect_tx(&bar->full[s], nblk * q4_block_bytes(D));
           __syncwarp();
           if (lane < nblk) {
@@ -822,9 +828,7 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
       if ((u += t.step) >= ntiles) break;
       tc_step<NC>(a, prefix, HR, nfresh, ntiles - u, t);
     }
-    // copies still on their way land before the CTA ends (or the wait gives up)
-    if (*reinterpret_cast<volatile int*>(&bar->dead))
-      for (int i = max(0, n - L::STAGES); i < n; ++i) mbar_wait(&bar->full[i % L::STAGES], (i / L::STAGES) & 1, a.timeout_ns);
+    if (lane == 0) bar->copied = n;
   } else if (warp == L::SOFT + L::UNPACK) {
     // ---- products: one thread ------------------------------------------------------------
     if (lane == 0) {
@@ -1144,7 +1148,14 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (the join kernel may start; it waits for this grid's end)
   __syncthreads();
   if (*reinterpret_cast<volatile int*>(&bar->dead)) {
-    // a wait ran out of time: every triple of the share is void
+    // A wait ran out of time (every role has ended, so this is settled).  Copies still on
+    // their way land before the CTA ends, or a wait for them gives up.
+    if (warp == L::SOFT + L::UNPACK + 1) {
+      const int n = *reinterpret_cast<volatile int*>(&bar->copied);
+      for (int i = max(0, n - L::STAGES); i < n; ++i)
+        if (i > 0 || a.stall != static_cast<int>(blockIdx.x) + 1) mbar_wait(&bar->full[i % L::STAGES], (i / L::STAGES) & 1, a.timeout_ns);
+    }
+    // Every triple of the share is void.
     TcTile t;
     tc_begin<NC>(a, prefix, HR, nfresh, u0, ntiles, t);
     int i0 = t.c.i;

@@ -193,6 +193,78 @@ AttendPlan attend_plan(int B, int rows, int D) {
   return p;
 }
 
+// spec_attend_q4, and with stall_cta >= 0 its test hook
+spec_status_t attend_entry(const void* q, const void* k_new, const void* v_new, const uint32_t* masks,
+                           const void* cache, const int32_t* block_table, const int32_t* lengths, int B, int N,
+                           int Hq, int Hkv, int D, int page_tokens, int num_pages, int max_pages, int k_shift,
+                           int v_shift, float scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+                           void* stream, int stall_cta = -1, unsigned long long timeout_ns = kWaitNs) {
+  try {
+    spec_status_t s = check_q4(Hkv, D, page_tokens, num_pages, k_shift, v_shift);
+    if (s != SPEC_OK) return s;
+    if (B < 0 || N < 1 || N > SPEC_MAX_TREE_NODES || max_pages < 1)
+      return fail(SPEC_ERR_INVALID_ARG, "bad sizes B=%d N=%d max_pages=%d (N in [1, %d])", B, N, max_pages, SPEC_MAX_TREE_NODES);
+    if (Hq < 1 || Hq % Hkv != 0) return fail(SPEC_ERR_INVALID_ARG, "Hq=%d is not a multiple of Hkv=%d", Hq, Hkv);
+    if (Hq / Hkv > 64) return fail(SPEC_ERR_UNSUPPORTED, "%d query heads to a kv head: at most 64", Hq / Hkv);
+    if (B > AT_MAX_B) return fail(SPEC_ERR_UNSUPPORTED, "B=%d beyond %d", B, AT_MAX_B);
+    if (!below_2g(max_pages, page_tokens)) return fail(SPEC_ERR_UNSUPPORTED, "max_pages * page_tokens must stay below 2^31");
+    if (!std::isfinite(scale)) return fail(SPEC_ERR_INVALID_ARG, "scale must be finite");
+    if ((k_new == nullptr) != (v_new == nullptr)) return fail(SPEC_ERR_INVALID_ARG, "k_new and v_new come together");
+    if (masks && !k_new) return fail(SPEC_ERR_INVALID_ARG, "masks without k_new and v_new");
+    if (B == 0) return SPEC_OK;
+    if (!q || !cache || !block_table || !lengths || !out) return fail(SPEC_ERR_INVALID_ARG, "NULL q/cache/block_table/lengths/out");
+    if (!aligned16(q) || !aligned16(cache) || !aligned16(out) || !aligned16(k_new) || !aligned16(v_new))
+      return fail(SPEC_ERR_INVALID_ARG, "q, k_new, v_new, cache and out must be 16-byte aligned");
+    s = check_ws(workspace, workspace_bytes, spec_attend_workspace_bytes(B, N, Hq, Hkv, D));
+    if (s != SPEC_OK) return s;
+    int dev;
+    DevInfo di;
+    s = device_info(di, dev);
+    if (s != SPEC_OK) return s;
+    AttendArgs a{};
+    a.q = static_cast<const uint16_t*>(q);
+    a.k_new = static_cast<const uint16_t*>(k_new);
+    a.v_new = static_cast<const uint16_t*>(v_new);
+    a.masks = masks;
+    a.cache = static_cast<const unsigned char*>(cache);
+    a.table = block_table;
+    a.lengths = lengths;
+    a.B = B;
+    a.N = N;
+    a.G = Hq / Hkv;
+    a.Hkv = Hkv;
+    a.P = page_tokens;
+    a.pages = num_pages;
+    a.W = max_pages;
+    a.NW = (N + 31) / 32;
+    const AttendPlan plan = attend_plan(B, N * a.G, D);
+    if (stall_cta >= 0 && !plan.tc) return fail(SPEC_ERR_UNSUPPORTED, "the test hook needs more rows");
+    a.row_tiles = plan.tiles;
+    a.by_g = a.G > 1 ? static_cast<uint32_t>((0x100000000ull + a.G - 1) / a.G) : 0u;
+    a.tile = plan.tc ? TC_TILE : AT_TILE;
+    a.fresh = plan.tc ? TC_FRESH_UNITS : AT_FRESH;
+    a.fresh_more = plan.tc ? 1 : AT_FRESH;
+    a.scale_log2 = static_cast<float>(1.4426950408889634 * static_cast<double>(scale));
+    a.k_mul = std::ldexp(1.f, k_shift);
+    a.v_mul = std::ldexp(1.f, v_shift);
+    a.out = static_cast<uint16_t*>(out);
+    a.lse = lse;
+    a.ws = static_cast<float*>(workspace);
+    a.timeout_ns = timeout_ns;
+    a.stall = stall_cta + 1;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    prof_mark(0, st);
+    if (plan.tc) s = launch_attend_tc(D, plan.size, di, dev, a, st);
+    else s = D == 128 ? launch_attend<128>(plan.size, di, dev, a, st) : launch_attend<64>(plan.size, di, dev, a, st);
+    if (s != SPEC_OK) return s;
+    prof_mark(1, st);
+    prof_mark(2, st);
+    return SPEC_OK;
+  } catch (...) {
+    return fail(SPEC_ERR_CUDA, "unexpected host exception");
+  }
+}
+
 // ---------------------------------------------------------------------------
 // logit adjustments
 // ---------------------------------------------------------------------------
@@ -379,68 +451,20 @@ spec_status_t spec_attend_q4(const void* q, const void* k_new, const void* v_new
                              int Hq, int Hkv, int D, int page_tokens, int num_pages, int max_pages, int k_shift,
                              int v_shift, float scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
                              void* stream) {
-  try {
-    spec_status_t s = check_q4(Hkv, D, page_tokens, num_pages, k_shift, v_shift);
-    if (s != SPEC_OK) return s;
-    if (B < 0 || N < 1 || N > SPEC_MAX_TREE_NODES || max_pages < 1)
-      return fail(SPEC_ERR_INVALID_ARG, "bad sizes B=%d N=%d max_pages=%d (N in [1, %d])", B, N, max_pages, SPEC_MAX_TREE_NODES);
-    if (Hq < 1 || Hq % Hkv != 0) return fail(SPEC_ERR_INVALID_ARG, "Hq=%d is not a multiple of Hkv=%d", Hq, Hkv);
-    if (Hq / Hkv > 64) return fail(SPEC_ERR_UNSUPPORTED, "%d query heads to a kv head: at most 64", Hq / Hkv);
-    if (B > AT_MAX_B) return fail(SPEC_ERR_UNSUPPORTED, "B=%d beyond %d", B, AT_MAX_B);
-    if (!below_2g(max_pages, page_tokens)) return fail(SPEC_ERR_UNSUPPORTED, "max_pages * page_tokens must stay below 2^31");
-    if (!std::isfinite(scale)) return fail(SPEC_ERR_INVALID_ARG, "scale must be finite");
-    if ((k_new == nullptr) != (v_new == nullptr)) return fail(SPEC_ERR_INVALID_ARG, "k_new and v_new come together");
-    if (masks && !k_new) return fail(SPEC_ERR_INVALID_ARG, "masks without k_new and v_new");
-    if (B == 0) return SPEC_OK;
-    if (!q || !cache || !block_table || !lengths || !out) return fail(SPEC_ERR_INVALID_ARG, "NULL q/cache/block_table/lengths/out");
-    if (!aligned16(q) || !aligned16(cache) || !aligned16(out) || !aligned16(k_new) || !aligned16(v_new))
-      return fail(SPEC_ERR_INVALID_ARG, "q, k_new, v_new, cache and out must be 16-byte aligned");
-    s = check_ws(workspace, workspace_bytes, spec_attend_workspace_bytes(B, N, Hq, Hkv, D));
-    if (s != SPEC_OK) return s;
-    int dev;
-    DevInfo di;
-    s = device_info(di, dev);
-    if (s != SPEC_OK) return s;
-    AttendArgs a{};
-    a.q = static_cast<const uint16_t*>(q);
-    a.k_new = static_cast<const uint16_t*>(k_new);
-    a.v_new = static_cast<const uint16_t*>(v_new);
-    a.masks = masks;
-    a.cache = static_cast<const unsigned char*>(cache);
-    a.table = block_table;
-    a.lengths = lengths;
-    a.B = B;
-    a.N = N;
-    a.G = Hq / Hkv;
-    a.Hkv = Hkv;
-    a.P = page_tokens;
-    a.pages = num_pages;
-    a.W = max_pages;
-    a.NW = (N + 31) / 32;
-    const AttendPlan plan = attend_plan(B, N * a.G, D);
-    a.row_tiles = plan.tiles;
-    a.by_g = a.G > 1 ? static_cast<uint32_t>((0x100000000ull + a.G - 1) / a.G) : 0u;
-    a.tile = plan.tc ? TC_TILE : AT_TILE;
-    a.fresh = plan.tc ? TC_FRESH_UNITS : AT_FRESH;
-    a.fresh_more = plan.tc ? 1 : AT_FRESH;
-    a.scale_log2 = static_cast<float>(1.4426950408889634 * static_cast<double>(scale));
-    a.k_mul = std::ldexp(1.f, k_shift);
-    a.v_mul = std::ldexp(1.f, v_shift);
-    a.out = static_cast<uint16_t*>(out);
-    a.lse = lse;
-    a.ws = static_cast<float*>(workspace);
-    a.timeout_ns = kWaitNs;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    prof_mark(0, st);
-    if (plan.tc) s = launch_attend_tc(D, plan.size, di, dev, a, st);
-    else s = D == 128 ? launch_attend<128>(plan.size, di, dev, a, st) : launch_attend<64>(plan.size, di, dev, a, st);
-    if (s != SPEC_OK) return s;
-    prof_mark(1, st);
-    prof_mark(2, st);
-    return SPEC_OK;
-  } catch (...) {
-    return fail(SPEC_ERR_CUDA, "unexpected host exception");
-  }
+  return attend_entry(q, k_new, v_new, masks, cache, block_table, lengths, B, N, Hq, Hkv, D, page_tokens, num_pages,
+                      max_pages, k_shift, v_shift, scale, out, lse, workspace, workspace_bytes, stream);
+}
+
+spec_status_t spec_debug_attend_stall(const void* q, const void* k_new, const void* v_new, const uint32_t* masks,
+                                      const void* cache, const int32_t* block_table, const int32_t* lengths, int B,
+                                      int N, int Hq, int Hkv, int D, int page_tokens, int num_pages, int max_pages,
+                                      int k_shift, int v_shift, float scale, int stall_cta, unsigned timeout_us,
+                                      void* out, float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  if (stall_cta < 0 || timeout_us < 100 || timeout_us > 1000000)
+    return fail(SPEC_ERR_INVALID_ARG, "stall_cta=%d timeout_us=%u (at least 0; 100..1000000)", stall_cta, timeout_us);
+  return attend_entry(q, k_new, v_new, masks, cache, block_table, lengths, B, N, Hq, Hkv, D, page_tokens, num_pages,
+                      max_pages, k_shift, v_shift, scale, out, lse, workspace, workspace_bytes, stream, stall_cta,
+                      1000ull * timeout_us);
 }
 
 spec_status_t spec_adjust_logits(const void* logits, spec_dtype_t dtype, const int32_t* history,

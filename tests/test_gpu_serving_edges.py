@@ -4,6 +4,8 @@ their types' ranges, the largest batches, waits that run out.
 Tolerances are those of test_gpu_serving.py (derived there); where a score is an
 infinity, the expected values come from the same reference with that node left out,
 which is what a weight of zero means."""
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -76,3 +78,34 @@ def test_attend_scores_of_minus_infinity(N, Hq, Hkv, D, every):
     c["k"][:, slice(None) if every else 0, :, 5] = float("-inf")
     assert (exp[1][0, 0] == -np.inf).all() and np.isfinite(exp[1][1:]).all()
     _close(_attend(c), exp, D)
+
+
+def _stalled(seed, B, N, Hq, Hkv, D, fresh, ctas):
+    """Calls in which a CTA's first copy is never started: what the CTA works on is NaN,
+    everything else has the bits of an ordinary call, and so has the next call."""
+    rng = np.random.default_rng(seed)
+    lengths, pages = rng.integers(1500, 2500, B), 64
+    cache = torch.from_numpy(base._cache(rng, pages, Hkv, 32, D)).to(DEV)
+    table, lens = i32(rng.integers(0, pages, (B, 80))), i32(lengths)
+    q = torch.randn(B, N, Hq, D, device=DEV, dtype=torch.bfloat16)
+    new = {x: torch.randn(B, N, Hkv, D, device=DEV, dtype=torch.bfloat16) for x in ("k_new", "v_new")} if fresh else {}
+    out, lse = sv.spec_attend_q4(q, cache, table, lens, **new)
+    assert torch.isfinite(lse).all()
+    for cta in (*ctas, 100000):
+        torch.cuda.synchronize()
+        t0 = time.perf_counter()
+        o, l = sv.spec_debug_attend_stall(q, cache, table, lens, cta, 2000, **new)
+        torch.cuda.synchronize()
+        assert time.perf_counter() - t0 < 5
+        void = torch.isnan(l)
+        assert void.any().item() == (cta < 100000) and not void.all()
+        assert torch.equal(torch.isnan(o), void[..., None].expand_as(o))
+        assert torch.equal(l[~void], lse[~void]) and torch.equal(o[~void], out[~void])
+        a = sv.spec_attend_q4(q, cache, table, lens, **new)
+        assert torch.equal(a[0], out) and torch.equal(a[1], lse)
+
+
+@pytest.mark.parametrize("B,N,Hq,Hkv,D", [(60, 13, 4, 1, 128), (40, 16, 16, 2, 128), (40, 65, 4, 2, 64), (30, 130, 2, 2, 128)])
+@pytest.mark.parametrize("fresh", [False, True])
+def test_attend_wait_that_runs_out_with_many_rows(B, N, Hq, Hkv, D, fresh):
+    _stalled(B, B, N, Hq, Hkv, D, fresh, (0, 1, 77, 151))

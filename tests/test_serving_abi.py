@@ -157,3 +157,11 @@ def test_reference_page_map_by_hand():
     assert slots.tolist() == [15, 12, 16, 17, 18, 19, 20, 21, -1]
     assert held.tolist() == [2, 2, 0] and state.tolist() == [1, 4]
     assert rng[3:5].tolist() == [4, 2]
+
+
+@pytest.mark.parametrize("kw,status", [(dict(cta=-1), BAD), (dict(us=99), BAD), (dict(us=1000001), BAD), (dict(N=0), BAD), (dict(D=96), UNSUP),
+                                       (dict(p_ws=0), WS), (dict(B=0, p_q=0, p_ws=0, wsb=0), B.SPEC_OK)])
+def test_attend_stall_hook_refusals(L, kw, status):
+    at = list(ATT).index("p_out")
+    args = dict(list(ATT.items())[:at] + [("cta", 0), ("us", 2000)] + list(ATT.items())[at:])
+    assert _call(L.spec_debug_attend_stall, args, **kw) == status
