@@ -433,10 +433,11 @@ spec_status_t spec_attend_q4(const void *q, const void *k_new, const void *v_new
 
 /* Test hook for the attention's bounded waits: runs spec_attend_q4 with every
  * device-side wait limited to timeout_us microseconds (100..1000000) while CTA
- * stall_cta leaves out the first copy of its share of the cached tokens, so that
- * the wait for it runs out.  What that CTA works on is NaN in out and lse, the
- * rest is as without the hook, and the context and the workspace stay usable.
- * SPEC_ERR_UNSUPPORTED for few rows a kv head. */
+ * stall_cta waits for one arrival more than the first copy of its share of the
+ * cached tokens brings, so that this wait runs out.  What waits for the copy (the
+ * CTA's share, with few rows a kv head the first half of it) is NaN in out and
+ * lse, the rest is as without the hook, and the context and the workspace stay
+ * usable. */
 spec_status_t spec_debug_attend_stall(const void *q, const void *k_new, const void *v_new, const uint32_t *masks,
                                       const void *cache, const int32_t *block_table, const int32_t *lengths, int B,
                                       int N, int Hq, int Hkv, int D, int page_tokens, int num_pages, int max_pages,

@@ -557,8 +557,8 @@ def spec_attend_q4(q, cache, block_table, lengths, *, k_new=None, v_new=None, ma
 @_serve
 def spec_debug_attend_stall(q, cache, block_table, lengths, stall_cta: int, timeout_us: int, *, k_new=None, v_new=None,
                             dev=None, stream=None):
-    """Test hook: spec_attend_q4 with short wait limits while CTA stall_cta waits for a
-    copy that never comes.  Returns (out, lse); what that CTA works on is NaN."""
+    """Test hook: spec_attend_q4 with short wait limits while CTA stall_cta waits for an
+    arrival that never comes.  Returns (out, lse); what waits for it is NaN."""
     pages, Hkv, P, D = _q4_shape(cache)
     B, N, Hq = q.shape[0], q.shape[1], q.shape[2]
     i32, bf = torch.int32, torch.bfloat16

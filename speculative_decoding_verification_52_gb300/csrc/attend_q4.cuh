@@ -90,7 +90,7 @@ struct AttendArgs {
   float* lse;                // [B, N, Hkv * G] or null
   float* ws;
   unsigned long long timeout_ns;
-  int stall;                 // test hook: 1 + the CTA whose first copy is left out (0: none)
+  int stall;                 // test hook: 1 + the CTA whose first stage waits for one arrival too many (0: none)
 };
 
 // ---------------------------------------------------------------------------
@@ -243,7 +243,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 __host__ __device__ constexpr int at_stage_bytes(int D) { return 2 * q4_block_bytes(D); }
 // of a pair: the queries' operand; in exchange, two buffers each, the weights
 // (each warp's operands), the maxima or sums, and the flags; a flag a stage (at
-// most 8); the list of fetches
+// most 8) and one more; the list of fetches
 __host__ __device__ constexpr int at_q_bytes(int D, int NR) { return NR * (D / 32) * 512; }
 __host__ __device__ constexpr int at_p_bytes(int NR) { return 2 * 2 * 2 * NR * 256; }
 __host__ __device__ constexpr int at_m_bytes(int NR) { return 2 * 2 * 8 * NR * 4; }
@@ -342,6 +342,8 @@ struct AtState {
   }
 };
 
+constexpr int AT_STUCK = 1 << 8;
+
 // What the two warps of a pair share.
 template <int D, int NR>
 struct AtPair {
@@ -359,6 +361,8 @@ struct AtPair {
     return reinterpret_cast<int*>(base + at_q_bytes(D, NR) + at_p_bytes(NR) + at_m_bytes(NR)) + buf * 2 + warp;
   }
   __device__ __forceinline__ int* arrived(int stage) const { return flag(2, 0) + stage; }
+  // AT_STUCK and the stages' phases at the time, once a wait of the first warp has failed
+  __device__ __forceinline__ int* stuck() const { return flag(2, 0) + 8; }
   __device__ __forceinline__ uint2* queue() const {
     return reinterpret_cast<uint2*>(base + at_q_bytes(D, NR) + at_p_bytes(NR) + at_m_bytes(NR) + 64);
   }
@@ -928,6 +932,19 @@ __device__ __forceinline__ uint2 at_source(const AttendArgs& a, const long long*
   return r;
 }
 
+// Once one of the pair's waits has failed: waits until no copy is on its way to the
+// stages, or, where some never came or none was started, for the limit once more.  (What
+// was started and not waited for is the next phase of its stage.)
+__device__ __noinline__ void at_drain(uint64_t* bars, int stages, uint32_t phase, unsigned long long limit) {
+  const uint64_t t0 = global_ns();
+  uint32_t open = (1u << stages) - 1u;
+  for (int i = 0; i < (1 << 24) && open; ++i) {
+    for (int s = 0; s < stages; ++s)
+      if (((open >> s) & 1u) && mbar_try_wait(&bars[s], (phase >> s) & 1u)) open ^= 1u << s;
+    if (global_ns() - t0 > limit) return;
+  }
+}
+
 template <int D, int NR>
 __global__ void __launch_bounds__(AT_THREADS, at_ctas(D, NR)) attend_q4_kernel(const __grid_constant__ AttendArgs a, int stages) {
   extern __shared__ __align__(128) unsigned char at_smem[];
@@ -944,6 +961,8 @@ __global__ void __launch_bounds__(AT_THREADS, at_ctas(D, NR)) attend_q4_kernel(c
 
   if ((threadIdx.x & 63) == 0) {
     for (int s = 0; s < stages; ++s) mbar_init(&bars[s], 1);
+    if (a.stall == static_cast<int>(blockIdx.x) + 1 && pair == 0) mbar_init(&bars[0], 2);   // (test hook)
+    *pr.stuck() = 0;
     mbar_fence_init();
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (the join kernel may start; it waits for this grid's end)
@@ -1038,7 +1057,8 @@ __global__ void __launch_bounds__(AT_THREADS, at_ctas(D, NR)) attend_q4_kernel(c
         // (a warp whose wait gave up goes on in step with the other one, over what
         // the stage holds, and its result is void)
         if (!failed && !mbar_wait(&bars[stage], (phase >> stage) & 1u, a.timeout_ns)) {
-          failed = true;   // no more copies are started; those on their way have had their time
+          failed = true;   // no more copies are started
+          if ((threadIdx.x & 63) == 0) *pr.stuck() = static_cast<int>(phase) | AT_STUCK;
         }
         phase ^= 1u << stage;
         poison |= !*pr.arrived(stage);
@@ -1057,6 +1077,7 @@ __global__ void __launch_bounds__(AT_THREADS, at_ctas(D, NR)) attend_q4_kernel(c
     }
   }
   __syncthreads();
+  if ((threadIdx.x & 63) == 0 && __builtin_expect(*pr.stuck(), 0)) at_drain(bars, stages, *pr.stuck(), a.timeout_ns);
 
   // Joins within the CTA.  A triple that begins in a pair's share and goes on is
   // joined by that pair, whose registers hold its first part; the other parts

@@ -731,7 +731,7 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&bar->full[i], 1);
+      mbar_init(&bar->full[i], i == 0 && a.stall == static_cast<int>(blockIdx.x) + 1 ? 2 : 1);   // (2: test hook)
       mbar_init(&bar->empty[i], L::UNPACK);
     }
     for (int i = 0; i < 2; ++i) {
@@ -795,9 +795,7 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
         if (!go) break;
         const bool all = __all_sync(0xffffffffu, ok);
         if (lane == 0) bar->arrived[s] = all;
-        if (TC_RARE(n == 0 && a.stall == static_cast<int>(blockIdx.x) + 1)) {
-          // (test hook: this tile never comes)
-        } else if (all) {
+        if (all) {
           if (lane == 0) mbar_arrive_expect_tx(&bar->full[s], nblk * q4_block_bytes(D));
           __syncwarp();
           if (lane < nblk) {
@@ -1152,8 +1150,7 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
     // their way land before the CTA ends, or a wait for them gives up.
     if (warp == L::SOFT + L::UNPACK + 1) {
       const int n = *reinterpret_cast<volatile int*>(&bar->copied);
-      for (int i = max(0, n - L::STAGES); i < n; ++i)
-        if (i > 0 || a.stall != static_cast<int>(blockIdx.x) + 1) mbar_wait(&bar->full[i % L::STAGES], (i / L::STAGES) & 1, a.timeout_ns);
+      for (int i = max(0, n - L::STAGES); i < n; ++i) mbar_wait(&bar->full[i % L::STAGES], (i / L::STAGES) & 1, a.timeout_ns);
     }
     // Every triple of the share is void.
     TcTile t;

@@ -238,7 +238,6 @@ spec_status_t attend_entry(const void* q, const void* k_new, const void* v_new, 
     a.W = max_pages;
     a.NW = (N + 31) / 32;
     const AttendPlan plan = attend_plan(B, N * a.G, D);
-    if (stall_cta >= 0 && !plan.tc) return fail(SPEC_ERR_UNSUPPORTED, "the test hook needs more rows");
     a.row_tiles = plan.tiles;
     a.by_g = a.G > 1 ? static_cast<uint32_t>((0x100000000ull + a.G - 1) / a.G) : 0u;
     a.tile = plan.tc ? TC_TILE : AT_TILE;

@@ -81,7 +81,7 @@ def test_attend_scores_of_minus_infinity(N, Hq, Hkv, D, every):
 
 
 def _stalled(seed, B, N, Hq, Hkv, D, fresh, ctas):
-    """Calls in which a CTA's first copy is never started: what the CTA works on is NaN,
+    """Calls in which a CTA waits for an arrival that never comes: what it works on is NaN,
     everything else has the bits of an ordinary call, and so has the next call."""
     rng = np.random.default_rng(seed)
     lengths, pages = rng.integers(1500, 2500, B), 64
@@ -109,3 +109,9 @@ def _stalled(seed, B, N, Hq, Hkv, D, fresh, ctas):
 @pytest.mark.parametrize("fresh", [False, True])
 def test_attend_wait_that_runs_out_with_many_rows(B, N, Hq, Hkv, D, fresh):
     _stalled(B, B, N, Hq, Hkv, D, fresh, (0, 1, 77, 151))
+
+
+@pytest.mark.parametrize("B,N,Hq,Hkv,D", [(120, 1, 16, 2, 128), (120, 6, 8, 2, 128), (100, 5, 16, 2, 128), (120, 3, 8, 2, 64), (60, 16, 16, 4, 64)])
+@pytest.mark.parametrize("fresh", [False, True])
+def test_attend_wait_that_runs_out_with_few_rows(B, N, Hq, Hkv, D, fresh):
+    _stalled(B, B, N, Hq, Hkv, D, fresh, (0, 1, 200, 303))
