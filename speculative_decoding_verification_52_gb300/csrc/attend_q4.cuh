@@ -401,9 +401,12 @@ __device__ __forceinline__ void at_load_q(const AttendArgs& a, int b, int h, int
     // (the factor is above zero, so that products compare as scores do: the
     // scale's sign goes into the operand, and no scale at all becomes a tiny one)
     const float mul = copysignf(__uint_as_float(static_cast<uint32_t>(127 + sh) << 23), a.scale_log2);
-    // a row with a NaN or an infinity has no finite scores: the factor says so
-    const float f = top < __builtin_huge_valf()
-                        ? fmaxf(fabsf(a.scale_log2) * a.k_mul * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23), 1.17549435e-38f)
+    // A row with a NaN has no other scores, and the factor says so.  (An infinity makes
+    // infinite ones of either sign, whatever the finite elements have become.)  A finite
+    // factor leaves a score of 0 what it is.
+    const float f = top <= __builtin_huge_valf()
+                        ? fminf(fmaxf(fabsf(a.scale_log2) * a.k_mul * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23), 1.17549435e-38f),
+                                3.402823466e+38f)
                         : __int_as_float(0x7fc00000);
     c[j][0] = __shfl_sync(0xffffffffu, f, 8 * t);
     c[j][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);

@@ -504,10 +504,13 @@ __device__ __noinline__ void tc_load_q(const uint16_t* from, int G, uint32_t by_
   lo = fminf(fminf(bar->qmin[0], bar->qmin[1]), fminf(bar->qmin[2], bar->qmin[3]));
   const float common = hi < __builtin_huge_valf() && hi > 0.f && hi <= lo * 256.f ? hi : 0.f;
   // in place, times the power of two that takes the largest to [128, 256); the
-  // factor is what takes the products back, with the scale
+  // factor is what takes the products back, with the scale (finite, so that a score of 0
+  // stays one)
   auto power = [](float top) { return top > 0.f ? min(7 - (static_cast<int>(__float_as_uint(top) >> 23) - 127), 100) : 0; };
   auto mult = [&](int e) { return copysignf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23), scale_log2); };
-  auto back = [&](int e) { return fmaxf(fabsf(scale_log2) * k_mul * __uint_as_float(static_cast<uint32_t>(127 - e) << 23), 1.17549435e-38f); };
+  auto back = [&](int e) {
+    return fminf(fmaxf(fabsf(scale_log2) * k_mul * __uint_as_float(static_cast<uint32_t>(127 - e) << 23), 1.17549435e-38f), 3.402823466e+38f);
+  };
   float mul = mult(power(common)), f = back(power(common));
   if (tid == 0) bar->common[fb] = common > 0.f ? f : 0.f;
 #pragma unroll 1
@@ -516,7 +519,7 @@ __device__ __noinline__ void tc_load_q(const uint16_t* from, int G, uint32_t by_
       const float top = factor[r];
       __syncwarp();   // (the threads of a row are in one warp)
       mul = mult(power(top));
-      f = top < __builtin_huge_valf() ? back(power(top)) : __int_as_float(0x7fc00000);
+      f = top <= __builtin_huge_valf() ? back(power(top)) : __int_as_float(0x7fc00000);   // (a NaN has no other scores, an infinity has)
     }
 #pragma unroll
     for (int i = 0; i < W; ++i) {

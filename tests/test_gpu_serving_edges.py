@@ -115,3 +115,30 @@ def test_attend_wait_that_runs_out_with_many_rows(B, N, Hq, Hkv, D, fresh):
 @pytest.mark.parametrize("fresh", [False, True])
 def test_attend_wait_that_runs_out_with_few_rows(B, N, Hq, Hkv, D, fresh):
     _stalled(B, B, N, Hq, Hkv, D, fresh, (0, 1, 200, 303))
+
+
+@pytest.mark.parametrize("N,Hq,Hkv,D", ROWS)
+@pytest.mark.parametrize("length", [0, 70])
+def test_attend_queries_with_infinities(N, Hq, Hkv, D, length):
+    """A query with an infinity has scores of -inf and +inf: all -inf is no weight at
+    all, one +inf is NaN."""
+    c = _case(74 + N, 2, N, Hq, Hkv, D, 32, [length, length], shifts=(0, 0))
+    blk = c["cache"]
+    blk[..., 5 // 2: 16 * D: D // 2] = (blk[..., 5 // 2: 16 * D: D // 2] & 0x0f) | 0x20   # element 5 of every key: +1 (times its scale)
+    c["k"][..., 5] = 1.0
+    exp = [x.copy() for x in _expect(c)]
+    c["q"][0, N - 1, 0, 5], c["q"][1, N - 1, Hq - 1, 5] = float("-inf"), float("inf")
+    sc = ref.q4_split(blk, D)[2].astype(int)
+    assert (sc[..., 0] > 0).all()
+    exp[0][0, N - 1, 0], exp[1][0, N - 1, 0] = 0, -np.inf
+    exp[0][1, N - 1, Hq - 1], exp[1][1, N - 1, Hq - 1] = np.nan, np.nan
+    _close(_attend(c), exp, D)
+
+
+@pytest.mark.parametrize("N", [1, 20, 64])
+def test_attend_largest_queries_against_keys_of_zero(N):
+    """Keys of zero score 0 whatever the queries and the shift."""
+    q = torch.full((1, N, 4, 128), 2.0 ** 126, dtype=torch.bfloat16, device=DEV)
+    out, lse = sv.spec_attend_q4(q, sv.q4_cache(2, 1, 32, 128, DEV), i32([[0, 1]]), i32([40]), k_shift=32)
+    assert not out.any()
+    np.testing.assert_allclose(f64(lse), np.log(40.0), rtol=0, atol=2.0 ** -20 * 5)
