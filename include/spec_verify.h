@@ -421,8 +421,10 @@ size_t spec_attend_workspace_bytes(int B, int N, int Hq, int Hkv, int D);
  * values that a row's mask rules out do not reach it, whatever they hold.  A
  * sequence whose length is negative or passes its table, or a needed page id
  * outside the cache, gives NaN in all its rows that need it, as does an
- * internal wait that hit its time limit.  q, k_new, v_new, out, cache and the
- * workspace must be 16-byte aligned.
+ * internal wait that hit its time limit.  Scores and the sums of weighted values
+ * are fp32, the latter in units of 2^v_shift and of weights of up to 2^15: beyond
+ * fp32's range they are infinities.  q, k_new, v_new, out, cache and the workspace
+ * must be 16-byte aligned.
  * Limits: 1 <= N <= 1024, B <= 4096, Hq a multiple of Hkv, Hq / Hkv <= 64,
  * num_pages * page_tokens and max_pages * page_tokens below 2^31. */
 spec_status_t spec_attend_q4(const void *q, const void *k_new, const void *v_new, const uint32_t *masks,

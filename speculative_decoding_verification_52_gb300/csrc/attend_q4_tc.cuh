@@ -40,11 +40,11 @@
 // 64 sequences of 128 rows at 2,048 tokens take 248 us, where the products at the
 // rate of a large library product would take 37.
 //
-// Fresh entries are converted to f16 in units of the cache's shifts (exact from
-// 2^-14 to 65504 of them, an absolute 2^-25 below, where the cache itself resolves
-// 2^-10).  A tile with an entry beyond that range, or with a NaN or an infinity, is
-// rare: its scores are computed on the CUDA cores, and its entries out of range
-// are added to O^T one by one, for the rows that see them.
+// The fresh entries are bf16 with bf16's range, and so are their products: the queries
+// stay as they are until a triple's first cached tile, keys and values go to their
+// buffers unchanged, and each weight is the sum of two bf16, in the two buffers of P.
+// A value that is a NaN or an infinity (rare) is left out of the product, which takes
+// 0 * inf for NaN, and added to O^T afterwards for the rows that see it.
 #pragma once
 
 #include <cuda.h>
@@ -81,8 +81,8 @@ struct TcLayout {
   static constexpr uint32_t shift = factor + 2 * NC * 4;      // [NC]: 7 - reference (TC_UNSET: none yet)
   static constexpr uint32_t corr = shift + NC * 4;             // [NC]
   static constexpr uint32_t top = corr + NC * 4;               // [4][NC]: maxima or sums of the four warps
-  static constexpr uint32_t seen = top + 4 * NC * 4;           // [4][NC]: mask words
-  static constexpr uint32_t rows = seen + 4 * NC * 4;          // [NC] 8 bytes: the rows' places in the output
+  static constexpr uint32_t fresh = top + 4 * NC * 4;          // [4][NC]: sums of the fresh tiles' weights, of the four warps
+  static constexpr uint32_t rows = fresh + 4 * NC * 4;         // [NC] 8 bytes: the rows' places in the output
   static constexpr uint32_t bars = rows + NC * 8;
   static constexpr uint32_t bytes = bars + 384;
   // tensor memory columns
@@ -91,7 +91,7 @@ struct TcLayout {
   static constexpr uint32_t t_cols = t_need <= 256 ? 256 : 512;
 };
 // A CTA's part of the workspace: two partials as in attend_q4.cuh, then the
-// weights of one tile (for fresh entries out of range)
+// weights of one tile (for fresh values that are no numbers)
 __host__ __device__ constexpr size_t tc_cta_floats(int D, int NC) {
   return 2 * static_cast<size_t>(NC) * (D + 4) + static_cast<size_t>(128) * NC;
 }
@@ -103,9 +103,17 @@ struct TcBars {
   int dead;       // a wait ran out of time
   float common[2]; // the factor of all rows of a triple, 0: they differ
   float qmax[4], qmin[4];
-  int wide[2];    // 1 + the last tile of the buffer that has fresh entries out of range
+  int wide[2];    // 1 + the last tile of the buffer that has fresh values that are no numbers
   int arrived[4]; // the stage's tile came (its page ids are in range)
   int copied;     // tiles whose copies were started, once the copying warp has ended
+  // arguments that functions out of line read
+  const uint32_t* masks;
+  unsigned long long limit;
+  uint16_t* out;
+  float* lse;
+  int N, G, Hq, NW, rows;
+  uint32_t by_g;
+  float scale_log2, k_mul, v_mul;
 };
 static_assert(sizeof(TcBars) <= 384, "barriers");
 
@@ -124,9 +132,9 @@ __device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lbo, uint32_
   return static_cast<uint64_t>((addr & 0x3ffffu) >> 4) | (static_cast<uint64_t>(lbo >> 4) << 16) |
          (static_cast<uint64_t>(sbo >> 4) << 32) | (1ull << 46);
 }
-// f16 operands, fp32 result, M = 128; A and B with their M or N direction contiguous where asked
-__host__ __device__ constexpr uint32_t tc_idesc(int n, bool a_mn, bool b_mn) {
-  return (1u << 4) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
+// f16 or bf16 operands, fp32 result, M = 128; A and B with their M or N direction contiguous where asked
+__host__ __device__ constexpr uint32_t tc_idesc(int n, bool bf16, bool a_mn, bool b_mn) {
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (8u << 24);
 }
 __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
   asm volatile(
@@ -339,25 +347,15 @@ __device__ __forceinline__ void tc_widen(uint32_t w0, uint32_t w1, uint32_t s2, 
 }
 // scale byte g of a word as an f16 pair of equals
 __device__ __forceinline__ uint32_t tc_scale(uint32_t sc, int g) { return e4m3x2_to_f16(__byte_perm(sc, 0u, g * 0x11)); }
-// eight f16 pairs of a fresh entry's 16 elements, in units of 1 / mul
-__device__ __forceinline__ void tc_narrow(const uint4& x, const uint4& y, float mul, uint32_t* r) {
-  const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) r[i] = f16x2_pack(__uint_as_float(w[i] << 16) * mul, __uint_as_float(w[i] & 0xffff0000u) * mul);
-}
-// the largest of |m| and the elements (NaN if there is one)
+// the largest of |m| and the elements (above infinity if there is a NaN)
 __device__ __forceinline__ uint32_t tc_most(uint32_t m, const uint4& x) {
   return bf16x2_max_nan(m, bf16x2_max_nan(bf16x2_max_nan(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), bf16x2_max_nan(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
 }
-__device__ __forceinline__ bool tc_fits(uint32_t most, float mul) {
-  return fmax_nan(__uint_as_float(most << 16), __uint_as_float(most & 0xffff0000u)) * mul <= 65504.f;
-}
-// 0 for the elements that do not fit
-__device__ __noinline__ void tc_drop(uint4* x, int n, float mul) {
-  uint16_t* e = reinterpret_cast<uint16_t*>(x);
-#pragma unroll 1
-  for (int i = 0; i < 8 * n; ++i)
-    if (!tc_fits(e[i] & 0x7fffu, mul)) e[i] = 0u;
+// 0 for the elements that are no numbers
+__device__ __forceinline__ uint32_t tc_numbers(uint32_t two) {
+  if ((two & 0x7f80u) == 0x7f80u) two &= 0xffff0000u;
+  if ((two & 0x7f800000u) == 0x7f800000u) two &= 0xffffu;
+  return two;
 }
 
 // a row of D elements to the L2 cache
@@ -389,75 +387,58 @@ __device__ __forceinline__ void tc_fresh_copy(const uint16_t* from, int stride, 
 }
 
 // A fresh tile's keys into tensor memory, a thread a node, its lane; they pass
-// through the values' buffer.  True when an element does not fit (the tile's scores
-// then are not taken from here).
+// through the values' buffer.
 template <int D>
-__device__ __noinline__ bool tc_fresh_key(const uint16_t* from, int stride, int left, float k_mul, uint32_t k_at, unsigned char* vbuf) {
-  const float mul = __fdiv_rn(1.f, k_mul);
-  unsigned char* mine = vbuf + (threadIdx.x & 127) * 16;
+__device__ __noinline__ void tc_fresh_key(const uint16_t* from, int stride, int left, uint32_t k_at, unsigned char* vbuf) {
+  const unsigned char* mine = vbuf + (threadIdx.x & 127) * 16;
   tc_fresh_copy<D>(from, stride, left, vbuf, 6);
-  uint32_t most = 0u;
 #pragma unroll 1
   for (int c = 0; c < D / 32; ++c) {
-    uint4 x[4];
+    uint32_t r[16];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      x[i] = *reinterpret_cast<const uint4*>(mine + (4 * c + i) * 2048);
-      most = tc_most(most, x[i]);
+      const uint4 x = *reinterpret_cast<const uint4*>(mine + (4 * c + i) * 2048);
+      r[4 * i] = x.x;
+      r[4 * i + 1] = x.y;
+      r[4 * i + 2] = x.z;
+      r[4 * i + 3] = x.w;
     }
-    uint32_t r[16];
-    tc_narrow(x[0], x[1], mul, r);
-    tc_narrow(x[2], x[3], mul, r + 8);
     __syncwarp();
     tc_st16(k_at + c * 16, r);
   }
-  return !tc_fits(most, mul);
 }
-// Its values, in place; 0 for what does not fit.  id: the threads' barrier.
+// Its values, in place; 0 for what is no number, and true if there is any.  id: the
+// threads' barrier.
 template <int D>
-__device__ __noinline__ bool tc_fresh_value(const uint16_t* from, int stride, int left, float v_mul, unsigned char* vbuf, int id) {
-  const float mul = __fdiv_rn(1.f, v_mul);
+__device__ __noinline__ bool tc_fresh_value(const uint16_t* from, int stride, int left, unsigned char* vbuf, int id) {
   unsigned char* mine = vbuf + (threadIdx.x & 127) * 16;
   tc_fresh_copy<D>(from, stride, left, vbuf, id);
-  uint32_t all = 0u;
-#pragma unroll 2
-  for (int j = 0; j < D / 8; j += 2) {
-    uint4* at[2] = {reinterpret_cast<uint4*>(mine + j * 2048), reinterpret_cast<uint4*>(mine + (j + 1) * 2048)};
-    uint4 x[2] = {*at[0], *at[1]};
-    const uint32_t most = tc_most(tc_most(0u, x[0]), x[1]);
-    all = bf16x2_max_nan(all, most);
-    if (TC_RARE(!tc_fits(most, mul))) {
-      uint4 y[2] = {x[0], x[1]};
-      tc_drop(y, 2, mul);
-      x[0] = y[0];
-      x[1] = y[1];
-    }
-    uint32_t r[8];
-    tc_narrow(x[0], x[1], mul, r);
-    *at[0] = make_uint4(r[0], r[1], r[2], r[3]);
-    *at[1] = make_uint4(r[4], r[5], r[6], r[7]);
+  uint32_t most = 0u;
+#pragma unroll 4
+  for (int j = 0; j < D / 8; ++j) most = tc_most(most, *reinterpret_cast<const uint4*>(mine + j * 2048));
+  if (!bf16x2_unbounded(most)) return false;
+#pragma unroll 1
+  for (int j = 0; j < D / 8; ++j) {
+    uint4* at = reinterpret_cast<uint4*>(mine + j * 2048);
+    const uint4 x = *at;
+    *at = make_uint4(tc_numbers(x.x), tc_numbers(x.y), tc_numbers(x.z), tc_numbers(x.w));
   }
-  return !tc_fits(all, mul);
+  return true;
 }
 
-// Queries of a row tile (128 threads; from: the first row's of the kv head).  Usually one power of two scales all rows,
-// so that the largest element lies in [128, 256); where the rows' largest elements
-// lie more than 2^8 apart, each row gets its own (an element is off by 2^-25 at
-// most: 2^-24 of its row's largest with one power of two, 2^-32 with its own).
-// (What runs once a triple is short loops: its code has left the instruction
-// caches by then, and a line of it takes as long to fetch as ten hot instructions
-// an instruction.  Unrolled, this function took 15,000 clocks.)
+// Queries of a row tile (128 threads; from: the first row's of the kv head), as they
+// are, by asynchronous copies.
 template <int D, int NC>
-__device__ __noinline__ void tc_load_q(const uint16_t* from, int G, uint32_t by_g, int Hq, float scale_log2, float k_mul, int row0, int rows, int qb,
-                                       int fb, unsigned char* smem, TcBars* bar) {
+__device__ __noinline__ void tc_copy_q(const uint16_t* from, int row0, int qb, unsigned char* smem) {
   using L = TcLayout<D, NC>;
+  const TcBars* bar = reinterpret_cast<const TcBars*>(smem + L::bars);
+  const int G = bar->G, Hq = bar->Hq, rows = bar->rows;
+  const uint32_t by_g = bar->by_g;
   // Four threads of a warp have a row, eight lanes eight rows (so that they access
   // different banks); a thread has W columns of core matrices.
   constexpr int W = D / 32;
-  const int tid = threadIdx.x - 32 * L::SOFT, part = (tid >> 3) & 3, quad = tid >> 5, r0 = 8 * quad + (tid & 7);
+  const int tid = threadIdx.x - 32 * L::SOFT, part = (tid >> 3) & 3, r0 = 8 * (tid >> 5) + (tid & 7);
   unsigned char* to = smem + L::q + qb * L::q_bytes + W * part * (NC * 16);
-  float* factor = reinterpret_cast<float*>(smem + L::factor) + fb * NC;
-  // as they are
 #pragma unroll 1
   for (int r = r0; r < NC; r += 32) {
     const bool there = row0 + r < rows;
@@ -469,6 +450,24 @@ __device__ __noinline__ void tc_load_q(const uint16_t* from, int G, uint32_t by_
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(at + i * (NC * 16)), "l"(p + 8 * i), "r"(there ? 16 : 0) : "memory");
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// The same, made f16 in place (each thread what it copied).  Usually one power of two
+// scales all rows, so that the largest element lies in [128, 256); where the rows'
+// largest elements lie more than 2^8 apart, each row gets its own (an element is off by 2^-25 at
+// most: 2^-24 of its row's largest with one power of two, 2^-32 with its own).
+// (What runs once a triple is short loops: its code has left the instruction
+// caches by then, and a line of it takes as long to fetch as ten hot instructions
+// an instruction.  Unrolled, this function took 15,000 clocks.)
+template <int D, int NC>
+__device__ __noinline__ void tc_scale_q(int qb, int fb, unsigned char* smem) {
+  using L = TcLayout<D, NC>;
+  TcBars* bar = reinterpret_cast<TcBars*>(smem + L::bars);
+  const float scale_log2 = bar->scale_log2, k_mul = bar->k_mul;
+  constexpr int W = D / 32;
+  const int tid = threadIdx.x - 32 * L::SOFT, part = (tid >> 3) & 3, quad = tid >> 5, r0 = 8 * quad + (tid & 7);
+  unsigned char* to = smem + L::q + qb * L::q_bytes + W * part * (NC * 16);
+  float* factor = reinterpret_cast<float*>(smem + L::factor) + fb * NC;
   // the rows' largest elements, in the factors' place
   float hi = 0.f, lo = __builtin_huge_valf();
   bool odd = false;
@@ -535,28 +534,7 @@ __device__ __noinline__ void tc_load_q(const uint16_t* from, int G, uint32_t by_
   named_bar_sync(6, 128);   // qmax and qmin are free again
 }
 
-// Scores of a tile with fresh entries out of range, on the CUDA cores, into the
-// products' place in tensor memory: this thread's node, the rows from col0.
-template <int D, int NC>
-__device__ __noinline__ void tc_wide_scores(const AttendArgs& args, int b, int h, int row0, int rows, int node, int col0, int cols,
-                                            const float* factor, uint32_t addr) {
-  const AttendArgs a = args;
-  for (int c = 0; c < cols; ++c) {
-    float s = 0.f;
-    const int r = row0 + col0 + c;
-    if (r < rows && node < a.N) {
-      const uint16_t* q = a.q + at_row(a, b, h, r) * D;
-      const uint16_t* k = a.k_new + ((static_cast<long long>(b) * a.N + node) * a.Hkv + h) * D;
-      for (int d = 0; d < D; ++d)
-        s += __uint_as_float(static_cast<uint32_t>(q[d]) << 16) * __uint_as_float(static_cast<uint32_t>(k[d]) << 16);
-      s = s * a.scale_log2 / factor[col0 + c];
-    }
-    __syncwarp();
-    tc_st1(addr + c, s);
-  }
-  tc_wait_st();
-}
-// Adds the fresh values out of range to O^T: this thread's column d, the rows from
+// Adds the fresh values that are no numbers to O^T: this thread's column d, the rows from
 // col0; weights (negative: the row does not see the node) at w[node][NC].
 template <int D, int NC>
 __device__ __noinline__ void tc_wide_values(const AttendArgs& args, int b, int h, int node0, int left, int d, int col0, int cols,
@@ -565,8 +543,8 @@ __device__ __noinline__ void tc_wide_values(const AttendArgs& args, int b, int h
   for (int j = 0; j < left; ++j) {
     float v = 0.f;
     if (d < D)
-      v = __uint_as_float(static_cast<uint32_t>(a.v_new[((static_cast<long long>(b) * a.N + node0 + j) * a.Hkv + h) * D + d]) << 16) / a.v_mul;
-    const bool odd = !(fabsf(v) <= 65504.f);
+      v = __uint_as_float(static_cast<uint32_t>(a.v_new[((static_cast<long long>(b) * a.N + node0 + j) * a.Hkv + h) * D + d]) << 16);
+    const bool odd = !(fabsf(v) < __builtin_huge_valf());
     if (!__any_sync(0xffffffffu, odd)) continue;
     for (int c = 0; c < cols; ++c) {
       const float p = __ldcg(w + j * NC + col0 + c);
@@ -596,28 +574,24 @@ __device__ __forceinline__ float tc_top(float (&x)[32]) {
   return x[0];
 }
 
-// bits of the rows of a part that do not see this thread's node: those without its
-// bit in the warp's words (a tree), or those before row `open` (a chain)
-__device__ __noinline__ uint32_t tc_hidden(bool tree, const uint32_t* seen, int open) {
-  if (!tree) return open <= 0 ? 0u : open >= 32 ? ~0u : (1u << open) - 1u;
-  uint32_t hide = 0u;
-#pragma unroll 1
-  for (int i = 0; i < TC_PART; ++i) hide |= (~(seen[i] >> (threadIdx.x & 31)) & 1u) << i;
-  return hide;
-}
-
 // New references for a part's rows: the 128 threads of a part call this together.
 // s_at: the tile's products (hide: bits of rows that do not see this thread's
-// token), o_at: the rows' sums of v so far, if there are any.
-template <int NC>
-__device__ __noinline__ void tc_raise(uint32_t s_at, uint32_t o_at, const float* factor, float* shift, float* corr, float* top,
-                                      uint32_t hide, bool sums, int quad, int id) {
-  const int lane = threadIdx.x & 31;
+// token), o_at: the rows' sums of v so far, if there are any.  factor: of each row, or
+// null: the scale is.
+template <int D, int NC>
+__device__ __noinline__ void tc_raise(unsigned char* smem, uint32_t s_at, uint32_t o_at, const float* factor, uint32_t hide, bool sums) {
+  using L = TcLayout<D, NC>;
+  const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, col0 = (threadIdx.x >> 7) * TC_PART, id = 1 + (threadIdx.x >> 7);
+  float* shift = reinterpret_cast<float*>(smem + L::shift) + col0;
+  float* corr = reinterpret_cast<float*>(smem + L::corr) + col0;
+  float* top = reinterpret_cast<float*>(smem + L::top) + col0;
+  float* fresh = reinterpret_cast<float*>(smem + L::fresh) + col0;
+  const float all = reinterpret_cast<const TcBars*>(smem + L::bars)->scale_log2;
   float z[TC_PART];
   tc_ld<TC_PART>(s_at, z);
 #pragma unroll
   for (int i = 0; i < TC_PART; i += 4) {
-    const float4 x = *reinterpret_cast<const float4*>(factor + i);
+    const float4 x = factor ? *reinterpret_cast<const float4*>(factor + i) : make_float4(all, all, all, all);
     const float f[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k) z[i + k] = (hide >> (i + k)) & 1u ? kNegInf : fmaxf(z[i + k] * f[k], kNegInf);   // (no NaN)
@@ -634,6 +608,7 @@ __device__ __noinline__ void tc_raise(uint32_t s_at, uint32_t o_at, const float*
   }
   named_bar_sync(id, 128);
   if (sums) {
+    fresh[quad * NC + lane] *= corr[lane];
     tc_fence_after();
 #pragma unroll 1
     for (int i = 0; i < TC_PART; i += 8) {
@@ -645,6 +620,122 @@ __device__ __noinline__ void tc_raise(uint32_t s_at, uint32_t o_at, const float*
     }
     tc_wait_st();
   }
+}
+
+// The sum of column lane / 4 of 8 over the lanes of a warp.
+__device__ __forceinline__ float tc_total(const float (&x)[8]) {
+  const int lane = threadIdx.x & 31;
+  float y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool up = lane & 16;
+    y[i] = (up ? x[i + 4] : x[i]) + __shfl_xor_sync(0xffffffffu, up ? x[i] : x[i + 4], 16);
+  }
+#pragma unroll
+  for (int o = 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const bool up = lane & (4 * o);
+      const float give = up ? y[i] : y[i + o];
+      y[i] = (up ? y[i + o] : y[i]) + __shfl_xor_sync(0xffffffffu, give, 4 * o);
+    }
+  y[0] += __shfl_xor_sync(0xffffffffu, y[0], 2);
+  return y[0] + __shfl_xor_sync(0xffffffffu, y[0], 1);
+}
+
+// The softmax of a tile without cached tokens: of fresh entries of sequence b, or of
+// nothing (n: the tile's number).  Called by the 128 threads of a part together.  True
+// (for all of them alike) when the tile has values that are no numbers, whose weights
+// then are in wide_w.  (It takes few arguments and keeps no array that is addressed:
+// local memory, for which the shared memory in use leaves next to no cache, made a tile
+// 10,000 clocks longer.)
+template <int D, int NC>
+__device__ __noinline__ bool tc_fresh_softmax(unsigned char* smem, bool of_fresh, int b, int row0, int at, int left, bool first, int n, uint32_t s_at,
+                                              uint32_t o_at, float* wide_w) {
+  using L = TcLayout<D, NC>;
+  TcBars* bar = reinterpret_cast<TcBars*>(smem + L::bars);
+  const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, part = threadIdx.x >> 7, col0 = part * TC_PART, id = 1 + part;
+  const int tok = 32 * quad + lane, x = n & 1;
+  float* shift = reinterpret_cast<float*>(smem + L::shift) + col0;
+  float* fresh = reinterpret_cast<float*>(smem + L::fresh) + col0;
+  // which of the part's rows do not see this thread's node
+  uint32_t hide = 0u;
+  if (of_fresh) {
+    const int open = (at + tok) * bar->G - row0 - col0;   // a chain: the node's first row
+    hide = open <= 0 ? 0u : open >= 32 ? ~0u : (1u << open) - 1u;
+    if (bar->masks) {   // a tree: the warp's 32 nodes are one word of each row's mask, a row a lane
+      const int r = row0 + col0 + lane, N = bar->N;
+      uint32_t w = 0u;
+      if (r < bar->rows && at + 32 * quad < N) w = __ldg(bar->masks + (static_cast<long long>(b) * N + r / bar->G) * bar->NW + at / 32 + quad);
+      hide = 0u;
+#pragma unroll 4
+      for (int i = 0; i < TC_PART; ++i) hide |= (~(__shfl_sync(0xffffffffu, w, i) >> lane) & 1u) << i;
+    }
+  }
+  if (tok >= left) hide = ~0u;
+  const unsigned long long limit = bar->limit;
+  const float scale = bar->scale_log2;
+  tc_wait(&bar->sready[x], (n >> 1) & 1, bar, limit);
+  tc_fence_after();
+  // Eight rows' scores against their references (the products are rounded as those were).
+  auto scores = [&](int i, float (&y)[8]) {
+    __syncwarp();
+    tc_ld<8>(s_at + i, y);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y[k] = (hide >> (i + k)) & 1u ? kNegInf : __fadd_rn(__fmul_rn(y[k], scale), shift[i + k]);
+  };
+  float m = 0.f;
+#pragma unroll 1
+  for (int i = 0; i < TC_PART; i += 8) {
+    float y[8];
+    scores(i, y);
+#pragma unroll
+    for (int k = 0; k < 8; k += 2) m = fmax3_nan(m, y[k], y[k + 1]);
+  }
+  if (tc_any<128>(id, !(m <= AT_PSHIFT + AT_ABOVE))) {
+    if (!first) tc_wait(&bar->pvdone[x ^ 1], ((n - 1) >> 1) & 1, bar, limit);
+    tc_raise<D, NC>(smem, s_at, o_at, nullptr, hide, !first);
+  }
+  // (one answer for the part, whatever the flag does once a wait has failed)
+  tc_wait(&bar->vready[x], (n >> 1) & 1, bar, limit);
+  const bool wide = tc_any<128>(id, *reinterpret_cast<volatile int*>(&bar->wide[x]) == n + 1);
+  // Each weight as the sum of two bf16, in the two buffers, in units of the sums of v; for
+  // values that are no numbers as it is, or -1 where the row does not see the node.
+  if (n >= 2) tc_wait(&bar->pvdone[x], ((n >> 1) & 1) ^ 1, bar, limit);
+  if (n >= 1) tc_wait(&bar->pvdone[x ^ 1], ((n - 1) >> 1) & 1, bar, limit);
+  unsigned char* hi = smem + L::p + x * L::p_bytes + tok * 16 + col0 / 8 * 2048;
+  unsigned char* lo = smem + L::p + (x ^ 1) * L::p_bytes + tok * 16 + col0 / 8 * 2048;
+  const float unit = __fdiv_rn(1.f, bar->v_mul);
+#pragma unroll 1
+  for (int i = 0; i < TC_PART; i += 8) {
+    float y[8];
+    scores(i, y);
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      y[k] = ex2_approx(y[k]);
+      if (wide) __stcg(wide_w + static_cast<size_t>(tok) * NC + col0 + i + k, (hide >> (i + k)) & 1u ? -1.f : y[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float p0 = y[2 * k] * unit, p1 = y[2 * k + 1] * unit;
+      h[k] = bf16x2_pack(p0, p1);
+      l[k] = bf16x2_pack(p0 - __uint_as_float(h[k] << 16), p1 - __uint_as_float(h[k] & 0xffff0000u));
+    }
+    *reinterpret_cast<uint4*>(hi + i / 8 * 2048) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(lo + i / 8 * 2048) = make_uint4(l[0], l[1], l[2], l[3]);
+    const float total = tc_total(y);
+    float* at = fresh + quad * NC + i + (lane >> 2);
+    if ((lane & 3) == 0) *at = (first ? 0.f : *at) + total;
+  }
+  tc_fence_before();
+  tc_proxy_fence();
+  __syncwarp();
+  if (lane == 0) {
+    mbar_arrive(&bar->sfree[x]);   // the scores have been read
+    mbar_arrive(&bar->pready[x]);
+  }
+  return wide;
 }
 
 // Where the 128 threads of a part of the rows leave their sums of weights of row c,
@@ -660,10 +751,18 @@ __device__ __forceinline__ float* tc_sums(const unsigned char* p, int c) {
 // tokens' threads, then O^T row by row, as the result or (not
 // whole) as a partial.
 template <int D, int NC>
-__device__ __noinline__ void tc_finish(uint16_t* out, float* lse, long long base, int G, uint32_t by_g, int Hq, float v_mul, int row0, int rows,
-                                       bool whole, float* partial, const unsigned char* p, const float* shift, float* corr, float* top,
-                                       long long* place, uint32_t o_at, int part) {
-  const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, col0 = part * TC_PART, id = 1 + part, d = 32 * quad + lane;
+__device__ __noinline__ void tc_finish(unsigned char* smem, long long base, int row0, bool whole, float* partial, uint32_t o_at) {
+  using L = TcLayout<D, NC>;
+  const TcBars* bar = reinterpret_cast<const TcBars*>(smem + L::bars);
+  const int lane = threadIdx.x & 31, quad = (threadIdx.x >> 5) & 3, part = threadIdx.x >> 7, col0 = part * TC_PART, id = 1 + part, d = 32 * quad + lane;
+  const int rows = bar->rows;
+  uint16_t* out = bar->out;
+  const unsigned char* p = smem + L::p + col0 / 8 * 2048;
+  const float* shift = reinterpret_cast<const float*>(smem + L::shift) + col0;
+  const float* fresh = reinterpret_cast<const float*>(smem + L::fresh) + col0;
+  float* corr = reinterpret_cast<float*>(smem + L::corr) + col0;
+  float* top = reinterpret_cast<float*>(smem + L::top) + col0;
+  long long* place = reinterpret_cast<long long*>(smem + L::rows) + col0;
   tc_fence_after();
   named_bar_sync(id, 128);
   // a warp adds up its 32 tokens of the part's rows, a row a lane, rotated so that
@@ -675,19 +774,20 @@ __device__ __noinline__ void tc_finish(uint16_t* out, float* lse, long long base
     for (int t = 0; t < 32; t += 4)
 #pragma unroll
       for (int k = 0; k < 4; ++k) x[k] += from[(t + k + lane) & 31];
-    top[quad * NC + lane] = (x[0] + x[1]) + (x[2] + x[3]);
+    top[quad * NC + lane] = ((x[0] + x[1]) + (x[2] + x[3])) + fresh[quad * NC + lane];
   }
   named_bar_sync(id, 128);
   if (quad == 0) {
-    const int i = lane;
+    const int i = lane, G = bar->G;
+    const uint32_t by_g = bar->by_g;
     const int x = min(row0 + col0 + i, rows - 1), node = by_g ? static_cast<int>(__umulhi(static_cast<uint32_t>(x), by_g)) : x;
-    place[i] = (base + static_cast<long long>(node) * Hq + (x - node * G)) * D;
+    place[i] = (base + static_cast<long long>(node) * bar->Hq + (x - node * G)) * D;
     const float sum = (top[i] + top[NC + i]) + (top[2 * NC + i] + top[3 * NC + i]);
     const int r = row0 + col0 + i;
     const float ref = -shift[i];
-    corr[i] = sum == 0.f ? 0.f : v_mul / sum;
+    corr[i] = sum == 0.f ? 0.f : bar->v_mul / sum;
     if (whole) {
-      if (r < rows && lse) lse[place[i] / D] = at_lse(ref, sum);
+      if (r < rows && bar->lse) bar->lse[place[i] / D] = at_lse(ref, sum);
     } else {
       float* ml = partial + static_cast<size_t>(NC) * D + col0 + i;
       ml[0] = ref;
@@ -751,6 +851,19 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
     }
     mbar_init(&bar->drain, 1);
     bar->dead = bar->copied = 0;
+    bar->masks = a.masks;
+    bar->limit = a.timeout_ns;
+    bar->N = a.N;
+    bar->G = a.G;
+    bar->NW = a.NW;
+    bar->rows = a.N * a.G;
+    bar->scale_log2 = a.scale_log2;
+    bar->v_mul = a.v_mul;
+    bar->k_mul = a.k_mul;
+    bar->by_g = a.by_g;
+    bar->Hq = a.Hkv * a.G;
+    bar->out = a.out;
+    bar->lse = a.lse;
     mbar_fence_init();
   }
   at_prefix<L::THREADS>(a, prefix, scratch);   // (synchronises the CTA)
@@ -770,7 +883,7 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bar->tmem;
-    float* cta_ws = a.ws + static_cast<size_t>(blockIdx.x) * tc_cta_floats(D, NC);
+  float* cta_ws = a.ws + static_cast<size_t>(blockIdx.x) * tc_cta_floats(D, NC);
 
   if (warp == L::SOFT + L::UNPACK + 1) {
     // ---- copies: up to four blocks a tile, a lane each --------------------------------
@@ -833,30 +946,39 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
   } else if (warp == L::SOFT + L::UNPACK) {
     // ---- products: one thread ------------------------------------------------------------
     if (lane == 0) {
-      constexpr uint32_t id_s = tc_idesc(NC, false, false), id_o = tc_idesc(NC, true, true);
+      constexpr uint32_t id_s = tc_idesc(NC, false, false, false), id_o = tc_idesc(NC, false, true, true);
+      constexpr uint32_t id_sb = tc_idesc(NC, true, false, false), id_ob = tc_idesc(NC, true, true, true);
       TcTile t;
       tc_begin<NC>(a, prefix, HR, nfresh, u0, ntiles, t);
-      bool pfirst = false;              // the tile before: was it a triple's first
+      bool pfirst = false, pfresh = false;   // the tile before: was it a triple's first, one of fresh entries
       int n = 0, tri = 0, ptri = 0;     // tiles, triples so far; the tile before's triple
-      auto add_v = [&](int m, bool first, int tr) {   // O^T += V^T P^T of tile m
+      uint32_t qphase = 0u;             // a bit per buffer of the queries
+      auto add_v = [&](int m, bool first, bool fresh, int tr) {   // O^T += V^T P^T of tile m
         const int x = m & 1;
         if (!tc_wait_one(&bar->pready[x], (m >> 1) & 1, bar, a.timeout_ns) || !tc_wait_one(&bar->vready[x], (m >> 1) & 1, bar, a.timeout_ns)) return false;
         const int ob = tr % L::QB;
         if (first && tr >= L::QB && !tc_wait_one(&bar->ofree[(tr - L::QB) & 1], ((tr - L::QB) >> 1) & 1, bar, a.timeout_ns)) return false;
         tc_fence_after();
         const uint64_t vd = tc_desc(sbase + L::v + x * TC_VBUF, 128, 2048), pd = tc_desc(sbase + L::p + x * L::p_bytes, 128, 2048);
+        const uint32_t id = fresh ? id_ob : id_o;
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)   // (16 tokens: 256 bytes on)
-          tc_mma_ss(tmem + L::t_o + ob * NC, vd + ks * 16, pd + ks * 16, id_o, !(first && ks == 0));
+          tc_mma_ss(tmem + L::t_o + ob * NC, vd + ks * 16, pd + ks * 16, id, !(first && ks == 0));
+        if (TC_RARE(fresh)) {   // the rest of the weights
+          const uint64_t rd = tc_desc(sbase + L::p + (x ^ 1) * L::p_bytes, 128, 2048);
+#pragma unroll 1
+          for (int ks = 0; ks < 8; ++ks) tc_mma_ss(tmem + L::t_o + ob * NC, vd + ks * 16, rd + ks * 16, id, true);
+        }
         tc_commit(&bar->pvdone[x]);
         return true;
       };
       bool ok = true;
       for (int u = 0;;) {
         const int x = n & 1, qb = tri % L::QB;
-        if (t.first) {   // (the triple before is finished beside the load of the queries)
-          if (n > 0) ok = add_v(n - 1, pfirst, ptri);
-          ok = ok && tc_wait_one(&bar->qready[qb], (tri / L::QB) & 1, bar, a.timeout_ns);
+        if (t.first && n > 0) ok = add_v(n - 1, pfirst, pfresh, ptri);   // (the triple before is finished beside the load of the queries)
+        if (t.first || (t.kind == TC_CACHED && t.at == 0)) {   // the queries, or the queries made f16
+          ok = ok && tc_wait_one(&bar->qready[qb], (qphase >> qb) & 1u, bar, a.timeout_ns);
+          qphase ^= 1u << qb;
         }
         ok = ok && tc_wait_one(&bar->kready[x], (n >> 1) & 1, bar, a.timeout_ns);
         if (ok && n >= 2) ok = tc_wait_one(&bar->sfree[x], ((n >> 1) & 1) ^ 1, bar, a.timeout_ns);
@@ -865,17 +987,18 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
         const uint64_t qd = tc_desc(sbase + L::q + qb * L::q_bytes, NC * 16, 128);
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks)   // (16 elements: two core-matrix columns on)
-          tc_mma_ts(tmem + L::t_s + x * NC, tmem + L::t_k + x * (D / 2) + ks * 8, qd + ks * (2 * NC), id_s, ks > 0);
+          tc_mma_ts(tmem + L::t_s + x * NC, tmem + L::t_k + x * (D / 2) + ks * 8, qd + ks * (2 * NC), t.kind == TC_CACHED ? id_s : id_sb, ks > 0);
         tc_commit(&bar->sready[x]);   // (and K's buffer is free)
         if (t.last) tc_commit(&bar->qfree[qb]);
-        if (n > 0 && !t.first) ok = add_v(n - 1, pfirst, ptri);
+        if (n > 0 && !t.first) ok = add_v(n - 1, pfirst, pfresh, ptri);
         if (!ok) break;
         pfirst = t.first;
+        pfresh = t.kind == TC_FRESH;
         ptri = tri;
         if (t.last) ++tri;
         ++n;
         if ((u += t.step) >= ntiles) {
-          add_v(n - 1, pfirst, ptri);
+          add_v(n - 1, pfirst, pfresh, ptri);
           break;
         }
         tc_step<NC>(a, prefix, HR, nfresh, ntiles - u, t);
@@ -896,18 +1019,25 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
     // do: over what the buffers hold, for results that are void.)
     for (int u = 0;;) {
       const int x = n & 1;
-      if (TC_RARE(t.first)) {
-        if (keys) {
-          const int qb = tri % L::QB;
+      if (TC_RARE(t.first || t.at == 0) && keys) {
+        // A triple's queries are bf16 for its fresh tiles and f16 from its first cached one.
+        const bool cached = t.kind == TC_CACHED;
+        if (t.first) {
           // (the factors have two buffers, which the softmax warps read to the triple's end)
-          if (tri >= L::QB) tc_wait(&bar->qfree[qb], ((tri / L::QB) & 1) ^ 1, bar, a.timeout_ns);
+          if (tri >= L::QB) tc_wait(&bar->qfree[tri % L::QB], ((tri / L::QB) & 1) ^ 1, bar, a.timeout_ns);
           if (tri >= 2) tc_wait(&bar->ofree[tri & 1], ((tri >> 1) & 1) ^ 1, bar, a.timeout_ns);
-          tc_load_q<D, NC>(a.q + at_row(a, t.c.b, t.h, 0) * D, a.G, a.by_g, a.Hkv * a.G, a.scale_log2, a.k_mul, t.row0, rows, qb, tri & 1, tc_smem, bar);
+          tc_copy_q<D, NC>(a.q + at_row(a, t.c.b, t.h, 0) * D, t.row0, tri % L::QB, tc_smem);
+          ++tri;
+        } else if (cached) {   // the products of the tile before have read them
+          tc_wait(&bar->sready[x ^ 1], ((n - 1) >> 1) & 1, bar, a.timeout_ns);
+        }
+        const int qb = (tri - 1) % L::QB;
+        if (cached) tc_scale_q<D, NC>(qb, (tri - 1) & 1, tc_smem);
+        if (cached || t.first) {
           tc_proxy_fence();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bar->qready[qb]);
         }
-        ++tri;
       }
       const int stage = copies % L::STAGES;
       if (t.kind == TC_CACHED) tc_wait(&bar->full[stage], (copies / L::STAGES) & 1, bar, a.timeout_ns);
@@ -931,7 +1061,7 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
         const uint32_t k_at = tmem + lane_at + L::t_k + x * (D / 2);
         if (TC_RARE(t.kind == TC_FRESH)) {
           if (n >= 2) tc_wait(&bar->pvdone[x], ((n >> 1) & 1) ^ 1, bar, a.timeout_ns);
-          if (tc_fresh_key<D>(a.k_new + fresh_at(), a.Hkv * D, t.left, a.k_mul, k_at, tc_smem + L::v + x * TC_VBUF)) *reinterpret_cast<volatile int*>(&bar->wide[x]) = n + 1;
+          tc_fresh_key<D>(a.k_new + fresh_at(), a.Hkv * D, t.left, k_at, tc_smem + L::v + x * TC_VBUF);
         } else {
           uint64_t sc = !mine ? 0ull : good ? scales(32 * D) : 0x7f7f7f7f7f7f7f7full;
 #pragma unroll 1
@@ -957,7 +1087,7 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
         if (n >= 2) tc_wait(&bar->pvdone[x], ((n >> 1) & 1) ^ 1, bar, a.timeout_ns);
         unsigned char* vb = tc_smem + L::v + x * TC_VBUF + tok * 16;
         if (TC_RARE(t.kind == TC_FRESH)) {
-          if (tc_fresh_value<D>(a.v_new + fresh_at(), a.Hkv * D, t.left, a.v_mul, tc_smem + L::v + x * TC_VBUF, L::UNPACK == 4 ? 6 : 7))
+          if (tc_fresh_value<D>(a.v_new + fresh_at(), a.Hkv * D, t.left, tc_smem + L::v + x * TC_VBUF, L::UNPACK == 4 ? 6 : 7))
             *reinterpret_cast<volatile int*>(&bar->wide[x]) = n + 1;
         } else {
           uint64_t sc = mine && good ? scales(34 * D) : 0ull;
@@ -992,8 +1122,6 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
     const uint32_t lane_at = static_cast<uint32_t>(32 * quad) << 16;
     float* shift = reinterpret_cast<float*>(tc_smem + L::shift) + col0;
     float* corr = reinterpret_cast<float*>(tc_smem + L::corr) + col0;
-    float* top = reinterpret_cast<float*>(tc_smem + L::top) + col0;            // [4][NC], the part's columns
-    uint32_t* seen = reinterpret_cast<uint32_t*>(tc_smem + L::seen) + quad * NC + col0;
     // Sums of weights of two neighbouring tokens: an even lane has the first half of
     // the rows, an odd one the second (a sum a row and thread beside the 32 scores
     // would not fit the registers).
@@ -1001,148 +1129,129 @@ __global__ void __launch_bounds__(TcLayout<D, NC>::THREADS, 1) attend_q4_tc_kern
     const bool odd = lane & 1;
     TcTile t;
     tc_begin<NC>(a, prefix, HR, nfresh, u0, ntiles, t);
-    int n = 0, tri = 0;
-    int itri = t.c.i;
-    float common = 0.f;                     // the rows' factor, 0: each its own
-    unsigned long long common2 = 0ull;      // what the packed product takes
-    for (int u = 0;;) {
-      const int x = n & 1, qb = tri % L::QB;
-      const float* factor = reinterpret_cast<const float*>(tc_smem + L::factor) + (tri & 1) * NC + col0;
-      if (TC_RARE(t.first)) {
-        itri = t.c.i;
-#pragma unroll
-        for (int i = 0; i < HC / 2; ++i) l[i] = 0.f;
-        for (int i = threadIdx.x & 127; i < HC; i += 128) shift[i] = TC_UNSET;
-        named_bar_sync(id, 128);
-      }
+    int n = 0, u = 0;
+    for (int tri = 0;; ++tri) {
+      // The part of a triple in the share: first the tiles without cached tokens, then, in a
+      // loop of their own, the cached ones.
       // (A warp whose wait fails goes on in step with the others, which it meets at
       // barriers; every wait then returns at once.)
-      tc_wait(&bar->sready[x], (n >> 1) & 1, bar, a.timeout_ns);
-      tc_fence_after();
-      const uint32_t s_at = tmem + lane_at + L::t_s + x * NC + col0;
-      const uint32_t o_at = tmem + lane_at + L::t_o + qb * NC + col0;
-      if (TC_RARE(t.first)) {
-        common = bar->common[tri & 1];
-        common2 = common == 0.f ? f2_pack(1.f, 1.f) : f2_pack(common, common);
-      }
-      bool wide = false, some = false;
-      int open = 0;   // in a fresh tile of a chain, the node's first row in the part
-      if (TC_RARE(t.kind != TC_CACHED || t.left < TC_TILE)) {
-        some = true;
-        if (t.kind == TC_FRESH) {
-          // (one answer for the part, whatever the flag does once a wait has failed; the
-          // values have been looked at, too)
-          tc_wait(&bar->vready[x], (n >> 1) & 1, bar, a.timeout_ns);
-          wide = tc_any<128>(id, *reinterpret_cast<volatile int*>(&bar->wide[x]) == n + 1);
-          if (a.masks) {   // the warp's 32 nodes are one word of each row's mask
-            for (int i = lane; i < HC; i += 32) {
-              const int r = t.row0 + col0 + i;
-              uint32_t w = 0u;
-              if (r < rows && t.at + 32 * quad < a.N)
-                w = __ldg(a.masks + (static_cast<long long>(t.c.b) * a.N + r / a.G) * a.NW + t.at / 32 + quad);
-              seen[i] = w;
-            }
-            __syncwarp();
-          } else {
-            open = (t.at + tok) * a.G - t.row0 - col0;
-          }
-          if (wide) {
-            tc_wide_scores<D, NC>(a, t.c.b, t.h, t.row0, rows, t.at + tok, col0, HC, factor - col0, s_at);
+      const int itri = t.c.i;
+      const uint32_t o_at = tmem + lane_at + L::t_o + tri % L::QB * NC + col0;
+      for (int i = threadIdx.x & 127; i < HC; i += 128) shift[i] = TC_UNSET;
+      named_bar_sync(id, 128);
+      bool first = true, ends = false;
+      if (t.kind == TC_CACHED) {
+        reinterpret_cast<float*>(tc_smem + L::fresh)[quad * NC + col0 + lane] = 0.f;
+      } else {
+        for (;;) {
+          float* w = cta_ws + 2 * static_cast<size_t>(NC) * (D + 4);
+          if (tc_fresh_softmax<D, NC>(tc_smem, t.kind == TC_FRESH, t.c.b, t.row0, t.at, t.left, first, n, tmem + lane_at + L::t_s + (n & 1) * NC + col0, o_at, w)) {
+            named_bar_sync(id, 128);   // the weights are written
+            tc_wait(&bar->pvdone[n & 1], (n >> 1) & 1, bar, a.timeout_ns);
+            tc_fence_after();
+            tc_wide_values<D, NC>(a, t.c.b, t.h, t.at, t.left, tok, col0, HC, w, o_at);
             tc_fence_before();
           }
+          first = false;
+          ends = t.ends;
+          ++n;
+          u += t.step;
+          if (t.last) break;
+          tc_step<NC>(a, prefix, HR, nfresh, ntiles - u, t);
+          if (t.kind == TC_CACHED) break;
         }
       }
-      // which of the rows do not see this thread's token
-      uint32_t hide = 0u;
-      if (TC_RARE(some)) {
-        hide = tc_hidden(t.kind == TC_FRESH && a.masks, seen, open);
-        if (tok >= t.left) hide = ~0u;
+#pragma unroll
+      for (int i = 0; i < HC / 2; ++i) l[i] = 0.f;
+      if (t.kind == TC_CACHED) {
+        const float* factor = reinterpret_cast<const float*>(tc_smem + L::factor) + (tri & 1) * NC + col0;
+        tc_wait(&bar->sready[n & 1], (n >> 1) & 1, bar, a.timeout_ns);   // (and so the queries have their factors)
+        const float common = bar->common[tri & 1];   // the rows' factor, 0: each its own
+        const unsigned long long common2 = common == 0.f ? f2_pack(1.f, 1.f) : f2_pack(common, common);
+        const int tiles = min(t.c.units - t.c.i, ntiles - u), n0 = n;
+        int left = t.c.len - t.at;                   // tokens of the sequence from the tile on
+        for (const int end = n + tiles; n < end; ++n, left -= TC_TILE) {
+          const int x = n & 1;
+          tc_wait(&bar->sready[x], (n >> 1) & 1, bar, a.timeout_ns);
+          tc_fence_after();
+          const uint32_t s_at = tmem + lane_at + L::t_s + x * NC + col0;
+          const bool some = left < TC_TILE, hides = tok >= left;   // no token of the sequence
+          float y[HC];
+          for (bool again = false;; again = true) {
+            tc_ld<HC>(s_at, y);
+            float m = 0.f;
+            // (After new references the products are rounded as those were: of scores above
+            // 2^28 a fused product would leave half a step, which is beyond any weight.)
+            const unsigned long long by = again ? f2_pack(1.f, 1.f) : common2;
+            if (TC_RARE(again || common == 0.f)) {
+#pragma unroll
+              for (int i = 0; i < HC; ++i) y[i] *= factor[i];
+            }
+            // (one factor for all rows: a value for each row and tile less to read, where
+            // the bandwidth of shared memory is what bounds a tile of many rows)
+#pragma unroll
+            for (int i = 0; i < HC; i += 4) {
+              const float4 s = *reinterpret_cast<const float4*>(shift + i);
+              f2_unpack(f2_fma(f2_pack(y[i], y[i + 1]), by, f2_pack(s.x, s.y)), y[i], y[i + 1]);
+              f2_unpack(f2_fma(f2_pack(y[i + 2], y[i + 3]), by, f2_pack(s.z, s.w)), y[i + 2], y[i + 3]);
+            }
+            if (TC_RARE(some)) {
+#pragma unroll
+              for (int i = 0; i < HC; ++i)
+                if (hides) y[i] = kNegInf;
+            }
+#pragma unroll
+            for (int i = 0; i < HC; i += 2) m = fmax3_nan(m, y[i], y[i + 1]);
+            // (in a row without a reference every score but -inf is far above it)
+            if (__builtin_expect(again || !tc_any<128>(id, !(m <= AT_PSHIFT + AT_ABOVE)), 1)) break;
+            const bool sums = !(first && n == n0);
+            if (sums) tc_wait(&bar->pvdone[x ^ 1], ((n - 1) >> 1) & 1, bar, a.timeout_ns);
+            tc_raise<D, NC>(tc_smem, s_at, o_at, factor, hides ? ~0u : 0u, sums);
+#pragma unroll
+            for (int i = 0; i < HC / 2; ++i) l[i] *= corr[(odd ? HC / 2 : 0) + i];
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar->sfree[x]);   // the scores have been read
+#pragma unroll
+          for (int i = 0; i < HC; ++i) y[i] = ex2_approx(y[i]);
+#pragma unroll
+          for (int i = 0; i < HC / 2; ++i) {
+            const float keep = odd ? y[i + HC / 2] : y[i], give = odd ? y[i] : y[i + HC / 2];
+            l[i] += keep + __shfl_xor_sync(0xffffffffu, give, 1);
+          }
+          if (n >= 2) tc_wait(&bar->pvdone[x], ((n >> 1) & 1) ^ 1, bar, a.timeout_ns);
+          // (a fresh tile's weights are in both buffers)
+          if (TC_RARE(n == n0 && n >= 1)) tc_wait(&bar->pvdone[x ^ 1], ((n - 1) >> 1) & 1, bar, a.timeout_ns);
+          unsigned char* pb = tc_smem + L::p + x * L::p_bytes + tok * 16 + col0 / 8 * 2048;
+#pragma unroll
+          for (int i = 0; i < HC; i += 8)
+            *reinterpret_cast<uint4*>(pb + i / 8 * 2048) = make_uint4(f16x2_pack(y[i], y[i + 1]), f16x2_pack(y[i + 2], y[i + 3]),
+                                                                      f16x2_pack(y[i + 4], y[i + 5]), f16x2_pack(y[i + 6], y[i + 7]));
+          tc_fence_before();
+          tc_proxy_fence();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bar->pready[x]);
+        }
+        u += tiles;
+        ends = t.c.i + tiles == t.c.units;
       }
-      const bool hides = some && __any_sync(0xffffffffu, hide != 0u);
-      float y[HC];
-      for (bool again = false;; again = true) {
-        tc_ld<HC>(s_at, y);
-        float m = 0.f;
-        // (After new references the products are rounded as those were: of scores above
-        // 2^28 a fused product would leave half a step, which is beyond any weight.)
-        const unsigned long long by = again ? f2_pack(1.f, 1.f) : common2;
-        if (TC_RARE(again || common == 0.f)) {
-#pragma unroll
-          for (int i = 0; i < HC; ++i) y[i] *= factor[i];
-        }
-        // (one factor for all rows: a value for each row and tile less to read, where
-        // the bandwidth of shared memory is what bounds a tile of many rows)
-#pragma unroll
-        for (int i = 0; i < HC; i += 4) {
-          const float4 s = *reinterpret_cast<const float4*>(shift + i);
-          f2_unpack(f2_fma(f2_pack(y[i], y[i + 1]), by, f2_pack(s.x, s.y)), y[i], y[i + 1]);
-          f2_unpack(f2_fma(f2_pack(y[i + 2], y[i + 3]), by, f2_pack(s.z, s.w)), y[i + 2], y[i + 3]);
-        }
-        if (TC_RARE(hides)) {
-#pragma unroll
-          for (int i = 0; i < HC; ++i)
-            if ((hide >> i) & 1u) y[i] = kNegInf;
-        }
-#pragma unroll
-        for (int i = 0; i < HC; i += 2) m = fmax3_nan(m, y[i], y[i + 1]);
-        // (in a row without a reference every score but -inf is far above it)
-        if (__builtin_expect(again || !tc_any<128>(id, !(m <= AT_PSHIFT + AT_ABOVE)), 1)) break;
-        if (!t.first) tc_wait(&bar->pvdone[(n - 1) & 1], ((n - 1) >> 1) & 1, bar, a.timeout_ns);
-        tc_raise<NC>(s_at, o_at, factor, shift, corr, top, hide, !t.first, quad, id);
-#pragma unroll
-        for (int i = 0; i < HC / 2; ++i) l[i] *= corr[(odd ? HC / 2 : 0) + i];
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bar->sfree[x]);   // the scores have been read
-#pragma unroll
-      for (int i = 0; i < HC; ++i) y[i] = ex2_approx(y[i]);
+      // the part's end
+      tc_wait(&bar->pvdone[(n - 1) & 1], ((n - 1) >> 1) & 1, bar, a.timeout_ns);
+      unsigned char* sums = tc_smem + L::p + col0 / 8 * 2048;
 #pragma unroll
       for (int i = 0; i < HC / 2; ++i) {
-        const float keep = odd ? y[i + HC / 2] : y[i], give = odd ? y[i] : y[i + HC / 2];
-        l[i] += keep + __shfl_xor_sync(0xffffffffu, give, 1);
+        tc_sums<D, NC>(sums, i)[tok] = odd ? 0.f : l[i];
+        tc_sums<D, NC>(sums, i + HC / 2)[tok] = odd ? l[i] : 0.f;
       }
-      if (TC_RARE(wide)) {   // weights for the values out of range, -1 where the row does not see the node
-        float* w = cta_ws + 2 * static_cast<size_t>(NC) * (D + 4) + static_cast<size_t>(tok) * NC + col0;
-#pragma unroll
-        for (int i = 0; i < HC; ++i) __stcg(w + i, (hide >> i) & 1u ? -1.f : y[i]);
-      }
-      if (n >= 2) tc_wait(&bar->pvdone[x], ((n >> 1) & 1) ^ 1, bar, a.timeout_ns);
-      unsigned char* pb = tc_smem + L::p + x * L::p_bytes + tok * 16 + col0 / 8 * 2048;
-#pragma unroll
-      for (int i = 0; i < HC; i += 8)
-        *reinterpret_cast<uint4*>(pb + i / 8 * 2048) = make_uint4(f16x2_pack(y[i], y[i + 1]), f16x2_pack(y[i + 2], y[i + 3]),
-                                                                  f16x2_pack(y[i + 4], y[i + 5]), f16x2_pack(y[i + 6], y[i + 7]));
+      tc_finish<D, NC>(tc_smem, at_row(a, t.c.b, t.h, 0), t.row0, itri == 0 && ends, cta_ws + (itri == 0 ? static_cast<size_t>(NC) * (D + 4) : 0), o_at);
       tc_fence_before();
-      tc_proxy_fence();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&bar->pready[x]);
-      if (TC_RARE(wide)) {
-        named_bar_sync(id, 128);   // the weights are written
-        tc_wait(&bar->pvdone[x], (n >> 1) & 1, bar, a.timeout_ns);
-        tc_fence_after();
-        tc_wide_values<D, NC>(a, t.c.b, t.h, t.at, t.left, tok, col0, HC, cta_ws + 2 * static_cast<size_t>(NC) * (D + 4), o_at);
-        tc_fence_before();
-      }
-      if (TC_RARE(t.last)) {
-        tc_wait(&bar->pvdone[x], (n >> 1) & 1, bar, a.timeout_ns);
-        unsigned char* sums = tc_smem + L::p + col0 / 8 * 2048;
-#pragma unroll
-        for (int i = 0; i < HC / 2; ++i) {
-          tc_sums<D, NC>(sums, i)[tok] = odd ? 0.f : l[i];
-          tc_sums<D, NC>(sums, i + HC / 2)[tok] = odd ? l[i] : 0.f;
-        }
-        tc_finish<D, NC>(a.out, a.lse, at_row(a, t.c.b, t.h, 0), a.G, a.by_g, a.Hkv * a.G, a.v_mul, t.row0, rows, itri == 0 && t.ends,
-                         cta_ws + (itri == 0 ? static_cast<size_t>(NC) * (D + 4) : 0), sums, shift, corr, top,
-                         reinterpret_cast<long long*>(tc_smem + L::rows) + col0, o_at, part);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bar->ofree[tri & 1]);
-        ++tri;
-        named_bar_sync(id, 128);   // top, corr and shift are free again
-      }
-      ++n;
-      if ((u += t.step) >= ntiles) break;
+      if (lane == 0) mbar_arrive(&bar->ofree[tri & 1]);
+      named_bar_sync(id, 128);   // top, corr and shift are free again
+      if (u >= ntiles) break;
+      t.c.i = t.c.units - 1;   // the next triple
+      t.step = 1;
       tc_step<NC>(a, prefix, HR, nfresh, ntiles - u, t);
     }
   }

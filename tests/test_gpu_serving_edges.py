@@ -142,3 +142,44 @@ def test_attend_largest_queries_against_keys_of_zero(N):
     out, lse = sv.spec_attend_q4(q, sv.q4_cache(2, 1, 32, 128, DEV), i32([[0, 1]]), i32([40]), k_shift=32)
     assert not out.any()
     np.testing.assert_allclose(f64(lse), np.log(40.0), rtol=0, atol=2.0 ** -20 * 5)
+
+
+@pytest.mark.parametrize("N,Hq,Hkv,D", ROWS[1:])
+def test_attend_large_finite_keys_at_small_shifts(N, Hq, Hkv, D):
+    """Scores far beyond the cache's, and within fp32: the node with the largest takes
+    all of the weight."""
+    c = _case(71 + N, 2, N, Hq, Hkv, D, 32, [40, 0], shifts=(-32, 0))
+    c["k"][:, 2] *= 2.0 ** 100
+    out, lse = (f64(x) for x in _attend(c))
+    assert np.isfinite(lse).all() and np.isfinite(out).all()
+    G = Hq // Hkv
+    k, v, q = (f64(c[x]) for x in ("k", "v", "q"))
+    z = np.einsum("bnid,bid->bni", q, np.repeat(k[:, 2], G, 1)) * D ** -0.5
+    assert (np.abs(z) > 2.0 ** 60).all()
+    wins = (z > 0) & (np.arange(N) >= 2)[None, :, None]
+    want = np.broadcast_to(np.repeat(v[:, 2], G, 1)[:, None], out.shape)
+    assert wins.any() and (np.abs(out - want) <= 2.0 ** -8 * np.abs(want))[wins].all()
+
+
+@pytest.mark.parametrize("N,Hq,Hkv,D", ROWS[1:])
+@pytest.mark.parametrize("shifts,ks,vs", [((0, 0), -20, -20), ((0, 0), -60, -45), ((32, 32), 0, 0), ((-32, -32), 8, 8), ((32, -32), 20, -10)])
+def test_attend_fresh_entries_far_from_the_caches_unit(N, Hq, Hkv, D, shifts, ks, vs):
+    """Fresh entries are bf16 whatever the shifts: keys of 2^ks (the queries make up
+    for it, so that the scores are ordinary ones) and values of 2^vs, in units of
+    2^shift; nothing is cached."""
+    c = _case(72 + N, 2, N, Hq, Hkv, D, 32, [0, 0], shifts=shifts)
+    c["k"] *= 2.0 ** ks
+    c["q"] *= 2.0 ** -ks
+    c["v"] *= 2.0 ** vs
+    _close(_attend(c), _expect(c), D)
+
+
+@pytest.mark.parametrize("N,Hq,Hkv,D", ROWS[1:])
+def test_attend_fresh_entries_of_every_size_together(N, Hq, Hkv, D):
+    """Nodes and columns of sizes between 2^-60 and 2^20 beside each other and beside
+    cached tokens."""
+    c = _case(73 + N, 3, N, Hq, Hkv, D, 32, [0, 70, 5], tree=True, shifts=(3, -4))
+    rng = c["rng"]
+    for x in ("k", "v"):
+        c[x] = (c[x].double() * torch.from_numpy(np.exp2(rng.integers(-60, 3, (3, N, Hkv, 1)) + rng.integers(-12, 13, (3, N, Hkv, D))))).to(torch.bfloat16)
+    _close(_attend(c), _expect(c), D)
