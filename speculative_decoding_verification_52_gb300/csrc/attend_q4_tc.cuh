@@ -26,10 +26,10 @@
 // the products, and one for the copies.  K, S^T, V and P have two buffers each,
 // queries and O^T two where tensor and shared memory hold them (NC = 64).  Each CTA
 // has one contiguous share of the list of tiles (attend_q4.cuh), with at most two
-// triples cut off at its ends, whose parts the join kernel puts together.  A triple's
-// first fresh tile counts for nine in the list: with it come the queries, the first
-// references and the triple's end (32 trees of 64 nodes over lengths of 1,024 to
-// 7,168: 725 us when it counted as one, 523 as nine).
+// triples cut off at its ends, whose parts the join kernel puts together.  Fresh tiles
+// count for several cached ones in the list: their keys and values come by loads that
+// somebody waits for, and with the first come the queries, the first references and the
+// triple's end.
 //
 // Bounds, per tile of 128 tokens and D = 128: 784 clocks of the bus; products
 // 1,024 clocks at NC = 128; unpacking 256 conversions, 256 multiplications and 16
@@ -54,7 +54,11 @@
 namespace sv {
 
 constexpr int TC_TILE = 128;                 // tokens of a tile
-constexpr int TC_FRESH_UNITS = 9;            // what a triple's first fresh tile counts in the list, in cached tiles
+// What a triple's first fresh tile counts in the list, in cached tiles, and another one.
+// 2 chunks of 1,024 tokens behind about 8,192 (D = 64): 9 and 1 378 us, 9 and 2 348, 9
+// and 4 312, 12 and 4 322; 32 trees of 64 nodes behind about 4,096, where only the first
+// matters: 6 357 us, 9 342, 12 335; behind 4,096 each: 338, 340, 344.
+constexpr int TC_FRESH_UNITS = 9, TC_FRESH_MORE = 4;
 constexpr int TC_PART = 32;                  // rows of a softmax thread
 // 7 - reference before any score.  Finite, so that a score of -inf weighs nothing
 // against it; every other score is far above the reference and sets a new one.
@@ -273,11 +277,11 @@ struct TcTile {
 };
 enum { TC_CACHED = 0, TC_FRESH = 1, TC_VOID = 2 };   // void: a length out of range (left = 1), or nothing at all (left = 0)
 
-// A triple's first fresh tile stands for a.fresh units, every other tile for one
-// (nfresh: units of the fresh tiles).  A share that begins within those units has a
-// tile of nothing first.
+// A triple's first fresh tile stands for TC_FRESH_UNITS units, another one for
+// TC_FRESH_MORE, a cached tile for one (nfresh: units of the fresh tiles).  A share that
+// begins within a fresh tile's units has a tile of nothing first.
 template <int NC>
-__device__ __noinline__ void tc_open_slow(int row_tiles, int N, int fresh, bool len_ok, int nfresh, TcTile& t) {
+__device__ __noinline__ void tc_open_slow(int row_tiles, int N, bool len_ok, int nfresh, TcTile& t) {
   t.h = t.c.pair / row_tiles;
   t.row0 = (t.c.pair - t.h * row_tiles) * NC;
   t.at = 0;
@@ -286,12 +290,13 @@ __device__ __noinline__ void tc_open_slow(int row_tiles, int N, int fresh, bool 
     t.kind = TC_VOID;
     t.left = 1;
   } else if (t.c.i < nfresh) {
-    const int j = t.c.i < fresh ? 0 : t.c.i - fresh + 1;
+    const int j = t.c.i < TC_FRESH_UNITS ? 0 : (t.c.i - TC_FRESH_UNITS) / TC_FRESH_MORE + 1;
+    const int from = j ? TC_FRESH_UNITS + (j - 1) * TC_FRESH_MORE : 0;
     t.at = j * TC_TILE;
     t.left = min(N - t.at, TC_TILE);
     t.kind = TC_FRESH;
-    t.step = t.c.i < fresh ? fresh - t.c.i : 1;
-    if (t.c.i > 0 && j == 0) {
+    t.step = (j ? from + TC_FRESH_MORE : TC_FRESH_UNITS) - t.c.i;
+    if (t.c.i > from) {
       t.kind = TC_VOID;
       t.left = 0;
     }
@@ -305,7 +310,7 @@ __device__ __noinline__ void tc_open_slow(int row_tiles, int N, int fresh, bool 
 template <int NC>
 __device__ __forceinline__ void tc_open(const AttendArgs& a, int nfresh, TcTile& t) {
   TcTile x = t;   // (by a copy: the tile itself stays in registers)
-  tc_open_slow<NC>(a.row_tiles, a.N, a.fresh, at_len_ok(a, t.c.len), nfresh, x);
+  tc_open_slow<NC>(a.row_tiles, a.N, at_len_ok(a, t.c.len), nfresh, x);
   t = x;
 }
 template <int NC>
@@ -327,7 +332,7 @@ __device__ __forceinline__ void tc_step(const AttendArgs& a, const long long* pr
     tc_open<NC>(a, nfresh, t);
   } else {
     t.first = false;
-    t.step = 1;
+    t.step = t.kind == TC_FRESH ? TC_FRESH_MORE : 1;
     t.at += TC_TILE;
     t.left = min((t.kind == TC_FRESH ? a.N : t.c.len) - t.at, TC_TILE);
   }

@@ -242,7 +242,7 @@ spec_status_t attend_entry(const void* q, const void* k_new, const void* v_new, 
     a.by_g = a.G > 1 ? static_cast<uint32_t>((0x100000000ull + a.G - 1) / a.G) : 0u;
     a.tile = plan.tc ? TC_TILE : AT_TILE;
     a.fresh = plan.tc ? TC_FRESH_UNITS : AT_FRESH;
-    a.fresh_more = plan.tc ? 1 : AT_FRESH;
+    a.fresh_more = plan.tc ? TC_FRESH_MORE : AT_FRESH;
     a.scale_log2 = static_cast<float>(1.4426950408889634 * static_cast<double>(scale));
     a.k_mul = std::ldexp(1.f, k_shift);
     a.v_mul = std::ldexp(1.f, v_shift);
