@@ -399,19 +399,24 @@ def _take(t, name: str, dtype, shape, dev: int):
 
 
 def _serve(fn):
-    """Runs a serving call on its tensors' device and the given stream: fn gets the
-    device's index and the stream's handle."""
+    """Runs a serving call on its tensors' device (its first argument's) and the given
+    stream: fn gets the device's index and the stream's handle."""
+    name = fn.__code__.co_varnames[0]
+
     @functools.wraps(fn)
-    def call(first, *args, stream=None, **kw):
+    def call(*args, stream=None, **kw):
+        if not args and name not in kw:
+            raise TypeError(f"{fn.__name__}() missing argument: '{name}'")
+        first = args[0] if args else kw[name]
         if not isinstance(first, torch.Tensor) or not first.is_cuda:
             raise ValueError(f"{fn.__name__}: tensors must be CUDA tensors")
         dev = first.get_device()
         if stream is None and dev == torch._C._cuda_getDevice():
-            return fn(first, *args, dev=dev, stream=torch._C._cuda_getCurrentRawStream(dev), **kw)
+            return fn(*args, dev=dev, stream=torch._C._cuda_getCurrentRawStream(dev), **kw)
         if stream is not None and stream.device.index != dev:
             raise ValueError(f"{fn.__name__}: the stream is on {stream.device}, the tensors on cuda:{dev}")
         with torch.cuda.device(dev), torch.cuda.stream(stream):
-            return fn(first, *args, dev=dev, stream=torch._C._cuda_getCurrentRawStream(dev), **kw)
+            return fn(*args, dev=dev, stream=torch._C._cuda_getCurrentRawStream(dev), **kw)
     return call
 
 

@@ -183,3 +183,13 @@ def test_attend_fresh_entries_of_every_size_together(N, Hq, Hkv, D):
     for x in ("k", "v"):
         c[x] = (c[x].double() * torch.from_numpy(np.exp2(rng.integers(-60, 3, (3, N, Hkv, 1)) + rng.integers(-12, 13, (3, N, Hkv, D))))).to(torch.bfloat16)
     _close(_attend(c), _expect(c), D)
+
+
+def test_first_argument_by_name():
+    """Every argument of the serving calls can be given by its name."""
+    c = _case(75, 1, 2, 4, 2, 64, 32, [40])
+    q, cache, table, lengths = c["q"].to(DEV), torch.from_numpy(c["cache"]).to(DEV), i32(c["table"]), i32(c["lengths"])
+    a, b = sv.spec_attend_q4(q, cache, table, lengths), sv.spec_attend_q4(q=q, cache=cache, block_table=table, lengths=lengths)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    x = torch.randn(1, 2, 40, device=DEV)
+    assert torch.equal(sv.spec_adjust_logits(logits=x), x)

@@ -165,3 +165,16 @@ def test_attend_stall_hook_refusals(L, kw, status):
     at = list(ATT).index("p_out")
     args = dict(list(ATT.items())[:at] + [("cta", 0), ("us", 2000)] + list(ATT.items())[at:])
     assert _call(L.spec_debug_attend_stall, args, **kw) == status
+
+
+def test_binding_takes_every_argument_by_name():
+    """Named or not, the first argument is looked at in the same way; none is an error
+    of the call."""
+    import speculative_decoding_verification_52_gb300 as sv
+    z = torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        sv.spec_page_map(lengths=z, count=z, held=z, ring=z, ring_state=z, block_table=z.view(1, 2), page_tokens=32, max_tokens=4)
+    with pytest.raises(ValueError, match="CUDA"):
+        sv.spec_adjust_logits(logits=torch.zeros(1, 1, 8))
+    with pytest.raises(TypeError, match="logits"):
+        sv.spec_adjust_logits()
