@@ -470,7 +470,8 @@ spec_status_t spec_debug_attend_stall(const void *q, const void *k_new, const vo
  *   l = logit; if v is in the prompt or n > 0: l = l > 0 ? l / repetition
  *   : l * repetition; if n > 0: l -= frequency * n + presence; l += biases;
  *   l = -inf where v is not allowed.
- * Tokens outside [0, V) are ignored, wherever they stand.  Limits: R <= 1024,
+ * (l / repetition is the product with the rounded reciprocal: two roundings, for
+ * penalties of 2^-126 to 2^126.)  Tokens outside [0, V) are ignored, wherever they stand.  Limits: R <= 1024,
  * Nt <= 1024, V <= 2^30. */
 spec_status_t spec_adjust_logits(const void *logits, spec_dtype_t dtype, const int32_t *history,
                                  const int32_t *prompt_lengths, const int32_t *history_lengths,

@@ -56,7 +56,10 @@ struct AdjustArgs {
 constexpr uint32_t AJ_SEEN = 1u, AJ_PATCH = 2u, AJ_ONE = 4u;   // flag, flag, one generated token
 
 struct AdjustScalars {
-  float rep, inv, freq, pres;   // inv = 1 / rep
+  // inv = 1 / rep, rounded: a quotient is its product with the logit, off by 2^-23 at most
+  // where one rounding would be 2^-24.  (Divisions take 197 us where this takes 176: 256 x 6
+  // rows of 128,256 bf16, everything on.)
+  float rep, inv, freq, pres;
 };
 
 __device__ __forceinline__ float adjust_one(float l, uint32_t word, int more, const AdjustScalars& s) {

@@ -193,3 +193,19 @@ def test_first_argument_by_name():
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
     x = torch.randn(1, 2, 40, device=DEV)
     assert torch.equal(sv.spec_adjust_logits(logits=x), x)
+
+
+def test_adjust_repetition_penalties_of_every_size():
+    """logit / repetition takes two roundings (of the reciprocal and of the product),
+    2^-24 each: 2^-23 (1 + 2^-25) of the quotient at most.  A negative logit's product
+    takes one."""
+    rng = np.random.default_rng(6)
+    rep = np.array([1.1, 1.3, 2.0 ** -126, 2.0 ** 126, 7.0, 0.3], np.float32)
+    B, V = len(rep), 4099
+    x = (rng.standard_normal((B, 1, V)) * np.array([3, 3, 1e-12, 1e12, 3, 3])[:, None, None]).astype(np.float32)
+    x = np.where((rep > 2)[:, None, None] | (rep < 0.1)[:, None, None], np.abs(x), x)
+    got = sv.spec_adjust_logits(f32(x), history=i32(np.broadcast_to(np.arange(V), (B, V))), history_lengths=i32(np.full(B, V)),
+                                prompt_lengths=i32(np.full(B, V)), repetition=f32(rep)).cpu().numpy()
+    r = rep[:, None, None].astype(np.float64)
+    exp = np.where(x > 0, x / r, x * r)
+    assert (np.abs(got - exp) <= 2.0 ** -23 * (1 + 2.0 ** -25) * np.abs(exp)).all()
