@@ -243,7 +243,7 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
 __host__ __device__ constexpr int at_stage_bytes(int D) { return 2 * q4_block_bytes(D); }
 // of a pair: the queries' operand; in exchange, two buffers each, the weights
 // (each warp's operands), the maxima or sums, and the flags; a flag a stage (at
-// most 8) and one more; the list of fetches
+// most 8); the list of fetches
 __host__ __device__ constexpr int at_q_bytes(int D, int NR) { return NR * (D / 32) * 512; }
 __host__ __device__ constexpr int at_p_bytes(int NR) { return 2 * 2 * 2 * NR * 256; }
 __host__ __device__ constexpr int at_m_bytes(int NR) { return 2 * 2 * 8 * NR * 4; }
@@ -361,8 +361,6 @@ struct AtPair {
     return reinterpret_cast<int*>(base + at_q_bytes(D, NR) + at_p_bytes(NR) + at_m_bytes(NR)) + buf * 2 + warp;
   }
   __device__ __forceinline__ int* arrived(int stage) const { return flag(2, 0) + stage; }
-  // AT_STUCK and the stages' phases at the time, once a wait of the first warp has failed
-  __device__ __forceinline__ int* stuck() const { return flag(2, 0) + 8; }
   __device__ __forceinline__ uint2* queue() const {
     return reinterpret_cast<uint2*>(base + at_q_bytes(D, NR) + at_p_bytes(NR) + at_m_bytes(NR) + 64);
   }
@@ -952,6 +950,7 @@ template <int D, int NR>
 __global__ void __launch_bounds__(AT_THREADS, at_ctas(D, NR)) attend_q4_kernel(const __grid_constant__ AttendArgs a, int stages) {
   extern __shared__ __align__(128) unsigned char at_smem[];
   __shared__ long long scratch[AT_THREADS / 32];
+  __shared__ int stuck[AT_PAIRS];   // AT_STUCK and the stages' phases at the time, once a wait of the first warp has failed
   constexpr int SB = at_stage_bytes(D), BB = q4_block_bytes(D);
   const int pair = threadIdx.x >> 6;
   unsigned char* ring = at_smem + static_cast<size_t>(pair) * stages * SB;
@@ -965,7 +964,7 @@ __global__ void __launch_bounds__(AT_THREADS, at_ctas(D, NR)) attend_q4_kernel(c
   if ((threadIdx.x & 63) == 0) {
     for (int s = 0; s < stages; ++s) mbar_init(&bars[s], 1);
     if (a.stall == static_cast<int>(blockIdx.x) + 1 && pair == 0) mbar_init(&bars[0], 2);   // (test hook)
-    *pr.stuck() = 0;
+    stuck[pair] = 0;
     mbar_fence_init();
   }
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // (the join kernel may start; it waits for this grid's end)
@@ -1061,7 +1060,7 @@ __global__ void __launch_bounds__(AT_THREADS, at_ctas(D, NR)) attend_q4_kernel(c
         // the stage holds, and its result is void)
         if (!failed && !mbar_wait(&bars[stage], (phase >> stage) & 1u, a.timeout_ns)) {
           failed = true;   // no more copies are started
-          if ((threadIdx.x & 63) == 0) *pr.stuck() = static_cast<int>(phase) | AT_STUCK;
+          if ((threadIdx.x & 63) == 0) stuck[pair] = static_cast<int>(phase) | AT_STUCK;
         }
         phase ^= 1u << stage;
         poison |= !*pr.arrived(stage);
@@ -1080,7 +1079,7 @@ __global__ void __launch_bounds__(AT_THREADS, at_ctas(D, NR)) attend_q4_kernel(c
     }
   }
   __syncthreads();
-  if ((threadIdx.x & 63) == 0 && __builtin_expect(*pr.stuck(), 0)) at_drain(bars, stages, *pr.stuck(), a.timeout_ns);
+  if ((threadIdx.x & 63) == 0 && __builtin_expect(stuck[pair], 0)) at_drain(bars, stages, stuck[pair], a.timeout_ns);
 
   // Joins within the CTA.  A triple that begins in a pair's share and goes on is
   // joined by that pair, whose registers hold its first part; the other parts
