@@ -179,7 +179,7 @@ struct AttendPlan {
 constexpr int kFewRows128 = 48, kFewRows64 = 72;
 AttendPlan attend_plan(int B, int rows, int D) {
   AttendPlan p{};
-  const int NC = rows <= 64 ? 64 : 128;
+  const int NC = D == 128 && rows <= 64 ? 64 : 128;   // (what there are kernels for)
   // (the largest batches leave no room for the tensor cores' kernel)
   p.tc = rows > (D == 128 ? kFewRows128 : kFewRows64) && tc_smem_bytes(D, NC, B) <= static_cast<size_t>(kMaxDynSmem);
   if (p.tc) {

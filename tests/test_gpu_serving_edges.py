@@ -209,3 +209,65 @@ def test_adjust_repetition_penalties_of_every_size():
     r = rep[:, None, None].astype(np.float64)
     exp = np.where(x > 0, x / r, x * r)
     assert (np.abs(got - exp) <= 2.0 ** -23 * (1 + 2.0 ** -25) * np.abs(exp)).all()
+
+
+@pytest.mark.parametrize("N,Hq,Hkv,D", ROWS)
+@pytest.mark.parametrize("scale", [0.0, -0.3, 2.0])
+def test_attend_scales_with_every_row_tile(N, Hq, Hkv, D, scale):
+    """A negative scale, a large one, and none, over cached and fresh entries."""
+    c = _case(77 + N, 3, N, Hq, Hkv, D, 32, [150, 0, 33], tree=True, shifts=(1, -2))
+    _close(_attend(c, scale=scale), _expect(c, scale), D)
+
+
+@pytest.mark.parametrize("N,Hq,Hkv,D", ROWS[1:])
+def test_attend_cached_tokens_alone_with_every_row_tile(N, Hq, Hkv, D):
+    """Without fresh entries; queries of one size and of very different ones."""
+    c = _case(78 + N, 4, N, Hq, Hkv, D, 32, [300, 0, 129, 1], fresh=False, shifts=(2, -3))
+    c["q"][2:] *= torch.from_numpy(np.exp2(c["rng"].integers(-14, 3, (2, N, Hq, 1)))).to(torch.bfloat16)
+    exp = _expect(c)
+    assert (exp[1][1] == -np.inf).all()
+    _close(_attend(c), exp, D)
+
+
+@pytest.mark.parametrize("N,Hq,D", [(1, 8, 128), (2, 8, 128), (6, 4, 128), (8, 4, 64)])
+def test_attend_largest_batch_of_few_rows(N, Hq, D):
+    rng = np.random.default_rng(N)
+    B, P, pages = 4096, 32, 16
+    lengths, table = rng.integers(0, 90, B), rng.integers(0, pages, (B, 3))
+    cache = base._cache(rng, pages, 1, P, D)
+    q = torch.randn(B, N, Hq, D, device=DEV, dtype=torch.bfloat16)
+    k, v = (torch.randn(B, N, 1, D, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    got = sv.spec_attend_q4(q, torch.from_numpy(cache).to(DEV), i32(table), i32(lengths), k_new=k, v_new=v)
+    rows = [0, 1, 2047, B - 1]
+    see = np.broadcast_to(np.tril(np.ones((N, N), bool)), (4, N, N))
+    exp = ref.attend(f64(q[rows]), cache, table[rows], lengths[rows], f64(k[rows]), f64(v[rows]), see, D ** -0.5, 0, 0)
+    _close([x[rows] for x in got], exp, D)
+    assert torch.isfinite(got[0]).all() and torch.isfinite(got[1]).all()
+
+
+def test_attend_captured_with_many_rows_and_a_shared_workspace():
+    """Two captured calls, of many rows and of few, that use one workspace in turn."""
+    cs = [_case(79, 2, 40, 16, 2, 128, 32, [300, 150]), _case(80, 3, 2, 16, 2, 64, 32, [100, 300, 7])]
+    ws = sv.workspace(max(sv.spec_attend_workspace_bytes(*c["q"].shape[:3], 2, c["D"]) for c in cs), DEV)
+    calls = []
+    for c in cs:
+        q, k, v = (c[x].to(DEV) for x in ("q", "k", "v"))
+        cache, table, lengths = torch.from_numpy(c["cache"]).to(DEV), i32(c["table"]), i32(c["lengths"])
+        out, lse = torch.empty_like(q), torch.empty(q.shape[:3], device=DEV)
+
+        def call(q=q, k=k, v=v, cache=cache, table=table, lengths=lengths, out=out, lse=lse):
+            sv.spec_attend_q4(q, cache, table, lengths, k_new=k, v_new=v, out=out, lse=lse, workspace_buf=ws)
+        call()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        calls.append((c, g, lengths, out, lse, call))   # (call keeps the tensors that the graph reads)
+    for news in ([[300, 150], [100, 300, 7]], [[1, 0], [0, 33, 290]]):
+        for (c, g, lengths, out, lse, _), new in zip(calls, news):
+            lengths.copy_(i32(new))
+            out.fill_(float("nan"))
+            g.replay()
+        torch.cuda.synchronize()
+        for (c, g, lengths, out, lse, _), new in zip(calls, news):
+            _close((out, lse), _expect(c, lengths=np.array(new)), c["D"])
