@@ -371,8 +371,8 @@ spec_status_t spec_page_map(const int32_t *lengths, const int32_t *count, const 
  *       e.g. spec_page_map's: entry t goes to slots[t], a slot outside the cache
  *       (negative: none) is skipped.  Two entries with one slot leave one of the
  *       two, groups of both may mix.
- * Nothing else in the cache is written.  Limit: num_pages * page_tokens below
- * 2^31. */
+ * Nothing else in the cache is written.  Limits: num_pages * page_tokens below
+ * 2^31, Hkv <= 65535. */
 spec_status_t spec_kv_store_q4(const void *k, const void *v, const int32_t *slots, int T, int Hkv, int D,
                                int page_tokens, int num_pages, int k_shift, int v_shift, void *cache, void *stream);
 
@@ -461,7 +461,8 @@ spec_status_t spec_debug_attend_stall(const void *q, const void *k_new, const vo
  *       uint32 (spec_tree_mask's, Nt = R) row r sees the nodes whose bits are
  *       set, node 0 excepted (the root is the history's last token).
  *   bias_tokens [B, M] int32, bias_values [B, M] float32, or both NULL: a
- *       token's biases are added in the list's order.
+ *       token's biases are added in the list's order (each biased token looks
+ *       through its sequence's whole list: meant for lists of up to some hundreds).
  *   allowed [B, R, ceil(V/32)] uint32 or NULL: bit v % 32 of word v / 32 lets
  *       row r take token v.
  *

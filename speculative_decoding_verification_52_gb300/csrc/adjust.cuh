@@ -21,8 +21,9 @@
 //      computed one by one from the input, a warp to a token and a lane to a row.
 //      Step 2 leaves them as they are (or masked), so the output may be the input.
 // Measured at 256 x 6 rows of 128,256 bf16, 2,048 tokens of history each: the copy
-// alone 130 us (6.1 TB/s), 154 us with the history's penalties, 179 us with 64
-// biases and a mask a row too.  Seen tokens done in step 3 as well, 3 million single
+// alone 130 us (6.1 TB/s), 154 us with the history's penalties, 176 us with 64
+// biases and a mask a row too (a step's mask words and then its logits are two loads
+// that wait for each other; ALU 54 %).  Seen tokens done in step 3 as well, 3 million single
 // updates, cost 52 us more than the copy; penalties on all vectors alike, with one
 // test a vector, 296 us in all.
 #pragma once

@@ -18,7 +18,7 @@
 //   lengths, and fetches it through a ring of its own.  A triple that lies in one
 //   pair's share is finished there.  A fresh tile counts as three: it waits for
 //   its loads, where a cached tile's have arrived (256 sequences of 4 nodes at
-//   2,048 tokens, 16 rows: 236 us when it counts as one, 226 as three).  The pairs
+//   2,048 tokens, 16 rows: 210 us when it counts as one, 206 as three).  The pairs
 //   of a CTA have neighbouring shares and join what they share at the end; what
 //   CTAs share goes through the workspace (reference, sum, sum of v) and a second
 //   kernel.  All joins are in the list's order.
@@ -26,7 +26,7 @@
 //   warp adds up one half of v's columns over both blocks.  So every code is
 //   unpacked once for all rows, and the sums of a warp fit its registers beside
 //   the operands (a warp that kept all columns of 24 rows moved 137 registers a
-//   block through local memory: 450 us where this took 390).  One barrier of the
+//   block through local memory and took a seventh longer).  One barrier of the
 //   two warps a tile: the weights are 2^(z - ref) for a reference that both know,
 //   and only a score above ref + 15 makes them agree on a new one.
 // * Everything is unpacked in f16, exactly: a code times its scale has 6
@@ -522,10 +522,11 @@ __device__ __noinline__ void at_agree(const AtPair<D, NR>& pr, int buf, const fl
 // Both halves of the work are loops over 16 tokens, unrolled where the registers hold
 // what that interleaves and the code of a tile stays small: up to 8 KB a warp gets
 // through it at about the rate of its scheduler, at 16 KB it takes 2.7 clocks an
-// instruction to fetch.  256 sequences at 2,048 tokens, D = 128: 32 rows unrolled 381
-// us, rolled 388; 24 rows two steps at a time 304, rolled 295 (D = 64: 215 and 219);
-// 16 rows unrolled 218, two steps 223; 8 rows unrolled 170, rolled 187.  So that they
-// can be loops, the weights are taken at once against the references as they are, and
+// instruction to fetch.  256 sequences at 2,048 tokens, D = 128: 32 rows unrolled 347
+// us, rolled 360; 24 rows two steps at a time 281, rolled 277; 16 rows unrolled 206, two
+// steps 214; 8 rows unrolled 155, rolled 169.  D = 64: 32 rows rolled 244, two steps 257;
+// 24 rows two steps 197, rolled 207; 8 rows unrolled 119, rolled 128.  So that they can be
+// loops, the weights are taken at once against the references as they are, and
 // only then the warps look whether a score was too far above one; if so, they agree on
 // new references and score the tile again.
 //
@@ -842,10 +843,10 @@ __device__ __forceinline__ float at_lse(float ref, float l) {
 }
 
 // CTAs an SM, of four warps: what the registers of a row tile leave room for.  256
-// sequences at 2,048 tokens, D = 128: 32 rows 381 us with two, 485 with three (306
-// bytes of a thread in local memory); 24 rows 293 with three, 315 with two; 16 rows 218
-// with three, 226 with four.  D = 64, half the sums: 64 rows (two tiles of 32) 476 us
-// with three, 489 with two.
+// sequences at 2,048 tokens, D = 128: 32 rows 347 us with two, 437 with three (part of
+// the sums in local memory, for which the shared memory in use leaves little cache); 24
+// rows 277 with three, 305 with two; 16 rows 206 with three, 212 with four.  D = 64, half
+// the sums: 32 rows 244 us with three, 258 with two; 24 rows 197 and 209.
 __host__ __device__ constexpr int at_ctas(int D, int NR) { return NR == 1 ? 4 : D == 64 ? (NR == 2 ? 4 : 3) : NR < 4 ? 3 : 2; }
 
 // the warp's part of a row's sum of weights
@@ -1043,8 +1044,7 @@ __global__ void __launch_bounds__(AT_THREADS, at_ctas(D, NR)) attend_q4_kernel(c
       const int f0 = (first + AT_FRESH - 1) / AT_FRESH, f1 = (min(last, nf) + AT_FRESH - 1) / AT_FRESH;
       // (In line: in a function of their own these tiles leave the cached ones' loop
       // more registers, but the state and the arguments then pass through memory: 24
-      // rows of 256 sequences at 2,048 tokens took 316 us where this takes 303, of 32
-      // at 16,384 239 us where this takes 246.)
+      // rows of 256 sequences at 2,048 tokens took 4 % longer, of 32 at 16,384 3 % less.)
       st.clear();
 #pragma unroll 1
       for (int i = f0; i < f1; ++i) at_fresh_tile<D, NR>(a, cur.b, h, row0, rows, i * AT_TILE, pr, st);

@@ -33,12 +33,16 @@
 //
 // Bounds, per tile of 128 tokens and D = 128: 784 clocks of the bus; products
 // 1,024 clocks at NC = 128; unpacking 256 conversions, 256 multiplications and 16
-// stores of 16 bytes a thread.  A tile takes about 3,400 clocks: the softmax of its
-// 16,384 scores, about 240 instructions a warp for 32 rows and 32 tokens, is what
-// takes them, by latency rather than by any unit's rate.  (With 64 rows a thread, in
-// eight warps, it was 4,300: half as many warps to wait with, and 13 KB of code.)
-// 64 sequences of 128 rows at 2,048 tokens take 248 us, where the products at the
-// rate of a large library product would take 37.
+// stores of 16 bytes a thread.  A cached tile takes 1.75 us, 3,600 clocks (32 trees of
+// 64 nodes without fresh entries, 8,192 tokens against 4,096: 473 and 285 us, 108 tiles
+// of a CTA apart): the softmax of its 16,384 scores, about 240 instructions a warp for
+// 32 rows and 32 tokens, is what takes them, by latency rather than by any unit's rate.
+// (With 64 rows a thread, in eight warps, it was a quarter more: half as many warps to
+// wait with, and 13 KB of code.)  That is 189 of the 285 us; the other 96 are the 3.4
+// triples of a CTA, whose queries, first references and ends pass through it one after
+// the other, and the call.  The trees' own entries add 50.  64 sequences of 128 rows at
+// 2,048 tokens take 189 us without fresh entries and 236 with them, where the products
+// at the rate of a large library product would take 37.
 //
 // The fresh entries are bf16 with bf16's range, and so are their products: the queries
 // stay as they are until a triple's first cached tile, keys and values go to their
@@ -262,7 +266,7 @@ __device__ __forceinline__ uint32_t tc_swz(uint32_t o) {
 
 // (Functions that are not inlined and that run for every triple take values, not the
 // kernel's arguments by reference: those are read like global memory, at a few
-// hundred clocks a time.  Chunks of 1,024 tokens took 475 us with the reference.)
+// hundred clocks a time.  Chunks of 1,024 tokens took a fifth longer with the reference.)
 
 // ---------------------------------------------------------------------------
 // the list of tiles of a CTA, walked alike by all roles

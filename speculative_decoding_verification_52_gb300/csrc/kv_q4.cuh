@@ -61,10 +61,9 @@ __device__ __forceinline__ float q4_sixth(float x) {
 // code as the exact quotient: x has 8 significant bits and t * s at most 7 for
 // each border t between two codes, so x / s either is t, and the rounding
 // restores it, or differs from t by at least t * 2^-8 >= 2^-10, twice the
-// rounding.  (Divisions cost about ten instructions each, and with them the kernel
-// would be bound by those and not by memory: 32,001 tokens of 8 heads of 128 take
-// 33.4 us, 5.0 TB/s, and took 37.5 with two divisions a group.)  The sign of a zero
-// that the rounding loses is put back.
+// rounding.  (Divisions cost about ten instructions each: 32,001 tokens of 8 heads of
+// 128 take 30.7 us, 5.5 TB/s, issue slots 78 % used, and took an eighth longer with two
+// divisions a group.)  The sign of a zero that the rounding loses is put back.
 __device__ __forceinline__ void q4_group(const uint4& lo, const uint4& hi, float mul, uint2& codes, uint32_t& scale) {
   const uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
   uint32_t m = bf16x2_abs(w[0]);
@@ -144,9 +143,9 @@ __global__ void __launch_bounds__(Q4_THREADS) kv_store_q4_kernel(const KvQ4Args 
   q4_put<D>(blk, in_page % Q4_BLOCK, g, true, codes, scale);
 }
 
-// Accepted drafts into the pages behind lengths[b].  A warp per sequence and
-// kv head (a CTA per sequence takes the heads in turn): the request is checked
-// by the CTA first, as a whole, so that a refused one changes nothing.
+// Accepted drafts into the pages behind lengths[b].  One CTA or more a sequence, whose
+// threads take a group each, key and value; every CTA checks the request first, as a
+// whole, so that a refused one changes nothing.
 template <int D>
 __global__ void __launch_bounds__(Q4_THREADS) kv_commit_q4_kernel(const KvQ4Args a) {
   constexpr int GR = D / 16;

@@ -64,7 +64,7 @@ spec_status_t launch_join(const DevInfo& di, const AttendArgs& a, int grid, int 
   cfg.blockDim = dim3(ATJ_THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];   // starts beside the attention's last CTAs and waits for them (12.1 -> 11.0 us a call for one token)
+  cudaLaunchAttribute attr[1];   // starts beside the attention's last CTAs and waits for them (a tenth less for one token)
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
@@ -171,11 +171,14 @@ struct AttendPlan {
   int size;       // NR of attend_q4_kernel (rows / 8 of a tile), NC of attend_q4_tc_kernel
   size_t floats;  // of the workspace
 };
-// Up to how many rows attend_q4_kernel is taken, against the tensor cores' kernel.  256
-// sequences at 2,048 tokens (and 32 at 8,192): D = 128, 48 rows (two tiles of 24) 546 us
-// against 771, 64 rows (two of 32) 689 against 773 (305 against 269); D = 64, 72 rows
-// (three of 24) 564 against 783 (240 against 281), 96 rows (three of 32) 724 against 783
-// (302 against 287).
+// Up to how many rows attend_q4_kernel is taken, against the tensor cores' kernel, whose
+// time hardly depends on the rows of a tile.  256 sequences at 2,048 tokens, and 32 at
+// 8,192, with fresh entries: D = 128, 48 rows (two tiles of 24) 508 us against 735, and
+// 244 against 225; 56 rows (two of 32) 640 against 730, and 298 against 224; 64 rows 648
+// against 732, and 304 against 226.  D = 64, 72 rows (three of 24) 523 against 746, and
+// 237 against 249; 80 rows (three of 32) 661 against 742, and 299 against 250.  So up to
+// the rows that tiles of 24 hold: beyond them one loses more with long contexts than it
+// gains with many short ones.
 constexpr int kFewRows128 = 48, kFewRows64 = 72;
 AttendPlan attend_plan(int B, int rows, int D) {
   AttendPlan p{};
