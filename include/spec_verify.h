@@ -481,6 +481,126 @@ spec_status_t spec_adjust_logits(const void *logits, spec_dtype_t dtype, const i
                                  const float *bias_values, const uint32_t *allowed, int B, int R, int V, int H, int Nt,
                                  int M, void *out, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Steps after a verification: what the emitted tokens' probabilities were, and a
+ * cache that keeps to a budget by dropping the tokens that attention passes over.
+ * A step of such a loop goes on with
+ *   spec_token_logprobs, spec_kv_commit_q4 -> spec_kv_weigh_q4 ->
+ *   spec_kv_evict_plan -> spec_kv_move_q4 (in every layer) -> spec_page_trim.
+ * Beside the cache a layer has weights [num_pages, Hkv, page_tokens] float32 and
+ * positions [num_pages, Hkv, page_tokens] int32, by the same slots: what attention
+ * has given to the token that a kv head keeps there, and which token that is.
+ * (Keys carry their positions; attention over the cache asks for no order.)
+ * ------------------------------------------------------------------------- */
+
+/* Log probabilities of given tokens, with ranks, entropies and alternatives.
+ *
+ *   logits [B, R, V] (dtype), e.g. those that were verified.
+ *   tokens [B, M] int32, e.g. out_tokens of spec_verify_*; a negative token: the
+ *       place has none, and its row is not read.
+ *   path [B, W] int32 or NULL: the rows of the tokens, e.g. out_path of
+ *       spec_verify_tree_greedy: token m > 0 belongs to row path[b, m - 1], token 0
+ *       to row 0 (W >= M - 1).  NULL: token m belongs to row m (R >= M).
+ *   temperature: 1e-4 and up.
+ *   logprobs [B, M] float32 (written): log softmax(row / temperature)[token].
+ *   entropy [B, M] float32 (written) or NULL: of that distribution, in nats.
+ *   ranks [B, M] int32 (written) or NULL: 1 + the tokens before the given one, in
+ *       the order of larger logits, then smaller tokens.
+ *   top_tokens int32, top_logprobs float32 [B, M, top_n] (written; may be NULL for
+ *       top_n = 0): the first top_n tokens of that order and their log
+ *       probabilities; -1 and -inf where fewer have a finite one.
+ *
+ * Logits of -2^100 and below (masks of a type's lowest value) count as -inf, those
+ * of 2^100 and above as +inf.  An invalid row (NaN, +inf, nothing finite), a token
+ * of V or more, a path entry outside [0, R): NaN, ranks and tokens -1.  A place
+ * without a token: 0, rank 0, tokens -1 with -inf.  Limits: top_n <= 32, V <= 2^30. */
+spec_status_t spec_token_logprobs(const void *logits, spec_dtype_t dtype, const int32_t *tokens, const int32_t *path,
+                                  float temperature, int B, int R, int V, int M, int W, int top_n, float *logprobs,
+                                  float *entropy, int32_t *ranks, int32_t *top_tokens, float *top_logprobs,
+                                  void *stream);
+
+/* The weight that a step's committed rows gave to each cached token, added up.
+ *
+ *   q [B, N, Hq, D] bf16, lse [B, N, Hq] float32: spec_attend_q4's.
+ *   path [B, W] int32 or NULL, count [B] int32 or NULL: the nodes that were
+ *       committed, as for spec_kv_commit_q4: the first count[b] entries of the path,
+ *       or nodes 0, 1, ...; a NULL count means all of them (W or N).
+ *   cache, block_table [B, max_pages]: with the committed entries in their places.
+ *   lengths [B] int32: the cached tokens before the commit.  Row i (the i-th
+ *       committed) sees the positions 0 .. lengths[b] + i.
+ *   weights [num_pages, Hkv, page_tokens] float32, new_weights the same (written;
+ *       may be weights itself, must not overlap it otherwise):
+ *         new = decay * old + sum over rows i that see the token, and over the query
+ *         heads of its kv head, of exp(scale * q_i.k - lse_i);
+ *       the tokens that were committed have no old weight.  k is what the cache
+ *       holds.  Slots of no token of the batch are left as they are.
+ *   positions [num_pages, Hkv, page_tokens] int32 (written) or NULL: the i-th
+ *       committed token's slots get first_positions[b] + i (first_positions [B] int32,
+ *       or NULL: lengths[b] + i).
+ *
+ * A row without a finite lse, and a score that is a NaN, add nothing.  Nothing is done for a
+ * sequence whose count is negative, or whose lengths, count or path spec_kv_commit_q4
+ * would refuse; tokens on a page outside the cache are passed over.  Different
+ * sequences' tokens must lie in different slots.
+ * Limits: 1 <= N, W <= 1024, B <= 4096, Hq a multiple of Hkv, Hq / Hkv <= 64,
+ * num_pages * page_tokens and max_pages * page_tokens below 2^31. */
+spec_status_t spec_kv_weigh_q4(const void *q, const float *lse, const int32_t *path, const int32_t *count,
+                               const void *cache, const int32_t *block_table, const int32_t *lengths,
+                               const int32_t *first_positions, int B, int N, int W, int Hq, int Hkv, int D,
+                               int page_tokens, int num_pages, int max_pages, int k_shift, float scale, float decay,
+                               const float *weights, float *new_weights, int32_t *positions, void *stream);
+
+/* Which tokens stay when sequences are cut to their budgets, and the moves that
+ * bring the others' places to the end.
+ *
+ *   weights, positions, block_table, lengths [B] int32: as above.
+ *   budgets [B] int32: tokens that each kv head of sequence b keeps; a negative one,
+ *       or one not below lengths[b]: all of them.
+ *   next_positions [B] int32: the position of the sequence's next token.
+ *   sinks, recent: tokens of a position below sinks, or of next_positions[b] - recent
+ *       and above, stay before all others.
+ *   moves [B, Hkv, max_moves, 2] int32 (written, 8-byte aligned): pairs of slots, from
+ *       and to; what is behind a head's moves is left as it is.
+ *   move_counts [B, Hkv] int32 (written), new_lengths [B] int32 (written, not lengths).
+ *
+ * Each head keeps the tokens of the largest weights (NaN counts as the least; equal
+ * ones: the lower place).  A token kept at a place (an index in the sequence) below
+ * the budget is not touched; the j-th that is kept at a place behind goes to the j-th
+ * place below that becomes free.  Weights, positions and the cache are not written.
+ * new_lengths is -1, and there are no moves, for a sequence that is to be cut and
+ * whose length is negative or passes its table, that has a page id outside the cache,
+ * or for which min(budget, length - budget) exceeds max_moves. */
+spec_status_t spec_kv_evict_plan(const float *weights, const int32_t *positions, const int32_t *block_table,
+                                 const int32_t *lengths, const int32_t *budgets, const int32_t *next_positions, int B,
+                                 int Hkv, int page_tokens, int num_pages, int max_pages, int sinks, int recent,
+                                 int max_moves, int32_t *moves, int32_t *move_counts, int32_t *new_lengths,
+                                 void *stream);
+
+/* A plan's moves: entries of the 4-bit cache from slot to slot, each kv head's by its
+ * own list, and with them weights and positions (either may be NULL).
+ *
+ *   moves [B, Hkv, max_moves, 2], move_counts [B, Hkv] int32: spec_kv_evict_plan's, or
+ *       others in which no slot that a head's move goes to is in another of its moves.
+ * A move with a slot outside the cache is left out. */
+spec_status_t spec_kv_move_q4(void *cache, float *weights, int32_t *positions, const int32_t *moves,
+                              const int32_t *move_counts, int B, int Hkv, int D, int page_tokens, int num_pages,
+                              int max_moves, void *stream);
+
+/* Pages that sequences no longer need, back to the pool of spec_page_map.
+ *
+ *   tokens [B] int32: the tokens that sequence b keeps pages for; those behind the
+ *       first ceil(tokens / page_tokens) of its held[b] pages are given back, in
+ *       sequence order, behind the ring's free ones.
+ *   held, ring (in/out), ring_state, block_table: as for spec_page_map.
+ *   new_held [B], new_ring_state [2] int32 (written; not the inputs' buffers), status
+ *       [B] int32 (written): 0; -1 for negative tokens, held outside [0, max_pages], a
+ *       ring_state outside the ring; -3 when the ring has no room.  A refused sequence
+ *       keeps its pages.
+ * Limits: ring_size * page_tokens and max_pages * page_tokens below 2^31. */
+spec_status_t spec_page_trim(const int32_t *tokens, const int32_t *held, int32_t *ring, const int32_t *ring_state,
+                             const int32_t *block_table, int B, int ring_size, int page_tokens, int max_pages,
+                             int32_t *new_held, int32_t *new_ring_state, int32_t *status, void *stream);
+
 /* Timing hooks for benchmarks: while enabled, each verify call records CUDA
  * events on the call's stream around its kernels (at most max_calls calls are
  * recorded).  spec_profile_end synchronises on the recorded events and returns

@@ -88,6 +88,16 @@ def lib() -> ctypes.CDLL:
             L.spec_debug_attend_stall.restype = I
             L.spec_adjust_logits.argtypes = [P, I] + [P] * 11 + [I] * 6 + [P] * 2
             L.spec_adjust_logits.restype = I
+            L.spec_token_logprobs.argtypes = [P, I, P, P, F] + [I] * 6 + [P] * 6
+            L.spec_token_logprobs.restype = I
+            L.spec_kv_weigh_q4.argtypes = [P] * 8 + [I] * 10 + [F] * 2 + [P] * 4
+            L.spec_kv_weigh_q4.restype = I
+            L.spec_kv_evict_plan.argtypes = [P] * 6 + [I] * 8 + [P] * 4
+            L.spec_kv_evict_plan.restype = I
+            L.spec_kv_move_q4.argtypes = [P] * 5 + [I] * 6 + [P]
+            L.spec_kv_move_q4.restype = I
+            L.spec_page_trim.argtypes = [P] * 5 + [I] * 4 + [P] * 4
+            L.spec_page_trim.restype = I
             L.spec_profile_begin.argtypes = [I]
             L.spec_profile_begin.restype = I
             L.spec_profile_end.argtypes = [P, P, P]
@@ -611,6 +621,148 @@ def spec_adjust_logits(logits, *, out=None, history=None, prompt_lengths=None, h
     if st:
         _check("spec_adjust_logits", st)
     return out
+
+
+# ---------------------------------------------------------------------------
+# steps after a verification
+# ---------------------------------------------------------------------------
+@_serve
+def spec_token_logprobs(logits, tokens, temperature: float = 1.0, *, path=None, top_n: int = 0, logprobs=None, entropy=None,
+                        ranks=None, top_tokens=None, top_logprobs=None, dev=None, stream=None):
+    """Log probabilities of tokens [B, M] int32 (negative: none) under logits [B, R, V]
+    (bf16/f32) at a temperature; token m belongs to row m, or with path [B, W] int32
+    (out_path) to row 0 (m = 0) or path[b, m - 1].  Returns (logprobs, entropy [B, M] f32,
+    ranks [B, M] int32, top_tokens int32, top_logprobs f32 [B, M, top_n])."""
+    if logits.dim() != 3 or tokens.dim() != 2:
+        raise ValueError(f"logits must be [B, R, V] and tokens [B, M], got {tuple(logits.shape)} and {tuple(tokens.shape)}")
+    B, R, V = logits.shape
+    M = tokens.shape[1]
+    i32, f32, two, three = torch.int32, torch.float32, (B, M), (B, M, top_n)
+    new = functools.partial(torch.empty, device=logits.device)
+    if logprobs is None:
+        logprobs = new(two, dtype=f32)
+    if entropy is None:
+        entropy = new(two, dtype=f32)
+    if ranks is None:
+        ranks = new(two, dtype=i32)
+    if top_tokens is None:
+        top_tokens = new(three, dtype=i32)
+    if top_logprobs is None:
+        top_logprobs = new(three, dtype=f32)
+    way = _cols(path, B, "path")
+    st = (_lib or lib()).spec_token_logprobs(
+        _take(logits, "logits", logits.dtype, (B, R, V), dev), _dtype_code(logits), _take(tokens, "tokens", i32, two, dev),
+        _take(path, "path", i32, way, dev), temperature, B, R, V, M, way[1] if way else 0, top_n,
+        _take(logprobs, "logprobs", f32, two, dev), _take(entropy, "entropy", f32, two, dev), _take(ranks, "ranks", i32, two, dev),
+        _take(top_tokens, "top_tokens", i32, three, dev), _take(top_logprobs, "top_logprobs", f32, three, dev), stream)
+    if st:
+        _check("spec_token_logprobs", st)
+    return logprobs, entropy, ranks, top_tokens, top_logprobs
+
+
+@_serve
+def spec_kv_weigh_q4(q, lse, cache, block_table, lengths, weights, *, count=None, path=None, positions=None,
+                     first_positions=None, new_weights=None, scale=None, decay: float = 1.0, k_shift: int = 0, dev=None, stream=None):
+    """Adds to weights [pages, Hkv, page_tokens] f32 what the committed rows of q [B, N, Hq,
+    D] bf16 with lse [B, N, Hq] f32 gave to each cached token: rows path[b, :count[b]], or
+    the first count[b] (None: all); lengths [B] before the commit.  Marks the committed
+    tokens in positions (int32, weights' shape).  In place unless new_weights is given;
+    returns it."""
+    pages, Hkv, P, D = _q4_shape(cache)
+    i32, f32 = torch.int32, torch.float32
+    if q.dim() != 4:
+        raise ValueError(f"q must be [B, N, Hq, D], got {tuple(q.shape)}")
+    B, N, Hq = q.shape[0], q.shape[1], q.shape[2]
+    if new_weights is None:
+        new_weights = weights
+    one, slots = (B,), (pages, Hkv, P)
+    table, way = _cols(block_table, B, "block_table"), _cols(path, B, "path")
+    st = (_lib or lib()).spec_kv_weigh_q4(
+        _take(q, "q", torch.bfloat16, (B, N, Hq, D), dev), _take(lse, "lse", f32, (B, N, Hq), dev), _take(path, "path", i32, way, dev),
+        _take(count, "count", i32, one, dev), _take(cache, "cache", torch.uint8, cache.shape, dev),
+        _take(block_table, "block_table", i32, table, dev), _take(lengths, "lengths", i32, one, dev),
+        _take(first_positions, "first_positions", i32, one, dev), B, N, way[1] if way else 0, Hq, Hkv, D, P, pages, table[1],
+        k_shift, D ** -0.5 if scale is None else scale, decay, _take(weights, "weights", f32, slots, dev),
+        _take(new_weights, "new_weights", f32, slots, dev), _take(positions, "positions", i32, slots, dev), stream)
+    if st:
+        _check("spec_kv_weigh_q4", st)
+    return new_weights
+
+
+@_serve
+def spec_kv_evict_plan(weights, positions, block_table, lengths, budgets, next_positions, *, sinks: int = 0, recent: int = 0,
+                       max_moves=None, moves=None, move_counts=None, new_lengths=None, dev=None, stream=None):
+    """Which tokens each kv head keeps when sequences are cut to budgets [B], and the moves
+    that fill the places below.  weights f32 and positions int32 [pages, Hkv, page_tokens],
+    lengths, next_positions [B] int32; room for max_moves a head (or moves' own).
+    Returns (moves [B, Hkv, max_moves, 2], move_counts [B, Hkv], new_lengths [B]) int32."""
+    if weights.dim() != 3:
+        raise ValueError(f"weights must be [pages, Hkv, page_tokens], got {tuple(weights.shape)}")
+    (pages, Hkv, P), B, i32 = weights.shape, lengths.numel(), torch.int32
+    if moves is not None:
+        if moves.dim() != 4 or max_moves not in (None, moves.shape[2]):
+            raise ValueError(f"moves must be [B, Hkv, max_moves, 2], got {tuple(moves.shape)} with max_moves={max_moves}")
+        max_moves = moves.shape[2]
+    elif max_moves is None:
+        raise ValueError("spec_kv_evict_plan: max_moves or moves is needed")
+    else:
+        moves = torch.empty((B, Hkv, max_moves, 2), dtype=i32, device=weights.device)
+    if move_counts is None:
+        move_counts = torch.empty((B, Hkv), dtype=i32, device=weights.device)
+    if new_lengths is None:
+        new_lengths = torch.empty((B,), dtype=i32, device=weights.device)
+    one, slots, table = (B,), (pages, Hkv, P), _cols(block_table, B, "block_table")
+    st = (_lib or lib()).spec_kv_evict_plan(
+        _take(weights, "weights", torch.float32, slots, dev), _take(positions, "positions", i32, slots, dev),
+        _take(block_table, "block_table", i32, table, dev), _take(lengths, "lengths", i32, one, dev),
+        _take(budgets, "budgets", i32, one, dev), _take(next_positions, "next_positions", i32, one, dev), B, Hkv, P, pages,
+        table[1], sinks, recent, max_moves, _take(moves, "moves", i32, (B, Hkv, max_moves, 2), dev),
+        _take(move_counts, "move_counts", i32, (B, Hkv), dev), _take(new_lengths, "new_lengths", i32, one, dev), stream)
+    if st:
+        _check("spec_kv_evict_plan", st)
+    return moves, move_counts, new_lengths
+
+
+@_serve
+def spec_kv_move_q4(cache, moves, move_counts, *, weights=None, positions=None, dev=None, stream=None):
+    """A plan's moves [B, Hkv, max_moves, 2] int32 (the first move_counts[b, h] of each head)
+    in the 4-bit cache and, given, in weights f32 and positions int32 [pages, Hkv,
+    page_tokens].  Returns the cache."""
+    pages, Hkv, P, D = _q4_shape(cache)
+    if moves.dim() != 4:
+        raise ValueError(f"moves must be [B, Hkv, max_moves, 2], got {tuple(moves.shape)}")
+    B, most, i32, slots = moves.shape[0], moves.shape[2], torch.int32, (pages, Hkv, P)
+    st = (_lib or lib()).spec_kv_move_q4(
+        _take(cache, "cache", torch.uint8, cache.shape, dev), _take(weights, "weights", torch.float32, slots, dev),
+        _take(positions, "positions", i32, slots, dev), _take(moves, "moves", i32, (B, Hkv, most, 2), dev),
+        _take(move_counts, "move_counts", i32, (B, Hkv), dev), B, Hkv, D, P, pages, most, stream)
+    if st:
+        _check("spec_kv_move_q4", st)
+    return cache
+
+
+@_serve
+def spec_page_trim(tokens, held, ring, ring_state, block_table, page_tokens: int, *, new_held=None, new_ring_state=None,
+                   status=None, dev=None, stream=None):
+    """Gives the pages that tokens [B] int32 do not need back to spec_page_map's ring
+    (updated in place).  Returns (new_held [B], new_ring_state [2], status [B]) int32."""
+    i32, B = torch.int32, tokens.numel()
+    new = functools.partial(torch.empty, dtype=i32, device=tokens.device)
+    if new_held is None:
+        new_held = new(B)
+    if new_ring_state is None:
+        new_ring_state = new(2)
+    if status is None:
+        status = new(B)
+    one, table = (B,), _cols(block_table, B, "block_table")
+    st = (_lib or lib()).spec_page_trim(
+        _take(tokens, "tokens", i32, one, dev), _take(held, "held", i32, one, dev), _take(ring, "ring", i32, (ring.numel(),), dev),
+        _take(ring_state, "ring_state", i32, (2,), dev), _take(block_table, "block_table", i32, table, dev), B, ring.numel(),
+        page_tokens, table[1], _take(new_held, "new_held", i32, one, dev), _take(new_ring_state, "new_ring_state", i32, (2,), dev),
+        _take(status, "status", i32, one, dev), stream)
+    if st:
+        _check("spec_page_trim", st)
+    return new_held, new_ring_state, status
 
 
 def spec_profile_begin(max_calls: int):

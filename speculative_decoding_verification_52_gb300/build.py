@@ -1,8 +1,8 @@
 """Build the CUDA library (libspecverify.so) in-tree with nvcc for sm_103a.
 
-Two translation units (verification and its neighbours in spec_verify.cu, the
-paged 4-bit cache and the logit adjustments in serving.cu), compiled in
-parallel; host code is plain C++17, device code targets ``compute_103a`` /
+Three translation units (verification and its neighbours in spec_verify.cu, the
+paged 4-bit cache and the logit adjustments in serving.cu, the steps after a
+verification in after_verify.cu), compiled in parallel; host code is plain C++17, device code targets ``compute_103a`` /
 ``sm_103a`` only.  The result sits next to this file and is
 what the Python binding loads.
 """
@@ -40,7 +40,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
     tmp = LIB + f".tmp{os.getpid()}"
-    units = [os.path.join(CSRC, f) for f in ("spec_verify.cu", "serving.cu")]
+    units = [os.path.join(CSRC, f) for f in ("spec_verify.cu", "serving.cu", "after_verify.cu")]
     cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "--threads", "0", "-Xcompiler", "-fPIC", "-shared",
            "-I", INCLUDE, "-o", tmp, *units]
     if verbose:

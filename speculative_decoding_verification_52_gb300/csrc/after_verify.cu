@@ -1,0 +1,330 @@
+// after_verify.cu -- host side of the steps after a verification declared in
+// include/spec_verify.h: log probabilities of the emitted tokens, weights of the cached
+// tokens, eviction by them (plan, moves).  Argument checks, launch shapes, dispatch;
+// one launch a call on the caller's stream, no sync.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "common.cuh"
+#include "evict.cuh"
+#include "host.cuh"
+#include "spec_verify.h"
+#include "token_logprobs.cuh"
+#include "weigh_q4.cuh"
+
+namespace {
+
+using namespace sv;
+using namespace svh;
+
+constexpr int kMaxShift = 32;
+
+bool q4_dim(int D) { return D == 64 || D == 128; }
+bool below_2g(long long a, long long b) { return a * b < (1LL << 31); }
+
+// what all calls over the cache's slots ask of its sizes
+spec_status_t check_pool(int B, int Hkv, int P, int pages, int max_pages) {
+  if (B < 0 || Hkv < 1 || P < 1 || pages < 1 || max_pages < 1)
+    return fail(SPEC_ERR_INVALID_ARG, "bad sizes B=%d Hkv=%d page_tokens=%d num_pages=%d max_pages=%d", B, Hkv, P, pages, max_pages);
+  if (P % Q4_BLOCK != 0) return fail(SPEC_ERR_INVALID_ARG, "page_tokens=%d is not a multiple of %d", P, Q4_BLOCK);
+  if (!below_2g(P, pages) || !below_2g(max_pages, P))
+    return fail(SPEC_ERR_UNSUPPORTED, "num_pages and max_pages times page_tokens must stay below 2^31");
+  return SPEC_OK;
+}
+
+template <class K, class A>
+spec_status_t launch_cluster(K kern, dim3 grid, int threads, size_t smem, int C, cudaStream_t st, const A& a, const char* what) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(C);
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = C > 1 ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a);
+  return e == cudaSuccess ? SPEC_OK : cuda_fail(e, what);
+}
+
+// ---------------------------------------------------------------------------
+// log probabilities
+// ---------------------------------------------------------------------------
+template <class T, int WARPS, bool TOP>
+spec_status_t launch_logprobs(int dev, const LogprobArgs& a, cudaStream_t st) {
+  auto kern = token_logprobs_kernel<T, WARPS, TOP>;
+  constexpr int TEAMS = LP_THREADS / (32 * WARPS);
+  constexpr size_t smem = sizeof(LpShared<WARPS>) * TEAMS;
+  if (smem > 48 * 1024 && !once_per_device(dev, [&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) == cudaSuccess;
+      }))
+    return fail(SPEC_ERR_CUDA, "log probabilities setup failed: %s", cudaGetErrorString(cudaGetLastError()));
+  const long long places = static_cast<long long>(a.B) * a.M, grid = (places + TEAMS - 1) / TEAMS * a.C;
+  if (grid > 0x7fffffffLL) return fail(SPEC_ERR_UNSUPPORTED, "batch too large for one call");
+  return launch_cluster(kern, dim3(static_cast<unsigned>(grid)), LP_THREADS, smem, a.C, st, a, "log probabilities launch");
+}
+template <class T>
+spec_status_t launch_logprobs(int dev, bool warp, const LogprobArgs& a, cudaStream_t st) {
+  if (warp) return a.top ? launch_logprobs<T, 1, true>(dev, a, st) : launch_logprobs<T, 1, false>(dev, a, st);
+  return a.top ? launch_logprobs<T, 8, true>(dev, a, st) : launch_logprobs<T, 8, false>(dev, a, st);
+}
+
+// ---------------------------------------------------------------------------
+// weights
+// ---------------------------------------------------------------------------
+template <int D, int NR>
+spec_status_t launch_weigh(const DevInfo& di, int dev, const WeighArgs& a, cudaStream_t st) {
+  auto kern = weigh_q4_kernel<D, NR>;
+  const size_t smem = 8 * (static_cast<size_t>(a.B) + 1) + 4 * static_cast<size_t>(a.B);
+  if (!once_per_device(dev, [&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 12 * WG_MAX_B + 8) == cudaSuccess;
+      }))
+    return fail(SPEC_ERR_CUDA, "weighing setup failed: %s", cudaGetErrorString(cudaGetLastError()));
+  kern<<<static_cast<unsigned>(di.sms * wg_ctas(NR)), WG_THREADS, smem, st>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? SPEC_OK : cuda_fail(e, "weighing launch");
+}
+template <int D>
+spec_status_t launch_weigh(int NR, const DevInfo& di, int dev, const WeighArgs& a, cudaStream_t st) {
+  switch (NR) {
+    case 1: return launch_weigh<D, 1>(di, dev, a, st);
+    case 2: return launch_weigh<D, 2>(di, dev, a, st);
+    case 3: return launch_weigh<D, 3>(di, dev, a, st);
+    default: return launch_weigh<D, 4>(di, dev, a, st);
+  }
+}
+
+}  // namespace
+
+extern "C" {
+
+spec_status_t spec_token_logprobs(const void* logits, spec_dtype_t dtype, const int32_t* tokens, const int32_t* path,
+                                  float temperature, int B, int R, int V, int M, int W, int top_n, float* logprobs,
+                                  float* entropy, int32_t* ranks, int32_t* top_tokens, float* top_logprobs, void* stream) {
+  try {
+    if (B < 0 || R < 1 || V < 1 || M < 1 || top_n < 0)
+      return fail(SPEC_ERR_INVALID_ARG, "bad sizes B=%d R=%d V=%d M=%d top_n=%d", B, R, V, M, top_n);
+    if (V > (1 << 30)) return fail(SPEC_ERR_UNSUPPORTED, "V=%d beyond 2^30", V);
+    if (top_n > LP_MAX_TOP) return fail(SPEC_ERR_UNSUPPORTED, "top_n=%d beyond %d", top_n, LP_MAX_TOP);
+    if (!dtype_ok(dtype)) return fail(SPEC_ERR_INVALID_ARG, "bad dtype");
+    if (!(temperature > 0.f) || !std::isfinite(temperature)) return fail(SPEC_ERR_INVALID_ARG, "temperature must be positive and finite");
+    if (temperature < 1e-4f) return fail(SPEC_ERR_UNSUPPORTED, "temperature %g below 1e-4", static_cast<double>(temperature));
+    if (path ? W < M - 1 : R < M) return fail(SPEC_ERR_INVALID_ARG, "M=%d tokens for %s of %d", M, path ? "a path" : "rows", path ? W : R);
+    if (static_cast<long long>(B) * M > 0x7fffffffLL) return fail(SPEC_ERR_UNSUPPORTED, "batch too large for one call");
+    if (B == 0) return SPEC_OK;
+    if (!logits || !tokens || !logprobs) return fail(SPEC_ERR_INVALID_ARG, "NULL logits/tokens/logprobs");
+    if (top_n > 0 && (!top_tokens || !top_logprobs)) return fail(SPEC_ERR_INVALID_ARG, "NULL top_tokens/top_logprobs");
+    if (reinterpret_cast<uintptr_t>(logits) % esz_of(dtype)) return fail(SPEC_ERR_INVALID_ARG, "logits must be aligned to their elements");
+    int dev;
+    DevInfo di;
+    spec_status_t s = device_info(di, dev);
+    if (s != SPEC_OK) return s;
+    LogprobArgs a{};
+    a.logits = static_cast<const unsigned char*>(logits);
+    a.tokens = tokens;
+    a.path = path;
+    a.B = B;
+    a.R = R;
+    a.V = V;
+    a.M = M;
+    a.W = W;
+    a.top = top_n;
+    a.c = static_cast<float>(1.4426950408889634 / static_cast<double>(temperature));
+    a.logprobs = logprobs;
+    a.entropy = entropy;
+    a.ranks = ranks;
+    a.top_tokens = top_tokens;
+    a.top_logprobs = top_logprobs;
+    // A warp a row up to 8 KB; else a CTA, and a cluster of CTAs where the places alone
+    // do not fill the device.
+    const long long places = static_cast<long long>(B) * M, bytes = static_cast<long long>(V) * esz_of(dtype);
+    const bool warp = bytes <= 8192;
+    a.C = 1;
+    if (!warp)
+      while (a.C < 8 && places * a.C < 4LL * di.sms && bytes / (2 * a.C) >= 8192) a.C *= 2;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    prof_mark(0, st);
+    s = dtype == SPEC_BF16 ? launch_logprobs<BF16T>(dev, warp, a, st) : launch_logprobs<F32T>(dev, warp, a, st);
+    if (s != SPEC_OK) return s;
+    prof_mark(1, st);
+    prof_mark(2, st);
+    return SPEC_OK;
+  } catch (...) {
+    return fail(SPEC_ERR_CUDA, "unexpected host exception");
+  }
+}
+
+spec_status_t spec_kv_weigh_q4(const void* q, const float* lse, const int32_t* path, const int32_t* count, const void* cache,
+                               const int32_t* block_table, const int32_t* lengths, const int32_t* first_positions, int B,
+                               int N, int W, int Hq, int Hkv, int D, int page_tokens, int num_pages, int max_pages,
+                               int k_shift, float scale, float decay, const float* weights, float* new_weights,
+                               int32_t* positions, void* stream) {
+  try {
+    if (!q4_dim(D)) return fail(SPEC_ERR_UNSUPPORTED, "D=%d: the 4-bit cache takes 64 or 128", D);
+    spec_status_t s = check_pool(B, Hkv, page_tokens, num_pages, max_pages);
+    if (s != SPEC_OK) return s;
+    if (N < 1 || N > SPEC_MAX_TREE_NODES || (path && W < 1))
+      return fail(SPEC_ERR_INVALID_ARG, "bad sizes N=%d W=%d (N in [1, %d])", N, W, SPEC_MAX_TREE_NODES);
+    if (Hq < 1 || Hq % Hkv != 0) return fail(SPEC_ERR_INVALID_ARG, "Hq=%d is not a multiple of Hkv=%d", Hq, Hkv);
+    if (Hq / Hkv > 64) return fail(SPEC_ERR_UNSUPPORTED, "%d query heads to a kv head: at most 64", Hq / Hkv);
+    if (B > WG_MAX_B) return fail(SPEC_ERR_UNSUPPORTED, "B=%d beyond %d", B, WG_MAX_B);
+    if (path && W > SPEC_MAX_TREE_NODES) return fail(SPEC_ERR_UNSUPPORTED, "W=%d beyond %d", W, SPEC_MAX_TREE_NODES);
+    if (std::abs(k_shift) > kMaxShift) return fail(SPEC_ERR_INVALID_ARG, "k_shift %d outside [-%d, %d]", k_shift, kMaxShift, kMaxShift);
+    if (!std::isfinite(scale) || !std::isfinite(decay)) return fail(SPEC_ERR_INVALID_ARG, "scale and decay must be finite");
+    if (B == 0) return SPEC_OK;
+    if (!q || !lse || !cache || !block_table || !lengths || !weights || !new_weights)
+      return fail(SPEC_ERR_INVALID_ARG, "NULL q/lse/cache/block_table/lengths/weights/new_weights");
+    if (!aligned16(q) || !aligned16(cache)) return fail(SPEC_ERR_INVALID_ARG, "q and cache must be 16-byte aligned");
+    int dev;
+    DevInfo di;
+    s = device_info(di, dev);
+    if (s != SPEC_OK) return s;
+    WeighArgs a{};
+    a.q = static_cast<const uint16_t*>(q);
+    a.lse = lse;
+    a.path = path;
+    a.count = count;
+    a.cache = static_cast<const unsigned char*>(cache);
+    a.table = block_table;
+    a.lengths = lengths;
+    a.first = first_positions;
+    a.weights = weights;
+    a.new_weights = new_weights;
+    a.positions = positions;
+    a.B = B;
+    a.N = N;
+    a.PW = path ? W : 0;
+    a.most = path ? W : N;
+    a.G = Hq / Hkv;
+    a.Hkv = Hkv;
+    a.P = page_tokens;
+    a.pages = num_pages;
+    a.W = max_pages;
+    a.scale_log2 = static_cast<float>(1.4426950408889634 * static_cast<double>(scale));
+    a.k_mul = std::ldexp(1.f, k_shift);
+    a.decay = decay;
+    const int rows = a.most * a.G, tiles = ceil_div(rows, 32), NR = ceil_div(ceil_div(rows, 8), tiles);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    prof_mark(0, st);
+    s = D == 128 ? launch_weigh<128>(NR, di, dev, a, st) : launch_weigh<64>(NR, di, dev, a, st);
+    if (s != SPEC_OK) return s;
+    prof_mark(1, st);
+    prof_mark(2, st);
+    return SPEC_OK;
+  } catch (...) {
+    return fail(SPEC_ERR_CUDA, "unexpected host exception");
+  }
+}
+
+spec_status_t spec_kv_evict_plan(const float* weights, const int32_t* positions, const int32_t* block_table,
+                                 const int32_t* lengths, const int32_t* budgets, const int32_t* next_positions, int B,
+                                 int Hkv, int page_tokens, int num_pages, int max_pages, int sinks, int recent,
+                                 int max_moves, int32_t* moves, int32_t* move_counts, int32_t* new_lengths, void* stream) {
+  try {
+    spec_status_t s = check_pool(B, Hkv, page_tokens, num_pages, max_pages);
+    if (s != SPEC_OK) return s;
+    if (sinks < 0 || recent < 0 || max_moves < 1)
+      return fail(SPEC_ERR_INVALID_ARG, "bad sizes sinks=%d recent=%d max_moves=%d", sinks, recent, max_moves);
+    if (B == 0) return SPEC_OK;
+    if (!weights || !positions || !block_table || !lengths || !budgets || !next_positions || !moves || !move_counts || !new_lengths)
+      return fail(SPEC_ERR_INVALID_ARG, "NULL pointer argument");
+    if (new_lengths == lengths) return fail(SPEC_ERR_INVALID_ARG, "new_lengths must not be lengths");
+    if (reinterpret_cast<uintptr_t>(moves) & 7u) return fail(SPEC_ERR_INVALID_ARG, "moves must be 8-byte aligned");
+    int dev;
+    DevInfo di;
+    s = device_info(di, dev);
+    if (s != SPEC_OK) return s;
+    PlanArgs a{};
+    a.weights = weights;
+    a.positions = positions;
+    a.table = block_table;
+    a.lengths = lengths;
+    a.budgets = budgets;
+    a.next = next_positions;
+    a.B = B;
+    a.Hkv = Hkv;
+    a.P = page_tokens;
+    a.pages = num_pages;
+    a.W = max_pages;
+    a.max_moves = max_moves;
+    a.sinks = sinks;
+    a.recent = recent;
+    a.moves = moves;
+    a.counts = move_counts;
+    a.new_lengths = new_lengths;
+    // a cluster where the heads alone do not fill the device and the table has room for long sequences
+    const long long pairs = static_cast<long long>(B) * Hkv, most = static_cast<long long>(max_pages) * page_tokens;
+    a.C = 1;
+    while (a.C < 8 && pairs * a.C < 2LL * di.sms && most / a.C > 2048) a.C *= 2;
+    if (pairs * a.C > 0x7fffffffLL) return fail(SPEC_ERR_UNSUPPORTED, "batch too large for one call");
+    a.cap = static_cast<int>(std::min<long long>(EV_CAP, (most / Q4_BLOCK + a.C) / a.C * Q4_BLOCK));
+    const size_t smem = 4 * (static_cast<size_t>(a.C > 1 ? 2 : 1) * EV_BINS + a.cap);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    prof_mark(0, st);
+    auto kern = a.C > 1 ? evict_plan_kernel<true> : evict_plan_kernel<false>;
+    if (!once_per_device(dev, [&] {
+          const int all = 4 * (2 * EV_BINS + EV_CAP);
+          return cudaFuncSetAttribute(evict_plan_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, all) == cudaSuccess &&
+                 cudaFuncSetAttribute(evict_plan_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, all) == cudaSuccess;
+        }))
+      return fail(SPEC_ERR_CUDA, "eviction plan setup failed: %s", cudaGetErrorString(cudaGetLastError()));
+    s = launch_cluster(kern, dim3(static_cast<unsigned>(pairs * a.C)), EV_THREADS, smem, a.C, st, a, "eviction plan launch");
+    if (s != SPEC_OK) return s;
+    prof_mark(1, st);
+    prof_mark(2, st);
+    return SPEC_OK;
+  } catch (...) {
+    return fail(SPEC_ERR_CUDA, "unexpected host exception");
+  }
+}
+
+spec_status_t spec_kv_move_q4(void* cache, float* weights, int32_t* positions, const int32_t* moves, const int32_t* move_counts,
+                              int B, int Hkv, int D, int page_tokens, int num_pages, int max_moves, void* stream) {
+  try {
+    if (!q4_dim(D)) return fail(SPEC_ERR_UNSUPPORTED, "D=%d: the 4-bit cache takes 64 or 128", D);
+    spec_status_t s = check_pool(B, Hkv, page_tokens, num_pages, 1);
+    if (s != SPEC_OK) return s;
+    if (max_moves < 1) return fail(SPEC_ERR_INVALID_ARG, "max_moves=%d must be positive", max_moves);
+    const long long pairs = static_cast<long long>(B) * Hkv;
+    if (pairs > 0x7fffffffLL) return fail(SPEC_ERR_UNSUPPORTED, "batch too large for one call");
+    if (B == 0) return SPEC_OK;
+    if (!cache || !moves || !move_counts) return fail(SPEC_ERR_INVALID_ARG, "NULL cache/moves/move_counts");
+    if (!aligned16(cache)) return fail(SPEC_ERR_INVALID_ARG, "cache must be 16-byte aligned");
+    if (reinterpret_cast<uintptr_t>(moves) & 7u) return fail(SPEC_ERR_INVALID_ARG, "moves must be 8-byte aligned");
+    int dev;
+    DevInfo di;
+    s = device_info(di, dev);
+    if (s != SPEC_OK) return s;
+    MoveArgs a{};
+    a.cache = static_cast<unsigned char*>(cache);
+    a.weights = weights;
+    a.positions = positions;
+    a.moves = moves;
+    a.counts = move_counts;
+    a.Hkv = Hkv;
+    a.P = page_tokens;
+    a.pages = num_pages;
+    a.max_moves = max_moves;
+    // enough CTAs a head for its longest list, no more than fill the device
+    const long long want = ceil_div(max_moves, MV_THREADS / 16), room = std::max<long long>(1, di.sms * 16 / pairs);
+    const dim3 grid(static_cast<unsigned>(pairs), static_cast<unsigned>(std::min(std::min(want, room), 65535LL)));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    prof_mark(0, st);
+    if (D == 128) kv_move_q4_kernel<128><<<grid, MV_THREADS, 0, st>>>(a);
+    else kv_move_q4_kernel<64><<<grid, MV_THREADS, 0, st>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "kv move launch");
+    prof_mark(1, st);
+    prof_mark(2, st);
+    return SPEC_OK;
+  } catch (...) {
+    return fail(SPEC_ERR_CUDA, "unexpected host exception");
+  }
+}
+
+}  // extern "C"

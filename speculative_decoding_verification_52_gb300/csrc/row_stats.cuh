@@ -49,17 +49,6 @@ struct RowStatsArgs {
   float* tv;
 };
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-
-__device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 // store v into the same shared-memory slot of CTA `peer` of this cluster
 __device__ __forceinline__ void st_peer_f32(float* local_slot, uint32_t peer, float v) {
   uint32_t remote;

@@ -1,5 +1,5 @@
 // serving.cu -- host side of the serving steps around verification declared in
-// include/spec_verify.h: the paged 4-bit cache (page map, store, commit,
+// include/spec_verify.h: the paged 4-bit cache (page map and trim, store, commit,
 // attention) and the logit adjustments.  Argument checks, launch shapes,
 // dispatch; one or two launches a call on the caller's stream, no sync.
 #include <cuda_runtime.h>
@@ -15,6 +15,7 @@
 #include "host.cuh"
 #include "kv_q4.cuh"
 #include "page_map.cuh"
+#include "page_trim.cuh"
 #include "spec_verify.h"
 
 namespace {
@@ -335,6 +336,51 @@ spec_status_t spec_page_map(const int32_t* lengths, const int32_t* count, const 
     page_map_kernel<<<grid, PM_THREADS, 0, st>>>(a);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return cuda_fail(e, "page map launch");
+    prof_mark(1, st);
+    prof_mark(2, st);
+    return SPEC_OK;
+  } catch (...) {
+    return fail(SPEC_ERR_CUDA, "unexpected host exception");
+  }
+}
+
+spec_status_t spec_page_trim(const int32_t* tokens, const int32_t* held, int32_t* ring, const int32_t* ring_state,
+                             const int32_t* block_table, int B, int ring_size, int page_tokens, int max_pages,
+                             int32_t* new_held, int32_t* new_ring_state, int32_t* status, void* stream) {
+  try {
+    if (B < 0 || ring_size < 1 || page_tokens < 1 || max_pages < 1)
+      return fail(SPEC_ERR_INVALID_ARG, "bad sizes B=%d ring_size=%d page_tokens=%d max_pages=%d", B, ring_size, page_tokens, max_pages);
+    if (!below_2g(ring_size, page_tokens) || !below_2g(max_pages, page_tokens))
+      return fail(SPEC_ERR_UNSUPPORTED, "ring_size and max_pages times page_tokens must stay below 2^31");
+    if (!ring || !ring_state || !new_ring_state || (B > 0 && (!tokens || !held || !block_table || !new_held || !status)))
+      return fail(SPEC_ERR_INVALID_ARG, "NULL pointer argument");
+    if ((B > 0 && new_held == held) || new_ring_state == ring_state)
+      return fail(SPEC_ERR_INVALID_ARG, "new_held / new_ring_state must not be held / ring_state");
+    int dev;
+    DevInfo di;
+    spec_status_t s = device_info(di, dev);
+    if (s != SPEC_OK) return s;
+    PageTrimArgs a{};
+    a.tokens = tokens;
+    a.held = held;
+    a.ring = ring;
+    a.ring_state = ring_state;
+    a.table = block_table;
+    a.B = B;
+    a.F = ring_size;
+    a.P = page_tokens;
+    a.W = max_pages;
+    a.new_held = new_held;
+    a.new_ring_state = new_ring_state;
+    a.status = status;
+    // up to eight pages a thread, no more CTAs than SMs
+    const long long most = std::min<long long>(static_cast<long long>(B) * max_pages, ring_size);
+    const unsigned grid = static_cast<unsigned>(std::max<long long>(1, std::min<long long>(di.sms, (most + 8 * PM_THREADS - 1) / (8 * PM_THREADS))));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    prof_mark(0, st);
+    page_trim_kernel<<<grid, PM_THREADS, 0, st>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return cuda_fail(e, "page trim launch");
     prof_mark(1, st);
     prof_mark(2, st);
     return SPEC_OK;
