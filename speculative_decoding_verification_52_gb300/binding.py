@@ -637,24 +637,24 @@ def spec_token_logprobs(logits, tokens, temperature: float = 1.0, *, path=None, 
         raise ValueError(f"logits must be [B, R, V] and tokens [B, M], got {tuple(logits.shape)} and {tuple(tokens.shape)}")
     B, R, V = logits.shape
     M = tokens.shape[1]
-    i32, f32, two, three = torch.int32, torch.float32, (B, M), (B, M, top_n)
-    new = functools.partial(torch.empty, device=logits.device)
-    if logprobs is None:
-        logprobs = new(two, dtype=f32)
-    if entropy is None:
-        entropy = new(two, dtype=f32)
-    if ranks is None:
-        ranks = new(two, dtype=i32)
-    if top_tokens is None:
-        top_tokens = new(three, dtype=i32)
-    if top_logprobs is None:
-        top_logprobs = new(three, dtype=f32)
+    i32, f32, two, three, n, m = torch.int32, torch.float32, (B, M), (B, M, top_n), B * M, top_n
+    if logprobs is entropy is ranks is top_tokens is top_logprobs is None and m >= 0:   # parts of one allocation
+        new = torch.empty(n * (3 + 2 * m), dtype=f32, device=logits.device)
+        at = new.data_ptr()
+        to = (at, at + 4 * n, at + 4 * n * (2 + m), at + 4 * n * (3 + m), at + 8 * n)
+        logprobs, entropy, top_logprobs = new.as_strided(two, (M, 1)), new.as_strided(two, (M, 1), n), new.as_strided(three, (M * m, m, 1), 2 * n)
+        whole = new.view(i32)
+        ranks, top_tokens = whole.as_strided(two, (M, 1), n * (2 + m)), whole.as_strided(three, (M * m, m, 1), n * (3 + m))
+    else:
+        logprobs, entropy, ranks, top_tokens, top_logprobs = out = tuple(
+            torch.empty(shape, dtype=dt, device=logits.device) if t is None else t for t, shape, dt in (
+                (logprobs, two, f32), (entropy, two, f32), (ranks, two, i32), (top_tokens, three, i32), (top_logprobs, three, f32)))
+        to = tuple(_take(t, name, dt, shape, dev) for t, name, dt, shape in zip(
+            out, ("logprobs", "entropy", "ranks", "top_tokens", "top_logprobs"), (f32, f32, i32, i32, f32), (two, two, two, three, three)))
     way = _cols(path, B, "path")
     st = (_lib or lib()).spec_token_logprobs(
         _take(logits, "logits", logits.dtype, (B, R, V), dev), _dtype_code(logits), _take(tokens, "tokens", i32, two, dev),
-        _take(path, "path", i32, way, dev), temperature, B, R, V, M, way[1] if way else 0, top_n,
-        _take(logprobs, "logprobs", f32, two, dev), _take(entropy, "entropy", f32, two, dev), _take(ranks, "ranks", i32, two, dev),
-        _take(top_tokens, "top_tokens", i32, three, dev), _take(top_logprobs, "top_logprobs", f32, three, dev), stream)
+        _take(path, "path", i32, way, dev), temperature, B, R, V, M, way[1] if way else 0, top_n, *to, stream)
     if st:
         _check("spec_token_logprobs", st)
     return logprobs, entropy, ranks, top_tokens, top_logprobs
@@ -707,11 +707,14 @@ def spec_kv_evict_plan(weights, positions, block_table, lengths, budgets, next_p
         raise ValueError("spec_kv_evict_plan: max_moves or moves is needed")
     else:
         moves = torch.empty((B, Hkv, max_moves, 2), dtype=i32, device=weights.device)
-    if move_counts is None:
-        move_counts = torch.empty((B, Hkv), dtype=i32, device=weights.device)
-    if new_lengths is None:
-        new_lengths = torch.empty((B,), dtype=i32, device=weights.device)
     one, slots, table = (B,), (pages, Hkv, P), _cols(block_table, B, "block_table")
+    if move_counts is None and new_lengths is None:   # parts of one allocation
+        new = torch.empty(B * (Hkv + 1), dtype=i32, device=weights.device)
+        move_counts, new_lengths = new.as_strided((B, Hkv), (Hkv, 1)), new.as_strided(one, (1,), B * Hkv)
+    elif move_counts is None:
+        move_counts = torch.empty((B, Hkv), dtype=i32, device=weights.device)
+    elif new_lengths is None:
+        new_lengths = torch.empty(one, dtype=i32, device=weights.device)
     st = (_lib or lib()).spec_kv_evict_plan(
         _take(weights, "weights", torch.float32, slots, dev), _take(positions, "positions", i32, slots, dev),
         _take(block_table, "block_table", i32, table, dev), _take(lengths, "lengths", i32, one, dev),
@@ -747,19 +750,20 @@ def spec_page_trim(tokens, held, ring, ring_state, block_table, page_tokens: int
     """Gives the pages that tokens [B] int32 do not need back to spec_page_map's ring
     (updated in place).  Returns (new_held [B], new_ring_state [2], status [B]) int32."""
     i32, B = torch.int32, tokens.numel()
-    new = functools.partial(torch.empty, dtype=i32, device=tokens.device)
-    if new_held is None:
-        new_held = new(B)
-    if new_ring_state is None:
-        new_ring_state = new(2)
-    if status is None:
-        status = new(B)
+    if new_held is new_ring_state is status is None:   # parts of one allocation
+        new = torch.empty(2 * B + 2, dtype=i32, device=tokens.device)
+        at = new.data_ptr()
+        new_held, status, new_ring_state = new.split_with_sizes((B, B, 2))
+        to = (at, at + 8 * B, at + 4 * B)
+    else:
+        new_held, new_ring_state, status = out = tuple(
+            torch.empty(n, dtype=i32, device=tokens.device) if t is None else t for t, n in ((new_held, B), (new_ring_state, 2), (status, B)))
+        to = tuple(_take(t, name, i32, (n,), dev) for t, name, n in zip(out, ("new_held", "new_ring_state", "status"), (B, 2, B)))
     one, table = (B,), _cols(block_table, B, "block_table")
     st = (_lib or lib()).spec_page_trim(
         _take(tokens, "tokens", i32, one, dev), _take(held, "held", i32, one, dev), _take(ring, "ring", i32, (ring.numel(),), dev),
         _take(ring_state, "ring_state", i32, (2,), dev), _take(block_table, "block_table", i32, table, dev), B, ring.numel(),
-        page_tokens, table[1], _take(new_held, "new_held", i32, one, dev), _take(new_ring_state, "new_ring_state", i32, (2,), dev),
-        _take(status, "status", i32, one, dev), stream)
+        page_tokens, table[1], *to, stream)
     if st:
         _check("spec_page_trim", st)
     return new_held, new_ring_state, status

@@ -58,7 +58,7 @@ spec_status_t launch_cluster(K kern, dim3 grid, int threads, size_t smem, int C,
 template <class T, int WARPS, bool TOP>
 spec_status_t launch_logprobs(int dev, const LogprobArgs& a, cudaStream_t st) {
   auto kern = token_logprobs_kernel<T, WARPS, TOP>;
-  constexpr int TEAMS = LP_THREADS / (32 * WARPS);
+  constexpr int TEAMS = lp_threads(WARPS) / (32 * WARPS);
   constexpr size_t smem = sizeof(LpShared<WARPS>) * TEAMS;
   if (smem > 48 * 1024 && !once_per_device(dev, [&] {
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) == cudaSuccess;
@@ -66,12 +66,12 @@ spec_status_t launch_logprobs(int dev, const LogprobArgs& a, cudaStream_t st) {
     return fail(SPEC_ERR_CUDA, "log probabilities setup failed: %s", cudaGetErrorString(cudaGetLastError()));
   const long long places = static_cast<long long>(a.B) * a.M, grid = (places + TEAMS - 1) / TEAMS * a.C;
   if (grid > 0x7fffffffLL) return fail(SPEC_ERR_UNSUPPORTED, "batch too large for one call");
-  return launch_cluster(kern, dim3(static_cast<unsigned>(grid)), LP_THREADS, smem, a.C, st, a, "log probabilities launch");
+  return launch_cluster(kern, dim3(static_cast<unsigned>(grid)), lp_threads(WARPS), smem, a.C, st, a, "log probabilities launch");
 }
 template <class T>
 spec_status_t launch_logprobs(int dev, bool warp, const LogprobArgs& a, cudaStream_t st) {
   if (warp) return a.top ? launch_logprobs<T, 1, true>(dev, a, st) : launch_logprobs<T, 1, false>(dev, a, st);
-  return a.top ? launch_logprobs<T, 8, true>(dev, a, st) : launch_logprobs<T, 8, false>(dev, a, st);
+  return a.top ? launch_logprobs<T, LP_WARPS, true>(dev, a, st) : launch_logprobs<T, LP_WARPS, false>(dev, a, st);
 }
 
 // ---------------------------------------------------------------------------
@@ -260,20 +260,23 @@ spec_status_t spec_kv_evict_plan(const float* weights, const int32_t* positions,
     // a cluster where the heads alone do not fill the device and the table has room for long sequences
     const long long pairs = static_cast<long long>(B) * Hkv, most = static_cast<long long>(max_pages) * page_tokens;
     a.C = 1;
-    while (a.C < 8 && pairs * a.C < 2LL * di.sms && most / a.C > 2048) a.C *= 2;
+    while (a.C < EV_CLUSTER && pairs * a.C < 2LL * di.sms && most / a.C > 4096) a.C *= 2;
     if (pairs * a.C > 0x7fffffffLL) return fail(SPEC_ERR_UNSUPPORTED, "batch too large for one call");
-    a.cap = static_cast<int>(std::min<long long>(EV_CAP, (most / Q4_BLOCK + a.C) / a.C * Q4_BLOCK));
-    const size_t smem = 4 * (static_cast<size_t>(a.C > 1 ? 2 : 1) * EV_BINS + a.cap);
+    a.cap = static_cast<int>(std::min<long long>(EV_CAP, (most + a.C * 128 - 1) / (a.C * 128) * 128 + (a.C > 1 ? 128 : 0)));
+    // several pairs a CTA where that leaves two CTAs an SM, with 48 KB of keys at most
+    a.rows = 1;
+    while (a.C == 1 && a.rows < EV_ROWS && pairs / (2 * a.rows) >= 2LL * di.sms && 2 * a.rows * a.cap <= 12288) a.rows *= 2;
+    const size_t smem = 4 * (static_cast<size_t>(EV_HISTS) * EV_BINS + static_cast<size_t>(a.rows) * a.cap);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     prof_mark(0, st);
     auto kern = a.C > 1 ? evict_plan_kernel<true> : evict_plan_kernel<false>;
     if (!once_per_device(dev, [&] {
-          const int all = 4 * (2 * EV_BINS + EV_CAP);
+          const int all = 4 * (EV_HISTS * EV_BINS + std::max(EV_CAP, 12288));
           return cudaFuncSetAttribute(evict_plan_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, all) == cudaSuccess &&
                  cudaFuncSetAttribute(evict_plan_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, all) == cudaSuccess;
         }))
       return fail(SPEC_ERR_CUDA, "eviction plan setup failed: %s", cudaGetErrorString(cudaGetLastError()));
-    s = launch_cluster(kern, dim3(static_cast<unsigned>(pairs * a.C)), EV_THREADS, smem, a.C, st, a, "eviction plan launch");
+    s = launch_cluster(kern, dim3(static_cast<unsigned>((pairs + a.rows - 1) / a.rows * a.C)), EV_THREADS, smem, a.C, st, a, "eviction plan launch");
     if (s != SPEC_OK) return s;
     prof_mark(1, st);
     prof_mark(2, st);

@@ -9,11 +9,12 @@
 // at most 6 entries of a head, where closing the gaps in order would move all that lie
 // behind the first.
 //
-// A cluster of 1 to 8 CTAs takes a (sequence, head), each a contiguous part of its
-// tokens.  The K-th largest key comes from a radix selection, 11 + 11 + 10 bits, over
+// A CTA or a cluster of up to 8 takes a (sequence, head), each CTA a contiguous part of
+// its tokens.  The K-th largest key comes from a radix selection, eight bits a pass, over
 // keys that stay in shared memory (those beyond its size are read again): a histogram
-// a pass, added up over the cluster.  Most selections end early, in a pass whose last
-// bin is needed whole.
+// for each warp, added up over the CTA and the cluster.  It ends early in a pass whose
+// last bin is needed whole.  (Three passes of 2,048 bins read 64 KB of the other CTAs'
+// shared memory a CTA and pass, which took 15,000 clocks.)
 //
 // Bound: 8 bytes a token read (weight and position); in the steady state the passes'
 // barriers, of which there are enough CTAs an SM to cover.
@@ -25,8 +26,10 @@
 namespace sv {
 
 constexpr int EV_THREADS = 256;
-constexpr int EV_BINS = 2048;
+constexpr int EV_BINS = 256;    // of a pass, eight bits; a bin a thread
+constexpr int EV_HISTS = EV_THREADS / 32 + 2;
 constexpr int EV_CAP = 8192;    // keys of a CTA in shared memory, at most
+constexpr int EV_CLUSTER = 8;   // CTAs of a cluster, at most
 
 struct PlanArgs {
   const float* weights;       // [pages, Hkv, P]
@@ -36,7 +39,8 @@ struct PlanArgs {
   const int32_t* budgets;     // [B]
   const int32_t* next;        // [B]
   int B, Hkv, P, pages, W, max_moves, sinks, recent;
-  int cap;                    // keys of a CTA in shared memory
+  int cap;                    // keys of a CTA, or of a pair, in shared memory (a multiple of 128)
+  int rows;                   // pairs of a CTA
   int C;                      // CTAs of a cluster
   int32_t* moves;             // [B, Hkv, max_moves, 2]
   int32_t* counts;            // [B, Hkv]
@@ -45,16 +49,34 @@ struct PlanArgs {
 
 // integers that compare as the weights do; NaN below everything
 __device__ __forceinline__ uint32_t ev_ordered(float w) {
-  if (w != w) return 0u;
   const uint32_t u = __float_as_uint(w + 0.f);   // (-0 becomes 0)
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
+  return w != w ? 0u : u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
 }
+
+// a value that k of the warp's lanes reach, the largest such; 0 if fewer have one above 0
+__device__ __forceinline__ uint32_t warp_kth(uint32_t v, int k) {
+  uint32_t m;
+  do {
+    m = __reduce_max_sync(0xffffffffu, v);
+    const bool top = v == m;
+    k -= __popc(__ballot_sync(0xffffffffu, top));
+    if (top) v = 0u;
+  } while (k > 0 && m != 0u);
+  return m;
+}
+
+constexpr int EV_FEW = 32;      // tokens to drop, up to which they are looked for themselves
+constexpr int EV_LIST = 128;    // places for candidates then
+constexpr int EV_ROWS = 4;      // (sequence, head) pairs of a CTA, at most
 
 struct EvShared {
   int warp[2][EV_THREADS / 32];
   int total[3];                // of this CTA: equal keys, free places, tokens to move
   int bad;
   uint32_t bin, need, equal;
+  int later[EV_ROWS];          // what the few tokens' search left to the selection
+  unsigned long long list[EV_ROWS][EV_LIST];
+  int dropped[EV_ROWS][EV_FEW];
 };
 
 // exclusive scan of x over the CTA; the sum comes back in `all`
@@ -86,163 +108,228 @@ __device__ __forceinline__ void ev_sync() {
   else __syncthreads();
 }
 
+// what a (sequence, head) asks for
+struct EvRow {
+  int pair, b, h, n, K;
+  const int32_t* table;
+  long long from;    // positions from here on stay
+  bool ok, cut;      // the length is in range; there is something to drop
+};
+__device__ __forceinline__ EvRow ev_row(const PlanArgs& a, int pair) {
+  EvRow r;
+  r.pair = pair;
+  r.b = pair / a.Hkv;
+  r.h = pair - r.b * a.Hkv;
+  r.n = a.lengths[r.b];
+  r.K = a.budgets[r.b];
+  r.table = a.table + static_cast<long long>(r.b) * a.W;
+  r.from = static_cast<long long>(a.next[r.b]) - a.recent;
+  r.ok = r.n >= 0 && static_cast<long long>(r.n) <= static_cast<long long>(a.W) * a.P;
+  r.cut = r.ok && r.K >= 0 && r.n > r.K;
+  if (r.cut && min(r.K, r.n - r.K) > a.max_moves) r.ok = r.cut = false;
+  return r;
+}
+__device__ __forceinline__ void ev_uncut(const PlanArgs& a, const EvRow& r, bool ok) {   // one thread
+  a.counts[r.pair] = 0;
+  if (r.h == 0) a.new_lengths[r.b] = ok ? r.n : -1;
+}
+__device__ __forceinline__ int ev_slot(const PlanArgs& a, const EvRow& r, int i) {
+  const int e = i / a.P;
+  return r.table[e] * a.P + (i - e * a.P);
+}
+__device__ __forceinline__ uint32_t ev_key(const PlanArgs& a, const EvRow& r, float w, int pos) {
+  return pos < a.sinks || pos >= r.from ? 0xffffffffu : ev_ordered(w);   // (as in ev_load)
+}
+
+// A warp's run of blocks [k0, k1): their tokens' keys, bits turned by `flip`, to keys[]
+// (tokens before `cap` of it; those behind the sequence's end count as kept), EV_AHEAD
+// blocks under way at a time, the places of 32 blocks looked up by a lane each; true if
+// a page is none.  worst: the complement of the thread's least key.
+constexpr int EV_AHEAD = 8;
+__device__ __forceinline__ bool ev_load(const PlanArgs& a, const EvRow& r, int k0, int k1, uint32_t flip, uint32_t* keys, int cap, uint32_t& worst) {
+  const int lane = threadIdx.x & 31, per = a.P / Q4_BLOCK;
+  const uint32_t span = r.from > a.sinks ? static_cast<uint32_t>(r.from - a.sinks) : 0u;   // positions that may go: sinks + [0, span)
+  bool bad = false;
+  for (int c0 = k0; c0 < k1; c0 += 32) {
+    uint32_t blk = 0u;   // of the chunk's lane-th block among the pool's
+    bool none = false;
+    if (c0 + lane < k1) {
+      const int e = (c0 + lane) / per, page = r.table[e];
+      none = page < 0 || page >= a.pages;
+      blk = (static_cast<uint32_t>(page) * a.Hkv + r.h) * per + (c0 + lane - e * per);
+    }
+    if (__any_sync(0xffffffffu, none)) {
+      bad = true;
+      continue;
+    }
+    const int c1 = min(k1, c0 + 32);
+    for (int k = c0; k < c1; k += EV_AHEAD) {
+      float w[EV_AHEAD];
+      int pos[EV_AHEAD];
+#pragma unroll
+      for (int u = 0; u < EV_AHEAD; ++u) {
+        // (behind the end the last block again: loads without a branch between them)
+        const unsigned long long at = static_cast<unsigned long long>(__shfl_sync(0xffffffffu, blk, min(k + u, c1 - 1) - c0)) * Q4_BLOCK + lane;
+        w[u] = __ldg(a.weights + at);
+        pos[u] = __ldg(a.positions + at);
+      }
+#pragma unroll
+      for (int u = 0; u < EV_AHEAD; ++u) {
+        const int i = (k + u) * Q4_BLOCK + lane;
+        if (k + u < c1) {
+          const bool stays = static_cast<uint32_t>(pos[u] - a.sinks) >= span || i >= r.n;
+          const uint32_t x = stays ? 0xffffffffu : ev_ordered(w[u]);
+          if (i - k0 * Q4_BLOCK < cap) keys[i - k0 * Q4_BLOCK] = x ^ flip;
+          worst = max(worst, ~x);
+        }
+      }
+    }
+  }
+  return bad;
+}
+
+// Few tokens to drop, as when a step's tokens push out as many: a warp looks for the
+// least keys themselves, much as the largest logits of a row are found
+// (token_logprobs.cuh): what the drop-th worst of its threads' worst reaches is listed,
+// and the list is put in order.  False where that does not do (a list that runs over, of
+// many equal keys).  (256 sequences of 8 heads that drop up to 6 of 2,054: the radix
+// selection, with a CTA for each, takes 39 us; this with a CTA's eight warps 24.)
+__device__ __forceinline__ bool ev_few(const PlanArgs& a, const EvRow& r, uint32_t* keys, unsigned long long* list, int* dropped) {
+  const int lane = threadIdx.x & 31, drop = r.n - r.K;
+  uint32_t worst = 0u;   // (of complements: the largest)
+  const bool bad = ev_load(a, r, 0, (r.n + Q4_BLOCK - 1) / Q4_BLOCK, 0xffffffffu, keys, a.cap, worst);
+  if (__any_sync(0xffffffffu, bad)) {
+    if (lane == 0) ev_uncut(a, r, false);
+    return true;
+  }
+  const uint32_t bound = warp_kth(worst, drop);
+  if (bound == 0u) return false;
+  __syncwarp();
+  int m = 0;
+  for (int i0 = 0; i0 < r.n; i0 += 128) {
+    const uint4 x = *reinterpret_cast<const uint4*>(keys + i0 + 4 * lane);   // (there is room for 128 at a time)
+    const uint32_t y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int i = i0 + 4 * lane + j;
+      const uint32_t all = __ballot_sync(0xffffffffu, y[j] >= bound && i < r.n);
+      if (all == 0u) continue;
+      const int p = m + __popc(all & ((1u << lane) - 1u));
+      if ((all >> lane & 1u) && p < EV_LIST) list[p] = (static_cast<unsigned long long>(y[j]) << 32) | static_cast<uint32_t>(i);
+      m += __popc(all);
+    }
+  }
+  if (m > EV_LIST) return false;
+  __syncwarp();
+  for (int i = lane; i < m; i += 32) {
+    const unsigned long long x = list[i];
+    int before = 0;
+#pragma unroll 4
+    for (int j = 0; j < m; ++j) before += list[j] > x;
+    if (before < drop) dropped[before] = static_cast<int>(x & 0xffffffffu);   // (equal keys: the last place goes first)
+  }
+  __syncwarp();
+  int32_t* moves = a.moves + 2 * static_cast<long long>(r.pair) * a.max_moves;
+  const int t = lane < drop ? dropped[lane] : r.n;
+  const uint32_t gone = __reduce_or_sync(0xffffffffu, t >= r.K && t < r.n ? 1u << (t - r.K) : 0u);   // of the places behind
+  int before = 0;
+  for (int j = 0; j < drop; ++j) before += __shfl_sync(0xffffffffu, t, j) < t;
+  if (t < r.K) moves[2 * before + 1] = ev_slot(a, r, t);
+  if (lane < drop && !(gone >> lane & 1u)) moves[2 * __popc(~gone & ((1u << lane) - 1u))] = ev_slot(a, r, r.K + lane);
+  if (lane == 0) {
+    a.counts[r.pair] = drop - __popc(gone);
+    if (r.h == 0) a.new_lengths[r.b] = r.K;
+  }
+  return true;
+}
+
+// Any number of tokens to drop: the selection, by a CTA or a cluster.
 template <bool CLUSTER>
-__global__ void __launch_bounds__(EV_THREADS) evict_plan_kernel(const PlanArgs a) {
-  extern __shared__ uint4 ev_dynamic[];
-  __shared__ EvShared sh;
-  uint32_t* hist0 = reinterpret_cast<uint32_t*>(ev_dynamic);   // [CLUSTER ? 2 : 1][EV_BINS]
-  uint32_t* keys = hist0 + (CLUSTER ? 2 : 1) * EV_BINS;
+__device__ __forceinline__ void ev_select(const PlanArgs& a, const EvRow& row, EvShared& sh, uint32_t* hist, uint32_t* keys) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int C = CLUSTER ? a.C : 1;
   const uint32_t rank = CLUSTER ? cluster_rank() : 0u;
-  const int pair = blockIdx.x / C, b = pair / a.Hkv, h = pair - b * a.Hkv;
   const bool first = rank == 0 && tid == 0;
-  const int n = a.lengths[b], budget = a.budgets[b];
-  // (the same for all CTAs of a sequence)
-  if (n < 0 || static_cast<long long>(n) > static_cast<long long>(a.W) * a.P || budget < 0 || n <= budget ||
-      min(budget, n - budget) > a.max_moves) {
-    if (first) {
-      const bool ok = n >= 0 && static_cast<long long>(n) <= static_cast<long long>(a.W) * a.P && (budget < 0 || n <= budget);
-      a.counts[pair] = 0;
-      if (h == 0) a.new_lengths[b] = ok ? n : -1;
-    }
-    return;
-  }
-  const int32_t* table = a.table + static_cast<long long>(b) * a.W;
-  const long long from = static_cast<long long>(a.next[b]) - a.recent;   // positions from here on stay
+  const int n = row.n, K = row.K;
+  const int32_t* table = row.table;
 
-  // this CTA's tokens
+  // this CTA's tokens, and of them a warp's
   const int blocks = (n + Q4_BLOCK - 1) / Q4_BLOCK;
   const int blk0 = static_cast<int>(static_cast<long long>(blocks) * rank / C);
   const int blk1 = static_cast<int>(static_cast<long long>(blocks) * (rank + 1) / C);
   const int base = blk0 * Q4_BLOCK, mine = max(0, min(n, blk1 * Q4_BLOCK) - base);
-
-  auto key_of = [&](long long at) {
-    const int pos = __ldg(a.positions + at);
-    const float w = __ldg(a.weights + at);
-    return pos < a.sinks || pos >= from ? 0xffffffffu : ev_ordered(w);
-  };
-  // keys into shared memory, a block a warp, four at a time; pages that are none are noted
-  bool bad = false;
-  for (int k0 = blk0 + warp; k0 < blk1; k0 += 4 * (EV_THREADS / 32)) {
-    int page[4], in[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int t = (k0 + u * (EV_THREADS / 32)) * Q4_BLOCK;
-      page[u] = 0;
-      if (t < n && k0 + u * (EV_THREADS / 32) < blk1) {
-        const int e = t / a.P;
-        in[u] = t - e * a.P;
-        page[u] = table[e];
-      }
-    }
-    float w[4];
-    int pos[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int k = k0 + u * (EV_THREADS / 32), i = k * Q4_BLOCK + lane - base;
-      if (k >= blk1) break;
-      if (page[u] < 0 || page[u] >= a.pages) {
-        bad = true;
-      } else if (i < mine && i < a.cap) {
-        const long long at = (static_cast<long long>(page[u]) * a.Hkv + h) * a.P + in[u] + lane;
-        w[u] = __ldg(a.weights + at);
-        pos[u] = __ldg(a.positions + at);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int k = k0 + u * (EV_THREADS / 32), i = k * Q4_BLOCK + lane - base;
-      if (k >= blk1) break;
-      if (page[u] >= 0 && page[u] < a.pages && i < mine && i < a.cap)
-        keys[i] = pos[u] < a.sinks || pos[u] >= from ? 0xffffffffu : ev_ordered(w[u]);
-    }
-  }
-  auto slot_of = [&](int i) {
-    const int e = i / a.P;
-    return table[e] * a.P + (i - e * a.P);
-  };
+  const int w0 = blk0 + (blk1 - blk0) * warp / (EV_THREADS / 32), w1 = blk0 + (blk1 - blk0) * (warp + 1) / (EV_THREADS / 32);
+  uint32_t worst = 0u;
+  bool bad = ev_load(a, row, w0, w1, 0u, keys + (w0 - blk0) * Q4_BLOCK, a.cap - (w0 - blk0) * Q4_BLOCK, worst);
+  auto slot_of = [&](int i) { return ev_slot(a, row, i); };
   auto key_at = [&](int i) {   // i: of this CTA's tokens
     if (i < a.cap) return keys[i];
     const int t = base + i, e = t / a.P;
-    return key_of((static_cast<long long>(table[e]) * a.Hkv + h) * a.P + (t - e * a.P));
+    const long long at = (static_cast<long long>(table[e]) * a.Hkv + row.h) * a.P + (t - e * a.P);
+    return ev_key(a, row, __ldg(a.weights + at), __ldg(a.positions + at));
   };
   bad = __syncthreads_or(bad);
   if constexpr (CLUSTER) {
     if (tid == 0) sh.bad = bad;
     cluster_sync_all();
-    for (int r = 0; r < C; ++r) bad |= ld_peer_u32(&sh.bad, r) != 0u;
+    bad = __any_sync(0xffffffffu, lane < C && ld_peer_u32(&sh.bad, lane) != 0u);
   }
   if (bad) {
-    if (first) {
-      a.counts[pair] = 0;
-      if (h == 0) a.new_lengths[b] = -1;
-    }
+    if (first) ev_uncut(a, row, false);
     if constexpr (CLUSTER) cluster_sync_all();   // (its shared memory was read)
     return;
   }
+  int32_t* moves = a.moves + 2 * static_cast<long long>(row.pair) * a.max_moves;
 
   // the K-th largest key
-  const int K = budget;
   uint32_t prefix = 0, need = static_cast<uint32_t>(K);
   uint32_t tau = K > 0 ? 0u : 0xffffffffu;   // what is above it stays (nothing, for a budget of 0),
   uint32_t take = 0;                         // and the first `take` of what equals it
+  static_assert(EV_BINS == EV_THREADS, "a bin a thread");
+  uint32_t* mine_hist = hist + warp * EV_BINS;
 #pragma unroll 1
-  for (int pass = K > 0 ? 0 : 3; pass < 3; ++pass) {
-    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
-    uint32_t* hist = hist0 + (CLUSTER && (pass & 1) ? EV_BINS : 0);
-    for (int i = tid; i < EV_BINS; i += EV_THREADS) hist[i] = 0u;
-    __syncthreads();
+  for (int pass = K > 0 ? 0 : 4; pass < 4; ++pass) {
+    const int shift = 24 - 8 * pass;
+#pragma unroll
+    for (int i = 0; i < EV_BINS / 32; ++i) mine_hist[32 * i + lane] = 0u;
+    __syncwarp();
     for (int i = tid; i < mine; i += EV_THREADS) {
       const uint32_t k = key_at(i);
-      if (pass == 0 || (k >> (shift + bits)) == prefix) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1u)], 1u);
-    }
-    ev_sync<CLUSTER>();
-    // thread t has the eight bins below 2048 - 8 t
-    constexpr int EACH = EV_BINS / EV_THREADS;
-    static_assert(EACH == 8, "two vectors a thread");
-    const int lo = EV_BINS - EACH * (tid + 1);
-    uint32_t c[EACH];
-#pragma unroll
-    for (int i = 0; i < EACH; ++i) c[i] = 0u;
-    for (int r = 0; r < C; ++r) {
-#pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        uint4 x;
-        if constexpr (CLUSTER) x = ld_peer_u128(hist + lo + 4 * v, r);
-        else x = *reinterpret_cast<const uint4*>(hist + lo + 4 * v);
-        c[4 * v] += x.x;
-        c[4 * v + 1] += x.y;
-        c[4 * v + 2] += x.z;
-        c[4 * v + 3] += x.w;
-      }
-    }
-    int sum = 0, all;
-#pragma unroll
-    for (int i = 0; i < EACH; ++i) sum += static_cast<int>(c[i]);
-    uint32_t above = static_cast<uint32_t>(ev_scan(sum, sh.warp[0], all));
-    if (above < need && need <= above + sum) {
-      bool found = false;
-#pragma unroll
-      for (int i = EACH - 1; i >= 0; --i) {
-        if (!found && need <= above + c[i]) {
-          found = true;
-          sh.bin = static_cast<uint32_t>(lo + i);
-          sh.need = need - above;
-          sh.equal = c[i];
-        }
-        if (!found) above += c[i];
-      }
+      if (pass == 0 || (k >> (shift + 8)) == prefix) atomicAdd(&mine_hist[(k >> shift) & 255u], 1u);
     }
     __syncthreads();
-    prefix = (prefix << bits) | sh.bin;
+    // thread t has the bin 255 - t: of the warps, then of the cluster
+    const int bin = EV_BINS - 1 - tid;
+    uint32_t c = 0u;
+#pragma unroll
+    for (int i = 0; i < EV_THREADS / 32; ++i) c += hist[i * EV_BINS + bin];
+    if constexpr (CLUSTER) {
+      uint32_t* sums = hist + (EV_THREADS / 32 + (pass & 1)) * EV_BINS;   // (two, as the next pass's come before the last one's are read)
+      sums[bin] = c;
+      cluster_sync_all();
+      uint32_t x[EV_CLUSTER];
+#pragma unroll
+      for (int r = 0; r < EV_CLUSTER; ++r) x[r] = ld_peer_u32(sums + bin, r < C ? r : 0);   // (all under way before the first sum)
+      c = 0u;
+#pragma unroll
+      for (int r = 0; r < EV_CLUSTER; ++r) c += r < C ? x[r] : 0u;
+    }
+    int all;
+    const uint32_t above = static_cast<uint32_t>(ev_scan(static_cast<int>(c), sh.warp[0], all));
+    if (above < need && need <= above + c) {
+      sh.bin = static_cast<uint32_t>(bin);
+      sh.need = need - above;
+      sh.equal = c;
+    }
+    __syncthreads();
+    prefix = (prefix << 8) | sh.bin;
     need = sh.need;
     const uint32_t equal = sh.equal;
     if (equal == need) {   // all that share these bits stay (some token does not, so they are not zero)
       tau = (prefix << shift) - 1u;
       break;
     }
-    if (pass == 2) {
+    if (pass == 3) {
       tau = prefix;
       take = need;
     }
@@ -260,7 +347,7 @@ __global__ void __launch_bounds__(EV_THREADS) evict_plan_kernel(const PlanArgs a
     if constexpr (CLUSTER) {
       if (tid == 0) sh.total[0] = all;
       cluster_sync_all();
-      for (uint32_t r = 0; r < rank; ++r) equal_before += static_cast<int>(ld_peer_u32(&sh.total[0], r));
+      equal_before += __reduce_add_sync(0xffffffffu, lane < static_cast<int>(rank) ? static_cast<int>(ld_peer_u32(&sh.total[0], lane)) : 0);
     }
   }
   int holes = 0, movers = 0, e = equal_before;
@@ -278,17 +365,11 @@ __global__ void __launch_bounds__(EV_THREADS) evict_plan_kernel(const PlanArgs a
       sh.total[2] = all_movers;
     }
     cluster_sync_all();
-    all_holes = 0;
-    for (uint32_t r = 0; r < static_cast<uint32_t>(C); ++r) {
-      const int x = static_cast<int>(ld_peer_u32(&sh.total[1], r)), y = static_cast<int>(ld_peer_u32(&sh.total[2], r));
-      if (r < rank) {
-        hole += x;
-        mover += y;
-      }
-      all_holes += x;
-    }
+    const int x = lane < C ? static_cast<int>(ld_peer_u32(&sh.total[1], lane)) : 0, y = lane < C ? static_cast<int>(ld_peer_u32(&sh.total[2], lane)) : 0;
+    hole += __reduce_add_sync(0xffffffffu, lane < static_cast<int>(rank) ? x : 0);
+    mover += __reduce_add_sync(0xffffffffu, lane < static_cast<int>(rank) ? y : 0);
+    all_holes = __reduce_add_sync(0xffffffffu, x);
   }
-  int32_t* moves = a.moves + 2 * static_cast<long long>(pair) * a.max_moves;
   if (holes + movers > 0) {
     e = equal_before;
     for (int i = i0; i < i1; ++i) {
@@ -302,10 +383,46 @@ __global__ void __launch_bounds__(EV_THREADS) evict_plan_kernel(const PlanArgs a
     }
   }
   if (first) {
-    a.counts[pair] = all_holes;
-    if (h == 0) a.new_lengths[b] = K;
+    a.counts[row.pair] = all_holes;
+    if (row.h == 0) a.new_lengths[row.b] = K;
   }
-  if constexpr (CLUSTER) cluster_sync_all();   // nobody ends while its shared memory is read
+  ev_sync<CLUSTER>();   // (nobody ends, or goes on, while shared memory is read)
+}
+
+// CLUSTER: a cluster a pair.  Else a CTA has `rows` pairs: a warp for each looks for few
+// tokens to drop, and the CTA takes the others one after the other.
+template <bool CLUSTER>
+__global__ void __launch_bounds__(EV_THREADS, 4) evict_plan_kernel(const PlanArgs a) {
+  extern __shared__ uint4 ev_dynamic[];
+  __shared__ EvShared sh;
+  uint32_t* hist = reinterpret_cast<uint32_t*>(ev_dynamic);   // the warps', and two of the CTA
+  uint32_t* keys = hist + EV_HISTS * EV_BINS;                 // [rows][cap]
+  if constexpr (CLUSTER) {
+    const EvRow row = ev_row(a, blockIdx.x / a.C);
+    if (!row.cut) {   // (the same for all CTAs of a sequence)
+      if (cluster_rank() == 0 && threadIdx.x == 0) ev_uncut(a, row, row.ok);
+      return;
+    }
+    ev_select<true>(a, row, sh, hist, keys);
+  } else {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, pair = blockIdx.x * a.rows + warp;
+    if (warp < a.rows) {
+      bool later = false;
+      if (pair < a.B * a.Hkv) {
+        const EvRow row = ev_row(a, pair);
+        if (!row.cut) {
+          if (lane == 0) ev_uncut(a, row, row.ok);
+        } else {
+          later = row.n - row.K > EV_FEW || row.n > a.cap;
+          if (!later) later = !ev_few(a, row, keys + warp * a.cap, sh.list[warp], sh.dropped[warp]);
+        }
+      }
+      if (lane == 0) sh.later[warp] = later;
+    }
+    __syncthreads();
+    for (int r = 0; r < a.rows; ++r)
+      if (sh.later[r]) ev_select<false>(a, ev_row(a, blockIdx.x * a.rows + r), sh, hist, keys);
+  }
 }
 
 // ---------------------------------------------------------------------------

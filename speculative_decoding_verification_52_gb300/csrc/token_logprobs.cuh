@@ -5,14 +5,14 @@
 //   logprob(t) = z_t - m - log S,   entropy = log S - (sum e^(z - m) (z - m)) / S,
 //   rank(t) = 1 + #{v: l_v > l_t, or l_v = l_t and v < t}.
 // Everything comes from one pass over the row, in the log2 domain (c = log2(e) / T),
-// with a running reference a thread; when it moves by d <= 0,
+// with a running reference a warp; when it moves by d <= 0,
 //   S' = 2^d S,  X' = 2^d (X + d S)   for X = sum 2^z z.
 //
 // The largest n.  A thread that has seen elements knows the largest of its own; in a
 // team of `WARPS` warps, the ceil(n / WARPS)-th largest of a warp's 32, taken as the
 // least over the warps, has n elements at or above it.  Only what reaches that bound
-// goes into a list: a few dozen elements beside the first tile's, since the bound is
-// taken anew after 1, 2, 4, ... tiles.  Equal elements are told apart by their index in
+// goes into a list: some dozens of elements, since the bound is taken anew after 1, 2,
+// 4, ... tiles.  Equal elements are told apart by their index in
 // the bound, too, so that a row of equal logits fills no list.  Where a list runs over all
 // the same (a row whose logits rise to its end), the team searches the row once for each
 // of its n largest.  Elements that the bound or the token's logit concerns are looked for
@@ -26,7 +26,9 @@
 
 namespace sv {
 
-constexpr int LP_THREADS = 256;
+constexpr int LP_WARPS = 8;        // of the CTA that takes a long row
+constexpr int LP_TEAMS = 8;        // warps of a CTA that take a short row each
+__host__ __device__ constexpr int lp_threads(int warps) { return warps == 1 ? 32 * LP_TEAMS : 32 * warps; }
 constexpr int LP_MAX_TOP = 32;
 constexpr float LP_FAR = 1.2676506002282294e30f;   // 2^100: logits of this size count as infinities
 
@@ -55,25 +57,19 @@ __device__ __forceinline__ float lp_value(unsigned long long k) {
 }
 __device__ __forceinline__ int lp_index(unsigned long long k) { return static_cast<int>(~static_cast<uint32_t>(k)); }
 
-// A thread's part of a row.  Exponents are (l - m) c, which is 0 for m itself however
-// large it is; l c - fl(m c), an instruction less, is off by what the product lost.
+// Sums of a part of a row against a reference (a logit; -2^100: nothing with a weight
+// yet).  Exponents are (l - m) c, which is 0 for m itself however large it is; l c -
+// fl(m c), an instruction less, is off by what the product lost.
 struct LpAcc {
-  float m, s, x;       // reference (a logit), sum 2^z, sum 2^z z
-  int at;              // index of m
-  __device__ __forceinline__ void init() {
-    m = -LP_FAR;
-    s = x = 0.f;
-    at = -1;
-  }
-  // to a reference of `to` (above the present one) at index i
-  __device__ __forceinline__ void raise(float to, float c, int i) {
+  float m, s, x;       // reference, sum 2^z, sum 2^z z
+  // to a reference of `to` (above the present one)
+  __device__ __forceinline__ void raise(float to, float c) {
     if (s > 0.f) {
       const float d = __fmul_rn(__fsub_rn(m, to), c), f = ex2_approx(d);   // (d <= 0)
       x = f * __fmaf_rn(d, s, x);
       s *= f;
     }
     m = to;
-    at = i;
   }
   __device__ __forceinline__ void merge(float m2, float s2, float x2, float c) {
     if (!(s2 > 0.f)) return;
@@ -127,26 +123,39 @@ __device__ __forceinline__ uint4 lp_load(const uint4* p) {
   return v;
 }
 
-// value of the k-th largest of the warp's lanes (k = 1..32), as an ordered integer
-__device__ __forceinline__ uint32_t lp_kth(uint32_t v, int k) {
-  const int lane = threadIdx.x & 31;
+// elements of a vector above t
+template <class T>
+__device__ __forceinline__ int lp_above(const uint4& q, float t) {
+  float x[T::vpe];
+  T::unpack(q, x);
+  int n = 0;
 #pragma unroll
-  for (int size = 2; size <= 32; size <<= 1) {
-#pragma unroll
-    for (int d = size >> 1; d > 0; d >>= 1) {
-      const uint32_t u = __shfl_xor_sync(0xffffffffu, v, d);
-      const bool larger = ((lane & d) == 0) == ((lane & size) == 0);   // this lane keeps the larger one
-      v = larger ? max(u, v) : min(u, v);
-    }
-  }
-  return __shfl_sync(0xffffffffu, v, k - 1);
+  for (int k = 0; k < T::vpe; ++k) n += x[k] > t;
+  return n;
+}
+template <>   // (t is a bf16, and so is the next number below one)
+__device__ __forceinline__ int lp_above<BF16T>(const uint4& q, float t) {
+  const uint32_t u = __byte_perm(__float_as_uint(t), 0u, 0x3232);
+  auto set = [&](uint32_t x) {
+    uint32_t d;
+    asm("set.gt.bf16x2.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(x), "r"(u));
+    return d;
+  };
+  auto add = [](uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("add.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+  };
+  const uint32_t n = add(add(set(q.x), set(q.y)), add(set(q.z), set(q.w)));
+  return static_cast<int>(__uint_as_float(n << 16) + __uint_as_float(n & 0xffff0000u));
 }
 
 template <int WARPS>
 struct LpShared {
-  static constexpr int CAP = WARPS == 1 ? 256 : 2048;   // places of a team's list
-  static constexpr int CAP2 = WARPS == 1 ? 1 : 256;     // of those that reach the last bound
-  unsigned long long list[CAP], list2[CAP2];
+  static constexpr int CAP = WARPS == 1 ? 128 : 1024;   // a team's list
+  static constexpr int CAP2 = WARPS == 1 ? 128 : 512;   // elements that reach the last bound
+  uint2 list[CAP];   // of what a thread had of a tile: the largest element (ordered), the first vector
+  unsigned long long list2[CAP2];
   unsigned long long bound[2][WARPS];   // two, so that a warp that is a step ahead does not change what another reads
   unsigned long long top[LP_MAX_TOP];
   float m[WARPS], s[WARPS], x[WARPS];
@@ -154,17 +163,33 @@ struct LpShared {
   int count, count2;
 };
 
+// the first n of m different keys, in order; `each` threads (a power of two) count for one
+__device__ __forceinline__ void lp_order(const unsigned long long* list, int m, int n, int tid, int team, unsigned long long* top) {
+  int each = 1;
+  while (each < 32 && each * 2 * m <= team) each *= 2;
+  const int sub = tid & (each - 1);
+  for (int i0 = 0; i0 < m; i0 += team / each) {   // (whole warps go on alike)
+    const int i = i0 + tid / each;
+    const unsigned long long k = i < m ? list[i] : 0ull;
+    int r = 0;
+#pragma unroll 4
+    for (int j = sub; j < m; j += each) r += list[j] > k;
+    for (int o = each >> 1; o > 0; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
+    if (sub == 0 && k != 0ull && r < n) top[r] = k;
+  }
+}
+
 template <int WARPS>
 __device__ __forceinline__ void lp_sync() {
   if constexpr (WARPS == 1) __syncwarp();
   else __syncthreads();
 }
 
-// One team a row, or a part of it: the CTA (WARPS = 8), or a warp.
+// One team a row, or a part of it: the CTA, or a warp.
 template <class T, int WARPS, bool TOP>
-__global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const LogprobArgs a) {
+__global__ void __launch_bounds__(lp_threads(WARPS), 1024 / lp_threads(WARPS)) token_logprobs_kernel(const LogprobArgs a) {
   using S = LpShared<WARPS>;
-  constexpr int TEAM = 32 * WARPS, TEAMS = LP_THREADS / TEAM, U = 4, E = T::vpe;
+  constexpr int TEAM = 32 * WARPS, TEAMS = lp_threads(WARPS) / TEAM, U = 4, E = T::vpe;
   extern __shared__ uint4 lp_dynamic[];
   const int tid = WARPS == 1 ? threadIdx.x & 31 : threadIdx.x, lane = threadIdx.x & 31, warp = tid >> 5;
   const int team = WARPS == 1 ? threadIdx.x >> 5 : 0;
@@ -202,12 +227,14 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const Log
   const uint4* body = reinterpret_cast<const uint4*>(base + head * T::esz);
   const float xt = fmax_nan(T::load(base, token), -LP_FAR);
   // (what equals the token's logit counts before it, not behind it)
-  const float below = xt == 0.f ? -1.401298464e-45f : __uint_as_float(__float_as_uint(xt) + (xt > 0.f ? 0xffffffffu : 1u));
+  constexpr uint32_t ULP = T::esz == 2 ? 0x10000u : 1u;
+  const float below = __uint_as_float(xt == 0.f ? 0x80000000u + ULP : xt > 0.f ? __float_as_uint(xt) - ULP : __float_as_uint(xt) + ULP);
 
   if (tid == 0) sh.count = sh.count2 = 0;
-  LpAcc acc;
-  acc.init();
-  int ahead = 0;       // elements before the token's in the order
+  LpAcc acc = {-LP_FAR, 0.f, 0.f};   // (m: the warp's)
+  float most = -LP_FAR;   // the largest of the thread's elements, and the last index of its tile
+  int at = 0;
+  int ahead = 0;          // elements before the token's in the order
   bool bad = false;
   // the odd elements, one a thread
   float odd = -LP_FAR;
@@ -216,10 +243,9 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const Log
     odd_at = tid < head ? tid : a.V - rest + tid - head;
     odd = fmax_nan(T::load(base, odd_at), -LP_FAR);
     bad = !(odd < LP_FAR);
-    if (odd > -LP_FAR && !bad) {
-      acc.raise(odd, a.c, odd_at);
-      acc.s = 1.f;
-    }
+    if (bad) odd = -LP_FAR;
+    most = odd;
+    at = odd_at;
     ahead = odd > xt || (odd == xt && odd_at < token);
   }
 
@@ -230,32 +256,32 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const Log
   int turn = 0;
   auto publish = [&]() {
     const int k = (n + WARPS - 1) / WARPS;
-    const uint32_t mine = acc.at >= 0 ? ev_ordered(acc.m) : 0u, v = lp_kth(mine, k);
-    const uint32_t last = __reduce_max_sync(0xffffffffu, mine == v ? static_cast<uint32_t>(acc.at) : 0u);
+    const uint32_t mine = most > -LP_FAR ? ev_ordered(most) : 0u, v = warp_kth(mine, k);
+    const uint32_t last = __reduce_max_sync(0xffffffffu, mine == v ? static_cast<uint32_t>(at) : 0u);
     turn ^= 1;
     if (lane == 0) sh.bound[turn][warp] = v == 0u ? 0ull : (static_cast<unsigned long long>(v) << 32) | static_cast<uint32_t>(~last);
   };
   auto refresh = [&]() {
-    bound = sh.bound[turn][0];
-#pragma unroll
-    for (int w = 1; w < WARPS; ++w) bound = min(bound, sh.bound[turn][w]);
+    const unsigned long long k = sh.bound[turn][lane % WARPS];
+    const uint32_t hi = __reduce_min_sync(0xffffffffu, static_cast<uint32_t>(k >> 32));
+    const uint32_t lo = __reduce_min_sync(0xffffffffu, static_cast<uint32_t>(k >> 32) == hi ? static_cast<uint32_t>(k) : 0xffffffffu);
+    bound = (static_cast<unsigned long long>(hi) << 32) | lo;
     bound_v = bound ? lp_value(bound) : -LP_FAR;
-  };
-  auto push = [&](float x, int i) {
-    const unsigned long long k = lp_key(x, i);
-    if (x > -LP_FAR && k >= bound) {
-      const int p = atomicAdd(&sh.count, 1);
-      if (p < S::CAP) sh.list[p] = k;
-    }
   };
 
   const int tiles = (v1 - v0 + TEAM * U - 1) / (TEAM * U);
   uint4 q[U];
   auto fetch = [&](int tile) {
+    const int v = v0 + tile * (TEAM * U) + tid;
+    if (v0 + (tile + 1) * (TEAM * U) <= v1) {
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
-      const int v = v0 + tile * (TEAM * U) + j * TEAM + tid;
-      q[j] = v < v1 ? lp_load(body + v) : lp_nothing<T>();
+      for (int j = 0; j < U; ++j) q[j] = lp_load(body + v + j * TEAM);
+    } else {
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        q[j] = lp_nothing<T>();
+        if (v + j * TEAM < v1) q[j] = lp_load(body + v + j * TEAM);
+      }
     }
   };
   fetch(0);
@@ -267,30 +293,46 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const Log
     for (int j = 0; j < U; ++j) w[j] = lp_clamp<T>(q[j]);
     if (tile + 1 < tiles) fetch(tile + 1);
     const int first = v0 + tile * (TEAM * U) + tid;
+    float all = tile == 0 ? odd : -LP_FAR;
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       top[j] = lp_vec_max<T>(w[j]);
-      bad |= !(top[j] < LP_FAR);
-      float x[E];
-      T::unpack(w[j], x);
-      if (top[j] > acc.m) {
-        int f = E - 1;
-#pragma unroll
-        for (int k = E - 2; k >= 0; --k)
-          if (x[k] == top[j]) f = k;
-        acc.raise(top[j], a.c, head + (first + j * TEAM) * E + f);
-      }
-      if (acc.at < 0) continue;   // nothing with a weight so far
+      all = fmax_nan(all, top[j]);
+    }
+    if (TOP && all > most) {
+      most = all;
+      at = head + (first + (U - 1) * TEAM) * E + E - 1;
+    }
+    bad |= !(all < LP_FAR);
+    // The warp's reference moves when an element passes it by 8 in the exponent (and for
+    // the first with a weight).  A reference for each thread that followed its largest
+    // element moved in some lane at three vectors of four.
+    if (__any_sync(0xffffffffu, __fmul_rn(__fsub_rn(all, acc.m), a.c) > (acc.m > -LP_FAR ? 8.f : 0.f))) {
+      const uint32_t k = __reduce_max_sync(0xffffffffu, ev_ordered(all));   // (a NaN is the least)
+      const float to = lp_value(static_cast<unsigned long long>(k) << 32);
+      if (to > acc.m) acc.raise(to, a.c);
+    }
+    if (acc.m > -LP_FAR) {
       const unsigned long long cc = f2_pack(a.c, a.c), mm = f2_pack(-acc.m, -acc.m);
+      if (tile == 0 && odd_at >= 0) {
+        const float z = __fmul_rn(__fsub_rn(odd, acc.m), a.c), e = ex2_approx(z);
+        acc.s += e;
+        acc.x += e * z;
+      }
       unsigned long long s2 = 0ull, x2 = 0ull;
 #pragma unroll
-      for (int k = 0; k < E; k += 2) {
-        const unsigned long long z = f2_mul(f2_add(f2_pack(x[k], x[k + 1]), mm), cc);
-        float z0, z1;
-        f2_unpack(z, z0, z1);
-        const unsigned long long e = f2_pack(ex2_approx(z0), ex2_approx(z1));
-        s2 = f2_add(s2, e);
-        x2 = f2_fma(e, z, x2);
+      for (int j = 0; j < U; ++j) {
+        float x[E];
+        T::unpack(w[j], x);
+#pragma unroll
+        for (int k = 0; k < E; k += 2) {
+          const unsigned long long z = f2_mul(f2_add(f2_pack(x[k], x[k + 1]), mm), cc);
+          float z0, z1;
+          f2_unpack(z, z0, z1);
+          const unsigned long long e = f2_pack(ex2_approx(z0), ex2_approx(z1));
+          s2 = f2_add(s2, e);
+          x2 = f2_fma(e, z, x2);
+        }
       }
       float s0, s1, x0, x1;
       f2_unpack(s2, s0, s1);
@@ -298,19 +340,19 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const Log
       acc.s += s0 + s1;
       acc.x += x0 + x1;
     }
-    // what stands before the token
+    // what stands before the token (few tiles have any)
+    if (__any_sync(0xffffffffu, all >= xt)) {
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
-      const int v = first + j * TEAM, i = head + v * E;
-      if (top[j] >= xt && v < v1) {
-        float x[E];
-        T::unpack(w[j], x);
-        const float t = i < token ? below : xt;
+      for (int j = 0; j < U; ++j) {
+        const int v = first + j * TEAM, i = head + v * E;
+        if (top[j] >= xt && v < v1) {
+          ahead += lp_above<T>(w[j], i < token ? below : xt);
+          if (i < token && token < i + E) {   // (what equals it behind it, and itself)
+            float x[E];
+            T::unpack(w[j], x);
 #pragma unroll
-        for (int k = 0; k < E; ++k) ahead += x[k] > t;
-        if (i < token && token < i + E) {   // (what equals it behind it, and itself)
-#pragma unroll
-          for (int k = 0; k < E; ++k) ahead -= x[k] == xt && i + k >= token;
+            for (int k = 0; k < E; ++k) ahead -= x[k] == xt && i + k >= token;
+          }
         }
       }
     }
@@ -319,21 +361,10 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const Log
         publish();
         lp_sync<WARPS>();
         refresh();
-        if (tile == 0 && odd_at >= 0) push(odd, odd_at);
       }
-#pragma unroll
-      for (int j = 0; j < U; ++j) {
-        if (top[j] >= bound_v && top[j] > -LP_FAR) {
-          float x[E];
-          T::unpack(w[j], x);
-          uint32_t hits = 0u;
-#pragma unroll
-          for (int k = 0; k < E; ++k) hits |= x[k] >= bound_v ? 1u << k : 0u;
-          for (; hits; hits &= hits - 1u) {
-            const int i = head + (first + j * TEAM) * E + __ffs(hits) - 1;
-            push(T::load(base, i), i);
-          }
-        }
+      if (all >= bound_v && all > -LP_FAR && (all > bound_v || head + first * E <= lp_index(bound))) {
+        const int p = atomicAdd(&sh.count, 1);
+        if (p < S::CAP) sh.list[p] = make_uint2(ev_ordered(all), static_cast<uint32_t>(first));
       }
     }
   }
@@ -341,8 +372,10 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const Log
   if constexpr (TOP) publish();   // the last bound
   if (TOP && tid < n) sh.top[tid] = 0ull;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    acc.merge(__shfl_down_sync(0xffffffffu, acc.m, o), __shfl_down_sync(0xffffffffu, acc.s, o), __shfl_down_sync(0xffffffffu, acc.x, o), a.c);
+  for (int o = 16; o > 0; o >>= 1) {   // (one reference)
+    acc.s += __shfl_xor_sync(0xffffffffu, acc.s, o);
+    acc.x += __shfl_xor_sync(0xffffffffu, acc.x, o);
+  }
   ahead = __reduce_add_sync(0xffffffffu, ahead);
   bad = __any_sync(0xffffffffu, bad);
   if (lane == 0) {
@@ -358,41 +391,32 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const Log
     refresh();
     const int count = sh.count;
     if (count <= S::CAP) {
-      // those that reach the last bound, each to the place that its rank among them is
-      const unsigned long long* list = sh.list;
-      int m = count;
-      if constexpr (WARPS == 1) {
-        m = 0;
-        for (int i0 = 0; i0 < count; i0 += 32) {
-          const unsigned long long k = i0 + lane < count ? sh.list[i0 + lane] : 0ull;
-          const bool in = k != 0ull && k >= bound;
-          const uint32_t all = __ballot_sync(0xffffffffu, in);
-          if (in) sh.list[m + __popc(all & ((1u << lane) - 1u))] = k;   // (not past what has been read)
-          m += __popc(all);
-          __syncwarp();
+      // the elements of the listed vectors that reach the last bound
+      auto take = [&](float x, int i) {
+        const unsigned long long k = lp_key(x, i);
+        if (x > -LP_FAR && k >= bound) {
+          const int p = atomicAdd(&sh.count2, 1);
+          if (p < S::CAP2) sh.list2[p] = k;
         }
-      } else {
-        for (int i = tid; i < count; i += TEAM) {
-          const unsigned long long k = sh.list[i];
-          if (k >= bound) {
-            const int p = atomicAdd(&sh.count2, 1);
-            if (p < S::CAP2) sh.list2[p] = k;
-          }
-        }
-        __syncthreads();
-        if (sh.count2 <= S::CAP2) {
-          list = sh.list2;
-          m = sh.count2;
-        }
+      };
+      for (int i = tid; i < count * U; i += TEAM) {
+        const uint2 e = sh.list[i / U];
+        const int v = static_cast<int>(e.y) + i % U * TEAM;
+        if (e.x < static_cast<uint32_t>(bound >> 32) || v >= v1) continue;
+        const uint4 w = __ldg(body + v);
+        if (lp_vec_max<T>(w) < bound_v) continue;
+        float x[E];
+        T::unpack(w, x);
+#pragma unroll
+        for (int k = 0; k < E; ++k) take(x[k], head + v * E + k);
       }
-      for (int i = tid; i < m; i += TEAM) {
-        const unsigned long long k = list[i];
-        int r = 0;
-        for (int j = 0; j < m; ++j) r += list[j] > k;
-        if (r < n) sh.top[r] = k;
-      }
+      if (odd_at >= 0) take(odd, odd_at);
+      lp_sync<WARPS>();
+    }
+    if (count <= S::CAP && sh.count2 <= S::CAP2) {
+      lp_order(sh.list2, sh.count2, n, tid, TEAM, sh.top);
     } else {
-      // the list ran over: the largest below the last found, n times
+      // a list ran over: the largest below the last found, n times
       unsigned long long last = ~0ull;
       for (int r = 0; r < n; ++r) {
         unsigned long long best = 0ull;
@@ -402,9 +426,8 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const Log
         };
         if (odd_at >= 0) take(odd, odd_at);
         for (int v = v0 + tid; v < v1; v += TEAM) {
-          const uint4 w = __ldg(body + v);
           float x[E];
-          T::unpack(w, x);
+          T::unpack(__ldg(body + v), x);
 #pragma unroll
           for (int k = 0; k < E; ++k) take(x[k], head + v * E + k);
         }
@@ -426,8 +449,7 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const Log
     __syncthreads();
     if (warp == 0) {   // the CTA's sums, in the first place
       const bool in = lane < WARPS;
-      LpAcc t;
-      t.init();
+      LpAcc t = {-LP_FAR, 0.f, 0.f};
       if (in) t.m = sh.m[lane], t.s = sh.s[lane], t.x = sh.x[lane];
       int before = in ? sh.ahead[lane] : 0;
       bool any = in && sh.bad[lane];
@@ -450,8 +472,7 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const Log
       if (part == 0) {
         if (warp == 0) {
           const bool in = lane < C;
-          LpAcc t;
-          t.init();
+          LpAcc t = {-LP_FAR, 0.f, 0.f};
           int before = 0, any = 0;
           if (in) {
             t.m = __uint_as_float(ld_peer_u32(&sh.m[0], lane));
@@ -479,17 +500,12 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const Log
             const int r = i / n, j = i - r * n;
             const unsigned long long* k = &sh.top[j];
             const uint32_t lo = ld_peer_u32(k, r), hi = ld_peer_u32(reinterpret_cast<const uint32_t*>(k) + 1, r);
-            sh.list[i] = (static_cast<unsigned long long>(hi) << 32) | lo;
+            sh.list2[i] = (static_cast<unsigned long long>(hi) << 32) | lo;
           }
           __syncthreads();
           if (tid < n) sh.top[tid] = 0ull;
           __syncthreads();
-          for (int i = tid; i < n * C; i += TEAM) {
-            const unsigned long long k = sh.list[i];
-            int r = 0;
-            for (int j = 0; j < n * C; ++j) r += sh.list[j] > k;
-            if (k != 0ull && r < n) sh.top[r] = k;
-          }
+          lp_order(sh.list2, n * C, n, tid, TEAM, sh.top);
         }
       }
       cluster_sync_all();   // nobody ends while its shared memory is read
@@ -497,15 +513,15 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const Log
     }
   }
   lp_sync<WARPS>();
-  const int at = C > 1 ? 1 : 0;
-  const float m = sh.m[at], s = sh.s[at];
-  const bool valid = !sh.bad[at] && s > 0.f;
+  const int in = C > 1 ? 1 : 0;
+  const float m = sh.m[in], s = sh.s[in];
+  const bool valid = !sh.bad[in] && s > 0.f;
   const float nan = __int_as_float(0x7fc00000), log_s = log2f(s), ln2 = 0.693147180559945f;
   auto logprob = [&](float x) { return x > -LP_FAR ? (__fmul_rn(__fsub_rn(x, m), a.c) - log_s) * ln2 : kNegInf; };
   if (tid == 0) {
     a.logprobs[place] = valid ? logprob(xt) : nan;
-    if (a.entropy) a.entropy[place] = valid ? fmaxf(log_s - sh.x[at] / s, 0.f) * ln2 : nan;
-    if (a.ranks) a.ranks[place] = valid ? sh.ahead[at] + 1 : -1;
+    if (a.entropy) a.entropy[place] = valid ? fmaxf(log_s - sh.x[in] / s, 0.f) * ln2 : nan;
+    if (a.ranks) a.ranks[place] = valid ? sh.ahead[in] + 1 : -1;
   }
   if (TOP && tid < n) {
     const unsigned long long k = sh.top[tid];
