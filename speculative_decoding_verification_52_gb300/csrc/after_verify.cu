@@ -14,6 +14,7 @@
 #include "spec_verify.h"
 #include "token_logprobs.cuh"
 #include "weigh_q4.cuh"
+#include "weigh_q4_tc.cuh"
 
 namespace {
 
@@ -98,6 +99,37 @@ spec_status_t launch_weigh(int NR, const DevInfo& di, int dev, const WeighArgs& 
     default: return launch_weigh<D, 4>(di, dev, a, st);
   }
 }
+
+template <int D>
+spec_status_t launch_weigh_tc(const DevInfo& di, int dev, const WeighArgs& a, cudaStream_t st) {
+  auto kern = weigh_q4_tc_kernel<D>;
+  TensorMapEncode encode = tensor_map_encode();
+  if (!encode) return fail(SPEC_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+  // the queries as [B][N][Hq][D], in boxes of the nodes and the kv head's query heads of a tile
+  CUtensorMap map;
+  const cuuint64_t heads = static_cast<cuuint64_t>(a.Hkv) * a.G, row = 2 * D;
+  const cuuint64_t dims[4] = {D, heads, static_cast<cuuint64_t>(a.N), static_cast<cuuint64_t>(a.B)};
+  const cuuint64_t strides[3] = {row, row * heads, row * heads * a.N};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(a.G), static_cast<cuuint32_t>(WT_ROWS / a.G), 1}, step[4] = {1, 1, 1, 1};
+  const CUresult r = encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t*>(a.q), dims, strides, box, step,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(SPEC_ERR_CUDA, "cuTensorMapEncodeTiled: %d", static_cast<int>(r));
+  const size_t fixed = (sizeof(WtShared<D>) + 15) / 16 * 16 + 1024 + 8;
+  if (!once_per_device(dev, [&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(fixed + 12 * WG_MAX_B)) == cudaSuccess;
+      }))
+    return fail(SPEC_ERR_CUDA, "weighing setup failed: %s", cudaGetErrorString(cudaGetLastError()));
+  kern<<<static_cast<unsigned>(2 * di.sms), WT_THREADS, fixed + 12 * static_cast<size_t>(a.B), st>>>(a, map);
+  const cudaError_t e = cudaGetLastError();
+  return e == cudaSuccess ? SPEC_OK : cuda_fail(e, "weighing launch");
+}
+
+// Rows of a sequence from which on the tensor cores' kernel is taken.
+#ifndef WT_FROM
+#define WT_FROM 129
+#endif
+constexpr int kWeighTcRows = WT_FROM;
 
 }  // namespace
 
@@ -208,10 +240,12 @@ spec_status_t spec_kv_weigh_q4(const void* q, const float* lse, const int32_t* p
     a.scale_log2 = static_cast<float>(1.4426950408889634 * static_cast<double>(scale));
     a.k_mul = std::ldexp(1.f, k_shift);
     a.decay = decay;
+    a.timeout_ns = kWaitNs;
     const int rows = a.most * a.G, tiles = ceil_div(rows, 32), NR = ceil_div(ceil_div(rows, 8), tiles);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     prof_mark(0, st);
-    s = D == 128 ? launch_weigh<128>(NR, di, dev, a, st) : launch_weigh<64>(NR, di, dev, a, st);
+    if (!path && rows >= kWeighTcRows) s = D == 128 ? launch_weigh_tc<128>(di, dev, a, st) : launch_weigh_tc<64>(di, dev, a, st);
+    else s = D == 128 ? launch_weigh<128>(NR, di, dev, a, st) : launch_weigh<64>(NR, di, dev, a, st);
     if (s != SPEC_OK) return s;
     prof_mark(1, st);
     prof_mark(2, st);

@@ -3,6 +3,7 @@
 // timing hooks of spec_profile_begin / spec_profile_end, argument predicates.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -124,6 +125,23 @@ inline void prof_mark(int slot, cudaStream_t st) {
   if (!g_prof.on || g_prof.calls >= g_prof.max_calls) return;
   cudaEventRecord(g_prof.ev[3 * g_prof.calls + slot], st);
   if (slot == 2) ++g_prof.calls;
+}
+
+// cuTensorMapEncodeTiled, null where the driver has none
+using TensorMapEncode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                     const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                     CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+inline TensorMapEncode tensor_map_encode() {
+  static TensorMapEncode fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    cudaGetLastError();
+    return reinterpret_cast<TensorMapEncode>(p);
+  }();
+  return fn;
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

@@ -39,6 +39,13 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16(uint32_t two) {
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(two)));
   return r;
 }
+__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t x) {
+  uint32_t r;
+  asm("{\n\t.reg .f16 a, b;\n\t.reg .f32 c, d;\n\tmov.b32 {a, b}, %1;\n\tcvt.f32.f16 c, a;\n\tcvt.f32.f16 d, b;\n\t"
+      "cvt.rn.bf16x2.f32 %0, d, c;\n\t}"
+      : "=r"(r) : "r"(x));
+  return r;
+}
 __device__ __forceinline__ uint32_t f16x2_mul(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
@@ -54,5 +61,15 @@ __device__ __forceinline__ uint32_t bf16x2_pack(float lo, float hi) {
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
+
+// sixteen codes (two words) under one scale (twice in s2) to eight f16 pairs
+__device__ __forceinline__ void tc_widen(uint32_t w0, uint32_t w1, uint32_t s2, uint32_t* r) {
+  e2m1x8_to_f16(w0, r);
+  e2m1x8_to_f16(w1, r + 4);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = f16x2_mul(r[i], s2);
+}
+// scale byte g of a word as an f16 pair of equals
+__device__ __forceinline__ uint32_t tc_scale(uint32_t sc, int g) { return e4m3x2_to_f16(__byte_perm(sc, 0u, g * 0x11)); }
 
 }  // namespace sv

@@ -112,22 +112,6 @@ spec_status_t launch_attend(int NR, const DevInfo& di, int dev, const AttendArgs
 // ---------------------------------------------------------------------------
 // attention on the tcgen05 tensor cores
 // ---------------------------------------------------------------------------
-using TensorMapEncode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                                     const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                     CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-TensorMapEncode tensor_map_encode() {
-  static TensorMapEncode fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q{};
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    cudaGetLastError();
-    return reinterpret_cast<TensorMapEncode>(p);
-  }();
-  return fn;
-}
-
 // dynamic shared memory: the layout, its alignment, the batch's prefix sums
 size_t tc_smem_bytes(uint32_t layout, int B) { return layout + 1024 + 8 * (static_cast<size_t>(B) + 1); }
 size_t tc_smem_bytes(int D, int NC, int B) {

@@ -42,6 +42,7 @@ struct WeighArgs {
   int32_t* positions;         // [pages, Hkv, P] or null
   int B, N, PW, most, G, Hkv, P, pages, W;   // most: rows that a sequence may commit
   float scale_log2, k_mul, decay;
+  unsigned long long timeout_ns;
 };
 
 // rows that sequence b commits; -1: nothing is done for it
@@ -56,9 +57,9 @@ __device__ __forceinline__ int wg_rows(const WeighArgs& a, int b) {
   return n;
 }
 
-// prefix[b]: blocks of sequences 0..b-1 (one head), rows[b]: rows of sequence b
+// prefix[b]: tiles (of `tile` tokens) of sequences 0..b-1 (one head), rows[b]: rows of sequence b
 template <int THREADS>
-__device__ void wg_prefix(const WeighArgs& a, long long* prefix, int* rows, long long* scratch) {
+__device__ void wg_prefix(const WeighArgs& a, int tile, long long* prefix, int* rows, long long* scratch) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   long long base = 0;
   for (int b0 = 0; b0 < a.B; b0 += THREADS) {
@@ -67,7 +68,7 @@ __device__ void wg_prefix(const WeighArgs& a, long long* prefix, int* rows, long
     if (b < a.B) {
       const int n = wg_rows(a, b);
       rows[b] = n;
-      v = n < 0 ? 0 : (a.lengths[b] + n + Q4_BLOCK - 1) / Q4_BLOCK;
+      v = n < 0 ? 0 : (static_cast<long long>(a.lengths[b]) + n + tile - 1) / tile;
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -239,7 +240,7 @@ __global__ void __launch_bounds__(WG_THREADS, wg_ctas(NR)) weigh_q4_kernel(const
   __shared__ long long scratch[WG_THREADS / 32];
   long long* prefix = wg_dynamic;                             // [B + 1]
   int* all_rows = reinterpret_cast<int*>(prefix + a.B + 1);   // [B]
-  wg_prefix<WG_THREADS>(a, prefix, all_rows, scratch);
+  wg_prefix<WG_THREADS>(a, Q4_BLOCK, prefix, all_rows, scratch);
   const long long units = prefix[a.B] * a.Hkv;
   const long long warps = static_cast<long long>(gridDim.x) * (WG_THREADS / 32);
   const long long w = static_cast<long long>(threadIdx.x >> 5) * gridDim.x + blockIdx.x;   // (short lists spread over the SMs)
