@@ -22,6 +22,7 @@ using namespace sv;
 using namespace svh;
 
 constexpr int kMaxShift = 32;
+constexpr int kSmemPerSm = 227 * 1024;   // shared memory that the CTAs of an SM can use together
 
 bool q4_dim(int D) { return D == 64 || D == 128; }
 bool below_2g(long long a, long long b) { return a * b < (1LL << 31); }
@@ -81,12 +82,19 @@ spec_status_t launch_logprobs(int dev, bool warp, const LogprobArgs& a, cudaStre
 template <int D, int NR>
 spec_status_t launch_weigh(const DevInfo& di, int dev, const WeighArgs& a, cudaStream_t st) {
   auto kern = weigh_q4_kernel<D, NR>;
-  const size_t smem = 8 * (static_cast<size_t>(a.B) + 1) + 4 * static_cast<size_t>(a.B);
+  constexpr int WARPS = WG_THREADS / 32;
+  // as many CTAs an SM as the registers allow, with two to eight stages; fewer CTAs
+  // where the largest batches leave no room for that (1.25 KB a CTA: the system's and the static part)
+  const size_t fixed = 8 * (static_cast<size_t>(a.B) + 1) + 4 * static_cast<size_t>(a.B), stage = WARPS * (wg_stage_bytes(D) + 8);
+  int ctas = wg_ctas(NR);
+  auto room = [&](int n) { return static_cast<long long>(kSmemPerSm / n) - 1280 - static_cast<long long>(fixed); };
+  while (ctas > 1 && room(ctas) < static_cast<long long>(3 * stage)) --ctas;
+  const int stages = static_cast<int>(std::min<long long>(8, room(ctas) / static_cast<long long>(stage)));
   if (!once_per_device(dev, [&] {
-        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 12 * WG_MAX_B + 8) == cudaSuccess;
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerSm - 1024) == cudaSuccess;
       }))
     return fail(SPEC_ERR_CUDA, "weighing setup failed: %s", cudaGetErrorString(cudaGetLastError()));
-  kern<<<static_cast<unsigned>(di.sms * wg_ctas(NR)), WG_THREADS, smem, st>>>(a);
+  kern<<<static_cast<unsigned>(di.sms * ctas), WG_THREADS, fixed + stages * stage, st>>>(a, stages);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? SPEC_OK : cuda_fail(e, "weighing launch");
 }
@@ -125,11 +133,9 @@ spec_status_t launch_weigh_tc(const DevInfo& di, int dev, const WeighArgs& a, cu
   return e == cudaSuccess ? SPEC_OK : cuda_fail(e, "weighing launch");
 }
 
-// Rows of a sequence from which on the tensor cores' kernel is taken.
-#ifndef WT_FROM
-#define WT_FROM 129
-#endif
-constexpr int kWeighTcRows = WT_FROM;
+// Up to how many rows the other kernel is taken, whose time grows with the rows of a
+// sequence, against the tensor cores', which take 64 in any case.
+constexpr int kWeighFewRows128 = 48, kWeighFewRows64 = 96;
 
 }  // namespace
 
@@ -244,7 +250,7 @@ spec_status_t spec_kv_weigh_q4(const void* q, const float* lse, const int32_t* p
     const int rows = a.most * a.G, tiles = ceil_div(rows, 32), NR = ceil_div(ceil_div(rows, 8), tiles);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     prof_mark(0, st);
-    if (!path && rows >= kWeighTcRows) s = D == 128 ? launch_weigh_tc<128>(di, dev, a, st) : launch_weigh_tc<64>(di, dev, a, st);
+    if (!path && rows > (D == 128 ? kWeighFewRows128 : kWeighFewRows64)) s = D == 128 ? launch_weigh_tc<128>(di, dev, a, st) : launch_weigh_tc<64>(di, dev, a, st);
     else s = D == 128 ? launch_weigh<128>(NR, di, dev, a, st) : launch_weigh<64>(NR, di, dev, a, st);
     if (s != SPEC_OK) return s;
     prof_mark(1, st);

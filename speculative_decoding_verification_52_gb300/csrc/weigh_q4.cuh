@@ -8,10 +8,10 @@
 // This kernel: the tokens are M of mma.m16n8k16, the rows N, eight at a time, as in
 // attend_q4.cuh: a thread's part of a key operand is D / 4 consecutive elements of a
 // token, unpacked in f16 exactly, the queries enter as f16 times a power of two per row.
-// A warp has a share of the list of all blocks (32 tokens of a head) and keeps its
-// queries in registers, up to 32 rows; more rows are taken in turns, over the same keys.
-// A block comes by plain 16-byte loads, 64 bytes of a token side by side, the next one's
-// while this one is weighed.
+// A warp has a share of the list of all blocks (32 tokens of a head), fetches their keys
+// through a ring of its own by bulk copies, and keeps its queries in registers, up to 32
+// rows; more rows are taken in turns, over the same keys.  A sequence's rows are taken
+// in as many groups of eight as it commits, not as the batch might.
 //
 // Bound: the keys' 9/16 byte an element and 8 bytes of weights a token.  A block (D =
 // 128) crosses the bus in about 110 clocks of an SM; it takes 64 conversions and 64
@@ -91,48 +91,13 @@ __device__ void wg_prefix(const WeighArgs& a, int tile, long long* prefix, int* 
   __syncthreads();
 }
 
-// a block as a lane loads it: D / 4 codes and their scales of four tokens
-template <int D>
-struct WgRaw {
-  uint32_t code[4][D / 32];
-  uint32_t scale[4];   // D = 128: two bytes
-  float weight;
-  long long at;        // of the lane's token among the weights; -1: no such page
-};
+// what a warp fetches of a block: codes, scales
+__host__ __device__ constexpr int wg_stage_bytes(int D) { return 18 * D; }
 
-template <int D>
-__device__ __forceinline__ void wg_fetch(const WeighArgs& a, int h, int page, int in_page, int t0, int end, int old, const float* from, WgRaw<D>& r) {
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  r.at = -1;
-  r.weight = 0.f;
-  if (page < 0 || page >= a.pages) return;
-  const unsigned char* blk = q4_block(const_cast<unsigned char*>(a.cache), page, h, in_page, a.Hkv, a.P, D);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int tok = g + 8 * i;
-    const unsigned char* c = blk + tok * (D / 2) + t * (D / 8);
-    if constexpr (D == 128) {
-      const uint4 x = __ldg(reinterpret_cast<const uint4*>(c));
-      r.code[i][0] = x.x, r.code[i][1] = x.y, r.code[i][2] = x.z, r.code[i][3] = x.w;
-      r.scale[i] = __ldg(reinterpret_cast<const uint16_t*>(blk + 32 * D + tok * (D / 16) + t * 2));
-    } else {
-      const uint2 x = __ldg(reinterpret_cast<const uint2*>(c));
-      r.code[i][0] = x.x, r.code[i][1] = x.y;
-      r.scale[i] = __ldg(blk + 32 * D + tok * (D / 16) + t);
-    }
-  }
-  // the token whose sum this lane ends up with
-  const int tok = (t >> 1) * 16 + (t & 1) * 8 + g;
-  if (t0 + tok < end) {
-    r.at = (static_cast<long long>(page) * a.Hkv + h) * a.P + in_page + tok;
-    if (t0 + tok < old) r.weight = from[r.at];
-  }
-}
-
-// rows 8 j + g of a chunk as f16 operands, and for the lane's columns 8 j + 2 t + e the
-// factor to the log2 domain and the row's lse there (infinite: the row adds nothing)
+// rows 8 j + g of a chunk as f16 operands, and for the columns 8 j + 2 t + e the factor to
+// the log2 domain and minus the row's lse there (-inf: the row adds nothing)
 template <int D, int NR>
-__device__ __forceinline__ void wg_load_q(const WeighArgs& a, int b, int h, int row0, int rows, uint32_t (&q)[NR][D / 8], float (&f)[NR][2], float (&l)[NR][2]) {
+__device__ __forceinline__ void wg_load_q(const WeighArgs& a, int b, int h, int row0, int rows, uint32_t (&q)[NR][D / 8], float4* fl) {
   constexpr int CH = D / 4;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
@@ -165,11 +130,10 @@ __device__ __forceinline__ void wg_load_q(const WeighArgs& a, int b, int h, int 
     const int sh = top > 0.f ? min(7 - ex, 100) : 0;
     const float mul = copysignf(__uint_as_float(static_cast<uint32_t>(127 + sh) << 23), a.scale_log2);
     const float back = fminf(fmaxf(fabsf(a.scale_log2) * a.k_mul * __uint_as_float(static_cast<uint32_t>(127 - sh) << 23), 1.17549435e-38f), 3.402823466e+38f);
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      f[j][e] = __shfl_sync(0xffffffffu, back, 8 * t + 4 * e);
-      l[j][e] = __shfl_sync(0xffffffffu, lse, 8 * t + 4 * e);
-    }
+    // (in shared memory: registers are what limits the warps of an SM)
+    const float4 both = make_float4(__shfl_sync(0xffffffffu, back, 8 * t), __shfl_sync(0xffffffffu, back, 8 * t + 4),
+                                    -__shfl_sync(0xffffffffu, lse, 8 * t), -__shfl_sync(0xffffffffu, lse, 8 * t + 4));
+    if (g == 0) fl[4 * j + t] = both;
 #pragma unroll
     for (int i = 0; i < CH / 8; ++i) {
       const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
@@ -179,49 +143,84 @@ __device__ __forceinline__ void wg_load_q(const WeighArgs& a, int b, int h, int 
   }
 }
 
-// the block's sums over a chunk of rows; the lane gets that of its token.  fresh: the
-// position of the block's first token behind the old ones; see: it has such tokens
+// d = A B (+ d); not volatile, so that products of different sums may pass each other
+template <bool ADD>
+__device__ __forceinline__ void wg_mma(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+  if constexpr (ADD)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// A block's sums over a chunk of rows, `groups` times eight of them; the lane gets that
+// of its token, (t >> 1) * 16 + (t & 1) * 8 + g.  from: the block's codes and scales; see:
+// it has tokens that not all rows see, the first `fresh` behind the old ones.
+// (The unpacked keys of sixteen tokens stay in registers while the groups pass by, which
+// a branch for each leaves out: sequences that commit fewer rows cost less.)
 template <int D, int NR>
-__device__ __forceinline__ float wg_block(const WgRaw<D>& r, const uint32_t (&q)[NR][D / 8], const float (&f)[NR][2], const float (&l)[NR][2],
-                                          bool see, int fresh, int row0, int G) {
+__device__ __forceinline__ float wg_block(const unsigned char* from, const uint32_t (&q)[NR][D / 8], const float4* fl,
+                                          int groups, bool see, int fresh, int row0, int G) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   float sum[4];
 #pragma unroll
   for (int m = 0; m < 2; ++m) {
-    float d[NR][4];
+    // eight tokens' rows of codes lie side by side, a quarter a lane; so do their scales
+    uint4 A[D / 16];
+    {
+      uint32_t code[2][D / 32], s2[2];
 #pragma unroll
-    for (int j = 0; j < NR; ++j) d[j][0] = d[j][1] = d[j][2] = d[j][3] = 0.f;
-    uint32_t s0 = e4m3x2_to_f16(r.scale[2 * m]), s1 = e4m3x2_to_f16(r.scale[2 * m + 1]);
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {   // eight codes of each of two tokens: two steps of 16
-      uint32_t lo[4], hi[4];
-      e2m1x8_to_f16(r.code[2 * m][i], lo);
-      e2m1x8_to_f16(r.code[2 * m + 1][i], hi);
-      const uint32_t sel = i < 2 ? 0x1010u : 0x3232u, x0 = __byte_perm(s0, 0u, sel), x1 = __byte_perm(s1, 0u, sel);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        lo[k] = f16x2_mul(lo[k], x0);
-        hi[k] = f16x2_mul(hi[k], x1);
+      for (int u = 0; u < 2; ++u) {
+        const int tok = 16 * m + 8 * u + g;
+        const unsigned char* c = from + tok * (D / 2) + t * (D / 8);
+        if constexpr (D == 128) {
+          const uint4 x = *reinterpret_cast<const uint4*>(c);
+          code[u][0] = x.x, code[u][1] = x.y, code[u][2] = x.z, code[u][3] = x.w;
+          s2[u] = e4m3x2_to_f16(*reinterpret_cast<const uint16_t*>(from + 16 * D + tok * (D / 16) + t * 2));
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2*>(c);
+          code[u][0] = x.x, code[u][1] = x.y;
+          s2[u] = e4m3x2_to_f16(from[16 * D + tok * (D / 16) + t]);
+        }
       }
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const uint4 A = make_uint4(lo[2 * k], hi[2 * k], lo[2 * k + 1], hi[2 * k + 1]);
+      for (int i = 0; i < D / 32; ++i) {   // eight codes of each of two tokens: two steps of 16
+        uint32_t lo[4], hi[4];
+        e2m1x8_to_f16(code[0][i], lo);
+        e2m1x8_to_f16(code[1][i], hi);
+        const uint32_t sel = i < 2 ? 0x1010u : 0x3232u, x0 = __byte_perm(s2[0], 0u, sel), x1 = __byte_perm(s2[1], 0u, sel);
 #pragma unroll
-        for (int j = 0; j < NR; ++j) mma_f16(d[j], A, q[j][4 * i + 2 * k], q[j][4 * i + 2 * k + 1]);
+        for (int k = 0; k < 2; ++k)
+          A[2 * i + k] = make_uint4(f16x2_mul(lo[2 * k], x0), f16x2_mul(hi[2 * k], x1), f16x2_mul(lo[2 * k + 1], x0), f16x2_mul(hi[2 * k + 1], x1));
       }
     }
     // a score that is no number weighs nothing
     float x[2] = {0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < NR; ++j)
+    for (int j = 0; j < NR; ++j) {
+      if (j > 0 && j >= groups) break;
+      const float4 c = fl[4 * j + t];
+      float d[4], e[4];   // (two chains of products)
+      wg_mma<false>(d, A[0], q[j][0], q[j][1]);
+      wg_mma<false>(e, A[1], q[j][2], q[j][3]);
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
+      for (int k = 2; k < D / 16; k += 2) {
+        wg_mma<true>(d, A[k], q[j][2 * k], q[j][2 * k + 1]);
+        wg_mma<true>(e, A[k + 1], q[j][2 * k + 2], q[j][2 * k + 3]);
+      }
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          float z = fmaxf(__fmaf_rn(d[j][e + 2 * u], f[j][e], -l[j][e]), kNegInf);
-          if (see && (fresh + 16 * m + 8 * u + g) * G > row0 + 8 * j + 2 * t + e) z = kNegInf;
-          x[u] += ex2_approx(z);
-        }
+      for (int k = 0; k < 4; ++k) d[k] += e[k];
+      if (see) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if ((fresh + 16 * m + 8 * (k >> 1) + g) * G > row0 + 8 * j + 2 * t + (k & 1)) d[k] = kNegInf;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k >> 1] += ex2_approx(fmaxf(__fmaf_rn(d[k], k & 1 ? c.y : c.x, k & 1 ? c.w : c.z), kNegInf));
+    }
     sum[2 * m] = x[0];
     sum[2 * m + 1] = x[1];
   }
@@ -232,22 +231,33 @@ __device__ __forceinline__ float wg_block(const WgRaw<D>& r, const uint32_t (&q)
   return (odd ? y1 : y0) + __shfl_xor_sync(0xffffffffu, odd ? y0 : y1, 1);
 }
 
-__host__ __device__ constexpr int wg_ctas(int NR) { return NR <= 2 ? 5 : NR == 3 ? 4 : 3; }
+__host__ __device__ constexpr int wg_ctas(int NR) { return NR == 1 ? 5 : NR <= 3 ? 4 : 3; }
 
 template <int D, int NR>
-__global__ void __launch_bounds__(WG_THREADS, wg_ctas(NR)) weigh_q4_kernel(const WeighArgs a) {
-  extern __shared__ long long wg_dynamic[];
+__global__ void __launch_bounds__(WG_THREADS, wg_ctas(NR)) weigh_q4_kernel(const WeighArgs a, int stages) {
+  extern __shared__ uint4 wg_dynamic[];
   __shared__ long long scratch[WG_THREADS / 32];
-  long long* prefix = wg_dynamic;                             // [B + 1]
-  int* all_rows = reinterpret_cast<int*>(prefix + a.B + 1);   // [B]
-  wg_prefix<WG_THREADS>(a, Q4_BLOCK, prefix, all_rows, scratch);
-  const long long units = prefix[a.B] * a.Hkv;
-  const long long warps = static_cast<long long>(gridDim.x) * (WG_THREADS / 32);
-  const long long w = static_cast<long long>(threadIdx.x >> 5) * gridDim.x + blockIdx.x;   // (short lists spread over the SMs)
-  const int lane = threadIdx.x & 31, t = lane & 3, g = lane >> 2;
+  constexpr int WARPS = WG_THREADS / 32;
+  __shared__ float4 fl[WARPS][4 * NR];   // of the columns of a lane: factors, -lse
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = lane & 3, g = lane >> 2;
   const int tok = (t >> 1) * 16 + (t & 1) * 8 + g;
+  unsigned char* ring = reinterpret_cast<unsigned char*>(wg_dynamic) + warp * stages * wg_stage_bytes(D);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<unsigned char*>(wg_dynamic) + WARPS * stages * wg_stage_bytes(D));
+  long long* prefix = reinterpret_cast<long long*>(bars + WARPS * stages);   // [B + 1]
+  int* all_rows = reinterpret_cast<int*>(prefix + a.B + 1);                  // [B]
+  for (int i = threadIdx.x; i < WARPS * stages; i += WG_THREADS) mbar_init(bars + i, 1);
+  mbar_fence_init();
+  bars += warp * stages;
+  wg_prefix<WG_THREADS>(a, Q4_BLOCK, prefix, all_rows, scratch);   // (synchronises the CTA)
+  const long long units = prefix[a.B] * a.Hkv;
+  const long long warps = static_cast<long long>(gridDim.x) * WARPS;
+  const long long w = static_cast<long long>(warp) * gridDim.x + blockIdx.x;   // (short lists spread over the SMs)
   long long u = units * w / warps;
   const long long u1 = units * (w + 1) / warps;
+  const int per = a.P / Q4_BLOCK;
+  int stage = 0;
+  uint32_t parity = 0u;
+  bool alive = true;
   while (u < u1) {
     int lo = 0, hi = a.B - 1;   // last b with prefix[b] * Hkv <= u that has blocks
     while (lo < hi) {
@@ -255,6 +265,7 @@ __global__ void __launch_bounds__(WG_THREADS, wg_ctas(NR)) weigh_q4_kernel(const
       if (prefix[mid] * a.Hkv <= u) lo = mid;
       else hi = mid - 1;
     }
+    // blocks [k0, k1) of head h of sequence b, in several passes where the rows are many
     const int b = lo, blocks = static_cast<int>(prefix[b + 1] - prefix[b]);
     const long long rem = u - prefix[b] * a.Hkv;
     const int h = static_cast<int>(rem / blocks), k0 = static_cast<int>(rem - static_cast<long long>(h) * blocks);
@@ -262,26 +273,80 @@ __global__ void __launch_bounds__(WG_THREADS, wg_ctas(NR)) weigh_q4_kernel(const
     u += k1 - k0;
     const int n = all_rows[b], old = a.lengths[b], end = old + n, rows = n * a.G;
     const int32_t* table = a.table + static_cast<long long>(b) * a.W;
+    const int first = (a.first ? a.first[b] : old) - old;
     for (int row0 = 0; row0 == 0 || row0 < rows; row0 += 8 * NR) {
+      // The places of 32 blocks, a lane each (the block's number among the pool's, ~0: on
+      // no page): of those from `look` on, to fetch; and of those from `have` on, to weigh.
+      auto places = [&](int from) {
+        uint32_t x = ~0u;
+        if (from + lane < k1) {
+          const int e = (from + lane) / per, page = table[e];
+          if (page >= 0 && page < a.pages) x = (static_cast<uint32_t>(page) * a.Hkv + h) * per + (from + lane - e * per);
+        }
+        return x;
+      };
+      int look = k0, ahead = 0;   // ahead: blocks of the run that have been fetched
+      uint32_t blk = places(k0), now = blk;
+      auto fetch = [&](int s) {
+        if (k0 + ahead - look == 32) {
+          look += 32;
+          blk = places(look);
+        }
+        const uint32_t x = __shfl_sync(0xffffffffu, blk, k0 + ahead - look);
+        if (lane == 0) {
+          if (x != ~0u) {
+            const unsigned char* from = a.cache + static_cast<unsigned long long>(x) * q4_block_bytes(D);
+            unsigned char* to = ring + s * wg_stage_bytes(D);
+            mbar_arrive_expect_tx(bars + s, wg_stage_bytes(D));
+            bulk_g2s(to, from, 16 * D, bars + s);
+            bulk_g2s(to + 16 * D, from + 32 * D, 2 * D, bars + s);
+          } else {
+            mbar_arrive(bars + s);
+          }
+        }
+        ++ahead;
+      };
+      for (int i = 0, s = stage; i < stages && k0 + i < k1 && alive; ++i) {
+        fetch(s);
+        if (++s == stages) s = 0;
+      }
       uint32_t q[NR][D / 8];
-      float f[NR][2], l[NR][2];
-      wg_load_q<D, NR>(a, b, h, row0, rows, q, f, l);
+      wg_load_q<D, NR>(a, b, h, row0, rows, q, fl[warp]);
+      __syncwarp();
+      const int groups = (min(rows - row0, 8 * NR) + 7) / 8;
       const float* from = row0 == 0 ? a.weights : a.new_weights;
       const int begun = row0 == 0 ? old : end;   // tokens that have a weight
       const float decay = row0 == 0 ? a.decay : 1.f;
-      WgRaw<D> next;
-      int page = table[k0 * Q4_BLOCK / a.P];
-      wg_fetch<D>(a, h, page, k0 * Q4_BLOCK % a.P, k0 * Q4_BLOCK, end, begun, from, next);
-      page = k0 + 1 < k1 ? table[(k0 + 1) * Q4_BLOCK / a.P] : -1;
       for (int k = k0; k < k1; ++k) {
-        const WgRaw<D> now = next;
-        const int t0 = k * Q4_BLOCK;
-        if (k + 1 < k1) wg_fetch<D>(a, h, page, (t0 + Q4_BLOCK) % a.P, t0 + Q4_BLOCK, end, begun, from, next);
-        page = k + 2 < k1 ? table[(t0 + 2 * Q4_BLOCK) / a.P] : -1;
-        const float x = wg_block<D, NR>(now, q, f, l, t0 + Q4_BLOCK > old, t0 - old, row0, a.G);
-        if (now.at >= 0) {
-          a.new_weights[now.at] = t0 + tok < begun ? __fmaf_rn(decay, now.weight, x) : x;
-          if (row0 == 0 && a.positions && t0 + tok >= old) a.positions[now.at] = (a.first ? a.first[b] : old) + (t0 + tok - old);
+        if (k > k0 && ((k - k0) & 31) == 0) now = look == k ? blk : places(k);
+        const uint32_t x = __shfl_sync(0xffffffffu, now, (k - k0) & 31);
+        const int pos = k * Q4_BLOCK + tok;
+        const long long at = static_cast<long long>(x) * Q4_BLOCK + tok;
+        const bool mine = x != ~0u && pos < end;
+        float had = 0.f;
+        if (mine && pos < begun) had = from[at];
+        if (alive && !__all_sync(0xffffffffu, mbar_wait(bars + stage, parity, a.timeout_ns))) alive = false;
+        float sum = wg_block<D, NR>(ring + stage * wg_stage_bytes(D), q, fl[warp], groups, (k + 1) * Q4_BLOCK > old, k * Q4_BLOCK - old, row0, a.G);
+        __syncwarp();
+        if (alive && k0 + ahead < k1) fetch(stage);
+        if (!alive) sum = __int_as_float(0x7fc00000);
+        if (mine) {
+          a.new_weights[at] = pos < begun ? __fmaf_rn(decay, had, sum) : sum;
+          if (row0 == 0 && a.positions && pos >= old) a.positions[at] = first + pos;
+        }
+        if (++stage == stages) {
+          stage = 0;
+          parity ^= 1u;
+        }
+        if (!alive) {   // copies that are still on their way
+          for (int i = k + 1; i < k0 + ahead; ++i) {
+            mbar_wait(bars + stage, parity, a.timeout_ns);
+            if (++stage == stages) {
+              stage = 0;
+              parity ^= 1u;
+            }
+          }
+          ahead = 0;
         }
       }
     }
