@@ -354,7 +354,7 @@ spec_status_t spec_kv_move_q4(void* cache, float* weights, int32_t* positions, c
     a.pages = num_pages;
     a.max_moves = max_moves;
     // enough CTAs a head for its longest list, no more than fill the device
-    const long long want = ceil_div(max_moves, MV_THREADS / 16), room = std::max<long long>(1, di.sms * 16 / pairs);
+    const long long want = ceil_div(max_moves, MV_THREADS), room = std::max<long long>(1, di.sms * 16 / pairs);
     const dim3 grid(static_cast<unsigned>(pairs), static_cast<unsigned>(std::min(std::min(want, room), 65535LL)));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     prof_mark(0, st);

@@ -426,13 +426,16 @@ __global__ void __launch_bounds__(EV_THREADS, 4) evict_plan_kernel(const PlanArg
 }
 
 // ---------------------------------------------------------------------------
-// The moves.  Sixteen lanes take one: its codes in 16-byte pieces, its two groups of
-// scales, its weight and its position.  No place that a plan names is source and
-// destination, so there is no order.  Bound: the bus, by sectors of 32 bytes, of which
-// the scales, the weight and the position fill an eighth or a quarter: 256 bytes read
-// and 256 written for a move of 152 (D = 128).
+// The moves.  A warp takes 32: a lane looks up where one of them goes, then sixteen lanes
+// carry one, its codes in 16-byte pieces, its two groups of scales, its weight and its
+// position, MV_AHEAD of them under way at a time.  No place that a plan names is source
+// and destination, so there is no order.  Bound: the bus, by sectors of 32 bytes, of
+// which the scales, the weight and the position fill an eighth or a quarter: 256 bytes
+// read and 256 written for a move of 152 (D = 128).  (With the places' divisions done by
+// all lanes of a move, they were two thirds of 40 us for 64 heads of about 3,500 moves.)
 // ---------------------------------------------------------------------------
 constexpr int MV_THREADS = 256;
+constexpr int MV_AHEAD = 4;
 
 struct MoveArgs {
   unsigned char* cache;       // [pages, Hkv, P / 32, 36 D]
@@ -446,12 +449,14 @@ struct MoveArgs {
 template <int D>
 __global__ void __launch_bounds__(MV_THREADS) kv_move_q4_kernel(const MoveArgs a) {
   constexpr int PIECES = D / 32;   // of a token's key or value codes
-  const int pair = blockIdx.x, h = pair % a.Hkv, l = threadIdx.x & 15;
-  const int count = min(a.counts[pair], a.max_moves);
+  const int pair = blockIdx.x, h = pair % a.Hkv, lane = threadIdx.x & 31, l = lane & 15;
+  const int count = min(a.counts[pair], a.max_moves), per = a.P / Q4_BLOCK;
   const long long slots = static_cast<long long>(a.pages) * a.P;
   const int2* moves = reinterpret_cast<const int2*>(a.moves) + static_cast<long long>(pair) * a.max_moves;
-  // what the lane carries: its bytes, and where they are in a block
+  // what the lane carries: its bytes, and where they are: in a block, or in the weights or positions
   int bytes = 0, at = 0, each = 0;
+  unsigned char* base = a.cache;
+  unsigned long long block = q4_block_bytes(D);
   if (l < 2 * PIECES) {
     bytes = 16;
     at = (l / PIECES) * (Q4_BLOCK * D / 2) + (l % PIECES) * 16;
@@ -460,22 +465,49 @@ __global__ void __launch_bounds__(MV_THREADS) kv_move_q4_kernel(const MoveArgs a
     bytes = D / 16;
     at = Q4_BLOCK * D + (l - 8) * (Q4_BLOCK * D / 16);
     each = D / 16;
+  } else if (l == 10 || l == 11) {
+    base = l == 10 ? reinterpret_cast<unsigned char*>(a.weights) : reinterpret_cast<unsigned char*>(a.positions);
+    bytes = base ? 4 : 0;
+    block = 4 * Q4_BLOCK;
+    each = 4;
   }
-  const bool weight = l == 10 && a.weights, position = l == 11 && a.positions;
-  for (int i = blockIdx.y * (MV_THREADS / 16) + (threadIdx.x >> 4); i < count; i += gridDim.y * (MV_THREADS / 16)) {
-    const int2 m = __ldg(moves + i);
-    if (m.x < 0 || m.y < 0 || m.x >= slots || m.y >= slots) continue;
-    const int p0 = m.x / a.P, t0 = m.x - p0 * a.P, p1 = m.y / a.P, t1 = m.y - p1 * a.P;
-    if (bytes) {
-      const unsigned char* src = q4_block(a.cache, p0, h, t0, a.Hkv, a.P, D) + at + (t0 % Q4_BLOCK) * each;
-      unsigned char* dst = q4_block(a.cache, p1, h, t1, a.Hkv, a.P, D) + at + (t1 % Q4_BLOCK) * each;
-      if (bytes == 16) *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(src);
-      else if (bytes == 8) *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(src);
-      else *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(src);
-    } else if (weight || position) {
-      const long long from = (static_cast<long long>(p0) * a.Hkv + h) * a.P + t0, to = (static_cast<long long>(p1) * a.Hkv + h) * a.P + t1;
-      if (weight) a.weights[to] = a.weights[from];
-      else a.positions[to] = a.positions[from];
+  for (int i0 = 32 * (blockIdx.y * (MV_THREADS / 32) + (threadIdx.x >> 5)); i0 < count; i0 += 32 * gridDim.y * (MV_THREADS / 32)) {
+    // the lane's move: numbers of the blocks among the pool's, rows in them; ~0: none
+    uint32_t from = ~0u, to = 0u, rows = 0u;
+    if (i0 + lane < count) {
+      const int2 m = __ldg(moves + i0 + lane);
+      if (m.x >= 0 && m.y >= 0 && m.x < slots && m.y < slots) {
+        const int b0 = m.x / Q4_BLOCK, p0 = b0 / per, b1 = m.y / Q4_BLOCK, p1 = b1 / per;
+        from = (static_cast<uint32_t>(p0) * a.Hkv + h) * per + (b0 - p0 * per);
+        to = (static_cast<uint32_t>(p1) * a.Hkv + h) * per + (b1 - p1 * per);
+        rows = (m.x % Q4_BLOCK) | (m.y % Q4_BLOCK) << 8;
+      }
+    }
+    const int n = min(32, count - i0);
+    for (int j0 = 0; j0 < n; j0 += 2 * MV_AHEAD) {
+      uint4 x[MV_AHEAD];
+      unsigned char* dst[MV_AHEAD];
+#pragma unroll
+      for (int u = 0; u < MV_AHEAD; ++u) {
+        const int j = j0 + 2 * u + (lane >> 4);
+        const uint32_t b0 = __shfl_sync(0xffffffffu, from, j), b1 = __shfl_sync(0xffffffffu, to, j), r = __shfl_sync(0xffffffffu, rows, j);
+        const bool go = b0 != ~0u && bytes;
+        const unsigned char* src = base + b0 * block + at + (r & 255u) * each;
+        dst[u] = go ? base + b1 * block + at + (r >> 8) * each : nullptr;
+        x[u] = make_uint4(0u, 0u, 0u, 0u);
+        if (go) {
+          if (bytes == 16) x[u] = *reinterpret_cast<const uint4*>(src);
+          else if (bytes == 8) *reinterpret_cast<uint2*>(&x[u]) = *reinterpret_cast<const uint2*>(src);
+          else x[u].x = *reinterpret_cast<const uint32_t*>(src);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < MV_AHEAD; ++u) {
+        if (!dst[u]) continue;
+        if (bytes == 16) *reinterpret_cast<uint4*>(dst[u]) = x[u];
+        else if (bytes == 8) *reinterpret_cast<uint2*>(dst[u]) = make_uint2(x[u].x, x[u].y);
+        else *reinterpret_cast<uint32_t*>(dst[u]) = x[u].x;
+      }
     }
   }
 }
