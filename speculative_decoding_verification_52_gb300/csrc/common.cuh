@@ -214,11 +214,11 @@ __device__ __forceinline__ uint32_t ld_peer_u32(const void* local, uint32_t peer
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote) : "memory");
   return v;
 }
-__device__ __forceinline__ uint4 ld_peer_u128(const void* local, uint32_t peer) {
+__device__ __forceinline__ unsigned long long ld_peer_u64(const void* local, uint32_t peer) {
   uint32_t remote;
-  uint4 v;
+  unsigned long long v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(smem_addr(local)), "r"(peer));
-  asm volatile("ld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(remote) : "memory");
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(remote) : "memory");
   return v;
 }
 

@@ -156,11 +156,12 @@ struct LpShared {
   static constexpr int CAP2 = WARPS == 1 ? 128 : 512;   // elements that reach the last bound
   uint2 list[CAP];   // of what a thread had of a tile: the largest element (ordered), the first vector
   unsigned long long list2[CAP2];
-  unsigned long long bound[2][WARPS];   // two, so that a warp that is a step ahead does not change what another reads
+  uint32_t picked[CAP];   // of the list, what reaches the last bound: the first vectors
+  unsigned long long bound[WARPS];
   unsigned long long top[LP_MAX_TOP];
   float m[WARPS], s[WARPS], x[WARPS];
   int ahead[WARPS], bad[WARPS];
-  int count, count2;
+  int count, count2, count3;
 };
 
 // the first n of m different keys, in order; `each` threads (a power of two) count for one
@@ -172,7 +173,7 @@ __device__ __forceinline__ void lp_order(const unsigned long long* list, int m, 
     const int i = i0 + tid / each;
     const unsigned long long k = i < m ? list[i] : 0ull;
     int r = 0;
-#pragma unroll 4
+#pragma unroll 8
     for (int j = sub; j < m; j += each) r += list[j] > k;
     for (int o = each >> 1; o > 0; o >>= 1) r += __shfl_xor_sync(0xffffffffu, r, o);
     if (sub == 0 && k != 0ull && r < n) top[r] = k;
@@ -230,7 +231,7 @@ __global__ void __launch_bounds__(lp_threads(WARPS), 1024 / lp_threads(WARPS)) t
   constexpr uint32_t ULP = T::esz == 2 ? 0x10000u : 1u;
   const float below = __uint_as_float(xt == 0.f ? 0x80000000u + ULP : xt > 0.f ? __float_as_uint(xt) - ULP : __float_as_uint(xt) + ULP);
 
-  if (tid == 0) sh.count = sh.count2 = 0;
+  if (tid == 0) sh.count = sh.count2 = sh.count3 = 0;
   LpAcc acc = {-LP_FAR, 0.f, 0.f};   // (m: the warp's)
   float most = -LP_FAR;   // the largest of the thread's elements, and the last index of its tile
   int at = 0;
@@ -253,16 +254,14 @@ __global__ void __launch_bounds__(lp_threads(WARPS), 1024 / lp_threads(WARPS)) t
   // threads' largest elements reach; 0 while some warp has none.
   unsigned long long bound = 0ull;
   float bound_v = -LP_FAR;
-  int turn = 0;
   auto publish = [&]() {
     const int k = (n + WARPS - 1) / WARPS;
     const uint32_t mine = most > -LP_FAR ? ev_ordered(most) : 0u, v = warp_kth(mine, k);
     const uint32_t last = __reduce_max_sync(0xffffffffu, mine == v ? static_cast<uint32_t>(at) : 0u);
-    turn ^= 1;
-    if (lane == 0) sh.bound[turn][warp] = v == 0u ? 0ull : (static_cast<unsigned long long>(v) << 32) | static_cast<uint32_t>(~last);
+    if (lane == 0) *const_cast<volatile unsigned long long*>(&sh.bound[warp]) = v == 0u ? 0ull : (static_cast<unsigned long long>(v) << 32) | static_cast<uint32_t>(~last);
   };
   auto refresh = [&]() {
-    const unsigned long long k = sh.bound[turn][lane % WARPS];
+    const unsigned long long k = *const_cast<volatile unsigned long long*>(&sh.bound[lane % WARPS]);
     const uint32_t hi = __reduce_min_sync(0xffffffffu, static_cast<uint32_t>(k >> 32));
     const uint32_t lo = __reduce_min_sync(0xffffffffu, static_cast<uint32_t>(k >> 32) == hi ? static_cast<uint32_t>(k) : 0xffffffffu);
     bound = (static_cast<unsigned long long>(hi) << 32) | lo;
@@ -357,9 +356,12 @@ __global__ void __launch_bounds__(lp_threads(WARPS), 1024 / lp_threads(WARPS)) t
       }
     }
     if constexpr (TOP) {
-      if ((tile & (tile + 1)) == 0 || bound == 0ull) {   // (alike in the whole team)
+      // (A bound only rises: one that another warp has not renewed yet serves, too.  The
+      // first tile's are waited for.)
+      if ((tile & (tile + 1)) == 0 || bound == 0ull) {
         publish();
-        lp_sync<WARPS>();
+        if (tile == 0) lp_sync<WARPS>();
+        else __syncwarp();
         refresh();
       }
       if (all >= bound_v && all > -LP_FAR && (all > bound_v || head + first * E <= lp_index(bound))) {
@@ -392,25 +394,41 @@ __global__ void __launch_bounds__(lp_threads(WARPS), 1024 / lp_threads(WARPS)) t
     const int count = sh.count;
     if (count <= S::CAP) {
       // the elements of the listed vectors that reach the last bound
-      auto take = [&](float x, int i) {
-        const unsigned long long k = lp_key(x, i);
-        if (x > -LP_FAR && k >= bound) {
-          const int p = atomicAdd(&sh.count2, 1);
-          if (p < S::CAP2) sh.list2[p] = k;
-        }
-      };
-      for (int i = tid; i < count * U; i += TEAM) {
-        const uint2 e = sh.list[i / U];
-        const int v = static_cast<int>(e.y) + i % U * TEAM;
-        if (e.x < static_cast<uint32_t>(bound >> 32) || v >= v1) continue;
-        const uint4 w = __ldg(body + v);
-        if (lp_vec_max<T>(w) < bound_v) continue;
-        float x[E];
-        T::unpack(w, x);
-#pragma unroll
-        for (int k = 0; k < E; ++k) take(x[k], head + v * E + k);
+      for (int i = tid; i < count; i += TEAM) {
+        const uint2 e = sh.list[i];
+        if (e.x >= static_cast<uint32_t>(bound >> 32)) sh.picked[atomicAdd(&sh.count3, 1)] = e.y;
       }
-      if (odd_at >= 0) take(odd, odd_at);
+      lp_sync<WARPS>();
+      // a vector a thread, so that all are loaded at once, and the odd elements' thread;
+      // places for a warp's elements by one addition
+      const int picked = sh.count3 * U;
+      for (int i0 = 0; i0 < max(picked, 1); i0 += TEAM) {   // (whole warps go on alike)
+        const int i = i0 + tid, v = i < picked ? static_cast<int>(sh.picked[i / U]) + i % U * TEAM : v1;
+        float x[E];
+        T::unpack(v < v1 ? __ldg(body + v) : lp_nothing<T>(), x);
+        const bool more = i0 == 0 && odd_at >= 0;
+        uint32_t hits = more && odd > -LP_FAR && lp_key(odd, odd_at) >= bound ? 1u << E : 0u;
+#pragma unroll
+        for (int k = 0; k < E; ++k) hits |= x[k] >= bound_v && x[k] > -LP_FAR && lp_key(x[k], head + v * E + k) >= bound ? 1u << k : 0u;
+        const int mine = __popc(hits);
+        int before = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, before, o);
+          if (lane >= o) before += y;
+        }
+        int p = 0;
+        if (lane == 31 && before) p = atomicAdd(&sh.count2, before);
+        p = __shfl_sync(0xffffffffu, p, 31) + before - mine;
+        for (; hits; hits &= hits - 1u) {
+          const int k = __ffs(hits) - 1;
+          float y = odd;
+#pragma unroll
+          for (int e = 0; e < E; ++e) y = e == k ? x[e] : y;
+          if (p < S::CAP2) sh.list2[p] = lp_key(y, k < E ? head + v * E + k : odd_at);
+          ++p;
+        }
+      }
       lp_sync<WARPS>();
     }
     if (count <= S::CAP && sh.count2 <= S::CAP2) {
@@ -435,9 +453,9 @@ __global__ void __launch_bounds__(lp_threads(WARPS), 1024 / lp_threads(WARPS)) t
         for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
         if constexpr (WARPS > 1) {
           __syncthreads();
-          if (lane == 0) sh.bound[0][warp] = best;
+          if (lane == 0) sh.bound[warp] = best;
           __syncthreads();
-          for (int w = 0; w < WARPS; ++w) best = max(best, sh.bound[0][w]);
+          for (int w = 0; w < WARPS; ++w) best = max(best, sh.bound[w]);
         }
         if (tid == 0) sh.top[r] = best;
         last = best;
@@ -498,9 +516,7 @@ __global__ void __launch_bounds__(lp_threads(WARPS), 1024 / lp_threads(WARPS)) t
         if constexpr (TOP) {
           for (int i = tid; i < n * C; i += TEAM) {
             const int r = i / n, j = i - r * n;
-            const unsigned long long* k = &sh.top[j];
-            const uint32_t lo = ld_peer_u32(k, r), hi = ld_peer_u32(reinterpret_cast<const uint32_t*>(k) + 1, r);
-            sh.list2[i] = (static_cast<unsigned long long>(hi) << 32) | lo;
+            sh.list2[i] = ld_peer_u64(&sh.top[j], r);
           }
           __syncthreads();
           if (tid < n) sh.top[tid] = 0ull;
