@@ -637,14 +637,13 @@ def spec_token_logprobs(logits, tokens, temperature: float = 1.0, *, path=None, 
         raise ValueError(f"logits must be [B, R, V] and tokens [B, M], got {tuple(logits.shape)} and {tuple(tokens.shape)}")
     B, R, V = logits.shape
     M = tokens.shape[1]
-    i32, f32, two, three, n, m = torch.int32, torch.float32, (B, M), (B, M, top_n), B * M, top_n
-    if logprobs is entropy is ranks is top_tokens is top_logprobs is None and m >= 0:   # parts of one allocation
-        new = torch.empty(n * (3 + 2 * m), dtype=f32, device=logits.device)
-        at = new.data_ptr()
-        to = (at, at + 4 * n, at + 4 * n * (2 + m), at + 4 * n * (3 + m), at + 8 * n)
-        logprobs, entropy, top_logprobs = new.as_strided(two, (M, 1)), new.as_strided(two, (M, 1), n), new.as_strided(three, (M * m, m, 1), 2 * n)
-        whole = new.view(i32)
-        ranks, top_tokens = whole.as_strided(two, (M, 1), n * (2 + m)), whole.as_strided(three, (M * m, m, 1), n * (3 + m))
+    i32, f32, two, three = torch.int32, torch.float32, (B, M), (B, M, top_n)
+    if logprobs is entropy is ranks is top_tokens is top_logprobs is None:   # (allocations are cheaper than views of one)
+        on = logits.device
+        logprobs, entropy = torch.empty(two, dtype=f32, device=on), torch.empty(two, dtype=f32, device=on)
+        ranks, top_tokens = torch.empty(two, dtype=i32, device=on), torch.empty(three, dtype=i32, device=on)
+        top_logprobs = torch.empty(three, dtype=f32, device=on)
+        to = (logprobs.data_ptr(), entropy.data_ptr(), ranks.data_ptr(), top_tokens.data_ptr(), top_logprobs.data_ptr())
     else:
         logprobs, entropy, ranks, top_tokens, top_logprobs = out = tuple(
             torch.empty(shape, dtype=dt, device=logits.device) if t is None else t for t, shape, dt in (
@@ -708,12 +707,9 @@ def spec_kv_evict_plan(weights, positions, block_table, lengths, budgets, next_p
     else:
         moves = torch.empty((B, Hkv, max_moves, 2), dtype=i32, device=weights.device)
     one, slots, table = (B,), (pages, Hkv, P), _cols(block_table, B, "block_table")
-    if move_counts is None and new_lengths is None:   # parts of one allocation
-        new = torch.empty(B * (Hkv + 1), dtype=i32, device=weights.device)
-        move_counts, new_lengths = new.as_strided((B, Hkv), (Hkv, 1)), new.as_strided(one, (1,), B * Hkv)
-    elif move_counts is None:
+    if move_counts is None:
         move_counts = torch.empty((B, Hkv), dtype=i32, device=weights.device)
-    elif new_lengths is None:
+    if new_lengths is None:
         new_lengths = torch.empty(one, dtype=i32, device=weights.device)
     st = (_lib or lib()).spec_kv_evict_plan(
         _take(weights, "weights", torch.float32, slots, dev), _take(positions, "positions", i32, slots, dev),
@@ -750,11 +746,11 @@ def spec_page_trim(tokens, held, ring, ring_state, block_table, page_tokens: int
     """Gives the pages that tokens [B] int32 do not need back to spec_page_map's ring
     (updated in place).  Returns (new_held [B], new_ring_state [2], status [B]) int32."""
     i32, B = torch.int32, tokens.numel()
-    if new_held is new_ring_state is status is None:   # parts of one allocation
-        new = torch.empty(2 * B + 2, dtype=i32, device=tokens.device)
-        at = new.data_ptr()
-        new_held, status, new_ring_state = new.split_with_sizes((B, B, 2))
-        to = (at, at + 8 * B, at + 4 * B)
+    if new_held is new_ring_state is status is None:
+        on = tokens.device
+        new_held, new_ring_state, status = (torch.empty(B, dtype=i32, device=on), torch.empty(2, dtype=i32, device=on),
+                                            torch.empty(B, dtype=i32, device=on))
+        to = (new_held.data_ptr(), new_ring_state.data_ptr(), status.data_ptr())
     else:
         new_held, new_ring_state, status = out = tuple(
             torch.empty(n, dtype=i32, device=tokens.device) if t is None else t for t, n in ((new_held, B), (new_ring_state, 2), (status, B)))
