@@ -84,14 +84,14 @@ spec_status_t launch_weigh(const DevInfo& di, int dev, const WeighArgs& a, cudaS
   auto kern = weigh_q4_kernel<D, NR>;
   constexpr int WARPS = WG_THREADS / 32;
   // as many CTAs an SM as the registers allow, with two to eight stages; fewer CTAs
-  // where the largest batches leave no room for that (1.25 KB a CTA: the system's and the static part)
+  // where the largest batches leave no room for that (2.25 KB a CTA: the system's and the static part)
   const size_t fixed = 8 * (static_cast<size_t>(a.B) + 1) + 4 * static_cast<size_t>(a.B), stage = WARPS * (wg_stage_bytes(D) + 8);
   int ctas = wg_ctas(NR);
-  auto room = [&](int n) { return static_cast<long long>(kSmemPerSm / n) - 1280 - static_cast<long long>(fixed); };
+  auto room = [&](int n) { return static_cast<long long>(kSmemPerSm / n) - 2304 - static_cast<long long>(fixed); };
   while (ctas > 1 && room(ctas) < static_cast<long long>(3 * stage)) --ctas;
   const int stages = static_cast<int>(std::min<long long>(8, room(ctas) / static_cast<long long>(stage)));
   if (!once_per_device(dev, [&] {
-        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerSm - 1024) == cudaSuccess;
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerSm - 4096) == cudaSuccess;
       }))
     return fail(SPEC_ERR_CUDA, "weighing setup failed: %s", cudaGetErrorString(cudaGetLastError()));
   kern<<<static_cast<unsigned>(di.sms * ctas), WG_THREADS, fixed + stages * stage, st>>>(a, stages);
