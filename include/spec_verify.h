@@ -484,13 +484,15 @@ spec_status_t spec_adjust_logits(const void *logits, spec_dtype_t dtype, const i
 /* ---------------------------------------------------------------------------
  * Steps after a verification: what the emitted tokens' probabilities were, and a
  * cache that keeps to a budget by dropping the tokens that attention passes over.
- * A step of such a loop goes on with
+ * The step of a loop that has verified goes on with
  *   spec_token_logprobs, spec_kv_commit_q4 -> spec_kv_weigh_q4 ->
  *   spec_kv_evict_plan -> spec_kv_move_q4 (in every layer) -> spec_page_trim.
  * Beside the cache a layer has weights [num_pages, Hkv, page_tokens] float32 and
  * positions [num_pages, Hkv, page_tokens] int32, by the same slots: what attention
  * has given to the token that a kv head keeps there, and which token that is.
  * (Keys carry their positions; attention over the cache asks for no order.)
+ * Limits of the calls over the cache: num_pages * page_tokens and max_pages *
+ * page_tokens below 2^31, num_pages * page_tokens * Hkv below 2^37.
  * ------------------------------------------------------------------------- */
 
 /* Log probabilities of given tokens, with ranks, entropies and alternatives.
@@ -541,9 +543,10 @@ spec_status_t spec_token_logprobs(const void *logits, spec_dtype_t dtype, const 
  * A row without a finite lse, and a score that is a NaN, add nothing.  Nothing is done for a
  * sequence whose count is negative, or whose lengths, count or path spec_kv_commit_q4
  * would refuse; tokens on a page outside the cache are passed over.  Different
- * sequences' tokens must lie in different slots.
- * Limits: 1 <= N, W <= 1024, B <= 4096, Hq a multiple of Hkv, Hq / Hkv <= 64,
- * num_pages * page_tokens and max_pages * page_tokens below 2^31. */
+ * sequences' tokens must lie in different slots.  An internal wait that hit its time
+ * limit gives NaN to the tokens that it held up.
+ * Limits: 1 <= N, W <= 1024, B <= 4096, Hq a multiple of Hkv, Hq / Hkv <= 64; q and
+ * cache must be 16-byte aligned. */
 spec_status_t spec_kv_weigh_q4(const void *q, const float *lse, const int32_t *path, const int32_t *count,
                                const void *cache, const int32_t *block_table, const int32_t *lengths,
                                const int32_t *first_positions, int B, int N, int W, int Hq, int Hkv, int D,
@@ -581,7 +584,8 @@ spec_status_t spec_kv_evict_plan(const float *weights, const int32_t *positions,
  *
  *   moves [B, Hkv, max_moves, 2], move_counts [B, Hkv] int32: spec_kv_evict_plan's, or
  *       others in which no slot that a head's move goes to is in another of its moves.
- * A move with a slot outside the cache is left out. */
+ * A move with a slot outside the cache is left out.  The cache must be 16-byte
+ * aligned, moves 8-byte. */
 spec_status_t spec_kv_move_q4(void *cache, float *weights, int32_t *positions, const int32_t *moves,
                               const int32_t *move_counts, int B, int Hkv, int D, int page_tokens, int num_pages,
                               int max_moves, void *stream);
@@ -590,7 +594,7 @@ spec_status_t spec_kv_move_q4(void *cache, float *weights, int32_t *positions, c
  *
  *   tokens [B] int32: the tokens that sequence b keeps pages for; those behind the
  *       first ceil(tokens / page_tokens) of its held[b] pages are given back, in
- *       sequence order, behind the ring's free ones.
+ *       sequence order, behind the ring's free ones (block_table is left as it is).
  *   held, ring (in/out), ring_state, block_table: as for spec_page_map.
  *   new_held [B], new_ring_state [2] int32 (written; not the inputs' buffers), status
  *       [B] int32 (written): 0; -1 for negative tokens, held outside [0, max_pages], a

@@ -34,6 +34,8 @@ spec_status_t check_pool(int B, int Hkv, int P, int pages, int max_pages) {
   if (P % Q4_BLOCK != 0) return fail(SPEC_ERR_INVALID_ARG, "page_tokens=%d is not a multiple of %d", P, Q4_BLOCK);
   if (!below_2g(P, pages) || !below_2g(max_pages, P))
     return fail(SPEC_ERR_UNSUPPORTED, "num_pages and max_pages times page_tokens must stay below 2^31");
+  if (static_cast<long long>(pages) * (P / Q4_BLOCK) * Hkv >= 0xffffffffLL)   // (blocks are numbered in 32 bits)
+    return fail(SPEC_ERR_UNSUPPORTED, "num_pages * page_tokens * Hkv must stay below 2^37");
   return SPEC_OK;
 }
 

@@ -48,7 +48,7 @@ WG = dict(p_q=16, p_lse=32, p_path=48, p_count=64, p_cache=80, p_table=96, p_len
     (dict(Hq=130), UNSUP), (dict(B=4097), UNSUP), (dict(ks=33), BAD), (dict(scale=float("inf")), BAD), (dict(decay=float("nan")), BAD),
     (dict(pages=1 << 26), UNSUP), (dict(maxp=1 << 26), UNSUP), (dict(p_q=0), BAD), (dict(p_lse=0), BAD), (dict(p_cache=0), BAD),
     (dict(p_table=0), BAD), (dict(p_len=0), BAD), (dict(p_w=0), BAD), (dict(p_new=0), BAD), (dict(p_q=24), BAD), (dict(p_cache=88), BAD),
-    (dict(B=0, p_q=0, p_new=0), OK),
+    (dict(B=0, p_q=0, p_new=0), OK), (dict(Hkv=1 << 14, Hq=1 << 14, P=1 << 10, pages=1 << 20), UNSUP),
 ])
 def test_weigh_refusals(L, kw, status):
     assert _call(L.spec_kv_weigh_q4, WG, **kw) == status
@@ -63,6 +63,7 @@ PLAN = dict(p_w=16, p_pos=32, p_table=48, p_len=64, p_budget=80, p_next=96, B=2,
     (dict(recent=-1), BAD), (dict(most=0), BAD), (dict(maxp=1 << 26), UNSUP), (dict(pages=1 << 26), UNSUP), (dict(p_w=0), BAD),
     (dict(p_pos=0), BAD), (dict(p_table=0), BAD), (dict(p_len=0), BAD), (dict(p_budget=0), BAD), (dict(p_next=0), BAD), (dict(p_moves=0), BAD),
     (dict(p_counts=0), BAD), (dict(p_new=0), BAD), (dict(p_new=64), BAD), (dict(p_moves=116), BAD), (dict(B=0, p_w=0), OK),
+    (dict(Hkv=1 << 14, P=1 << 10, pages=1 << 20), UNSUP),
 ])
 def test_plan_refusals(L, kw, status):
     assert _call(L.spec_kv_evict_plan, PLAN, **kw) == status
