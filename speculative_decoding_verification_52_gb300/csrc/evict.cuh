@@ -261,6 +261,7 @@ __device__ __forceinline__ void ev_select(const PlanArgs& a, const EvRow& row, E
   const int w0 = blk0 + (blk1 - blk0) * warp / (EV_THREADS / 32), w1 = blk0 + (blk1 - blk0) * (warp + 1) / (EV_THREADS / 32);
   uint32_t worst = 0u;
   bool bad = ev_load(a, row, w0, w1, 0u, keys + (w0 - blk0) * Q4_BLOCK, a.cap - (w0 - blk0) * Q4_BLOCK, worst);
+  const bool here = mine <= a.cap;   // all keys are in shared memory
   auto slot_of = [&](int i) { return ev_slot(a, row, i); };
   auto key_at = [&](int i) {   // i: of this CTA's tokens
     if (i < a.cap) return keys[i];
@@ -293,9 +294,19 @@ __device__ __forceinline__ void ev_select(const PlanArgs& a, const EvRow& row, E
 #pragma unroll
     for (int i = 0; i < EV_BINS / 32; ++i) mine_hist[32 * i + lane] = 0u;
     __syncwarp();
-    for (int i = tid; i < mine; i += EV_THREADS) {
-      const uint32_t k = key_at(i);
+    auto count = [&](uint32_t k) {
       if (pass == 0 || (k >> (shift + 8)) == prefix) atomicAdd(&mine_hist[(k >> shift) & 255u], 1u);
+    };
+    if (here) {
+      for (int i = 4 * tid; i < mine; i += 4 * EV_THREADS) {
+        const uint4 k = *reinterpret_cast<const uint4*>(keys + i);
+        count(k.x);
+        if (i + 1 < mine) count(k.y);
+        if (i + 2 < mine) count(k.z);
+        if (i + 3 < mine) count(k.w);
+      }
+    } else {
+      for (int i = tid; i < mine; i += EV_THREADS) count(key_at(i));
     }
     __syncthreads();
     // thread t has the bin 255 - t: of the warps, then of the cluster
@@ -335,14 +346,27 @@ __device__ __forceinline__ void ev_select(const PlanArgs& a, const EvRow& row, E
     }
   }
 
-  // Consecutive tokens a thread (an odd number, which lie in different banks): equal
-  // keys are counted first, then free places and tokens to move.
-  const int per = ((mine + EV_THREADS - 1) / EV_THREADS) | 1;
+  // Consecutive tokens a thread, an odd number of fours, so that the threads' vectors lie in
+  // different banks: equal keys are counted first, then free places and tokens to move.
+  const int per = 4 * (((mine + 4 * EV_THREADS - 1) / (4 * EV_THREADS)) | 1);
   const int i0 = min(mine, tid * per), i1 = min(mine, i0 + per);
+  auto each = [&](auto&& f) {   // f(token, key)
+    if (here) {
+      for (int i = i0; i < i1; i += 4) {
+        const uint4 k = *reinterpret_cast<const uint4*>(keys + i);
+        f(i, k.x);
+        if (i + 1 < i1) f(i + 1, k.y);
+        if (i + 2 < i1) f(i + 2, k.z);
+        if (i + 3 < i1) f(i + 3, k.w);
+      }
+    } else {
+      for (int i = i0; i < i1; ++i) f(i, key_at(i));
+    }
+  };
   int equal_before = 0, all = 0;
   if (take > 0) {
     int x = 0;
-    for (int i = i0; i < i1; ++i) x += key_at(i) == tau;
+    each([&](int, uint32_t k) { x += k == tau; });
     equal_before = ev_scan(x, sh.warp[1], all);
     if constexpr (CLUSTER) {
       if (tid == 0) sh.total[0] = all;
@@ -351,12 +375,11 @@ __device__ __forceinline__ void ev_select(const PlanArgs& a, const EvRow& row, E
     }
   }
   int holes = 0, movers = 0, e = equal_before;
-  for (int i = i0; i < i1; ++i) {
-    const uint32_t k = key_at(i);
+  each([&](int i, uint32_t k) {
     const bool kept = k > tau || (k == tau && e++ < static_cast<int>(take));
     if (base + i < K) holes += !kept;
     else movers += kept;
-  }
+  });
   int all_holes, all_movers;
   int hole = ev_scan(holes, sh.warp[0], all_holes), mover = ev_scan(movers, sh.warp[1], all_movers);
   if constexpr (CLUSTER) {
@@ -372,15 +395,12 @@ __device__ __forceinline__ void ev_select(const PlanArgs& a, const EvRow& row, E
   }
   if (holes + movers > 0) {
     e = equal_before;
-    for (int i = i0; i < i1; ++i) {
-      const uint32_t k = key_at(i);
+    each([&](int i, uint32_t k) {
       const bool kept = k > tau || (k == tau && e++ < static_cast<int>(take));
-      if (base + i < K) {
-        if (!kept) moves[2 * hole++ + 1] = slot_of(base + i);
-      } else if (kept) {
-        moves[2 * mover++] = slot_of(base + i);
-      }
-    }
+      if (kept == (base + i < K)) return;
+      int32_t* at = moves + (kept ? 2 * mover++ : 2 * hole++ + 1);
+      *at = slot_of(base + i);
+    });
   }
   if (first) {
     a.counts[row.pair] = all_holes;
