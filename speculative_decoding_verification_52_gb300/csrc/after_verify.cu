@@ -193,13 +193,18 @@ spec_status_t spec_token_logprobs(const void* logits, spec_dtype_t dtype, const 
     a.ranks = ranks;
     a.top_tokens = top_tokens;
     a.top_logprobs = top_logprobs;
-    // A warp a row up to 8 KB; else a CTA, and a cluster of CTAs where the places alone
-    // do not fill the device.
+    // A warp a row where the rows are short or many enough, else a CTA, and a cluster of
+    // CTAs where the rows alone do not fill the device.  In us, five alternatives, a CTA
+    // against a warp a row: rows of 1 KB, 16 of them 14.8 and 5.5; of 4 KB, 304 of them 6.2
+    // and 7.2, 608 8.5 and 7.2, 2,432 28 and 8.6; of 16 KB, 608 9.1 and 15.3, 2,432 28 and
+    // 18; of 32 KB, 5,000 73 and 67; of 64 KB, 5,000 103 and 121.  CTAs a row, 128,256 bf16
+    // and 20 alternatives: one row, 1 15.5, 2 12.6, 4 9.9, 8 9.9; 64 rows, 1 16.9, 4 12.2, 8
+    // 17.1; 152 rows, 1 17.4, 2 15.9, 4 22.1; 320 rows, 1 26.0, 2 30.6.
     const long long places = static_cast<long long>(B) * M, bytes = static_cast<long long>(V) * esz_of(dtype);
-    const bool warp = bytes <= 8192;
+    const bool warp = bytes <= 2048 || (bytes <= 32768 && 1024 * places >= di.sms * bytes);
     a.C = 1;
     if (!warp)
-      while (a.C < 8 && places * a.C < 4LL * di.sms && bytes / (2 * a.C) >= 8192) a.C *= 2;
+      while (a.C < 8 && places * 2 * a.C <= 2LL * di.sms && bytes / (2 * a.C) >= 8192) a.C *= 2;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     prof_mark(0, st);
     s = dtype == SPEC_BF16 ? launch_logprobs<BF16T>(dev, warp, a, st) : launch_logprobs<F32T>(dev, warp, a, st);
@@ -312,13 +317,17 @@ spec_status_t spec_kv_evict_plan(const float* weights, const int32_t* positions,
     a.moves = moves;
     a.counts = move_counts;
     a.new_lengths = new_lengths;
-    // a cluster where the heads alone do not fill the device and the table has room for long sequences
+    // A cluster where the heads alone do not fill the device and the table has room for long
+    // sequences (64 heads of 32,768 tokens, in us: 1 CTA a head 366, 2 144, 4 29, 8 27; 16 of
+    // 65,536: 736, 362, 140, 29).
     const long long pairs = static_cast<long long>(B) * Hkv, most = static_cast<long long>(max_pages) * page_tokens;
     a.C = 1;
     while (a.C < EV_CLUSTER && pairs * a.C < 2LL * di.sms && most / a.C > 4096) a.C *= 2;
     if (pairs * a.C > 0x7fffffffLL) return fail(SPEC_ERR_UNSUPPORTED, "batch too large for one call");
     a.cap = static_cast<int>(std::min<long long>(EV_CAP, (most + a.C * 128 - 1) / (a.C * 128) * 128 + (a.C > 1 ? 128 : 0)));
-    // several pairs a CTA where that leaves two CTAs an SM, with 48 KB of keys at most
+    // Several heads a CTA, whose warps look for few tokens to drop, where that leaves two
+    // CTAs an SM, with 48 KB of keys at most (2,048 heads, in us: 1 a CTA 43, 2 24, 4 15;
+    // that drop half of 4,096 tokens, CTA by CTA: 64, 65, 65).
     a.rows = 1;
     while (a.C == 1 && a.rows < EV_ROWS && pairs / (2 * a.rows) >= 2LL * di.sms && 2 * a.rows * a.cap <= 12288) a.rows *= 2;
     const size_t smem = 4 * (static_cast<size_t>(EV_HISTS) * EV_BINS + static_cast<size_t>(a.rows) * a.cap);

@@ -13,10 +13,15 @@
 // rows; more rows are taken in turns, over the same keys.  A sequence's rows are taken
 // in as many groups of eight as it commits, not as the batch might.
 //
-// Bound: the keys' 9/16 byte an element and 8 bytes of weights a token.  A block (D =
-// 128) crosses the bus in about 110 clocks of an SM; it takes 64 conversions and 64
-// multiplications (32 clocks each), 16 products per eight rows (32 clocks) and 8
-// exponentials a lane per eight rows.
+// Bound: the keys' 9/16 byte an element and 8 bytes of weights a token, 50 us of 256
+// sequences of 2,048 tokens and 8 heads of 128; it takes 126 (2.7 TB/s) for chains of which
+// 3.2 nodes of 4 query heads are committed on average, 530 instructions a block of 32
+// tokens: 64 conversions and as many multiplications of code pairs, 16 products and 14
+// exponentials a lane for each eight rows.  Sixteen warps an SM, as many as the registers
+// allow (five CTAs, through local memory: 209 us; three: 128), issue 56 % of the time, by
+// the latency of what depends on each other: two chains of products a sum 126 us, one 128.
+// With the next block in registers instead of rings, and all rows that the batch may
+// commit, it was 157 us.
 #pragma once
 
 #include "common.cuh"
@@ -125,6 +130,9 @@ __device__ __forceinline__ void wg_load_q(const WeighArgs& a, int b, int h, int 
     float top = fmax_nan(__uint_as_float(mx << 16), __uint_as_float(mx & 0xffff0000u));
     top = fmax_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = fmax_nan(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // (a row with elements that are no numbers has no finite lse, or should not have one)
+    const bool counts = top < __builtin_huge_valf() && lse < __builtin_huge_valf();
+    if (!counts) lse = __builtin_huge_valf();
     // to [128, 256): what f16 then cannot hold is below 2^-32 of the largest element
     const int ex = static_cast<int>(__float_as_uint(top) >> 23) - 127;
     const int sh = top > 0.f ? min(7 - ex, 100) : 0;
@@ -138,7 +146,7 @@ __device__ __forceinline__ void wg_load_q(const WeighArgs& a, int b, int h, int 
     for (int i = 0; i < CH / 8; ++i) {
       const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) q[j][4 * i + k] = f16x2_pack(__uint_as_float(x[k] << 16) * mul, __uint_as_float(x[k] & 0xffff0000u) * mul);
+      for (int k = 0; k < 4; ++k) q[j][4 * i + k] = counts ? f16x2_pack(__uint_as_float(x[k] << 16) * mul, __uint_as_float(x[k] & 0xffff0000u) * mul) : 0u;
     }
   }
 }
@@ -197,8 +205,7 @@ __device__ __forceinline__ float wg_block(const unsigned char* from, const uint3
           A[2 * i + k] = make_uint4(f16x2_mul(lo[2 * k], x0), f16x2_mul(hi[2 * k], x1), f16x2_mul(lo[2 * k + 1], x0), f16x2_mul(hi[2 * k + 1], x1));
       }
     }
-    // a score that is no number weighs nothing
-    float x[2] = {0.f, 0.f};
+    unsigned long long x[2] = {0ull, 0ull};   // of the two tokens, the even and the odd columns
 #pragma unroll
     for (int j = 0; j < NR; ++j) {
       if (j > 0 && j >= groups) break;
@@ -219,16 +226,27 @@ __device__ __forceinline__ float wg_block(const unsigned char* from, const uint3
           if ((fresh + 16 * m + 8 * (k >> 1) + g) * G > row0 + 8 * j + 2 * t + (k & 1)) d[k] = kNegInf;
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k) x[k >> 1] += ex2_approx(fmaxf(__fmaf_rn(d[k], k & 1 ? c.y : c.x, k & 1 ? c.w : c.z), kNegInf));
+      for (int k = 0; k < 2; ++k) {
+        float z0, z1;
+        f2_unpack(f2_fma(f2_pack(d[2 * k], d[2 * k + 1]), f2_pack(c.x, c.y), f2_pack(c.z, c.w)), z0, z1);
+        x[k] = f2_add(x[k], f2_pack(ex2_approx(z0), ex2_approx(z1)));
+      }
     }
-    sum[2 * m] = x[0];
-    sum[2 * m + 1] = x[1];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      float x0, x1;
+      f2_unpack(x[k], x0, x1);
+      sum[2 * m + k] = x0 + x1;
+    }
   }
   // over the four lanes of a token, each of which keeps one of the four tokens
   const bool up = t & 2, odd = t & 1;
   const float a0 = up ? sum[2] : sum[0], a1 = up ? sum[3] : sum[1], b0 = up ? sum[0] : sum[2], b1 = up ? sum[1] : sum[3];
   const float y0 = a0 + __shfl_xor_sync(0xffffffffu, b0, 2), y1 = a1 + __shfl_xor_sync(0xffffffffu, b1, 2);
-  return (odd ? y1 : y0) + __shfl_xor_sync(0xffffffffu, odd ? y0 : y1, 1);
+  const float all = (odd ? y1 : y0) + __shfl_xor_sync(0xffffffffu, odd ? y0 : y1, 1);
+  // (the queries are numbers here: a sum that is none is a token's whose keys are none, and
+  // none of whose scores weighs anything)
+  return all == all ? all : 0.f;
 }
 
 __host__ __device__ constexpr int wg_ctas(int NR) { return NR == 1 ? 5 : NR <= 3 ? 4 : 3; }

@@ -18,9 +18,12 @@
 // warp took 2,200 clocks a tile, three times what adding it up takes.)  A path's nodes do
 // not lie side by side: its rows are few, and weigh_q4.cuh's.
 //
-// Bound: issue, about 3.5 instructions a score; beside it an exponential a score (32 a
-// clock and SM) and 2 D operations of the tensor cores; a row's 2 D bytes are read once a
-// unit, from the L2 cache.
+// Bound, 2 chunks of 1,024 tokens behind 2,048 and 14,336, 16 query and 2 kv heads of 64
+// (285 million scores): 64 us.  Their exponentials take 31 at 32 a clock and SM, the
+// products 21, the adding warps' instructions about as long as the exponentials; the 278
+// units are 1.8 rounds of 152 CTAs, of which the second is not full.  A unit costs about
+// 2.3 us by itself (its place in the list, its keys' way from memory), which is why units
+// of few tiles go two an SM.
 #pragma once
 
 #include <cuda.h>

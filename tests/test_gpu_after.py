@@ -90,6 +90,19 @@ def test_logprobs_of_many_rows(B):
     _check_logprobs(x, rng.integers(-1, 20000, (B, 1)), 0.9, None, 5)
 
 
+@pytest.mark.parametrize("V,rows", [(4096, 1300), (16384, 4900), (1030, 3)])
+@pytest.mark.parametrize("n", [5, 32])
+def test_logprobs_of_a_warp_a_row(V, rows, n):
+    """Short rows, or many of them: a warp each."""
+    rng = np.random.default_rng(V + n)
+    x = torch.randn(rows, 1, V, generator=torch.Generator(device=DEV).manual_seed(V), device=DEV) * 2
+    x = x.to(torch.bfloat16)
+    tokens = rng.integers(0, V, (rows, 1))
+    some = np.unique(np.concatenate([[0, rows - 1], rng.integers(0, rows, 40)]))
+    got = sv.spec_token_logprobs(x, i32(tokens), 0.8, top_n=n)
+    _compare_logprobs([t[some] for t in got], ref.logprobs(f64(x[some]), tokens[some], 0.8, None, n))
+
+
 @pytest.mark.parametrize("V", [1000, 9001])
 def test_logprobs_of_tree_paths(V):
     rng = np.random.default_rng(V)
