@@ -110,10 +110,9 @@ spec_status_t launch_weigh(int NR, const DevInfo& di, int dev, const WeighArgs& 
   }
 }
 
-template <int D, int ROWS>
+template <int D>
 spec_status_t launch_weigh_tc(const DevInfo& di, int dev, const WeighArgs& a, cudaStream_t st) {
-  using F = WtForm<D, ROWS>;
-  auto kern = weigh_q4_tc_kernel<D, ROWS>;
+  auto kern = weigh_q4_tc_kernel<D>;
   TensorMapEncode encode = tensor_map_encode();
   if (!encode) return fail(SPEC_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
   // the queries as [B][N][Hq][D], in boxes of the nodes and the kv head's query heads of a tile
@@ -121,36 +120,29 @@ spec_status_t launch_weigh_tc(const DevInfo& di, int dev, const WeighArgs& a, cu
   const cuuint64_t heads = static_cast<cuuint64_t>(a.Hkv) * a.G, row = 2 * D;
   const cuuint64_t dims[4] = {D, heads, static_cast<cuuint64_t>(a.N), static_cast<cuuint64_t>(a.B)};
   const cuuint64_t strides[3] = {row, row * heads, row * heads * a.N};
-  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(a.G), static_cast<cuuint32_t>(ROWS / a.G), 1}, step[4] = {1, 1, 1, 1};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(a.G), static_cast<cuuint32_t>(WT_ROWS / a.G), 1}, step[4] = {1, 1, 1, 1};
   const CUresult r = encode(&map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<uint16_t*>(a.q), dims, strides, box, step,
                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(SPEC_ERR_CUDA, "cuTensorMapEncodeTiled: %d", static_cast<int>(r));
-  const size_t fixed = (sizeof(WtShared<D, ROWS>) + 15) / 16 * 16 + 1024 + 8;
+  const size_t fixed = (sizeof(WtShared<D>) + 15) / 16 * 16 + 1024 + 8;
   if (!once_per_device(dev, [&] {
         return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(fixed + 12 * WG_MAX_B)) == cudaSuccess;
       }))
     return fail(SPEC_ERR_CUDA, "weighing setup failed: %s", cudaGetErrorString(cudaGetLastError()));
-  kern<<<static_cast<unsigned>(F::CTAS * di.sms), F::THREADS, fixed + 12 * static_cast<size_t>(a.B), st>>>(a, map);
+  kern<<<static_cast<unsigned>(2 * di.sms), WT_THREADS, fixed + 12 * static_cast<size_t>(a.B), st>>>(a, map);
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? SPEC_OK : cuda_fail(e, "weighing launch");
 }
 
 // Which kernel, by the rows that a sequence may commit and D: few rows, whose kernel's time
-// grows with the rows, tiles of 64 of them, or many in tiles of 128.  256 sequences at
-// 2,048 tokens and 8 at 16,384, 8 kv heads of 4 query heads, in us:
-//   D = 128   36 rows 227 and 61 (few), 308 and 68 (tiles of 64);   52: 308 and 67 (64)
-//   D = 64    68 rows 246 and 67 (few), 302 and 66 (64);   100: 336 and 90 (few), 304 and 66 (64)
-// so few rows up to what tiles of 24 and 32 hold.  8 at 16,384, tiles of 64 and of 128:
-//   D = 64    1,024 rows 259 and 260, 2,048 485 and 458, 4,096 956 and 871
-//   D = 128   1,024 rows 289 and 303, 2,048 546 and 554, 4,096 1,078 and 1,079
-// A path's nodes do not lie side by side: few rows.
-constexpr int kWeighFewRows128 = 48, kWeighFewRows64 = 96, kWeighManyRows = 2048;
-
-template <int D>
-spec_status_t launch_weigh_tc(int rows, const DevInfo& di, int dev, const WeighArgs& a, cudaStream_t st) {
-  return rows >= kWeighManyRows ? launch_weigh_tc<D, 128>(di, dev, a, st) : launch_weigh_tc<D, 64>(di, dev, a, st);
-}
+// grows with the rows, or tiles of 64 of them on the tensor cores.  256 sequences at 2,048
+// tokens and 8 at 16,384, 8 kv heads of 4 query heads, in us:
+//   D = 128   36 rows 227 and 61 (few), 308 and 68 (many);   52: 308 and 67 (many)
+//   D = 64    68 rows 246 and 67 (few), 302 and 66 (many);   100: 336 and 90 (few), 304 and 66 (many)
+// so few rows up to what two and three turns of 32 hold.  A path's nodes do not lie side by
+// side: few rows.
+constexpr int kWeighFewRows128 = 48, kWeighFewRows64 = 96;
 
 }  // namespace
 
@@ -270,7 +262,7 @@ spec_status_t spec_kv_weigh_q4(const void* q, const float* lse, const int32_t* p
     const int rows = a.most * a.G, tiles = ceil_div(rows, 32), NR = ceil_div(ceil_div(rows, 8), tiles);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     prof_mark(0, st);
-    if (!path && rows > (D == 128 ? kWeighFewRows128 : kWeighFewRows64)) s = D == 128 ? launch_weigh_tc<128>(rows, di, dev, a, st) : launch_weigh_tc<64>(rows, di, dev, a, st);
+    if (!path && rows > (D == 128 ? kWeighFewRows128 : kWeighFewRows64)) s = D == 128 ? launch_weigh_tc<128>(di, dev, a, st) : launch_weigh_tc<64>(di, dev, a, st);
     else s = D == 128 ? launch_weigh<128>(NR, di, dev, a, st) : launch_weigh<64>(NR, di, dev, a, st);
     if (s != SPEC_OK) return s;
     prof_mark(1, st);

@@ -65,6 +65,25 @@ __device__ __forceinline__ void tc_ld(uint32_t addr, float (&x)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) x[i] = __uint_as_float(r[i]);
 }
+// 32 columns in two steps, between which something else may be done
+__device__ __forceinline__ void tc_ld32_start(uint32_t addr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tc_ld32_end(uint32_t (&r)[32], float (&x)[32]) {
+  tc_wait_ld();
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    asm volatile("" : "+r"(r[i]));   // (not used before the wait)
+    x[i] = __uint_as_float(r[i]);
+  }
+}
 __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),

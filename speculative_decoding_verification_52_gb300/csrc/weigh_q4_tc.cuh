@@ -1,29 +1,28 @@
 // weigh_q4_tc.cuh -- the weights of cached tokens (weigh_q4.cuh) for many rows, on the
 // tcgen05 tensor cores: chunks of prompts, whose rows meet every cached token.
 //
-//   S[128 tokens x 128 rows] = K[128 x D] Q^T    (A = K in tensor memory, B = Q in shared memory)
+//   S[128 tokens x 64 rows] = K[128 x D] Q^T    (A = K in tensor memory, B = Q in shared memory)
 //
-// (or 64 rows) in bf16: a code times its scale has 6 significant bits, the queries are bf16
-// as they come, and one factor takes all products to the log2 domain.  With the tokens as
-// M a thread has one token and adds up its row of S; nothing crosses threads.  The unit of
+// in bf16: a code times its scale has 6 significant bits, the queries are bf16 as they
+// come, and one factor takes all products to the log2 domain.  With the tokens as M a
+// thread has one token and adds up its row of S; nothing crosses threads.  The unit of
 // work is a tile of 128 tokens of a head, whose keys are unpacked once and stay in
-// tensor memory while the rows pass by, two or three tiles of them under way in S and
-// four or six in shared memory.
+// tensor memory while the rows pass by, 64 at a time, two tiles of rows under way in S
+// and four or six in shared memory.
 //
-// Roles of a CTA: four warps or three times four that add up, every third tile of rows
-// each; four that unpack a unit's keys and bring the rows' lse; one that has the queries
-// copied; one that issues the products.
-// The queries come by tensor-map copies of ROWS / G nodes with their G query heads, in the
+// Roles of a CTA (two an SM): four warps that add up, four that unpack a unit's keys and
+// bring the rows' lse, one that has the queries copied, one that issues the products.
+// The queries come by tensor-map copies of 64 / G nodes with their G query heads, in the
 // 128-byte swizzle that the tensor cores read.  (Asynchronous copies of 16 bytes by a
 // warp took 2,200 clocks a tile, three times what adding it up takes.)  A path's nodes do
 // not lie side by side: its rows are few, and weigh_q4.cuh's.
 //
 // Bound, 2 chunks of 1,024 tokens behind 2,048 and 14,336, 16 query and 2 kv heads of 64
-// (285 million scores): 64 us.  Their exponentials take 31 at 32 a clock and SM, the
-// products 21, the adding warps' instructions about as long as the exponentials; the 278
-// units are 1.8 rounds of 152 CTAs, of which the second is not full.  A unit costs about
-// 2.3 us by itself (its place in the list, its keys' way from memory), which is why units
-// of few tiles go two an SM.
+// (285 million scores): 75 us.  Products of 128 x 64 x 16, which take as long as ones of
+// 128 x 128 x 16, keep the tensor cores busy most of it; the exponentials take 31 us at 32
+// a clock and SM, the adding warps' instructions about as long.  (A second set of adding
+// warps changed 75 to 72 us, and units of few tiles by a tenth for the worse.)  A unit
+// costs about 2 us by itself (its place in the list, its keys' way from memory).
 #pragma once
 
 #include <cuda.h>
@@ -34,30 +33,19 @@
 namespace sv {
 
 constexpr int WT_TILE = 128;      // tokens of a unit
+constexpr int WT_ROWS = 64;       // rows of a tile, the last of which stay empty where G does not divide it
+constexpr int WT_WARPS = 10, WT_THREADS = 32 * WT_WARPS;
+constexpr uint32_t WT_COLS = 256; // tensor memory: two buffers of S, two of K
 
-// The kernel's two forms: ROWS a tile (the last stay empty where G does not divide it),
-// BUFS buffers of S, SETS sets of four warps that add them up, CTAS an SM.
-//   64, 2, 1, 2: units of few tiles, of which two CTAs have twice as many under way;
-//   128, 3, 3, 1: many tiles.
-template <int D, int ROWS>
-struct WtForm {
-  static constexpr bool MANY = ROWS == 128;
-  static constexpr int BUFS = MANY ? 3 : 2, SETS = MANY ? 3 : 1, CTAS = MANY ? 1 : 2;
-  static constexpr int WARPS = 4 * SETS + 6, THREADS = 32 * WARPS;
-  static constexpr int STAGES = D == 64 ? 6 : 4;              // tiles of queries in shared memory
-  static constexpr uint32_t COLS = MANY ? 512 : 256;          // tensor memory: S, two buffers of K
-  static_assert(ROWS * BUFS + D <= static_cast<int>(COLS), "tensor memory");
-};
-
-template <int D, int ROWS>
+template <int D>
 struct WtShared {
-  using F = WtForm<D, ROWS>;
-  unsigned char q[F::STAGES][ROWS * D * 2];      // [D / 64][ROWS][128 bytes], swizzled
-  float neg_lse[F::STAGES][ROWS];                // -lse log2(e); -inf: the row adds nothing
-  uint64_t qfull[F::STAGES], qempty[F::STAGES], kfull[2], kempty[2], sready[F::BUFS], sfree[F::BUFS], drain;
-  float other[2][F::SETS][WT_TILE];              // the tokens' sums of all sets but the first, for two units
+  static constexpr uint32_t q_bytes = WT_ROWS * D * 2;
+  static constexpr int STAGES = D == 64 ? 6 : 4;   // tiles of queries
+  unsigned char q[STAGES][q_bytes];                // [D / 64][64 rows][128 bytes], swizzled
+  float neg_lse[STAGES][WT_ROWS];         // -lse log2(e); -inf: the row adds nothing
+  uint64_t qfull[STAGES], qempty[STAGES], kfull[2], kempty[2], sready[2], sfree[2], drain;
   uint32_t tmem;
-  int dead;                                      // a wait ran out of time
+  int dead;                                  // a wait ran out of time
 };
 
 __device__ __noinline__ bool wt_wait_long(uint64_t* bar, uint32_t parity, int* dead, unsigned long long limit);
@@ -115,35 +103,31 @@ __device__ __forceinline__ WtUnit wt_unit(const WeighArgs& a, int per, const lon
   return x;
 }
 
-template <int D, int ROWS>
-__global__ void __launch_bounds__(WtForm<D, ROWS>::THREADS, WtForm<D, ROWS>::CTAS) weigh_q4_tc_kernel(const WeighArgs a, const __grid_constant__ CUtensorMap map) {
-  using F = WtForm<D, ROWS>;
-  using S = WtShared<D, ROWS>;
-  constexpr int SETS = F::SETS, BUFS = F::BUFS, WARPS = F::WARPS, STAGES = F::STAGES;
+template <int D>
+__global__ void __launch_bounds__(WT_THREADS, 2) weigh_q4_tc_kernel(const WeighArgs a, const __grid_constant__ CUtensorMap map) {
+  using S = WtShared<D>;
   extern __shared__ __align__(128) unsigned char wt_raw[];
-  __shared__ long long scratch[WARPS];
+  __shared__ long long scratch[WT_WARPS];
   unsigned char* aligned = wt_raw + ((1024u - (smem_addr(wt_raw) & 1023u)) & 1023u);
   S& sh = *reinterpret_cast<S*>(aligned);
   long long* prefix = reinterpret_cast<long long*>(aligned + (sizeof(S) + 15) / 16 * 16);   // [B + 1], in tiles
   int* all_rows = reinterpret_cast<int*>(prefix + a.B + 1);                               // [B]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, quad = warp & 3;
   const unsigned long long limit = a.timeout_ns;
-  const int nodes = ROWS / a.G, per = nodes * a.G;   // nodes and rows of a tile
+  const int nodes = WT_ROWS / a.G, per = nodes * a.G;   // nodes and rows of a tile
 
-  if (per < ROWS) {   // (rows that no copy writes)
-    for (int i = threadIdx.x; i < static_cast<int>(sizeof(sh.q) / 16); i += F::THREADS) reinterpret_cast<uint4*>(sh.q)[i] = make_uint4(0u, 0u, 0u, 0u);
+  if (per < WT_ROWS) {   // (rows that no copy writes)
+    for (int i = threadIdx.x; i < static_cast<int>(sizeof(sh.q) / 16); i += WT_THREADS) reinterpret_cast<uint4*>(sh.q)[i] = make_uint4(0u, 0u, 0u, 0u);
     tc_proxy_fence();
   }
   if (threadIdx.x == 0) {
-    for (int i = 0; i < STAGES; ++i) {
+    for (int i = 0; i < S::STAGES; ++i) {
       mbar_init(&sh.qfull[i], 2);
       mbar_init(&sh.qempty[i], 5);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.kfull[i], 4);
       mbar_init(&sh.kempty[i], 1);
-    }
-    for (int i = 0; i < BUFS; ++i) {
       mbar_init(&sh.sready[i], 1);
       mbar_init(&sh.sfree[i], 4);
     }
@@ -151,52 +135,54 @@ __global__ void __launch_bounds__(WtForm<D, ROWS>::THREADS, WtForm<D, ROWS>::CTA
     sh.dead = 0;
     mbar_fence_init();
   }
-  wg_prefix<F::THREADS>(a, WT_TILE, prefix, all_rows, scratch);   // (synchronises the CTA)
+  wg_prefix<WT_THREADS>(a, WT_TILE, prefix, all_rows, scratch);   // (synchronises the CTA)
   const long long units = prefix[a.B] * a.Hkv;
   if (blockIdx.x >= units) return;
-  if (warp == WARPS - 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sh.tmem)), "r"(F::COLS) : "memory");
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sh.tmem)), "r"(WT_COLS) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     tc_fence_before();
   }
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sh.tmem, t_k = tmem + BUFS * ROWS;   // S in front, K: D / 2 columns each
+  const uint32_t tmem = sh.tmem, t_k = tmem + 2 * WT_ROWS;   // S: columns 0..127; K: D / 2 each from 128 on
 
-  if (warp < 4 * SETS) {
-    // ---- sums: a thread a token, a set of four warps every third tile of rows ---------------
-    const int set = warp >> 2;
+  if (warp < 4) {
+    // ---- sums: a thread a token -------------------------------------------------------
     const uint32_t lane_at = static_cast<uint32_t>(32 * quad) << 16;
     const float f = a.scale_log2 * a.k_mul;
-    int c = 0, n = 0;   // tiles of rows, units so far
-    for (long long u = blockIdx.x; u < units; u += gridDim.x, ++n) {
+    int c = 0;   // tiles of rows so far
+    for (long long u = blockIdx.x; u < units; u += gridDim.x) {
       const WtUnit x = wt_unit(a, per, prefix, all_rows, u);
       const int pos = x.t0 + 32 * quad + lane;
       long long at = -1;
       float old = 0.f;
-      if (set == 0 && pos < x.end) {
+      if (pos < x.end) {
         const int e = pos / a.P, page = a.table[static_cast<long long>(x.b) * a.W + e];
         if (page >= 0 && page < a.pages) at = (static_cast<long long>(page) * a.Hkv + x.h) * a.P + (pos - e * a.P);
         if (at >= 0 && pos < x.old) old = a.weights[at];
       }
       float sum = 0.f;
       for (int i = x.first; i < x.last; ++i, ++c) {
-        const int buf = c % BUFS, s = c % STAGES;
-        if (c % SETS != set) continue;
-        wt_wait(&sh.sready[buf], (c / BUFS) & 1, &sh.dead, limit);
+        const int buf = c & 1, s = c % S::STAGES;
+        wt_wait(&sh.sready[buf], (c >> 1) & 1, &sh.dead, limit);
+        wt_wait(&sh.qfull[s], (c / S::STAGES) & 1, &sh.dead, limit);   // (long since: what brought the lse is seen here, too)
         tc_fence_after();
         const float* nl = sh.neg_lse[s];
         const int hidden = (pos - x.old) * a.G - i * per;   // rows of the tile that do not see the token
-        const uint32_t s_at = tmem + lane_at + buf * ROWS;
+        const uint32_t s_at = tmem + lane_at + buf * WT_ROWS;
         float part = 0.f;
         bool odd = __any_sync(0xffffffffu, hidden > 0);
         if (!odd) {
           const unsigned long long ff = f2_pack(f, f);
           unsigned long long t0 = 0ull, t1 = 0ull;
+          uint32_t r[2][32];
+          tc_ld32_start(s_at, r[0]);
 #pragma unroll
-          for (int k = 0; k < ROWS; k += 32) {
+          for (int k = 0; k < WT_ROWS; k += 32) {   // (the second half comes beside the first one's sums)
             float y[32];
-            tc_ld<32>(s_at + k, y);
+            tc_ld32_end(r[k / 32], y);
+            if (k == 0) tc_ld32_start(s_at + 32, r[1]);
 #pragma unroll
             for (int j = 0; j < 32; j += 4) {
               const float4 l = *reinterpret_cast<const float4*>(nl + k + j);
@@ -215,7 +201,7 @@ __global__ void __launch_bounds__(WtForm<D, ROWS>::THREADS, WtForm<D, ROWS>::CTA
         if (TC_RARE(odd)) {   // rows that do not see the token, and scores that are no numbers, weigh nothing
           part = 0.f;
 #pragma unroll 1
-          for (int k = 0; k < ROWS; k += 8) {
+          for (int k = 0; k < WT_ROWS; k += 8) {
             float y[8];
             __syncwarp();
             tc_ld<8>(s_at + k, y);
@@ -231,18 +217,13 @@ __global__ void __launch_bounds__(WtForm<D, ROWS>::THREADS, WtForm<D, ROWS>::CTA
           mbar_arrive(&sh.qempty[s]);
         }
       }
-      if (set > 0) sh.other[n & 1][set - 1][32 * quad + lane] = sum;
-      if constexpr (SETS > 1) named_bar_sync(1, 128 * SETS);
-      if (set == 0)
-#pragma unroll
-        for (int k = 0; k < SETS - 1; ++k) sum += sh.other[n & 1][k][32 * quad + lane];
       if (at >= 0) {
         if (*reinterpret_cast<volatile int*>(&sh.dead)) sum = __int_as_float(0x7fc00000);
         a.new_weights[at] = pos < x.old ? __fmaf_rn(a.decay, old, sum) : sum;
         if (a.positions && pos >= x.old) a.positions[at] = (a.first ? a.first[x.b] : x.old) + (pos - x.old);
       }
     }
-  } else if (warp < 4 * SETS + 4) {
+  } else if (warp < 8) {
     // ---- keys: a thread a token; then lse: a warp every fourth tile ---------------------------------------------------------
     const uint32_t lane_at = static_cast<uint32_t>(32 * quad) << 16;
     int n = 0, c = 0;   // units with rows, tiles of rows so far
@@ -285,49 +266,49 @@ __global__ void __launch_bounds__(WtForm<D, ROWS>::THREADS, WtForm<D, ROWS>::CTA
       const float* lse = a.lse + static_cast<long long>(x.b) * a.N * (a.Hkv * a.G) + x.h * a.G;
       for (int i = x.first; i < x.last; ++i, ++c) {
         if ((c & 3) != quad) continue;
-        float l[ROWS / 32];
+        float l[WT_ROWS / 32];
 #pragma unroll
-        for (int k = 0; k < ROWS / 32; ++k) {
+        for (int k = 0; k < WT_ROWS / 32; ++k) {
           const int r = 32 * k + lane, row = i * per + r, node = row / a.G;
           l[k] = r < per && row < x.rows ? __ldg(lse + static_cast<long long>(node) * (a.Hkv * a.G) + (row - node * a.G)) : __builtin_huge_valf();
         }
-        const int s = c % STAGES;
-        if (c >= STAGES) wt_wait(&sh.qempty[s], ((c / STAGES) & 1) ^ 1, &sh.dead, limit);
+        const int s = c % S::STAGES;
+        if (c >= S::STAGES) wt_wait(&sh.qempty[s], ((c / S::STAGES) & 1) ^ 1, &sh.dead, limit);
 #pragma unroll
-        for (int k = 0; k < ROWS / 32; ++k)
+        for (int k = 0; k < WT_ROWS / 32; ++k)
           sh.neg_lse[s][32 * k + lane] = fabsf(l[k]) < __builtin_huge_valf() ? l[k] * -1.44269504088896f : kNegInf;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.qfull[s]);
       }
     }
-  } else if (warp == 4 * SETS + 4) {
+  } else if (warp == 8) {
     // ---- queries: one thread ------------------------------------------------------------------
     int c = 0;
     bool go = lane == 0;
     for (long long u = blockIdx.x; go && u < units; u += gridDim.x) {
       const WtUnit x = wt_unit(a, per, prefix, all_rows, u);
       for (int i = x.first; i < x.last; ++i, ++c) {
-        const int s = c % STAGES;
+        const int s = c % S::STAGES;
         // (Warps whose wait has failed go on in step and release stages whose copies may
         // still be on their way; the flag was set before they did.)
-        if (c >= STAGES) go = wt_wait(&sh.qempty[s], ((c / STAGES) & 1) ^ 1, &sh.dead, limit) && !*reinterpret_cast<volatile int*>(&sh.dead);
+        if (c >= S::STAGES) go = wt_wait(&sh.qempty[s], ((c / S::STAGES) & 1) ^ 1, &sh.dead, limit) && !*reinterpret_cast<volatile int*>(&sh.dead);
         if (!go) break;
         mbar_arrive_expect_tx(&sh.qfull[s], static_cast<uint32_t>(per) * D * 2);
 #pragma unroll
         for (int k = 0; k < D / 64; ++k)
           asm volatile(
               "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
-                  smem_addr(sh.q[s]) + k * (ROWS * 128)),
+                  smem_addr(sh.q[s]) + k * (WT_ROWS * 128)),
               "l"(&map), "r"(64 * k), "r"(x.h * a.G), "r"(i * nodes), "r"(x.b), "r"(smem_addr(&sh.qfull[s]))
               : "memory");
       }
     }
     // what was started has arrived before the CTA ends
     if (lane == 0)
-      for (int t = max(0, c - STAGES); t < c; ++t) wt_drain(&sh.qfull[t % STAGES], (t / STAGES) & 1, limit);
+      for (int t = max(0, c - S::STAGES); t < c; ++t) wt_drain(&sh.qfull[t % S::STAGES], (t / S::STAGES) & 1, limit);
   } else if (lane == 0) {
     // ---- products: one thread ---------------------------------------------------------------
-    constexpr uint32_t id = tc_idesc(ROWS, true, false, false);
+    constexpr uint32_t id = tc_idesc(WT_ROWS, true, false, false);
     int c = 0, n = 0;
     bool ok = true;
     for (long long u = blockIdx.x; ok && u < units; u += gridDim.x) {
@@ -335,15 +316,15 @@ __global__ void __launch_bounds__(WtForm<D, ROWS>::THREADS, WtForm<D, ROWS>::CTA
       if (x.first >= x.last) continue;
       ok = wt_wait(&sh.kfull[n & 1], (n >> 1) & 1, &sh.dead, limit);
       for (int i = x.first; ok && i < x.last; ++i, ++c) {
-        const int buf = c % BUFS, s = c % STAGES;
-        ok = wt_wait(&sh.qfull[s], (c / STAGES) & 1, &sh.dead, limit);
-        if (ok && c >= BUFS) ok = wt_wait(&sh.sfree[buf], ((c / BUFS) & 1) ^ 1, &sh.dead, limit);
+        const int buf = c & 1, s = c % S::STAGES;
+        ok = wt_wait(&sh.qfull[s], (c / S::STAGES) & 1, &sh.dead, limit);
+        if (ok && c >= 2) ok = wt_wait(&sh.sfree[buf], ((c >> 1) & 1) ^ 1, &sh.dead, limit);
         if (!ok) break;
         tc_fence_after();
         const uint64_t qd = tc_desc_128(smem_addr(sh.q[s]));
 #pragma unroll
         for (int k = 0; k < D / 16; ++k)   // (16 elements: 32 bytes on; 64: the next part)
-          tc_mma_ts(tmem + buf * ROWS, t_k + (n & 1) * (D / 2) + k * 8, qd + (k / 4) * (ROWS * 128 / 16) + (k % 4) * 2, id, k > 0);
+          tc_mma_ts(tmem + buf * WT_ROWS, t_k + (n & 1) * (D / 2) + k * 8, qd + (k / 4) * (WT_ROWS * 128 / 16) + (k % 4) * 2, id, k > 0);
         tc_commit(&sh.sready[buf]);
         tc_commit(&sh.qempty[s]);
       }
@@ -355,7 +336,7 @@ __global__ void __launch_bounds__(WtForm<D, ROWS>::THREADS, WtForm<D, ROWS>::CTA
   }
   __syncwarp();
   __syncthreads();
-  if (warp == WARPS - 1) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(F::COLS) : "memory");
+  if (warp == 9) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(WT_COLS) : "memory");
 }
 
 }  // namespace sv
