@@ -18,7 +18,7 @@
 // not lie side by side: its rows are few, and weigh_q4.cuh's.
 //
 // Bound, 2 chunks of 1,024 tokens behind 2,048 and 14,336, 16 query and 2 kv heads of 64
-// (285 million scores): 75 us.  Products of 128 x 64 x 16, which take as long as ones of
+// (285 million scores): 78 us.  Products of 128 x 64 x 16, which take as long as ones of
 // 128 x 128 x 16, keep the tensor cores busy most of it; the exponentials take 31 us at 32
 // a clock and SM, the adding warps' instructions about as long.  (A second set of adding
 // warps changed 75 to 72 us, and units of few tiles by a tenth for the worse.)  A unit
@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(WT_THREADS, 2) weigh_q4_tc_kernel(const WeighA
         wt_wait(&sh.qfull[s], (c / S::STAGES) & 1, &sh.dead, limit);   // (long since: what brought the lse is seen here, too)
         tc_fence_after();
         const float* nl = sh.neg_lse[s];
-        const int hidden = (pos - x.old) * a.G - i * per;   // rows of the tile that do not see the token
+        const int hidden = max(0, pos - x.old) * a.G - i * per;   // rows of the tile that do not see the token (its distance times G may pass 32 bits)
         const uint32_t s_at = tmem + lane_at + buf * WT_ROWS;
         float part = 0.f;
         bool odd = __any_sync(0xffffffffu, hidden > 0);

@@ -309,6 +309,19 @@ def test_weigh_chunk_over_long_context():
     _run_weigh(_weigh_case(13, 1, 257, 2, 1, 128, 32, [1000], count=np.array([257])))
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("N,G", [(2, 64), (1, 2)])
+def test_weigh_of_very_long_sequences(N, G, D):
+    """34 million tokens, of which three pages lie in the cache: a token's distance times the
+    query heads of its kv head passes 32 bits."""
+    c, W = _weigh_case(19, 1, N, G, 1, D, 2048, [5000], count=np.array([N])), 16602
+    table = np.full((1, W), -1)
+    table[0, 0], table[0, -2:] = c["table"][0, 0], c["table"][0, 1:3]
+    c["table"], c["lengths"] = table, c["lengths"] + (W - 3) * 2048
+    assert c["lengths"][0] * 64 >= 2 ** 31
+    _run_weigh(c)
+
+
 def test_weigh_requests_that_are_refused_or_ask_nothing():
     """Bad lengths, counts and paths leave a sequence as it is; the others are served.  A
     count of 0 lets the weights decay.  Pages outside the cache are passed over."""
