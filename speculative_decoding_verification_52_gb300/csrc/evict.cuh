@@ -23,6 +23,8 @@
 // most of it barriers of the cluster and of the CTAs.
 #pragma once
 
+#include <limits.h>
+
 #include "common.cuh"
 #include "kv_q4.cuh"
 
@@ -115,7 +117,7 @@ __device__ __forceinline__ void ev_sync() {
 struct EvRow {
   int pair, b, h, n, K;
   const int32_t* table;
-  long long from;    // positions from here on stay
+  int from;          // positions from here on stay
   bool ok, cut;      // the length is in range; there is something to drop
 };
 __device__ __forceinline__ EvRow ev_row(const PlanArgs& a, int pair) {
@@ -126,7 +128,7 @@ __device__ __forceinline__ EvRow ev_row(const PlanArgs& a, int pair) {
   r.n = a.lengths[r.b];
   r.K = a.budgets[r.b];
   r.table = a.table + static_cast<long long>(r.b) * a.W;
-  r.from = static_cast<long long>(a.next[r.b]) - a.recent;
+  r.from = static_cast<int>(max(static_cast<long long>(a.next[r.b]) - a.recent, static_cast<long long>(INT_MIN)));
   r.ok = r.n >= 0 && static_cast<long long>(r.n) <= static_cast<long long>(a.W) * a.P;
   r.cut = r.ok && r.K >= 0 && r.n > r.K;
   if (r.cut && min(r.K, r.n - r.K) > a.max_moves) r.ok = r.cut = false;
@@ -141,7 +143,7 @@ __device__ __forceinline__ int ev_slot(const PlanArgs& a, const EvRow& r, int i)
   return r.table[e] * a.P + (i - e * a.P);
 }
 __device__ __forceinline__ uint32_t ev_key(const PlanArgs& a, const EvRow& r, float w, int pos) {
-  return pos < a.sinks || pos >= r.from ? 0xffffffffu : ev_ordered(w);   // (as in ev_load)
+  return pos < a.sinks || pos >= r.from ? 0xffffffffu : ev_ordered(w);
 }
 
 // A warp's run of blocks [k0, k1): their tokens' keys, bits turned by `flip`, to keys[]
@@ -151,7 +153,6 @@ __device__ __forceinline__ uint32_t ev_key(const PlanArgs& a, const EvRow& r, fl
 constexpr int EV_AHEAD = 8;
 __device__ __forceinline__ bool ev_load(const PlanArgs& a, const EvRow& r, int k0, int k1, uint32_t flip, uint32_t* keys, int cap, uint32_t& worst) {
   const int lane = threadIdx.x & 31, per = a.P / Q4_BLOCK;
-  const uint32_t span = r.from > a.sinks ? static_cast<uint32_t>(r.from - a.sinks) : 0u;   // positions that may go: sinks + [0, span)
   bool bad = false;
   for (int c0 = k0; c0 < k1; c0 += 32) {
     uint32_t blk = 0u;   // of the chunk's lane-th block among the pool's
@@ -180,8 +181,7 @@ __device__ __forceinline__ bool ev_load(const PlanArgs& a, const EvRow& r, int k
       for (int u = 0; u < EV_AHEAD; ++u) {
         const int i = (k + u) * Q4_BLOCK + lane;
         if (k + u < c1) {
-          const bool stays = static_cast<uint32_t>(pos[u] - a.sinks) >= span || i >= r.n;
-          const uint32_t x = stays ? 0xffffffffu : ev_ordered(w[u]);
+          const uint32_t x = i >= r.n ? 0xffffffffu : ev_key(a, r, w[u], pos[u]);
           if (i - k0 * Q4_BLOCK < cap) keys[i - k0 * Q4_BLOCK] = x ^ flip;
           worst = max(worst, ~x);
         }
@@ -473,7 +473,8 @@ template <int D>
 __global__ void __launch_bounds__(MV_THREADS) kv_move_q4_kernel(const MoveArgs a) {
   constexpr int PIECES = D / 32;   // of a token's key or value codes
   const int pair = blockIdx.x, h = pair % a.Hkv, lane = threadIdx.x & 31, l = lane & 15;
-  const int count = min(a.counts[pair], a.max_moves), per = a.P / Q4_BLOCK;
+  const uint32_t count = max(0, min(a.counts[pair], a.max_moves));   // (a step of the loop below may pass 31 bits)
+  const int per = a.P / Q4_BLOCK;
   const long long slots = static_cast<long long>(a.pages) * a.P;
   const int2* moves = reinterpret_cast<const int2*>(a.moves) + static_cast<long long>(pair) * a.max_moves;
   // what the lane carries: its bytes, and where they are: in a block, or in the weights or positions
@@ -494,7 +495,7 @@ __global__ void __launch_bounds__(MV_THREADS) kv_move_q4_kernel(const MoveArgs a
     block = 4 * Q4_BLOCK;
     each = 4;
   }
-  for (int i0 = 32 * (blockIdx.y * (MV_THREADS / 32) + (threadIdx.x >> 5)); i0 < count; i0 += 32 * gridDim.y * (MV_THREADS / 32)) {
+  for (uint32_t i0 = 32 * (blockIdx.y * (MV_THREADS / 32) + (threadIdx.x >> 5)); i0 < count; i0 += 32 * gridDim.y * (MV_THREADS / 32)) {
     // the lane's move: numbers of the blocks among the pool's, rows in them; ~0: none
     uint32_t from = ~0u, to = 0u, rows = 0u;
     if (i0 + lane < count) {
@@ -506,7 +507,7 @@ __global__ void __launch_bounds__(MV_THREADS) kv_move_q4_kernel(const MoveArgs a
         rows = (m.x % Q4_BLOCK) | (m.y % Q4_BLOCK) << 8;
       }
     }
-    const int n = min(32, count - i0);
+    const int n = min(32u, count - i0);
     for (int j0 = 0; j0 < n; j0 += 2 * MV_AHEAD) {
       uint4 x[MV_AHEAD];
       unsigned char* dst[MV_AHEAD];

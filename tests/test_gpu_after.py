@@ -510,6 +510,17 @@ def test_plan_of_no_numbers():
         _plan(w, pos, table, [500, 400], [budget] * 2, nxt, 3, 7, 300)
 
 
+def test_plan_of_extreme_positions():
+    """Positions, next positions and ranges at the ends of 32 bits."""
+    rng, w, pos, table, nxt = _plan_case(7, 2, 32, [500, 400])
+    ends = np.array([-2 ** 31, -2 ** 31 + 2, -1, 0, 3, 2 ** 31 - 1])
+    pos = np.where(rng.random(pos.shape) < 0.3, ends[rng.integers(0, 6, pos.shape)], pos)
+    for nxt in ([2 ** 31 - 1, 420], [-2 ** 31, 0], [100, -2 ** 31]):
+        for sinks, recent in ((4, 0), (0, 64), (2 ** 31 - 1, 0), (4, 2 ** 31 - 1)):
+            for budget in (250, 390):
+                _plan(w, pos, table, [500, 400], [budget] * 2, np.array(nxt), sinks, recent, 300)
+
+
 def test_plan_long_tables_and_keys_that_do_not_fit():
     """Short sequences in wide tables (clusters with idle CTAs), and a part of a sequence
     that is longer than its CTA's keys in shared memory."""
